@@ -170,6 +170,10 @@ def _prepare_adamw(case, gen):
               "flat_mval": torch.zeros_like(m), "flat_vval": torch.zeros_like(m)}
     for k in [k[5:] for k in s if k.startswith("flat_")]:
         s[k] = _views(s["flat_" + k], sizes, BLOCK if k in ("ms", "vs") else 1)
+    if own:  # the handle that a program keeps which steps the same tensors again and again
+        import einsum_device_side_gb300 as trop
+        values = (s["mval"], s["vval"]) if "ms" in s else None
+        s["plan"] = trop.AdamWPlan(s["p"], s["g"], s["m"], s["v"], s.get("ms"), s.get("vs"), values=values)
     return s
 
 
@@ -324,12 +328,11 @@ def _run_own(s):
                                                         ignore_index=IGNORE)
             out |= {"dx": dx, "dw": dw}
         return out
+    s["plan"].step(s["step"], **HYPER)
     if case["state"] == "f32":
-        trop.adamw_step(s["p"], s["g"], s["m"], s["v"], step=s["step"], **HYPER)
         out = {"p": s["flat_p"], "m": s["flat_m"], "v": s["flat_v"]}
     else:
-        trop.adamw_step(s["p"], s["g"], s["m"], s["v"], s["ms"], s["vs"], step=s["step"], **HYPER)
-        trop.adamw_state_values(s["m"], s["v"], s["ms"], s["vs"], out=(s["mval"], s["vval"]))
+        s["plan"].state_values()
         out = {"p": s["flat_p"], "m": s["flat_mval"], "v": s["flat_vval"]}
     s["step"] += 1
     return out
