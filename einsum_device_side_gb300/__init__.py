@@ -5,6 +5,10 @@ Every function here marshals torch CUDA tensors into the C ABI declared in
 runs in that library's CUDA kernels.  There is no CPU fallback: if the
 library is missing the first call raises.
 
+The training operators that stand around a tropical product and its gradient
+(layer norm, the cross entropy of a linear head, AdamW) are in ``train.py`` and
+reached from here too.
+
 Semirings: ``"maxplus"`` (max, +), ``"minplus"`` (min, +), ``"maxtimes"``
 (max, *).  Argmax tensors are int32.
 """
@@ -21,6 +25,8 @@ __all__ = [
     "TropicalError", "load", "permute_trace", "permute_pair", "gemm", "einsum", "contract_tree",
     "tree_backtrack", "stats", "reset_stats", "sync_pool", "release_pool", "plan_describe", "version",
     "SEMIRINGS",
+    "layer_norm", "layer_norm_backward", "LayerNorm", "linear_cross_entropy", "linear_cross_entropy_backward",
+    "LinearCrossEntropy", "adamw_step", "adamw_state_values", "AdamWPlan", "AdamW",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -133,6 +139,16 @@ def load(path: str | None = None):
         "tropical_debug_bounds_report": (I, [ctypes.POINTER(ctypes.c_uint), ctypes.POINTER(ctypes.c_int),
                                              ctypes.POINTER(ctypes.c_uint64), I]),
         "tropical_debug_bounds_trim": (I, [I64]),
+        "tropical_layer_norm": (I, [TP, P, P, I, ctypes.c_double, TP, P, P, P]),
+        "tropical_layer_norm_backward": (I, [TP, TP, P, P, P, I, TP, P, P, P]),
+        "tropical_linear_cross_entropy": (I, [TP, TP, TP, I64, I, P, P, P, P, P]),
+        "tropical_linear_cross_entropy_backward": (I, [P, I64, TP, TP, TP, I64, P, P, TP, TP, P]),
+        "tropical_adamw_step": (I, [I64, P, I, I, I, I, P, P]),
+        "tropical_adamw_state_values": (I, [I64, P, P]),
+        "tropical_adamw_plan_create": (I, [I64, P, I, I, I, I, P, ctypes.POINTER(P)]),
+        "tropical_adamw_plan_step": (I, [P, P, P]),
+        "tropical_adamw_plan_values": (I, [P, P]),
+        "tropical_adamw_plan_destroy": (I, [P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -142,7 +158,7 @@ def load(path: str | None = None):
     _lib = lib
     _fc = None if debug else _load_fastcall(path)
     if _fc is not None:
-        _fc.set_torch_handles(torch.float32, torch.int32, torch.int64, torch.float64,
+        _fc.set_torch_handles(torch.float32, torch.int32, torch.int64, torch.float64, torch.bfloat16, torch.float16,
                               _raw_stream or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
     return lib
 
@@ -607,7 +623,8 @@ def debug_set_wait_mode(mode: int):
 
 
 # translation units of the library, by the id the bounds-checked build records with a line
-_BOUNDS_FILES = {1: "unary.cu", 2: "gemm.cu", 3: "gemm64.cu", 4: "gemm_int.cu", 5: "backward.cu", 6: "backtrack.cu"}
+_BOUNDS_FILES = {1: "unary.cu", 2: "gemm.cu", 3: "gemm64.cu", 4: "gemm_int.cu", 5: "backward.cu", 6: "backtrack.cu",
+                 7: "layer_norm.cu", 8: "adamw.cu", 9: "linear_ce.cu"}
 
 
 def debug_bounds_report(reset: bool = False) -> dict | None:
@@ -659,3 +676,7 @@ def plan_describe(spec: str, shape_a, stride_a, shape_b, stride_b) -> str:
     _check(lib.tropical_plan_describe(spec.encode(), len(shape_a), arr(shape_a), arr(stride_a), len(shape_b),
                                       arr(shape_b), arr(stride_b), buf, 1024))
     return buf.value.decode()
+
+
+from .train import (AdamW, AdamWPlan, LayerNorm, LinearCrossEntropy, adamw_state_values, adamw_step,  # noqa: E402
+                    layer_norm, layer_norm_backward, linear_cross_entropy, linear_cross_entropy_backward)

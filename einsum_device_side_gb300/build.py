@@ -32,6 +32,8 @@ LIB_DEBUG = os.path.join(BUILD_DEBUG, "libtropical_gb300.so")
 VARIANTS = {"release": (BUILD, LIB, []), "debug": (BUILD_DEBUG, LIB_DEBUG, ["-DTROP_DEBUG_BOUNDS=1"])}
 SOURCES = ["runtime.cpp", "api.cpp", "unary.cu", "gemm.cu", "gemm64.cu", "gemm_int.cu", "backtrack.cu", "backward.cu",
            "noalloc.cu"]
+TRAIN = ["train.cpp", "layer_norm.cu", "adamw.cu", "linear_ce.cu"]  # the training operators
+SOURCES += TRAIN
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fno-strict-aliasing",
           "-ftz=false", "-prec-div=true", "-prec-sqrt=true", "-fmad=false",
@@ -50,6 +52,8 @@ def _stale(obj: str, src: str) -> bool:
         return True
     deps = [src, os.path.join(CSRC, "internal.h"), os.path.join(CSRC, "bounds.h"),
             os.path.join(ROOT, "include", "tropical.h")]
+    if os.path.basename(src) in TRAIN:
+        deps += [os.path.join(CSRC, "train.h"), os.path.join(CSRC, "tcgen05.h")]
     return any(os.path.getmtime(d) > os.path.getmtime(obj) for d in deps)
 
 

@@ -33,6 +33,7 @@ int register_backward_kernels();
 int register_gemm64_kernels();
 int register_gemm_int_kernels();
 int register_backtrack_kernels();
+int register_linear_ce_kernels();
 int launch_fill_i32(int32_t* p, int64_t n, int32_t value, cudaStream_t s);
 
 int register_kernels_for_device()
@@ -43,6 +44,7 @@ int register_kernels_for_device()
     TROP_TRY(register_gemm64_kernels());
     TROP_TRY(register_gemm_int_kernels());
     TROP_TRY(register_backtrack_kernels());
+    TROP_TRY(register_linear_ce_kernels());
     return TROP_OK;
 }
 

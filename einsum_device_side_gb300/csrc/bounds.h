@@ -89,7 +89,14 @@ __device__ __forceinline__ bool bounds_ok(const void* p, int bytes, const Span& 
 #define TROP_TU 0
 #endif
 #define TROP_IN(ptr, bytes, span) ::trop::bounds_ok((ptr), (bytes), (span), (TROP_TU << 16) | __LINE__)
+// a contiguous block of `bytes` at p, for kernels whose tensors come in a table (the record is the launch's)
+__device__ __forceinline__ Span span_bytes_dev(const void* p, int64_t bytes, unsigned* rep)
+{
+    const char* b = static_cast<const char*>(p);
+    return Span{b, b ? b + bytes : b, rep};
+}
 #else
+__device__ __forceinline__ Span span_bytes_dev(const void*, int64_t, unsigned*) { return Span{}; }
 #define TROP_IN(ptr, bytes, span) true
 #endif
 #endif

@@ -153,28 +153,31 @@ static PyObject* fc_einsum(PyObject* self, PyObject* const* a, Py_ssize_t nargs)
 /* ---- tensor-taking variants: the same calls, reading each tensor's data_ptr(), dtype, shape and
  * stride() through the C API (the tensors are treated as plain Python objects with those
  * attributes), so the Python wrapper does no per-argument work.  set_torch_handles() gives the
- * dtype objects (matched by identity: float32, int32, int64, float64 -> the trop_dtype codes)
- * and the function returning a device's current raw stream. */
-static PyObject* g_dtype_obj[4];
+ * dtype objects (matched by identity: float32, int32, int64, float64, bfloat16, float16 -> the
+ * trop_dtype codes) and the function returning a device's current raw stream. */
+#define N_DTYPES 6       /* f32, i32, i64, f64, bf16, f16: the trop_dtype codes */
+#define N_TROPICAL 4     /* the ones that the tropical operations know */
+static PyObject* g_dtype_obj[N_DTYPES];
 static PyObject* g_raw_stream;
 static PyObject *s_data_ptr, *s_shape, *s_stride, *s_dtype, *s_get_device, *s_cuda_stream;
 
 static PyObject* fc_set_torch_handles(PyObject* self, PyObject* const* a, Py_ssize_t nargs)
 {
     (void)self;
-    if (check_nargs(nargs, 5, "set_torch_handles") < 0) return NULL;
-    for (int i = 0; i < 4; ++i) {
+    if (check_nargs(nargs, N_DTYPES + 1, "set_torch_handles") < 0) return NULL;
+    for (int i = 0; i < N_DTYPES; ++i) {
         Py_XDECREF(g_dtype_obj[i]);
         Py_INCREF(a[i]);
         g_dtype_obj[i] = a[i];
     }
     Py_XDECREF(g_raw_stream);
-    Py_INCREF(a[4]);
-    g_raw_stream = a[4];
+    Py_INCREF(a[N_DTYPES]);
+    g_raw_stream = a[N_DTYPES];
     Py_RETURN_NONE;
 }
 
-static int obj_tensor(trop_tensor* t, PyObject* obj)
+/* the descriptor of a tensor object whose dtype is one of the first n_dtypes */
+static int obj_tensor_of(trop_tensor* t, PyObject* obj, int n_dtypes)
 {
     PyObject* p = PyObject_CallMethodNoArgs(obj, s_data_ptr);
     if (!p) return -1;
@@ -184,7 +187,7 @@ static int obj_tensor(trop_tensor* t, PyObject* obj)
     PyObject* dt = PyObject_GetAttr(obj, s_dtype);
     if (!dt) return -1;
     t->dtype = -1;  /* unknown dtypes reach the C ABI as -1, which it refuses */
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < n_dtypes; ++i)
         if (dt == g_dtype_obj[i]) t->dtype = i;
     Py_DECREF(dt);
     PyObject* shape = PyObject_GetAttr(obj, s_shape);
@@ -209,6 +212,8 @@ static int obj_tensor(trop_tensor* t, PyObject* obj)
     Py_DECREF(stride);
     return rc;
 }
+
+static int obj_tensor(trop_tensor* t, PyObject* obj) { return obj_tensor_of(t, obj, N_TROPICAL); }
 
 /* the stream handle: stream.cuda_stream, or the current raw stream of obj's device */
 static int obj_stream(PyObject* stream, PyObject* obj, void** out)
@@ -297,6 +302,130 @@ static PyObject* fc_permute_pair_t(PyObject* self, PyObject* const* a, Py_ssize_
     return PyLong_FromLong(rc);
 }
 
+/* ---- training operators.  Tensors as objects; "or None" leaves one out. */
+
+/* address of a tensor object, NULL for None */
+static int obj_ptr(PyObject* obj, void** out)
+{
+    *out = NULL;
+    if (obj == Py_None) return 0;
+    PyObject* p = PyObject_CallMethodNoArgs(obj, s_data_ptr);
+    if (!p) return -1;
+    const int bad = as_ptr(p, out) < 0;
+    Py_DECREF(p);
+    return bad ? -1 : 0;
+}
+static int as_double(PyObject* o, double* out)
+{
+    *out = PyFloat_AsDouble(o);
+    return (*out == -1.0 && PyErr_Occurred()) ? -1 : 0;
+}
+
+/* layer_norm_t(x, weight or None, bias or None, wdtype, eps, y, mean or None, rstd or None, stream or None) */
+static PyObject* fc_layer_norm_t(PyObject* self, PyObject* const* a, Py_ssize_t nargs)
+{
+    (void)self;
+    if (check_nargs(nargs, 9, "layer_norm_t") < 0) return NULL;
+    trop_tensor x, y;
+    void *w, *b, *mean, *rstd, *stream;
+    int64_t wdtype;
+    double eps;
+    if (obj_tensor_of(&x, a[0], N_DTYPES) < 0 || obj_ptr(a[1], &w) < 0 || obj_ptr(a[2], &b) < 0 ||
+        as_i64(a[3], &wdtype) < 0 || as_double(a[4], &eps) < 0 || obj_tensor_of(&y, a[5], N_DTYPES) < 0 ||
+        obj_ptr(a[6], &mean) < 0 || obj_ptr(a[7], &rstd) < 0 || obj_stream(a[8], a[0], &stream) < 0)
+        return NULL;
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = tropical_layer_norm(&x, w, b, (int)wdtype, eps, &y, (float*)mean, (float*)rstd, stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
+/* layer_norm_backward_t(dy, x, mean, rstd, weight or None, wdtype, dx or None, dweight or None, dbias or None,
+ * stream or None) */
+static PyObject* fc_layer_norm_backward_t(PyObject* self, PyObject* const* a, Py_ssize_t nargs)
+{
+    (void)self;
+    if (check_nargs(nargs, 10, "layer_norm_backward_t") < 0) return NULL;
+    trop_tensor dy, x, dx;
+    void *mean, *rstd, *w, *dw, *db, *stream;
+    int64_t wdtype;
+    if (obj_tensor_of(&dy, a[0], N_DTYPES) < 0 || obj_tensor_of(&x, a[1], N_DTYPES) < 0 || obj_ptr(a[2], &mean) < 0 ||
+        obj_ptr(a[3], &rstd) < 0 || obj_ptr(a[4], &w) < 0 || as_i64(a[5], &wdtype) < 0 ||
+        (a[6] != Py_None && obj_tensor_of(&dx, a[6], N_DTYPES) < 0) || obj_ptr(a[7], &dw) < 0 ||
+        obj_ptr(a[8], &db) < 0 || obj_stream(a[9], a[1], &stream) < 0)
+        return NULL;
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = tropical_layer_norm_backward(&dy, &x, (float*)mean, (float*)rstd, w, (int)wdtype,
+                                      a[6] == Py_None ? NULL : &dx, dw, db, stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
+/* linear_ce_t(x, w, target, ignore_index, mean, loss or None, lse, total or None, kept or None, stream or None) */
+static PyObject* fc_linear_ce_t(PyObject* self, PyObject* const* a, Py_ssize_t nargs)
+{
+    (void)self;
+    if (check_nargs(nargs, 10, "linear_ce_t") < 0) return NULL;
+    trop_tensor x, w, t;
+    void *loss, *lse, *total, *kept, *stream;
+    int64_t ignore;
+    const int mean = PyObject_IsTrue(a[4]);
+    if (obj_tensor_of(&x, a[0], N_DTYPES) < 0 || obj_tensor_of(&w, a[1], N_DTYPES) < 0 ||
+        obj_tensor_of(&t, a[2], N_DTYPES) < 0 || as_i64(a[3], &ignore) < 0 || mean < 0 || obj_ptr(a[5], &loss) < 0 ||
+        obj_ptr(a[6], &lse) < 0 || obj_ptr(a[7], &total) < 0 || obj_ptr(a[8], &kept) < 0 ||
+        obj_stream(a[9], a[0], &stream) < 0)
+        return NULL;
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = tropical_linear_cross_entropy(&x, &w, &t, ignore, mean, (float*)loss, (float*)lse, (float*)total,
+                                       (float*)kept, stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
+/* linear_ce_backward_t(dloss, dloss_stride, x, w, target, ignore_index, lse, kept or None, dx or None, dw or None,
+ * stream or None) */
+static PyObject* fc_linear_ce_backward_t(PyObject* self, PyObject* const* a, Py_ssize_t nargs)
+{
+    (void)self;
+    if (check_nargs(nargs, 11, "linear_ce_backward_t") < 0) return NULL;
+    trop_tensor x, w, t, dx, dw;
+    void *g, *lse, *kept, *stream;
+    int64_t sg, ignore;
+    if (obj_ptr(a[0], &g) < 0 || as_i64(a[1], &sg) < 0 || obj_tensor_of(&x, a[2], N_DTYPES) < 0 ||
+        obj_tensor_of(&w, a[3], N_DTYPES) < 0 || obj_tensor_of(&t, a[4], N_DTYPES) < 0 || as_i64(a[5], &ignore) < 0 ||
+        obj_ptr(a[6], &lse) < 0 || obj_ptr(a[7], &kept) < 0 ||
+        (a[8] != Py_None && obj_tensor_of(&dx, a[8], N_DTYPES) < 0) ||
+        (a[9] != Py_None && obj_tensor_of(&dw, a[9], N_DTYPES) < 0) || obj_stream(a[10], a[2], &stream) < 0)
+        return NULL;
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = tropical_linear_cross_entropy_backward((float*)g, sg, &x, &w, &t, ignore, (float*)lse, (float*)kept,
+                                                a[8] == Py_None ? NULL : &dx, a[9] == Py_None ? NULL : &dw, stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
+/* adamw_plan_step(plan address, lr, beta1, beta2, eps, weight_decay, grad_scale, step, tensor, stream or None) */
+static PyObject* fc_adamw_plan_step(PyObject* self, PyObject* const* a, Py_ssize_t nargs)
+{
+    (void)self;
+    if (check_nargs(nargs, 10, "adamw_plan_step") < 0) return NULL;
+    trop_adamw_options o;
+    void *plan, *stream;
+    if (as_ptr(a[0], &plan) < 0 || as_double(a[1], &o.lr) < 0 || as_double(a[2], &o.beta1) < 0 ||
+        as_double(a[3], &o.beta2) < 0 || as_double(a[4], &o.eps) < 0 || as_double(a[5], &o.weight_decay) < 0 ||
+        as_double(a[6], &o.grad_scale) < 0 || as_i64(a[7], &o.step) < 0 || obj_stream(a[9], a[8], &stream) < 0)
+        return NULL;
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = tropical_adamw_plan_step((trop_adamw_plan)plan, &o, stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
 static PyObject* fc_last_error(PyObject* self, PyObject* const* a, Py_ssize_t nargs)
 {
     (void)self;
@@ -312,11 +441,20 @@ static PyMethodDef methods[] = {
     {"einsum", (PyCFunction)(void (*)(void))fc_einsum, METH_FASTCALL, "tropical_einsum_pairwise"},
     {"last_error", (PyCFunction)(void (*)(void))fc_last_error, METH_FASTCALL, "tropical_last_error"},
     {"set_torch_handles", (PyCFunction)(void (*)(void))fc_set_torch_handles, METH_FASTCALL,
-     "dtype objects (float32, int32, int64, float64) and the current-raw-stream function"},
+     "dtype objects (float32, int32, int64, float64, bfloat16, float16) and the current-raw-stream function"},
     {"permute_trace_t", (PyCFunction)(void (*)(void))fc_permute_trace_t, METH_FASTCALL,
      "tropical_permute_trace on tensor objects"},
     {"permute_pair_t", (PyCFunction)(void (*)(void))fc_permute_pair_t, METH_FASTCALL,
      "tropical_permute_pair on tensor objects"},
+    {"layer_norm_t", (PyCFunction)(void (*)(void))fc_layer_norm_t, METH_FASTCALL,
+     "tropical_layer_norm on tensor objects"},
+    {"layer_norm_backward_t", (PyCFunction)(void (*)(void))fc_layer_norm_backward_t, METH_FASTCALL,
+     "tropical_layer_norm_backward on tensor objects"},
+    {"linear_ce_t", (PyCFunction)(void (*)(void))fc_linear_ce_t, METH_FASTCALL,
+     "tropical_linear_cross_entropy on tensor objects"},
+    {"linear_ce_backward_t", (PyCFunction)(void (*)(void))fc_linear_ce_backward_t, METH_FASTCALL,
+     "tropical_linear_cross_entropy_backward on tensor objects"},
+    {"adamw_plan_step", (PyCFunction)(void (*)(void))fc_adamw_plan_step, METH_FASTCALL, "tropical_adamw_plan_step"},
     {NULL, NULL, 0, NULL},
 };
 

@@ -1,0 +1,931 @@
+// linear_ce.cu -- softmax cross entropy of a linear head, without keeping its logits.
+//
+// Tokens x [N, D], weights w [V, D] (bf16 or f16), targets t [N]:
+//   l[i, v]  = sum_d x[i, d] w[v, d]                 (products exact, sums in f32)
+//   lse[i]   = log sum_v exp l[i, v]
+//   loss[i]  = lse[i] - l[i, t[i]]
+// and, given g[i] = d(total)/d(loss[i]):
+//   P[i, v]  = g[i] (exp(l[i, v] - lse[i]) - [v = t[i]])
+//   dx       = P w,   dw = P^T x.
+// The logits are the ordinary (+, x) product under a log-sum-exp, the smooth form of the library's
+// max-plus contraction; unlike that one they are multiply-accumulates and run on the tensor cores.
+//
+// One kernel, k_tile, computes all four products as 256-column tiles in tensor memory; what
+// differs is where an accumulator goes:
+//   LSE   a tile's logits are folded into each row's running maximum and sum of exponentials in
+//         registers; the logits of a unit of tiles leave as one (maximum, sum) pair per row
+//   GRAD  the logits are formed again and leave as P, for a piece of the vocabulary at a time, so
+//         that P takes a bounded workspace whatever V is
+//   DX    P w over a piece (added to the pieces before it in f32)
+//   DW    P^T x: the piece's rows of dw, whole
+// Operand tiles come by TMA into a ring of 128-byte-swizzled stages; one thread issues the
+// products, eight warps empty one accumulator while the next one fills.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+
+#define TROP_TU 9  // this file's id in a bounds-violation record
+#include "internal.h"
+#include "tcgen05.h"
+#include "train.h"
+
+namespace trop {
+
+namespace {
+
+enum { LSE = 0, GRAD = 1, DX = 2, DW = 3 };
+
+constexpr int CG = 1;                 // CTAs that share an accumulator tile
+constexpr int TM = 128 * CG;          // rows of an output tile
+constexpr int TN = 256;               // columns
+constexpr int TK = 64;                // depth of a stage: one 128-byte row of 16-bit elements
+constexpr int A_BYTES = 128 * TK * 2;         // of one CTA
+constexpr int B_BYTES = TN / CG * TK * 2;
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int STAGES = CG == 1 ? 4 : 6;
+constexpr int SMEM = STAGES * STAGE_BYTES + 1024;
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS = 128 + 32 * EPI_WARPS;
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
+constexpr float NO_MAX = -3.0e38f;  // running maximum before any logit (finite: 2^(NO_MAX - M) = 0)
+
+// The target of row i: its column, -1 where the row is left out, -2 where it lies outside the vocabulary.
+struct Targets {
+    const void* p;
+    int64_t stride, ignore, V;
+    int wide;  // int64, else int32
+    Span sp;
+};
+__device__ __forceinline__ int64_t target_of(const Targets& t, int64_t i)
+{
+    int64_t v;
+    if (t.wide) {
+        const int64_t* q = (const int64_t*)t.p + i * t.stride;
+        v = TROP_IN(q, 8, t.sp) ? *q : t.ignore;
+    } else {
+        const int32_t* q = (const int32_t*)t.p + i * t.stride;
+        v = TROP_IN(q, 4, t.sp) ? *q : t.ignore;
+    }
+    return v == t.ignore ? -1 : v < 0 || v >= t.V ? -2 : v;
+}
+
+struct Job {
+    int mt, nt, inner, ks;  // tiles along rows and columns; column tiles of a unit; splits of the depth
+    int kt, kper;           // depth in stages, and of one split
+    int units;
+    int a0, ak0, b0, bk0;   // first row / depth of A and of B in their tensor maps
+    int rows, cols;         // of the output (cols: LSE the vocabulary, GRAD the piece)
+    uint32_t* error;
+    Targets tgt;
+    // LSE
+    float2* part;           // [2 * (units / mt)][mt * TM]
+    float* at;              // [rows]: the logit of the target
+    // GRAD
+    void* P;
+    int64_t ldp;
+    int64_t v0;             // the piece's first column
+    const float* lse;
+    const float* g;
+    int64_t sg;
+    const float* count;     // nullable: g is divided by it
+    const float* scale;     // nullable: {factor of P, factor of the products with P}
+    // DX, DW
+    void* out;              // null while pieces are still to come
+    int64_t ldo;
+    int vec;                // rows of out start on 16 bytes
+    float* acc;             // [ks][rows][cols] or null
+    int add;                // acc holds the pieces before
+    Span sp_part, sp_at, sp_P, sp_lse, sp_g, sp_out, sp_acc;
+};
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float a, float b)
+{
+    if (BF16) {
+        __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<uint32_t*>(&h);
+    }
+    __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&h);
+}
+
+struct Unit {
+    int m, n, k0, k1;  // row tile, first column tile, stages
+};
+template <int MODE>
+__device__ __forceinline__ Unit unit_of(const Job& j, int u)
+{
+    Unit r;
+    if (MODE == LSE || MODE == GRAD) {  // rows fastest: the units that run together share columns of w
+        r.m = u % j.mt;
+        r.n = (u / j.mt) * j.inner;
+        r.k0 = 0;
+        r.k1 = j.kt;
+    } else {
+        r.n = u % j.nt;
+        u /= j.nt;
+        r.m = u % j.mt;
+        r.k0 = (u / j.mt) * j.kper;
+        r.k1 = min(j.kt, r.k0 + j.kper);
+    }
+    return r;
+}
+
+// ------------------------------------------------------------------ what becomes of an accumulator tile
+// A thread has one row and 128 of the tile's columns, in four loads of 32.
+
+// 2^n of a whole n <= 0, exactly (zero from 2^-127 down)
+__device__ __forceinline__ float pow2_whole(float n) { return __int_as_float(((int)fmaxf(n, -127.f) + 127) << 23); }
+
+struct RowState {
+    float M, s;        // LSE: integer reference (in log2 units) and the sum of 2^(l log2e - M)
+    int64_t t;         // target column
+    float nlse, g;     // GRAD: -lse log2e, gradient
+};
+
+__device__ __forceinline__ void lse_chunk(RowState& r, float (&v)[32], int left, int64_t col, float* at, const Job& j)
+{
+    if (left < 32) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i >= left) v[i] = -INFINITY;
+    }
+    float m[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        m[i] = fmaxf(v[i], v[i + 4]);
+#pragma unroll
+        for (int k = 8; k < 32; k += 4) m[i] = fmaxf(m[i], v[i + k]);
+    }
+    const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+    // The reference is the maximum rounded up to a whole power of two: rescaling by a change of it
+    // is exact, so the sum's only roundings are its own.
+    const float M = fmaxf(r.M, ceilf(top * LOG2E));
+    float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 32; ++i) a[i & 3] += ex2(__fmaf_rn(v[i], LOG2E, -M));
+    r.s = r.s * pow2_whole(r.M - M) + ((a[0] + a[1]) + (a[2] + a[3]));
+    r.M = M;
+    const int64_t d = r.t - col;
+    if (d >= 0 && d < 32) {
+        float x = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i == (int)d) x = v[i];
+        if (TROP_IN(at, 4, j.sp_at)) *at = x;
+    }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void grad_chunk(const RowState& r, float (&v)[32], int64_t col, uint16_t* dst, bool live,
+                                           const Job& j)
+{
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = ex2(__fmaf_rn(v[i], LOG2E, r.nlse));
+    const int64_t d = r.t - col;
+    if (d >= 0 && d < 32) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i == (int)d) v[i] -= 1.f;
+    }
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = r.t == -1 ? 0u : pack2<BF16>(v[2 * i] * r.g, v[2 * i + 1] * r.g);
+    if (live) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (TROP_IN(dst + 8 * i, 16, j.sp_P))
+                *reinterpret_cast<uint4*>(dst + 8 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void out_chunk(float (&v)[32], int col, int64_t row, const Job& j, float* acc, float alpha)
+{
+    const int left = j.cols - col;
+    if (left <= 0) return;
+    if (j.add) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < left && TROP_IN(acc + i, 4, j.sp_acc)) v[i] += acc[i];
+    }
+    if (!j.out) {
+        if (left >= 32 && (((uintptr_t)acc) & 15) == 0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (TROP_IN(acc + 4 * i, 16, j.sp_acc))
+                    *reinterpret_cast<float4*>(acc + 4 * i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (i < left && TROP_IN(acc + i, 4, j.sp_acc)) acc[i] = v[i];
+        }
+        return;
+    }
+    uint16_t* dst = (uint16_t*)j.out + row * j.ldo + col;
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = pack2<BF16>(v[2 * i] * alpha, v[2 * i + 1] * alpha);
+    if (j.vec && left >= 32) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (TROP_IN(dst + 8 * i, 16, j.sp_out))
+                *reinterpret_cast<uint4*>(dst + 8 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < left && TROP_IN(dst + i, 2, j.sp_out)) dst[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+    }
+}
+
+// ------------------------------------------------------------------ the kernel
+template <int MODE, bool BF16>
+__global__ void __launch_bounds__(THREADS, 1)
+    k_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const Job j)
+{
+    constexpr bool A_MN = MODE == DW, B_MN = MODE == DX || MODE == DW;
+    extern __shared__ uint8_t dyn[];
+    __shared__ __align__(8) uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], drain;
+    __shared__ uint32_t tmem_slot;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = CG == 2 ? cluster_ctarank() : 0;
+    const uint32_t ring = (smem_u32(dyn) + 1023u) & ~1023u;
+    const int first = blockIdx.x / CG, step = gridDim.x / CG;
+
+    if (warp == 1 && lane == 0) {
+        for (int s = 0; s < STAGES; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
+        for (int b = 0; b < 2; ++b) mbar_init(&tfull[b], 1), mbar_init(&tempty[b], EPI_WARPS * CG);
+        mbar_init(&drain, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0 && lane == 0) tma_prefetch_map(&map_a), tma_prefetch_map(&map_b);
+    if (warp == 2) tmem_alloc_all<CG>(&tmem_slot);
+    tc_fence_before();
+    __syncthreads();
+    if (CG == 2) cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    pdl_wait();
+
+    bool ok = true;
+    if (warp == 0) {
+        if (lane == 0) {  // loads
+            int s = 0;
+            uint32_t phase = 0, issued = 0;
+            for (int u = first; u < j.units && ok; u += step) {
+                const Unit t = unit_of<MODE>(j, u);
+                const int n_end = min(j.nt, t.n + (MODE == LSE ? j.inner : 1));
+                for (int n = t.n; n < n_end && ok; ++n)
+                    for (int k = t.k0; k < t.k1; ++k) {
+                        if (!(ok = mbar_wait(&empty[s], phase ^ 1))) break;
+                        if (rank == 0) mbar_expect_tx(&full[s], STAGE_BYTES * CG);
+                        const uint32_t bar = CG == 2 ? mapa(smem_u32(&full[s]), 0) : smem_u32(&full[s]);
+                        const uint32_t sa = ring + s * STAGE_BYTES, sb = sa + A_BYTES;
+                        const int am = j.a0 + t.m * TM + rank * 128, bm = j.b0 + n * TN + rank * (TN / CG);
+                        const int ak = j.ak0 + k * TK, bk = j.bk0 + k * TK;
+                        if (A_MN) {
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) tma_load_2d<CG>(sa + c * 8192, &map_a, am + 64 * c, ak, bar);
+                        } else {
+                            tma_load_2d<CG>(sa, &map_a, ak, am, bar);
+                        }
+                        if (B_MN) {
+#pragma unroll
+                            for (int c = 0; c < TN / CG / 64; ++c)
+                                tma_load_2d<CG>(sb + c * 8192, &map_b, bm + 64 * c, bk, bar);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < TN / CG / 128; ++c)
+                                tma_load_2d<CG>(sb + c * 16384, &map_b, bk, bm + 128 * c, bar);
+                        }
+                        ++issued;
+                        if (++s == STAGES) s = 0, phase ^= 1;
+                    }
+            }
+            if (!ok && rank == 0)  // no copy may land after the CTA has left
+                for (uint32_t i = 0; i < min(issued, (uint32_t)STAGES); ++i) {
+                    if (--s < 0) s = STAGES - 1, phase ^= 1;
+                    (void)mbar_wait(&full[s], phase);
+                }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {  // products
+            constexpr uint32_t idesc = mma_desc(BF16, A_MN, B_MN, TM, TN);
+            int s = 0;
+            uint32_t phase = 0, tile = 0;
+            for (int u = first; u < j.units && ok; u += step) {
+                const Unit t = unit_of<MODE>(j, u);
+                const int n_end = min(j.nt, t.n + (MODE == LSE ? j.inner : 1));
+                for (int n = t.n; n < n_end && ok; ++n, ++tile) {
+                    const uint32_t b = tile & 1;
+                    if (!(ok = mbar_wait_cluster(&tempty[b], ((tile >> 1) & 1) ^ 1))) break;
+                    tc_fence_after();
+                    for (int k = t.k0; k < t.k1; ++k) {
+                        if (!(ok = mbar_wait_cluster(&full[s], phase))) break;
+                        tc_fence_after();
+                        const uint32_t sa = ring + s * STAGE_BYTES;
+                        const uint64_t da = smem_desc(sa, A_MN ? 8192 : 16), db = smem_desc(sa + A_BYTES, B_MN ? 8192 : 16);
+#pragma unroll
+                        for (int i = 0; i < TK / 16; ++i)  // 16 k: 32 bytes along a row, or 16 rows
+                            tc_mma<CG>(tmem + b * TN, da + i * (A_MN ? 128 : 2), db + i * (B_MN ? 128 : 2), idesc,
+                                       k > t.k0 || i > 0);
+                        tc_commit<CG>(&empty[s]);
+                        if (++s == STAGES) s = 0, phase ^= 1;
+                    }
+                    if (ok) tc_commit<CG>(&tfull[b]);
+                }
+            }
+            if (!ok) {  // no product may run after the CTA has left
+                tc_commit<CG>(&drain);
+                (void)mbar_wait(&drain, 0);
+            }
+        }
+    } else if (warp >= 4) {  // results
+        const int quad = warp & 3, half = (warp - 4) >> 2;
+        uint32_t tile = 0;
+        float mul = 1.f, alpha = 1.f, inv = 1.f;
+        if (MODE != LSE && j.scale) mul = j.scale[0], alpha = j.scale[1];
+        if (MODE == GRAD && j.count) inv = j.count[0];
+        for (int u = first; u < j.units && ok; u += step) {
+            const Unit t = unit_of<MODE>(j, u);
+            const int n_end = min(j.nt, t.n + (MODE == LSE ? j.inner : 1));
+            const int64_t row = (int64_t)t.m * TM + rank * 128 + quad * 32 + lane;
+            const bool live = row < j.rows;
+            RowState r;
+            r.M = NO_MAX;
+            r.s = 0.f;
+            r.t = -1;
+            if (MODE == LSE || MODE == GRAD) {
+                if (live) r.t = target_of(j.tgt, row);
+            }
+            if (MODE == GRAD) {
+                r.nlse = 0.f;
+                r.g = 0.f;
+                if (live && TROP_IN(j.lse + row, 4, j.sp_lse) && TROP_IN(j.g + row * j.sg, 4, j.sp_g)) {
+                    r.nlse = -j.lse[row] * LOG2E;
+                    r.g = r.t == -2 ? NAN : __fdiv_rn(j.g[row * j.sg], inv) * mul;
+                }
+            }
+            for (int n = t.n; n < n_end && ok; ++n, ++tile) {
+                const uint32_t b = tile & 1;
+                ok = mbar_wait(&tfull[b], (tile >> 1) & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t src = tmem + b * TN + half * 128 + ((uint32_t)(quad * 32) << 16);
+                uint32_t v[2][32];
+                tmem_ld32(src, v[0]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    tmem_wait_ld(v[c & 1]);
+                    if (c < 3) {
+                        tmem_ld32(src + (c + 1) * 32, v[(c + 1) & 1]);
+                    } else {  // the accumulator is in registers: the next tile may fill it
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive_cluster(CG == 2 ? mapa(smem_u32(&tempty[b]), 0) : mapa(smem_u32(&tempty[b]), rank));
+                    }
+                    float f[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[c & 1][i]);
+                    const int col = n * TN + half * 128 + c * 32;
+                    if (MODE == LSE) {
+                        lse_chunk(r, f, j.cols - col, col, j.at + row, j);
+                    } else if (MODE == GRAD) {
+                        grad_chunk<BF16>(r, f, j.v0 + col, (uint16_t*)j.P + row * j.ldp + col, live, j);
+                    } else if (live) {
+                        float* acc = j.acc ? j.acc + ((int64_t)(t.k0 / j.kper) * j.rows + row) * j.cols + col : nullptr;
+                        out_chunk<BF16>(f, col, row, j, acc, alpha);
+                    }
+                }
+            }
+            if (MODE == LSE && ok) {
+                float2* q = j.part + ((int64_t)(t.n / j.inner) * 2 + half) * ((int64_t)j.mt * TM) + row;
+                if (TROP_IN(q, 8, j.sp_part)) *q = make_float2(r.M, r.s);
+            }
+        }
+    }
+    if (!ok && lane == 0) {
+        *(volatile uint32_t*)j.error = 1;
+        __threadfence_system();
+    }
+    __syncwarp();
+    pdl_signal();
+    tc_fence_before();
+    __syncthreads();
+    if (CG == 2) cluster_sync_all();
+    if (warp == 2) tmem_free_all<CG>(tmem);
+}
+
+// ------------------------------------------------------------------ joining the units' pairs
+// lse and loss of 32 rows per CTA: 8 warps share the G pairs of a row, each row's pairs in one
+// order.  With `mean` wanted the CTAs leave their sums and the last one to arrive adds them in
+// CTA order.
+struct JoinJob {
+    const float2* part;
+    int64_t stride;  // of one unit's pairs
+    int G;
+    int64_t rows;
+    const float* at;
+    Targets tgt;
+    float* loss;   // nullable [rows]
+    float* lse;    // [rows]
+    float* total;  // {sum or mean of the losses, rows kept}: nullable
+    float* kept;
+    int mean;
+    float2* sums;  // [CTAs]
+    uint32_t* ticket;
+    Span sp_part, sp_at, sp_loss, sp_lse, sp_total, sp_kept;
+};
+__global__ void __launch_bounds__(256) k_lse_join(const JoinJob j)
+{
+    pdl_wait();
+    pdl_signal();
+    __shared__ float2 sh[8][33];
+    __shared__ float red[2][32];
+    __shared__ bool last;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row = (int64_t)blockIdx.x * 32 + lane;
+    float M = NO_MAX, s = 0.f;
+    for (int g = warp; g < j.G; g += 8) {
+        const float2* p = j.part + (int64_t)g * j.stride + row;
+        if (row < j.rows && TROP_IN(p, 8, j.sp_part)) {
+            const float2 q = *p;
+            const float m = fmaxf(M, q.x);
+            s = s * pow2_whole(M - m) + q.y * pow2_whole(q.x - m);
+            M = m;
+        }
+    }
+    sh[warp][lane] = make_float2(M, s);
+    __syncthreads();
+    if (warp == 0) {
+        for (int w = 1; w < 8; ++w) {
+            const float2 q = sh[w][lane];
+            const float m = fmaxf(M, q.x);
+            s = s * pow2_whole(M - m) + q.y * pow2_whole(q.x - m);
+            M = m;
+        }
+        float loss = 0.f, keep = 0.f;
+        if (row < j.rows) {
+            // M is a whole number of powers of two: M ln 2 + log s in two pieces of ln 2
+            const float lse = __fmaf_rn(M, LN2, __fmaf_rn(M, -1.9046542121259335e-09f, logf(s)));
+            const int64_t t = target_of(j.tgt, row);
+            if (TROP_IN(j.lse + row, 4, j.sp_lse)) j.lse[row] = lse;
+            if (t >= 0 && TROP_IN(j.at + row, 4, j.sp_at)) loss = lse - j.at[row];
+            if (t == -2) loss = NAN;
+            keep = t == -1 ? 0.f : 1.f;
+            if (j.loss && TROP_IN(j.loss + row, 4, j.sp_loss)) j.loss[row] = loss;
+        }
+        for (int o = 16; o > 0; o >>= 1) {
+            loss += __shfl_xor_sync(0xffffffffu, loss, o);
+            keep += __shfl_xor_sync(0xffffffffu, keep, o);
+        }
+        if (lane == 0) {
+            j.sums[blockIdx.x] = make_float2(loss, keep);
+            __threadfence();
+            last = atomicAdd(j.ticket, 1u) == gridDim.x - 1;
+        }
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    float a = 0.f, b = 0.f;
+    for (int i = threadIdx.x; i < gridDim.x; i += 256) {
+        const float2 q = __ldcg(&j.sums[i]);
+        a += q.x;
+        b += q.y;
+    }
+    for (int o = 16; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    if (lane == 0) red[0][warp] = a, red[1][warp] = b;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        a = b = 0.f;
+        for (int w = 0; w < 8; ++w) a += red[0][w], b += red[1][w];
+        if (j.total && TROP_IN(j.total, 4, j.sp_total)) *j.total = j.mean ? __fdiv_rn(a, b) : a;
+        if (j.kept && TROP_IN(j.kept, 4, j.sp_kept)) *j.kept = b;
+        *j.ticket = 0;
+    }
+}
+
+// ------------------------------------------------------------------ f16: the range of P
+// P's entries go down to g / V, far below what f16 resolves, so P is stored times
+// 2^14 / max |g| and the products are scaled back.  (bf16 has f32's range and needs none of it.)
+__global__ void __launch_bounds__(256) k_gscale(const float* g, int64_t sg, int64_t n, const float* count, float* scale,
+                                                Span sp_g)
+{
+    pdl_wait();
+    pdl_signal();
+    __shared__ float red[8];
+    float m = 0.f;
+    for (int64_t i = threadIdx.x; i < (sg ? n : 1); i += 256)
+        if (TROP_IN(g + i * sg, 4, sp_g)) m = fmaxf(m, fabsf(g[i * sg]));
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < 8; ++w) m = fmaxf(m, red[w]);
+        if (count) m = __fdiv_rn(m, count[0]);
+        const bool fine = m > 0.f && m < INFINITY;  // nothing kept, all zero, or not finite: leave P as it is
+        scale[0] = fine ? __fdiv_rn(16384.f, m) : 1.f;
+        scale[1] = fine ? m * 6.103515625e-05f : 1.f;
+    }
+}
+
+// ------------------------------------------------------------------ sums of the depth's splits
+template <bool BF16>
+__global__ void __launch_bounds__(256) k_split_join(const float* acc, int ks, int64_t rows, int64_t cols, uint16_t* out,
+                                                    int64_t ldo, const float* scale, Span sp_acc, Span sp_out)
+{
+    pdl_wait();
+    pdl_signal();
+    const float alpha = scale ? scale[1] : 1.f;
+    const int64_t n = rows * cols;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        float s = 0.f;
+        for (int k = 0; k < ks; ++k)
+            if (TROP_IN(acc + k * n + i, 4, sp_acc)) s += acc[k * n + i];
+        uint16_t* dst = out + (i / cols) * ldo + i % cols;
+        if (TROP_IN(dst, 2, sp_out)) *dst = (uint16_t)(pack2<BF16>(s * alpha, 0.f) & 0xffff);
+    }
+}
+
+// ------------------------------------------------------------------ operands that TMA cannot read
+__global__ void __launch_bounds__(256) k_pack16(const uint16_t* in, int64_t sr, int64_t sc, int64_t rows, int64_t cols,
+                                                uint16_t* out, int64_t ld, Span sp_in)
+{
+    pdl_wait();
+    pdl_signal();
+    const int64_t n = rows * cols;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / cols, c = i % cols;
+        const uint16_t* p = in + r * sr + c * sc;
+        out[r * ld + c] = TROP_IN(p, 2, sp_in) ? *p : (uint16_t)0;
+    }
+}
+__global__ void __launch_bounds__(256) k_zero16(uint16_t* out, int64_t sr, int64_t rows, int64_t cols, Span sp)
+{
+    pdl_wait();
+    pdl_signal();
+    const int64_t n = rows * cols;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        uint16_t* p = out + (i / cols) * sr + i % cols;
+        if (TROP_IN(p, 2, sp)) *p = 0;
+    }
+}
+
+// ------------------------------------------------------------------ host
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// a row-major 16-bit matrix, its rows 16-byte aligned, read in boxes of `box_rows` x 64
+int make_map(CUtensorMap* map, bool bf16, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows)
+{
+    const EncodeTiledFn enc = (EncodeTiledFn)tensor_map_encoder();
+    if (!enc) return set_error(TROP_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, one[2] = {1, 1};
+    auto encode = [&] {
+        return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                   const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult r = encode();
+    if (r == CUDA_ERROR_INVALID_CONTEXT) {  // a host thread (autograd's, say) that has not touched the device yet
+        int dev = 0;
+        cudaGetDevice(&dev);
+        cudaSetDevice(dev);
+        r = encode();
+    }
+    if (r != CUDA_SUCCESS) return set_error(TROP_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return TROP_OK;
+}
+
+struct Matrix16 {
+    const uint16_t* p;
+    int64_t rows, cols, ld;
+};
+
+// Workspace blocks of one call, given back in any case.
+struct Blocks {
+    cudaStream_t s;
+    void* p[8];
+    int n = 0;
+    explicit Blocks(cudaStream_t st) : s(st) {}
+    ~Blocks()
+    {
+        for (int i = 0; i < n; ++i) pool_retire(p[i], s);
+    }
+    int get(size_t bytes, void** out)
+    {
+        TROP_TRY(pool_alloc(bytes, s, out));
+        p[n++] = *out;
+        return TROP_OK;
+    }
+};
+
+int grid_for(int64_t n, int sm) { return (int)std::min<int64_t>((n + 255) / 256, (int64_t)sm * 8); }
+
+// The operand as TMA can read it: itself, or a packed copy.
+int readable(const Mat16& a, int sm, Blocks& ws, Matrix16* out)
+{
+    *out = {(const uint16_t*)a.p, a.rows, a.cols, a.sr};
+    if (a.rows == 1) out->ld = (a.cols + 7) / 8 * 8;  // no second row: any pitch
+    if ((a.sc == 1 || a.cols == 1) && out->ld % 8 == 0 && out->ld >= a.cols && out->ld < (int64_t)1 << 38 &&
+        ((uintptr_t)a.p & 15) == 0)
+        return TROP_OK;
+    const int64_t ld = (a.cols + 7) / 8 * 8;
+    void* p;
+    TROP_TRY(ws.get((size_t)a.rows * ld * 2, &p));
+    const int64_t size[2] = {a.rows, a.cols}, stride[2] = {a.sr, a.sc};
+    const cudaError_t e = launch_pdl(k_pack16, dim3(grid_for(a.rows * a.cols, sm)), dim3(256), 0, ws.s,
+                                     (const uint16_t*)a.p, a.sr, a.sc, a.rows, a.cols, (uint16_t*)p, ld,
+                                     span_of(a.p, 2, 2, size, stride));
+    if (e != cudaSuccess) return cuda_error(e, "k_pack16 launch");
+    count_launches(1);
+    *out = {(const uint16_t*)p, a.rows, a.cols, ld};
+    return TROP_OK;
+}
+
+template <int MODE, bool BF16>
+int launch_tile(const CUtensorMap& a, const CUtensorMap& b, const Job& j, int sm, cudaStream_t s)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)std::min(j.units, sm / CG) * CG);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CG == 2 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_tile<MODE, BF16>, a, b, j);
+    if (e != cudaSuccess) return cuda_error(e, "k_tile launch");
+    count_launches(1);
+    return TROP_OK;
+}
+template <int MODE>
+int launch_tile(bool bf16, const CUtensorMap& a, const CUtensorMap& b, const Job& j, int sm, cudaStream_t s)
+{
+    return bf16 ? launch_tile<MODE, true>(a, b, j, sm, s) : launch_tile<MODE, false>(a, b, j, sm, s);
+}
+
+int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+Targets targets_of(const LinearCe& q)
+{
+    const int64_t size[1] = {q.x.rows}, stride[1] = {q.starget};
+    return {q.target, q.starget, q.ignore, q.w.rows, q.target_wide, span_of(q.target, q.target_wide ? 8 : 4, 1, size, stride)};
+}
+
+// The join of the pairs of `rows` tokens (G = 0: no pair, the sums of no token).
+int launch_join(JoinJob t, float2* sums, cudaStream_t s)
+{
+    const int ctas = std::max(1, cdiv(t.rows, 32));
+    TROP_TRY(stream_tickets(s, 1, &t.ticket));
+    t.sums = sums;
+    t.sp_loss = span_bytes(t.loss, (size_t)t.rows * 4);
+    t.sp_lse = span_bytes(t.lse, (size_t)t.rows * 4);
+    t.sp_total = span_bytes(t.total, 4);
+    t.sp_kept = span_bytes(t.kept, 4);
+    const cudaError_t e = launch_pdl(k_lse_join, dim3(ctas), dim3(256), 0, s, t);
+    if (e != cudaSuccess) return cuda_error(e, "k_lse_join launch");
+    count_launches(1);
+    return TROP_OK;
+}
+
+template <int MODE, bool BF16>
+cudaError_t allow_smem()
+{
+    return cudaFuncSetAttribute(k_tile<MODE, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+}
+
+}  // namespace
+
+int register_linear_ce_kernels()
+{
+    const cudaError_t e[] = {allow_smem<LSE, true>(), allow_smem<LSE, false>(), allow_smem<GRAD, true>(),
+                             allow_smem<GRAD, false>(), allow_smem<DX, true>(), allow_smem<DX, false>(),
+                             allow_smem<DW, true>(), allow_smem<DW, false>()};
+    for (const cudaError_t r : e)
+        if (r != cudaSuccess) return cuda_error(r, "cudaFuncSetAttribute(k_tile)");
+    return TROP_OK;
+}
+
+int launch_linear_ce(const LinearCe& q, float* loss, float* lse, float* total, float* kept, int mean, cudaStream_t s)
+{
+    const DeviceInfo* dev;
+    TROP_TRY(ensure_device(&dev));
+    const int sm = dev->sm_count;
+    Blocks ws(s);
+    JoinJob t = {};
+    t.rows = q.x.rows;
+    t.tgt = targets_of(q);
+    t.loss = loss;
+    t.lse = lse;
+    t.total = total;
+    t.kept = kept;
+    t.mean = mean;
+    const size_t sums = (size_t)std::max(1, cdiv(t.rows, 32)) * sizeof(float2);
+    void* p;
+    if (t.rows == 0) {
+        TROP_TRY(ws.get(sums, &p));
+        return launch_join(t, (float2*)p, s);
+    }
+    Matrix16 x, w;
+    TROP_TRY(readable(q.x, sm, ws, &x));
+    TROP_TRY(readable(q.w, sm, ws, &w));
+    Job j = {};
+    TROP_TRY(device_error_word(&j.error));
+    j.rows = (int)x.rows;
+    j.cols = (int)w.rows;
+    j.mt = cdiv(x.rows, TM);
+    j.nt = cdiv(w.rows, TN);
+    j.kt = cdiv(x.cols, TK);
+    j.kper = j.kt;
+    // column tiles of a unit: the fewest rounds of tiles, then the fewest pairs to join
+    int64_t best = INT64_MAX;
+    for (int c = 1; c <= 32 && c <= j.nt; ++c) {
+        const int64_t cost = (int64_t)cdiv((int64_t)j.mt * cdiv(j.nt, c), sm / CG) * c;
+        if (cost <= best) best = cost, j.inner = c;
+    }
+    const int groups = cdiv(j.nt, j.inner);
+    j.units = j.mt * groups;
+    j.tgt = t.tgt;
+    t.stride = (int64_t)j.mt * TM;
+    t.G = 2 * groups;
+    const size_t pairs = (size_t)t.G * t.stride * sizeof(float2), at = (size_t)(x.rows + 63) / 64 * 64 * 4;
+    TROP_TRY(ws.get(pairs + at + sums, &p));
+    t.part = j.part = (float2*)p;
+    t.at = j.at = (float*)((char*)p + pairs);
+    t.sp_part = j.sp_part = span_bytes(j.part, pairs);
+    t.sp_at = j.sp_at = span_bytes(j.at, (size_t)x.rows * 4);
+    CUtensorMap ma, mb;
+    TROP_TRY(make_map(&ma, q.bf16, x.p, x.cols, x.rows, x.ld, 128));
+    TROP_TRY(make_map(&mb, q.bf16, w.p, w.cols, w.rows, w.ld, 128));
+    TROP_TRY(launch_tile<LSE>(q.bf16, ma, mb, j, sm, s));
+    return launch_join(t, (float2*)((char*)p + pairs + at), s);
+}
+
+int launch_linear_ce_backward(const LinearCe& q, const float* g, int64_t sg, const float* lse, const float* kept,
+                              const Mat16* dx, const Mat16* dw, cudaStream_t s)
+{
+    const DeviceInfo* dev;
+    TROP_TRY(ensure_device(&dev));
+    const int sm = dev->sm_count, pairs = sm / CG;
+    const int64_t N = q.x.rows, D = q.x.cols, V = q.w.rows;
+    Blocks ws(s);
+    Matrix16 x, w;
+    TROP_TRY(readable(q.x, sm, ws, &x));
+    TROP_TRY(readable(q.w, sm, ws, &w));
+
+    // A piece of the vocabulary: P takes at most 512 MiB (and at least 16 tiles' columns).
+    const int64_t whole = (V + TN - 1) / TN * TN;
+    int64_t piece = ((int64_t)1 << 28) / std::max<int64_t>(N, 1) / TN * TN;
+    piece = std::min(whole, std::max<int64_t>(piece, 16 * TN));
+    const int pieces = cdiv(V, piece);
+    // Splits of dx's depth (a piece's columns): the fewest rounds of stages, each split costing about
+    // the time of 8 stages more for its partial sums.
+    const int dx_mt = cdiv(N, TM), dx_nt = cdiv(D, TN), dx_kt = cdiv(std::min(piece, V), TK);
+    int ks = 1;
+    if (dx) {
+        int64_t best = INT64_MAX;
+        for (int c = 1; c <= std::min(dx_kt, 64); ++c) {
+            const int per = cdiv(dx_kt, c);
+            if (cdiv(dx_kt, per) != c) continue;
+            const int64_t cost = (int64_t)cdiv((int64_t)dx_mt * dx_nt * c, pairs) * (per + (c > 1 ? 8 : 0));
+            if (cost < best) best = cost, ks = c;
+        }
+    }
+    const size_t p_bytes = (size_t)N * piece * 2;
+    const bool summed = dx && (ks > 1 || pieces > 1);
+    const size_t acc_bytes = summed ? (size_t)ks * N * D * 4 : 0;
+    void *P, *acc = nullptr, *scale = nullptr;
+    TROP_TRY(ws.get(p_bytes, &P));
+    if (summed) TROP_TRY(ws.get(acc_bytes, &acc));
+    if (!q.bf16) {
+        TROP_TRY(ws.get(8, &scale));
+        const int64_t size[1] = {N}, stride[1] = {sg};
+        const cudaError_t e = launch_pdl(k_gscale, dim3(1), dim3(256), 0, s, g, sg, N, kept, (float*)scale,
+                                         span_of(g, 4, 1, size, stride));
+        if (e != cudaSuccess) return cuda_error(e, "k_gscale launch");
+        count_launches(1);
+    }
+    CUtensorMap x_k, w_k, x_mn, w_mn, p_k, p_mn;
+    TROP_TRY(make_map(&x_k, q.bf16, x.p, D, N, x.ld, 128));
+    TROP_TRY(make_map(&w_k, q.bf16, w.p, D, V, w.ld, 128));
+    TROP_TRY(make_map(&x_mn, q.bf16, x.p, D, N, x.ld, 64));
+    TROP_TRY(make_map(&w_mn, q.bf16, w.p, D, V, w.ld, 64));
+    for (int i = 0; i < pieces; ++i) {
+        const int64_t v0 = i * piece, cols = std::min(piece, V - v0);
+        TROP_TRY(make_map(&p_k, q.bf16, P, cols, N, piece, 128));
+        TROP_TRY(make_map(&p_mn, q.bf16, P, cols, N, piece, 64));
+        Job j = {};
+        TROP_TRY(device_error_word(&j.error));
+        j.inner = 1;
+        j.ks = 1;
+        j.scale = (const float*)scale;
+        {
+            Job t = j;
+            t.rows = (int)N;
+            t.cols = (int)cols;
+            t.mt = cdiv(N, TM);
+            t.nt = cdiv(cols, TN);
+            t.kt = t.kper = cdiv(D, TK);
+            t.units = t.mt * t.nt;
+            t.b0 = (int)v0;
+            t.v0 = v0;
+            t.tgt = targets_of(q);
+            t.P = P;
+            t.ldp = piece;
+            t.lse = lse;
+            t.g = g;
+            t.sg = sg;
+            t.count = kept;
+            t.sp_P = span_bytes(P, p_bytes);
+            t.sp_lse = span_bytes(lse, (size_t)N * 4);
+            const int64_t size[1] = {N}, stride[1] = {sg};
+            t.sp_g = span_of(g, 4, 1, size, stride);
+            TROP_TRY(launch_tile<GRAD>(q.bf16, x_k, w_k, t, sm, s));
+        }
+        if (dw) {
+            Job t = j;
+            t.rows = (int)cols;
+            t.cols = (int)D;
+            t.mt = cdiv(cols, TM);
+            t.nt = cdiv(D, TN);
+            t.kt = t.kper = cdiv(N, TK);
+            t.units = t.mt * t.nt;
+            t.out = (uint16_t*)dw->p + v0 * dw->sr;
+            t.ldo = dw->sr;
+            t.vec = ((uintptr_t)t.out & 15) == 0 && dw->sr % 8 == 0;
+            const int64_t size[2] = {cols, D}, stride[2] = {dw->sr, 1};
+            t.sp_out = span_of(t.out, 2, 2, size, stride);
+            TROP_TRY(launch_tile<DW>(q.bf16, p_mn, x_mn, t, sm, s));
+        }
+        if (dx) {
+            Job t = j;
+            t.rows = (int)N;
+            t.cols = (int)D;
+            t.mt = dx_mt;
+            t.nt = dx_nt;
+            t.kt = cdiv(cols, TK);
+            t.kper = cdiv(dx_kt, ks);  // the last piece may have fewer splits: those it lacks stay as they are
+            t.ks = cdiv(t.kt, t.kper);
+            t.units = t.mt * t.nt * t.ks;
+            t.bk0 = (int)v0;
+            t.acc = (float*)acc;
+            t.add = i > 0;
+            t.sp_acc = span_bytes(acc, acc_bytes);
+            if (ks == 1 && i == pieces - 1) {
+                t.out = dx->p;
+                t.ldo = dx->sr;
+                t.vec = ((uintptr_t)t.out & 15) == 0 && dx->sr % 8 == 0;
+                const int64_t size[2] = {N, D}, stride[2] = {dx->sr, 1};
+                t.sp_out = span_of(t.out, 2, 2, size, stride);
+            }
+            TROP_TRY(launch_tile<DX>(q.bf16, p_k, w_mn, t, sm, s));
+        }
+    }
+    if (dx && ks > 1) {
+        const int64_t size[2] = {N, D}, stride[2] = {dx->sr, 1};
+        const Span sp_out = span_of(dx->p, 2, 2, size, stride), sp_acc = span_bytes(acc, acc_bytes);
+        const dim3 grid(grid_for(N * D, sm));
+        const cudaError_t e = q.bf16 ? launch_pdl(k_split_join<true>, grid, dim3(256), 0, s, (const float*)acc, ks, N, D,
+                                                  (uint16_t*)dx->p, dx->sr, (const float*)scale, sp_acc, sp_out)
+                                     : launch_pdl(k_split_join<false>, grid, dim3(256), 0, s, (const float*)acc, ks, N, D,
+                                                  (uint16_t*)dx->p, dx->sr, (const float*)scale, sp_acc, sp_out);
+        if (e != cudaSuccess) return cuda_error(e, "k_split_join launch");
+        count_launches(1);
+    }
+    return TROP_OK;
+}
+
+// Rows of 16-bit elements set to zero (gradients of an empty sum).
+int launch_zero16(const Mat16& m, cudaStream_t s)
+{
+    const DeviceInfo* dev;
+    TROP_TRY(ensure_device(&dev));
+    const int64_t size[2] = {m.rows, m.cols}, stride[2] = {m.sr, 1};
+    const cudaError_t e = launch_pdl(k_zero16, dim3(grid_for(m.rows * m.cols, dev->sm_count)), dim3(256), 0, s,
+                                     (uint16_t*)m.p, m.sr, m.rows, m.cols, span_of(m.p, 2, 2, size, stride));
+    if (e != cudaSuccess) return cuda_error(e, "k_zero16 launch");
+    count_launches(1);
+    return TROP_OK;
+}
+
+}  // namespace trop

@@ -1,0 +1,444 @@
+"""Training operators: layer norm, the cross entropy of a linear head, AdamW.
+
+What stands around a tropical product and its gradient (``gemm``,
+``gemm_backward``, ``TropicalGemm``) when a model is trained with them.  Like
+the rest of the package these functions marshal torch CUDA tensors into the C
+ABI of ``include/tropical.h``; all computation runs in the library's kernels,
+on the current stream or the one given.
+"""
+
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+import einsum_device_side_gb300 as _pkg
+
+_CODES = {torch.float32: 0, torch.int32: 1, torch.int64: 2, torch.float64: 3, torch.bfloat16: 4, torch.float16: 5}
+BLOCK = 256  # elements that share one scale of an 8-bit AdamW state
+
+
+def _lib():
+    return _pkg._lib or _pkg.load()
+
+
+def _fail(code: int, message: str):
+    raise _pkg.TropicalError(code, message)
+
+
+def _desc(t):
+    """The C descriptor of a tensor, or None."""
+    if t is None:
+        return None
+    d = _pkg.TropTensor()
+    d.data = t.data_ptr() if t.numel() else None
+    d.dtype = _CODES.get(t.dtype, -1)
+    d.rank = t.dim()
+    if d.rank:
+        d.shape[:d.rank] = t.shape
+        d.stride[:d.rank] = t.stride()
+    return ctypes.byref(d)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _check_vector(t, name: str, like, dtype, n: int):
+    """A contiguous vector of n elements beside `like`, or None."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        _fail(-4, f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != (n,):
+        _fail(-5, f"{name} has shape {tuple(t.shape)}, not ({n},)")
+    if t.get_device() != like.get_device():
+        _fail(-3, f"{name} is on {t.device}, the operands on {like.device}")
+    if not t.is_contiguous():
+        _fail(-1, f"{name} must be contiguous")
+
+
+def _rows(t, name: str):
+    """[..., C] as a matrix (a copy only where the leading axes do not merge into one stride)."""
+    if t.dim() == 2:
+        return t
+    if t.dim() == 0:
+        _fail(-1, f"{name} has no axis")
+    return t.reshape(-1, t.shape[-1]) if t.numel() else t.new_empty((t.shape[:-1].numel(), t.shape[-1]))
+
+
+def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+               eps: float = 1e-5, out_dtype: torch.dtype | None = None, out: torch.Tensor | None = None, stream=None):
+    """Layer norm over the last axis: ``(x - mean) * rstd * weight + bias``.
+
+    ``x``: float32, bfloat16 or float16, its last axis contiguous.  ``weight`` and ``bias`` are optional, of one type:
+    x's or float32.  The result has x's type; a float32 ``x`` (a tropical product, say) may give ``out_dtype``
+    bfloat16 or float16.  Returns ``(y, mean, rstd)``, the float32 statistics with x's leading shape:
+    what ``layer_norm_backward`` reads."""
+    lib = _lib()
+    x2 = _rows(x, "x")
+    n, c = x2.shape
+    w = weight if weight is not None else bias
+    wdtype = w.dtype if w is not None else x.dtype
+    _check_vector(weight, "weight", x, wdtype, c)
+    _check_vector(bias, "bias", x, wdtype, c)
+    if out is None:
+        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+        y = out if x.dim() == 2 else out.view(n, c)
+    else:
+        if out.shape != x.shape or (out_dtype is not None and out.dtype != out_dtype):
+            _fail(-5, f"out is {tuple(out.shape)} {out.dtype}, not {tuple(x.shape)} {out_dtype or x.dtype}")
+        y = out if x.dim() == 2 else out.view(n, c)
+    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    rstd = torch.empty_like(mean)
+    if _pkg._fc is not None:
+        rc = _pkg._fc.layer_norm_t(x2, weight, bias, _CODES.get(wdtype, -1), eps, y, mean, rstd, stream)
+    else:
+        rc = lib.tropical_layer_norm(_desc(x2), _ptr(weight), _ptr(bias), _CODES.get(wdtype, -1), eps, _desc(y),
+                                     _ptr(mean), _ptr(rstd), _pkg._stream(stream, x))
+    if rc:
+        _pkg._check(rc)
+    return out, mean, rstd
+
+
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                        weight: torch.Tensor | None = None, *, want_x: bool = True, want_weight: bool = True,
+                        want_bias: bool = True, weight_dtype: torch.dtype | None = None, stream=None):
+    """Gradient of ``layer_norm``: ``(dx, dweight, dbias)``, an unwanted one None.  ``dy`` has the forward's result type;
+    the weight's and bias's gradients have ``weight``'s type (``weight_dtype`` without one, by default x's)."""
+    lib = _lib()
+    x2, dy2 = _rows(x, "x"), _rows(dy, "dy")
+    if dy.shape != x.shape:
+        _fail(-5, f"dy has shape {tuple(dy.shape)}, x {tuple(x.shape)}")
+    n, c = x2.shape
+    wdtype = weight.dtype if weight is not None else weight_dtype or x.dtype
+    _check_vector(weight, "weight", x, wdtype, c)
+    _check_vector(mean if mean.dim() == 1 else mean.view(-1), "mean", x, torch.float32, n)
+    _check_vector(rstd if rstd.dim() == 1 else rstd.view(-1), "rstd", x, torch.float32, n)
+    if dy.get_device() != x.get_device():
+        _fail(-3, f"dy is on {dy.device}, x on {x.device}")
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if want_x else None
+    dx2 = dx if dx is None or x.dim() == 2 else dx.view(n, c)
+    dw = torch.empty(c, dtype=wdtype, device=x.device) if want_weight else None
+    db = torch.empty(c, dtype=wdtype, device=x.device) if want_bias else None
+    code = _CODES.get(wdtype, -1)
+    if _pkg._fc is not None:
+        rc = _pkg._fc.layer_norm_backward_t(dy2, x2, mean, rstd, weight, code, dx2, dw, db, stream)
+    else:
+        rc = lib.tropical_layer_norm_backward(_desc(dy2), _desc(x2), _ptr(mean), _ptr(rstd), _ptr(weight), code,
+                                              _desc(dx2), _ptr(dw), _ptr(db), _pkg._stream(stream, x))
+    if rc:
+        _pkg._check(rc)
+    return dx, dw, db
+
+
+class LayerNorm(torch.autograd.Function):
+    """Autograd over layer norm: ``LayerNorm.apply(x, weight, bias, eps, out_dtype)``."""
+
+    @staticmethod
+    def forward(ctx, x, weight=None, bias=None, eps=1e-5, out_dtype=None):
+        y, mean, rstd = layer_norm(x, weight, bias, eps, out_dtype)
+        ctx.save_for_backward(x, weight, mean, rstd)
+        ctx.bias_dtype = None if bias is None else bias.dtype
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, weight, mean, rstd = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dx, dw, db = layer_norm_backward(dy if dy.stride(-1) == 1 else dy.contiguous(), x, mean, rstd, weight,
+                                         want_x=need[0], want_weight=need[1], want_bias=need[2],
+                                         weight_dtype=ctx.bias_dtype)
+        return dx, dw, db, None, None
+
+
+_REDUCTIONS = ("none", "mean", "sum")
+
+
+def _check_head(x, w, target):
+    if x.get_device() != w.get_device() or x.get_device() != target.get_device():
+        _fail(-3, f"x is on {x.device}, w on {w.device}, target on {target.device}")
+
+
+def linear_cross_entropy(x: torch.Tensor, w: torch.Tensor, target: torch.Tensor, reduction: str = "mean",
+                         ignore_index: int = -100, stream=None):
+    """Softmax cross entropy of the logits ``x @ w.T`` without forming them in memory.
+
+    ``x`` [N, D] and ``w`` [V, D]: both bfloat16 or both float16, any strides; ``target`` [N]: int32 or int64.  Returns
+    ``(loss, lse, kept)``: the loss (one per token for ``reduction="none"``, else a scalar; tokens whose target is
+    ``ignore_index`` have none), the log-sum-exp of each token's logits, and the number of tokens kept, all float32.
+    A target outside the vocabulary gives NaN."""
+    lib = _lib()
+    if reduction not in _REDUCTIONS:
+        _fail(-1, f"reduction must be one of {_REDUCTIONS}, got {reduction!r}")
+    _check_head(x, w, target)
+    n = x.shape[0] if x.dim() else 0
+    few = torch.empty(2, dtype=torch.float32, device=x.device)
+    total, kept = few[0], few[1]
+    each = torch.empty((2, n) if reduction == "none" else (1, n), dtype=torch.float32, device=x.device)
+    lse = each[-1]
+    loss = each[0] if reduction == "none" else None
+    if _pkg._fc is not None:
+        rc = _pkg._fc.linear_ce_t(x, w, target, ignore_index, reduction == "mean", loss, lse,
+                                  total if loss is None else None, kept, stream)
+    else:
+        rc = lib.tropical_linear_cross_entropy(_desc(x), _desc(w), _desc(target), ignore_index, reduction == "mean",
+                                               _ptr(loss), _ptr(lse), _ptr(total) if loss is None else None, _ptr(kept),
+                                               _pkg._stream(stream, x))
+    if rc:
+        _pkg._check(rc)
+    return total if loss is None else loss, lse, kept
+
+
+def linear_cross_entropy_backward(dloss: torch.Tensor, x: torch.Tensor, w: torch.Tensor, target: torch.Tensor,
+                                  lse: torch.Tensor, kept: torch.Tensor | None = None, ignore_index: int = -100, *,
+                                  want_x: bool = True, want_w: bool = True, stream=None):
+    """Gradient of ``linear_cross_entropy``: ``(dx, dw)`` in the operands' type, an unwanted one None.
+
+    ``dloss``: float32, one per token or a scalar for all of them.  With ``kept`` (the mean's gradient) it is divided by
+    that count.  The logits are formed again in pieces of the vocabulary."""
+    lib = _lib()
+    _check_head(x, w, target)
+    if dloss.dtype != torch.float32:
+        _fail(-4, f"dloss must be float32, got {dloss.dtype}")
+    if dloss.dim() > 1 or (dloss.dim() == 1 and dloss.shape[0] != x.shape[0]):
+        _fail(-5, f"dloss has shape {tuple(dloss.shape)}: one per token or a scalar is wanted")
+    _check_vector(lse, "lse", x, torch.float32, x.shape[0])
+    if kept is not None and (kept.dtype != torch.float32 or kept.numel() != 1):
+        _fail(-4, "kept must be one float32")
+    for t, name in ((dloss, "dloss"), (kept, "kept")):
+        if t is not None and t.get_device() != x.get_device():
+            _fail(-3, f"{name} is on {t.device}, x on {x.device}")
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if want_x else None
+    dw = torch.empty(w.shape, dtype=w.dtype, device=w.device) if want_w else None
+    stride = dloss.stride(0) if dloss.dim() else 0
+    if _pkg._fc is not None:
+        rc = _pkg._fc.linear_ce_backward_t(dloss, stride, x, w, target, ignore_index, lse, kept, dx, dw, stream)
+    else:
+        rc = lib.tropical_linear_cross_entropy_backward(_ptr(dloss), stride, _desc(x), _desc(w), _desc(target),
+                                                        ignore_index, _ptr(lse), _ptr(kept), _desc(dx), _desc(dw),
+                                                        _pkg._stream(stream, x))
+    if rc:
+        _pkg._check(rc)
+    return dx, dw
+
+
+class LinearCrossEntropy(torch.autograd.Function):
+    """Autograd over the head's loss: ``LinearCrossEntropy.apply(x, w, target, reduction, ignore_index)``."""
+
+    @staticmethod
+    def forward(ctx, x, w, target, reduction="mean", ignore_index=-100):
+        loss, lse, kept = linear_cross_entropy(x, w, target, reduction, ignore_index)
+        ctx.save_for_backward(x, w, target, lse, kept)
+        ctx.reduction, ctx.ignore_index = reduction, ignore_index
+        return loss
+
+    @staticmethod
+    def backward(ctx, dloss):
+        x, w, target, lse, kept = ctx.saved_tensors
+        dx, dw = linear_cross_entropy_backward(dloss, x, w, target, lse, kept if ctx.reduction == "mean" else None,
+                                               ctx.ignore_index, want_x=ctx.needs_input_grad[0],
+                                               want_w=ctx.needs_input_grad[1])
+        return dx, dw, None, None, None
+
+
+class _Tensor(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in ("param", "grad", "exp_avg", "exp_avg_sq", "exp_avg_scale",
+                                               "exp_avg_sq_scale", "copy")] + [("numel", ctypes.c_int64)]
+
+
+class _State(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in ("exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale",
+                                               "exp_avg_value", "exp_avg_sq_value")] + [("numel", ctypes.c_int64)]
+
+
+class _Options(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_double) for k in ("lr", "beta1", "beta2", "eps", "weight_decay", "grad_scale")] + \
+               [("step", ctypes.c_int64)]
+
+
+def _column(ts, name: str, n: int, dtype, sizes, device):
+    """The addresses of a list of contiguous tensors of one type and of these sizes."""
+    if len(ts) != n:
+        _fail(-5, f"{len(ts)} tensors in {name} for {n} parameters")
+    out = []
+    for i, (t, size) in enumerate(zip(ts, sizes)):
+        if t.dtype != dtype:
+            _fail(-4, f"{name}[{i}] must be {dtype}, got {t.dtype}")
+        if t.numel() != size:
+            _fail(-5, f"{name}[{i}] has {t.numel()} elements, not {size}")
+        if t.get_device() != device:
+            _fail(-3, f"{name}[{i}] is on {t.device}, the parameters on cuda:{device}")
+        if not t.is_contiguous():
+            _fail(-1, f"{name}[{i}] must be contiguous")
+        out.append(t.data_ptr() or None)
+    return out
+
+
+def _table(params, grads, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, copies):
+    n = len(params)
+    if n == 0:
+        return (_Tensor * 1)(), 0, 0, 0, 32, 0, [], -1
+    sizes = [p.numel() for p in params]
+    device, pdtype, gdtype = params[0].get_device(), params[0].dtype, grads[0].dtype if len(grads) else params[0].dtype
+    if (exp_avg_scale is None) != (exp_avg_sq_scale is None):
+        _fail(-1, "8-bit states have scales of both moments")
+    bits = 32 if exp_avg_scale is None else 8
+    mdtype, vdtype = (torch.float32, torch.float32) if bits == 32 else (torch.int8, torch.uint8)
+    columns = {"param": _column(params, "params", n, pdtype, sizes, device),
+               "grad": _column(grads, "grads", n, gdtype, sizes, device),
+               "exp_avg": _column(exp_avg, "exp_avg", n, mdtype, sizes, device),
+               "exp_avg_sq": _column(exp_avg_sq, "exp_avg_sq", n, vdtype, sizes, device)}
+    if bits == 8:
+        blocks = [-(-s // BLOCK) for s in sizes]
+        columns["exp_avg_scale"] = _column(exp_avg_scale, "exp_avg_scale", n, torch.float32, blocks, device)
+        columns["exp_avg_sq_scale"] = _column(exp_avg_sq_scale, "exp_avg_sq_scale", n, torch.float32, blocks, device)
+    cdtype = 0
+    if copies is not None and len(copies):
+        cdtype = _CODES.get(copies[0].dtype, -1)
+        columns["copy"] = _column(copies, "copies", n, copies[0].dtype, sizes, device)
+    table = (_Tensor * n)()
+    for i, e in enumerate(table):
+        for k, v in columns.items():
+            setattr(e, k, v[i])
+        e.numel = sizes[i]
+    return table, n, _CODES.get(pdtype, -1), _CODES.get(gdtype, -1), bits, cdtype, sizes, device
+
+
+def _state_table(exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, out):
+    n = len(exp_avg)
+    sizes = [t.numel() for t in exp_avg]
+    blocks = [-(-s // BLOCK) for s in sizes]
+    device = exp_avg[0].get_device() if n else -1
+    columns = {"exp_avg": _column(exp_avg, "exp_avg", n, torch.int8, sizes, device),
+               "exp_avg_sq": _column(exp_avg_sq, "exp_avg_sq", n, torch.uint8, sizes, device),
+               "exp_avg_scale": _column(exp_avg_scale, "exp_avg_scale", n, torch.float32, blocks, device),
+               "exp_avg_sq_scale": _column(exp_avg_sq_scale, "exp_avg_sq_scale", n, torch.float32, blocks, device),
+               "exp_avg_value": _column(out[0], "out[0]", n, torch.float32, sizes, device),
+               "exp_avg_sq_value": _column(out[1], "out[1]", n, torch.float32, sizes, device)}
+    table = (_State * max(1, n))()
+    for i in range(n):
+        for k, v in columns.items():
+            setattr(table[i], k, v[i])
+        table[i].numel = sizes[i]
+    return table, n
+
+
+def adamw_step(params, grads, exp_avg, exp_avg_sq, exp_avg_scale=None, exp_avg_sq_scale=None, *, step: int,
+               lr: float = 1e-3, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+               weight_decay: float = 0.01, grad_scale: float = 1.0, copies=None, stream=None):
+    """One AdamW step over lists of tensors, in place; ``step`` counts from 1.
+
+    ``params``: float32, bfloat16 or float16, all of one type; ``grads`` of one type (any for float32 parameters, else
+    the parameters' or float32).  States: float32 like the parameters, or 8-bit codes (int8 ``exp_avg``, uint8
+    ``exp_avg_sq``) with their float32 scales, one for every 256 elements.  ``copies``: 16-bit copies of float32
+    parameters that the step writes too.  Every tensor is contiguous.  A program that steps the same tensors again and
+    again keeps an ``AdamWPlan`` (or ``AdamW``), which reads the lists once."""
+    lib = _lib()
+    table, n, p, g, bits, c, _, device = _table(params, grads, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, copies)
+    o = _Options(lr, beta1, beta2, eps, weight_decay, grad_scale, step)
+    _pkg._check(lib.tropical_adamw_step(n, table, p, g, bits, c, ctypes.byref(o),
+                                        _pkg._stream(stream, params[0] if n else None) if n else None))
+
+
+def adamw_state_values(exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, out=None, stream=None):
+    """8-bit AdamW states as the values they stand for: two lists of float32 tensors (``out``: the lists to fill)."""
+    lib = _lib()
+    if out is None:
+        out = tuple([torch.empty(t.shape, dtype=torch.float32, device=t.device) for t in ts] for ts in (exp_avg, exp_avg_sq))
+    table, n = _state_table(exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, out)
+    _pkg._check(lib.tropical_adamw_state_values(n, table, _pkg._stream(stream, exp_avg[0]) if n else None))
+    return out
+
+
+class AdamWPlan:
+    """AdamW steps over the tensors given here (the lists of ``adamw_step``), checked and laid out once.  Like a tree plan
+    it binds the buffers: ``step`` reads the gradients' current contents and updates parameters and states in place.
+    ``values``: a pair of lists of float32 tensors that ``state_values`` fills from 8-bit states.  The tensors are kept
+    referenced for the plan's lifetime."""
+
+    def __init__(self, params, grads, exp_avg, exp_avg_sq, exp_avg_scale=None, exp_avg_sq_scale=None, *, copies=None,
+                 values=None):
+        lib = _lib()
+        self._h = None
+        lists = (params, grads, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, copies)
+        table, n, p, g, bits, c, _, _ = _table(*lists)
+        states = None
+        if values is not None:
+            if bits != 8:
+                _fail(-1, "values of states that are not in 8 bits")
+            states, _ = _state_table(exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, values)
+        h = ctypes.c_void_p()
+        _pkg._check(lib.tropical_adamw_plan_create(n, table, p, g, bits, c, states, ctypes.byref(h)))
+        self._h = h.value
+        self._keep = [None if t is None else list(t) for t in lists]
+        self._like = params[0] if n else torch.empty(0, device="cuda")
+        self.values = values
+
+    def step(self, step: int, lr: float = 1e-3, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+             weight_decay: float = 0.01, grad_scale: float = 1.0, stream=None):
+        """One step; ``step`` counts from 1."""
+        if self._h is None:
+            raise RuntimeError("plan is closed")
+        if _pkg._fc is not None:
+            rc = _pkg._fc.adamw_plan_step(self._h, lr, beta1, beta2, eps, weight_decay, grad_scale, step, self._like,
+                                          stream)
+        else:
+            o = _Options(lr, beta1, beta2, eps, weight_decay, grad_scale, step)
+            rc = _pkg._lib.tropical_adamw_plan_step(self._h, ctypes.byref(o), _pkg._stream(stream, self._like))
+        if rc:
+            _pkg._check(rc)
+
+    def state_values(self, stream=None):
+        """Fills and returns ``values``."""
+        if self._h is None:
+            raise RuntimeError("plan is closed")
+        _pkg._check(_pkg._lib.tropical_adamw_plan_values(self._h, _pkg._stream(stream, self._like)))
+        return self.values
+
+    def close(self):
+        if getattr(self, "_h", None) is not None:
+            _pkg._check(_pkg._lib.tropical_adamw_plan_destroy(self._h))
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class AdamW:
+    """AdamW with its states: ``AdamW(params, grads, state_bits=8)``, then ``step()`` whenever the gradients' buffers hold
+    new ones.  ``grads`` are the buffers the backward pass writes (``p.grad`` of each parameter by default, which must
+    exist and stay in place).  ``copies`` as in ``adamw_step``."""
+
+    def __init__(self, params, grads=None, lr: float = 1e-3, beta1: float = 0.9, beta2: float = 0.999,
+                 eps: float = 1e-8, weight_decay: float = 0.01, state_bits: int = 32, copies=None):
+        params = [p.detach() for p in params] if grads is not None else list(params)
+        if grads is None:
+            grads = [p.grad for p in params]
+            if any(g is None for g in grads):
+                _fail(-1, "a parameter has no gradient buffer")
+            params = [p.detach() for p in params]
+        if state_bits not in (8, 32):
+            _fail(-1, f"states of {state_bits} bits")
+        new = lambda p, dtype, n=None: torch.zeros(p.shape if n is None else n, dtype=dtype, device=p.device)  # noqa: E731
+        self.params, self.grads, self.steps = params, list(grads), 0
+        self.options = dict(lr=lr, beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay)
+        self.exp_avg_scale = self.exp_avg_sq_scale = None
+        if state_bits == 32:
+            self.exp_avg = [new(p, torch.float32) for p in params]
+            self.exp_avg_sq = [new(p, torch.float32) for p in params]
+        else:
+            self.exp_avg = [new(p, torch.int8) for p in params]
+            self.exp_avg_sq = [new(p, torch.uint8) for p in params]
+            self.exp_avg_scale = [new(p, torch.float32, -(-p.numel() // BLOCK)) for p in params]
+            self.exp_avg_sq_scale = [new(p, torch.float32, -(-p.numel() // BLOCK)) for p in params]
+        self._plan = AdamWPlan(params, self.grads, self.exp_avg, self.exp_avg_sq, self.exp_avg_scale,
+                               self.exp_avg_sq_scale, copies=copies)
+
+    def step(self, grad_scale: float = 1.0, stream=None):
+        self.steps += 1
+        self._plan.step(self.steps, grad_scale=grad_scale, stream=stream, **self.options)

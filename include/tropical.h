@@ -86,7 +86,9 @@ extern "C" {
 #define TROP_MAX_RANK 32
 
 typedef enum { TROP_MAXPLUS = 0, TROP_MINPLUS = 1, TROP_MAXTIMES = 2 } trop_semiring;
-typedef enum { TROP_F32 = 0, TROP_I32 = 1, TROP_I64 = 2, TROP_F64 = 3 } trop_dtype;
+/* TROP_BF16 and TROP_F16 are types of the training operators only; the tropical operations refuse
+ * them with TROP_ERR_DTYPE. */
+typedef enum { TROP_F32 = 0, TROP_I32 = 1, TROP_I64 = 2, TROP_F64 = 3, TROP_BF16 = 4, TROP_F16 = 5 } trop_dtype;
 
 enum {
     TROP_OK = 0,
@@ -354,6 +356,148 @@ int tropical_tree_backtrack(int n_inputs, const trop_tensor* inputs, int n_nodes
                             const trop_node* nodes, int32_t* const* node_argmax,
                             int64_t root_index, int n_labels, int32_t* assignment, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Training operators: what stands around a tropical product and its gradient
+ * (tropical_gemm_backward) when a model is trained with them -- a norm between
+ * layers, a loss with its gradient at the end, the update that applies the
+ * gradients [PR35's batched autograd functions are the training interface
+ * these complete; they have no counterpart on the pages].  Types: f32, bf16,
+ * f16 as stated at each; every sum and statistic is held in f32 and every
+ * stored value rounded once.  Results repeat bit for bit (no atomics in any
+ * sum).  The conventions at the top of this file hold.
+ * ------------------------------------------------------------------------- */
+
+/* Layer norm over the last axis of x [rows, cols]:
+ *   mean = sum x / cols, rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps),
+ *   y = (x - mean) rstd weight + bias.
+ * x, y: f32, bf16 or f16, the last axis contiguous, any row stride (0 allowed
+ * for x); y has x's type, or bf16 or f16 beside an f32 x.  weight, bias:
+ * nullable [cols], contiguous, both of type wdtype: x's or f32.  mean, rstd:
+ * nullable f32 [rows], what the backward call reads.
+ * Errors: INVALID_ARG, SHAPE (cols == 0 or shapes differ), DTYPE, UNSUPPORTED
+ * (last axis strided, an extent of 2^31 - 1024 or more), HOST_POINTER,
+ * DEVICE_MISMATCH, CUDA. */
+int tropical_layer_norm(const trop_tensor* x, const void* weight, const void* bias, int wdtype, double eps,
+                        const trop_tensor* y, float* mean, float* rstd, void* stream);
+
+/* Backward of tropical_layer_norm: with h = (x - mean) rstd and u = dy weight,
+ *   dx = rstd (u - mean_cols(u) - h mean_cols(u h)),
+ *   dweight = sum over the rows of dy h, dbias = sum over the rows of dy.
+ * dy has y's type; dx x's; dweight and dbias wdtype.  Each of the three is
+ * nullable (not wanted).  weight NULL counts as ones.  No row: zeros.
+ * Errors: as tropical_layer_norm, plus OOM. */
+int tropical_layer_norm_backward(const trop_tensor* dy, const trop_tensor* x, const float* mean, const float* rstd,
+                                 const void* weight, int wdtype, const trop_tensor* dx, void* dweight, void* dbias,
+                                 void* stream);
+
+/* Softmax cross entropy of a linear head, without keeping the logits: tokens
+ * x [N, D], weights w [V, D] (both bf16 or both f16, any strides), target [N]
+ * (i32 or i64, any stride); l = x w^T with f32 sums,
+ *   lse[i] = log sum_v exp l[i, v],  loss[i] = lse[i] - l[i, target[i]].
+ * A token whose target is ignore_index has loss 0 and counts nowhere; any
+ * other target outside [0, V) gives a NaN loss (and NaN gradients).
+ * lse: f32 [N], what the backward call reads.  loss: nullable f32 [N].
+ * total: nullable f32, the losses' sum, or with mean != 0 that over the tokens
+ * kept (NaN if there is none).  kept: nullable f32, the number of those.
+ * Operands whose rows TMA cannot read (a last axis that is not contiguous,
+ * rows that do not start on 16 bytes) are packed into workspace first.
+ * Errors: INVALID_ARG, SHAPE (D or V zero, shapes differ), DTYPE, UNSUPPORTED
+ * (extents of 2^31 - 1024 or more, too many tiles), HOST_POINTER,
+ * DEVICE_MISMATCH, OOM, CUDA. */
+int tropical_linear_cross_entropy(const trop_tensor* x, const trop_tensor* w, const trop_tensor* target,
+                                  int64_t ignore_index, int mean, float* loss, float* lse, float* total, float* kept,
+                                  void* stream);
+
+/* Backward of tropical_linear_cross_entropy: with g[i] = dloss[i * dloss_stride]
+ * (over *kept when kept is given: the mean's gradient; stride 0: one gradient
+ * for all tokens) and P[i, v] = g[i] (exp(l[i, v] - lse[i]) - [v == target[i]]),
+ *   dx = P w,  dw = P^T x.
+ * The logits are formed again, in pieces of the vocabulary; P is rounded to
+ * the operands' type for the two products (in f16 scaled by 2^14 / max |g|
+ * first, so that small probabilities keep their digits), whose sums are f32.
+ * dx, dw: nullable, the operands' type and shapes, last axis contiguous.
+ * Workspace: P of one piece (at most 512 MiB, or 4096 columns), and the f32
+ * sums of dx when its depth is split or comes in several pieces.
+ * Errors: as tropical_linear_cross_entropy. */
+int tropical_linear_cross_entropy_backward(const float* dloss, int64_t dloss_stride, const trop_tensor* x,
+                                           const trop_tensor* w, const trop_tensor* target, int64_t ignore_index,
+                                           const float* lse, const float* kept, const trop_tensor* dx,
+                                           const trop_tensor* dw, void* stream);
+
+/* One tensor of an AdamW step: numel contiguous elements everywhere.  exp_avg
+ * and exp_avg_sq are f32, or with 8-bit states int8 and uint8 with one f32
+ * scale for every 256 consecutive elements (the last block may be short).
+ * copy: nullable, a 16-bit copy of f32 parameters that the step writes too. */
+typedef struct {
+    void* param;
+    const void* grad;
+    void* exp_avg;
+    void* exp_avg_sq;
+    float* exp_avg_scale;
+    float* exp_avg_sq_scale;
+    void* copy;
+    int64_t numel;
+} trop_adamw_tensor;
+
+/* Scalars of a step; each is taken to f32 once (1 - beta and the bias
+ * corrections from the doubles).  step: 1 for the first.  grad_scale
+ * multiplies the gradients (1: none). */
+typedef struct {
+    double lr, beta1, beta2, eps, weight_decay, grad_scale;
+    int64_t step;
+} trop_adamw_options;
+
+/* One AdamW step (decoupled weight decay) over n tensors, in place:
+ *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2,
+ *   p = p (1 - lr weight_decay)
+ *       - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * in f32, every operation rounded once, none contracted.  Parameters of
+ * param_dtype (f32, bf16, f16), gradients of grad_dtype (any of these for f32
+ * parameters, else the parameters' or f32).  state_bits 32 or 8.  8-bit codes:
+ * m is c |c| scale with scale = max |m| / 127^2 over the block, sqrt(v) is
+ * c^2 scale with scale = max sqrt(v) / 255^2, c rounded to nearest in the
+ * square root's domain and at least 1 for sqrt(v) > 0 (both scales formed as a
+ * product with the f32 nearest 1 / 127^2 and 1 / 255^2); a block in which a new
+ * state is not finite reads back as NaN.  The step uses the unrounded states.
+ * The tensor table is read during the call only.
+ * Errors: INVALID_ARG, DTYPE, UNSUPPORTED (a tensor of 2^43 elements or more),
+ * HOST_POINTER, DEVICE_MISMATCH, CUDA. */
+int tropical_adamw_step(int64_t n, const trop_adamw_tensor* tensors, int param_dtype, int grad_dtype, int state_bits,
+                        int copy_dtype, const trop_adamw_options* options, void* stream);
+
+/* A plan of AdamW steps: the tensors checked and their table laid out once.  It
+ * binds the buffers given here (as a tree plan does): every step reads the
+ * current contents of the gradients and updates parameters and states in
+ * place.  The caller keeps the buffers alive while the plan is used.  Create's
+ * errors are tropical_adamw_step's (*plan is NULL on failure); step's are
+ * INVALID_ARG, DEVICE_MISMATCH (the plan is another device's) and CUDA.
+ * tropical_adamw_plan_values writes the values of 8-bit states (see below) to
+ * the buffers of `states`, which were given at creation (nullable; INVALID_ARG
+ * if they were not).  Steps of one plan from several host threads are the
+ * caller's to order.  Destroying a plan while a step runs is allowed: the
+ * launch carries its table. */
+typedef struct trop_adamw_plan_s* trop_adamw_plan;
+struct trop_adamw_state_s;
+int tropical_adamw_plan_create(int64_t n, const trop_adamw_tensor* tensors, int param_dtype, int grad_dtype,
+                               int state_bits, int copy_dtype, const struct trop_adamw_state_s* states,
+                               trop_adamw_plan* plan);
+int tropical_adamw_plan_step(trop_adamw_plan plan, const trop_adamw_options* options, void* stream);
+int tropical_adamw_plan_values(trop_adamw_plan plan, void* stream);
+int tropical_adamw_plan_destroy(trop_adamw_plan plan);
+
+/* 8-bit states as the f32 values they stand for (exp_avg_value: m;
+ * exp_avg_sq_value: v), for checkpoints, inspection or a change to 32 bits. */
+typedef struct trop_adamw_state_s {
+    const void* exp_avg;
+    const void* exp_avg_sq;
+    const float* exp_avg_scale;
+    const float* exp_avg_sq_scale;
+    float* exp_avg_value;
+    float* exp_avg_sq_value;
+    int64_t numel;
+} trop_adamw_state;
+int tropical_adamw_state_values(int64_t n, const trop_adamw_state* states, void* stream);
+
 /* Drain the workspace retirement queue: wait for every pending event and
  * return the blocks to the pool [WR "Open decisions" 1: explicit
  * synchronize() is a drain point].  The only call that may block the host. */
@@ -390,7 +534,8 @@ int tropical_device_wait_timeouts(unsigned int* count, int reset);
  * (computed on the host from extents and strides); an access outside it is
  * skipped and counted, and the first one's location and address kept.
  * *line = (file id << 16) | source line, the file ids being 1 unary.cu, 2
- * gemm.cu, 3 gemm64.cu, 4 gemm_int.cu, 5 backward.cu, 6 backtrack.cu.
+ * gemm.cu, 3 gemm64.cu, 4 gemm_int.cu, 5 backward.cu, 6 backtrack.cu, 7
+ * layer_norm.cu, 8 adamw.cu, 9 linear_ce.cu.
  * Reads the record of the current device without synchronising: call it once
  * the work to inspect has completed.  reset != 0 clears the record.  The
  * normal build returns TROP_ERR_UNSUPPORTED with *count = 0.  It stands in
