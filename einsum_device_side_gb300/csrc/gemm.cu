@@ -1900,10 +1900,6 @@ EncodeTiledFn encode_tiled()
     return state.load(std::memory_order_acquire) == 1 ? fn.load(std::memory_order_relaxed) : nullptr;
 }
 
-}  // namespace
-void* tensor_map_encoder() { return (void*)encode_tiled(); }
-namespace {
-
 // A 3-D tensor map of a row-major f32 operand [batch][rows][cols] (cols contiguous) with a
 // [1][box_rows][box_cols] box; false when TMA cannot describe it (the caller keeps the
 // cp.async kernel).  Strides in elements.

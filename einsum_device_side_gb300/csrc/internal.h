@@ -266,8 +266,6 @@ int launch_gemm(const GemmDesc& g, cudaStream_t s, const char** kernel_name);
 int launch_gemm_f64(const GemmDesc& g, cudaStream_t s);
 // The integer GEMM (gemm_int.cu); launch_gemm forwards TROP_I32 / TROP_I64 descriptors here.
 int launch_gemm_int(const GemmDesc& g, cudaStream_t s);
-// cuTensorMapEncodeTiled from the driver (nullptr if it is not available).
-void* tensor_map_encoder();
 // The route launch_gemm takes for g (kernel, operand swap, vector width, staging) as text.
 void describe_gemm(const GemmDesc& g, char* buf, size_t n);
 

@@ -587,11 +587,26 @@ __global__ void __launch_bounds__(256) k_zero16(uint16_t* out, int64_t sr, int64
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+// from the driver, looked up once (the library does not link against libcuda); nullptr if it is not there
+EncodeTiledFn encode_tiled()
+{
+    static const EncodeTiledFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            p = nullptr;
+        }
+        return (EncodeTiledFn)p;
+    }();
+    return fn;
+}
 
 // a row-major 16-bit matrix, its rows 16-byte aligned, read in boxes of `box_rows` x 64
 int make_map(CUtensorMap* map, bool bf16, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows)
 {
-    const EncodeTiledFn enc = (EncodeTiledFn)tensor_map_encoder();
+    const EncodeTiledFn enc = encode_tiled();
     if (!enc) return set_error(TROP_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * 2};
     const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, one[2] = {1, 1};
