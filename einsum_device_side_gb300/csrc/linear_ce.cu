@@ -40,7 +40,7 @@ namespace {
 
 enum { LSE = 0, GRAD = 1, DX = 2, DW = 3 };
 
-constexpr int CG = 1;                 // CTAs that share an accumulator tile
+constexpr int CG = 2;                 // CTAs that share an accumulator tile
 constexpr int TM = 128 * CG;          // rows of an output tile
 constexpr int TN = 256;               // columns
 constexpr int TK = 64;                // depth of a stage: one 128-byte row of 16-bit elements
