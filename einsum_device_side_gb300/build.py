@@ -33,7 +33,7 @@ VARIANTS = {"release": (BUILD, LIB, []), "debug": (BUILD_DEBUG, LIB_DEBUG, ["-DT
 SOURCES = ["runtime.cpp", "api.cpp", "unary.cu", "gemm.cu", "gemm64.cu", "gemm_int.cu", "backtrack.cu", "backward.cu",
            "noalloc.cu"]
 TRAIN = ["train.cpp", "layer_norm.cu", "adamw.cu", "linear_ce.cu"]  # the training operators
-SOURCES += TRAIN
+SOURCES += TRAIN + ["scratch.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fno-strict-aliasing",
           "-ftz=false", "-prec-div=true", "-prec-sqrt=true", "-fmad=false",
@@ -53,7 +53,7 @@ def _stale(obj: str, src: str) -> bool:
     deps = [src, os.path.join(CSRC, "internal.h"), os.path.join(CSRC, "bounds.h"),
             os.path.join(ROOT, "include", "tropical.h")]
     if os.path.basename(src) in TRAIN:
-        deps += [os.path.join(CSRC, "train.h"), os.path.join(CSRC, "tcgen05.h")]
+        deps += [os.path.join(CSRC, h) for h in ("train.h", "tcgen05.h", "packed.h")]
     return any(os.path.getmtime(d) > os.path.getmtime(obj) for d in deps)
 
 

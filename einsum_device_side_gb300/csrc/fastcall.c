@@ -321,49 +321,145 @@ static int as_double(PyObject* o, double* out)
     return (*out == -1.0 && PyErr_Occurred()) ? -1 : 0;
 }
 
-/* layer_norm_t(x, weight or None, bias or None, wdtype, eps, y, mean or None, rstd or None, stream or None) */
+/* The device number of a tensor object, -1 for the host's; -2 on error. */
+static long obj_device(PyObject* obj)
+{
+    PyObject* d = PyObject_CallMethodNoArgs(obj, s_get_device);
+    if (!d) return -2;
+    const long v = PyLong_AsLong(d);
+    Py_DECREF(d);
+    return v == -1 && PyErr_Occurred() ? -2 : v;
+}
+
+/* A function below that is given something out of the ordinary (a vector that is strided, of another
+ * length or type, on another device) returns PLAIN_PATH and launches nothing: the Python wrapper
+ * then checks every argument by itself and says which it was. */
+#define PLAIN_PATH 1
+
+/* A vector of n contiguous elements of `dtype` on `device`, or None: 0 with its address, PLAIN_PATH, or -1. */
+static int obj_vector(PyObject* obj, int64_t n, int32_t dtype, long device, void** out)
+{
+    *out = NULL;
+    if (obj == Py_None) return 0;
+    trop_tensor t;
+    if (obj_tensor_of(&t, obj, N_DTYPES) < 0) return -1;
+    const long d = obj_device(obj);
+    if (d == -2) return -1;
+    int64_t count = 1;
+    for (int i = t.rank - 1; i >= 0; --i) {
+        if (t.shape[i] != 1 && t.stride[i] != count) return PLAIN_PATH;
+        count *= t.shape[i];
+    }
+    *out = t.data;
+    return count == n && t.dtype == dtype && d == device ? 0 : PLAIN_PATH;
+}
+#define VECTOR(obj, n, dtype, out)                                        \
+    do {                                                                  \
+        const int v_ = obj_vector((obj), (n), (dtype), device, (out));    \
+        if (v_ < 0) return NULL;                                          \
+        if (v_ > 0) return PyLong_FromLong(PLAIN_PATH);                   \
+    } while (0)
+
+/* [..., C] as a matrix: the leading axes merged where they make one stride, else PLAIN_PATH. */
+static int as_rows(trop_tensor* t)
+{
+    if (t->rank == 2) return 0;
+    if (t->rank < 2) return PLAIN_PATH;
+    int64_t rows = 1, stride = 0;
+    for (int i = t->rank - 2; i >= 0; --i) {
+        if (t->shape[i] == 1) continue;
+        if (t->shape[i] == 0) return PLAIN_PATH;
+        if (rows > 1 && t->stride[i] != rows * stride) return PLAIN_PATH;
+        if (rows == 1) stride = t->stride[i];
+        rows *= t->shape[i];
+    }
+    const int64_t c = t->shape[t->rank - 1], sc = t->stride[t->rank - 1];
+    t->shape[0] = rows;
+    t->stride[0] = rows > 1 ? stride : c;
+    t->shape[1] = c;
+    t->stride[1] = sc;
+    t->rank = 2;
+    return 0;
+}
+static int32_t dtype_or(PyObject* obj, int32_t other)
+{
+    if (obj == Py_None) return other;
+    PyObject* dt = PyObject_GetAttr(obj, s_dtype);
+    if (!dt) return -2;
+    int32_t code = -1;
+    for (int i = 0; i < N_DTYPES; ++i)
+        if (dt == g_dtype_obj[i]) code = i;
+    Py_DECREF(dt);
+    return code;
+}
+
+/* layer_norm_t(x, weight or None, bias or None, eps, y, mean, rstd, stream or None) */
 static PyObject* fc_layer_norm_t(PyObject* self, PyObject* const* a, Py_ssize_t nargs)
 {
     (void)self;
-    if (check_nargs(nargs, 9, "layer_norm_t") < 0) return NULL;
+    if (check_nargs(nargs, 8, "layer_norm_t") < 0) return NULL;
     trop_tensor x, y;
     void *w, *b, *mean, *rstd, *stream;
-    int64_t wdtype;
     double eps;
-    if (obj_tensor_of(&x, a[0], N_DTYPES) < 0 || obj_ptr(a[1], &w) < 0 || obj_ptr(a[2], &b) < 0 ||
-        as_i64(a[3], &wdtype) < 0 || as_double(a[4], &eps) < 0 || obj_tensor_of(&y, a[5], N_DTYPES) < 0 ||
-        obj_ptr(a[6], &mean) < 0 || obj_ptr(a[7], &rstd) < 0 || obj_stream(a[8], a[0], &stream) < 0)
+    if (obj_tensor_of(&x, a[0], N_DTYPES) < 0 || as_double(a[3], &eps) < 0 || obj_tensor_of(&y, a[4], N_DTYPES) < 0 ||
+        obj_stream(a[7], a[0], &stream) < 0)
         return NULL;
+    if (as_rows(&x) || as_rows(&y)) return PyLong_FromLong(PLAIN_PATH);
+    const long device = obj_device(a[0]);
+    const int32_t wdtype = dtype_or(a[1] != Py_None ? a[1] : a[2], x.dtype);
+    if (device == -2 || wdtype == -2) return NULL;
+    VECTOR(a[1], x.shape[1], wdtype, &w);
+    VECTOR(a[2], x.shape[1], wdtype, &b);
+    VECTOR(a[5], x.shape[0], TROP_F32, &mean);
+    VECTOR(a[6], x.shape[0], TROP_F32, &rstd);
     int rc;
     Py_BEGIN_ALLOW_THREADS
-    rc = tropical_layer_norm(&x, w, b, (int)wdtype, eps, &y, (float*)mean, (float*)rstd, stream);
+    rc = tropical_layer_norm(&x, w, b, wdtype, eps, &y, (float*)mean, (float*)rstd, stream);
     Py_END_ALLOW_THREADS
     return PyLong_FromLong(rc);
 }
 
-/* layer_norm_backward_t(dy, x, mean, rstd, weight or None, wdtype, dx or None, dweight or None, dbias or None,
+/* layer_norm_backward_t(dy, x, mean, rstd, weight or None, dx or None, dweight or None, dbias or None,
  * stream or None) */
 static PyObject* fc_layer_norm_backward_t(PyObject* self, PyObject* const* a, Py_ssize_t nargs)
 {
     (void)self;
-    if (check_nargs(nargs, 10, "layer_norm_backward_t") < 0) return NULL;
+    if (check_nargs(nargs, 9, "layer_norm_backward_t") < 0) return NULL;
     trop_tensor dy, x, dx;
     void *mean, *rstd, *w, *dw, *db, *stream;
-    int64_t wdtype;
-    if (obj_tensor_of(&dy, a[0], N_DTYPES) < 0 || obj_tensor_of(&x, a[1], N_DTYPES) < 0 || obj_ptr(a[2], &mean) < 0 ||
-        obj_ptr(a[3], &rstd) < 0 || obj_ptr(a[4], &w) < 0 || as_i64(a[5], &wdtype) < 0 ||
-        (a[6] != Py_None && obj_tensor_of(&dx, a[6], N_DTYPES) < 0) || obj_ptr(a[7], &dw) < 0 ||
-        obj_ptr(a[8], &db) < 0 || obj_stream(a[9], a[1], &stream) < 0)
+    if (obj_tensor_of(&dy, a[0], N_DTYPES) < 0 || obj_tensor_of(&x, a[1], N_DTYPES) < 0 ||
+        (a[5] != Py_None && obj_tensor_of(&dx, a[5], N_DTYPES) < 0) || obj_stream(a[8], a[1], &stream) < 0)
         return NULL;
+    if (as_rows(&dy) || as_rows(&x) || (a[5] != Py_None && as_rows(&dx))) return PyLong_FromLong(PLAIN_PATH);
+    const long device = obj_device(a[1]), other = obj_device(a[0]);
+    const int32_t wdtype = dtype_or(a[4] != Py_None ? a[4] : a[6] != Py_None ? a[6] : a[7], x.dtype);
+    if (device == -2 || other == -2 || wdtype == -2) return NULL;
+    if (device != other) return PyLong_FromLong(PLAIN_PATH);
+    VECTOR(a[2], x.shape[0], TROP_F32, &mean);
+    VECTOR(a[3], x.shape[0], TROP_F32, &rstd);
+    VECTOR(a[4], x.shape[1], wdtype, &w);
+    VECTOR(a[6], x.shape[1], wdtype, &dw);
+    VECTOR(a[7], x.shape[1], wdtype, &db);
     int rc;
     Py_BEGIN_ALLOW_THREADS
-    rc = tropical_layer_norm_backward(&dy, &x, (float*)mean, (float*)rstd, w, (int)wdtype,
-                                      a[6] == Py_None ? NULL : &dx, dw, db, stream);
+    rc = tropical_layer_norm_backward(&dy, &x, (float*)mean, (float*)rstd, w, wdtype, a[5] == Py_None ? NULL : &dx, dw,
+                                      db, stream);
     Py_END_ALLOW_THREADS
     return PyLong_FromLong(rc);
 }
 
-/* linear_ce_t(x, w, target, ignore_index, mean, loss or None, lse, total or None, kept or None, stream or None) */
+/* x, w and target of the head's loss on one device: 0, PLAIN_PATH, or -1 */
+static int head_operands(PyObject* const* a, trop_tensor* x, trop_tensor* w, trop_tensor* t, long* device)
+{
+    if (obj_tensor_of(x, a[0], N_DTYPES) < 0 || obj_tensor_of(w, a[1], N_DTYPES) < 0 || obj_tensor_of(t, a[2], N_DTYPES) < 0)
+        return -1;
+    const long d = obj_device(a[0]), e = obj_device(a[1]), f = obj_device(a[2]);
+    if (d == -2 || e == -2 || f == -2) return -1;
+    *device = d;
+    return d == e && d == f && x->rank == 2 ? 0 : PLAIN_PATH;
+}
+
+/* linear_ce_t(x, w, target, ignore_index, mean, loss or None, lse, total or None, kept, stream or None) */
 static PyObject* fc_linear_ce_t(PyObject* self, PyObject* const* a, Py_ssize_t nargs)
 {
     (void)self;
@@ -371,12 +467,15 @@ static PyObject* fc_linear_ce_t(PyObject* self, PyObject* const* a, Py_ssize_t n
     trop_tensor x, w, t;
     void *loss, *lse, *total, *kept, *stream;
     int64_t ignore;
+    long device;
     const int mean = PyObject_IsTrue(a[4]);
-    if (obj_tensor_of(&x, a[0], N_DTYPES) < 0 || obj_tensor_of(&w, a[1], N_DTYPES) < 0 ||
-        obj_tensor_of(&t, a[2], N_DTYPES) < 0 || as_i64(a[3], &ignore) < 0 || mean < 0 || obj_ptr(a[5], &loss) < 0 ||
-        obj_ptr(a[6], &lse) < 0 || obj_ptr(a[7], &total) < 0 || obj_ptr(a[8], &kept) < 0 ||
-        obj_stream(a[9], a[0], &stream) < 0)
-        return NULL;
+    const int usual = head_operands(a, &x, &w, &t, &device);
+    if (usual < 0 || as_i64(a[3], &ignore) < 0 || mean < 0 || obj_stream(a[9], a[0], &stream) < 0) return NULL;
+    if (usual > 0) return PyLong_FromLong(PLAIN_PATH);
+    VECTOR(a[5], x.shape[0], TROP_F32, &loss);
+    VECTOR(a[6], x.shape[0], TROP_F32, &lse);
+    VECTOR(a[7], 1, TROP_F32, &total);
+    VECTOR(a[8], 1, TROP_F32, &kept);
     int rc;
     Py_BEGIN_ALLOW_THREADS
     rc = tropical_linear_cross_entropy(&x, &w, &t, ignore, mean, (float*)loss, (float*)lse, (float*)total,
@@ -385,25 +484,31 @@ static PyObject* fc_linear_ce_t(PyObject* self, PyObject* const* a, Py_ssize_t n
     return PyLong_FromLong(rc);
 }
 
-/* linear_ce_backward_t(dloss, dloss_stride, x, w, target, ignore_index, lse, kept or None, dx or None, dw or None,
- * stream or None) */
+/* linear_ce_backward_t(x, w, target, ignore_index, dloss, lse, kept or None, dx or None, dw or None, stream or None) */
 static PyObject* fc_linear_ce_backward_t(PyObject* self, PyObject* const* a, Py_ssize_t nargs)
 {
     (void)self;
-    if (check_nargs(nargs, 11, "linear_ce_backward_t") < 0) return NULL;
-    trop_tensor x, w, t, dx, dw;
-    void *g, *lse, *kept, *stream;
-    int64_t sg, ignore;
-    if (obj_ptr(a[0], &g) < 0 || as_i64(a[1], &sg) < 0 || obj_tensor_of(&x, a[2], N_DTYPES) < 0 ||
-        obj_tensor_of(&w, a[3], N_DTYPES) < 0 || obj_tensor_of(&t, a[4], N_DTYPES) < 0 || as_i64(a[5], &ignore) < 0 ||
-        obj_ptr(a[6], &lse) < 0 || obj_ptr(a[7], &kept) < 0 ||
-        (a[8] != Py_None && obj_tensor_of(&dx, a[8], N_DTYPES) < 0) ||
-        (a[9] != Py_None && obj_tensor_of(&dw, a[9], N_DTYPES) < 0) || obj_stream(a[10], a[2], &stream) < 0)
+    if (check_nargs(nargs, 10, "linear_ce_backward_t") < 0) return NULL;
+    trop_tensor x, w, t, g, dx, dw;
+    void *lse, *kept, *stream;
+    int64_t ignore;
+    long device;
+    const int usual = head_operands(a, &x, &w, &t, &device);
+    if (usual < 0 || as_i64(a[3], &ignore) < 0 || obj_tensor_of(&g, a[4], N_DTYPES) < 0 ||
+        (a[7] != Py_None && obj_tensor_of(&dx, a[7], N_DTYPES) < 0) ||
+        (a[8] != Py_None && obj_tensor_of(&dw, a[8], N_DTYPES) < 0) || obj_stream(a[9], a[0], &stream) < 0)
         return NULL;
+    const long other = obj_device(a[4]);
+    if (other == -2) return NULL;
+    if (usual > 0 || other != device || g.dtype != TROP_F32 || g.rank > 1 || (g.rank == 1 && g.shape[0] != x.shape[0]))
+        return PyLong_FromLong(PLAIN_PATH);
+    VECTOR(a[5], x.shape[0], TROP_F32, &lse);
+    VECTOR(a[6], 1, TROP_F32, &kept);
     int rc;
     Py_BEGIN_ALLOW_THREADS
-    rc = tropical_linear_cross_entropy_backward((float*)g, sg, &x, &w, &t, ignore, (float*)lse, (float*)kept,
-                                                a[8] == Py_None ? NULL : &dx, a[9] == Py_None ? NULL : &dw, stream);
+    rc = tropical_linear_cross_entropy_backward((float*)g.data, g.rank ? g.stride[0] : 0, &x, &w, &t, ignore, (float*)lse,
+                                                (float*)kept, a[7] == Py_None ? NULL : &dx, a[8] == Py_None ? NULL : &dw,
+                                                stream);
     Py_END_ALLOW_THREADS
     return PyLong_FromLong(rc);
 }
@@ -422,6 +527,20 @@ static PyObject* fc_adamw_plan_step(PyObject* self, PyObject* const* a, Py_ssize
     int rc;
     Py_BEGIN_ALLOW_THREADS
     rc = tropical_adamw_plan_step((trop_adamw_plan)plan, &o, stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
+/* adamw_plan_values(plan address, tensor, stream or None) */
+static PyObject* fc_adamw_plan_values(PyObject* self, PyObject* const* a, Py_ssize_t nargs)
+{
+    (void)self;
+    if (check_nargs(nargs, 3, "adamw_plan_values") < 0) return NULL;
+    void *plan, *stream;
+    if (as_ptr(a[0], &plan) < 0 || obj_stream(a[2], a[1], &stream) < 0) return NULL;
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = tropical_adamw_plan_values((trop_adamw_plan)plan, stream);
     Py_END_ALLOW_THREADS
     return PyLong_FromLong(rc);
 }
@@ -455,6 +574,7 @@ static PyMethodDef methods[] = {
     {"linear_ce_backward_t", (PyCFunction)(void (*)(void))fc_linear_ce_backward_t, METH_FASTCALL,
      "tropical_linear_cross_entropy_backward on tensor objects"},
     {"adamw_plan_step", (PyCFunction)(void (*)(void))fc_adamw_plan_step, METH_FASTCALL, "tropical_adamw_plan_step"},
+    {"adamw_plan_values", (PyCFunction)(void (*)(void))fc_adamw_plan_values, METH_FASTCALL, "tropical_adamw_plan_values"},
     {NULL, NULL, 0, NULL},
 };
 

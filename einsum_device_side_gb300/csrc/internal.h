@@ -83,6 +83,13 @@ enum { ST_ALLOC, ST_HIT, ST_MALLOC, ST_RETIRED, ST_RELEASED, ST_EVWAIT, ST_LEAKE
 int pool_alloc(size_t bytes, cudaStream_t stream, void** out);
 void pool_retire(void* ptr, cudaStream_t stream);
 
+// A block of at most SCRATCH_MOST bytes that stays the stream's (scratch.cpp): false where it is larger
+// or the launches are being captured, and the pool has to serve.  One block per call; it is valid in
+// stream order until the next call on this stream from this host thread.
+constexpr size_t SCRATCH_MOST = 16u << 20;
+bool stream_scratch(size_t bytes, cudaStream_t s, void** out);
+void release_scratch();  // the caller has synchronised
+
 // Zeroed per-stream counters for atomic arrival tickets (the kernels reset them to zero).
 int stream_tickets(cudaStream_t s, size_t count, uint32_t** out);
 

@@ -17,8 +17,6 @@
 // The weight's and bias's gradients are summed without atomics: a persistent block keeps the sums
 // of its columns over all its rows in registers and writes them once; k_norm_join adds the blocks'
 // sums in block order, so results repeat bit for bit.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -26,43 +24,30 @@
 
 #define TROP_TU 7  // this file's id in a bounds-violation record
 #include "internal.h"
+#include "packed.h"
 #include "train.h"
 
 namespace trop {
 namespace {
 
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
-template <typename T> __device__ __forceinline__ T from_f32(float v);
-template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
-template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
-
-// VEC elements that lie together, moved as 16-byte (or one 8-byte, or scalar) accesses
-template <typename T, int VEC>
-struct alignas(VEC * sizeof(T) >= 16 ? 16 : VEC * sizeof(T)) Pack {
-    T e[VEC];
-};
+// VEC elements that lie together, one access where they make 16 (or 8) bytes
 template <typename T, int VEC>
 __device__ __forceinline__ void load(const T* p, float (&v)[VEC], const Span& sp)
 {
-    if (TROP_IN(p, VEC * sizeof(T), sp)) {
-        const Pack<T, VEC> q = *reinterpret_cast<const Pack<T, VEC>*>(p);
+    (void)sp;
+    Raw<T, VEC> q;
+    if (TROP_IN(p, VEC * sizeof(T), sp)) q.read(p);
+    else q.zero();
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = to_f32(q.e[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = 0.f;
-    }
+    for (int i = 0; i < VEC; ++i) v[i] = q.get(i);
 }
 template <typename T, int VEC>
 __device__ __forceinline__ void store(T* p, const float (&v)[VEC], const Span& sp)
 {
-    Pack<T, VEC> q;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) q.e[i] = from_f32<T>(v[i]);
-    if (TROP_IN(p, VEC * sizeof(T), sp)) *reinterpret_cast<Pack<T, VEC>*>(p) = q;
+    (void)sp;
+    Raw<T, VEC> q;
+    q.set(v);
+    if (TROP_IN(p, VEC * sizeof(T), sp)) q.write(p);
 }
 
 // Sums of K values over the group of a row: a warp (several rows per block), or the whole block.
@@ -87,6 +72,52 @@ __device__ __forceinline__ void group_sum(float (&v)[K], float (*sh)[K])
         for (int k = 0; k < K; ++k) v[k] += sh[w][k];
 }
 
+template <int K>
+__device__ __forceinline__ void warp_sum(float (&v)[K])
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+}
+// The same over a row's group with one barrier: callers alternate between two of `sh`.
+template <int K>
+__device__ __forceinline__ void group_sum_turn(float (&v)[K], float (*sh)[K])
+{
+    warp_sum<K>(v);
+    if (blockDim.x == 32) return;
+    if ((threadIdx.x & 31) == 0)
+#pragma unroll
+        for (int k = 0; k < K; ++k) sh[threadIdx.x >> 5][k] = v[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = 0.f;
+    for (int w = 0; w < (int)(blockDim.x >> 5); ++w)
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[k] += sh[w][k];
+}
+// `bytes` (a multiple of 16) between 16-byte boundaries, counted by the mbarrier
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+constexpr int RING_STAGES = 8;
+// A copy did not land within its bounded wait: say so, and wait (bounded) for the others before the
+// block leaves.
+__device__ void ring_failed(uint64_t* full, int stages, int s, uint32_t phase, uint32_t* error)
+{
+    if (threadIdx.x != 0) return;
+    *(volatile uint32_t*)error = 1;
+    __threadfence_system();
+    for (int i = 0; i < stages; ++i) {
+        (void)mbar_wait(&full[s], phase);
+        if (++s == stages) s = 0, phase ^= 1;
+    }
+}
+
 struct NormJob {
     int64_t rows, cols;
     float inv_cols, eps;
@@ -98,45 +129,35 @@ struct NormJob {
     Span sp_x, sp_y, sp_dy, sp_dx, sp_w, sp_b, sp_mean, sp_rstd, sp_pw, sp_pb;
 };
 
+// Threads a block may have: where a thread holds more than 64 bytes of its row, registers allow 256.
+template <typename T, int VEC, int NV>
+constexpr int most_threads() { return VEC * NV * sizeof(T) <= 64 ? 1024 : 256; }
+
+// One row in a group's registers: statistics, result.
 template <typename TX, typename TY, typename TW, int VEC, int NV>
-__global__ void __launch_bounds__(1024) k_norm(const NormJob j)
+__device__ __forceinline__ void norm_row(const NormJob& j, int64_t row, Raw<TX, VEC> (&q)[NV], float (*sh)[32][1])
 {
-    pdl_wait();
-    pdl_signal();
-    __shared__ float sh[32][1];
-    const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    if (row >= j.rows) return;  // (a block of several rows has one warp per row)
-    const TX* x = (const TX*)j.x + row * j.sx;
-    float v[NV][VEC];
+    const int cols = (int)j.cols;
     float s[1] = {0.f};
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int64_t c = (int64_t)(k * blockDim.x + threadIdx.x) * VEC;
-        if (c < j.cols) {
-            load<TX, VEC>(x + c, v[k], j.sp_x);
-        } else {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) v[k][i] = 0.f;
-        }
-    }
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) s[0] += v[k][i];
-    group_sum<1>(s, sh);
+        for (int i = 0; i < VEC; ++i) s[0] += q[k].get(i);
+    group_sum_turn<1>(s, sh[0]);
     const float mean = s[0] * j.inv_cols;
     s[0] = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        const int64_t c = (int64_t)(k * blockDim.x + threadIdx.x) * VEC;
-        if (c < j.cols)
+        const int c = (k * blockDim.x + threadIdx.x) * VEC;
+        q[k].again();
+        if (c < cols)
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                v[k][i] -= mean;
-                s[0] = __fmaf_rn(v[k][i], v[k][i], s[0]);
+                const float d = q[k].get(i) - mean;
+                s[0] = __fmaf_rn(d, d, s[0]);
             }
     }
-    group_sum<1>(s, sh);
+    group_sum_turn<1>(s, sh[1]);
     const float rstd = __fdiv_rn(1.f, __fsqrt_rn(__fmaf_rn(s[0], j.inv_cols, j.eps)));
     if (threadIdx.x == 0) {
         if (j.mean && TROP_IN(j.mean + row, 4, j.sp_mean)) j.mean[row] = mean;
@@ -145,18 +166,57 @@ __global__ void __launch_bounds__(1024) k_norm(const NormJob j)
     TY* y = (TY*)j.y + row * j.sy;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        const int64_t c = (int64_t)(k * blockDim.x + threadIdx.x) * VEC;
-        if (c < j.cols) {
+        const int c = (k * blockDim.x + threadIdx.x) * VEC;
+        if (c < cols) {
             float w[VEC], b[VEC], o[VEC];
+            q[k].again();
             if (j.w) load<TW, VEC>((const TW*)j.w + c, w, j.sp_w);
             if (j.b) load<TW, VEC>((const TW*)j.b + c, b, j.sp_b);
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                o[i] = v[k][i] * rstd;
+                o[i] = (q[k].get(i) - mean) * rstd;
                 if (j.w) o[i] *= w[i];
                 if (j.b) o[i] += b[i];
             }
             store<TY, VEC>(y + c, o, j.sp_y);
+        }
+    }
+}
+
+// Rows from global memory; a group that holds little of a row fetches its next row before it works
+// on this one.
+template <typename TX, typename TY, typename TW, int VEC, int NV>
+__global__ void __launch_bounds__((most_threads<TX, VEC, NV>()),
+                                  (most_threads<TX, VEC, NV>() == 1024 ? 1 : VEC * NV == 64 && sizeof(TX) == 2 ? 3 : 2))
+    k_norm(const NormJob j)
+{
+    pdl_wait();
+    pdl_signal();
+    __shared__ float sh[2][32][1];
+    constexpr bool AHEAD = VEC * NV * sizeof(TX) <= 32;
+    const int64_t step = (int64_t)gridDim.x * blockDim.y;
+    const int cols = (int)j.cols;
+    auto fetch = [&](Raw<TX, VEC> (&q)[NV], int64_t row) {
+        const TX* x = (const TX*)j.x + row * j.sx;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = (k * blockDim.x + threadIdx.x) * VEC;
+            if (row < j.rows && c < cols && TROP_IN(x + c, VEC * sizeof(TX), j.sp_x)) q[k].read(x + c);
+            else q[k].zero();
+        }
+    };
+    int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    Raw<TX, VEC> q[NV], ahead[AHEAD ? NV : 1];
+    if (AHEAD && row < j.rows) fetch(q, row);
+    for (; row < j.rows; row += step) {
+        if constexpr (AHEAD) {
+            fetch(ahead, row + step);
+            norm_row<TX, TY, TW, VEC, NV>(j, row, q, sh);
+#pragma unroll
+            for (int k = 0; k < NV; ++k) q[k] = ahead[k];
+        } else {
+            fetch(q, row);
+            norm_row<TX, TY, TW, VEC, NV>(j, row, q, sh);
         }
     }
 }
@@ -200,100 +260,238 @@ __global__ void __launch_bounds__(1024) k_norm_long(const NormJob j)
     }
 }
 
-// TX: x and dx; TY: dy.
-template <typename TX, typename TY, typename TW, int VEC, int NV, int MAXT>
-__global__ void __launch_bounds__(MAXT) k_norm_back(const NormJob j)
+// One row of the backward pass in a group's registers: h and u in place of x and dy, the weight's
+// and bias's sums, and the row's two sums.
+template <int VEC, int NV>
+__device__ __forceinline__ void back_sums(float (&h)[NV][VEC], float (&d)[NV][VEC], const float (&w)[NV][VEC],
+                                          float (&aw)[NV][VEC], float (&ab)[NV][VEC], float mean, float rstd, float (&s)[2])
 {
-    pdl_wait();
-    pdl_signal();
-    extern __shared__ float across[];  // blocks of several rows: [rows][cols]
-    __shared__ float sh[32][2];
-    float aw[NV][VEC], ab[NV][VEC], w[NV][VEC];
+    s[0] = s[1] = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            h[k][i] = (h[k][i] - mean) * rstd;
+            aw[k][i] = __fmaf_rn(d[k][i], h[k][i], aw[k][i]);
+            ab[k][i] += d[k][i];
+            d[k][i] *= w[k][i];
+            s[0] += d[k][i];
+            s[1] = __fmaf_rn(d[k][i], h[k][i], s[1]);
+        }
+}
+template <typename TX, int VEC, int NV>
+__device__ __forceinline__ void back_store(const NormJob& j, int64_t row, const float (&h)[NV][VEC],
+                                           const float (&d)[NV][VEC], float rstd, const float (&s)[2])
+{
+    const float flat = s[0] * j.inv_cols, along = s[1] * j.inv_cols;
+    TX* dx = (TX*)j.dx + row * j.sdx;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        const int64_t c = (int64_t)(k * blockDim.x + threadIdx.x) * VEC;
+        const int c = (k * blockDim.x + threadIdx.x) * VEC;
+        if (c < (int)j.cols) {
+            float o[VEC];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) aw[k][i] = ab[k][i] = 0.f, w[k][i] = 1.f;
-        if (j.w && c < j.cols) load<TW, VEC>((const TW*)j.w + c, w[k], j.sp_w);
-    }
-    for (int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; row < j.rows;
-         row += (int64_t)gridDim.x * blockDim.y) {
-        const TX* x = (const TX*)j.x + row * j.sx;
-        const TY* dy = (const TY*)j.dy + row * j.sdy;
-        float h[NV][VEC], d[NV][VEC];
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int64_t c = (int64_t)(k * blockDim.x + threadIdx.x) * VEC;
-            if (c < j.cols) {
-                load<TX, VEC>(x + c, h[k], j.sp_x);
-                load<TY, VEC>(dy + c, d[k], j.sp_dy);
-            }
-        }
-        const float mean = TROP_IN(j.mean + row, 4, j.sp_mean) ? j.mean[row] : 0.f;
-        const float rstd = TROP_IN(j.rstd + row, 4, j.sp_rstd) ? j.rstd[row] : 0.f;
-        float s[2] = {0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int64_t c = (int64_t)(k * blockDim.x + threadIdx.x) * VEC;
-            if (c < j.cols)
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    h[k][i] = (h[k][i] - mean) * rstd;
-                    aw[k][i] = __fmaf_rn(d[k][i], h[k][i], aw[k][i]);
-                    ab[k][i] += d[k][i];
-                    d[k][i] *= w[k][i];
-                    s[0] += d[k][i];
-                    s[1] = __fmaf_rn(d[k][i], h[k][i], s[1]);
-                }
-        }
-        if (!j.dx) continue;
-        group_sum<2>(s, sh);
-        const float flat = s[0] * j.inv_cols, along = s[1] * j.inv_cols;
-        TX* dx = (TX*)j.dx + row * j.sdx;
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int64_t c = (int64_t)(k * blockDim.x + threadIdx.x) * VEC;
-            if (c < j.cols) {
-                float o[VEC];
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) o[i] = rstd * (d[k][i] - flat - h[k][i] * along);
-                store<TX, VEC>(dx + c, o, j.sp_dx);
-            }
+            for (int i = 0; i < VEC; ++i) o[i] = rstd * (d[k][i] - flat - h[k][i] * along);
+            store<TX, VEC>(dx + c, o, j.sp_dx);
         }
     }
-    if (!j.part_w && !j.part_b) return;
+}
+// The block's column sums into its row of the partial sums.  Blocks of several warps that each took
+// rows of their own (blockDim.y > 1) add theirs in warp order, through `across` [warps][cols].
+template <int VEC, int NV>
+__device__ __forceinline__ void back_partials(const NormJob& j, const float (&aw)[NV][VEC], const float (&ab)[NV][VEC],
+                                              float* across)
+{
+    const int cols = (int)j.cols;
     for (int which = 0; which < 2; ++which) {
         float* part = which ? j.part_b : j.part_w;
         if (!part) continue;
         const Span& sp = which ? j.sp_pb : j.sp_pw;
-        part += (int64_t)blockIdx.x * j.cols;
-        if (blockDim.y > 1) {  // the block's rows were shared by several warps: add theirs in warp order
-            __syncthreads();
+        (void)sp;
+        part += (int64_t)blockIdx.x * cols;
+        if (blockDim.y > 1) __syncthreads();
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int64_t c = (int64_t)(k * blockDim.x + threadIdx.x) * VEC;
-                if (c < j.cols)
+        for (int k = 0; k < NV; ++k) {
+            const int c = (k * blockDim.x + threadIdx.x) * VEC;
+            if (c >= cols) continue;
+            if (blockDim.y > 1) {
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i)
-                        across[threadIdx.y * j.cols + c + i] = which ? ab[k][i] : aw[k][i];
+                for (int i = 0; i < VEC; ++i) across[threadIdx.y * cols + c + i] = which ? ab[k][i] : aw[k][i];
+            } else if (VEC % 4 == 0) {
+#pragma unroll
+                for (int i = 0; i < VEC; i += 4) {
+                    const float4 v = which ? make_float4(ab[k][i], ab[k][i + 1 < VEC ? i + 1 : 0], ab[k][i + 2 < VEC ? i + 2 : 0],
+                                                         ab[k][i + 3 < VEC ? i + 3 : 0])
+                                           : make_float4(aw[k][i], aw[k][i + 1 < VEC ? i + 1 : 0], aw[k][i + 2 < VEC ? i + 2 : 0],
+                                                         aw[k][i + 3 < VEC ? i + 3 : 0]);
+                    if (TROP_IN(part + c + i, 16, sp)) *reinterpret_cast<float4*>(part + c + i) = v;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    if (TROP_IN(part + c + i, 4, sp)) part[c + i] = which ? ab[k][i] : aw[k][i];
             }
+        }
+        if (blockDim.y > 1) {
             __syncthreads();
-            for (int64_t c = threadIdx.y * 32 + threadIdx.x; c < j.cols; c += 32 * blockDim.y) {
+            for (int c = threadIdx.y * 32 + threadIdx.x; c < cols; c += 32 * blockDim.y) {
                 float a = 0.f;
-                for (int r = 0; r < (int)blockDim.y; ++r) a += across[r * j.cols + c];
+                for (int r = 0; r < (int)blockDim.y; ++r) a += across[r * cols + c];
                 if (TROP_IN(part + c, 4, sp)) part[c] = a;
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int64_t c = (int64_t)(k * blockDim.x + threadIdx.x) * VEC;
-                if (c < j.cols)
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i)
-                        if (TROP_IN(part + c + i, 4, sp)) part[c + i] = which ? ab[k][i] : aw[k][i];
             }
         }
     }
+}
+template <typename TW, int VEC, int NV>
+__device__ __forceinline__ void back_init(const NormJob& j, float (&w)[NV][VEC], float (&aw)[NV][VEC], float (&ab)[NV][VEC])
+{
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int c = (k * blockDim.x + threadIdx.x) * VEC;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) aw[k][i] = ab[k][i] = 0.f, w[k][i] = 1.f;
+        if (j.w && c < (int)j.cols) load<TW, VEC>((const TW*)j.w + c, w[k], j.sp_w);
+    }
+}
+
+// Rows from global memory, U of a group's rows on their way at a time.  TX: x and dx; TY: dy.
+template <typename TX, typename TY, typename TW, int VEC, int NV, int U, int MAXT>
+__global__ void __launch_bounds__(MAXT) k_norm_back(const NormJob j)
+{
+    pdl_wait();
+    pdl_signal();
+    extern __shared__ __align__(16) uint8_t dyn[];
+    __shared__ float sh[2][32][2];
+    float aw[NV][VEC], ab[NV][VEC], w[NV][VEC];
+    back_init<TW, VEC, NV>(j, w, aw, ab);
+    const int64_t step = (int64_t)gridDim.x * blockDim.y;
+    const int cols = (int)j.cols;
+    int turn = 0;
+    for (int64_t row0 = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; row0 < j.rows; row0 += step * U) {
+        Raw<TX, VEC> qx[U][NV];
+        Raw<TY, VEC> qd[U][NV];
+        float mean[U], rstd[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = row0 + u * step;
+            const bool live = row < j.rows;
+            mean[u] = live && TROP_IN(j.mean + row, 4, j.sp_mean) ? j.mean[row] : 0.f;
+            rstd[u] = live && TROP_IN(j.rstd + row, 4, j.sp_rstd) ? j.rstd[row] : 0.f;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int c = (k * blockDim.x + threadIdx.x) * VEC;
+                const TX* x = (const TX*)j.x + row * j.sx + c;
+                const TY* dy = (const TY*)j.dy + row * j.sdy + c;
+                if (live && c < cols && TROP_IN(x, VEC * sizeof(TX), j.sp_x) && TROP_IN(dy, VEC * sizeof(TY), j.sp_dy)) {
+                    qx[u][k].read(x);
+                    qd[u][k].read(dy);
+                } else {  // dy = 0: nothing in any sum
+                    qx[u][k].zero();
+                    qd[u][k].zero();
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = row0 + u * step;
+            if (row >= j.rows) break;
+            float h[NV][VEC], d[NV][VEC], s[2];
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) h[k][i] = qx[u][k].get(i), d[k][i] = qd[u][k].get(i);
+            back_sums<VEC, NV>(h, d, w, aw, ab, mean[u], rstd[u], s);
+            if (!j.dx) continue;
+            group_sum_turn<2>(s, sh[turn]);
+            turn ^= 1;
+            back_store<TX, VEC, NV>(j, row, h, d, rstd[u], s);
+        }
+    }
+    if (j.part_w || j.part_b) back_partials<VEC, NV>(j, aw, ab, reinterpret_cast<float*>(dyn));
+}
+
+// Rows through shared memory: a ring of `stages` rows of x and dy, each brought by two bulk copies, so
+// that several rows per block are on their way whatever the block is doing; the barrier of a row's
+// sums also says that its stage has been read.
+template <typename TX, typename TY, typename TW, int VEC, int NV, int MAXT>
+__global__ void __launch_bounds__(MAXT) k_norm_back_ring(const NormJob j, int stages, uint32_t* error)
+{
+    pdl_wait();
+    pdl_signal();
+    extern __shared__ __align__(16) uint8_t dyn[];
+    __shared__ float sh[2][32][2];
+    __shared__ __align__(8) uint64_t full[RING_STAGES];
+    const int cols = (int)j.cols;
+    const uint32_t xb = cols * sizeof(TX), db = cols * sizeof(TY);
+    const int64_t first = blockIdx.x, step = gridDim.x;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    auto fetch = [&](int s, int64_t row) {
+        const TX* x = (const TX*)j.x + row * j.sx;
+        const TY* dy = (const TY*)j.dy + row * j.sdy;
+        if (TROP_IN(x, (int)xb, j.sp_x) && TROP_IN(dy, (int)db, j.sp_dy)) {
+            mbar_expect_tx(&full[s], xb + db);
+            bulk_load(dyn + (size_t)s * (xb + db), x, xb, &full[s]);
+            bulk_load(dyn + (size_t)s * (xb + db) + xb, dy, db, &full[s]);
+        } else {
+            mbar_expect_tx(&full[s], 0);
+        }
+    };
+    int64_t ahead = first;  // the next row to fetch (thread 0)
+    if (threadIdx.x == 0)
+        for (int s = 0; s < stages && ahead < j.rows; ++s, ahead += step) fetch(s, ahead);
+    float aw[NV][VEC], ab[NV][VEC], w[NV][VEC];
+    back_init<TW, VEC, NV>(j, w, aw, ab);
+    int s = 0, turn = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    float mean = 0.f, rstd = 0.f;
+    if (first < j.rows && TROP_IN(j.mean + first, 4, j.sp_mean) && TROP_IN(j.rstd + first, 4, j.sp_rstd))
+        mean = j.mean[first], rstd = j.rstd[first];
+    for (int64_t row = first; row < j.rows; row += step) {
+        float mean2 = 0.f, rstd2 = 0.f;  // the next row's
+        if (row + step < j.rows && TROP_IN(j.mean + row + step, 4, j.sp_mean) && TROP_IN(j.rstd + row + step, 4, j.sp_rstd))
+            mean2 = j.mean[row + step], rstd2 = j.rstd[row + step];
+        ok = mbar_wait(&full[s], phase);
+        const uint8_t* at = dyn + (size_t)s * (xb + db);
+        float h[NV][VEC], d[NV][VEC], sum[2];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = (k * blockDim.x + threadIdx.x) * VEC;
+            Raw<TX, VEC> qx;
+            Raw<TY, VEC> qd;
+            qx.zero();  // past the row dy = 0: nothing in any sum
+            qd.zero();
+            if (c < cols) {
+                qx.read(reinterpret_cast<const TX*>(at) + c);
+                qd.read(reinterpret_cast<const TY*>(at + xb) + c);
+            }
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) h[k][i] = qx.get(i), d[k][i] = qd.get(i);
+        }
+        back_sums<VEC, NV>(h, d, w, aw, ab, mean, rstd, sum);
+        warp_sum<2>(sum);
+        if ((threadIdx.x & 31) == 0) sh[turn][threadIdx.x >> 5][0] = sum[0], sh[turn][threadIdx.x >> 5][1] = sum[1];
+        ok = __syncthreads_and(ok);
+        if (!ok) break;
+        if (threadIdx.x == 0 && ahead < j.rows) fetch(s, ahead), ahead += step;
+        if (j.dx) {
+            sum[0] = sum[1] = 0.f;
+            for (int q = 0; q < (int)(blockDim.x >> 5); ++q) sum[0] += sh[turn][q][0], sum[1] += sh[turn][q][1];
+            back_store<TX, VEC, NV>(j, row, h, d, rstd, sum);
+        }
+        turn ^= 1;
+        mean = mean2, rstd = rstd2;
+        if (++s == stages) s = 0, phase ^= 1;
+    }
+    if (!ok) {
+        ring_failed(full, stages, s, phase, error);
+        return;
+    }
+    if (j.part_w || j.part_b) back_partials<VEC, NV>(j, aw, ab, nullptr);
 }
 
 template <typename TX, typename TY, typename TW>
@@ -350,31 +548,46 @@ __global__ void __launch_bounds__(256) k_norm_columns(const NormJob j)
     if (j.part_b && TROP_IN(j.part_b + at, 4, j.sp_pb)) j.part_b[at] = ab;
 }
 
-// The blocks' column sums added in block order: 32 columns per block, eight warps taking every
-// eighth block's sums, blockIdx.y choosing the weight or the bias.
+// The blocks' column sums: 32 columns per block of threads, 32 warps taking every 32nd block's sums
+// in block order, blockIdx.y choosing the weight or the bias.
 template <typename TW>
-__global__ void __launch_bounds__(256) k_norm_join(const float* part_w, const float* part_b, int blocks, int64_t cols,
-                                                   TW* dw, TW* db, Span sp_pw, Span sp_pb, Span sp_dw, Span sp_db)
+__global__ void __launch_bounds__(1024) k_norm_join(const float* part_w, const float* part_b, int blocks, int64_t cols,
+                                                    TW* dw, TW* db, Span sp_pw, Span sp_pb, Span sp_dw, Span sp_db)
 {
     pdl_wait();
     pdl_signal();
-    __shared__ float sh[8][33];
+    __shared__ float sh[32][33];
     const bool bias = dw == nullptr || blockIdx.y == 1;
     const float* part = bias ? part_b : part_w;
     const Span sp = bias ? sp_pb : sp_pw;
+    (void)sp;
     TW* out = bias ? db : dw;
     const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
     float a = 0.f;
-    if (c < cols)
-#pragma unroll 4
-        for (int b = threadIdx.y; b < blocks; b += 8)
+    if (c < cols) {
+        float v[4];
+        int b = threadIdx.y;
+        for (; b + 96 < blocks; b += 128) {  // four loads on their way
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float* p = part + (b + 32 * k) * cols + c;
+                v[k] = TROP_IN(p, 4, sp) ? *p : 0.f;
+            }
+            a += (v[0] + v[1]) + (v[2] + v[3]);
+        }
+        for (; b < blocks; b += 32)
             if (TROP_IN(part + b * cols + c, 4, sp)) a += part[b * cols + c];
+    }
     sh[threadIdx.y][threadIdx.x] = a;
     __syncthreads();
-    if (threadIdx.y == 0 && c < cols) {
-        for (int w = 1; w < 8; ++w) a += sh[w][threadIdx.x];
+    // warp y sums column y's 32 values
+    a = sh[threadIdx.x][threadIdx.y];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    const int64_t col = (int64_t)blockIdx.x * 32 + threadIdx.y;
+    if (threadIdx.x == 0 && col < cols) {
         const float o[1] = {a};
-        store<TW, 1>(out + c, o, bias ? sp_db : sp_dw);
+        store<TW, 1>(out + col, o, bias ? sp_db : sp_dw);
     }
 }
 template <typename TW>
@@ -399,9 +612,65 @@ bool aligned(const void* p, int64_t stride, size_t elem, int vec, int64_t rows)
         count_launches(1);                                                            \
     } while (0)
 
-// A row's group: 32 threads (four rows per block), or one block per row.  Vectors per thread: the
-// fewest that keep the group at 256 threads or less, then wider groups.
-bool shape_of(int64_t units, int most_nv, int* nv, dim3* block)
+// A row's group of the forward pass: as many vectors per thread as still leave 8 warps per SM at
+// work, so that long batches put a row into one warp (no barrier, up to 16 loads on their way per
+// thread) and a few rows are spread over many threads.  16384x4096 bf16: a warp per row, see the
+// head of this file; 16x512 f32: 128 threads per row.
+template <typename TX, int VEC>
+bool forward_shape(int64_t units, int64_t rows, int sm, int* nv, dim3* block)
+{
+    for (int n = VEC == 8 ? 8 : 16; n >= 1; n /= 2) {
+        const int64_t most = VEC * n * sizeof(TX) <= 64 ? 1024 : 256;
+        const int64_t g = ((units + n - 1) / n + 31) / 32 * 32;
+        if (g > most) break;
+        *nv = n;
+        *block = g == 32 ? dim3(32, 8) : dim3((unsigned)g, 1);
+        if (rows * (g / 32) >= (int64_t)sm * 8) return true;
+    }
+    return *nv > 0;
+}
+
+template <typename TX, typename TY, typename TW, int VEC>
+int norm_rows(const NormJob& j, int nv, dim3 grid, dim3 block, cudaStream_t s)
+{
+    switch (nv) {
+    case 1: TROP_LAUNCH((k_norm<TX, TY, TW, VEC, 1>), grid, block, 0, j); break;
+    case 2: TROP_LAUNCH((k_norm<TX, TY, TW, VEC, 2>), grid, block, 0, j); break;
+    case 4: TROP_LAUNCH((k_norm<TX, TY, TW, VEC, 4>), grid, block, 0, j); break;
+    case 8: TROP_LAUNCH((k_norm<TX, TY, TW, VEC, 8>), grid, block, 0, j); break;
+    default: TROP_LAUNCH((k_norm<TX, TY, TW, VEC, VEC == 8 ? 8 : 16>), grid, block, 0, j);
+    }
+    return TROP_OK;
+}
+
+// Bytes of an SM's rings.
+constexpr size_t RING_BYTES = 196608;
+
+template <typename TX, typename TY, typename TW>
+int norm_forward(const NormJob& j, int sm, cudaStream_t s)
+{
+    constexpr int V = 16 / sizeof(TX);
+    const bool vec = j.cols % V == 0 && aligned(j.x, j.sx, sizeof(TX), V, j.rows) &&
+                     aligned(j.y, j.sy, sizeof(TY), V, j.rows) && aligned(j.w, 0, sizeof(TW), V, 1) &&
+                     aligned(j.b, 0, sizeof(TW), V, 1);
+    int nv = 0;
+    dim3 block;
+    const bool fits = vec ? forward_shape<TX, V>(j.cols / V, j.rows, sm, &nv, &block)
+                          : forward_shape<TX, 1>(j.cols, j.rows, sm, &nv, &block);
+    if (!fits) {
+        TROP_LAUNCH((k_norm_long<TX, TY, TW>), dim3((unsigned)j.rows), dim3(1024), 0, j);
+        return TROP_OK;
+    }
+    // blocks that fetch ahead walk over the rows; the others take one row each
+    int64_t blocks = (j.rows + block.y - 1) / block.y;
+    if ((vec ? 16 : sizeof(TX)) * nv <= 32) blocks = std::min<int64_t>(blocks, (int64_t)sm * std::max<int>(1, 2048 / (int)(block.x * block.y)));
+    const dim3 grid((unsigned)blocks);
+    return vec ? norm_rows<TX, TY, TW, V>(j, nv, grid, block, s) : norm_rows<TX, TY, TW, 1>(j, nv, grid, block, s);
+}
+
+// A row's group of the backward pass, whose threads keep the column sums too: 16 elements at most,
+// the fewest vectors per thread that keep the group at 256 threads or less, then wider groups.
+bool backward_shape(int64_t units, int most_nv, int* nv, dim3* block)
 {
     int n = 1;
     while (n < most_nv && units > (int64_t)n * 256) n *= 2;
@@ -410,34 +679,6 @@ bool shape_of(int64_t units, int most_nv, int* nv, dim3* block)
     *nv = n;
     *block = g == 32 ? dim3(32, 4) : dim3((unsigned)g, 1);
     return true;
-}
-
-template <typename TX, typename TY, typename TW>
-int norm_forward(const NormJob& j, cudaStream_t s)
-{
-    constexpr int V = 16 / sizeof(TX);
-    const bool vec = j.cols % V == 0 && aligned(j.x, j.sx, sizeof(TX), V, j.rows) &&
-                     aligned(j.y, j.sy, sizeof(TY), V, j.rows) && aligned(j.w, 0, sizeof(TW), V, 1) &&
-                     aligned(j.b, 0, sizeof(TW), V, 1);
-    int nv;
-    dim3 block;
-    if (!shape_of(vec ? j.cols / V : j.cols, vec ? 4 : 16, &nv, &block)) {
-        TROP_LAUNCH((k_norm_long<TX, TY, TW>), dim3((unsigned)j.rows), dim3(1024), 0, j);
-        return TROP_OK;
-    }
-    const dim3 grid((unsigned)((j.rows + block.y - 1) / block.y));
-    if (vec) {
-        if (nv == 1) TROP_LAUNCH((k_norm<TX, TY, TW, V, 1>), grid, block, 0, j);
-        else if (nv == 2) TROP_LAUNCH((k_norm<TX, TY, TW, V, 2>), grid, block, 0, j);
-        else TROP_LAUNCH((k_norm<TX, TY, TW, V, 4>), grid, block, 0, j);
-    } else if (nv <= 2) {
-        TROP_LAUNCH((k_norm<TX, TY, TW, 1, 2>), grid, block, 0, j);
-    } else if (nv == 4) {
-        TROP_LAUNCH((k_norm<TX, TY, TW, 1, 4>), grid, block, 0, j);
-    } else {
-        TROP_LAUNCH((k_norm<TX, TY, TW, 1, 16>), grid, block, 0, j);
-    }
-    return TROP_OK;
 }
 
 template <typename TX, typename TY, typename TW>
@@ -450,25 +691,32 @@ int norm_backward(NormJob j, const NormVec& dw, const NormVec& db, int sm, cudaS
                      aligned(j.w, 0, sizeof(TW), V, 1);
     int nv = 0;
     dim3 block;
-    const bool fits = shape_of(vec ? j.cols / V : j.cols, vec ? MOST : 16, &nv, &block);
+    const bool fits = backward_shape(vec ? j.cols / V : j.cols, vec ? MOST : 16, &nv, &block);
     const bool sums = dw.p || db.p;
+    // rows of x and dy that bulk copies can bring, enough of them to fill a ring
+    const size_t row_bytes = j.cols * (sizeof(TX) + sizeof(TY));
+    const bool ring = fits && vec && block.y == 1 && block.x >= 64 && block.x <= 512 && j.cols * sizeof(TY) % 16 == 0 &&
+                      aligned(j.dy, j.sdy, 1, 16, 1) && (j.sdy * sizeof(TY)) % 16 == 0 && j.sx % V == 0 && j.rows >= 4 * sm;
+    const int per_sm = block.x > 256 ? 1 : std::max<int>(2, 512 / (int)block.x);  // blocks that share an SM
+    const int stages = (int)std::min<size_t>(RING_STAGES, RING_BYTES / per_sm / row_bytes);
     int blocks = 0;
-    if (fits) {
-        blocks = (int)std::min<int64_t>((j.rows + block.y - 1) / block.y,
-                                        (int64_t)sm * std::max<int>(1, 512 / (int)(block.x * block.y)));
-    } else {
-        blocks = (int)std::min<int64_t>(j.rows, std::max<int64_t>(1, (int64_t)sm * 8 * 256 / j.cols));
-    }
-    void *pw = nullptr, *pb = nullptr;
-    const size_t bytes = (size_t)blocks * j.cols * 4;
-    if (dw.p) TROP_TRY(pool_alloc(bytes, s, &pw));
-    struct Give {
-        void* p;
+    if (ring) blocks = (int)std::min<int64_t>(j.rows, (int64_t)sm * per_sm);
+    else if (fits) blocks = (int)std::min<int64_t>((j.rows + block.y - 1) / block.y, (int64_t)sm * std::max<int>(1, 512 / (int)(block.x * block.y)));
+    else blocks = (int)std::min<int64_t>(j.rows, std::max<int64_t>(1, (int64_t)sm * 8 * 256 / j.cols));
+    const size_t bytes = (size_t)blocks * j.cols * 4, spaced = (bytes + 255) / 256 * 256;
+    struct Workspace {
+        void* p = nullptr;
         cudaStream_t s;
-        ~Give() { if (p) pool_retire(p, s); }
-    } give_w{pw, s};
-    if (db.p) TROP_TRY(pool_alloc(bytes, s, &pb));
-    Give give_b{pb, s};
+        ~Workspace() { if (p) pool_retire(p, s); }
+    } ws;
+    ws.s = s;
+    void* part = nullptr;
+    if (sums && !stream_scratch(2 * spaced, s, &part)) {
+        TROP_TRY(pool_alloc(2 * spaced, s, &part));
+        ws.p = part;
+    }
+    void* const pw = dw.p ? part : nullptr;
+    void* const pb = db.p ? (char*)part + spaced : nullptr;
     j.part_w = (float*)pw;
     j.part_b = (float*)pb;
     j.sp_pw = span_bytes(pw, bytes);
@@ -477,29 +725,40 @@ int norm_backward(NormJob j, const NormVec& dw, const NormVec& db, int sm, cudaS
         if (j.dx) TROP_LAUNCH((k_norm_back_long<TX, TY, TW>), dim3((unsigned)j.rows), dim3(1024), 0, j);
         if (sums)
             TROP_LAUNCH((k_norm_columns<TX, TY>), dim3((unsigned)((j.cols + 255) / 256), (unsigned)blocks), dim3(256), 0, j);
+    } else if (ring && stages >= 2) {
+        uint32_t* error;
+        TROP_TRY(device_error_word(&error));
+        const dim3 grid((unsigned)blocks);
+        const size_t smem = stages * row_bytes;
+        const auto kernel = nv == 1   ? k_norm_back_ring<TX, TY, TW, V, 1, 512>
+                            : nv == 2 ? k_norm_back_ring<TX, TY, TW, V, 2, 512>
+                                      : k_norm_back_ring<TX, TY, TW, V, MOST, 512>;
+        const cudaError_t a = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (a != cudaSuccess) return cuda_error(a, "cudaFuncSetAttribute(k_norm_back_ring)");
+        TROP_LAUNCH(kernel, grid, block, smem, j, stages, error);
     } else {
         const dim3 grid((unsigned)blocks);
         const size_t smem = block.y > 1 ? block.y * (size_t)j.cols * 4 : 0;
         const bool wide = block.x > 512;
         if (vec) {
-            if (nv == 1) TROP_LAUNCH((k_norm_back<TX, TY, TW, V, 1, 512>), grid, block, smem, j);
-            else if (nv == 2 && !wide) TROP_LAUNCH((k_norm_back<TX, TY, TW, V, 2, 512>), grid, block, smem, j);
-            else if (nv == 2) TROP_LAUNCH((k_norm_back<TX, TY, TW, V, 2, 1024>), grid, block, smem, j);
-            else if (!wide) TROP_LAUNCH((k_norm_back<TX, TY, TW, V, MOST, 512>), grid, block, smem, j);
-            else TROP_LAUNCH((k_norm_back<TX, TY, TW, V, MOST, 1024>), grid, block, smem, j);
+            if (nv == 1) TROP_LAUNCH((k_norm_back<TX, TY, TW, V, 1, 4, 512>), grid, block, smem, j);
+            else if (nv == 2 && !wide) TROP_LAUNCH((k_norm_back<TX, TY, TW, V, 2, 1, 512>), grid, block, smem, j);
+            else if (nv == 2) TROP_LAUNCH((k_norm_back<TX, TY, TW, V, 2, 1, 1024>), grid, block, smem, j);
+            else if (!wide) TROP_LAUNCH((k_norm_back<TX, TY, TW, V, MOST, 1, 512>), grid, block, smem, j);
+            else TROP_LAUNCH((k_norm_back<TX, TY, TW, V, MOST, 1, 1024>), grid, block, smem, j);
         } else if (nv <= 2) {
-            TROP_LAUNCH((k_norm_back<TX, TY, TW, 1, 2, 512>), grid, block, smem, j);
+            TROP_LAUNCH((k_norm_back<TX, TY, TW, 1, 2, 4, 512>), grid, block, smem, j);
         } else if (nv == 4) {
-            TROP_LAUNCH((k_norm_back<TX, TY, TW, 1, 4, 512>), grid, block, smem, j);
+            TROP_LAUNCH((k_norm_back<TX, TY, TW, 1, 4, 4, 512>), grid, block, smem, j);
         } else if (!wide) {
-            TROP_LAUNCH((k_norm_back<TX, TY, TW, 1, 16, 512>), grid, block, smem, j);
+            TROP_LAUNCH((k_norm_back<TX, TY, TW, 1, 16, 1, 512>), grid, block, smem, j);
         } else {
-            TROP_LAUNCH((k_norm_back<TX, TY, TW, 1, 16, 1024>), grid, block, smem, j);
+            TROP_LAUNCH((k_norm_back<TX, TY, TW, 1, 16, 1, 1024>), grid, block, smem, j);
         }
     }
     if (sums) {
         const dim3 grid((unsigned)((j.cols + 31) / 32), dw.p && db.p ? 2 : 1);
-        TROP_LAUNCH((k_norm_join<TW>), grid, dim3(32, 8), 0, (const float*)pw, (const float*)pb, blocks, j.cols,
+        TROP_LAUNCH((k_norm_join<TW>), grid, dim3(32, 32), 0, (const float*)pw, (const float*)pb, blocks, j.cols,
                     (TW*)dw.p, (TW*)db.p, j.sp_pw, j.sp_pb, span_bytes(dw.p, j.cols * sizeof(TW)),
                     span_bytes(db.p, j.cols * sizeof(TW)));
     }
@@ -542,6 +801,9 @@ using bf16 = __nv_bfloat16;
 int launch_layer_norm(int64_t rows, int64_t cols, const NormMat& x, const NormVec& w, const NormVec& b, double eps,
                       const NormMat& y, float* mean, float* rstd, cudaStream_t s)
 {
+    const DeviceInfo* dev;
+    TROP_TRY(ensure_device(&dev));
+    const int sm = dev->sm_count;
     NormJob j = job_of(rows, cols, x, w);
     j.eps = (float)eps;
     j.b = b.p;
@@ -555,12 +817,12 @@ int launch_layer_norm(int64_t rows, int64_t cols, const NormMat& x, const NormVe
     j.sp_rstd = span_bytes(rstd, rows * 4);
     const int tw = w.p ? w.dtype : b.p ? b.dtype : x.dtype;
     if (x.dtype == TROP_F32)
-        return y.dtype == TROP_F32    ? norm_forward<float, float, float>(j, s)
-               : y.dtype == TROP_BF16 ? norm_forward<float, bf16, float>(j, s)
-                                      : norm_forward<float, __half, float>(j, s);
+        return y.dtype == TROP_F32    ? norm_forward<float, float, float>(j, sm, s)
+               : y.dtype == TROP_BF16 ? norm_forward<float, bf16, float>(j, sm, s)
+                                      : norm_forward<float, __half, float>(j, sm, s);
     if (x.dtype == TROP_BF16)
-        return tw == TROP_F32 ? norm_forward<bf16, bf16, float>(j, s) : norm_forward<bf16, bf16, bf16>(j, s);
-    return tw == TROP_F32 ? norm_forward<__half, __half, float>(j, s) : norm_forward<__half, __half, __half>(j, s);
+        return tw == TROP_F32 ? norm_forward<bf16, bf16, float>(j, sm, s) : norm_forward<bf16, bf16, bf16>(j, sm, s);
+    return tw == TROP_F32 ? norm_forward<__half, __half, float>(j, sm, s) : norm_forward<__half, __half, __half>(j, sm, s);
 }
 
 int launch_layer_norm_backward(int64_t rows, int64_t cols, const NormMat& dy, const NormMat& x, const float* mean,

@@ -10,7 +10,7 @@
 // The logits are the ordinary (+, x) product under a log-sum-exp, the smooth form of the library's
 // max-plus contraction; unlike that one they are multiply-accumulates and run on the tensor cores.
 //
-// One kernel, k_tile, computes all four products as 256-column tiles in tensor memory; what
+// One kernel, k_tile, computes all four products as tiles in tensor memory; what
 // differs is where an accumulator goes:
 //   LSE   a tile's logits are folded into each row's running maximum and sum of exponentials in
 //         registers; the logits of a unit of tiles leave as one (maximum, sum) pair per row
@@ -21,8 +21,6 @@
 // Operand tiles come by TMA into a ring of 128-byte-swizzled stages; one thread issues the
 // products, eight warps empty one accumulator while the next one fills.
 #include <cuda.h>
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -31,6 +29,7 @@
 
 #define TROP_TU 9  // this file's id in a bounds-violation record
 #include "internal.h"
+#include "packed.h"
 #include "tcgen05.h"
 #include "train.h"
 
@@ -40,17 +39,28 @@ namespace {
 
 enum { LSE = 0, GRAD = 1, DX = 2, DW = 3 };
 
-constexpr int CG = 2;                 // CTAs that share an accumulator tile
-constexpr int TM = 128 * CG;          // rows of an output tile
-constexpr int TN = 256;               // columns
-constexpr int TK = 64;                // depth of a stage: one 128-byte row of 16-bit elements
-constexpr int A_BYTES = 128 * TK * 2;         // of one CTA
-constexpr int B_BYTES = TN / CG * TK * 2;
-constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-constexpr int STAGES = CG == 1 ? 4 : 6;
-constexpr int SMEM = STAGES * STAGE_BYTES + 1024;
+constexpr int TK = 64;                 // depth of a stage: one 128-byte row of 16-bit elements
+constexpr int A_BYTES = 128 * TK * 2;  // of one CTA
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 128 + 32 * EPI_WARPS;
+
+// A tile's shape: CG CTAs share it, each with 128 of its rows and all TN columns in tensor memory,
+// NACC accumulators taking the stages of the depth in turn.
+template <int CG_, int TN_, int NACC_>
+struct Shape {
+    static constexpr int CG = CG_, TN = TN_, NACC = NACC_;
+    static constexpr int TM = 128 * CG;
+    static constexpr int B_BYTES = TN / CG * TK * 2;
+    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+    static constexpr int STAGES = 196608 / STAGE_BYTES;
+    static constexpr int SMEM = STAGES * STAGE_BYTES + 1024;
+    static constexpr int BUFS = NACC * TN == 512 ? 1 : 2;  // tiles in tensor memory at a time
+};
+using Pair = Shape<2, 256, 1>;   // products bound by the tensor cores
+using Deep = Shape<2, 256, 2>;   // long logits: half the depth per accumulator
+using Few = Shape<1, 128, 2>;    // up to 128 tokens: bound by reading the weights
+using Few1 = Shape<1, 128, 1>;
+
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float NO_MAX = -3.0e38f;  // running maximum before any logit (finite: 2^(NO_MAX - M) = 0)
@@ -78,7 +88,8 @@ __device__ __forceinline__ int64_t target_of(const Targets& t, int64_t i)
 struct Job {
     int mt, nt, inner, ks;  // tiles along rows and columns; column tiles of a unit; splits of the depth
     int kt, kper;           // depth in stages, and of one split
-    int units;
+    int units, band;
+    int a_bytes;            // of A in a stage
     int a0, ak0, b0, bk0;   // first row / depth of A and of B in their tensor maps
     int rows, cols;         // of the output (cols: LSE the vocabulary, GRAD the piece)
     uint32_t* error;
@@ -104,15 +115,14 @@ struct Job {
     Span sp_part, sp_at, sp_P, sp_lse, sp_g, sp_out, sp_acc;
 };
 
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack2(float a, float b)
+// `yes` where i == d, else `no`, as one select: written out so that 32 of them in a row do not
+// become an indexed array, which would put the logits into local memory (128 bytes a thread; the
+// loss of a tile then took 18,000 cycles against the 8,000 of its products at D = 1000).
+__device__ __forceinline__ float where(int i, int d, float yes, float no)
 {
-    if (BF16) {
-        __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<uint32_t*>(&h);
-    }
-    __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<uint32_t*>(&h);
+    float r;
+    asm("{\n .reg .pred p;\n setp.eq.s32 p, %1, %2;\n selp.f32 %0, %3, %4, p;\n}" : "=f"(r) : "r"(i), "r"(d), "f"(yes), "f"(no));
+    return r;
 }
 
 struct Unit {
@@ -122,9 +132,14 @@ template <int MODE>
 __device__ __forceinline__ Unit unit_of(const Job& j, int u)
 {
     Unit r;
-    if (MODE == LSE || MODE == GRAD) {  // rows fastest: the units that run together share columns of w
-        r.m = u % j.mt;
-        r.n = (u / j.mt) * j.inner;
+    if (MODE == LSE || MODE == GRAD) {
+        // groups of `band` row tiles, rows fastest: the units that run together cover about as many
+        // row tiles as column tiles, so each operand tile is fetched by many of them at a time
+        const int groups = j.units / j.mt, per = j.band * groups;
+        const int g = u / per, m0 = g * j.band, wide = min(j.band, j.mt - m0);
+        u -= g * per;
+        r.m = m0 + u % wide;
+        r.n = (u / wide) * j.inner;
         r.k0 = 0;
         r.k1 = j.kt;
     } else {
@@ -176,8 +191,7 @@ __device__ __forceinline__ void lse_chunk(RowState& r, float (&v)[32], int left,
     if (d >= 0 && d < 32) {
         float x = 0.f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i == (int)d) x = v[i];
+        for (int i = 0; i < 32; ++i) x = where(i, (int)d, v[i], x);
         if (TROP_IN(at, 4, j.sp_at)) *at = x;
     }
 }
@@ -191,8 +205,7 @@ __device__ __forceinline__ void grad_chunk(const RowState& r, float (&v)[32], in
     const int64_t d = r.t - col;
     if (d >= 0 && d < 32) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i == (int)d) v[i] -= 1.f;
+        for (int i = 0; i < 32; ++i) v[i] -= where(i, (int)d, 1.f, 0.f);
     }
     uint32_t w[16];
 #pragma unroll
@@ -244,12 +257,130 @@ __device__ __forceinline__ void out_chunk(float (&v)[32], int col, int64_t row, 
     }
 }
 
+// ------------------------------------------------------------------ joining the units' pairs
+// lse and loss of `rows` tokens from their units' (reference, sum) pairs; the losses' sum.
+struct JoinJob {
+    const float2* part;
+    int64_t stride;  // of one unit's pairs
+    int G;
+    int64_t rows;
+    const float* at;
+    Targets tgt;
+    float* loss;   // nullable [rows]
+    float* lse;    // [rows]
+    float* total;  // {sum or mean of the losses, rows kept}: nullable
+    float* kept;
+    int mean;
+    float2* sums;  // [CTAs]
+    uint32_t* ticket;
+    Span sp_part, sp_at, sp_loss, sp_lse, sp_total, sp_kept;
+};
+__device__ __forceinline__ void join_pair(float& M, float& s, float2 q)
+{
+    const float m = fmaxf(M, q.x);
+    s = s * pow2_whole(M - m) + q.y * pow2_whole(q.x - m);
+    M = m;
+}
+// 32 rows by WARPS warps, each row's pairs in one order whatever runs when: {sum of their losses, rows
+// kept} in every lane of warp 0.
+template <int WARPS>
+__device__ __forceinline__ float2 join_rows(const JoinJob& j, int64_t row0, float2 (*sh)[33])
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row = row0 + lane;
+    float M = NO_MAX, s = 0.f;
+    if (row < j.rows) {
+        int g = warp;
+        for (; g + 3 * WARPS < j.G; g += 4 * WARPS) {  // four loads on their way
+            float2 q[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2* p = j.part + (int64_t)(g + k * WARPS) * j.stride + row;
+                q[k] = TROP_IN(p, 8, j.sp_part) ? __ldcg(p) : make_float2(NO_MAX, 0.f);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) join_pair(M, s, q[k]);
+        }
+        for (; g < j.G; g += WARPS) {
+            const float2* p = j.part + (int64_t)g * j.stride + row;
+            if (TROP_IN(p, 8, j.sp_part)) join_pair(M, s, __ldcg(p));
+        }
+    }
+    sh[warp][lane] = make_float2(M, s);
+    __syncthreads();
+    float loss = 0.f, keep = 0.f;
+    if (warp == 0) {
+        for (int w = 1; w < WARPS; ++w) join_pair(M, s, sh[w][lane]);
+        if (row < j.rows) {
+            // M is a whole number of powers of two: M ln 2 + log s in two pieces of ln 2
+            const float lse = __fmaf_rn(M, LN2, __fmaf_rn(M, -1.9046542121259335e-09f, logf(s)));
+            const int64_t t = target_of(j.tgt, row);
+            if (TROP_IN(j.lse + row, 4, j.sp_lse)) j.lse[row] = lse;
+            if (t >= 0 && TROP_IN(j.at + row, 4, j.sp_at)) loss = lse - __ldcg(j.at + row);
+            if (t == -2) loss = NAN;
+            keep = t == -1 ? 0.f : 1.f;
+            if (j.loss && TROP_IN(j.loss + row, 4, j.sp_loss)) j.loss[row] = loss;
+        }
+        for (int o = 16; o > 0; o >>= 1) {
+            loss += __shfl_xor_sync(0xffffffffu, loss, o);
+            keep += __shfl_xor_sync(0xffffffffu, keep, o);
+        }
+    }
+    return make_float2(loss, keep);
+}
+__device__ __forceinline__ void join_total(const JoinJob& j, float loss, float keep)
+{
+    if (j.total && TROP_IN(j.total, 4, j.sp_total)) *j.total = j.mean ? __fdiv_rn(loss, keep) : loss;
+    if (j.kept && TROP_IN(j.kept, 4, j.sp_kept)) *j.kept = keep;
+}
+
+// Many tokens: 32 rows per CTA; the CTAs leave their sums and the last one to arrive adds them in CTA
+// order.
+__global__ void __launch_bounds__(256) k_lse_join(const __grid_constant__ JoinJob j)
+{
+    pdl_wait();
+    pdl_signal();
+    __shared__ float2 sh[8][33];
+    __shared__ float red[2][32];
+    __shared__ bool last;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const float2 mine = join_rows<8>(j, (int64_t)blockIdx.x * 32, sh);
+    if (threadIdx.x == 0) {
+        j.sums[blockIdx.x] = mine;
+        __threadfence();
+        last = atomicAdd(j.ticket, 1u) == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    float a = 0.f, b = 0.f;
+    for (int i = threadIdx.x; i < gridDim.x; i += 256) {
+        const float2 q = __ldcg(&j.sums[i]);
+        a += q.x;
+        b += q.y;
+    }
+    for (int o = 16; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    if (lane == 0) red[0][warp] = a, red[1][warp] = b;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        a = b = 0.f;
+        for (int w = 0; w < 8; ++w) a += red[0][w], b += red[1][w];
+        join_total(j, a, b);
+        *j.ticket = 0;
+    }
+}
+
 // ------------------------------------------------------------------ the kernel
-template <int MODE, bool BF16>
+template <int MODE, bool BF16, typename S>
 __global__ void __launch_bounds__(THREADS, 1)
-    k_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const Job j)
+    k_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+           const __grid_constant__ Job j, const __grid_constant__ JoinJob join)
 {
     constexpr bool A_MN = MODE == DW, B_MN = MODE == DX || MODE == DW;
+    constexpr int CG = S::CG, TM = S::TM, TN = S::TN, NACC = S::NACC, STAGES = S::STAGES, STAGE_BYTES = S::STAGE_BYTES, BUFS = S::BUFS;
     extern __shared__ uint8_t dyn[];
     __shared__ __align__(8) uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], drain;
     __shared__ uint32_t tmem_slot;
@@ -284,7 +415,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int n = t.n; n < n_end && ok; ++n)
                     for (int k = t.k0; k < t.k1; ++k) {
                         if (!(ok = mbar_wait(&empty[s], phase ^ 1))) break;
-                        if (rank == 0) mbar_expect_tx(&full[s], STAGE_BYTES * CG);
+                        if (rank == 0) mbar_expect_tx(&full[s], (j.a_bytes + S::B_BYTES) * CG);
                         const uint32_t bar = CG == 2 ? mapa(smem_u32(&full[s]), 0) : smem_u32(&full[s]);
                         const uint32_t sa = ring + s * STAGE_BYTES, sb = sa + A_BYTES;
                         const int am = j.a0 + t.m * TM + rank * 128, bm = j.b0 + n * TN + rank * (TN / CG);
@@ -301,7 +432,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                                 tma_load_2d<CG>(sb + c * 8192, &map_b, bm + 64 * c, bk, bar);
                         } else {
 #pragma unroll
-                            for (int c = 0; c < TN / CG / 128; ++c)
+                            for (int c = 0; c < (TN / CG + 127) / 128; ++c)
                                 tma_load_2d<CG>(sb + c * 16384, &map_b, bk, bm + 128 * c, bar);
                         }
                         ++issued;
@@ -323,8 +454,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const Unit t = unit_of<MODE>(j, u);
                 const int n_end = min(j.nt, t.n + (MODE == LSE ? j.inner : 1));
                 for (int n = t.n; n < n_end && ok; ++n, ++tile) {
-                    const uint32_t b = tile & 1;
-                    if (!(ok = mbar_wait_cluster(&tempty[b], ((tile >> 1) & 1) ^ 1))) break;
+                    const uint32_t b = tile % BUFS, acc = tmem + b * (NACC * TN);
+                    if (!(ok = mbar_wait_cluster(&tempty[b], ((tile / BUFS) & 1) ^ 1))) break;
                     tc_fence_after();
                     for (int k = t.k0; k < t.k1; ++k) {
                         if (!(ok = mbar_wait_cluster(&full[s], phase))) break;
@@ -333,8 +464,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                         const uint64_t da = smem_desc(sa, A_MN ? 8192 : 16), db = smem_desc(sa + A_BYTES, B_MN ? 8192 : 16);
 #pragma unroll
                         for (int i = 0; i < TK / 16; ++i)  // 16 k: 32 bytes along a row, or 16 rows
-                            tc_mma<CG>(tmem + b * TN, da + i * (A_MN ? 128 : 2), db + i * (B_MN ? 128 : 2), idesc,
-                                       k > t.k0 || i > 0);
+                            tc_mma<CG>(acc + (NACC == 2 ? ((k - t.k0) & 1) * TN : 0), da + i * (A_MN ? 128 : 2),
+                                       db + i * (B_MN ? 128 : 2), idesc, k >= t.k0 + NACC || i > 0);
                         tc_commit<CG>(&empty[s]);
                         if (++s == STAGES) s = 0, phase ^= 1;
                     }
@@ -373,29 +504,39 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
             for (int n = t.n; n < n_end && ok; ++n, ++tile) {
-                const uint32_t b = tile & 1;
-                ok = mbar_wait(&tfull[b], (tile >> 1) & 1);
+                const uint32_t b = tile % BUFS;
+                ok = mbar_wait(&tfull[b], (tile / BUFS) & 1);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t src = tmem + b * TN + half * 128 + ((uint32_t)(quad * 32) << 16);
+                constexpr int HALF = TN / 2, CHUNKS = HALF / 32;  // columns of a warp, loads of 32
+                const uint32_t src = tmem + b * (NACC * TN) + half * HALF + ((uint32_t)(quad * 32) << 16);
+                const bool both = NACC == 2 && t.k1 - t.k0 > 1;  // a single stage left the second one unwritten
                 uint32_t v[2][32];
                 tmem_ld32(src, v[0]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    tmem_wait_ld(v[c & 1]);
-                    if (c < 3) {
-                        tmem_ld32(src + (c + 1) * 32, v[(c + 1) & 1]);
-                    } else {  // the accumulator is in registers: the next tile may fill it
+                for (int c = 0; c < CHUNKS; ++c) {
+                    float f[32];
+                    if (NACC == 2) {
+                        if (both) tmem_ld32(src + TN + c * 32, v[1]);
+                        tmem_wait_ld(v[0]);
+                        tmem_wait_ld(v[1]);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            f[i] = both ? __uint_as_float(v[0][i]) + __uint_as_float(v[1][i]) : __uint_as_float(v[0][i]);
+                        if (c < CHUNKS - 1) tmem_ld32(src + (c + 1) * 32, v[0]);
+                    } else {
+                        tmem_wait_ld(v[c & 1]);
+                        if (c < CHUNKS - 1) tmem_ld32(src + (c + 1) * 32, v[(c + 1) & 1]);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[c & 1][i]);
+                    }
+                    if (c == CHUNKS - 1) {  // the accumulator is in registers: the next tile may fill it
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive_cluster(CG == 2 ? mapa(smem_u32(&tempty[b]), 0) : mapa(smem_u32(&tempty[b]), rank));
+                        if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&tempty[b]), 0));
                     }
-                    float f[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[c & 1][i]);
-                    const int col = n * TN + half * 128 + c * 32;
+                    const int col = n * TN + half * HALF + c * 32;
                     if (MODE == LSE) {
                         lse_chunk(r, f, j.cols - col, col, j.at + row, j);
                     } else if (MODE == GRAD) {
@@ -422,98 +563,27 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncthreads();
     if (CG == 2) cluster_sync_all();
     if (warp == 2) tmem_free_all<CG>(tmem);
-}
-
-// ------------------------------------------------------------------ joining the units' pairs
-// lse and loss of 32 rows per CTA: 8 warps share the G pairs of a row, each row's pairs in one
-// order.  With `mean` wanted the CTAs leave their sums and the last one to arrive adds them in
-// CTA order.
-struct JoinJob {
-    const float2* part;
-    int64_t stride;  // of one unit's pairs
-    int G;
-    int64_t rows;
-    const float* at;
-    Targets tgt;
-    float* loss;   // nullable [rows]
-    float* lse;    // [rows]
-    float* total;  // {sum or mean of the losses, rows kept}: nullable
-    float* kept;
-    int mean;
-    float2* sums;  // [CTAs]
-    uint32_t* ticket;
-    Span sp_part, sp_at, sp_loss, sp_lse, sp_total, sp_kept;
-};
-__global__ void __launch_bounds__(256) k_lse_join(const JoinJob j)
-{
-    pdl_wait();
-    pdl_signal();
-    __shared__ float2 sh[8][33];
-    __shared__ float red[2][32];
-    __shared__ bool last;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t row = (int64_t)blockIdx.x * 32 + lane;
-    float M = NO_MAX, s = 0.f;
-    for (int g = warp; g < j.G; g += 8) {
-        const float2* p = j.part + (int64_t)g * j.stride + row;
-        if (row < j.rows && TROP_IN(p, 8, j.sp_part)) {
-            const float2 q = *p;
-            const float m = fmaxf(M, q.x);
-            s = s * pow2_whole(M - m) + q.y * pow2_whole(q.x - m);
-            M = m;
-        }
-    }
-    sh[warp][lane] = make_float2(M, s);
-    __syncthreads();
-    if (warp == 0) {
-        for (int w = 1; w < 8; ++w) {
-            const float2 q = sh[w][lane];
-            const float m = fmaxf(M, q.x);
-            s = s * pow2_whole(M - m) + q.y * pow2_whole(q.x - m);
-            M = m;
-        }
+    if constexpr (MODE == LSE && CG == 1) {
+        // Few tokens: the last CTA to arrive joins the pairs here, which spares a launch (about 3 us).
+        __shared__ float2 sh[THREADS / 32][33];
+        __shared__ uint32_t arrived;
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0) arrived = atomicAdd(join.ticket, 1u);
+        __syncthreads();
+        if (arrived != gridDim.x - 1) return;
+        __threadfence();
         float loss = 0.f, keep = 0.f;
-        if (row < j.rows) {
-            // M is a whole number of powers of two: M ln 2 + log s in two pieces of ln 2
-            const float lse = __fmaf_rn(M, LN2, __fmaf_rn(M, -1.9046542121259335e-09f, logf(s)));
-            const int64_t t = target_of(j.tgt, row);
-            if (TROP_IN(j.lse + row, 4, j.sp_lse)) j.lse[row] = lse;
-            if (t >= 0 && TROP_IN(j.at + row, 4, j.sp_at)) loss = lse - j.at[row];
-            if (t == -2) loss = NAN;
-            keep = t == -1 ? 0.f : 1.f;
-            if (j.loss && TROP_IN(j.loss + row, 4, j.sp_loss)) j.loss[row] = loss;
+        for (int64_t row0 = 0; row0 < join.rows; row0 += 32) {
+            const float2 q = join_rows<THREADS / 32>(join, row0, sh);
+            loss += q.x;
+            keep += q.y;
+            __syncthreads();
         }
-        for (int o = 16; o > 0; o >>= 1) {
-            loss += __shfl_xor_sync(0xffffffffu, loss, o);
-            keep += __shfl_xor_sync(0xffffffffu, keep, o);
+        if (threadIdx.x == 0) {
+            join_total(join, loss, keep);
+            *join.ticket = 0;
         }
-        if (lane == 0) {
-            j.sums[blockIdx.x] = make_float2(loss, keep);
-            __threadfence();
-            last = atomicAdd(j.ticket, 1u) == gridDim.x - 1;
-        }
-    }
-    __syncthreads();
-    if (!last) return;
-    __threadfence();
-    float a = 0.f, b = 0.f;
-    for (int i = threadIdx.x; i < gridDim.x; i += 256) {
-        const float2 q = __ldcg(&j.sums[i]);
-        a += q.x;
-        b += q.y;
-    }
-    for (int o = 16; o > 0; o >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-        b += __shfl_xor_sync(0xffffffffu, b, o);
-    }
-    if (lane == 0) red[0][warp] = a, red[1][warp] = b;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        a = b = 0.f;
-        for (int w = 0; w < 8; ++w) a += red[0][w], b += red[1][w];
-        if (j.total && TROP_IN(j.total, 4, j.sp_total)) *j.total = j.mean ? __fdiv_rn(a, b) : a;
-        if (j.kept && TROP_IN(j.kept, 4, j.sp_kept)) *j.kept = b;
-        *j.ticket = 0;
     }
 }
 
@@ -542,20 +612,39 @@ __global__ void __launch_bounds__(256) k_gscale(const float* g, int64_t sg, int6
 }
 
 // ------------------------------------------------------------------ sums of the depth's splits
-template <bool BF16>
+// Four columns of a row per thread and step where rows allow 16-byte loads.
+template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(256) k_split_join(const float* acc, int ks, int64_t rows, int64_t cols, uint16_t* out,
                                                     int64_t ldo, const float* scale, Span sp_acc, Span sp_out)
 {
     pdl_wait();
     pdl_signal();
+    constexpr int W = VEC ? 4 : 1;
     const float alpha = scale ? scale[1] : 1.f;
-    const int64_t n = rows * cols;
+    const int64_t n = rows * cols / W, per_row = cols / W;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        float s = 0.f;
-        for (int k = 0; k < ks; ++k)
-            if (TROP_IN(acc + k * n + i, 4, sp_acc)) s += acc[k * n + i];
-        uint16_t* dst = out + (i / cols) * ldo + i % cols;
-        if (TROP_IN(dst, 2, sp_out)) *dst = (uint16_t)(pack2<BF16>(s * alpha, 0.f) & 0xffff);
+        float s[W];
+#pragma unroll
+        for (int w = 0; w < W; ++w) s[w] = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < ks; ++k) {
+            const float* p = acc + (k * n + i) * W;
+            if (!TROP_IN(p, 4 * W, sp_acc)) continue;
+            if (VEC) {
+                const float4 q = *reinterpret_cast<const float4*>(p);
+                s[0] += q.x, s[1] += q.y, s[2] += q.z, s[3] += q.w;
+            } else {
+                s[0] += *p;
+            }
+        }
+        const int64_t r = i / per_row;
+        uint16_t* dst = out + r * ldo + (i - r * per_row) * W;
+        if (VEC) {
+            if (TROP_IN(dst, 8, sp_out))
+                *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<BF16>(s[0] * alpha, s[1] * alpha), pack2<BF16>(s[2] * alpha, s[3] * alpha));
+        } else if (TROP_IN(dst, 2, sp_out)) {
+            *dst = (uint16_t)(pack2<BF16>(s[0] * alpha, 0.f) & 0xffff);
+        }
     }
 }
 
@@ -641,6 +730,8 @@ struct Blocks {
     {
         for (int i = 0; i < n; ++i) pool_retire(p[i], s);
     }
+    // the call's one small block, from what the stream keeps where that serves
+    int small(size_t bytes, void** out) { return stream_scratch(bytes, s, out) ? (int)TROP_OK : get(bytes, out); }
     int get(size_t bytes, void** out)
     {
         TROP_TRY(pool_alloc(bytes, s, out));
@@ -672,33 +763,47 @@ int readable(const Mat16& a, int sm, Blocks& ws, Matrix16* out)
     return TROP_OK;
 }
 
-template <int MODE, bool BF16>
-int launch_tile(const CUtensorMap& a, const CUtensorMap& b, const Job& j, int sm, cudaStream_t s)
+template <int MODE, bool BF16, typename S>
+int launch_tile(const CUtensorMap& a, const CUtensorMap& b, const Job& j, const JoinJob& join, int sm, cudaStream_t s)
 {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)std::min(j.units, sm / CG) * CG);
+    cfg.gridDim = dim3((unsigned)std::min(j.units, sm / S::CG) * S::CG);
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = SMEM;
+    cfg.dynamicSmemBytes = S::SMEM;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.x = S::CG;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = CG == 2 ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_tile<MODE, BF16>, a, b, j);
+    cfg.numAttrs = S::CG == 2 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_tile<MODE, BF16, S>, a, b, j, join);
     if (e != cudaSuccess) return cuda_error(e, "k_tile launch");
     count_launches(1);
     return TROP_OK;
 }
-template <int MODE>
-int launch_tile(bool bf16, const CUtensorMap& a, const CUtensorMap& b, const Job& j, int sm, cudaStream_t s)
+template <int MODE, typename S>
+int launch_tile(bool bf16, const CUtensorMap& a, const CUtensorMap& b, const Job& j, int sm, cudaStream_t s,
+                const JoinJob& join = JoinJob())
 {
-    return bf16 ? launch_tile<MODE, true>(a, b, j, sm, s) : launch_tile<MODE, false>(a, b, j, sm, s);
+    return bf16 ? launch_tile<MODE, true, S>(a, b, j, join, sm, s) : launch_tile<MODE, false, S>(a, b, j, join, sm, s);
 }
 
+// Row tiles of a band: as many as keep their operand (a row tile's whole depth) in about 48 MB of
+// the L2, so that the other operand is read from memory once per band.  8192x2048x65536: all 32 row
+// tiles (33 MB) 1269 us, bands of 16 / 12 / 8 / 4 1293 / 1305 / 1330 / 1378 us.
+// Up to this many tokens one row tile of one CTA holds them all, and reading the weights is the work.
+constexpr int64_t FEW_TOKENS = 128;
+// A logit's sum loses up to a last place of its accumulator every 16 products; past this depth two
+// accumulators share it.
+constexpr int64_t DEEP_LOGITS = 2048;
+// Rows of such a tile's box: the tokens' only.  The tile's other rows keep what shared memory holds,
+// and so do the accumulator's, which nobody reads.
+int few_rows(int64_t rows) { return (int)((rows + 7) / 8 * 8); }
+
+int band_of(int mt, int64_t tile_bytes) { return (int)std::min<int64_t>(mt, std::max<int64_t>(8, (48 << 20) / tile_bytes)); }
 int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 Targets targets_of(const LinearCe& q)
@@ -711,31 +816,27 @@ Targets targets_of(const LinearCe& q)
 int launch_join(JoinJob t, float2* sums, cudaStream_t s)
 {
     const int ctas = std::max(1, cdiv(t.rows, 32));
-    TROP_TRY(stream_tickets(s, 1, &t.ticket));
     t.sums = sums;
-    t.sp_loss = span_bytes(t.loss, (size_t)t.rows * 4);
-    t.sp_lse = span_bytes(t.lse, (size_t)t.rows * 4);
-    t.sp_total = span_bytes(t.total, 4);
-    t.sp_kept = span_bytes(t.kept, 4);
     const cudaError_t e = launch_pdl(k_lse_join, dim3(ctas), dim3(256), 0, s, t);
     if (e != cudaSuccess) return cuda_error(e, "k_lse_join launch");
     count_launches(1);
     return TROP_OK;
 }
 
-template <int MODE, bool BF16>
+template <int MODE, typename S>
 cudaError_t allow_smem()
 {
-    return cudaFuncSetAttribute(k_tile<MODE, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    const cudaError_t e = cudaFuncSetAttribute(k_tile<MODE, true, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    return e != cudaSuccess ? e : cudaFuncSetAttribute(k_tile<MODE, false, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
 }
 
 }  // namespace
 
 int register_linear_ce_kernels()
 {
-    const cudaError_t e[] = {allow_smem<LSE, true>(), allow_smem<LSE, false>(), allow_smem<GRAD, true>(),
-                             allow_smem<GRAD, false>(), allow_smem<DX, true>(), allow_smem<DX, false>(),
-                             allow_smem<DW, true>(), allow_smem<DW, false>()};
+    const cudaError_t e[] = {allow_smem<LSE, Pair>(), allow_smem<LSE, Deep>(), allow_smem<LSE, Few>(),
+                             allow_smem<GRAD, Pair>(), allow_smem<GRAD, Few1>(), allow_smem<DX, Pair>(),
+                             allow_smem<DX, Few1>(), allow_smem<DW, Pair>()};
     for (const cudaError_t r : e)
         if (r != cudaSuccess) return cuda_error(r, "cudaFuncSetAttribute(k_tile)");
     return TROP_OK;
@@ -755,15 +856,22 @@ int launch_linear_ce(const LinearCe& q, float* loss, float* lse, float* total, f
     t.total = total;
     t.kept = kept;
     t.mean = mean;
+    t.sp_loss = span_bytes(t.loss, (size_t)t.rows * 4);
+    t.sp_lse = span_bytes(t.lse, (size_t)t.rows * 4);
+    t.sp_total = span_bytes(t.total, 4);
+    t.sp_kept = span_bytes(t.kept, 4);
+    TROP_TRY(stream_tickets(s, 1, &t.ticket));
     const size_t sums = (size_t)std::max(1, cdiv(t.rows, 32)) * sizeof(float2);
     void* p;
     if (t.rows == 0) {
-        TROP_TRY(ws.get(sums, &p));
+        TROP_TRY(ws.small(sums, &p));
         return launch_join(t, (float2*)p, s);
     }
     Matrix16 x, w;
     TROP_TRY(readable(q.x, sm, ws, &x));
     TROP_TRY(readable(q.w, sm, ws, &w));
+    const bool few = x.rows <= FEW_TOKENS;
+    const int TM = few ? Few::TM : Pair::TM, TN = few ? Few::TN : Pair::TN, CG = few ? 1 : 2;
     Job j = {};
     TROP_TRY(device_error_word(&j.error));
     j.rows = (int)x.rows;
@@ -780,19 +888,24 @@ int launch_linear_ce(const LinearCe& q, float* loss, float* lse, float* total, f
     }
     const int groups = cdiv(j.nt, j.inner);
     j.units = j.mt * groups;
+    j.band = band_of(j.mt, TM * x.cols * 2);
     j.tgt = t.tgt;
     t.stride = (int64_t)j.mt * TM;
     t.G = 2 * groups;
     const size_t pairs = (size_t)t.G * t.stride * sizeof(float2), at = (size_t)(x.rows + 63) / 64 * 64 * 4;
-    TROP_TRY(ws.get(pairs + at + sums, &p));
+    TROP_TRY(ws.small(pairs + at + sums, &p));
     t.part = j.part = (float2*)p;
     t.at = j.at = (float*)((char*)p + pairs);
     t.sp_part = j.sp_part = span_bytes(j.part, pairs);
     t.sp_at = j.sp_at = span_bytes(j.at, (size_t)x.rows * 4);
+    const int a_rows = few ? few_rows(x.rows) : 128;
+    j.a_bytes = a_rows * TK * 2;
     CUtensorMap ma, mb;
-    TROP_TRY(make_map(&ma, q.bf16, x.p, x.cols, x.rows, x.ld, 128));
+    TROP_TRY(make_map(&ma, q.bf16, x.p, x.cols, x.rows, x.ld, a_rows));
     TROP_TRY(make_map(&mb, q.bf16, w.p, w.cols, w.rows, w.ld, 128));
-    TROP_TRY(launch_tile<LSE>(q.bf16, ma, mb, j, sm, s));
+    if (few) return launch_tile<LSE, Few>(q.bf16, ma, mb, j, sm, s, t);
+    TROP_TRY((x.cols > DEEP_LOGITS ? launch_tile<LSE, Deep>(q.bf16, ma, mb, j, sm, s)
+                                   : launch_tile<LSE, Pair>(q.bf16, ma, mb, j, sm, s)));
     return launch_join(t, (float2*)((char*)p + pairs + at), s);
 }
 
@@ -801,17 +914,20 @@ int launch_linear_ce_backward(const LinearCe& q, const float* g, int64_t sg, con
 {
     const DeviceInfo* dev;
     TROP_TRY(ensure_device(&dev));
-    const int sm = dev->sm_count, pairs = sm / CG;
     const int64_t N = q.x.rows, D = q.x.cols, V = q.w.rows;
+    const bool few = N <= FEW_TOKENS;
+    const int TM = few ? Few1::TM : Pair::TM, TN = few ? Few1::TN : Pair::TN;  // of the logits and of dx
+    const int sm = dev->sm_count, teams = few ? sm : sm / 2;
+    const int a_rows = few ? few_rows(N) : 128;
     Blocks ws(s);
     Matrix16 x, w;
     TROP_TRY(readable(q.x, sm, ws, &x));
     TROP_TRY(readable(q.w, sm, ws, &w));
 
-    // A piece of the vocabulary: P takes at most 512 MiB (and at least 16 tiles' columns).
-    const int64_t whole = (V + TN - 1) / TN * TN;
-    int64_t piece = ((int64_t)1 << 28) / std::max<int64_t>(N, 1) / TN * TN;
-    piece = std::min(whole, std::max<int64_t>(piece, 16 * TN));
+    // A piece of the vocabulary: P takes at most 512 MiB (and at least 4096 columns).
+    const int64_t whole = (V + 255) / 256 * 256;
+    int64_t piece = ((int64_t)1 << 28) / N / 256 * 256;
+    piece = std::min(whole, std::max<int64_t>(piece, 4096));
     const int pieces = cdiv(V, piece);
     // Splits of dx's depth (a piece's columns): the fewest rounds of stages, each split costing about
     // the time of 8 stages more for its partial sums.
@@ -822,7 +938,7 @@ int launch_linear_ce_backward(const LinearCe& q, const float* g, int64_t sg, con
         for (int c = 1; c <= std::min(dx_kt, 64); ++c) {
             const int per = cdiv(dx_kt, c);
             if (cdiv(dx_kt, per) != c) continue;
-            const int64_t cost = (int64_t)cdiv((int64_t)dx_mt * dx_nt * c, pairs) * (per + (c > 1 ? 8 : 0));
+            const int64_t cost = (int64_t)cdiv((int64_t)dx_mt * dx_nt * c, teams) * (per + (c > 1 ? 8 : 0));
             if (cost < best) best = cost, ks = c;
         }
     }
@@ -841,18 +957,19 @@ int launch_linear_ce_backward(const LinearCe& q, const float* g, int64_t sg, con
         count_launches(1);
     }
     CUtensorMap x_k, w_k, x_mn, w_mn, p_k, p_mn;
-    TROP_TRY(make_map(&x_k, q.bf16, x.p, D, N, x.ld, 128));
+    TROP_TRY(make_map(&x_k, q.bf16, x.p, D, N, x.ld, a_rows));
     TROP_TRY(make_map(&w_k, q.bf16, w.p, D, V, w.ld, 128));
     TROP_TRY(make_map(&x_mn, q.bf16, x.p, D, N, x.ld, 64));
     TROP_TRY(make_map(&w_mn, q.bf16, w.p, D, V, w.ld, 64));
     for (int i = 0; i < pieces; ++i) {
         const int64_t v0 = i * piece, cols = std::min(piece, V - v0);
-        TROP_TRY(make_map(&p_k, q.bf16, P, cols, N, piece, 128));
+        TROP_TRY(make_map(&p_k, q.bf16, P, cols, N, piece, a_rows));
         TROP_TRY(make_map(&p_mn, q.bf16, P, cols, N, piece, 64));
         Job j = {};
         TROP_TRY(device_error_word(&j.error));
         j.inner = 1;
         j.ks = 1;
+        j.a_bytes = a_rows * TK * 2;
         j.scale = (const float*)scale;
         {
             Job t = j;
@@ -862,6 +979,7 @@ int launch_linear_ce_backward(const LinearCe& q, const float* g, int64_t sg, con
             t.nt = cdiv(cols, TN);
             t.kt = t.kper = cdiv(D, TK);
             t.units = t.mt * t.nt;
+            t.band = band_of(t.mt, TM * D * 2);
             t.b0 = (int)v0;
             t.v0 = v0;
             t.tgt = targets_of(q);
@@ -875,22 +993,24 @@ int launch_linear_ce_backward(const LinearCe& q, const float* g, int64_t sg, con
             t.sp_lse = span_bytes(lse, (size_t)N * 4);
             const int64_t size[1] = {N}, stride[1] = {sg};
             t.sp_g = span_of(g, 4, 1, size, stride);
-            TROP_TRY(launch_tile<GRAD>(q.bf16, x_k, w_k, t, sm, s));
+            TROP_TRY((few ? launch_tile<GRAD, Few1>(q.bf16, x_k, w_k, t, sm, s)
+                           : launch_tile<GRAD, Pair>(q.bf16, x_k, w_k, t, sm, s)));
         }
         if (dw) {
             Job t = j;
             t.rows = (int)cols;
             t.cols = (int)D;
-            t.mt = cdiv(cols, TM);
-            t.nt = cdiv(D, TN);
+            t.mt = cdiv(cols, Pair::TM);
+            t.nt = cdiv(D, Pair::TN);
             t.kt = t.kper = cdiv(N, TK);
+            t.a_bytes = A_BYTES;
             t.units = t.mt * t.nt;
             t.out = (uint16_t*)dw->p + v0 * dw->sr;
             t.ldo = dw->sr;
             t.vec = ((uintptr_t)t.out & 15) == 0 && dw->sr % 8 == 0;
             const int64_t size[2] = {cols, D}, stride[2] = {dw->sr, 1};
             t.sp_out = span_of(t.out, 2, 2, size, stride);
-            TROP_TRY(launch_tile<DW>(q.bf16, p_mn, x_mn, t, sm, s));
+            TROP_TRY((launch_tile<DW, Pair>(q.bf16, p_mn, x_mn, t, sm, s)));
         }
         if (dx) {
             Job t = j;
@@ -913,17 +1033,18 @@ int launch_linear_ce_backward(const LinearCe& q, const float* g, int64_t sg, con
                 const int64_t size[2] = {N, D}, stride[2] = {dx->sr, 1};
                 t.sp_out = span_of(t.out, 2, 2, size, stride);
             }
-            TROP_TRY(launch_tile<DX>(q.bf16, p_k, w_mn, t, sm, s));
+            TROP_TRY((few ? launch_tile<DX, Few1>(q.bf16, p_k, w_mn, t, sm, s)
+                           : launch_tile<DX, Pair>(q.bf16, p_k, w_mn, t, sm, s)));
         }
     }
     if (dx && ks > 1) {
         const int64_t size[2] = {N, D}, stride[2] = {dx->sr, 1};
         const Span sp_out = span_of(dx->p, 2, 2, size, stride), sp_acc = span_bytes(acc, acc_bytes);
-        const dim3 grid(grid_for(N * D, sm));
-        const cudaError_t e = q.bf16 ? launch_pdl(k_split_join<true>, grid, dim3(256), 0, s, (const float*)acc, ks, N, D,
-                                                  (uint16_t*)dx->p, dx->sr, (const float*)scale, sp_acc, sp_out)
-                                     : launch_pdl(k_split_join<false>, grid, dim3(256), 0, s, (const float*)acc, ks, N, D,
-                                                  (uint16_t*)dx->p, dx->sr, (const float*)scale, sp_acc, sp_out);
+        const bool vec = D % 4 == 0 && dx->sr % 4 == 0 && ((uintptr_t)dx->p & 7) == 0;
+        const auto kernel = q.bf16 ? (vec ? k_split_join<true, true> : k_split_join<true, false>)
+                                   : (vec ? k_split_join<false, true> : k_split_join<false, false>);
+        const cudaError_t e = launch_pdl(kernel, dim3(grid_for(N * D / (vec ? 4 : 1), sm)), dim3(256), 0, s, (const float*)acc,
+                                         ks, N, D, (uint16_t*)dx->p, dx->sr, (const float*)scale, sp_acc, sp_out);
         if (e != cudaSuccess) return cuda_error(e, "k_split_join launch");
         count_launches(1);
     }

@@ -718,6 +718,7 @@ extern "C" int tropical_release_pool(void)
         T.arrays.clear();
         T.retired.clear();
     }
+    release_scratch();
     cudaSetDevice(cur);
     P.free_.clear();
     for (cudaEvent_t e : P.events_) cudaEventDestroy(e);

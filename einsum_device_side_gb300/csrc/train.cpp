@@ -358,22 +358,14 @@ extern "C" int tropical_adamw_step(int64_t n, const trop_adamw_tensor* tensors, 
     AdamwScalars k;
     TROP_TRY(adamw_scalars(options, &k));
     TROP_TRY(adamw_tensors(n, tensors, param_dtype, grad_dtype, state_bits, copy_dtype));
-    return guarded([&] {
-        TablesOwner o;
-        TROP_TRY(adamw_tables_fill(o.t, n, tensors, param_dtype, grad_dtype, state_bits == 8, copy_dtype));
-        return launch_adamw(*o.t, k, (cudaStream_t)stream);
-    });
+    return launch_adamw(n, tensors, param_dtype, grad_dtype, state_bits == 8, copy_dtype, k, (cudaStream_t)stream);
 }
 
 extern "C" int tropical_adamw_state_values(int64_t n, const trop_adamw_state* states, void* stream)
 {
     clear_error();
     TROP_TRY(adamw_states(n, states));
-    return guarded([&] {
-        TablesOwner o;
-        TROP_TRY(adamw_states_fill(o.t, n, states));
-        return launch_adamw_values(*o.t, (cudaStream_t)stream);
-    });
+    return launch_adamw_values(n, states, (cudaStream_t)stream);
 }
 
 extern "C" int tropical_adamw_plan_create(int64_t n, const trop_adamw_tensor* tensors, int param_dtype, int grad_dtype,
@@ -425,7 +417,7 @@ extern "C" int tropical_adamw_plan_step(trop_adamw_plan plan, const trop_adamw_o
     AdamwScalars k;
     TROP_TRY(adamw_scalars(options, &k));
     TROP_TRY(plan_ready(plan));
-    return launch_adamw(*plan->tables.t, k, (cudaStream_t)stream);
+    return launch_adamw_plan(*plan->tables.t, k, (cudaStream_t)stream);
 }
 
 extern "C" int tropical_adamw_plan_values(trop_adamw_plan plan, void* stream)
@@ -433,7 +425,7 @@ extern "C" int tropical_adamw_plan_values(trop_adamw_plan plan, void* stream)
     clear_error();
     TROP_TRY(plan_ready(plan));
     if (!plan->values) return set_error(TROP_ERR_INVALID_ARG, "the plan was made without buffers for the states' values");
-    return launch_adamw_values(*plan->tables.t, (cudaStream_t)stream);
+    return launch_adamw_plan_values(*plan->tables.t, (cudaStream_t)stream);
 }
 
 extern "C" int tropical_adamw_plan_destroy(trop_adamw_plan plan)

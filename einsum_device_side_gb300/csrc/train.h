@@ -55,14 +55,18 @@ struct AdamwScalars {
     float decay, lr;          // 1 - lr weight_decay; lr / (1 - beta1^step)
     float gscale;             // the gradient's factor
 };
-// The tensors of a step (and the states whose values are wanted), laid out for the launches.
+// A plan's tensors (and the states whose values are wanted), laid out in device memory.
 struct AdamwTables;
 AdamwTables* adamw_tables();
 void adamw_tables_free(AdamwTables* t);
 int adamw_tables_fill(AdamwTables* a, int64_t n, const trop_adamw_tensor* t, int pdtype, int gdtype, int state8,
                       int copy_dtype);
 int adamw_states_fill(AdamwTables* a, int64_t n, const trop_adamw_state* t);
-int launch_adamw(const AdamwTables& a, const AdamwScalars& k, cudaStream_t s);
-int launch_adamw_values(const AdamwTables& a, cudaStream_t s);
+int launch_adamw_plan(const AdamwTables& a, const AdamwScalars& k, cudaStream_t s);
+int launch_adamw_plan_values(const AdamwTables& a, cudaStream_t s);
+// One call's tensors, in the launches' parameters.
+int launch_adamw(int64_t n, const trop_adamw_tensor* t, int pdtype, int gdtype, int state8, int copy_dtype,
+                 const AdamwScalars& k, cudaStream_t s);
+int launch_adamw_values(int64_t n, const trop_adamw_state* t, cudaStream_t s);
 
 }  // namespace trop

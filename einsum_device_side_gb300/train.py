@@ -23,6 +23,16 @@ def _lib():
     return _pkg._lib or _pkg.load()
 
 
+def _fast():
+    """The CPython binding (the library loaded), or None where ctypes serves every call."""
+    if _pkg._fc is None:
+        _lib()
+    return _pkg._fc
+
+
+_empty, _empty_like, _f32 = torch.empty, torch.empty_like, torch.float32
+
+
 def _fail(code: int, message: str):
     raise _pkg.TropicalError(code, message)
 
@@ -76,29 +86,27 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.
     x's or float32.  The result has x's type; a float32 ``x`` (a tropical product, say) may give ``out_dtype``
     bfloat16 or float16.  Returns ``(y, mean, rstd)``, the float32 statistics with x's leading shape:
     what ``layer_norm_backward`` reads."""
-    lib = _lib()
+    fc = _fast()
+    if out is None:
+        out = _empty_like(x) if out_dtype is None else _empty_like(x, dtype=out_dtype)
+    elif out.shape != x.shape or (out_dtype is not None and out.dtype != out_dtype):
+        _fail(-5, f"out is {tuple(out.shape)} {out.dtype}, not {tuple(x.shape)} {out_dtype or x.dtype}")
+    mean = _empty(x.shape[:-1], dtype=_f32, device=x.device)
+    rstd = _empty_like(mean)
+    if fc is not None:
+        rc = fc.layer_norm_t(x, weight, bias, eps, out, mean, rstd, stream)
+        if rc == 0:
+            return out, mean, rstd
+        if rc < 0:
+            _pkg._check(rc)
     x2 = _rows(x, "x")
     n, c = x2.shape
     w = weight if weight is not None else bias
     wdtype = w.dtype if w is not None else x.dtype
     _check_vector(weight, "weight", x, wdtype, c)
     _check_vector(bias, "bias", x, wdtype, c)
-    if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
-        y = out if x.dim() == 2 else out.view(n, c)
-    else:
-        if out.shape != x.shape or (out_dtype is not None and out.dtype != out_dtype):
-            _fail(-5, f"out is {tuple(out.shape)} {out.dtype}, not {tuple(x.shape)} {out_dtype or x.dtype}")
-        y = out if x.dim() == 2 else out.view(n, c)
-    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    rstd = torch.empty_like(mean)
-    if _pkg._fc is not None:
-        rc = _pkg._fc.layer_norm_t(x2, weight, bias, _CODES.get(wdtype, -1), eps, y, mean, rstd, stream)
-    else:
-        rc = lib.tropical_layer_norm(_desc(x2), _ptr(weight), _ptr(bias), _CODES.get(wdtype, -1), eps, _desc(y),
-                                     _ptr(mean), _ptr(rstd), _pkg._stream(stream, x))
-    if rc:
-        _pkg._check(rc)
+    _pkg._check(_lib().tropical_layer_norm(_desc(x2), _ptr(weight), _ptr(bias), _CODES.get(wdtype, -1), eps,
+                                        _desc(out.view(n, c)), _ptr(mean), _ptr(rstd), _pkg._stream(stream, x)))
     return out, mean, rstd
 
 
@@ -107,29 +115,31 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
                         want_bias: bool = True, weight_dtype: torch.dtype | None = None, stream=None):
     """Gradient of ``layer_norm``: ``(dx, dweight, dbias)``, an unwanted one None.  ``dy`` has the forward's result type;
     the weight's and bias's gradients have ``weight``'s type (``weight_dtype`` without one, by default x's)."""
-    lib = _lib()
-    x2, dy2 = _rows(x, "x"), _rows(dy, "dy")
+    fc = _fast()
     if dy.shape != x.shape:
         _fail(-5, f"dy has shape {tuple(dy.shape)}, x {tuple(x.shape)}")
-    n, c = x2.shape
     wdtype = weight.dtype if weight is not None else weight_dtype or x.dtype
+    c = x.shape[-1]
+    dx = _empty_like(x) if want_x else None
+    dw = _empty(c, dtype=wdtype, device=x.device) if want_weight else None
+    db = None if not want_bias else _empty_like(dw) if want_weight else _empty(c, dtype=wdtype, device=x.device)
+    if fc is not None:
+        rc = fc.layer_norm_backward_t(dy, x, mean, rstd, weight, dx, dw, db, stream)
+        if rc == 0:
+            return dx, dw, db
+        if rc < 0:
+            _pkg._check(rc)
+    x2, dy2 = _rows(x, "x"), _rows(dy, "dy")
+    n = x2.shape[0]
     _check_vector(weight, "weight", x, wdtype, c)
-    _check_vector(mean if mean.dim() == 1 else mean.view(-1), "mean", x, torch.float32, n)
-    _check_vector(rstd if rstd.dim() == 1 else rstd.view(-1), "rstd", x, torch.float32, n)
+    _check_vector(mean.reshape(-1), "mean", x, torch.float32, n)
+    _check_vector(rstd.reshape(-1), "rstd", x, torch.float32, n)
     if dy.get_device() != x.get_device():
         _fail(-3, f"dy is on {dy.device}, x on {x.device}")
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if want_x else None
-    dx2 = dx if dx is None or x.dim() == 2 else dx.view(n, c)
-    dw = torch.empty(c, dtype=wdtype, device=x.device) if want_weight else None
-    db = torch.empty(c, dtype=wdtype, device=x.device) if want_bias else None
-    code = _CODES.get(wdtype, -1)
-    if _pkg._fc is not None:
-        rc = _pkg._fc.layer_norm_backward_t(dy2, x2, mean, rstd, weight, code, dx2, dw, db, stream)
-    else:
-        rc = lib.tropical_layer_norm_backward(_desc(dy2), _desc(x2), _ptr(mean), _ptr(rstd), _ptr(weight), code,
-                                              _desc(dx2), _ptr(dw), _ptr(db), _pkg._stream(stream, x))
-    if rc:
-        _pkg._check(rc)
+    mean, rstd = mean.contiguous(), rstd.contiguous()
+    _pkg._check(_lib().tropical_layer_norm_backward(_desc(dy2), _desc(x2), _ptr(mean), _ptr(rstd), _ptr(weight),
+                                                 _CODES.get(wdtype, -1), _desc(None if dx is None else dx.view(n, c)),
+                                                 _ptr(dw), _ptr(db), _pkg._stream(stream, x)))
     return dx, dw, db
 
 
@@ -169,26 +179,25 @@ def linear_cross_entropy(x: torch.Tensor, w: torch.Tensor, target: torch.Tensor,
     ``(loss, lse, kept)``: the loss (one per token for ``reduction="none"``, else a scalar; tokens whose target is
     ``ignore_index`` have none), the log-sum-exp of each token's logits, and the number of tokens kept, all float32.
     A target outside the vocabulary gives NaN."""
-    lib = _lib()
+    fc = _fast()
     if reduction not in _REDUCTIONS:
         _fail(-1, f"reduction must be one of {_REDUCTIONS}, got {reduction!r}")
-    _check_head(x, w, target)
     n = x.shape[0] if x.dim() else 0
-    few = torch.empty(2, dtype=torch.float32, device=x.device)
-    total, kept = few[0], few[1]
-    each = torch.empty((2, n) if reduction == "none" else (1, n), dtype=torch.float32, device=x.device)
-    lse = each[-1]
-    loss = each[0] if reduction == "none" else None
-    if _pkg._fc is not None:
-        rc = _pkg._fc.linear_ce_t(x, w, target, ignore_index, reduction == "mean", loss, lse,
-                                  total if loss is None else None, kept, stream)
-    else:
-        rc = lib.tropical_linear_cross_entropy(_desc(x), _desc(w), _desc(target), ignore_index, reduction == "mean",
-                                               _ptr(loss), _ptr(lse), _ptr(total) if loss is None else None, _ptr(kept),
-                                               _pkg._stream(stream, x))
-    if rc:
-        _pkg._check(rc)
-    return total if loss is None else loss, lse, kept
+    total, kept = _empty(2, dtype=_f32, device=x.device).unbind()
+    lse = _empty(n, dtype=_f32, device=x.device)
+    loss = _empty_like(lse) if reduction == "none" else None
+    each, mean = loss is not None, reduction == "mean"
+    if fc is not None:
+        rc = fc.linear_ce_t(x, w, target, ignore_index, mean, loss, lse, None if each else total, kept, stream)
+        if rc == 0:
+            return loss if each else total, lse, kept
+        if rc < 0:
+            _pkg._check(rc)
+    _check_head(x, w, target)
+    _pkg._check(_lib().tropical_linear_cross_entropy(_desc(x), _desc(w), _desc(target), ignore_index, mean, _ptr(loss),
+                                                  _ptr(lse), None if each else _ptr(total), _ptr(kept),
+                                                  _pkg._stream(stream, x)))
+    return loss if each else total, lse, kept
 
 
 def linear_cross_entropy_backward(dloss: torch.Tensor, x: torch.Tensor, w: torch.Tensor, target: torch.Tensor,
@@ -198,7 +207,15 @@ def linear_cross_entropy_backward(dloss: torch.Tensor, x: torch.Tensor, w: torch
 
     ``dloss``: float32, one per token or a scalar for all of them.  With ``kept`` (the mean's gradient) it is divided by
     that count.  The logits are formed again in pieces of the vocabulary."""
-    lib = _lib()
+    fc = _fast()
+    dx = _empty(x.shape, dtype=x.dtype, device=x.device) if want_x else None
+    dw = _empty(w.shape, dtype=w.dtype, device=w.device) if want_w else None
+    if fc is not None:
+        rc = fc.linear_ce_backward_t(x, w, target, ignore_index, dloss, lse, kept, dx, dw, stream)
+        if rc == 0:
+            return dx, dw
+        if rc < 0:
+            _pkg._check(rc)
     _check_head(x, w, target)
     if dloss.dtype != torch.float32:
         _fail(-4, f"dloss must be float32, got {dloss.dtype}")
@@ -210,17 +227,9 @@ def linear_cross_entropy_backward(dloss: torch.Tensor, x: torch.Tensor, w: torch
     for t, name in ((dloss, "dloss"), (kept, "kept")):
         if t is not None and t.get_device() != x.get_device():
             _fail(-3, f"{name} is on {t.device}, x on {x.device}")
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if want_x else None
-    dw = torch.empty(w.shape, dtype=w.dtype, device=w.device) if want_w else None
-    stride = dloss.stride(0) if dloss.dim() else 0
-    if _pkg._fc is not None:
-        rc = _pkg._fc.linear_ce_backward_t(dloss, stride, x, w, target, ignore_index, lse, kept, dx, dw, stream)
-    else:
-        rc = lib.tropical_linear_cross_entropy_backward(_ptr(dloss), stride, _desc(x), _desc(w), _desc(target),
-                                                        ignore_index, _ptr(lse), _ptr(kept), _desc(dx), _desc(dw),
-                                                        _pkg._stream(stream, x))
-    if rc:
-        _pkg._check(rc)
+    _pkg._check(_lib().tropical_linear_cross_entropy_backward(
+        _ptr(dloss), dloss.stride(0) if dloss.dim() else 0, _desc(x), _desc(w), _desc(target), ignore_index, _ptr(lse),
+        _ptr(kept), _desc(dx), _desc(dw), _pkg._stream(stream, x)))
     return dx, dw
 
 
@@ -394,7 +403,12 @@ class AdamWPlan:
         """Fills and returns ``values``."""
         if self._h is None:
             raise RuntimeError("plan is closed")
-        _pkg._check(_pkg._lib.tropical_adamw_plan_values(self._h, _pkg._stream(stream, self._like)))
+        if _pkg._fc is not None:
+            rc = _pkg._fc.adamw_plan_values(self._h, self._like, stream)
+        else:
+            rc = _pkg._lib.tropical_adamw_plan_values(self._h, _pkg._stream(stream, self._like))
+        if rc:
+            _pkg._check(rc)
         return self.values
 
     def close(self):

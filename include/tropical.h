@@ -474,8 +474,9 @@ int tropical_adamw_step(int64_t n, const trop_adamw_tensor* tensors, int param_d
  * tropical_adamw_plan_values writes the values of 8-bit states (see below) to
  * the buffers of `states`, which were given at creation (nullable; INVALID_ARG
  * if they were not).  Steps of one plan from several host threads are the
- * caller's to order.  Destroying a plan while a step runs is allowed: the
- * launch carries its table. */
+ * caller's to order.  The table lies in device memory: creation allocates it
+ * and copies it there (OOM besides the errors above), destruction frees it
+ * (cudaFree waits for the device). */
 typedef struct trop_adamw_plan_s* trop_adamw_plan;
 struct trop_adamw_state_s;
 int tropical_adamw_plan_create(int64_t n, const trop_adamw_tensor* tensors, int param_dtype, int grad_dtype,
