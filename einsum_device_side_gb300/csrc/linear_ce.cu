@@ -53,9 +53,13 @@ struct Shape {
     static constexpr int B_BYTES = TN / CG * TK * 2;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int STAGES = 196608 / STAGE_BYTES;
-    static constexpr int SMEM = STAGES * STAGE_BYTES + 1024;
+    static constexpr int RING = STAGES * STAGE_BYTES;
     static constexpr int BUFS = NACC * TN == 512 ? 1 : 2;  // tiles in tensor memory at a time
 };
+constexpr int BOX_BYTES = 4096;  // 32 rows of 128 bytes: what a result warp hands to one store
+// dynamic shared memory: the ring, the result warps' boxes (LSE has none), room to align
+template <int MODE, typename S>
+constexpr int smem_bytes() { return S::RING + (MODE == LSE ? 0 : EPI_WARPS * BOX_BYTES) + 1024; }
 using Pair = Shape<2, 256, 1>;   // products bound by the tensor cores
 using Deep = Shape<2, 256, 2>;   // long logits: half the depth per accumulator
 using Few = Shape<1, 128, 2>;    // up to 128 tokens: bound by reading the weights
@@ -91,6 +95,7 @@ struct Job {
     int units, band;
     int a_bytes;            // of A in a stage
     int a0, ak0, b0, bk0;   // first row / depth of A and of B in their tensor maps
+    int pad_rows;           // rows of one split's f32 sums
     int rows, cols;         // of the output (cols: LSE the vocabulary, GRAD the piece)
     uint32_t* error;
     Targets tgt;
@@ -98,8 +103,6 @@ struct Job {
     float2* part;           // [2 * (units / mt)][mt * TM]
     float* at;              // [rows]: the logit of the target
     // GRAD
-    void* P;
-    int64_t ldp;
     int64_t v0;             // the piece's first column
     const float* lse;
     const float* g;
@@ -107,12 +110,11 @@ struct Job {
     const float* count;     // nullable: g is divided by it
     const float* scale;     // nullable: {factor of P, factor of the products with P}
     // DX, DW
-    void* out;              // null while pieces are still to come
+    void* out;              // null: f32 sums, through map_c
     int64_t ldo;
-    int vec;                // rows of out start on 16 bytes
-    float* acc;             // [ks][rows][cols] or null
-    int add;                // acc holds the pieces before
-    Span sp_part, sp_at, sp_P, sp_lse, sp_g, sp_out, sp_acc;
+    int vec;                // rows of out start on 16 bytes: through map_c
+    int add;                // f32 sums: added to the pieces before
+    Span sp_part, sp_at, sp_lse, sp_g, sp_out;
 };
 
 // `yes` where i == d, else `no`, as one select: written out so that 32 of them in a row do not
@@ -197,8 +199,7 @@ __device__ __forceinline__ void lse_chunk(RowState& r, float (&v)[32], int left,
 }
 
 template <bool BF16>
-__device__ __forceinline__ void grad_chunk(const RowState& r, float (&v)[32], int64_t col, uint16_t* dst, bool live,
-                                           const Job& j)
+__device__ __forceinline__ void grad_chunk(const RowState& r, float (&v)[32], int64_t col, uint32_t (&w)[16])
 {
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = ex2(__fmaf_rn(v[i], LOG2E, r.nlse));
@@ -207,54 +208,51 @@ __device__ __forceinline__ void grad_chunk(const RowState& r, float (&v)[32], in
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] -= where(i, (int)d, 1.f, 0.f);
     }
-    uint32_t w[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) w[i] = r.t == -1 ? 0u : pack2<BF16>(v[2 * i] * r.g, v[2 * i + 1] * r.g);
-    if (live) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (TROP_IN(dst + 8 * i, 16, j.sp_P))
-                *reinterpret_cast<uint4*>(dst + 8 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-    }
 }
 
-template <bool BF16>
-__device__ __forceinline__ void out_chunk(float (&v)[32], int col, int64_t row, const Job& j, float* acc, float alpha)
+// `words` 32-bit words of the lane's row into its warp's box from 16-byte piece `piece` on, swizzled as
+// the box's store expects: piece p of row r lies at p ^ (r mod 8), so the lanes' writes spread over all
+// banks.
+template <int WORDS>
+__device__ __forceinline__ void to_box(uint32_t box, int lane, int piece, const uint32_t (&w)[WORDS])
 {
-    const int left = j.cols - col;
-    if (left <= 0) return;
-    if (j.add) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < left && TROP_IN(acc + i, 4, j.sp_acc)) v[i] += acc[i];
-    }
-    if (!j.out) {
-        if (left >= 32 && (((uintptr_t)acc) & 15) == 0) {
+    for (int i = 0; i < WORDS / 4; ++i)
+        st_shared16(box + lane * 128 + (((piece + i) ^ (lane & 7)) << 4), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+}
+// The warp's box to (x, y), where that lies in the output.
+__device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t box, int lane, int x, int y, int cols, int rows,
+                                          bool add)
+{
+    async_proxy_fence();
+    __syncwarp();
+    if (lane == 0 && x < cols && y < rows) tma_store_2d(map, box, x, y, add);
+}
+// Before the box is written again: the store has read it.
+__device__ __forceinline__ void box_free(int lane)
+{
+    if (lane == 0) tma_store_wait_read();
+    __syncwarp();
+}
+
+// The same for an output whose rows do not start on 16 bytes: the warp writes row after row, its lanes
+// neighbouring elements.
+__device__ __forceinline__ void copy_box(uint32_t box, int lane, int x, int64_t y, const Job& j)
+{
+    __syncwarp();
+    const int rows = (int)min((int64_t)32, j.rows - y);
+    for (int r = 0; r < rows; ++r)
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (TROP_IN(acc + 4 * i, 16, j.sp_acc))
-                    *reinterpret_cast<float4*>(acc + 4 * i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (i < left && TROP_IN(acc + i, 4, j.sp_acc)) acc[i] = v[i];
+        for (int h = 0; h < 2; ++h) {
+            const int e = h * 32 + lane;
+            uint16_t v;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(box + r * 128 + (((e >> 3) ^ (r & 7)) << 4) + (e & 7) * 2));
+            uint16_t* dst = (uint16_t*)j.out + (y + r) * j.ldo + x + e;
+            if (x + e < j.cols && TROP_IN(dst, 2, j.sp_out)) *dst = v;
         }
-        return;
-    }
-    uint16_t* dst = (uint16_t*)j.out + row * j.ldo + col;
-    uint32_t w[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = pack2<BF16>(v[2 * i] * alpha, v[2 * i + 1] * alpha);
-    if (j.vec && left >= 32) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (TROP_IN(dst + 8 * i, 16, j.sp_out))
-                *reinterpret_cast<uint4*>(dst + 8 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < left && TROP_IN(dst + i, 2, j.sp_out)) dst[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
-    }
+    __syncwarp();
 }
 
 // ------------------------------------------------------------------ joining the units' pairs
@@ -377,7 +375,7 @@ __global__ void __launch_bounds__(256) k_lse_join(const __grid_constant__ JoinJo
 template <int MODE, bool BF16, typename S>
 __global__ void __launch_bounds__(THREADS, 1)
     k_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-           const __grid_constant__ Job j, const __grid_constant__ JoinJob join)
+           const __grid_constant__ CUtensorMap map_c, const __grid_constant__ Job j, const __grid_constant__ JoinJob join)
 {
     constexpr bool A_MN = MODE == DW, B_MN = MODE == DX || MODE == DW;
     constexpr int CG = S::CG, TM = S::TM, TN = S::TN, NACC = S::NACC, STAGES = S::STAGES, STAGE_BYTES = S::STAGE_BYTES, BUFS = S::BUFS;
@@ -479,6 +477,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     } else if (warp >= 4) {  // results
         const int quad = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t box = ring + S::RING + (warp - 4) * BOX_BYTES;
         uint32_t tile = 0;
         float mul = 1.f, alpha = 1.f, inv = 1.f;
         if (MODE != LSE && j.scale) mul = j.scale[0], alpha = j.scale[1];
@@ -539,12 +538,31 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const int col = n * TN + half * HALF + c * 32;
                     if (MODE == LSE) {
                         lse_chunk(r, f, j.cols - col, col, j.at + row, j);
-                    } else if (MODE == GRAD) {
-                        grad_chunk<BF16>(r, f, j.v0 + col, (uint16_t*)j.P + row * j.ldp + col, live, j);
-                    } else if (live) {
-                        float* acc = j.acc ? j.acc + ((int64_t)(t.k0 / j.kper) * j.rows + row) * j.cols + col : nullptr;
-                        out_chunk<BF16>(f, col, row, j, acc, alpha);
+                        continue;
                     }
+                    const int row0 = t.m * TM + rank * 128 + quad * 32;
+                    if (MODE != GRAD && !j.out) {  // f32 sums: a box of 32 columns
+                        uint32_t w[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(f[i]);
+                        box_free(lane);
+                        to_box<32>(box, lane, 0, w);
+                        store_box(&map_c, box, lane, col, (t.k0 / j.kper) * j.pad_rows + row0, j.cols,
+                                  (t.k0 / j.kper) * j.pad_rows + j.rows, j.add);
+                        continue;
+                    }
+                    uint32_t w[16];
+                    if (MODE == GRAD) {
+                        grad_chunk<BF16>(r, f, j.v0 + col, w);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) w[i] = pack2<BF16>(f[2 * i] * alpha, f[2 * i + 1] * alpha);
+                    }
+                    if (c % 2 == 0) box_free(lane);  // a box of 64 columns, in two halves
+                    to_box<16>(box, lane, (c % 2) * 4, w);
+                    if (c % 2 == 0) continue;
+                    if (MODE == GRAD || j.vec) store_box(&map_c, box, lane, col - 32, row0, j.cols, j.rows, false);
+                    else copy_box(box, lane, col - 32, row0, j);
                 }
             }
             if (MODE == LSE && ok) {
@@ -553,6 +571,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         }
     }
+    if (MODE != LSE && warp >= 4 && lane == 0) tma_store_wait();
     if (!ok && lane == 0) {
         *(volatile uint32_t*)j.error = 1;
         __threadfence_system();
@@ -614,8 +633,8 @@ __global__ void __launch_bounds__(256) k_gscale(const float* g, int64_t sg, int6
 // ------------------------------------------------------------------ sums of the depth's splits
 // Four columns of a row per thread and step where rows allow 16-byte loads.
 template <bool BF16, bool VEC>
-__global__ void __launch_bounds__(256) k_split_join(const float* acc, int ks, int64_t rows, int64_t cols, uint16_t* out,
-                                                    int64_t ldo, const float* scale, Span sp_acc, Span sp_out)
+__global__ void __launch_bounds__(256) k_split_join(const float* acc, int ks, int64_t slice, int64_t lda, int64_t rows,
+                                                    int64_t cols, uint16_t* out, int64_t ldo, const float* scale, Span sp_acc, Span sp_out)
 {
     pdl_wait();
     pdl_signal();
@@ -623,12 +642,13 @@ __global__ void __launch_bounds__(256) k_split_join(const float* acc, int ks, in
     const float alpha = scale ? scale[1] : 1.f;
     const int64_t n = rows * cols / W, per_row = cols / W;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / per_row, c = (i - r * per_row) * W;
         float s[W];
 #pragma unroll
         for (int w = 0; w < W; ++w) s[w] = 0.f;
 #pragma unroll 4
         for (int k = 0; k < ks; ++k) {
-            const float* p = acc + (k * n + i) * W;
+            const float* p = acc + k * slice + r * lda + c;
             if (!TROP_IN(p, 4 * W, sp_acc)) continue;
             if (VEC) {
                 const float4 q = *reinterpret_cast<const float4*>(p);
@@ -637,8 +657,7 @@ __global__ void __launch_bounds__(256) k_split_join(const float* acc, int ks, in
                 s[0] += *p;
             }
         }
-        const int64_t r = i / per_row;
-        uint16_t* dst = out + r * ldo + (i - r * per_row) * W;
+        uint16_t* dst = out + r * ldo + c;
         if (VEC) {
             if (TROP_IN(dst, 8, sp_out))
                 *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<BF16>(s[0] * alpha, s[1] * alpha), pack2<BF16>(s[2] * alpha, s[3] * alpha));
@@ -692,16 +711,20 @@ EncodeTiledFn encode_tiled()
     return fn;
 }
 
-// a row-major 16-bit matrix, its rows 16-byte aligned, read in boxes of `box_rows` x 64
-int make_map(CUtensorMap* map, bool bf16, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows)
+// a row-major matrix of bf16, f16 or f32, its rows 16-byte aligned, in boxes of `box_rows` x 128 bytes
+int make_map(CUtensorMap* map, int type, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows)
 {
+    const bool wide = type == TROP_F32;
     const EncodeTiledFn enc = encode_tiled();
     if (!enc) return set_error(TROP_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
-    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, one[2] = {1, 1};
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * (wide ? 4 : 2)};
+    const cuuint32_t box[2] = {wide ? 32u : 64u, (cuuint32_t)box_rows}, one[2] = {1, 1};
     auto encode = [&] {
-        return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-                   const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+        return enc(map,
+                   wide                ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                   : type == TROP_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                   2, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     };
     CUresult r = encode();
@@ -764,12 +787,13 @@ int readable(const Mat16& a, int sm, Blocks& ws, Matrix16* out)
 }
 
 template <int MODE, bool BF16, typename S>
-int launch_tile(const CUtensorMap& a, const CUtensorMap& b, const Job& j, const JoinJob& join, int sm, cudaStream_t s)
+int launch_tile(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const Job& j, const JoinJob& join, int sm,
+                cudaStream_t s)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)std::min(j.units, sm / S::CG) * S::CG);
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = S::SMEM;
+    cfg.dynamicSmemBytes = smem_bytes<MODE, S>();
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -779,16 +803,16 @@ int launch_tile(const CUtensorMap& a, const CUtensorMap& b, const Job& j, const 
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = S::CG == 2 ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_tile<MODE, BF16, S>, a, b, j, join);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_tile<MODE, BF16, S>, a, b, c, j, join);
     if (e != cudaSuccess) return cuda_error(e, "k_tile launch");
     count_launches(1);
     return TROP_OK;
 }
 template <int MODE, typename S>
-int launch_tile(bool bf16, const CUtensorMap& a, const CUtensorMap& b, const Job& j, int sm, cudaStream_t s,
-                const JoinJob& join = JoinJob())
+int launch_tile(bool bf16, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const Job& j, int sm,
+                cudaStream_t s, const JoinJob& join = JoinJob())
 {
-    return bf16 ? launch_tile<MODE, true, S>(a, b, j, join, sm, s) : launch_tile<MODE, false, S>(a, b, j, join, sm, s);
+    return bf16 ? launch_tile<MODE, true, S>(a, b, c, j, join, sm, s) : launch_tile<MODE, false, S>(a, b, c, j, join, sm, s);
 }
 
 // Row tiles of a band: as many as keep their operand (a row tile's whole depth) in about 48 MB of
@@ -826,8 +850,8 @@ int launch_join(JoinJob t, float2* sums, cudaStream_t s)
 template <int MODE, typename S>
 cudaError_t allow_smem()
 {
-    const cudaError_t e = cudaFuncSetAttribute(k_tile<MODE, true, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
-    return e != cudaSuccess ? e : cudaFuncSetAttribute(k_tile<MODE, false, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    const cudaError_t e = cudaFuncSetAttribute(k_tile<MODE, true, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<MODE, S>());
+    return e != cudaSuccess ? e : cudaFuncSetAttribute(k_tile<MODE, false, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<MODE, S>());
 }
 
 }  // namespace
@@ -871,6 +895,7 @@ int launch_linear_ce(const LinearCe& q, float* loss, float* lse, float* total, f
     TROP_TRY(readable(q.x, sm, ws, &x));
     TROP_TRY(readable(q.w, sm, ws, &w));
     const bool few = x.rows <= FEW_TOKENS;
+    const int type = q.bf16 ? TROP_BF16 : TROP_F16;
     const int TM = few ? Few::TM : Pair::TM, TN = few ? Few::TN : Pair::TN, CG = few ? 1 : 2;
     Job j = {};
     TROP_TRY(device_error_word(&j.error));
@@ -901,11 +926,11 @@ int launch_linear_ce(const LinearCe& q, float* loss, float* lse, float* total, f
     const int a_rows = few ? few_rows(x.rows) : 128;
     j.a_bytes = a_rows * TK * 2;
     CUtensorMap ma, mb;
-    TROP_TRY(make_map(&ma, q.bf16, x.p, x.cols, x.rows, x.ld, a_rows));
-    TROP_TRY(make_map(&mb, q.bf16, w.p, w.cols, w.rows, w.ld, 128));
-    if (few) return launch_tile<LSE, Few>(q.bf16, ma, mb, j, sm, s, t);
-    TROP_TRY((x.cols > DEEP_LOGITS ? launch_tile<LSE, Deep>(q.bf16, ma, mb, j, sm, s)
-                                   : launch_tile<LSE, Pair>(q.bf16, ma, mb, j, sm, s)));
+    TROP_TRY(make_map(&ma, type, x.p, x.cols, x.rows, x.ld, a_rows));
+    TROP_TRY(make_map(&mb, type, w.p, w.cols, w.rows, w.ld, 128));
+    if (few) return launch_tile<LSE, Few>(q.bf16, ma, mb, ma, j, sm, s, t);
+    TROP_TRY((x.cols > DEEP_LOGITS ? launch_tile<LSE, Deep>(q.bf16, ma, mb, ma, j, sm, s)
+                                   : launch_tile<LSE, Pair>(q.bf16, ma, mb, ma, j, sm, s)));
     return launch_join(t, (float2*)((char*)p + pairs + at), s);
 }
 
@@ -916,6 +941,7 @@ int launch_linear_ce_backward(const LinearCe& q, const float* g, int64_t sg, con
     TROP_TRY(ensure_device(&dev));
     const int64_t N = q.x.rows, D = q.x.cols, V = q.w.rows;
     const bool few = N <= FEW_TOKENS;
+    const int type = q.bf16 ? TROP_BF16 : TROP_F16;
     const int TM = few ? Few1::TM : Pair::TM, TN = few ? Few1::TN : Pair::TN;  // of the logits and of dx
     const int sm = dev->sm_count, teams = few ? sm : sm / 2;
     const int a_rows = few ? few_rows(N) : 128;
@@ -938,13 +964,15 @@ int launch_linear_ce_backward(const LinearCe& q, const float* g, int64_t sg, con
         for (int c = 1; c <= std::min(dx_kt, 64); ++c) {
             const int per = cdiv(dx_kt, c);
             if (cdiv(dx_kt, per) != c) continue;
+            if (c > 1 && c * N * D * 4 > (int64_t)1 << 30) break;  // 1 GiB of partial sums
             const int64_t cost = (int64_t)cdiv((int64_t)dx_mt * dx_nt * c, teams) * (per + (c > 1 ? 8 : 0));
             if (cost < best) best = cost, ks = c;
         }
     }
     const size_t p_bytes = (size_t)N * piece * 2;
-    const bool summed = dx && (ks > 1 || pieces > 1);
-    const size_t acc_bytes = summed ? (size_t)ks * N * D * 4 : 0;
+    const bool summed = dx && (ks > 1 || pieces > 1);  // f32 sums, [ks][pad_rows][lda]
+    const int64_t lda = (D + 3) / 4 * 4, pad_rows = (N + 31) / 32 * 32;
+    const size_t acc_bytes = summed ? (size_t)ks * pad_rows * lda * 4 : 0;
     void *P, *acc = nullptr, *scale = nullptr;
     TROP_TRY(ws.get(p_bytes, &P));
     if (summed) TROP_TRY(ws.get(acc_bytes, &acc));
@@ -956,15 +984,15 @@ int launch_linear_ce_backward(const LinearCe& q, const float* g, int64_t sg, con
         if (e != cudaSuccess) return cuda_error(e, "k_gscale launch");
         count_launches(1);
     }
-    CUtensorMap x_k, w_k, x_mn, w_mn, p_k, p_mn;
-    TROP_TRY(make_map(&x_k, q.bf16, x.p, D, N, x.ld, a_rows));
-    TROP_TRY(make_map(&w_k, q.bf16, w.p, D, V, w.ld, 128));
-    TROP_TRY(make_map(&x_mn, q.bf16, x.p, D, N, x.ld, 64));
-    TROP_TRY(make_map(&w_mn, q.bf16, w.p, D, V, w.ld, 64));
+    CUtensorMap x_k, w_k, x_mn, w_mn, p_k, p_mn, c;
+    TROP_TRY(make_map(&x_k, type, x.p, D, N, x.ld, a_rows));
+    TROP_TRY(make_map(&w_k, type, w.p, D, V, w.ld, 128));
+    TROP_TRY(make_map(&x_mn, type, x.p, D, N, x.ld, 64));
+    TROP_TRY(make_map(&w_mn, type, w.p, D, V, w.ld, 64));
     for (int i = 0; i < pieces; ++i) {
         const int64_t v0 = i * piece, cols = std::min(piece, V - v0);
-        TROP_TRY(make_map(&p_k, q.bf16, P, cols, N, piece, a_rows));
-        TROP_TRY(make_map(&p_mn, q.bf16, P, cols, N, piece, 64));
+        TROP_TRY(make_map(&p_k, type, P, cols, N, piece, a_rows));
+        TROP_TRY(make_map(&p_mn, type, P, cols, N, piece, 64));
         Job j = {};
         TROP_TRY(device_error_word(&j.error));
         j.inner = 1;
@@ -983,18 +1011,16 @@ int launch_linear_ce_backward(const LinearCe& q, const float* g, int64_t sg, con
             t.b0 = (int)v0;
             t.v0 = v0;
             t.tgt = targets_of(q);
-            t.P = P;
-            t.ldp = piece;
             t.lse = lse;
             t.g = g;
             t.sg = sg;
             t.count = kept;
-            t.sp_P = span_bytes(P, p_bytes);
             t.sp_lse = span_bytes(lse, (size_t)N * 4);
             const int64_t size[1] = {N}, stride[1] = {sg};
             t.sp_g = span_of(g, 4, 1, size, stride);
-            TROP_TRY((few ? launch_tile<GRAD, Few1>(q.bf16, x_k, w_k, t, sm, s)
-                           : launch_tile<GRAD, Pair>(q.bf16, x_k, w_k, t, sm, s)));
+            TROP_TRY(make_map(&c, type, P, cols, N, piece, 32));
+            TROP_TRY((few ? launch_tile<GRAD, Few1>(q.bf16, x_k, w_k, c, t, sm, s)
+                           : launch_tile<GRAD, Pair>(q.bf16, x_k, w_k, c, t, sm, s)));
         }
         if (dw) {
             Job t = j;
@@ -1010,7 +1036,8 @@ int launch_linear_ce_backward(const LinearCe& q, const float* g, int64_t sg, con
             t.vec = ((uintptr_t)t.out & 15) == 0 && dw->sr % 8 == 0;
             const int64_t size[2] = {cols, D}, stride[2] = {dw->sr, 1};
             t.sp_out = span_of(t.out, 2, 2, size, stride);
-            TROP_TRY((launch_tile<DW, Pair>(q.bf16, p_mn, x_mn, t, sm, s)));
+            if (t.vec) TROP_TRY(make_map(&c, type, t.out, D, cols, t.ldo, 32));
+            TROP_TRY((launch_tile<DW, Pair>(q.bf16, p_mn, x_mn, t.vec ? c : p_mn, t, sm, s)));
         }
         if (dx) {
             Job t = j;
@@ -1023,28 +1050,31 @@ int launch_linear_ce_backward(const LinearCe& q, const float* g, int64_t sg, con
             t.ks = cdiv(t.kt, t.kper);
             t.units = t.mt * t.nt * t.ks;
             t.bk0 = (int)v0;
-            t.acc = (float*)acc;
-            t.add = i > 0;
-            t.sp_acc = span_bytes(acc, acc_bytes);
-            if (ks == 1 && i == pieces - 1) {
+            if (summed) {
+                t.pad_rows = (int)pad_rows;
+                t.add = i > 0;
+                TROP_TRY(make_map(&c, TROP_F32, acc, D, ks * pad_rows, lda, 32));
+            } else {
                 t.out = dx->p;
                 t.ldo = dx->sr;
                 t.vec = ((uintptr_t)t.out & 15) == 0 && dx->sr % 8 == 0;
                 const int64_t size[2] = {N, D}, stride[2] = {dx->sr, 1};
                 t.sp_out = span_of(t.out, 2, 2, size, stride);
+                if (t.vec) TROP_TRY(make_map(&c, type, t.out, D, N, t.ldo, 32));
             }
-            TROP_TRY((few ? launch_tile<DX, Few1>(q.bf16, p_k, w_mn, t, sm, s)
-                           : launch_tile<DX, Pair>(q.bf16, p_k, w_mn, t, sm, s)));
+            const CUtensorMap& to = summed || t.vec ? c : p_k;
+            TROP_TRY((few ? launch_tile<DX, Few1>(q.bf16, p_k, w_mn, to, t, sm, s)
+                           : launch_tile<DX, Pair>(q.bf16, p_k, w_mn, to, t, sm, s)));
         }
     }
-    if (dx && ks > 1) {
+    if (summed) {
         const int64_t size[2] = {N, D}, stride[2] = {dx->sr, 1};
         const Span sp_out = span_of(dx->p, 2, 2, size, stride), sp_acc = span_bytes(acc, acc_bytes);
         const bool vec = D % 4 == 0 && dx->sr % 4 == 0 && ((uintptr_t)dx->p & 7) == 0;
         const auto kernel = q.bf16 ? (vec ? k_split_join<true, true> : k_split_join<true, false>)
                                    : (vec ? k_split_join<false, true> : k_split_join<false, false>);
         const cudaError_t e = launch_pdl(kernel, dim3(grid_for(N * D / (vec ? 4 : 1), sm)), dim3(256), 0, s, (const float*)acc,
-                                         ks, N, D, (uint16_t*)dx->p, dx->sr, (const float*)scale, sp_acc, sp_out);
+                                         ks, pad_rows * lda, lda, N, D, (uint16_t*)dx->p, dx->sr, (const float*)scale, sp_acc, sp_out);
         if (e != cudaSuccess) return cuda_error(e, "k_split_join launch");
         count_launches(1);
     }
