@@ -160,6 +160,7 @@ def load(path: str | None = None):
     if _fc is not None:
         _fc.set_torch_handles(torch.float32, torch.int32, torch.int64, torch.float64, torch.bfloat16, torch.float16,
                               _raw_stream or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
+        _fc.set_torch_allocators(torch.empty, torch.empty_like, torch.float32)
     return lib
 
 

@@ -106,18 +106,20 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int left, const Span& sp
     }
 }
 
-// rint(sqrt(u) * levels) + 1.5 * 2^23, sqrt and product each rounded once, for u in [0, 1].  The
-// approximate root decides unless the product comes so near to half way between two whole numbers
-// that its error (under 2^-20 relative, 255 * 2^-20 < 2^-12) could; then the rounded root does.
-__device__ __forceinline__ float code_of(float u, float levels)
+// rint(sqrt(u) * levels) for u in [0, 1], sqrt and product each rounded once, plus 1.5 * 2^23.  The
+// approximate root (2^-23 relative) decides where the product is further from half way between two
+// whole numbers than both ways' errors together, 2.5 * 2^-23 * 255 < NEAR; `off` takes the distance to the
+// whole number, and where one of a lane's codes comes nearer to a half, code_exact forms them again.
+constexpr float NEAR = 1.220703125e-4f;  // 2^-13
+__device__ __forceinline__ float code_of(float u, float levels, float& off)
 {
     float r;
     asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(u));  // (a flushed u has code 0 either way)
-    const float t = r * levels;
-    float c = t + TO_WHOLE;
-    if (fabsf(t - (c - TO_WHOLE)) > 0.5f - 0.0009765625f) c = __fmul_rn(__fsqrt_rn(u), levels) + TO_WHOLE;
+    const float t = r * levels, c = t + TO_WHOLE;
+    off = fmaxf(off, fabsf(t - (c - TO_WHOLE)));
     return c;
 }
+__device__ __forceinline__ float code_exact(float u, float levels) { return __fmul_rn(__fsqrt_rn(u), levels) + TO_WHOLE; }
 __device__ __forceinline__ uint32_t low_bytes(const uint32_t (&w)[4])
 {
     return __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
@@ -237,87 +239,136 @@ __global__ void __launch_bounds__(256) k_adamw(const __grid_constant__ TAB tab, 
 // warp is contiguous.  The largest magnitude is taken over the values' bits, which order like the
 // magnitudes and let a NaN win: a block with a NaN or an infinity has a scale that is not finite,
 // and all of it reads back as NaN.
+template <typename TP, typename TG>
+struct Block8 {
+    Raw<TP, 4> p[2];
+    Raw<TG, 4> g[2];
+    uint32_t cm[2], cr[2];
+    float ms, rs;
+};
+template <typename T, bool FULL>
+__device__ __forceinline__ void load_raw(const T* p, int left, const Span& sp, Raw<T, 4>& q)
+{
+    float v[4];
+    if (FULL) {
+        if (TROP_IN(p, 4 * sizeof(T), sp)) q.read(p);
+        else q.zero();
+    } else {
+        load4<T, false>(p, left, sp, v);
+        q.set(v);
+    }
+}
 template <typename TP, typename TG, bool FULL>
-__device__ __forceinline__ void step8_block(const trop_adamw_tensor& t, int64_t base, int size, const AdamwScalars& k,
-                                            int copy16, unsigned* rep)
+__device__ __forceinline__ void load_block(const trop_adamw_tensor& t, int64_t base, int size, unsigned* rep, Block8<TP, TG>& x)
 {
     const int lane = threadIdx.x & 31;
-    const TP* pp = (const TP*)t.param + base;
-    const TG* pg = (const TG*)t.grad + base;
-    uint8_t* pm = (uint8_t*)t.exp_avg + base;
-    uint8_t* pr = (uint8_t*)t.exp_avg_sq + base;
-    float* ps = t.exp_avg_scale + base / BLOCK;
-    float* qs = t.exp_avg_sq_scale + base / BLOCK;
-    const Span sp_p = span_bytes_dev(t.param, t.numel * sizeof(TP), rep), sp_g = span_bytes_dev(t.grad, t.numel * sizeof(TG), rep);
-    const Span sp_m = span_bytes_dev(t.exp_avg, t.numel, rep), sp_r = span_bytes_dev(t.exp_avg_sq, t.numel, rep);
     const int64_t scales = (t.numel + BLOCK - 1) / BLOCK * 4;
-    const Span sp_ms = span_bytes_dev(t.exp_avg_scale, scales, rep), sp_rs = span_bytes_dev(t.exp_avg_sq_scale, scales, rep);
-    (void)sp_ms, (void)sp_rs;
-    float p[2][4], g[2][4], m[2][4], r[2][4];
-    uint32_t cm[2], cr[2];
-    const float ms = TROP_IN(ps, 4, sp_ms) ? *ps : 0.f, rs = TROP_IN(qs, 4, sp_rs) ? *qs : 0.f;
+    const float* ps = t.exp_avg_scale + base / BLOCK;
+    const float* qs = t.exp_avg_sq_scale + base / BLOCK;
+    x.ms = TROP_IN(ps, 4, span_bytes_dev(t.exp_avg_scale, scales, rep)) ? *ps : 0.f;
+    x.rs = TROP_IN(qs, 4, span_bytes_dev(t.exp_avg_sq_scale, scales, rep)) ? *qs : 0.f;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int i = h * 128 + lane * 4;
-        load4<TP, FULL>(pp + i, size - i, sp_p, p[h]);
-        load4<TG, FULL>(pg + i, size - i, sp_g, g[h]);
-        cm[h] = load_codes<FULL>(pm + i, size - i, sp_m);
-        cr[h] = load_codes<FULL>(pr + i, size - i, sp_r);
+        load_raw<TP, FULL>((const TP*)t.param + base + i, size - i, span_bytes_dev(t.param, t.numel * sizeof(TP), rep), x.p[h]);
+        load_raw<TG, FULL>((const TG*)t.grad + base + i, size - i, span_bytes_dev(t.grad, t.numel * sizeof(TG), rep), x.g[h]);
+        x.cm[h] = load_codes<FULL>((const uint8_t*)t.exp_avg + base + i, size - i, span_bytes_dev(t.exp_avg, t.numel, rep));
+        x.cr[h] = load_codes<FULL>((const uint8_t*)t.exp_avg_sq + base + i, size - i, span_bytes_dev(t.exp_avg_sq, t.numel, rep));
     }
+    (void)scales;
+}
+template <typename TP, typename TG, bool FULL>
+__device__ __forceinline__ void step_block(const trop_adamw_tensor& t, int64_t base, int size, const AdamwScalars& k,
+                                           int copy16, unsigned* rep, const Block8<TP, TG>& x)
+{
+    const int lane = threadIdx.x & 31;
+    float m[2][4], r[2][4];
     uint32_t mtop = 0, rtop = 0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int i = h * 128 + lane * 4;
+        float p[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const float a = byte_to_f32<true>(cm[h], q), c = byte_to_f32<false>(cr[h], q);
-            m[h][q] = __fmul_rn(__fmul_rn(a, fabsf(a)), ms);
-            const float root = __fmul_rn(__fmul_rn(c, c), rs);
+            const float a = byte_to_f32<true>(x.cm[h], q), c = byte_to_f32<false>(x.cr[h], q);
+            m[h][q] = __fmul_rn(__fmul_rn(a, fabsf(a)), x.ms);
+            const float root = __fmul_rn(__fmul_rn(c, c), x.rs);
             float v = __fmul_rn(root, root);
-            step1(p[h][q], g[h][q], m[h][q], v, r[h][q], k);
+            p[q] = x.p[h].get(q);
+            step1(p[q], x.g[h].get(q), m[h][q], v, r[h][q], k);
             if (FULL || i + q < size) {
                 mtop = max(mtop, __float_as_uint(m[h][q]) & 0x7fffffffu);
                 rtop = max(rtop, __float_as_uint(r[h][q]) & 0x7fffffffu);
             }
         }
-        store_param<TP, FULL>(t, base, i, size - i, rep, copy16, p[h]);
+        store_param<TP, FULL>(t, base, i, size - i, rep, copy16, p);
     }
     const float mt = __uint_as_float(__reduce_max_sync(0xffffffffu, mtop));
     const float rt = __uint_as_float(__reduce_max_sync(0xffffffffu, rtop));
     const float mi = mt > 0.f ? __fdiv_rn(1.f, mt) : 0.f, ri = rt > 0.f ? __fdiv_rn(1.f, rt) : 0.f;
+    float xm[2][4], xr[2][4], off = 0.f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            xm[h][q] = code_of(fminf(__fmul_rn(fabsf(m[h][q]), mi), 1.f), 127.f, off);
+            xr[h][q] = code_of(fminf(__fmul_rn(r[h][q], ri), 1.f), 255.f, off);
+        }
+    if (off > 0.5f - NEAR) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                xm[h][q] = code_exact(fminf(__fmul_rn(fabsf(m[h][q]), mi), 1.f), 127.f);
+                xr[h][q] = code_exact(fminf(__fmul_rn(r[h][q], ri), 1.f), 255.f);
+            }
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int i = h * 128 + lane * 4;
         uint32_t wm[4], wr[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const float a = m[h][q], z = r[h][q];
-            const float c = code_of(fminf(__fmul_rn(fabsf(a), mi), 1.f), 127.f) - TO_WHOLE;
-            wm[q] = __float_as_uint(copysignf(c, a) + TO_WHOLE);
-            const uint32_t w = __float_as_uint(code_of(fminf(__fmul_rn(z, ri), 1.f), 255.f));
-            wr[q] = z > 0.f ? max(w, __float_as_uint(TO_WHOLE + 1.f)) : w;
+            wm[q] = __float_as_uint(copysignf(xm[h][q] - TO_WHOLE, m[h][q]) + TO_WHOLE);
+            wr[q] = __float_as_uint(xr[h][q]);
+            if (r[h][q] > 0.f) wr[q] = max(wr[q], __float_as_uint(TO_WHOLE + 1.f));
         }
-        store_codes<FULL>(pm + i, size - i, sp_m, low_bytes(wm));
-        store_codes<FULL>(pr + i, size - i, sp_r, low_bytes(wr));
+        store_codes<FULL>((uint8_t*)t.exp_avg + base + i, size - i, span_bytes_dev(t.exp_avg, t.numel, rep), low_bytes(wm));
+        store_codes<FULL>((uint8_t*)t.exp_avg_sq + base + i, size - i, span_bytes_dev(t.exp_avg_sq, t.numel, rep), low_bytes(wr));
     }
     if (lane == 0) {
-        if (TROP_IN(ps, 4, sp_ms)) *ps = __fmul_rn(mt, 1.f / 16129.f);
-        if (TROP_IN(qs, 4, sp_rs)) *qs = __fmul_rn(rt, 1.f / 65025.f);
+        const int64_t scales = (t.numel + BLOCK - 1) / BLOCK * 4;
+        float* ps = t.exp_avg_scale + base / BLOCK;
+        float* qs = t.exp_avg_sq_scale + base / BLOCK;
+        if (TROP_IN(ps, 4, span_bytes_dev(t.exp_avg_scale, scales, rep))) *ps = __fmul_rn(mt, 1.f / 16129.f);
+        if (TROP_IN(qs, 4, span_bytes_dev(t.exp_avg_sq_scale, scales, rep))) *qs = __fmul_rn(rt, 1.f / 65025.f);
+        (void)scales;
     }
 }
 template <typename TP, typename TG, typename TAB>
-__global__ void __launch_bounds__(256, 4) k_adamw8(const __grid_constant__ TAB tab, const AdamwScalars k, int copy16)
+__global__ void __launch_bounds__(256, 4)
+    k_adamw8(const __grid_constant__ TAB tab, const AdamwScalars k, int copy16)
 {
     const Entry<trop_adamw_tensor>& x = tab.of(blockIdx.x);
+    const int64_t base = (int64_t)(blockIdx.x - x.start) * CHUNK + (threadIdx.x >> 5) * BLOCK, left = x.e.numel - base;
+    constexpr int APART = CHUNK / 2;  // a warp's two blocks, both on their way before either is worked on
     pdl_wait();  // (the table is older than the kernel before)
     pdl_signal();
-    const int64_t base = (int64_t)(blockIdx.x - x.start) * CHUNK, left = x.e.numel - base;
+    if (x.vec && left >= APART + BLOCK) {
+        Block8<TP, TG> a, b;
+        load_block<TP, TG, true>(x.e, base, BLOCK, tab.rep, a);
+        load_block<TP, TG, true>(x.e, base + APART, BLOCK, tab.rep, b);
+        step_block<TP, TG, true>(x.e, base, BLOCK, k, copy16, tab.rep, a);
+        step_block<TP, TG, true>(x.e, base + APART, BLOCK, k, copy16, tab.rep, b);
+        return;
+    }
 #pragma unroll 1
-    for (int b = threadIdx.x >> 5; b < CHUNK / BLOCK; b += 8) {
-        const int64_t size = left - b * BLOCK;
+    for (int h = 0; h < 2; ++h) {
+        const int64_t size = left - h * APART;
         if (size <= 0) break;
-        if (x.vec && size >= BLOCK) step8_block<TP, TG, true>(x.e, base + b * BLOCK, BLOCK, k, copy16, tab.rep);
-        else step8_block<TP, TG, false>(x.e, base + b * BLOCK, (int)min(size, (int64_t)BLOCK), k, copy16, tab.rep);
+        Block8<TP, TG> a;
+        load_block<TP, TG, false>(x.e, base + h * APART, (int)min(size, (int64_t)BLOCK), tab.rep, a);
+        step_block<TP, TG, false>(x.e, base + h * APART, (int)min(size, (int64_t)BLOCK), k, copy16, tab.rep, a);
     }
 }
 

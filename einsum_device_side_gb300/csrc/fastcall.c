@@ -393,6 +393,111 @@ static int32_t dtype_or(PyObject* obj, int32_t other)
     return code;
 }
 
+/* Results allocated here rather than in the Python wrapper, which saves its interpreter several us per
+ * call: torch.empty(n, dtype=, device=) and torch.empty_like(t), by the handles set_torch_allocators
+ * was given. */
+static PyObject *g_empty, *g_empty_like, *g_f32, *g_empty_kw, *s_device, *s_unbind;
+
+static PyObject* fc_set_torch_allocators(PyObject* self, PyObject* const* a, Py_ssize_t nargs)
+{
+    (void)self;
+    if (check_nargs(nargs, 3, "set_torch_allocators") < 0) return NULL;
+    if (!g_empty_kw) g_empty_kw = Py_BuildValue("(ss)", "dtype", "device");
+    if (!g_empty_kw) return NULL;
+    PyObject** to[3] = {&g_empty, &g_empty_like, &g_f32};
+    for (int i = 0; i < 3; ++i) {
+        Py_INCREF(a[i]);
+        Py_XSETREF(*to[i], a[i]);
+    }
+    Py_RETURN_NONE;
+}
+/* an uninitialised vector of n elements beside `like` */
+static PyObject* new_vector(int64_t n, PyObject* dtype, PyObject* like)
+{
+    PyObject* size = PyLong_FromLongLong((long long)n);
+    PyObject* device = size ? PyObject_GetAttr(like, s_device) : NULL;
+    PyObject* r = NULL;
+    if (device) {
+        PyObject* args[3] = {size, dtype, device};
+        r = PyObject_Vectorcall(g_empty, args, 1, g_empty_kw);
+    }
+    Py_XDECREF(size);
+    Py_XDECREF(device);
+    return r;
+}
+/* data pointer of a tensor made here */
+static int fresh_ptr(PyObject* t, void** out) { return t ? obj_ptr(t, out) : -1; }
+
+/* layer_norm(x, weight or None, bias or None, eps, stream or None) -> (y, mean, rstd) of a matrix x,
+ * or a status: PLAIN_PATH or an error code */
+static PyObject* fc_layer_norm(PyObject* self, PyObject* const* a, Py_ssize_t nargs)
+{
+    (void)self;
+    if (check_nargs(nargs, 5, "layer_norm") < 0) return NULL;
+    trop_tensor x, y;
+    void *w, *b, *mean, *rstd, *stream;
+    double eps;
+    if (obj_tensor_of(&x, a[0], N_DTYPES) < 0 || as_double(a[3], &eps) < 0 || obj_stream(a[4], a[0], &stream) < 0) return NULL;
+    if (!g_empty || x.rank != 2 || x.dtype < 0) return PyLong_FromLong(PLAIN_PATH);
+    const long device = obj_device(a[0]);
+    const int32_t wdtype = dtype_or(a[1] != Py_None ? a[1] : a[2], x.dtype);
+    if (device == -2 || wdtype == -2) return NULL;
+    if (device < 0) return PyLong_FromLong(PLAIN_PATH);
+    VECTOR(a[1], x.shape[1], wdtype, &w);
+    VECTOR(a[2], x.shape[1], wdtype, &b);
+    PyObject* oy = PyObject_CallOneArg(g_empty_like, a[0]);
+    PyObject* om = oy ? new_vector(x.shape[0], g_f32, a[0]) : NULL;
+    PyObject* orr = om ? PyObject_CallOneArg(g_empty_like, om) : NULL;
+    PyObject* out = NULL;
+    if (orr && obj_tensor_of(&y, oy, N_DTYPES) == 0 && fresh_ptr(om, &mean) == 0 && fresh_ptr(orr, &rstd) == 0) {
+        int rc;
+        Py_BEGIN_ALLOW_THREADS
+        rc = tropical_layer_norm(&x, w, b, wdtype, eps, &y, (float*)mean, (float*)rstd, stream);
+        Py_END_ALLOW_THREADS
+        out = rc == 0 ? PyTuple_Pack(3, oy, om, orr) : PyLong_FromLong(rc);
+    }
+    Py_XDECREF(oy);
+    Py_XDECREF(om);
+    Py_XDECREF(orr);
+    return out;
+}
+
+/* layer_norm_backward(dy, x, mean, rstd, weight, stream or None) -> (dx, dweight, dbias) of a matrix x, all
+ * three wanted, or a status */
+static PyObject* fc_layer_norm_backward(PyObject* self, PyObject* const* a, Py_ssize_t nargs)
+{
+    (void)self;
+    if (check_nargs(nargs, 6, "layer_norm_backward") < 0) return NULL;
+    trop_tensor dy, x, dx;
+    void *mean, *rstd, *w, *dw, *db, *stream;
+    if (obj_tensor_of(&dy, a[0], N_DTYPES) < 0 || obj_tensor_of(&x, a[1], N_DTYPES) < 0 || obj_stream(a[5], a[1], &stream) < 0)
+        return NULL;
+    const long device = obj_device(a[1]), other = obj_device(a[0]);
+    const int32_t wdtype = dtype_or(a[4], x.dtype);
+    if (device == -2 || other == -2 || wdtype == -2) return NULL;
+    if (!g_empty || a[4] == Py_None || x.rank != 2 || dy.rank != 2 || x.dtype < 0 || device < 0 || device != other ||
+        dy.shape[0] != x.shape[0] || dy.shape[1] != x.shape[1])
+        return PyLong_FromLong(PLAIN_PATH);
+    VECTOR(a[2], x.shape[0], TROP_F32, &mean);
+    VECTOR(a[3], x.shape[0], TROP_F32, &rstd);
+    VECTOR(a[4], x.shape[1], wdtype, &w);
+    PyObject* ox = PyObject_CallOneArg(g_empty_like, a[1]);
+    PyObject* ow = ox ? PyObject_CallOneArg(g_empty_like, a[4]) : NULL;
+    PyObject* ob = ow ? PyObject_CallOneArg(g_empty_like, a[4]) : NULL;
+    PyObject* out = NULL;
+    if (ob && obj_tensor_of(&dx, ox, N_DTYPES) == 0 && fresh_ptr(ow, &dw) == 0 && fresh_ptr(ob, &db) == 0) {
+        int rc;
+        Py_BEGIN_ALLOW_THREADS
+        rc = tropical_layer_norm_backward(&dy, &x, (float*)mean, (float*)rstd, w, wdtype, &dx, dw, db, stream);
+        Py_END_ALLOW_THREADS
+        out = rc == 0 ? PyTuple_Pack(3, ox, ow, ob) : PyLong_FromLong(rc);
+    }
+    Py_XDECREF(ox);
+    Py_XDECREF(ow);
+    Py_XDECREF(ob);
+    return out;
+}
+
 /* layer_norm_t(x, weight or None, bias or None, eps, y, mean, rstd, stream or None) */
 static PyObject* fc_layer_norm_t(PyObject* self, PyObject* const* a, Py_ssize_t nargs)
 {
@@ -484,6 +589,42 @@ static PyObject* fc_linear_ce_t(PyObject* self, PyObject* const* a, Py_ssize_t n
     return PyLong_FromLong(rc);
 }
 
+/* linear_ce(x, w, target, ignore_index, reduction: 0 none, 1 mean, 2 sum, stream or None) ->
+ * (loss, lse, kept), or a status */
+static PyObject* fc_linear_ce(PyObject* self, PyObject* const* a, Py_ssize_t nargs)
+{
+    (void)self;
+    if (check_nargs(nargs, 6, "linear_ce") < 0) return NULL;
+    trop_tensor x, w, t;
+    void *loss = NULL, *lse, *few, *stream;
+    int64_t ignore, reduction;
+    long device;
+    const int usual = head_operands(a, &x, &w, &t, &device);
+    if (usual < 0 || as_i64(a[3], &ignore) < 0 || as_i64(a[4], &reduction) < 0 || obj_stream(a[5], a[0], &stream) < 0) return NULL;
+    if (!g_empty || usual > 0 || device < 0) return PyLong_FromLong(PLAIN_PATH);
+    PyObject* of = new_vector(2, g_f32, a[0]);
+    PyObject* ol = of ? new_vector(x.shape[0], g_f32, a[0]) : NULL;
+    PyObject* oe = !ol ? NULL : reduction == 0 ? PyObject_CallOneArg(g_empty_like, ol) : Py_NewRef(Py_None);
+    PyObject* two = oe ? PyObject_CallMethodNoArgs(of, s_unbind) : NULL;
+    PyObject* out = NULL;
+    if (two && fresh_ptr(of, &few) == 0 && fresh_ptr(ol, &lse) == 0 && obj_ptr(oe, &loss) == 0) {
+        int rc;
+        Py_BEGIN_ALLOW_THREADS
+        rc = tropical_linear_cross_entropy(&x, &w, &t, ignore, reduction == 1, (float*)loss, (float*)lse,
+                                           reduction == 0 ? NULL : (float*)few, (float*)few + 1, stream);
+        Py_END_ALLOW_THREADS
+        if (rc) out = PyLong_FromLong(rc);
+        else if (PyTuple_Check(two) && PyTuple_GET_SIZE(two) == 2)
+            out = PyTuple_Pack(3, reduction == 0 ? oe : PyTuple_GET_ITEM(two, 0), ol, PyTuple_GET_ITEM(two, 1));
+        else PyErr_SetString(PyExc_RuntimeError, "unbind did not give two tensors");
+    }
+    Py_XDECREF(of);
+    Py_XDECREF(ol);
+    Py_XDECREF(oe);
+    Py_XDECREF(two);
+    return out;
+}
+
 /* linear_ce_backward_t(x, w, target, ignore_index, dloss, lse, kept or None, dx or None, dw or None, stream or None) */
 static PyObject* fc_linear_ce_backward_t(PyObject* self, PyObject* const* a, Py_ssize_t nargs)
 {
@@ -565,6 +706,13 @@ static PyMethodDef methods[] = {
      "tropical_permute_trace on tensor objects"},
     {"permute_pair_t", (PyCFunction)(void (*)(void))fc_permute_pair_t, METH_FASTCALL,
      "tropical_permute_pair on tensor objects"},
+    {"set_torch_allocators", (PyCFunction)(void (*)(void))fc_set_torch_allocators, METH_FASTCALL,
+     "torch.empty, torch.empty_like, torch.float32"},
+    {"layer_norm", (PyCFunction)(void (*)(void))fc_layer_norm, METH_FASTCALL, "tropical_layer_norm, its results allocated"},
+    {"layer_norm_backward", (PyCFunction)(void (*)(void))fc_layer_norm_backward, METH_FASTCALL,
+     "tropical_layer_norm_backward, its results allocated"},
+    {"linear_ce", (PyCFunction)(void (*)(void))fc_linear_ce, METH_FASTCALL,
+     "tropical_linear_cross_entropy, its results allocated"},
     {"layer_norm_t", (PyCFunction)(void (*)(void))fc_layer_norm_t, METH_FASTCALL,
      "tropical_layer_norm on tensor objects"},
     {"layer_norm_backward_t", (PyCFunction)(void (*)(void))fc_layer_norm_backward_t, METH_FASTCALL,
@@ -584,6 +732,8 @@ static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fastcall", "hot ent
 PyMODINIT_FUNC PyInit__fastcall(void)
 {
     s_data_ptr = PyUnicode_InternFromString("data_ptr");
+    s_device = PyUnicode_InternFromString("device");
+    s_unbind = PyUnicode_InternFromString("unbind");
     s_shape = PyUnicode_InternFromString("shape");
     s_stride = PyUnicode_InternFromString("stride");
     s_dtype = PyUnicode_InternFromString("dtype");

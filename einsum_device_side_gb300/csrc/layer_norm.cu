@@ -21,6 +21,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #define TROP_TU 7  // this file's id in a bounds-violation record
 #include "internal.h"
@@ -48,6 +49,75 @@ __device__ __forceinline__ void store(T* p, const float (&v)[VEC], const Span& s
     Raw<T, VEC> q;
     q.set(v);
     if (TROP_IN(p, VEC * sizeof(T), sp)) q.write(p);
+}
+
+// Elements are worked on two at a time (packed f32 operations: with 16-bit rows the instructions per
+// element, not memory, would bound these kernels); where elements come one by one, one at a time.
+template <int VEC>
+constexpr int pairs = VEC >= 2 ? VEC / 2 : 1;
+template <int VEC>
+using Pair = std::conditional_t<(VEC >= 2), float2, float>;
+__device__ __forceinline__ float2 p_add(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 p_mul(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 p_fma(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float p_sum(float2 a) { return a.x + a.y; }
+__device__ __forceinline__ float p_add(float a, float b) { return a + b; }
+__device__ __forceinline__ float p_mul(float a, float b) { return a * b; }
+__device__ __forceinline__ float p_fma(float a, float b, float c) { return __fmaf_rn(a, b, c); }
+__device__ __forceinline__ float p_sum(float a) { return a; }
+template <typename P>
+__device__ __forceinline__ P p_of(float v)
+{
+    if constexpr (sizeof(P) == 8) return make_float2(v, v);
+    else return v;
+}
+template <typename T, int VEC>
+__device__ __forceinline__ Pair<VEC> pair_of(const Raw<T, VEC>& q, int i)
+{
+    if constexpr (VEC >= 2) return make_float2(q.get(2 * i), q.get(2 * i + 1));
+    else return q.get(0);
+}
+template <int VEC>
+__device__ __forceinline__ Pair<VEC> pair_at(const float (&v)[VEC], int i)
+{
+    if constexpr (VEC >= 2) return make_float2(v[2 * i], v[2 * i + 1]);
+    else return v[0];
+}
+template <int VEC>
+__device__ __forceinline__ void apart(const Pair<VEC> (&o)[pairs<VEC>], float (&v)[VEC])
+{
+    if constexpr (VEC >= 2) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = i % 2 ? o[i / 2].y : o[i / 2].x;
+    } else {
+        v[0] = o[0];
+    }
+}
+// one row's values: (x - mean)^2 summed, and the result
+template <typename T, int VEC>
+__device__ __forceinline__ Pair<VEC> squares(const Raw<T, VEC>& q, float mean, Pair<VEC> a)
+{
+#pragma unroll
+    for (int i = 0; i < pairs<VEC>; ++i) {
+        const Pair<VEC> d = p_add(pair_of<T, VEC>(q, i), p_of<Pair<VEC>>(-mean));
+        a = p_fma(d, d, a);
+    }
+    return a;
+}
+template <typename TX, typename TY, int VEC>
+__device__ __forceinline__ void normed(const Raw<TX, VEC>& q, float mean, float rstd, bool has_w, const float (&w)[VEC], bool has_b,
+                                       const float (&b)[VEC], TY* y, const Span& sp)
+{
+    Pair<VEC> o[pairs<VEC>];
+#pragma unroll
+    for (int i = 0; i < pairs<VEC>; ++i) {
+        o[i] = p_mul(p_add(pair_of<TX, VEC>(q, i), p_of<Pair<VEC>>(-mean)), p_of<Pair<VEC>>(rstd));
+        if (has_w) o[i] = p_mul(o[i], pair_at<VEC>(w, i));
+        if (has_b) o[i] = p_add(o[i], pair_at<VEC>(b, i));
+    }
+    float v[VEC];
+    apart<VEC>(o, v);
+    store<TY, VEC>(y, v, sp);
 }
 
 // Sums of K values over the group of a row: a warp (several rows per block), or the whole block.
@@ -138,25 +208,22 @@ template <typename TX, typename TY, typename TW, int VEC, int NV>
 __device__ __forceinline__ void norm_row(const NormJob& j, int64_t row, Raw<TX, VEC> (&q)[NV], float (*sh)[32][1])
 {
     const int cols = (int)j.cols;
-    float s[1] = {0.f};
+    Pair<VEC> a = p_of<Pair<VEC>>(0.f);
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) s[0] += q[k].get(i);
+        for (int i = 0; i < pairs<VEC>; ++i) a = p_add(a, pair_of<TX, VEC>(q[k], i));
+    float s[1] = {p_sum(a)};
     group_sum_turn<1>(s, sh[0]);
     const float mean = s[0] * j.inv_cols;
-    s[0] = 0.f;
+    a = p_of<Pair<VEC>>(0.f);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int c = (k * blockDim.x + threadIdx.x) * VEC;
         q[k].again();
-        if (c < cols)
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const float d = q[k].get(i) - mean;
-                s[0] = __fmaf_rn(d, d, s[0]);
-            }
+        if (c < cols) a = squares<TX, VEC>(q[k], mean, a);
     }
+    s[0] = p_sum(a);
     group_sum_turn<1>(s, sh[1]);
     const float rstd = __fdiv_rn(1.f, __fsqrt_rn(__fmaf_rn(s[0], j.inv_cols, j.eps)));
     if (threadIdx.x == 0) {
@@ -168,17 +235,11 @@ __device__ __forceinline__ void norm_row(const NormJob& j, int64_t row, Raw<TX, 
     for (int k = 0; k < NV; ++k) {
         const int c = (k * blockDim.x + threadIdx.x) * VEC;
         if (c < cols) {
-            float w[VEC], b[VEC], o[VEC];
+            float w[VEC], b[VEC];
             q[k].again();
             if (j.w) load<TW, VEC>((const TW*)j.w + c, w, j.sp_w);
             if (j.b) load<TW, VEC>((const TW*)j.b + c, b, j.sp_b);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                o[i] = (q[k].get(i) - mean) * rstd;
-                if (j.w) o[i] *= w[i];
-                if (j.b) o[i] += b[i];
-            }
-            store<TY, VEC>(y + c, o, j.sp_y);
+            normed<TX, TY, VEC>(q[k], mean, rstd, j.w, w, j.b, b, y + c, j.sp_y);
         }
     }
 }
@@ -221,6 +282,76 @@ __global__ void __launch_bounds__((most_threads<TX, VEC, NV>()),
     }
 }
 
+// Short rows, a warp per row and U of its rows at a time: U rows' loads are on their way together, and
+// their sums' shuffles run side by side.
+template <typename TX, typename TY, typename TW, int VEC, int NV, int U>
+__global__ void __launch_bounds__(256, 4) k_norm_short(const NormJob j)
+{
+    pdl_wait();
+    pdl_signal();
+    const int cols = (int)j.cols;
+    const int64_t step = (int64_t)gridDim.x * blockDim.y;
+    for (int64_t row0 = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; row0 < j.rows; row0 += step * U) {
+        Raw<TX, VEC> q[U][NV];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = row0 + u * step;
+            const TX* x = (const TX*)j.x + row * j.sx;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int c = (k * 32 + threadIdx.x) * VEC;
+                if (row < j.rows && c < cols && TROP_IN(x + c, VEC * sizeof(TX), j.sp_x)) q[u][k].read(x + c);
+                else q[u][k].zero();
+            }
+        }
+        float mean[U], rstd[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            Pair<VEC> a = p_of<Pair<VEC>>(0.f);
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int i = 0; i < pairs<VEC>; ++i) a = p_add(a, pair_of<TX, VEC>(q[u][k], i));
+            mean[u] = p_sum(a);
+        }
+        warp_sum<U>(mean);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            mean[u] *= j.inv_cols;
+            Pair<VEC> a = p_of<Pair<VEC>>(0.f);
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+                if ((k * 32 + (int)threadIdx.x) * VEC < cols) a = squares<TX, VEC>(q[u][k], mean[u], a);
+            rstd[u] = p_sum(a);
+        }
+        warp_sum<U>(rstd);
+#pragma unroll
+        for (int u = 0; u < U; ++u) rstd[u] = __fdiv_rn(1.f, __fsqrt_rn(__fmaf_rn(rstd[u], j.inv_cols, j.eps)));
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = (k * 32 + threadIdx.x) * VEC;
+            if (c >= cols) continue;
+            float w[VEC], b[VEC];
+            if (j.w) load<TW, VEC>((const TW*)j.w + c, w, j.sp_w);
+            if (j.b) load<TW, VEC>((const TW*)j.b + c, b, j.sp_b);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t row = row0 + u * step;
+                if (row >= j.rows) break;
+                normed<TX, TY, VEC>(q[u][k], mean[u], rstd[u], j.w, w, j.b, b, (TY*)j.y + row * j.sy + c, j.sp_y);
+            }
+        }
+        if (threadIdx.x == 0)
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t row = row0 + u * step;
+                if (row >= j.rows) break;
+                if (j.mean && TROP_IN(j.mean + row, 4, j.sp_mean)) j.mean[row] = mean[u];
+                if (j.rstd && TROP_IN(j.rstd + row, 4, j.sp_rstd)) j.rstd[row] = rstd[u];
+            }
+    }
+}
+
 // Rows longer than a block's registers: one block per row, three walks over it.
 template <typename TX, typename TY, typename TW>
 __global__ void __launch_bounds__(1024) k_norm_long(const NormJob j)
@@ -260,47 +391,142 @@ __global__ void __launch_bounds__(1024) k_norm_long(const NormJob j)
     }
 }
 
-// One row of the backward pass in a group's registers: h and u in place of x and dy, the weight's
-// and bias's sums, and the row's two sums.
+// One row of the backward pass in a group's registers: h and dy, then u in its place, the weight's and
+// bias's sums, and the row's two sums.
 template <int VEC, int NV>
-__device__ __forceinline__ void back_sums(float (&h)[NV][VEC], float (&d)[NV][VEC], const float (&w)[NV][VEC],
-                                          float (&aw)[NV][VEC], float (&ab)[NV][VEC], float mean, float rstd, float (&s)[2])
+using Pairs = Pair<VEC>[NV][pairs<VEC>];
+template <typename TX, typename TY, int VEC, int NV>
+__device__ __forceinline__ void back_row(const Raw<TX, VEC> (&qx)[NV], const Raw<TY, VEC> (&qd)[NV], float mean, float rstd,
+                                         Pairs<VEC, NV>& h, Pairs<VEC, NV>& d)
 {
-    s[0] = s[1] = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            h[k][i] = (h[k][i] - mean) * rstd;
-            aw[k][i] = __fmaf_rn(d[k][i], h[k][i], aw[k][i]);
-            ab[k][i] += d[k][i];
-            d[k][i] *= w[k][i];
-            s[0] += d[k][i];
-            s[1] = __fmaf_rn(d[k][i], h[k][i], s[1]);
+        for (int i = 0; i < pairs<VEC>; ++i) {
+            h[k][i] = p_mul(p_add(pair_of<TX, VEC>(qx[k], i), p_of<Pair<VEC>>(-mean)), p_of<Pair<VEC>>(rstd));
+            d[k][i] = pair_of<TY, VEC>(qd[k], i);
         }
 }
-template <typename TX, int VEC, int NV>
-__device__ __forceinline__ void back_store(const NormJob& j, int64_t row, const float (&h)[NV][VEC],
-                                           const float (&d)[NV][VEC], float rstd, const float (&s)[2])
+// A thread's column sums, in registers, or where 1024 threads leave too few of those, in its own words
+// of shared memory (16 bytes a pair; no other thread touches them).
+template <int VEC, int NV, bool SHARED>
+struct Sums {
+    Pairs<VEC, NV> w, b;
+    __device__ __forceinline__ void init(void*)
+    {
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int i = 0; i < pairs<VEC>; ++i) w[k][i] = b[k][i] = p_of<Pair<VEC>>(0.f);
+    }
+    __device__ __forceinline__ void add(int k, int i, Pair<VEC> d, Pair<VEC> h)
+    {
+        w[k][i] = p_fma(d, h, w[k][i]);
+        b[k][i] = p_add(b[k][i], d);
+    }
+    __device__ __forceinline__ Pair<VEC> get(int k, int i, int which) const { return which ? b[k][i] : w[k][i]; }
+};
+template <int VEC, int NV>
+struct Sums<VEC, NV, true> {
+    Pair<VEC>* at;
+    __device__ __forceinline__ Pair<VEC>& word(int k, int i, int which) const
+    {
+        return at[((k * pairs<VEC> + i) * 2 + which) * blockDim.x + threadIdx.x];
+    }
+    __device__ __forceinline__ void init(void* shared)
+    {
+        at = reinterpret_cast<Pair<VEC>*>(shared);
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int i = 0; i < pairs<VEC>; ++i) word(k, i, 0) = word(k, i, 1) = p_of<Pair<VEC>>(0.f);
+    }
+    __device__ __forceinline__ void add(int k, int i, Pair<VEC> d, Pair<VEC> h)
+    {
+        word(k, i, 0) = p_fma(d, h, word(k, i, 0));
+        word(k, i, 1) = p_add(word(k, i, 1), d);
+    }
+    __device__ __forceinline__ Pair<VEC> get(int k, int i, int which) const { return word(k, i, which); }
+};
+// The weight's values: kept in registers, or read again for every row.
+template <typename TW, int VEC, int NV, bool KEPT>
+struct Weights {
+    Pairs<VEC, NV> w;
+    __device__ __forceinline__ void init(const NormJob& j)
+    {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = (k * blockDim.x + threadIdx.x) * VEC;
+            float v[VEC];
+            const bool has = j.w && c < (int)j.cols;
+            if (has) load<TW, VEC>((const TW*)j.w + c, v, j.sp_w);
+#pragma unroll
+            for (int i = 0; i < pairs<VEC>; ++i) w[k][i] = has ? pair_at<VEC>(v, i) : p_of<Pair<VEC>>(1.f);
+        }
+    }
+    // d times the weight
+    __device__ __forceinline__ void times(const NormJob&, int k, Pair<VEC> (&d)[pairs<VEC>]) const
+    {
+#pragma unroll
+        for (int i = 0; i < pairs<VEC>; ++i) d[i] = p_mul(d[i], w[k][i]);
+    }
+};
+template <typename TW, int VEC, int NV>
+struct Weights<TW, VEC, NV, false> {
+    __device__ __forceinline__ void init(const NormJob&) {}
+    __device__ __forceinline__ void times(const NormJob& j, int k, Pair<VEC> (&d)[pairs<VEC>]) const
+    {
+        const int c = (k * blockDim.x + threadIdx.x) * VEC;
+        if (!j.w || c >= (int)j.cols) return;
+        float v[VEC];
+        load<TW, VEC>((const TW*)j.w + c, v, j.sp_w);
+#pragma unroll
+        for (int i = 0; i < pairs<VEC>; ++i) d[i] = p_mul(d[i], pair_at<VEC>(v, i));
+    }
+};
+template <int VEC, int NV, typename W, typename S>
+__device__ __forceinline__ void back_sums(const NormJob& j, const Pairs<VEC, NV>& h, Pairs<VEC, NV>& d, const W& w, S& acc,
+                                          float (&s)[2])
 {
-    const float flat = s[0] * j.inv_cols, along = s[1] * j.inv_cols;
+    Pair<VEC> flat = p_of<Pair<VEC>>(0.f), along = flat;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+#pragma unroll
+        for (int i = 0; i < pairs<VEC>; ++i) acc.add(k, i, d[k][i], h[k][i]);
+        w.times(j, k, d[k]);
+#pragma unroll
+        for (int i = 0; i < pairs<VEC>; ++i) {
+            flat = p_add(flat, d[k][i]);
+            along = p_fma(d[k][i], h[k][i], along);
+        }
+    }
+    s[0] = p_sum(flat);
+    s[1] = p_sum(along);
+}
+template <typename TX, int VEC, int NV>
+__device__ __forceinline__ void back_store(const NormJob& j, int64_t row, const Pairs<VEC, NV>& h, const Pairs<VEC, NV>& d,
+                                           float rstd, const float (&s)[2])
+{
+    const Pair<VEC> flat = p_of<Pair<VEC>>(-s[0] * j.inv_cols), along = p_of<Pair<VEC>>(-s[1] * j.inv_cols);
     TX* dx = (TX*)j.dx + row * j.sdx;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int c = (k * blockDim.x + threadIdx.x) * VEC;
         if (c < (int)j.cols) {
-            float o[VEC];
+            Pair<VEC> o[pairs<VEC>];
+            float v[VEC];
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) o[i] = rstd * (d[k][i] - flat - h[k][i] * along);
-            store<TX, VEC>(dx + c, o, j.sp_dx);
+            for (int i = 0; i < pairs<VEC>; ++i)
+                o[i] = p_mul(p_fma(h[k][i], along, p_add(d[k][i], flat)), p_of<Pair<VEC>>(rstd));
+            apart<VEC>(o, v);
+            store<TX, VEC>(dx + c, v, j.sp_dx);
         }
     }
 }
 // The block's column sums into its row of the partial sums.  Blocks of several warps that each took
 // rows of their own (blockDim.y > 1) add theirs in warp order, through `across` [warps][cols].
-template <int VEC, int NV>
-__device__ __forceinline__ void back_partials(const NormJob& j, const float (&aw)[NV][VEC], const float (&ab)[NV][VEC],
-                                              float* across)
+template <int VEC, int NV, typename S>
+__device__ __forceinline__ void back_partials(const NormJob& j, const S& acc, float* across)
 {
     const int cols = (int)j.cols;
     for (int which = 0; which < 2; ++which) {
@@ -314,22 +540,16 @@ __device__ __forceinline__ void back_partials(const NormJob& j, const float (&aw
         for (int k = 0; k < NV; ++k) {
             const int c = (k * blockDim.x + threadIdx.x) * VEC;
             if (c >= cols) continue;
+            Pair<VEC> o[pairs<VEC>];
+            float v[VEC];
+#pragma unroll
+            for (int i = 0; i < pairs<VEC>; ++i) o[i] = acc.get(k, i, which);
+            apart<VEC>(o, v);
             if (blockDim.y > 1) {
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) across[threadIdx.y * cols + c + i] = which ? ab[k][i] : aw[k][i];
-            } else if (VEC % 4 == 0) {
-#pragma unroll
-                for (int i = 0; i < VEC; i += 4) {
-                    const float4 v = which ? make_float4(ab[k][i], ab[k][i + 1 < VEC ? i + 1 : 0], ab[k][i + 2 < VEC ? i + 2 : 0],
-                                                         ab[k][i + 3 < VEC ? i + 3 : 0])
-                                           : make_float4(aw[k][i], aw[k][i + 1 < VEC ? i + 1 : 0], aw[k][i + 2 < VEC ? i + 2 : 0],
-                                                         aw[k][i + 3 < VEC ? i + 3 : 0]);
-                    if (TROP_IN(part + c + i, 16, sp)) *reinterpret_cast<float4*>(part + c + i) = v;
-                }
+                for (int i = 0; i < VEC; ++i) across[threadIdx.y * cols + c + i] = v[i];
             } else {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i)
-                    if (TROP_IN(part + c + i, 4, sp)) part[c + i] = which ? ab[k][i] : aw[k][i];
+                store<float, VEC>(part + c, v, sp);
             }
         }
         if (blockDim.y > 1) {
@@ -342,17 +562,6 @@ __device__ __forceinline__ void back_partials(const NormJob& j, const float (&aw
         }
     }
 }
-template <typename TW, int VEC, int NV>
-__device__ __forceinline__ void back_init(const NormJob& j, float (&w)[NV][VEC], float (&aw)[NV][VEC], float (&ab)[NV][VEC])
-{
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int c = (k * blockDim.x + threadIdx.x) * VEC;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) aw[k][i] = ab[k][i] = 0.f, w[k][i] = 1.f;
-        if (j.w && c < (int)j.cols) load<TW, VEC>((const TW*)j.w + c, w[k], j.sp_w);
-    }
-}
 
 // Rows from global memory, U of a group's rows on their way at a time.  TX: x and dx; TY: dy.
 template <typename TX, typename TY, typename TW, int VEC, int NV, int U, int MAXT>
@@ -361,9 +570,12 @@ __global__ void __launch_bounds__(MAXT) k_norm_back(const NormJob j)
     pdl_wait();
     pdl_signal();
     extern __shared__ __align__(16) uint8_t dyn[];
-    __shared__ float sh[2][32][2];
-    float aw[NV][VEC], ab[NV][VEC], w[NV][VEC];
-    back_init<TW, VEC, NV>(j, w, aw, ab);
+    __shared__ float sh[2][32][2 * U];
+    constexpr bool WIDE = MAXT > 512;  // sums in shared memory, weights read again
+    Sums<VEC, NV, WIDE> acc;
+    Weights<TW, VEC, NV, !WIDE> w;
+    acc.init(dyn);
+    w.init(j);
     const int64_t step = (int64_t)gridDim.x * blockDim.y;
     const int cols = (int)j.cols;
     int turn = 0;
@@ -391,23 +603,34 @@ __global__ void __launch_bounds__(MAXT) k_norm_back(const NormJob j)
                 }
             }
         }
+        // the U rows' sums, joined at once; h and u are formed again for the result
+        float sums[2 * U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            Pairs<VEC, NV> h, d;
+            float s[2];
+            back_row<TX, TY, VEC, NV>(qx[u], qd[u], mean[u], rstd[u], h, d);
+            back_sums<VEC, NV>(j, h, d, w, acc, s);
+            sums[2 * u] = s[0], sums[2 * u + 1] = s[1];
+        }
+        if (!j.dx) continue;
+        group_sum_turn<2 * U>(sums, sh[turn]);
+        turn ^= 1;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t row = row0 + u * step;
             if (row >= j.rows) break;
-            float h[NV][VEC], d[NV][VEC], s[2];
+            Pairs<VEC, NV> h, d;
 #pragma unroll
-            for (int k = 0; k < NV; ++k)
+            for (int k = 0; k < NV; ++k) qx[u][k].again(), qd[u][k].again();
+            back_row<TX, TY, VEC, NV>(qx[u], qd[u], mean[u], rstd[u], h, d);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) h[k][i] = qx[u][k].get(i), d[k][i] = qd[u][k].get(i);
-            back_sums<VEC, NV>(h, d, w, aw, ab, mean[u], rstd[u], s);
-            if (!j.dx) continue;
-            group_sum_turn<2>(s, sh[turn]);
-            turn ^= 1;
+            for (int k = 0; k < NV; ++k) w.times(j, k, d[k]);
+            const float s[2] = {sums[2 * u], sums[2 * u + 1]};
             back_store<TX, VEC, NV>(j, row, h, d, rstd[u], s);
         }
     }
-    if (j.part_w || j.part_b) back_partials<VEC, NV>(j, aw, ab, reinterpret_cast<float*>(dyn));
+    if (j.part_w || j.part_b) back_partials<VEC, NV>(j, acc, reinterpret_cast<float*>(dyn));
 }
 
 // Rows through shared memory: a ring of `stages` rows of x and dy, each brought by two bulk copies, so
@@ -443,8 +666,10 @@ __global__ void __launch_bounds__(MAXT) k_norm_back_ring(const NormJob j, int st
     int64_t ahead = first;  // the next row to fetch (thread 0)
     if (threadIdx.x == 0)
         for (int s = 0; s < stages && ahead < j.rows; ++s, ahead += step) fetch(s, ahead);
-    float aw[NV][VEC], ab[NV][VEC], w[NV][VEC];
-    back_init<TW, VEC, NV>(j, w, aw, ab);
+    Sums<VEC, NV, false> acc;
+    Weights<TW, VEC, NV, true> w;
+    acc.init(nullptr);
+    w.init(j);
     int s = 0, turn = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -457,22 +682,22 @@ __global__ void __launch_bounds__(MAXT) k_norm_back_ring(const NormJob j, int st
             mean2 = j.mean[row + step], rstd2 = j.rstd[row + step];
         ok = mbar_wait(&full[s], phase);
         const uint8_t* at = dyn + (size_t)s * (xb + db);
-        float h[NV][VEC], d[NV][VEC], sum[2];
+        Raw<TX, VEC> qx[NV];
+        Raw<TY, VEC> qd[NV];
+        Pairs<VEC, NV> h, d;
+        float sum[2];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int c = (k * blockDim.x + threadIdx.x) * VEC;
-            Raw<TX, VEC> qx;
-            Raw<TY, VEC> qd;
-            qx.zero();  // past the row dy = 0: nothing in any sum
-            qd.zero();
+            qx[k].zero();  // past the row dy = 0: nothing in any sum
+            qd[k].zero();
             if (c < cols) {
-                qx.read(reinterpret_cast<const TX*>(at) + c);
-                qd.read(reinterpret_cast<const TY*>(at + xb) + c);
+                qx[k].read(reinterpret_cast<const TX*>(at) + c);
+                qd[k].read(reinterpret_cast<const TY*>(at + xb) + c);
             }
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) h[k][i] = qx.get(i), d[k][i] = qd.get(i);
         }
-        back_sums<VEC, NV>(h, d, w, aw, ab, mean, rstd, sum);
+        back_row<TX, TY, VEC, NV>(qx, qd, mean, rstd, h, d);
+        back_sums<VEC, NV>(j, h, d, w, acc, sum);
         warp_sum<2>(sum);
         if ((threadIdx.x & 31) == 0) sh[turn][threadIdx.x >> 5][0] = sum[0], sh[turn][threadIdx.x >> 5][1] = sum[1];
         ok = __syncthreads_and(ok);
@@ -491,7 +716,7 @@ __global__ void __launch_bounds__(MAXT) k_norm_back_ring(const NormJob j, int st
         ring_failed(full, stages, s, phase, error);
         return;
     }
-    if (j.part_w || j.part_b) back_partials<VEC, NV>(j, aw, ab, nullptr);
+    if (j.part_w || j.part_b) back_partials<VEC, NV>(j, acc, nullptr);
 }
 
 template <typename TX, typename TY, typename TW>
@@ -653,9 +878,20 @@ int norm_forward(const NormJob& j, int sm, cudaStream_t s)
     const bool vec = j.cols % V == 0 && aligned(j.x, j.sx, sizeof(TX), V, j.rows) &&
                      aligned(j.y, j.sy, sizeof(TY), V, j.rows) && aligned(j.w, 0, sizeof(TW), V, 1) &&
                      aligned(j.b, 0, sizeof(TW), V, 1);
+    const int64_t units = j.cols / V;
+    if (vec && units <= 128 && j.rows >= (int64_t)sm * 16) {
+        const int nv = units <= 32 ? 1 : units <= 64 ? 2 : 4;
+        const dim3 block(32, 8);
+        const int64_t blocks = std::min<int64_t>((j.rows * nv + 31) / 32, (int64_t)sm * 4);
+        const auto kernel = nv == 1   ? k_norm_short<TX, TY, TW, V, 1, 4>
+                            : nv == 2 ? k_norm_short<TX, TY, TW, V, 2, 2>
+                                      : k_norm_short<TX, TY, TW, V, 4, 1>;
+        TROP_LAUNCH(kernel, dim3((unsigned)blocks), block, 0, j);
+        return TROP_OK;
+    }
     int nv = 0;
     dim3 block;
-    const bool fits = vec ? forward_shape<TX, V>(j.cols / V, j.rows, sm, &nv, &block)
+    const bool fits = vec ? forward_shape<TX, V>(units, j.rows, sm, &nv, &block)
                           : forward_shape<TX, 1>(j.cols, j.rows, sm, &nv, &block);
     if (!fits) {
         TROP_LAUNCH((k_norm_long<TX, TY, TW>), dim3((unsigned)j.rows), dim3(1024), 0, j);
@@ -694,11 +930,12 @@ int norm_backward(NormJob j, const NormVec& dw, const NormVec& db, int sm, cudaS
     const bool fits = backward_shape(vec ? j.cols / V : j.cols, vec ? MOST : 16, &nv, &block);
     const bool sums = dw.p || db.p;
     // rows of x and dy that bulk copies can bring, enough of them to fill a ring
-    const size_t row_bytes = j.cols * (sizeof(TX) + sizeof(TY));
-    const bool ring = fits && vec && block.y == 1 && block.x >= 64 && block.x <= 512 && j.cols * sizeof(TY) % 16 == 0 &&
-                      aligned(j.dy, j.sdy, 1, 16, 1) && (j.sdy * sizeof(TY)) % 16 == 0 && j.sx % V == 0 && j.rows >= 4 * sm;
+    const size_t pair = j.cols * (sizeof(TX) + sizeof(TY));
     const int per_sm = block.x > 256 ? 1 : std::max<int>(2, 512 / (int)block.x);  // blocks that share an SM
-    const int stages = (int)std::min<size_t>(RING_STAGES, RING_BYTES / per_sm / row_bytes);
+    const int stages = (int)std::min<size_t>(RING_STAGES, RING_BYTES / per_sm / pair);
+    // rows of x and dy that bulk copies can bring (16-byte granules), and enough of them to fill a ring
+    const bool ring = fits && vec && block.y == 1 && block.x >= 64 && block.x <= 512 && j.cols * sizeof(TY) % 16 == 0 &&
+                      aligned(j.dy, j.sdy * sizeof(TY), 1, 16, j.rows) && j.rows >= 4 * sm && stages >= 2;
     int blocks = 0;
     if (ring) blocks = (int)std::min<int64_t>(j.rows, (int64_t)sm * per_sm);
     else if (fits) blocks = (int)std::min<int64_t>((j.rows + block.y - 1) / block.y, (int64_t)sm * std::max<int>(1, 512 / (int)(block.x * block.y)));
@@ -725,11 +962,11 @@ int norm_backward(NormJob j, const NormVec& dw, const NormVec& db, int sm, cudaS
         if (j.dx) TROP_LAUNCH((k_norm_back_long<TX, TY, TW>), dim3((unsigned)j.rows), dim3(1024), 0, j);
         if (sums)
             TROP_LAUNCH((k_norm_columns<TX, TY>), dim3((unsigned)((j.cols + 255) / 256), (unsigned)blocks), dim3(256), 0, j);
-    } else if (ring && stages >= 2) {
+    } else if (ring) {
         uint32_t* error;
         TROP_TRY(device_error_word(&error));
         const dim3 grid((unsigned)blocks);
-        const size_t smem = stages * row_bytes;
+        const size_t smem = stages * pair;
         const auto kernel = nv == 1   ? k_norm_back_ring<TX, TY, TW, V, 1, 512>
                             : nv == 2 ? k_norm_back_ring<TX, TY, TW, V, 2, 512>
                                       : k_norm_back_ring<TX, TY, TW, V, MOST, 512>;
@@ -738,23 +975,23 @@ int norm_backward(NormJob j, const NormVec& dw, const NormVec& db, int sm, cudaS
         TROP_LAUNCH(kernel, grid, block, smem, j, stages, error);
     } else {
         const dim3 grid((unsigned)blocks);
-        const size_t smem = block.y > 1 ? block.y * (size_t)j.cols * 4 : 0;
         const bool wide = block.x > 512;
-        if (vec) {
-            if (nv == 1) TROP_LAUNCH((k_norm_back<TX, TY, TW, V, 1, 4, 512>), grid, block, smem, j);
-            else if (nv == 2 && !wide) TROP_LAUNCH((k_norm_back<TX, TY, TW, V, 2, 1, 512>), grid, block, smem, j);
-            else if (nv == 2) TROP_LAUNCH((k_norm_back<TX, TY, TW, V, 2, 1, 1024>), grid, block, smem, j);
-            else if (!wide) TROP_LAUNCH((k_norm_back<TX, TY, TW, V, MOST, 1, 512>), grid, block, smem, j);
-            else TROP_LAUNCH((k_norm_back<TX, TY, TW, V, MOST, 1, 1024>), grid, block, smem, j);
-        } else if (nv <= 2) {
-            TROP_LAUNCH((k_norm_back<TX, TY, TW, 1, 2, 4, 512>), grid, block, smem, j);
-        } else if (nv == 4) {
-            TROP_LAUNCH((k_norm_back<TX, TY, TW, 1, 4, 4, 512>), grid, block, smem, j);
-        } else if (!wide) {
-            TROP_LAUNCH((k_norm_back<TX, TY, TW, 1, 16, 1, 512>), grid, block, smem, j);
-        } else {
-            TROP_LAUNCH((k_norm_back<TX, TY, TW, 1, 16, 1, 1024>), grid, block, smem, j);
+        const auto kernel = !vec ? (nv <= 2  ? k_norm_back<TX, TY, TW, 1, 2, 4, 512>
+                                    : nv == 4 ? k_norm_back<TX, TY, TW, 1, 4, 4, 512>
+                                    : wide    ? k_norm_back<TX, TY, TW, 1, 16, 1, 1024>
+                                              : k_norm_back<TX, TY, TW, 1, 16, 1, 512>)
+                            : nv == 1         ? k_norm_back<TX, TY, TW, V, 1, 4, 512>
+                            : nv == 2 && wide ? k_norm_back<TX, TY, TW, V, 2, 1, 1024>
+                            : nv == 2         ? k_norm_back<TX, TY, TW, V, 2, 1, 512>
+                            : wide            ? k_norm_back<TX, TY, TW, V, MOST, 1, 1024>
+                                              : k_norm_back<TX, TY, TW, V, MOST, 1, 512>;
+        // warps' sums to add up, or all sums of a wide block: 16 elements a thread, two floats each
+        const size_t smem = wide ? (size_t)block.x * 16 * 8 : block.y > 1 ? block.y * (size_t)j.cols * 4 : 0;
+        if (smem > 49152) {
+            const cudaError_t a = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (a != cudaSuccess) return cuda_error(a, "cudaFuncSetAttribute(k_norm_back)");
         }
+        TROP_LAUNCH(kernel, grid, block, smem, j);
     }
     if (sums) {
         const dim3 grid((unsigned)((j.cols + 31) / 32), dw.p && db.p ? 2 : 1);

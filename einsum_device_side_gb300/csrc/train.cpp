@@ -15,31 +15,39 @@ namespace {
 
 constexpr int64_t MOST = INT32_MAX - 1024;  // rows and columns the kernels index in 32 bits
 
-// Device-pointer checks of many tensors: a pointer inside an allocation already checked in this
-// call is not asked about again (torch's allocator hands out pieces of a few large allocations).
+// Device-pointer checks of a call's tensors: one driver query each (a third of the runtime's), and none for
+// a pointer inside an allocation already checked in this call (torch's allocator hands out pieces of a
+// few large ones).  Whatever is not plain memory of the current device goes the long way.
 struct PointerCheck {
     uintptr_t lo[16], hi[16];
-    int n = 0, at = 0;
+    int n = 0, at = 0, device = -1;
+    PointerCheck() { cudaGetDevice(&device); }
     int operator()(const void* p, const char* name)
     {
         const uintptr_t a = (uintptr_t)p;
         for (int i = 0; i < n; ++i)
             if (a >= lo[i] && a < hi[i]) return TROP_OK;
-        TROP_TRY(check_device_pointer(p, name));
-        using Fn = CUresult (*)(CUdeviceptr*, size_t*, CUdeviceptr);
-        static const Fn range = [] {
+        using Fn = CUresult (*)(unsigned int, CUpointer_attribute*, void**, CUdeviceptr);
+        static const Fn query = [] {
             void* f = nullptr;
             cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-            if (cudaGetDriverEntryPointByVersion("cuMemGetAddressRange", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            if (cudaGetDriverEntryPointByVersion("cuPointerGetAttributes", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
                 q != cudaDriverEntryPointSuccess) {
                 cudaGetLastError();
                 f = nullptr;
             }
             return (Fn)f;
         }();
+        unsigned int type = 0;
+        int ordinal = -1;
         CUdeviceptr base = 0;
         size_t size = 0;
-        if (range && range(&base, &size, (CUdeviceptr)a) == CUDA_SUCCESS && size) {
+        CUpointer_attribute what[4] = {CU_POINTER_ATTRIBUTE_MEMORY_TYPE, CU_POINTER_ATTRIBUTE_DEVICE_ORDINAL,
+                                       CU_POINTER_ATTRIBUTE_RANGE_START_ADDR, CU_POINTER_ATTRIBUTE_RANGE_SIZE};
+        void* to[4] = {&type, &ordinal, &base, &size};
+        if (!p || !query || query(4, what, to, (CUdeviceptr)a) != CUDA_SUCCESS || type != CU_MEMORYTYPE_DEVICE || ordinal != device)
+            return check_device_pointer(p, name);
+        if (size) {
             lo[at] = base;
             hi[at] = base + size;
             at = (at + 1) % 16;

@@ -87,6 +87,12 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.
     bfloat16 or float16.  Returns ``(y, mean, rstd)``, the float32 statistics with x's leading shape:
     what ``layer_norm_backward`` reads."""
     fc = _fast()
+    if out is None and out_dtype is None and fc is not None:  # the usual call
+        r = fc.layer_norm(x, weight, bias, eps, stream)
+        if r.__class__ is tuple:
+            return r
+        if r < 0:
+            _pkg._check(r)
     if out is None:
         out = _empty_like(x) if out_dtype is None else _empty_like(x, dtype=out_dtype)
     elif out.shape != x.shape or (out_dtype is not None and out.dtype != out_dtype):
@@ -116,6 +122,12 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
     """Gradient of ``layer_norm``: ``(dx, dweight, dbias)``, an unwanted one None.  ``dy`` has the forward's result type;
     the weight's and bias's gradients have ``weight``'s type (``weight_dtype`` without one, by default x's)."""
     fc = _fast()
+    if want_x and want_weight and want_bias and fc is not None and weight is not None:  # the usual call
+        r = fc.layer_norm_backward(dy, x, mean, rstd, weight, stream)
+        if r.__class__ is tuple:
+            return r
+        if r < 0:
+            _pkg._check(r)
     if dy.shape != x.shape:
         _fail(-5, f"dy has shape {tuple(dy.shape)}, x {tuple(x.shape)}")
     wdtype = weight.dtype if weight is not None else weight_dtype or x.dtype
@@ -163,7 +175,7 @@ class LayerNorm(torch.autograd.Function):
         return dx, dw, db, None, None
 
 
-_REDUCTIONS = ("none", "mean", "sum")
+_REDUCTIONS = {"none": 0, "mean": 1, "sum": 2}
 
 
 def _check_head(x, w, target):
@@ -180,8 +192,15 @@ def linear_cross_entropy(x: torch.Tensor, w: torch.Tensor, target: torch.Tensor,
     ``ignore_index`` have none), the log-sum-exp of each token's logits, and the number of tokens kept, all float32.
     A target outside the vocabulary gives NaN."""
     fc = _fast()
-    if reduction not in _REDUCTIONS:
-        _fail(-1, f"reduction must be one of {_REDUCTIONS}, got {reduction!r}")
+    code = _REDUCTIONS.get(reduction)
+    if code is None:
+        _fail(-1, f"reduction must be one of {tuple(_REDUCTIONS)}, got {reduction!r}")
+    if fc is not None:  # the usual call
+        r = fc.linear_ce(x, w, target, ignore_index, code, stream)
+        if r.__class__ is tuple:
+            return r
+        if r < 0:
+            _pkg._check(r)
     n = x.shape[0] if x.dim() else 0
     total, kept = _empty(2, dtype=_f32, device=x.device).unbind()
     lse = _empty(n, dtype=_f32, device=x.device)
