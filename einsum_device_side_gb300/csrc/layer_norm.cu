@@ -904,12 +904,20 @@ int norm_forward(const NormJob& j, int sm, cudaStream_t s)
     return vec ? norm_rows<TX, TY, TW, V>(j, nv, grid, block, s) : norm_rows<TX, TY, TW, 1>(j, nv, grid, block, s);
 }
 
-// A row's group of the backward pass, whose threads keep the column sums too: 16 elements at most,
-// the fewest vectors per thread that keep the group at 256 threads or less, then wider groups.
-bool backward_shape(int64_t units, int most_nv, int* nv, dim3* block)
+// A row's group of the backward pass, whose threads keep the column sums too: 16 elements at most.  Few
+// rows: the fewest vectors per thread that keep the group at 256 threads or less, then wider groups.
+// `many` rows: as many elements per thread as leave a warp or two per row, since what a row costs beside
+// its elements (sums, barrier) is the group's: 65536x1024 f32 with 256 threads per row 213 us, with 64
+// 134 us.
+bool backward_shape(int64_t units, int most_nv, bool many, int* nv, dim3* block)
 {
     int n = 1;
-    while (n < most_nv && units > (int64_t)n * 256) n *= 2;
+    if (many && units > 32 && units <= 64) n = 2;
+    else if (many)
+        for (n = most_nv; n > 1 && units < (int64_t)n * 48; n /= 2) {
+        }
+    else
+        while (n < most_nv && units > (int64_t)n * 256) n *= 2;
     const int64_t g = ((units + n - 1) / n + 31) / 32 * 32;
     if (g > 1024) return false;
     *nv = n;
@@ -927,7 +935,7 @@ int norm_backward(NormJob j, const NormVec& dw, const NormVec& db, int sm, cudaS
                      aligned(j.w, 0, sizeof(TW), V, 1);
     int nv = 0;
     dim3 block;
-    const bool fits = backward_shape(vec ? j.cols / V : j.cols, vec ? MOST : 16, &nv, &block);
+    const bool fits = backward_shape(vec ? j.cols / V : j.cols, vec ? MOST : 16, vec && j.rows >= 16 * sm, &nv, &block);
     const bool sums = dw.p || db.p;
     // rows of x and dy that bulk copies can bring, enough of them to fill a ring
     const size_t pair = j.cols * (sizeof(TX) + sizeof(TY));
@@ -982,6 +990,7 @@ int norm_backward(NormJob j, const NormVec& dw, const NormVec& db, int sm, cudaS
                                               : k_norm_back<TX, TY, TW, 1, 16, 1, 512>)
                             : nv == 1         ? k_norm_back<TX, TY, TW, V, 1, 4, 512>
                             : nv == 2 && wide ? k_norm_back<TX, TY, TW, V, 2, 1, 1024>
+                            : block.y > 1     ? k_norm_back<TX, TY, TW, V, 2, 2, 512>
                             : nv == 2         ? k_norm_back<TX, TY, TW, V, 2, 1, 512>
                             : wide            ? k_norm_back<TX, TY, TW, V, MOST, 1, 1024>
                                               : k_norm_back<TX, TY, TW, V, MOST, 1, 512>;

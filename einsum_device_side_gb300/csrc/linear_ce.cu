@@ -10,12 +10,12 @@
 // The logits are the ordinary (+, x) product under a log-sum-exp, the smooth form of the library's
 // max-plus contraction; unlike that one they are multiply-accumulates and run on the tensor cores.
 //
-// One kernel, k_tile, computes all four products as tiles in tensor memory; what
-// differs is where an accumulator goes:
+// One kernel, k_tile, computes all four products as tiles in tensor memory; what differs is where an
+// accumulator goes:
 //   LSE   a tile's logits are folded into each row's running maximum and sum of exponentials in
 //         registers; the logits of a unit of tiles leave as one (maximum, sum) pair per row
-//   GRAD  the logits are formed again and leave as P, for a piece of the vocabulary at a time, so
-//         that P takes a bounded workspace whatever V is
+//   GRAD  the logits are formed again and leave as P (scaled, in the operands' type), for a piece of
+//         the vocabulary at a time, so that P takes a bounded workspace whatever V is
 //   DX    P w over a piece (added to the pieces before it in f32)
 //   DW    P^T x: the piece's rows of dw, whole
 // Operand tiles come by TMA into a ring of 128-byte-swizzled stages; one thread issues the
@@ -45,13 +45,13 @@ constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 128 + 32 * EPI_WARPS;
 
 // A tile's shape: CG CTAs share it, each with 128 of its rows and all TN columns in tensor memory,
-// NACC accumulators taking the stages of the depth in turn.
-template <int CG_, int TN_, int NACC_>
+// NACC accumulators taking the stages of the depth in turn.  A stage holds SUB slices of TK.
+template <int CG_, int TN_, int NACC_, int SUB_ = 1>
 struct Shape {
-    static constexpr int CG = CG_, TN = TN_, NACC = NACC_;
+    static constexpr int CG = CG_, TN = TN_, NACC = NACC_, SUB = SUB_;
     static constexpr int TM = 128 * CG;
     static constexpr int B_BYTES = TN / CG * TK * 2;
-    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+    static constexpr int STAGE_BYTES = SUB * (A_BYTES + B_BYTES);
     static constexpr int STAGES = 196608 / STAGE_BYTES;
     static constexpr int RING = STAGES * STAGE_BYTES;
     static constexpr int BUFS = NACC * TN == 512 ? 1 : 2;  // tiles in tensor memory at a time
@@ -62,7 +62,9 @@ template <int MODE, typename S>
 constexpr int smem_bytes() { return S::RING + (MODE == LSE ? 0 : EPI_WARPS * BOX_BYTES) + 1024; }
 using Pair = Shape<2, 256, 1>;   // products bound by the tensor cores
 using Deep = Shape<2, 256, 2>;   // long logits: half the depth per accumulator
-using Few = Shape<1, 128, 2>;    // up to 128 tokens: bound by reading the weights
+// Up to 128 tokens: bound by reading the weights, in two slices at a time so that a row's 256 bytes are
+// asked for together (16x4096x131072: one slice 181 us, two 178 us, three 185 us).
+using Few = Shape<1, 128, 2, 2>;
 using Few1 = Shape<1, 128, 1>;
 
 constexpr float LOG2E = 1.4426950408889634f;
@@ -89,8 +91,37 @@ __device__ __forceinline__ int64_t target_of(const Targets& t, int64_t i)
     return v == t.ignore ? -1 : v < 0 || v >= t.V ? -2 : v;
 }
 
+// The tokens' gradients g[i * sg] (over *count, where that is given), and how P is stored for the 16-bit
+// products: times `top` / max |g|, undone in f32 when the products leave.  A target's entry, g (p - 1),
+// is then close to -top when p is small, a value the type holds; g itself would be rounded by the
+// same factor for every token of a batch (0.3 % of all gradients for an unlucky 1 / 7783).  In f16
+// top = 2^14 besides lifts P's entries of g / V into the type's range.
+struct GradScale {
+    const float* g;
+    int64_t sg;
+    const float* count;
+    const float* given;  // {factor of P, factor of the products}; null with one g for all tokens
+    float top;
+    Span sp;
+};
+__device__ __forceinline__ float2 scale_of(float m, float top)
+{
+    const bool fine = m > 0.f && m < INFINITY;  // nothing kept, all zero, or not finite: P as it is
+    return fine ? make_float2(__fdiv_rn(top, m), __fdiv_rn(m, top)) : make_float2(1.f, 1.f);
+}
+__device__ __forceinline__ float grad_of(const GradScale& q, int64_t i)
+{
+    const float v = TROP_IN(q.g + i * q.sg, 4, q.sp) ? q.g[i * q.sg] : 0.f;
+    return q.count ? __fdiv_rn(v, *q.count) : v;
+}
+__device__ __forceinline__ float2 grad_scale(const GradScale& q)
+{
+    if (q.given) return make_float2(q.given[0], q.given[1]);
+    return scale_of(fabsf(grad_of(q, 0)), q.top);
+}
+
 struct Job {
-    int mt, nt, inner, ks;  // tiles along rows and columns; column tiles of a unit; splits of the depth
+    int mt, nt, inner;      // tiles along rows and columns; column tiles of a unit
     int kt, kper;           // depth in stages, and of one split
     int units, band;
     int a_bytes;            // of A in a stage
@@ -105,16 +136,13 @@ struct Job {
     // GRAD
     int64_t v0;             // the piece's first column
     const float* lse;
-    const float* g;
-    int64_t sg;
-    const float* count;     // nullable: g is divided by it
-    const float* scale;     // nullable: {factor of P, factor of the products with P}
+    GradScale grad;
     // DX, DW
     void* out;              // null: f32 sums, through map_c
     int64_t ldo;
     int vec;                // rows of out start on 16 bytes: through map_c
     int add;                // f32 sums: added to the pieces before
-    Span sp_part, sp_at, sp_lse, sp_g, sp_out;
+    Span sp_part, sp_at, sp_lse, sp_out;
 };
 
 // `yes` where i == d, else `no`, as one select: written out so that 32 of them in a row do not
@@ -378,7 +406,7 @@ __global__ void __launch_bounds__(THREADS, 1)
            const __grid_constant__ CUtensorMap map_c, const __grid_constant__ Job j, const __grid_constant__ JoinJob join)
 {
     constexpr bool A_MN = MODE == DW, B_MN = MODE == DX || MODE == DW;
-    constexpr int CG = S::CG, TM = S::TM, TN = S::TN, NACC = S::NACC, STAGES = S::STAGES, STAGE_BYTES = S::STAGE_BYTES, BUFS = S::BUFS;
+    constexpr int CG = S::CG, TM = S::TM, TN = S::TN, NACC = S::NACC, STAGES = S::STAGES, STAGE_BYTES = S::STAGE_BYTES, BUFS = S::BUFS, SUB = S::SUB;
     extern __shared__ uint8_t dyn[];
     __shared__ __align__(8) uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], drain;
     __shared__ uint32_t tmem_slot;
@@ -413,25 +441,29 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int n = t.n; n < n_end && ok; ++n)
                     for (int k = t.k0; k < t.k1; ++k) {
                         if (!(ok = mbar_wait(&empty[s], phase ^ 1))) break;
-                        if (rank == 0) mbar_expect_tx(&full[s], (j.a_bytes + S::B_BYTES) * CG);
+                        if (rank == 0) mbar_expect_tx(&full[s], SUB * (j.a_bytes + S::B_BYTES) * CG);
                         const uint32_t bar = CG == 2 ? mapa(smem_u32(&full[s]), 0) : smem_u32(&full[s]);
-                        const uint32_t sa = ring + s * STAGE_BYTES, sb = sa + A_BYTES;
                         const int am = j.a0 + t.m * TM + rank * 128, bm = j.b0 + n * TN + rank * (TN / CG);
-                        const int ak = j.ak0 + k * TK, bk = j.bk0 + k * TK;
-                        if (A_MN) {
 #pragma unroll
-                            for (int c = 0; c < 2; ++c) tma_load_2d<CG>(sa + c * 8192, &map_a, am + 64 * c, ak, bar);
-                        } else {
-                            tma_load_2d<CG>(sa, &map_a, ak, am, bar);
-                        }
-                        if (B_MN) {
+                        for (int sub = 0; sub < SUB; ++sub) {
+                            const uint32_t sa = ring + s * STAGE_BYTES + sub * A_BYTES;
+                            const uint32_t sb = ring + s * STAGE_BYTES + SUB * A_BYTES + sub * S::B_BYTES;
+                            const int ak = j.ak0 + (k * SUB + sub) * TK, bk = j.bk0 + (k * SUB + sub) * TK;
+                            if (A_MN) {
 #pragma unroll
-                            for (int c = 0; c < TN / CG / 64; ++c)
-                                tma_load_2d<CG>(sb + c * 8192, &map_b, bm + 64 * c, bk, bar);
-                        } else {
+                                for (int c = 0; c < 2; ++c) tma_load_2d<CG>(sa + c * 8192, &map_a, am + 64 * c, ak, bar);
+                            } else {
+                                tma_load_2d<CG>(sa, &map_a, ak, am, bar);
+                            }
+                            if (B_MN) {
 #pragma unroll
-                            for (int c = 0; c < (TN / CG + 127) / 128; ++c)
-                                tma_load_2d<CG>(sb + c * 16384, &map_b, bk, bm + 128 * c, bar);
+                                for (int c = 0; c < TN / CG / 64; ++c)
+                                    tma_load_2d<CG>(sb + c * 8192, &map_b, bm + 64 * c, bk, bar);
+                            } else {
+#pragma unroll
+                                for (int c = 0; c < (TN / CG + 127) / 128; ++c)
+                                    tma_load_2d<CG>(sb + c * 16384, &map_b, bk, bm + 128 * c, bar);
+                            }
                         }
                         ++issued;
                         if (++s == STAGES) s = 0, phase ^= 1;
@@ -458,12 +490,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int k = t.k0; k < t.k1; ++k) {
                         if (!(ok = mbar_wait_cluster(&full[s], phase))) break;
                         tc_fence_after();
-                        const uint32_t sa = ring + s * STAGE_BYTES;
-                        const uint64_t da = smem_desc(sa, A_MN ? 8192 : 16), db = smem_desc(sa + A_BYTES, B_MN ? 8192 : 16);
 #pragma unroll
-                        for (int i = 0; i < TK / 16; ++i)  // 16 k: 32 bytes along a row, or 16 rows
-                            tc_mma<CG>(acc + (NACC == 2 ? ((k - t.k0) & 1) * TN : 0), da + i * (A_MN ? 128 : 2),
-                                       db + i * (B_MN ? 128 : 2), idesc, k >= t.k0 + NACC || i > 0);
+                        for (int sub = 0; sub < SUB; ++sub) {
+                            const uint32_t sa = ring + s * STAGE_BYTES + sub * A_BYTES;
+                            const uint32_t sb = ring + s * STAGE_BYTES + SUB * A_BYTES + sub * S::B_BYTES;
+                            const uint64_t da = smem_desc(sa, A_MN ? 8192 : 16), db = smem_desc(sb, B_MN ? 8192 : 16);
+#pragma unroll
+                            for (int i = 0; i < TK / 16; ++i)  // 16 k: 32 bytes along a row, or 16 rows
+                                tc_mma<CG>(acc + (NACC == 2 ? ((k - t.k0) & 1) * TN : 0), da + i * (A_MN ? 128 : 2),
+                                           db + i * (B_MN ? 128 : 2), idesc, k >= t.k0 + NACC || i > 0 || sub > 0);
+                        }
                         tc_commit<CG>(&empty[s]);
                         if (++s == STAGES) s = 0, phase ^= 1;
                     }
@@ -479,9 +515,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int quad = warp & 3, half = (warp - 4) >> 2;
         const uint32_t box = ring + S::RING + (warp - 4) * BOX_BYTES;
         uint32_t tile = 0;
-        float mul = 1.f, alpha = 1.f, inv = 1.f;
-        if (MODE != LSE && j.scale) mul = j.scale[0], alpha = j.scale[1];
-        if (MODE == GRAD && j.count) inv = j.count[0];
+        const float2 scale = MODE == LSE ? make_float2(1.f, 1.f) : grad_scale(j.grad);
         for (int u = first; u < j.units && ok; u += step) {
             const Unit t = unit_of<MODE>(j, u);
             const int n_end = min(j.nt, t.n + (MODE == LSE ? j.inner : 1));
@@ -497,9 +531,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (MODE == GRAD) {
                 r.nlse = 0.f;
                 r.g = 0.f;
-                if (live && TROP_IN(j.lse + row, 4, j.sp_lse) && TROP_IN(j.g + row * j.sg, 4, j.sp_g)) {
+                if (live && TROP_IN(j.lse + row, 4, j.sp_lse)) {
                     r.nlse = -j.lse[row] * LOG2E;
-                    r.g = r.t == -2 ? NAN : __fdiv_rn(j.g[row * j.sg], inv) * mul;
+                    r.g = r.t == -2 ? NAN : grad_of(j.grad, row) * scale.x;
                 }
             }
             for (int n = t.n; n < n_end && ok; ++n, ++tile) {
@@ -556,7 +590,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         grad_chunk<BF16>(r, f, j.v0 + col, w);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) w[i] = pack2<BF16>(f[2 * i] * alpha, f[2 * i + 1] * alpha);
+                        for (int i = 0; i < 16; ++i) w[i] = pack2<BF16>(f[2 * i] * scale.y, f[2 * i + 1] * scale.y);
                     }
                     if (c % 2 == 0) box_free(lane);  // a box of 64 columns, in two halves
                     to_box<16>(box, lane, (c % 2) * 4, w);
@@ -606,27 +640,22 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
 }
 
-// ------------------------------------------------------------------ f16: the range of P
-// P's entries go down to g / V, far below what f16 resolves, so P is stored times
-// 2^14 / max |g| and the products are scaled back.  (bf16 has f32's range and needs none of it.)
-__global__ void __launch_bounds__(256) k_gscale(const float* g, int64_t sg, int64_t n, const float* count, float* scale,
-                                                Span sp_g)
+// ------------------------------------------------------------------ the largest gradient of a batch
+__global__ void __launch_bounds__(1024) k_gscale(const GradScale q, int64_t n, float* scale)
 {
     pdl_wait();
     pdl_signal();
-    __shared__ float red[8];
+    __shared__ float red[32];
     float m = 0.f;
-    for (int64_t i = threadIdx.x; i < (sg ? n : 1); i += 256)
-        if (TROP_IN(g + i * sg, 4, sp_g)) m = fmaxf(m, fabsf(g[i * sg]));
+    for (int64_t i = threadIdx.x; i < n; i += 1024) m = fmaxf(m, fabsf(grad_of(q, i)));
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int w = 1; w < 8; ++w) m = fmaxf(m, red[w]);
-        if (count) m = __fdiv_rn(m, count[0]);
-        const bool fine = m > 0.f && m < INFINITY;  // nothing kept, all zero, or not finite: leave P as it is
-        scale[0] = fine ? __fdiv_rn(16384.f, m) : 1.f;
-        scale[1] = fine ? m * 6.103515625e-05f : 1.f;
+        for (int w = 1; w < 32; ++w) m = fmaxf(m, red[w]);
+        const float2 r = scale_of(m, q.top);
+        scale[0] = r.x;
+        scale[1] = r.y;
     }
 }
 
@@ -634,12 +663,12 @@ __global__ void __launch_bounds__(256) k_gscale(const float* g, int64_t sg, int6
 // Four columns of a row per thread and step where rows allow 16-byte loads.
 template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(256) k_split_join(const float* acc, int ks, int64_t slice, int64_t lda, int64_t rows,
-                                                    int64_t cols, uint16_t* out, int64_t ldo, const float* scale, Span sp_acc, Span sp_out)
+                                                    int64_t cols, uint16_t* out, int64_t ldo, const GradScale grad, Span sp_acc, Span sp_out)
 {
     pdl_wait();
     pdl_signal();
     constexpr int W = VEC ? 4 : 1;
-    const float alpha = scale ? scale[1] : 1.f;
+    const float alpha = grad_scale(grad).y;
     const int64_t n = rows * cols / W, per_row = cols / W;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
         const int64_t r = i / per_row, c = (i - r * per_row) * W;
@@ -903,7 +932,7 @@ int launch_linear_ce(const LinearCe& q, float* loss, float* lse, float* total, f
     j.cols = (int)w.rows;
     j.mt = cdiv(x.rows, TM);
     j.nt = cdiv(w.rows, TN);
-    j.kt = cdiv(x.cols, TK);
+    j.kt = cdiv(x.cols, few ? Few::SUB * TK : TK);
     j.kper = j.kt;
     // column tiles of a unit: the fewest rounds of tiles, then the fewest pairs to join
     int64_t best = INT64_MAX;
@@ -976,13 +1005,14 @@ int launch_linear_ce_backward(const LinearCe& q, const float* g, int64_t sg, con
     void *P, *acc = nullptr, *scale = nullptr;
     TROP_TRY(ws.get(p_bytes, &P));
     if (summed) TROP_TRY(ws.get(acc_bytes, &acc));
-    if (!q.bf16) {
-        TROP_TRY(ws.get(8, &scale));
-        const int64_t size[1] = {N}, stride[1] = {sg};
-        const cudaError_t e = launch_pdl(k_gscale, dim3(1), dim3(256), 0, s, g, sg, N, kept, (float*)scale,
-                                         span_of(g, 4, 1, size, stride));
+    const int64_t gsize[1] = {N}, gstride[1] = {sg};
+    GradScale grad = {g, sg, kept, nullptr, q.bf16 ? 1.f : 16384.f, span_of(g, 4, 1, gsize, gstride)};
+    if (sg != 0) {
+        TROP_TRY(ws.small(8, &scale));
+        const cudaError_t e = launch_pdl(k_gscale, dim3(1), dim3(1024), 0, s, grad, N, (float*)scale);
         if (e != cudaSuccess) return cuda_error(e, "k_gscale launch");
         count_launches(1);
+        grad.given = (const float*)scale;
     }
     CUtensorMap x_k, w_k, x_mn, w_mn, p_k, p_mn, c;
     TROP_TRY(make_map(&x_k, type, x.p, D, N, x.ld, a_rows));
@@ -996,9 +1026,8 @@ int launch_linear_ce_backward(const LinearCe& q, const float* g, int64_t sg, con
         Job j = {};
         TROP_TRY(device_error_word(&j.error));
         j.inner = 1;
-        j.ks = 1;
         j.a_bytes = a_rows * TK * 2;
-        j.scale = (const float*)scale;
+        j.grad = grad;
         {
             Job t = j;
             t.rows = (int)N;
@@ -1012,12 +1041,7 @@ int launch_linear_ce_backward(const LinearCe& q, const float* g, int64_t sg, con
             t.v0 = v0;
             t.tgt = targets_of(q);
             t.lse = lse;
-            t.g = g;
-            t.sg = sg;
-            t.count = kept;
             t.sp_lse = span_bytes(lse, (size_t)N * 4);
-            const int64_t size[1] = {N}, stride[1] = {sg};
-            t.sp_g = span_of(g, 4, 1, size, stride);
             TROP_TRY(make_map(&c, type, P, cols, N, piece, 32));
             TROP_TRY((few ? launch_tile<GRAD, Few1>(q.bf16, x_k, w_k, c, t, sm, s)
                            : launch_tile<GRAD, Pair>(q.bf16, x_k, w_k, c, t, sm, s)));
@@ -1047,8 +1071,7 @@ int launch_linear_ce_backward(const LinearCe& q, const float* g, int64_t sg, con
             t.nt = dx_nt;
             t.kt = cdiv(cols, TK);
             t.kper = cdiv(dx_kt, ks);  // the last piece may have fewer splits: those it lacks stay as they are
-            t.ks = cdiv(t.kt, t.kper);
-            t.units = t.mt * t.nt * t.ks;
+            t.units = t.mt * t.nt * cdiv(t.kt, t.kper);
             t.bk0 = (int)v0;
             if (summed) {
                 t.pad_rows = (int)pad_rows;
@@ -1074,7 +1097,7 @@ int launch_linear_ce_backward(const LinearCe& q, const float* g, int64_t sg, con
         const auto kernel = q.bf16 ? (vec ? k_split_join<true, true> : k_split_join<true, false>)
                                    : (vec ? k_split_join<false, true> : k_split_join<false, false>);
         const cudaError_t e = launch_pdl(kernel, dim3(grid_for(N * D / (vec ? 4 : 1), sm)), dim3(256), 0, s, (const float*)acc,
-                                         ks, pad_rows * lda, lda, N, D, (uint16_t*)dx->p, dx->sr, (const float*)scale, sp_acc, sp_out);
+                                         ks, pad_rows * lda, lda, N, D, (uint16_t*)dx->p, dx->sr, grad, sp_acc, sp_out);
         if (e != cudaSuccess) return cuda_error(e, "k_split_join launch");
         count_launches(1);
     }
