@@ -10,17 +10,32 @@
 // from sums of squares, so that a large mean costs no digits.
 //
 // Both directions are bound by memory: each reads its rows once, into registers.
-//   k_norm, k_norm_back   a row per group of 32 .. 1024 threads, each holding up to 16 (32)
-//                         elements of it, as 16-byte vectors where rows are aligned to them
+//   k_norm          a row per group of 32 .. 1024 threads, each holding up to 16 vectors of it (16 bytes where
+//                   the rows are aligned to them, else one element)
+//   k_norm_short    short rows, many of them: a warp takes several at a time
+//   k_norm_off      many rows that do not start on 16 bytes: whole vectors all the same, a block's rows all
+//                   at one offset
+//   k_norm_back, k_norm_back_off, k_norm_back_ring   the same backward; the ring brings the rows of x and dy
+//                   by bulk copies ahead of their turn
 //   k_norm_long, k_norm_back_long, k_norm_columns   rows longer than a block's registers: the row
-//                         is walked again for each pass (it stays in L2)
+//                   is walked again for each pass (it stays in L2)
 // The weight's and bias's gradients are summed without atomics: a persistent block keeps the sums
-// of its columns over all its rows in registers and writes them once; k_norm_join adds the blocks'
+// of its columns over all its rows and writes them once; k_norm_join adds the blocks'
 // sums in block order, so results repeat bit for bit.
+//
+// Measured (device time, a copy runs at 6.8 TB/s):    forward               backward
+//   16384x4096  f32                                   82 us, 6.6 TB/s       131 us, 6.2 TB/s
+//   16384x4096  bf16                                  50 us, 5.4 TB/s        68 us, 5.9 TB/s
+//   65536x256   f32                                   22 us, 6.1 TB/s        36 us, 5.5 TB/s
+//   4096x16384  bf16                                  53 us, 5.1 TB/s       129 us, 3.1 TB/s (sums in shared memory)
+//   65536x1001  f32 (rows off 16 bytes)              135 us, 3.9 TB/s       148 us, 5.3 TB/s
+//   65536x1001  bf16                                  75 us, 3.5 TB/s       120 us, 3.3 TB/s
+// With 16-bit rows the instructions per element come near the bound: they are worked on in packed pairs.
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cstdint>
+#include <initializer_list>
 #include <type_traits>
 
 #define TROP_TU 7  // this file's id in a bounds-violation record
@@ -352,6 +367,173 @@ __global__ void __launch_bounds__(256, 4) k_norm_short(const NormJob j)
     }
 }
 
+// Rows that do not start on 16 bytes, as every row of an odd number of columns but one in VEC does: row r
+// starts `off` elements into a 16-byte granule, and off repeats every `period` rows.  A block takes rows
+// of one offset only, so that its threads' vectors, the granules of its rows, hold the same columns in
+// all of them: thread's column c = vector * VEC - off.  A row's first and last vector may be partial; it
+// is written element by element, so that nothing outside the row is touched.
+struct Offset {
+    int off, cls;
+    int64_t first, step;  // of the block's rows: cls + period * (first + i * step)
+};
+template <typename T, int VEC>
+__device__ __forceinline__ Offset offset_of(const void* base, int64_t stride, int period)
+{
+    Offset o;
+    o.cls = blockIdx.x % period;
+    o.off = (int)(((uintptr_t)((const T*)base + o.cls * stride) % 16) / sizeof(T));
+    o.first = (int64_t)(blockIdx.x / period) * blockDim.y + threadIdx.y;
+    o.step = (int64_t)(gridDim.x / period) * blockDim.y;
+    return o;
+}
+template <int VEC>
+__device__ __forceinline__ bool whole(int c, int cols) { return c >= 0 && c + VEC <= cols; }
+template <typename T, int VEC>
+__device__ __forceinline__ void load_part(const T* row, int c, int cols, float (&v)[VEC], const Span& sp)
+{
+    (void)sp;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = c + i >= 0 && c + i < cols && TROP_IN(row + c + i, sizeof(T), sp) ? to_f32(row[c + i]) : 0.f;
+}
+// (Of 16-bit rows a granule inside the matrix is read whole and the neighbouring rows' elements are put to
+// zero: forward of 65536x1001 bf16 94 us, element by element 118 us.  Of f32 rows, whose granules have four
+// elements, that costs more registers than it saves: backward of 65536x1001 348 us, element by element 148 us.)
+template <typename T, int VEC>
+__device__ __forceinline__ void load_off(const T* row, int c, int cols, const T* begin, const T* end, Raw<T, VEC>& q, const Span& sp)
+{
+    (void)sp;
+    if (sizeof(T) == 2 ? row + c >= begin && row + c + VEC <= end : whole<VEC>(c, cols)) {
+        if (TROP_IN(row + c, VEC * sizeof(T), sp)) q.read(row + c);
+        else q.zero();
+        if (sizeof(T) == 2 && !whole<VEC>(c, cols)) {
+            constexpr int E = 4 / sizeof(T);  // elements of a word
+#pragma unroll
+            for (int i = 0; i < Raw<T, VEC>::N; ++i) {
+                uint32_t keep = 0;
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if (c + i * E + e >= 0 && c + i * E + e < cols) keep |= (E == 1 ? 0xffffffffu : 0xffffu) << 16 * e;
+                q.w[i] &= keep;
+            }
+        }
+    } else {
+        float v[VEC];
+        load_part<T, VEC>(row, c, cols, v, sp);
+        q.set(v);
+    }
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store_off(T* row, int c, int cols, const float (&v)[VEC], const Span& sp)
+{
+    if (whole<VEC>(c, cols)) {
+        store<T, VEC>(row + c, v, sp);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            if (c + i >= 0 && c + i < cols && TROP_IN(row + c + i, sizeof(T), sp)) row[c + i] = from_f32<T>(v[i]);
+    }
+}
+
+// U rows of a group at a time; the weight and bias lie in shared memory, moved by the block's offset.
+template <typename T, typename TW, int VEC, int NV, int U>
+__global__ void __launch_bounds__(NV == 4 ? 672 : 256) k_norm_off(const NormJob j, int period)
+{
+    pdl_wait();
+    pdl_signal();
+    extern __shared__ __align__(16) uint8_t dyn[];
+    __shared__ float sh[2][32][U];
+    const int cols = (int)j.cols, span = (cols + VEC - 1 + VEC) / VEC * VEC;  // (off + cols at most)
+    const Offset o = offset_of<T, VEC>(j.x, j.sx, period);
+    const T* const end = (const T*)j.x + (j.rows - 1) * j.sx + cols;
+    TW* sw = reinterpret_cast<TW*>(dyn);
+    TW* sb = sw + span;
+    for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < span; i += blockDim.x * blockDim.y) {
+        const int c = i - o.off;
+        const bool in = c >= 0 && c < cols;
+        if (j.w) sw[i] = in && TROP_IN((const TW*)j.w + c, sizeof(TW), j.sp_w) ? ((const TW*)j.w)[c] : from_f32<TW>(0.f);
+        if (j.b) sb[i] = in && TROP_IN((const TW*)j.b + c, sizeof(TW), j.sp_b) ? ((const TW*)j.b)[c] : from_f32<TW>(0.f);
+    }
+    __syncthreads();
+    for (int64_t n = o.first; o.cls + period * n < j.rows; n += o.step * U) {
+        Raw<T, VEC> q[U][NV];
+        float mean[U], rstd[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = o.cls + period * (n + u * o.step);
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int c = (k * blockDim.x + threadIdx.x) * VEC - o.off;
+                if (row < j.rows && c < cols) load_off<T, VEC>((const T*)j.x + row * j.sx, c, cols, (const T*)j.x, end, q[u][k], j.sp_x);
+                else q[u][k].zero();
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            Pair<VEC> a = p_of<Pair<VEC>>(0.f);
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int i = 0; i < pairs<VEC>; ++i) a = p_add(a, pair_of<T, VEC>(q[u][k], i));
+            mean[u] = p_sum(a);
+        }
+        group_sum_turn<U>(mean, sh[0]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            mean[u] *= j.inv_cols;
+            Pair<VEC> a = p_of<Pair<VEC>>(0.f);
+            float edge = 0.f;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int c = (k * blockDim.x + threadIdx.x) * VEC - o.off;
+                if (whole<VEC>(c, cols)) {
+                    a = squares<T, VEC>(q[u][k], mean[u], a);
+                } else if (c < cols) {
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) {
+                        const float d = c + i >= 0 && c + i < cols ? q[u][k].get(i) - mean[u] : 0.f;
+                        edge = __fmaf_rn(d, d, edge);
+                    }
+                }
+            }
+            rstd[u] = p_sum(a) + edge;
+        }
+        group_sum_turn<U>(rstd, sh[1]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) rstd[u] = __fdiv_rn(1.f, __fsqrt_rn(__fmaf_rn(rstd[u], j.inv_cols, j.eps)));
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int at = (k * blockDim.x + threadIdx.x) * VEC, c = at - o.off;
+            if (c >= cols) continue;
+            Raw<TW, VEC> w, b;
+            if (j.w) w.read(sw + at);
+            if (j.b) b.read(sb + at);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t row = o.cls + period * (n + u * o.step);
+                if (row >= j.rows) break;
+                Pair<VEC> r[pairs<VEC>];
+                float v[VEC];
+#pragma unroll
+                for (int i = 0; i < pairs<VEC>; ++i) {
+                    r[i] = p_mul(p_add(pair_of<T, VEC>(q[u][k], i), p_of<Pair<VEC>>(-mean[u])), p_of<Pair<VEC>>(rstd[u]));
+                    if (j.w) r[i] = p_mul(r[i], pair_of<TW, VEC>(w, i));
+                    if (j.b) r[i] = p_add(r[i], pair_of<TW, VEC>(b, i));
+                }
+                apart<VEC>(r, v);
+                store_off<T, VEC>((T*)j.y + row * j.sy, c, cols, v, j.sp_y);
+            }
+        }
+        if (threadIdx.x == 0)
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t row = o.cls + period * (n + u * o.step);
+                if (row >= j.rows) break;
+                if (j.mean && TROP_IN(j.mean + row, 4, j.sp_mean)) j.mean[row] = mean[u];
+                if (j.rstd && TROP_IN(j.rstd + row, 4, j.sp_rstd)) j.rstd[row] = rstd[u];
+            }
+    }
+}
+
 // Rows longer than a block's registers: one block per row, three walks over it.
 template <typename TX, typename TY, typename TW>
 __global__ void __launch_bounds__(1024) k_norm_long(const NormJob j)
@@ -484,16 +666,16 @@ struct Weights<TW, VEC, NV, false> {
         for (int i = 0; i < pairs<VEC>; ++i) d[i] = p_mul(d[i], pair_at<VEC>(v, i));
     }
 };
+// `times(k, d)` multiplies vector k by the weight.
 template <int VEC, int NV, typename W, typename S>
-__device__ __forceinline__ void back_sums(const NormJob& j, const Pairs<VEC, NV>& h, Pairs<VEC, NV>& d, const W& w, S& acc,
-                                          float (&s)[2])
+__device__ __forceinline__ void back_sums(const Pairs<VEC, NV>& h, Pairs<VEC, NV>& d, const W& times, S& acc, float (&s)[2])
 {
     Pair<VEC> flat = p_of<Pair<VEC>>(0.f), along = flat;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
 #pragma unroll
         for (int i = 0; i < pairs<VEC>; ++i) acc.add(k, i, d[k][i], h[k][i]);
-        w.times(j, k, d[k]);
+        times(k, d[k]);
 #pragma unroll
         for (int i = 0; i < pairs<VEC>; ++i) {
             flat = p_add(flat, d[k][i]);
@@ -526,7 +708,7 @@ __device__ __forceinline__ void back_store(const NormJob& j, int64_t row, const 
 // The block's column sums into its row of the partial sums.  Blocks of several warps that each took
 // rows of their own (blockDim.y > 1) add theirs in warp order, through `across` [warps][cols].
 template <int VEC, int NV, typename S>
-__device__ __forceinline__ void back_partials(const NormJob& j, const S& acc, float* across)
+__device__ __forceinline__ void back_partials(const NormJob& j, const S& acc, float* across, int off = 0)
 {
     const int cols = (int)j.cols;
     for (int which = 0; which < 2; ++which) {
@@ -538,16 +720,18 @@ __device__ __forceinline__ void back_partials(const NormJob& j, const S& acc, fl
         if (blockDim.y > 1) __syncthreads();
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int c = (k * blockDim.x + threadIdx.x) * VEC;
+            const int c = (k * blockDim.x + threadIdx.x) * VEC - off;
             if (c >= cols) continue;
             Pair<VEC> o[pairs<VEC>];
             float v[VEC];
 #pragma unroll
             for (int i = 0; i < pairs<VEC>; ++i) o[i] = acc.get(k, i, which);
             apart<VEC>(o, v);
-            if (blockDim.y > 1) {
+            if (blockDim.y > 1 || cols % VEC != 0 || off != 0) {
+                float* to = blockDim.y > 1 ? across + threadIdx.y * cols : part;
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) across[threadIdx.y * cols + c + i] = v[i];
+                for (int i = 0; i < VEC; ++i)
+                    if (c + i >= 0 && c + i < cols && (blockDim.y > 1 || TROP_IN(part + c + i, 4, sp))) to[c + i] = v[i];
             } else {
                 store<float, VEC>(part + c, v, sp);
             }
@@ -610,7 +794,7 @@ __global__ void __launch_bounds__(MAXT) k_norm_back(const NormJob j)
             Pairs<VEC, NV> h, d;
             float s[2];
             back_row<TX, TY, VEC, NV>(qx[u], qd[u], mean[u], rstd[u], h, d);
-            back_sums<VEC, NV>(j, h, d, w, acc, s);
+            back_sums<VEC, NV>(h, d, [&](int k, Pair<VEC>(&e)[pairs<VEC>]) { w.times(j, k, e); }, acc, s);
             sums[2 * u] = s[0], sums[2 * u + 1] = s[1];
         }
         if (!j.dx) continue;
@@ -631,6 +815,112 @@ __global__ void __launch_bounds__(MAXT) k_norm_back(const NormJob j)
         }
     }
     if (j.part_w || j.part_b) back_partials<VEC, NV>(j, acc, reinterpret_cast<float*>(dyn));
+}
+
+// The same for rows that do not start on 16 bytes: a block's rows share one offset (see k_norm_off), so
+// its threads' columns, and with them their sums, stay the same ones.  WIDE: up to 1024 threads of 64
+// registers, the sums and the weight (moved by the offset) in shared memory.
+template <typename T, typename TW, int VEC, int NV, int U, bool WIDE>
+__global__ void __launch_bounds__(WIDE ? 1024 : 512) k_norm_back_off(const NormJob j, int period)
+{
+    pdl_wait();
+    pdl_signal();
+    extern __shared__ __align__(16) uint8_t dyn[];
+    __shared__ float sh[2][32][2 * U];
+    const int cols = (int)j.cols;
+    const Offset o = offset_of<T, VEC>(j.x, j.sx, period);
+    const T *const end_x = (const T*)j.x + (j.rows - 1) * j.sx + cols, *const end_dy = (const T*)j.dy + (j.rows - 1) * j.sdy + cols;
+    Sums<VEC, NV, WIDE> acc;
+    acc.init(dyn);
+    TW* const sw = reinterpret_cast<TW*>(dyn + (size_t)blockDim.x * NV * VEC * 8);
+    Pairs<VEC, WIDE ? 1 : NV> w;
+    if (WIDE) {
+        for (int i = threadIdx.x; i < NV * VEC * (int)blockDim.x; i += blockDim.x) {
+            const int c = i - o.off;
+            const bool in = j.w && c >= 0 && c < cols && TROP_IN((const TW*)j.w + c, sizeof(TW), j.sp_w);
+            sw[i] = in ? ((const TW*)j.w)[c] : from_f32<TW>(j.w ? 0.f : 1.f);
+        }
+        __syncthreads();
+    } else {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = (k * blockDim.x + threadIdx.x) * VEC - o.off;
+            float v[VEC];
+            if (j.w) load_part<TW, VEC>((const TW*)j.w, c, cols, v, j.sp_w);
+#pragma unroll
+            for (int i = 0; i < pairs<VEC>; ++i) w[WIDE ? 0 : k][i] = j.w ? pair_at<VEC>(v, i) : p_of<Pair<VEC>>(1.f);
+        }
+    }
+    const auto times = [&](int k, Pair<VEC>(&d)[pairs<VEC>]) {
+        if (WIDE) {
+            Raw<TW, VEC> q;
+            q.read(sw + (k * blockDim.x + threadIdx.x) * VEC);
+#pragma unroll
+            for (int i = 0; i < pairs<VEC>; ++i) d[i] = p_mul(d[i], pair_of<TW, VEC>(q, i));
+        } else {
+#pragma unroll
+            for (int i = 0; i < pairs<VEC>; ++i) d[i] = p_mul(d[i], w[WIDE ? 0 : k][i]);
+        }
+    };
+    int turn = 0;
+    for (int64_t n = o.first; o.cls + period * n < j.rows; n += o.step * U) {
+        Raw<T, VEC> qx[U][NV], qd[U][NV];
+        float mean[U], rstd[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = o.cls + period * (n + u * o.step);
+            const bool live = row < j.rows;
+            mean[u] = live && TROP_IN(j.mean + row, 4, j.sp_mean) ? j.mean[row] : 0.f;
+            rstd[u] = live && TROP_IN(j.rstd + row, 4, j.sp_rstd) ? j.rstd[row] : 0.f;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int c = (k * blockDim.x + threadIdx.x) * VEC - o.off;
+                if (live && c < cols) {
+                    load_off<T, VEC>((const T*)j.x + row * j.sx, c, cols, (const T*)j.x, end_x, qx[u][k], j.sp_x);
+                    load_off<T, VEC>((const T*)j.dy + row * j.sdy, c, cols, (const T*)j.dy, end_dy, qd[u][k], j.sp_dy);
+                } else {  // dy = 0: nothing in any sum
+                    qx[u][k].zero();
+                    qd[u][k].zero();
+                }
+            }
+        }
+        float sums[2 * U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            Pairs<VEC, NV> h, d;
+            float s[2];
+            back_row<T, T, VEC, NV>(qx[u], qd[u], mean[u], rstd[u], h, d);
+            back_sums<VEC, NV>(h, d, times, acc, s);
+            sums[2 * u] = s[0], sums[2 * u + 1] = s[1];
+        }
+        if (!j.dx) continue;
+        group_sum_turn<2 * U>(sums, sh[turn]);
+        turn ^= 1;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = o.cls + period * (n + u * o.step);
+            if (row >= j.rows) break;
+            Pairs<VEC, NV> h, d;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) qx[u][k].again(), qd[u][k].again();
+            back_row<T, T, VEC, NV>(qx[u], qd[u], mean[u], rstd[u], h, d);
+            const Pair<VEC> flat = p_of<Pair<VEC>>(-sums[2 * u] * j.inv_cols), along = p_of<Pair<VEC>>(-sums[2 * u + 1] * j.inv_cols);
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                times(k, d[k]);
+                const int c = (k * blockDim.x + threadIdx.x) * VEC - o.off;
+                if (c >= cols) continue;
+                Pair<VEC> r[pairs<VEC>];
+                float v[VEC];
+#pragma unroll
+                for (int i = 0; i < pairs<VEC>; ++i)
+                    r[i] = p_mul(p_fma(h[k][i], along, p_add(d[k][i], flat)), p_of<Pair<VEC>>(rstd[u]));
+                apart<VEC>(r, v);
+                store_off<T, VEC>((T*)j.dx + row * j.sdx, c, cols, v, j.sp_dx);
+            }
+        }
+    }
+    if (j.part_w || j.part_b) back_partials<VEC, NV>(j, acc, reinterpret_cast<float*>(dyn), o.off);
 }
 
 // Rows through shared memory: a ring of `stages` rows of x and dy, each brought by two bulk copies, so
@@ -697,7 +987,7 @@ __global__ void __launch_bounds__(MAXT) k_norm_back_ring(const NormJob j, int st
             }
         }
         back_row<TX, TY, VEC, NV>(qx, qd, mean, rstd, h, d);
-        back_sums<VEC, NV>(j, h, d, w, acc, sum);
+        back_sums<VEC, NV>(h, d, [&](int k, Pair<VEC>(&e)[pairs<VEC>]) { w.times(j, k, e); }, acc, sum);
         warp_sum<2>(sum);
         if ((threadIdx.x & 31) == 0) sh[turn][threadIdx.x >> 5][0] = sum[0], sh[turn][threadIdx.x >> 5][1] = sum[1];
         ok = __syncthreads_and(ok);
@@ -830,6 +1120,28 @@ bool aligned(const void* p, int64_t stride, size_t elem, int vec, int64_t rows)
     return !p || (((uintptr_t)p % (elem * vec)) == 0 && (rows <= 1 || stride % vec == 0));
 }
 
+// After how many rows the rows' places in 16-byte granules repeat, the same for all the matrices: 0 where
+// they differ, or an element straddles granules.
+struct Rows {
+    const void* p;
+    int64_t stride;
+};
+int offset_period(size_t elem, int64_t rows, std::initializer_list<Rows> all)
+{
+    const int64_t v = 16 / elem;
+    int64_t base = -1, stride = 0;
+    for (const Rows& m : all) {
+        if (!m.p) continue;
+        if ((uintptr_t)m.p % elem) return 0;
+        const int64_t b = ((uintptr_t)m.p % 16) / elem, s = rows > 1 ? m.stride % v : 0;
+        if (base < 0) base = b, stride = s;
+        else if (b != base || s != stride) return 0;
+    }
+    int period = 1;
+    while (period * stride % v) period *= 2;
+    return period;
+}
+
 #define TROP_LAUNCH(kernel, grid, block, smem, ...)                                   \
     do {                                                                              \
         const cudaError_t e_ = launch_pdl(kernel, grid, block, smem, s, __VA_ARGS__); \
@@ -839,8 +1151,8 @@ bool aligned(const void* p, int64_t stride, size_t elem, int vec, int64_t rows)
 
 // A row's group of the forward pass: as many vectors per thread as still leave 8 warps per SM at
 // work, so that long batches put a row into one warp (no barrier, up to 16 loads on their way per
-// thread) and a few rows are spread over many threads.  16384x4096 bf16: a warp per row, see the
-// head of this file; 16x512 f32: 128 threads per row.
+// thread) and a few rows are spread over many threads: 16384x4096 bf16, two warps per row; 16x512 f32,
+// 128 threads per row.
 template <typename TX, int VEC>
 bool forward_shape(int64_t units, int64_t rows, int sm, int* nv, dim3* block)
 {
@@ -888,6 +1200,31 @@ int norm_forward(const NormJob& j, int sm, cudaStream_t s)
                                       : k_norm_short<TX, TY, TW, V, 4, 1>;
         TROP_LAUNCH(kernel, dim3((unsigned)blocks), block, 0, j);
         return TROP_OK;
+    }
+    if constexpr (std::is_same<TX, TY>::value) {
+        const int period = vec ? 0 : offset_period(sizeof(TX), j.rows, {{j.x, j.sx}, {j.y, j.sy}});
+        const int64_t vecs = (j.cols + V - 1) / V + 1;
+        // f32 rows of more than a warp: the scalar kernel's 16 loads a thread win (16384x4093 139 us, here 166 us)
+        if (period > 0 && vecs <= (sizeof(TX) == 2 ? 2048 : 128) && j.rows >= (int64_t)sm * 16) {
+            const int nv = vecs <= 32 ? 1 : vecs <= 64 ? 2 : 4;
+            const int64_t g = ((vecs + nv - 1) / nv + 31) / 32 * 32;
+            const dim3 block((unsigned)g, g == 32 ? 8 : 1);
+            const size_t smem = 2 * (size_t)(j.cols + 2 * V) * sizeof(TW);
+            const auto kernel = nv == 1   ? k_norm_off<TX, TW, V, 1, 4>
+                                : nv == 2 ? k_norm_off<TX, TW, V, 2, 2>
+                                          : k_norm_off<TX, TW, V, 4, 1>;
+            if (smem > 49152) {
+                const cudaError_t a = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                if (a != cudaSuccess) return cuda_error(a, "cudaFuncSetAttribute(k_norm_off)");
+            }
+            int per_sm = 0;  // as many blocks as run at once: none waits for a place
+            const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, (int)(g * block.y), smem);
+            if (e != cudaSuccess) return cuda_error(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor(k_norm_off)");
+            int64_t blocks = std::min<int64_t>((j.rows + block.y - 1) / block.y, (int64_t)sm * std::max(1, per_sm));
+            blocks = std::max<int64_t>(1, blocks / period) * period;
+            TROP_LAUNCH(kernel, dim3((unsigned)blocks), block, smem, j, period);
+            return TROP_OK;
+        }
     }
     int nv = 0;
     dim3 block;
@@ -937,6 +1274,23 @@ int norm_backward(NormJob j, const NormVec& dw, const NormVec& db, int sm, cudaS
     dim3 block;
     const bool fits = backward_shape(vec ? j.cols / V : j.cols, vec ? MOST : 16, vec && j.rows >= 16 * sm, &nv, &block);
     const bool sums = dw.p || db.p;
+    // Many rows off the 16-byte granules: eight elements a thread, four rows at a time, where that fills an
+    // SM's 512 threads of 128 registers; else sixteen a thread, one row at a time, and so for 16-bit rows too
+    // where a block gets eight rows or more: 65536x1001 bf16 119 us, with eight a thread 186 us, but
+    // 2999x1001 23.5 us, with eight 16.3 us (partial sums of more blocks).
+    int period = 0;
+    if constexpr (std::is_same<TX, TY>::value)
+        if (!vec && j.rows >= (int64_t)sm * 8 && j.cols + V > 8 * V && j.cols + V <= 16384)
+            period = offset_period(sizeof(TX), j.rows, {{j.x, j.sx}, {j.dy, j.sdy}, {j.dx, j.sdx}});
+    const int64_t off_vecs = (j.cols + V - 1) / V + 1;
+    int64_t off_g = ((off_vecs * V + 7) / 8 + 31) / 32 * 32, off_per_sm = 512 / (off_g == 32 ? 128 : off_g);
+    const int64_t wide_g = ((off_vecs * V + 15) / 16 + 31) / 32 * 32;
+    const bool off_wide = wide_g > 32 && (off_g * off_per_sm < 384 || (sizeof(TX) == 2 && j.rows * wide_g >= (int64_t)sm * 1024 * 8));
+    if (off_wide) {
+        off_g = wide_g;
+        off_per_sm = std::min<int64_t>(1024 / off_g, 220000 / (off_g * 16 * (8 + sizeof(TW))));
+    }
+    const dim3 off_block((unsigned)off_g, off_g == 32 ? 4 : 1);  // (a wide block has one group: off_g >= 64)
     // rows of x and dy that bulk copies can bring, enough of them to fill a ring
     const size_t pair = j.cols * (sizeof(TX) + sizeof(TY));
     const int per_sm = block.x > 256 ? 1 : std::max<int>(2, 512 / (int)block.x);  // blocks that share an SM
@@ -945,7 +1299,10 @@ int norm_backward(NormJob j, const NormVec& dw, const NormVec& db, int sm, cudaS
     const bool ring = fits && vec && block.y == 1 && block.x >= 64 && block.x <= 512 && j.cols * sizeof(TY) % 16 == 0 &&
                       aligned(j.dy, j.sdy * sizeof(TY), 1, 16, j.rows) && j.rows >= 4 * sm && stages >= 2;
     int blocks = 0;
-    if (ring) blocks = (int)std::min<int64_t>(j.rows, (int64_t)sm * per_sm);
+    if (period > 0) {
+        blocks = (int)std::min<int64_t>((j.rows + off_block.y - 1) / off_block.y, sm * off_per_sm);
+        blocks = std::max(1, blocks / period) * period;
+    } else if (ring) blocks = (int)std::min<int64_t>(j.rows, (int64_t)sm * per_sm);
     else if (fits) blocks = (int)std::min<int64_t>((j.rows + block.y - 1) / block.y, (int64_t)sm * std::max<int>(1, 512 / (int)(block.x * block.y)));
     else blocks = (int)std::min<int64_t>(j.rows, std::max<int64_t>(1, (int64_t)sm * 8 * 256 / j.cols));
     const size_t bytes = (size_t)blocks * j.cols * 4, spaced = (bytes + 255) / 256 * 256;
@@ -966,7 +1323,17 @@ int norm_backward(NormJob j, const NormVec& dw, const NormVec& db, int sm, cudaS
     j.part_b = (float*)pb;
     j.sp_pw = span_bytes(pw, bytes);
     j.sp_pb = span_bytes(pb, bytes);
-    if (!fits) {
+    if (period > 0) {
+        if constexpr (std::is_same<TX, TY>::value) {
+            const size_t smem = off_wide ? off_g * 16 * (8 + sizeof(TW)) : off_block.y > 1 ? off_block.y * (size_t)j.cols * 4 : 0;
+            const auto kernel = off_wide ? k_norm_back_off<TX, TW, V, 16 / V, 1, true> : k_norm_back_off<TX, TW, V, 8 / V, 4, false>;
+            if (smem > 49152) {
+                const cudaError_t a = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                if (a != cudaSuccess) return cuda_error(a, "cudaFuncSetAttribute(k_norm_back_off)");
+            }
+            TROP_LAUNCH(kernel, dim3((unsigned)blocks), off_block, smem, j, period);
+        }
+    } else if (!fits) {
         if (j.dx) TROP_LAUNCH((k_norm_back_long<TX, TY, TW>), dim3((unsigned)j.rows), dim3(1024), 0, j);
         if (sums)
             TROP_LAUNCH((k_norm_columns<TX, TY>), dim3((unsigned)((j.cols + 255) / 256), (unsigned)blocks), dim3(256), 0, j);

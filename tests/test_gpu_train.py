@@ -106,6 +106,34 @@ def test_layer_norm_both_directions(trop, rows, cols, dt):
     _close(db, wb, dt, 32 * U * dy.double().abs().sum(0))
 
 
+# many rows of which most start off the 16-byte granules: every offset, a row of one vector, and the widths
+# around each change of the kernels' shapes
+OFF_SIZES = [(2500, 3), (2477, 33), (2600, 129), (2433, 257), (2700, 510), (2600, 1001), (2440, 4093), (2433, 8189),
+             (1300, 2047), (1250, 4097), (1217, 16375), (19500, 1001)]
+
+
+@pytest.mark.parametrize("dt", [F, B, H])
+@pytest.mark.parametrize("rows,cols", OFF_SIZES)
+def test_layer_norm_of_many_rows_off_the_granules(trop, rows, cols, dt):
+    test_layer_norm_both_directions(trop, rows, cols, dt)
+
+
+@pytest.mark.parametrize("dt", [F, B])
+@pytest.mark.parametrize("cols,pad", [(64, 1), (100, 3), (200, 7), (96, 4)])
+def test_layer_norm_of_many_strided_rows_off_the_granules(trop, cols, pad, dt):
+    rows = 2500
+    wide, w, b, dy = _norm_case(rows, cols + pad, dt, cols + pad)
+    w, b = w[:cols], b[:cols]
+    x, dy = wide[:, pad:], dy.to(dt)[:, pad:]
+    y, mean, rstd = trop.layer_norm(x, w, b)
+    wy, _, _, _ = _norm_plain(x, w, b, 1e-5)
+    _close(y, wy, dt, 64 * U * (x.double().abs().amax(1, keepdim=True) + 4) * (w.double().abs() + 1) + 64 * U * b.double().abs())
+    dx, dw, db = trop.layer_norm_backward(dy, x, mean, rstd, w)
+    z = (x.double() - mean.double()[:, None]) * rstd.double()[:, None]
+    wx, ww, wb = _norm_plain_back(dy, z, rstd.double(), w)
+    assert _norm(dx, wx) <= max(ROUND[dt], 64 * U) and _norm(dw, ww) <= 64 * U and _norm(db, wb) <= 64 * U
+
+
 @pytest.mark.parametrize("ydt", [B, H])
 def test_layer_norm_of_f32_gives_16_bits(trop, ydt):
     x, w, b, dy = _norm_case(37, 520, F, 5)

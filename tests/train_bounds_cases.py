@@ -53,6 +53,8 @@ def main() -> int:
         norm(2500, 64, dt)       # short rows, several at a time
         norm(2600, 512, dt)
         norm(700, 2048, dt)      # rows through the ring
+        for cols in (7, 33, 257, 1001, 2047, 4085, 8191):  # many rows off the 16-byte granules
+            norm(2440, cols, dt)
         norm(60, 128, dt, pad=8)
         norm(60, 100, dt, pad=3, shift=1)
 
