@@ -697,6 +697,62 @@ __global__ void __launch_bounds__(256) k_split_join(const float* acc, int ks, in
 }
 
 // ------------------------------------------------------------------ operands that TMA cannot read
+// Rows of consecutive elements that start or repeat off 16 bytes: a warp per row, 4-byte words.  A row that
+// starts inside a word shifts two of them together; a word that reaches outside the matrix is read by halves.
+constexpr int PACK_WORDS = 8;  // of a thread at once: 64 warps then have 64 KB of an SM on their way
+__global__ void __launch_bounds__(256) k_pack_rows(const uint16_t* in, int64_t sr, int64_t rows, int64_t cols, uint16_t* out,
+                                                   int64_t ld, Span sp_in)
+{
+    pdl_wait();
+    pdl_signal();
+    const uint16_t* const end = in + (rows - 1) * sr + cols;
+    const int64_t words = (cols + 1) / 2;
+    for (int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.y; r < rows; r += (int64_t)gridDim.x * 8) {
+        const uint16_t* const row = in + r * sr;
+        uint32_t* const to = reinterpret_cast<uint32_t*>(out + r * ld);
+        const int odd = ((uintptr_t)row & 2) != 0;
+        for (int64_t at = threadIdx.x; at < words; at += 32 * PACK_WORDS) {
+            uint32_t lo[PACK_WORDS], hi[PACK_WORDS];
+            const int64_t first = at - threadIdx.x;
+            if (first + 32 * PACK_WORDS < words && (row > in || first > 0)) {  // nothing reaches outside
+                const uint32_t* const src = reinterpret_cast<const uint32_t*>(row - odd) + at;
+#pragma unroll
+                for (int u = 0; u < PACK_WORDS; ++u) {
+                    lo[u] = TROP_IN(src + 32 * u, 4, sp_in) ? src[32 * u] : 0;
+                    hi[u] = odd && TROP_IN(src + 32 * u + 1, 4, sp_in) ? src[32 * u + 1] : 0;
+                }
+#pragma unroll
+                for (int u = 0; u < PACK_WORDS; ++u) to[at + 32 * u] = odd ? __funnelshift_r(lo[u], hi[u], 16) : lo[u];
+                continue;
+            }
+#pragma unroll
+            for (int u = 0; u < PACK_WORDS; ++u) {
+                lo[u] = hi[u] = 0;
+                if (at + 32 * u >= words) continue;
+                const uint16_t* const p = row + 2 * (at + 32 * u);
+                if (p - odd >= in && p - odd + 2 <= end) {
+                    if (TROP_IN(p - odd, 4, sp_in)) lo[u] = *reinterpret_cast<const uint32_t*>(p - odd);
+                } else if (TROP_IN(p, 2, sp_in)) {
+                    lo[u] = (uint32_t)*p << 16 * odd;
+                }
+                if (!odd) continue;
+                if (p + 3 <= end) {
+                    if (TROP_IN(p + 1, 4, sp_in)) hi[u] = *reinterpret_cast<const uint32_t*>(p + 1);
+                } else if (p + 1 < end && TROP_IN(p + 1, 2, sp_in)) {
+                    hi[u] = p[1];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < PACK_WORDS; ++u) {
+                const int64_t w = at + 32 * u;
+                if (w >= words) break;
+                const uint32_t v = odd ? __funnelshift_r(lo[u], hi[u], 16) : lo[u];
+                to[w] = 2 * w + 1 < cols ? v : v & 0xffffu;
+            }
+        }
+    }
+}
+// Any strides, an element at a time.
 __global__ void __launch_bounds__(256) k_pack16(const uint16_t* in, int64_t sr, int64_t sc, int64_t rows, int64_t cols,
                                                 uint16_t* out, int64_t ld, Span sp_in)
 {
@@ -806,10 +862,14 @@ int readable(const Mat16& a, int sm, Blocks& ws, Matrix16* out)
     void* p;
     TROP_TRY(ws.get((size_t)a.rows * ld * 2, &p));
     const int64_t size[2] = {a.rows, a.cols}, stride[2] = {a.sr, a.sc};
-    const cudaError_t e = launch_pdl(k_pack16, dim3(grid_for(a.rows * a.cols, sm)), dim3(256), 0, ws.s,
-                                     (const uint16_t*)a.p, a.sr, a.sc, a.rows, a.cols, (uint16_t*)p, ld,
-                                     span_of(a.p, 2, 2, size, stride));
-    if (e != cudaSuccess) return cuda_error(e, "k_pack16 launch");
+    const Span span = span_of(a.p, 2, 2, size, stride);
+    const dim3 by_rows((unsigned)std::min<int64_t>((a.rows + 7) / 8, (int64_t)sm * 8));
+    const cudaError_t e =
+        a.sc == 1 && a.sr >= 0
+            ? launch_pdl(k_pack_rows, by_rows, dim3(32, 8), 0, ws.s, (const uint16_t*)a.p, a.sr, a.rows, a.cols, (uint16_t*)p, ld, span)
+            : launch_pdl(k_pack16, dim3(grid_for(a.rows * a.cols, sm)), dim3(256), 0, ws.s, (const uint16_t*)a.p, a.sr, a.sc,
+                         a.rows, a.cols, (uint16_t*)p, ld, span);
+    if (e != cudaSuccess) return cuda_error(e, "operand packing launch");
     count_launches(1);
     *out = {(const uint16_t*)p, a.rows, a.cols, ld};
     return TROP_OK;

@@ -76,7 +76,8 @@ def main() -> int:
             near(f"dw {n}x{d}x{v} {dt} {red}", dw, wr.grad, 2e-2)
 
     for dt in (B, H):
-        for n, d, v in ((2, 8, 3), (5, 64, 300), (128, 72, 1000), (129, 65, 257), (300, 512, 2050), (70, 2100, 700), (260, 2100, 300)):
+        for n, d, v in ((2, 8, 3), (5, 64, 300), (128, 72, 1000), (129, 65, 257), (300, 512, 2050), (70, 2100, 700), (260, 2100, 300),
+                        (37, 1031, 300)):
             loss(n, d, v, dt)
         loss(20, 64, 100, dt, shift=3)
 
