@@ -1204,10 +1204,10 @@ int norm_forward(const NormJob& j, int sm, cudaStream_t s)
     if constexpr (std::is_same<TX, TY>::value) {
         const int period = vec ? 0 : offset_period(sizeof(TX), j.rows, {{j.x, j.sx}, {j.y, j.sy}});
         const int64_t vecs = (j.cols + V - 1) / V + 1;
+        const int nv = vecs <= 32 ? 1 : vecs <= 64 ? 2 : 4;
+        const int64_t g = ((vecs + nv - 1) / nv + 31) / 32 * 32;
         // f32 rows of more than a warp: the scalar kernel's 16 loads a thread win (16384x4093 139 us, here 166 us)
-        if (period > 0 && vecs <= (sizeof(TX) == 2 ? 2048 : 128) && j.rows >= (int64_t)sm * 16) {
-            const int nv = vecs <= 32 ? 1 : vecs <= 64 ? 2 : 4;
-            const int64_t g = ((vecs + nv - 1) / nv + 31) / 32 * 32;
+        if (period > 0 && vecs <= (sizeof(TX) == 2 ? 2048 : 128) && j.rows * (g / 32) >= (int64_t)sm * 16) {
             const dim3 block((unsigned)g, g == 32 ? 8 : 1);
             const size_t smem = 2 * (size_t)(j.cols + 2 * V) * sizeof(TW);
             const auto kernel = nv == 1   ? k_norm_off<TX, TW, V, 1, 4>

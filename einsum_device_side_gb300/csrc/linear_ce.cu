@@ -697,14 +697,36 @@ __global__ void __launch_bounds__(256) k_split_join(const float* acc, int ks, in
 }
 
 // ------------------------------------------------------------------ operands that TMA cannot read
-// Rows of consecutive elements that start or repeat off 16 bytes: a warp per row, 4-byte words.  A row that
-// starts inside a word shifts two of them together; a word that reaches outside the matrix is read by halves.
+// The copy of one operand, or of both: rows of consecutive elements by a warp each, in 4-byte words (a row
+// that starts inside a word shifts two of them together; a word that reaches outside the matrix is read by
+// halves), any other strides an element at a time.  60000x2049: 92 us, 5.3 TB/s; by elements 285 us.
+struct Pack {
+    const uint16_t* in;
+    int64_t sr, sc, rows, cols;
+    uint16_t* out;
+    int64_t ld;
+    Span sp;
+};
 constexpr int PACK_WORDS = 8;  // of a thread at once: 64 warps then have 64 KB of an SM on their way
-__global__ void __launch_bounds__(256) k_pack_rows(const uint16_t* in, int64_t sr, int64_t rows, int64_t cols, uint16_t* out,
-                                                   int64_t ld, Span sp_in)
+__global__ void __launch_bounds__(256) k_pack(const Pack first, const Pack second)
 {
     pdl_wait();
     pdl_signal();
+    const Pack& a = blockIdx.y ? second : first;
+    const uint16_t* const in = a.in;
+    uint16_t* const out = a.out;
+    const int64_t sr = a.sr, rows = a.rows, cols = a.cols, ld = a.ld;
+    const Span& sp_in = a.sp;
+    (void)sp_in;
+    if (a.sc != 1 || sr < 0) {
+        const int64_t n = rows * cols, sc = a.sc;
+        for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.y * 32 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+            const int64_t r = i / cols, c = i % cols;
+            const uint16_t* p = in + r * sr + c * sc;
+            out[r * ld + c] = TROP_IN(p, 2, sp_in) ? *p : (uint16_t)0;
+        }
+        return;
+    }
     const uint16_t* const end = in + (rows - 1) * sr + cols;
     const int64_t words = (cols + 1) / 2;
     for (int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.y; r < rows; r += (int64_t)gridDim.x * 8) {
@@ -713,8 +735,8 @@ __global__ void __launch_bounds__(256) k_pack_rows(const uint16_t* in, int64_t s
         const int odd = ((uintptr_t)row & 2) != 0;
         for (int64_t at = threadIdx.x; at < words; at += 32 * PACK_WORDS) {
             uint32_t lo[PACK_WORDS], hi[PACK_WORDS];
-            const int64_t first = at - threadIdx.x;
-            if (first + 32 * PACK_WORDS < words && (row > in || first > 0)) {  // nothing reaches outside
+            const int64_t begin = at - threadIdx.x;
+            if (begin + 32 * PACK_WORDS < words && (row > in || begin > 0)) {  // nothing reaches outside
                 const uint32_t* const src = reinterpret_cast<const uint32_t*>(row - odd) + at;
 #pragma unroll
                 for (int u = 0; u < PACK_WORDS; ++u) {
@@ -750,19 +772,6 @@ __global__ void __launch_bounds__(256) k_pack_rows(const uint16_t* in, int64_t s
                 to[w] = 2 * w + 1 < cols ? v : v & 0xffffu;
             }
         }
-    }
-}
-// Any strides, an element at a time.
-__global__ void __launch_bounds__(256) k_pack16(const uint16_t* in, int64_t sr, int64_t sc, int64_t rows, int64_t cols,
-                                                uint16_t* out, int64_t ld, Span sp_in)
-{
-    pdl_wait();
-    pdl_signal();
-    const int64_t n = rows * cols;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / cols, c = i % cols;
-        const uint16_t* p = in + r * sr + c * sc;
-        out[r * ld + c] = TROP_IN(p, 2, sp_in) ? *p : (uint16_t)0;
     }
 }
 __global__ void __launch_bounds__(256) k_zero16(uint16_t* out, int64_t sr, int64_t rows, int64_t cols, Span sp)
@@ -828,50 +837,73 @@ struct Matrix16 {
     int64_t rows, cols, ld;
 };
 
-// Workspace blocks of one call, given back in any case.
-struct Blocks {
+// A call's workspace: one block of parts, from what the stream keeps where that serves, else from the pool and
+// given back in any case.  Every call takes one at most: a second would be the same memory.
+struct Workspace {
     cudaStream_t s;
-    void* p[8];
-    int n = 0;
-    explicit Blocks(cudaStream_t st) : s(st) {}
-    ~Blocks()
+    size_t bytes = 0;
+    char* base = nullptr;
+    void* own = nullptr;
+    explicit Workspace(cudaStream_t st) : s(st) {}
+    ~Workspace()
     {
-        for (int i = 0; i < n; ++i) pool_retire(p[i], s);
+        if (own) pool_retire(own, s);
     }
-    // the call's one small block, from what the stream keeps where that serves
-    int small(size_t bytes, void** out) { return stream_scratch(bytes, s, out) ? (int)TROP_OK : get(bytes, out); }
-    int get(size_t bytes, void** out)
+    size_t add(size_t n)  // a part's offset
     {
-        TROP_TRY(pool_alloc(bytes, s, out));
-        p[n++] = *out;
+        const size_t at = bytes;
+        bytes += (n + 255) / 256 * 256;
+        return at;
+    }
+    int take()
+    {
+        void* p = nullptr;
+        if (bytes && !stream_scratch(bytes, s, &p)) {
+            TROP_TRY(pool_alloc(bytes, s, &p));
+            own = p;
+        }
+        base = (char*)p;
         return TROP_OK;
     }
 };
 
 int grid_for(int64_t n, int sm) { return (int)std::min<int64_t>((n + 255) / 256, (int64_t)sm * 8); }
 
-// The operand as TMA can read it: itself, or a packed copy.
-int readable(const Mat16& a, int sm, Blocks& ws, Matrix16* out)
+// The operands as TMA can read them: themselves, or packed copies, both made by one launch.
+struct Operand {
+    Matrix16 m;
+    const Mat16& a;
+    size_t at = 0;
+    bool packed = false;
+    Operand(const Mat16& a_, Workspace& ws) : m{(const uint16_t*)a_.p, a_.rows, a_.cols, a_.sr}, a(a_)
+    {
+        if (a.rows == 1) m.ld = (a.cols + 7) / 8 * 8;  // no second row: any pitch
+        packed = !((a.sc == 1 || a.cols == 1) && m.ld % 8 == 0 && m.ld >= a.cols && m.ld < (int64_t)1 << 38 &&
+                   ((uintptr_t)a.p & 15) == 0);
+        if (!packed) return;
+        m.ld = (a.cols + 7) / 8 * 8;
+        at = ws.add((size_t)a.rows * m.ld * 2);
+    }
+    Pack job() const
+    {
+        const int64_t size[2] = {a.rows, a.cols}, stride[2] = {a.sr, a.sc};
+        const Span sp = span_of(a.p, 2, 2, size, stride);
+        return {(const uint16_t*)a.p, a.sr, a.sc, a.rows, a.cols, const_cast<uint16_t*>(m.p), m.ld, sp};
+    }
+};
+int pack(Operand& x, Operand& w, const Workspace& ws, int sm)
 {
-    *out = {(const uint16_t*)a.p, a.rows, a.cols, a.sr};
-    if (a.rows == 1) out->ld = (a.cols + 7) / 8 * 8;  // no second row: any pitch
-    if ((a.sc == 1 || a.cols == 1) && out->ld % 8 == 0 && out->ld >= a.cols && out->ld < (int64_t)1 << 38 &&
-        ((uintptr_t)a.p & 15) == 0)
-        return TROP_OK;
-    const int64_t ld = (a.cols + 7) / 8 * 8;
-    void* p;
-    TROP_TRY(ws.get((size_t)a.rows * ld * 2, &p));
-    const int64_t size[2] = {a.rows, a.cols}, stride[2] = {a.sr, a.sc};
-    const Span span = span_of(a.p, 2, 2, size, stride);
-    const dim3 by_rows((unsigned)std::min<int64_t>((a.rows + 7) / 8, (int64_t)sm * 8));
-    const cudaError_t e =
-        a.sc == 1 && a.sr >= 0
-            ? launch_pdl(k_pack_rows, by_rows, dim3(32, 8), 0, ws.s, (const uint16_t*)a.p, a.sr, a.rows, a.cols, (uint16_t*)p, ld, span)
-            : launch_pdl(k_pack16, dim3(grid_for(a.rows * a.cols, sm)), dim3(256), 0, ws.s, (const uint16_t*)a.p, a.sr, a.sc,
-                         a.rows, a.cols, (uint16_t*)p, ld, span);
-    if (e != cudaSuccess) return cuda_error(e, "operand packing launch");
+    int64_t blocks = 0;
+    for (Operand* o : {&x, &w})
+        if (o->packed) {
+            o->m.p = (const uint16_t*)(ws.base + o->at);
+            blocks = std::max(blocks, (o->a.rows + 7) / 8);
+        }
+    if (blocks == 0) return TROP_OK;
+    const dim3 grid((unsigned)std::min<int64_t>(blocks, (int64_t)sm * 8), x.packed && w.packed ? 2 : 1);
+    const cudaError_t e = launch_pdl(k_pack, grid, dim3(32, 8), 0, ws.s, (x.packed ? x : w).job(), w.job());
+    if (e != cudaSuccess) return cuda_error(e, "k_pack launch");
     count_launches(1);
-    *out = {(const uint16_t*)p, a.rows, a.cols, ld};
     return TROP_OK;
 }
 
@@ -960,7 +992,7 @@ int launch_linear_ce(const LinearCe& q, float* loss, float* lse, float* total, f
     const DeviceInfo* dev;
     TROP_TRY(ensure_device(&dev));
     const int sm = dev->sm_count;
-    Blocks ws(s);
+    Workspace ws(s);
     JoinJob t = {};
     t.rows = q.x.rows;
     t.tgt = targets_of(q);
@@ -975,14 +1007,13 @@ int launch_linear_ce(const LinearCe& q, float* loss, float* lse, float* total, f
     t.sp_kept = span_bytes(t.kept, 4);
     TROP_TRY(stream_tickets(s, 1, &t.ticket));
     const size_t sums = (size_t)std::max(1, cdiv(t.rows, 32)) * sizeof(float2);
-    void* p;
+    const size_t at_sums = ws.add(sums);
     if (t.rows == 0) {
-        TROP_TRY(ws.small(sums, &p));
-        return launch_join(t, (float2*)p, s);
+        TROP_TRY(ws.take());
+        return launch_join(t, (float2*)(ws.base + at_sums), s);
     }
-    Matrix16 x, w;
-    TROP_TRY(readable(q.x, sm, ws, &x));
-    TROP_TRY(readable(q.w, sm, ws, &w));
+    Operand ox(q.x, ws), ow(q.w, ws);
+    const Matrix16 &x = ox.m, &w = ow.m;
     const bool few = x.rows <= FEW_TOKENS;
     const int type = q.bf16 ? TROP_BF16 : TROP_F16;
     const int TM = few ? Few::TM : Pair::TM, TN = few ? Few::TN : Pair::TN, CG = few ? 1 : 2;
@@ -1007,9 +1038,11 @@ int launch_linear_ce(const LinearCe& q, float* loss, float* lse, float* total, f
     t.stride = (int64_t)j.mt * TM;
     t.G = 2 * groups;
     const size_t pairs = (size_t)t.G * t.stride * sizeof(float2), at = (size_t)(x.rows + 63) / 64 * 64 * 4;
-    TROP_TRY(ws.small(pairs + at + sums, &p));
-    t.part = j.part = (float2*)p;
-    t.at = j.at = (float*)((char*)p + pairs);
+    const size_t at_part = ws.add(pairs), at_logit = ws.add(at);
+    TROP_TRY(ws.take());
+    TROP_TRY(pack(ox, ow, ws, sm));
+    t.part = j.part = (float2*)(ws.base + at_part);
+    t.at = j.at = (float*)(ws.base + at_logit);
     t.sp_part = j.sp_part = span_bytes(j.part, pairs);
     t.sp_at = j.sp_at = span_bytes(j.at, (size_t)x.rows * 4);
     const int a_rows = few ? few_rows(x.rows) : 128;
@@ -1020,7 +1053,39 @@ int launch_linear_ce(const LinearCe& q, float* loss, float* lse, float* total, f
     if (few) return launch_tile<LSE, Few>(q.bf16, ma, mb, ma, j, sm, s, t);
     TROP_TRY((x.cols > DEEP_LOGITS ? launch_tile<LSE, Deep>(q.bf16, ma, mb, ma, j, sm, s)
                                    : launch_tile<LSE, Pair>(q.bf16, ma, mb, ma, j, sm, s)));
-    return launch_join(t, (float2*)((char*)p + pairs + at), s);
+    return launch_join(t, (float2*)(ws.base + at_sums), s);
+}
+
+// Splits of a product's depth of kt stages: the fewest rounds of stages, each split costing about the time of
+// 8 stages more for its partial sums of `bytes` (1 GiB of them at most).  dw of 8192x128x256, one tile of 128
+// stages, takes 64 splits: the whole backward pass 30 us, without splits 55 us.
+int splits(int tiles, int kt, int teams, int64_t bytes)
+{
+    int ks = 1;
+    int64_t best = INT64_MAX;
+    for (int c = 1; c <= std::min(kt, 64); ++c) {
+        const int per = cdiv(kt, c);
+        if (cdiv(kt, per) != c) continue;
+        if (c > 1 && c * bytes > (int64_t)1 << 30) break;
+        const int64_t cost = (int64_t)cdiv((int64_t)tiles * c, teams) * (per + (c > 1 ? 8 : 0));
+        if (cost < best) best = cost, ks = c;
+    }
+    return ks;
+}
+// The splits' f32 sums [ks][slab rows][lda], added in order, into rows of 16-bit elements.
+int launch_split_join(bool bf16, const float* acc, int ks, int64_t slab, int64_t lda, int64_t rows, int64_t D, uint16_t* out,
+                      int64_t ldo, const GradScale& grad, int sm, cudaStream_t s)
+{
+    const int64_t size[2] = {rows, D}, stride[2] = {ldo, 1};
+    const Span sp_out = span_of(out, 2, 2, size, stride), sp_acc = span_bytes(acc, (size_t)ks * slab * lda * 4);
+    const bool vec = D % 4 == 0 && ldo % 4 == 0 && ((uintptr_t)out & 7) == 0;
+    const auto kernel = bf16 ? (vec ? k_split_join<true, true> : k_split_join<true, false>)
+                             : (vec ? k_split_join<false, true> : k_split_join<false, false>);
+    const cudaError_t e = launch_pdl(kernel, dim3(grid_for(rows * D / (vec ? 4 : 1), sm)), dim3(256), 0, s, acc, ks, slab * lda, lda,
+                                     rows, D, out, ldo, grad, sp_acc, sp_out);
+    if (e != cudaSuccess) return cuda_error(e, "k_split_join launch");
+    count_launches(1);
+    return TROP_OK;
 }
 
 int launch_linear_ce_backward(const LinearCe& q, const float* g, int64_t sg, const float* lse, const float* kept,
@@ -1034,45 +1099,39 @@ int launch_linear_ce_backward(const LinearCe& q, const float* g, int64_t sg, con
     const int TM = few ? Few1::TM : Pair::TM, TN = few ? Few1::TN : Pair::TN;  // of the logits and of dx
     const int sm = dev->sm_count, teams = few ? sm : sm / 2;
     const int a_rows = few ? few_rows(N) : 128;
-    Blocks ws(s);
-    Matrix16 x, w;
-    TROP_TRY(readable(q.x, sm, ws, &x));
-    TROP_TRY(readable(q.w, sm, ws, &w));
+    Workspace ws(s);
+    Operand ox(q.x, ws), ow(q.w, ws);
+    const Matrix16 &x = ox.m, &w = ow.m;
 
     // A piece of the vocabulary: P takes at most 512 MiB (and at least 4096 columns).
     const int64_t whole = (V + 255) / 256 * 256;
     int64_t piece = ((int64_t)1 << 28) / N / 256 * 256;
     piece = std::min(whole, std::max<int64_t>(piece, 4096));
     const int pieces = cdiv(V, piece);
-    // Splits of dx's depth (a piece's columns): the fewest rounds of stages, each split costing about
-    // the time of 8 stages more for its partial sums.
     const int dx_mt = cdiv(N, TM), dx_nt = cdiv(D, TN), dx_kt = cdiv(std::min(piece, V), TK);
-    int ks = 1;
-    if (dx) {
-        int64_t best = INT64_MAX;
-        for (int c = 1; c <= std::min(dx_kt, 64); ++c) {
-            const int per = cdiv(dx_kt, c);
-            if (cdiv(dx_kt, per) != c) continue;
-            if (c > 1 && c * N * D * 4 > (int64_t)1 << 30) break;  // 1 GiB of partial sums
-            const int64_t cost = (int64_t)cdiv((int64_t)dx_mt * dx_nt * c, teams) * (per + (c > 1 ? 8 : 0));
-            if (cost < best) best = cost, ks = c;
-        }
-    }
+    const int dw_mt = cdiv(std::min(piece, V), Pair::TM), dw_nt = cdiv(D, Pair::TN), dw_kt = cdiv(N, TK);
+    const int ks = dx ? splits(dx_mt * dx_nt, dx_kt, teams, N * D * 4) : 1;
+    const int ks_w = dw ? splits(dw_mt * dw_nt, dw_kt, sm / 2, std::min(piece, V) * D * 4) : 1;
     const size_t p_bytes = (size_t)N * piece * 2;
     const bool summed = dx && (ks > 1 || pieces > 1);  // f32 sums, [ks][pad_rows][lda]
     const int64_t lda = (D + 3) / 4 * 4, pad_rows = (N + 31) / 32 * 32;
     const size_t acc_bytes = summed ? (size_t)ks * pad_rows * lda * 4 : 0;
-    void *P, *acc = nullptr, *scale = nullptr;
-    TROP_TRY(ws.get(p_bytes, &P));
-    if (summed) TROP_TRY(ws.get(acc_bytes, &acc));
+    const int64_t pad_cols = (std::min(piece, V) + 31) / 32 * 32;
+    const size_t accw_bytes = ks_w > 1 ? (size_t)ks_w * pad_cols * lda * 4 : 0;
+    const size_t at_p = ws.add(p_bytes), at_acc = ws.add(acc_bytes), at_accw = ws.add(accw_bytes), at_scale = ws.add(8);
+    TROP_TRY(ws.take());
+    TROP_TRY(pack(ox, ow, ws, sm));
+    void* const P = ws.base + at_p;
+    float* const acc = (float*)(ws.base + at_acc);
+    float* const accw = (float*)(ws.base + at_accw);
+    float* const scale = (float*)(ws.base + at_scale);
     const int64_t gsize[1] = {N}, gstride[1] = {sg};
     GradScale grad = {g, sg, kept, nullptr, q.bf16 ? 1.f : 16384.f, span_of(g, 4, 1, gsize, gstride)};
     if (sg != 0) {
-        TROP_TRY(ws.small(8, &scale));
-        const cudaError_t e = launch_pdl(k_gscale, dim3(1), dim3(1024), 0, s, grad, N, (float*)scale);
+        const cudaError_t e = launch_pdl(k_gscale, dim3(1), dim3(1024), 0, s, grad, N, scale);
         if (e != cudaSuccess) return cuda_error(e, "k_gscale launch");
         count_launches(1);
-        grad.given = (const float*)scale;
+        grad.given = scale;
     }
     CUtensorMap x_k, w_k, x_mn, w_mn, p_k, p_mn, c;
     TROP_TRY(make_map(&x_k, type, x.p, D, N, x.ld, a_rows));
@@ -1111,17 +1170,25 @@ int launch_linear_ce_backward(const LinearCe& q, const float* g, int64_t sg, con
             t.rows = (int)cols;
             t.cols = (int)D;
             t.mt = cdiv(cols, Pair::TM);
-            t.nt = cdiv(D, Pair::TN);
-            t.kt = t.kper = cdiv(N, TK);
+            t.nt = dw_nt;
+            t.kt = dw_kt;
+            t.kper = cdiv(dw_kt, ks_w);
             t.a_bytes = A_BYTES;
-            t.units = t.mt * t.nt;
-            t.out = (uint16_t*)dw->p + v0 * dw->sr;
-            t.ldo = dw->sr;
-            t.vec = ((uintptr_t)t.out & 15) == 0 && dw->sr % 8 == 0;
-            const int64_t size[2] = {cols, D}, stride[2] = {dw->sr, 1};
-            t.sp_out = span_of(t.out, 2, 2, size, stride);
-            if (t.vec) TROP_TRY(make_map(&c, type, t.out, D, cols, t.ldo, 32));
-            TROP_TRY((launch_tile<DW, Pair>(q.bf16, p_mn, x_mn, t.vec ? c : p_mn, t, sm, s)));
+            t.units = t.mt * t.nt * ks_w;
+            uint16_t* const out = (uint16_t*)dw->p + v0 * dw->sr;
+            if (ks_w > 1) {
+                t.pad_rows = (int)pad_cols;
+                TROP_TRY(make_map(&c, TROP_F32, accw, D, ks_w * pad_cols, lda, 32));
+            } else {
+                t.out = out;
+                t.ldo = dw->sr;
+                t.vec = ((uintptr_t)t.out & 15) == 0 && dw->sr % 8 == 0;
+                const int64_t size[2] = {cols, D}, stride[2] = {dw->sr, 1};
+                t.sp_out = span_of(t.out, 2, 2, size, stride);
+                if (t.vec) TROP_TRY(make_map(&c, type, t.out, D, cols, t.ldo, 32));
+            }
+            TROP_TRY((launch_tile<DW, Pair>(q.bf16, p_mn, x_mn, ks_w > 1 || t.vec ? c : p_mn, t, sm, s)));
+            if (ks_w > 1) TROP_TRY(launch_split_join(q.bf16, accw, ks_w, pad_cols, lda, cols, D, out, dw->sr, grad, sm, s));
         }
         if (dx) {
             Job t = j;
@@ -1150,17 +1217,7 @@ int launch_linear_ce_backward(const LinearCe& q, const float* g, int64_t sg, con
                            : launch_tile<DX, Pair>(q.bf16, p_k, w_mn, to, t, sm, s)));
         }
     }
-    if (summed) {
-        const int64_t size[2] = {N, D}, stride[2] = {dx->sr, 1};
-        const Span sp_out = span_of(dx->p, 2, 2, size, stride), sp_acc = span_bytes(acc, acc_bytes);
-        const bool vec = D % 4 == 0 && dx->sr % 4 == 0 && ((uintptr_t)dx->p & 7) == 0;
-        const auto kernel = q.bf16 ? (vec ? k_split_join<true, true> : k_split_join<true, false>)
-                                   : (vec ? k_split_join<false, true> : k_split_join<false, false>);
-        const cudaError_t e = launch_pdl(kernel, dim3(grid_for(N * D / (vec ? 4 : 1), sm)), dim3(256), 0, s, (const float*)acc,
-                                         ks, pad_rows * lda, lda, N, D, (uint16_t*)dx->p, dx->sr, grad, sp_acc, sp_out);
-        if (e != cudaSuccess) return cuda_error(e, "k_split_join launch");
-        count_launches(1);
-    }
+    if (summed) TROP_TRY(launch_split_join(q.bf16, acc, ks, pad_rows, lda, N, D, (uint16_t*)dx->p, dx->sr, grad, sm, s));
     return TROP_OK;
 }
 

@@ -295,7 +295,8 @@ def _logit_error(x, w):
 
 HEAD_SIZES = [(1, 8, 1), (1, 8, 2), (1, 64, 300), (2, 7, 5), (4, 64, 256), (127, 64, 255), (128, 72, 256), (129, 100, 257),
               (255, 8, 513), (256, 256, 256), (257, 65, 1000), (300, 513, 77), (33, 1000, 2049), (600, 40, 5003), (16, 2048, 4096),
-              (37, 1031, 515), (140, 2049, 300)]  # (long rows at every offset)
+              (37, 1031, 515), (140, 2049, 300),  # (long rows at every offset)
+              (2100, 72, 300), (1999, 65, 130)]  # (dw's tokens split)
 
 
 @pytest.mark.parametrize("dt", [B, H])
