@@ -18,6 +18,11 @@
 // single call's tensor table travels in the kernel's parameters, where a block finds its tensor by
 // bisection; that of a plan of many tensors lies in device memory with each block's tensor written
 // down, because a launch with 30 KB of parameters takes the host about 8 us instead of 2.
+//
+// Measured, 2^27 f32 elements in 96 tensors: 32-bit states 532 us, 7.1 TB/s; 8-bit states 632 us with the
+// states' values read back (2^25 elements: the step 119 us, 73 % of the issue slots: the codes' arithmetic, about
+// 85 instructions an element and thread, bounds it before memory does).  Twelve small tensors: 4.7 us, the
+// launch.  4096 elements a block: 16 of each array a thread, all loads on their way before the first is used.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -1191,6 +1191,7 @@ int norm_forward(const NormJob& j, int sm, cudaStream_t s)
                      aligned(j.y, j.sy, sizeof(TY), V, j.rows) && aligned(j.w, 0, sizeof(TW), V, 1) &&
                      aligned(j.b, 0, sizeof(TW), V, 1);
     const int64_t units = j.cols / V;
+    // many short rows (65536x512 f32: 46 us, a warp per row and one row at a time 81 us; bf16 26 us and 50 us)
     if (vec && units <= 128 && j.rows >= (int64_t)sm * 16) {
         const int nv = units <= 32 ? 1 : units <= 64 ? 2 : 4;
         const dim3 block(32, 8);
@@ -1291,11 +1292,11 @@ int norm_backward(NormJob j, const NormVec& dw, const NormVec& db, int sm, cudaS
         off_per_sm = std::min<int64_t>(1024 / off_g, 220000 / (off_g * 16 * (8 + sizeof(TW))));
     }
     const dim3 off_block((unsigned)off_g, off_g == 32 ? 4 : 1);  // (a wide block has one group: off_g >= 64)
-    // rows of x and dy that bulk copies can bring, enough of them to fill a ring
     const size_t pair = j.cols * (sizeof(TX) + sizeof(TY));
     const int per_sm = block.x > 256 ? 1 : std::max<int>(2, 512 / (int)block.x);  // blocks that share an SM
     const int stages = (int)std::min<size_t>(RING_STAGES, RING_BYTES / per_sm / pair);
-    // rows of x and dy that bulk copies can bring (16-byte granules), and enough of them to fill a ring
+    // Rows of x and dy that bulk copies can bring (16-byte granules), and enough of them to fill a ring:
+    // 16384x4096 bf16 69 us, loaded by the threads themselves 129 us; f32 130 us and 138 us.
     const bool ring = fits && vec && block.y == 1 && block.x >= 64 && block.x <= 512 && j.cols * sizeof(TY) % 16 == 0 &&
                       aligned(j.dy, j.sdy * sizeof(TY), 1, 16, j.rows) && j.rows >= 4 * sm && stages >= 2;
     int blocks = 0;

@@ -20,6 +20,15 @@
 //   DW    P^T x: the piece's rows of dw, whole
 // Operand tiles come by TMA into a ring of 128-byte-swizzled stages; one thread issues the
 // products, eight warps empty one accumulator while the next one fills.
+//
+// Tiles of 256 x 256 by pairs of CTAs: each CTA loads half of each operand tile, so that a stage's 64 KB feed
+// twice the products of a CTA alone (8192x2048x65536 forward: CTAs alone 1433 us, pairs 1265 us).  The largest
+// cases are bound by the tensor cores at the clock that the power limit leaves them, small ones by the chain of
+// launches, few tokens by reading the weights (measured, bf16):
+//   8192x2048x65536   forward 1265 us, 1738 TFLOP/s; backward 3960 us, 1666 TFLOP/s of the three products
+//   16x4096x131072    forward 178 us, 6.0 TB/s; backward 570 us
+//   1021x1000x32003   forward 52 us, backward 169 us
+//   16x512x2000       forward 18 us, backward 24 us
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -62,7 +71,7 @@ template <int MODE, typename S>
 constexpr int smem_bytes() { return S::RING + (MODE == LSE ? 0 : EPI_WARPS * BOX_BYTES) + 1024; }
 using Pair = Shape<2, 256, 1>;   // products bound by the tensor cores
 using Deep = Shape<2, 256, 2>;   // long logits: half the depth per accumulator
-// Up to 128 tokens: bound by reading the weights, in two slices at a time so that a row's 256 bytes are
+// Few tokens: bound by reading the weights, in two slices at a time so that a row's 256 bytes are
 // asked for together (16x4096x131072: one slice 181 us, two 178 us, three 185 us).
 using Few = Shape<1, 128, 2, 2>;
 using Few1 = Shape<1, 128, 1>;
@@ -307,50 +316,48 @@ __device__ __forceinline__ void join_pair(float& M, float& s, float2 q)
     s = s * pow2_whole(M - m) + q.y * pow2_whole(q.x - m);
     M = m;
 }
-// 32 rows by WARPS warps, each row's pairs in one order whatever runs when: {sum of their losses, rows
-// kept} in every lane of warp 0.
-template <int WARPS>
-__device__ __forceinline__ float2 join_rows(const JoinJob& j, int64_t row0, float2 (*sh)[33])
+// 32 rows' pairs shared out to `parts` warps: the lane's row, its pairs part, part + parts, ... in that order.
+__device__ __forceinline__ float2 join_part(const JoinJob& j, int64_t row, int part, int parts)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t row = row0 + lane;
     float M = NO_MAX, s = 0.f;
     if (row < j.rows) {
-        int g = warp;
-        for (; g + 3 * WARPS < j.G; g += 4 * WARPS) {  // four loads on their way
+        int g = part;
+        for (; g + 3 * parts < j.G; g += 4 * parts) {  // four loads on their way
             float2 q[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float2* p = j.part + (int64_t)(g + k * WARPS) * j.stride + row;
+                const float2* p = j.part + (int64_t)(g + k * parts) * j.stride + row;
                 q[k] = TROP_IN(p, 8, j.sp_part) ? __ldcg(p) : make_float2(NO_MAX, 0.f);
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) join_pair(M, s, q[k]);
         }
-        for (; g < j.G; g += WARPS) {
+        for (; g < j.G; g += parts) {
             const float2* p = j.part + (int64_t)g * j.stride + row;
             if (TROP_IN(p, 8, j.sp_part)) join_pair(M, s, __ldcg(p));
         }
     }
-    sh[warp][lane] = make_float2(M, s);
-    __syncthreads();
-    float loss = 0.f, keep = 0.f;
-    if (warp == 0) {
-        for (int w = 1; w < WARPS; ++w) join_pair(M, s, sh[w][lane]);
-        if (row < j.rows) {
-            // M is a whole number of powers of two: M ln 2 + log s in two pieces of ln 2
-            const float lse = __fmaf_rn(M, LN2, __fmaf_rn(M, -1.9046542121259335e-09f, logf(s)));
-            const int64_t t = target_of(j.tgt, row);
-            if (TROP_IN(j.lse + row, 4, j.sp_lse)) j.lse[row] = lse;
-            if (t >= 0 && TROP_IN(j.at + row, 4, j.sp_at)) loss = lse - __ldcg(j.at + row);
-            if (t == -2) loss = NAN;
-            keep = t == -1 ? 0.f : 1.f;
-            if (j.loss && TROP_IN(j.loss + row, 4, j.sp_loss)) j.loss[row] = loss;
-        }
-        for (int o = 16; o > 0; o >>= 1) {
-            loss += __shfl_xor_sync(0xffffffffu, loss, o);
-            keep += __shfl_xor_sync(0xffffffffu, keep, o);
-        }
+    return make_float2(M, s);
+}
+// The parts' pairs of 32 rows, joined in part order by one warp; {sum of the rows' losses, rows kept} in every lane.
+__device__ __forceinline__ float2 join_rows(const JoinJob& j, int64_t row, const float2 (*sh)[33], int parts)
+{
+    const int lane = threadIdx.x & 31;
+    float M = NO_MAX, s = 0.f, loss = 0.f, keep = 0.f;
+    for (int w = 0; w < parts; ++w) join_pair(M, s, sh[w][lane]);
+    if (row < j.rows) {
+        // M is a whole number of powers of two: M ln 2 + log s in two pieces of ln 2
+        const float lse = __fmaf_rn(M, LN2, __fmaf_rn(M, -1.9046542121259335e-09f, logf(s)));
+        const int64_t t = target_of(j.tgt, row);
+        if (TROP_IN(j.lse + row, 4, j.sp_lse)) j.lse[row] = lse;
+        if (t >= 0 && TROP_IN(j.at + row, 4, j.sp_at)) loss = lse - __ldcg(j.at + row);
+        if (t == -2) loss = NAN;
+        keep = t == -1 ? 0.f : 1.f;
+        if (j.loss && TROP_IN(j.loss + row, 4, j.sp_loss)) j.loss[row] = loss;
+    }
+    for (int o = 16; o > 0; o >>= 1) {
+        loss += __shfl_xor_sync(0xffffffffu, loss, o);
+        keep += __shfl_xor_sync(0xffffffffu, keep, o);
     }
     return make_float2(loss, keep);
 }
@@ -370,11 +377,16 @@ __global__ void __launch_bounds__(256) k_lse_join(const __grid_constant__ JoinJo
     __shared__ float red[2][32];
     __shared__ bool last;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const float2 mine = join_rows<8>(j, (int64_t)blockIdx.x * 32, sh);
-    if (threadIdx.x == 0) {
-        j.sums[blockIdx.x] = mine;
-        __threadfence();
-        last = atomicAdd(j.ticket, 1u) == gridDim.x - 1;
+    const int64_t row = (int64_t)blockIdx.x * 32 + lane;
+    sh[warp][lane] = join_part(j, row, warp, 8);
+    __syncthreads();
+    if (warp == 0) {
+        const float2 mine = join_rows(j, row, sh, 8);
+        if (lane == 0) {
+            j.sums[blockIdx.x] = mine;
+            __threadfence();
+            last = atomicAdd(j.ticket, 1u) == gridDim.x - 1;
+        }
     }
     __syncthreads();
     if (!last) return;
@@ -626,13 +638,18 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncthreads();
         if (arrived != gridDim.x - 1) return;
         __threadfence();
-        float loss = 0.f, keep = 0.f;
-        for (int64_t row0 = 0; row0 < join.rows; row0 += 32) {
-            const float2 q = join_rows<THREADS / 32>(join, row0, sh);
-            loss += q.x;
-            keep += q.y;
-            __syncthreads();
+        // 32 rows to a group of warps, all groups at once
+        __shared__ float2 red[THREADS / 32];
+        const int groups = (int)((join.rows + 31) / 32), parts = THREADS / 32 / groups, group = warp / parts;
+        if (group < groups) sh[warp][lane] = join_part(join, group * 32 + lane, warp % parts, parts);
+        __syncthreads();
+        if (warp < groups) {
+            const float2 q = join_rows(join, warp * 32 + lane, sh + warp * parts, parts);
+            if (lane == 0) red[warp] = q;
         }
+        __syncthreads();
+        float loss = 0.f, keep = 0.f;
+        for (int w = 0; w < groups; ++w) loss += red[w].x, keep += red[w].y;
         if (threadIdx.x == 0) {
             join_total(join, loss, keep);
             *join.ticket = 0;
@@ -939,10 +956,14 @@ int launch_tile(bool bf16, const CUtensorMap& a, const CUtensorMap& b, const CUt
 // Row tiles of a band: as many as keep their operand (a row tile's whole depth) in about 48 MB of
 // the L2, so that the other operand is read from memory once per band.  8192x2048x65536: all 32 row
 // tiles (33 MB) 1269 us, bands of 16 / 12 / 8 / 4 1293 / 1305 / 1330 / 1378 us.
-// Up to this many tokens one row tile of one CTA holds them all, and reading the weights is the work.
+// Up to this many tokens one row tile of one CTA holds them all, and reading the weights is the work.  Forward
+// against pairs of CTAs and a join of its own: 8 tokens x 4096 x 65536 92 us and 145 us; 64 x 512 x 8000 18 us and
+// 20.5 us; 64 x 2048 x 32000 32.5 us and 34.7 us; at 128 tokens 36.6 us and 34.4 us there, 17.4 us and 20.8 us with 512 x
+// 8000.  Backward, 128x4096x131072: 647 us and 658 us.
 constexpr int64_t FEW_TOKENS = 128;
 // A logit's sum loses up to a last place of its accumulator every 16 products; past this depth two
-// accumulators share it.
+// accumulators share it, which leaves no room for a second tile.  Logits of 4096 products: relative error of
+// lse 2.2e-7 (8192x4096x32768 in 1324 us), in one accumulator 4.4e-7 (1284 us).
 constexpr int64_t DEEP_LOGITS = 2048;
 // Rows of such a tile's box: the tokens' only.  The tile's other rows keep what shared memory holds,
 // and so do the accumulator's, which nobody reads.
