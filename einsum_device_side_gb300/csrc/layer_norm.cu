@@ -28,7 +28,7 @@
 //   16384x4096  bf16                                  50 us, 5.4 TB/s        68 us, 5.9 TB/s
 //   65536x256   f32                                   22 us, 6.1 TB/s        36 us, 5.5 TB/s
 //   4096x16384  bf16                                  53 us, 5.1 TB/s       129 us, 3.1 TB/s (sums in shared memory)
-//   65536x1001  f32 (rows off 16 bytes)              135 us, 3.9 TB/s       148 us, 5.3 TB/s
+//   65536x1001  f32 (rows off 16 bytes)              100 us, 5.3 TB/s       148 us, 5.3 TB/s
 //   65536x1001  bf16                                  75 us, 3.5 TB/s       120 us, 3.3 TB/s
 // With 16-bit rows the instructions per element come near the bound: they are worked on in packed pairs.
 #include <cuda_runtime.h>
@@ -1207,13 +1207,14 @@ int norm_forward(const NormJob& j, int sm, cudaStream_t s)
         const int64_t vecs = (j.cols + V - 1) / V + 1;
         const int nv = vecs <= 32 ? 1 : vecs <= 64 ? 2 : 4;
         const int64_t g = ((vecs + nv - 1) / nv + 31) / 32 * 32;
-        // f32 rows of more than a warp: the scalar kernel's 16 loads a thread win (16384x4093 139 us, here 166 us)
-        if (period > 0 && vecs <= (sizeof(TX) == 2 ? 2048 : 128) && j.rows * (g / 32) >= (int64_t)sm * 16) {
+        // Two f32 rows at a time (65536x1001 100 us, one 120 us, the scalar kernel 135 us), one 16-bit row (75 us; two
+        // spill: 104 us; scalar 158 us).
+        if (period > 0 && vecs <= 2048 && j.rows * (g / 32) >= (int64_t)sm * 16) {
             const dim3 block((unsigned)g, g == 32 ? 8 : 1);
             const size_t smem = 2 * (size_t)(j.cols + 2 * V) * sizeof(TW);
             const auto kernel = nv == 1   ? k_norm_off<TX, TW, V, 1, 4>
                                 : nv == 2 ? k_norm_off<TX, TW, V, 2, 2>
-                                          : k_norm_off<TX, TW, V, 4, 1>;
+                                          : k_norm_off<TX, TW, V, 4, sizeof(TX) == 2 ? 1 : 2>;
             if (smem > 49152) {
                 const cudaError_t a = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
                 if (a != cudaSuccess) return cuda_error(a, "cudaFuncSetAttribute(k_norm_off)");
