@@ -393,13 +393,17 @@ __device__ __forceinline__ void load_part(const T* row, int c, int cols, float (
 {
     (void)sp;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = c + i >= 0 && c + i < cols && TROP_IN(row + c + i, sizeof(T), sp) ? to_f32(row[c + i]) : 0.f;
+    for (int i = 0; i < VEC; ++i) {
+        const bool in = c + i >= 0 && c + i < cols && TROP_IN(row + c + i, sizeof(T), sp);
+        v[i] = in ? to_f32(row[c + i]) : 0.f;
+    }
 }
 // (Of 16-bit rows a granule inside the matrix is read whole and the neighbouring rows' elements are put to
 // zero: forward of 65536x1001 bf16 94 us, element by element 118 us.  Of f32 rows, whose granules have four
 // elements, that costs more registers than it saves: backward of 65536x1001 348 us, element by element 148 us.)
 template <typename T, int VEC>
-__device__ __forceinline__ void load_off(const T* row, int c, int cols, const T* begin, const T* end, Raw<T, VEC>& q, const Span& sp)
+__device__ __forceinline__ void load_off(const T* row, int c, int cols, const T* begin, const T* end, Raw<T, VEC>& q,
+                                         const Span& sp)
 {
     (void)sp;
     if (sizeof(T) == 2 ? row + c >= begin && row + c + VEC <= end : whole<VEC>(c, cols)) {
@@ -463,8 +467,10 @@ __global__ void __launch_bounds__(NV == 4 ? 672 : 256) k_norm_off(const NormJob 
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 const int c = (k * blockDim.x + threadIdx.x) * VEC - o.off;
-                if (row < j.rows && c < cols) load_off<T, VEC>((const T*)j.x + row * j.sx, c, cols, (const T*)j.x, end, q[u][k], j.sp_x);
-                else q[u][k].zero();
+                if (row < j.rows && c < cols)
+                    load_off<T, VEC>((const T*)j.x + row * j.sx, c, cols, (const T*)j.x, end, q[u][k], j.sp_x);
+                else
+                    q[u][k].zero();
             }
         }
 #pragma unroll
@@ -904,7 +910,8 @@ __global__ void __launch_bounds__(WIDE ? 1024 : 512) k_norm_back_off(const NormJ
 #pragma unroll
             for (int k = 0; k < NV; ++k) qx[u][k].again(), qd[u][k].again();
             back_row<T, T, VEC, NV>(qx[u], qd[u], mean[u], rstd[u], h, d);
-            const Pair<VEC> flat = p_of<Pair<VEC>>(-sums[2 * u] * j.inv_cols), along = p_of<Pair<VEC>>(-sums[2 * u + 1] * j.inv_cols);
+            const Pair<VEC> flat = p_of<Pair<VEC>>(-sums[2 * u] * j.inv_cols);
+            const Pair<VEC> along = p_of<Pair<VEC>>(-sums[2 * u + 1] * j.inv_cols);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 times(k, d[k]);
@@ -1238,7 +1245,8 @@ int norm_forward(const NormJob& j, int sm, cudaStream_t s)
     }
     // blocks that fetch ahead walk over the rows; the others take one row each
     int64_t blocks = (j.rows + block.y - 1) / block.y;
-    if ((vec ? 16 : sizeof(TX)) * nv <= 32) blocks = std::min<int64_t>(blocks, (int64_t)sm * std::max<int>(1, 2048 / (int)(block.x * block.y)));
+    if ((vec ? 16 : sizeof(TX)) * nv <= 32)
+        blocks = std::min<int64_t>(blocks, (int64_t)sm * std::max<int>(1, 2048 / (int)(block.x * block.y)));
     const dim3 grid((unsigned)blocks);
     return vec ? norm_rows<TX, TY, TW, V>(j, nv, grid, block, s) : norm_rows<TX, TY, TW, 1>(j, nv, grid, block, s);
 }
@@ -1287,7 +1295,8 @@ int norm_backward(NormJob j, const NormVec& dw, const NormVec& db, int sm, cudaS
     const int64_t off_vecs = (j.cols + V - 1) / V + 1;
     int64_t off_g = ((off_vecs * V + 7) / 8 + 31) / 32 * 32, off_per_sm = 512 / (off_g == 32 ? 128 : off_g);
     const int64_t wide_g = ((off_vecs * V + 15) / 16 + 31) / 32 * 32;
-    const bool off_wide = wide_g > 32 && (off_g * off_per_sm < 384 || (sizeof(TX) == 2 && j.rows * wide_g >= (int64_t)sm * 1024 * 8));
+    const bool off_many = sizeof(TX) == 2 && j.rows * wide_g >= (int64_t)sm * 1024 * 8;
+    const bool off_wide = wide_g > 32 && (off_g * off_per_sm < 384 || off_many);
     if (off_wide) {
         off_g = wide_g;
         off_per_sm = std::min<int64_t>(1024 / off_g, 220000 / (off_g * 16 * (8 + sizeof(TW))));
@@ -1305,7 +1314,9 @@ int norm_backward(NormJob j, const NormVec& dw, const NormVec& db, int sm, cudaS
         blocks = (int)std::min<int64_t>((j.rows + off_block.y - 1) / off_block.y, sm * off_per_sm);
         blocks = std::max(1, blocks / period) * period;
     } else if (ring) blocks = (int)std::min<int64_t>(j.rows, (int64_t)sm * per_sm);
-    else if (fits) blocks = (int)std::min<int64_t>((j.rows + block.y - 1) / block.y, (int64_t)sm * std::max<int>(1, 512 / (int)(block.x * block.y)));
+    else if (fits)
+        blocks = (int)std::min<int64_t>((j.rows + block.y - 1) / block.y,
+                                        (int64_t)sm * std::max<int>(1, 512 / (int)(block.x * block.y)));
     else blocks = (int)std::min<int64_t>(j.rows, std::max<int64_t>(1, (int64_t)sm * 8 * 256 / j.cols));
     const size_t bytes = (size_t)blocks * j.cols * 4, spaced = (bytes + 255) / 256 * 256;
     struct Workspace {
@@ -1328,7 +1339,8 @@ int norm_backward(NormJob j, const NormVec& dw, const NormVec& db, int sm, cudaS
     if (period > 0) {
         if constexpr (std::is_same<TX, TY>::value) {
             const size_t smem = off_wide ? off_g * 16 * (8 + sizeof(TW)) : off_block.y > 1 ? off_block.y * (size_t)j.cols * 4 : 0;
-            const auto kernel = off_wide ? k_norm_back_off<TX, TW, V, 16 / V, 1, true> : k_norm_back_off<TX, TW, V, 8 / V, 4, false>;
+            const auto kernel = off_wide ? k_norm_back_off<TX, TW, V, 16 / V, 1, true>
+                                         : k_norm_back_off<TX, TW, V, 8 / V, 4, false>;
             if (smem > 49152) {
                 const cudaError_t a = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
                 if (a != cudaSuccess) return cuda_error(a, "cudaFuncSetAttribute(k_norm_back_off)");

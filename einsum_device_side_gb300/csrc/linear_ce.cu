@@ -418,7 +418,8 @@ __global__ void __launch_bounds__(THREADS, 1)
            const __grid_constant__ CUtensorMap map_c, const __grid_constant__ Job j, const __grid_constant__ JoinJob join)
 {
     constexpr bool A_MN = MODE == DW, B_MN = MODE == DX || MODE == DW;
-    constexpr int CG = S::CG, TM = S::TM, TN = S::TN, NACC = S::NACC, STAGES = S::STAGES, STAGE_BYTES = S::STAGE_BYTES, BUFS = S::BUFS, SUB = S::SUB;
+    constexpr int CG = S::CG, TM = S::TM, TN = S::TN, NACC = S::NACC, STAGES = S::STAGES;
+    constexpr int STAGE_BYTES = S::STAGE_BYTES, BUFS = S::BUFS, SUB = S::SUB;
     extern __shared__ uint8_t dyn[];
     __shared__ __align__(8) uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], drain;
     __shared__ uint32_t tmem_slot;
@@ -992,8 +993,9 @@ int launch_join(JoinJob t, float2* sums, cudaStream_t s)
 template <int MODE, typename S>
 cudaError_t allow_smem()
 {
-    const cudaError_t e = cudaFuncSetAttribute(k_tile<MODE, true, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<MODE, S>());
-    return e != cudaSuccess ? e : cudaFuncSetAttribute(k_tile<MODE, false, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<MODE, S>());
+    constexpr cudaFuncAttribute most = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    const cudaError_t e = cudaFuncSetAttribute(k_tile<MODE, true, S>, most, smem_bytes<MODE, S>());
+    return e != cudaSuccess ? e : cudaFuncSetAttribute(k_tile<MODE, false, S>, most, smem_bytes<MODE, S>());
 }
 
 }  // namespace
