@@ -4,7 +4,9 @@ What stands around a tropical product and its gradient (``gemm``,
 ``gemm_backward``, ``TropicalGemm``) when a model is trained with them.  Like
 the rest of the package these functions marshal torch CUDA tensors into the C
 ABI of ``include/tropical.h``; all computation runs in the library's kernels,
-on the current stream or the one given.
+on the current stream or the one given (``stream``; copies and results too, as
+under ``torch.cuda.stream``: the caller orders the inputs before the call and
+the results' use after it).
 """
 
 from __future__ import annotations
@@ -55,6 +57,34 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _tensors(*values):
+    for v in values:
+        if isinstance(v, torch.Tensor):
+            yield v
+        elif isinstance(v, (list, tuple)):
+            yield from _tensors(*v)
+
+
+def _stream_object(stream):
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream.cuda_stream)
+
+
+def _on_stream(f, stream, *args, **kwargs):
+    """``f`` with `stream` current: the copies it makes and the results it allocates then belong to the stream its kernels
+    run on, in order with them.  The allocator is told of the tensors that one stream owns and the other uses, so that it
+    hands out none of their memory while the other stream is not through with it."""
+    stream = _stream_object(stream)
+    caller = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        result = f(*args, **kwargs)
+    if caller.cuda_stream != stream.cuda_stream:
+        for t in _tensors(args, tuple(kwargs.values())):
+            t.record_stream(stream)
+        for t in _tensors(result):
+            t.record_stream(caller)
+    return result
+
+
 def _check_vector(t, name: str, like, dtype, n: int):
     """A contiguous vector of n elements beside `like`, or None."""
     if t is None:
@@ -86,6 +116,8 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.
     x's or float32.  The result has x's type; a float32 ``x`` (a tropical product, say) may give ``out_dtype``
     bfloat16 or float16.  Returns ``(y, mean, rstd)``, the float32 statistics with x's leading shape:
     what ``layer_norm_backward`` reads."""
+    if stream is not None:
+        return _on_stream(layer_norm, stream, x, weight, bias, eps, out_dtype, out)
     fc = _fast()
     if out is None and out_dtype is None and fc is not None:  # the usual call
         r = fc.layer_norm(x, weight, bias, eps, stream)
@@ -121,6 +153,9 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
                         want_bias: bool = True, weight_dtype: torch.dtype | None = None, stream=None):
     """Gradient of ``layer_norm``: ``(dx, dweight, dbias)``, an unwanted one None.  ``dy`` has the forward's result type;
     the weight's and bias's gradients have ``weight``'s type (``weight_dtype`` without one, by default x's)."""
+    if stream is not None:
+        return _on_stream(layer_norm_backward, stream, dy, x, mean, rstd, weight, want_x=want_x, want_weight=want_weight,
+                          want_bias=want_bias, weight_dtype=weight_dtype)
     fc = _fast()
     if want_x and want_weight and want_bias and fc is not None and weight is not None:  # the usual call
         r = fc.layer_norm_backward(dy, x, mean, rstd, weight, stream)
@@ -191,6 +226,8 @@ def linear_cross_entropy(x: torch.Tensor, w: torch.Tensor, target: torch.Tensor,
     ``(loss, lse, kept)``: the loss (one per token for ``reduction="none"``, else a scalar; tokens whose target is
     ``ignore_index`` have none), the log-sum-exp of each token's logits, and the number of tokens kept, all float32.
     A target outside the vocabulary gives NaN."""
+    if stream is not None:
+        return _on_stream(linear_cross_entropy, stream, x, w, target, reduction, ignore_index)
     fc = _fast()
     code = _REDUCTIONS.get(reduction)
     if code is None:
@@ -226,6 +263,9 @@ def linear_cross_entropy_backward(dloss: torch.Tensor, x: torch.Tensor, w: torch
 
     ``dloss``: float32, one per token or a scalar for all of them.  With ``kept`` (the mean's gradient) it is divided by
     that count.  The logits are formed again in pieces of the vocabulary."""
+    if stream is not None:
+        return _on_stream(linear_cross_entropy_backward, stream, dloss, x, w, target, lse, kept, ignore_index, want_x=want_x,
+                          want_w=want_w)
     fc = _fast()
     dx = _empty(x.shape, dtype=x.dtype, device=x.device) if want_x else None
     dw = _empty(w.shape, dtype=w.dtype, device=w.device) if want_w else None
@@ -363,6 +403,10 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, exp_avg_scale=None, exp_avg_s
     ``exp_avg_sq``) with their float32 scales, one for every 256 elements.  ``copies``: 16-bit copies of float32
     parameters that the step writes too.  Every tensor is contiguous.  A program that steps the same tensors again and
     again keeps an ``AdamWPlan`` (or ``AdamW``), which reads the lists once."""
+    if stream is not None:
+        return _on_stream(adamw_step, stream, params, grads, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, step=step,
+                          lr=lr, beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay, grad_scale=grad_scale,
+                          copies=copies)
     lib = _lib()
     table, n, p, g, bits, c, _, device = _table(params, grads, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, copies)
     o = _Options(lr, beta1, beta2, eps, weight_decay, grad_scale, step)
@@ -372,6 +416,8 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, exp_avg_scale=None, exp_avg_s
 
 def adamw_state_values(exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, out=None, stream=None):
     """8-bit AdamW states as the values they stand for: two lists of float32 tensors (``out``: the lists to fill)."""
+    if stream is not None:
+        return _on_stream(adamw_state_values, stream, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, out)
     lib = _lib()
     if out is None:
         out = tuple([torch.empty(t.shape, dtype=torch.float32, device=t.device) for t in ts] for ts in (exp_avg, exp_avg_sq))
@@ -401,6 +447,7 @@ class AdamWPlan:
         _pkg._check(lib.tropical_adamw_plan_create(n, table, p, g, bits, c, states, ctypes.byref(h)))
         self._h = h.value
         self._keep = [None if t is None else list(t) for t in lists]
+        self._streams = {}  # given to step or state_values: they use the tensors
         self._like = params[0] if n else torch.empty(0, device="cuda")
         self.values = values
 
@@ -409,6 +456,8 @@ class AdamWPlan:
         """One step; ``step`` counts from 1."""
         if self._h is None:
             raise RuntimeError("plan is closed")
+        if stream is not None:
+            self._streams[stream.cuda_stream] = stream
         if _pkg._fc is not None:
             rc = _pkg._fc.adamw_plan_step(self._h, lr, beta1, beta2, eps, weight_decay, grad_scale, step, self._like,
                                           stream)
@@ -422,6 +471,8 @@ class AdamWPlan:
         """Fills and returns ``values``."""
         if self._h is None:
             raise RuntimeError("plan is closed")
+        if stream is not None:
+            self._streams[stream.cuda_stream] = stream
         if _pkg._fc is not None:
             rc = _pkg._fc.adamw_plan_values(self._h, self._like, stream)
         else:
@@ -434,6 +485,10 @@ class AdamWPlan:
         if getattr(self, "_h", None) is not None:
             _pkg._check(_pkg._lib.tropical_adamw_plan_destroy(self._h))
             self._h = None
+            for s in self._streams.values():  # steps that are still on their way: the memory is not handed out before
+                for t in _tensors(self._keep, self.values):
+                    t.record_stream(_stream_object(s))
+            self._streams = {}
 
     def __del__(self):
         try:

@@ -1,0 +1,80 @@
+"""The training operators' host side at its edges, with stand-ins for the device.  No GPU."""
+
+import contextlib
+
+import pytest
+import torch
+
+
+@pytest.fixture()
+def train(monkeypatch):
+    """train.py with the C calls replaced by a record of them: (name, arguments, current stream)."""
+    from einsum_device_side_gb300 import train as module
+
+    class Library:
+        def __getattr__(self, name):
+            def call(*args):
+                module.calls.append((name, args, module.current[-1]))
+                return module.answers.pop(0) if module.answers else 0
+            return call
+
+    class Stream:
+        def __init__(self, handle):
+            self.cuda_stream, self.device = handle, None
+
+    @contextlib.contextmanager
+    def use(stream):
+        module.current.append(stream)
+        yield
+        module.current.pop()
+
+    home = Stream(1)
+    for name, value in (("calls", []), ("answers", []), ("current", [home]), ("Side", Stream), ("recorded", [])):
+        monkeypatch.setattr(module, name, value, raising=False)
+    monkeypatch.setattr(module._pkg, "_lib", Library())
+    monkeypatch.setattr(module._pkg, "_fc", None)
+    monkeypatch.setattr(module, "_fast", lambda: None)
+    monkeypatch.setattr(module._pkg, "_stream", lambda stream=None, like=None: (stream or module.current[-1]).cuda_stream)
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "stream", use)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: module.current[-1])
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: module.recorded.append((t.data_ptr(), s.cuda_stream)),
+                        raising=False)
+    return module
+
+
+def test_copies_and_results_belong_to_the_stream_given(train, monkeypatch):
+    """Rows whose leading axes do not merge are copied: the copy, like the results, has to be made on the stream that the
+    kernel uses."""
+    side, made = train.Side(7), []
+    reshape, empty, empty_like = torch.Tensor.reshape, torch.empty, torch.empty_like
+    monkeypatch.setattr(torch.Tensor, "reshape", lambda t, *s: made.append(train.current[-1]) or reshape(t, *s))
+    monkeypatch.setattr(train, "_empty", lambda *a, **k: made.append(train.current[-1]) or empty(*a, **k))
+    monkeypatch.setattr(train, "_empty_like", lambda *a, **k: made.append(train.current[-1]) or empty_like(*a, **k))
+    x = torch.zeros(3, 9, 8)[:, :5]
+    y, mean, rstd = train.layer_norm(x, stream=side)
+    assert made and all(s is side for s in made)
+    made.clear()
+    dx, _, _ = train.layer_norm_backward(x, x, mean, rstd, want_weight=False, want_bias=False, stream=side)
+    assert made and all(s is side for s in made)
+    assert [c[0] for c in train.calls] == ["tropical_layer_norm", "tropical_layer_norm_backward"]
+    assert all(c[1][-1] == side.cuda_stream for c in train.calls)
+    # the allocator knows: inputs are used on the side stream, results on the caller's
+    assert (x.data_ptr(), 7) in train.recorded
+    assert all((t.data_ptr(), 1) in train.recorded for t in (y, mean, rstd, dx))
+
+
+def test_a_plan_s_tensors_outlive_its_steps_on_another_stream(train, monkeypatch):
+    import ctypes
+    t = [torch.zeros(4) for _ in range(4)]
+
+    def create(*args):
+        ctypes.cast(args[-1], ctypes.POINTER(ctypes.c_void_p))[0] = 5
+        return 0
+
+    monkeypatch.setattr(type(train._pkg._lib), "tropical_adamw_plan_create", staticmethod(create), raising=False)
+    plan = train.AdamWPlan(*([x] for x in t))
+    plan.step(1, stream=train.Side(7))
+    assert not train.recorded
+    plan.close()
+    assert sorted(train.recorded) == sorted((x.data_ptr(), 7) for x in t)
