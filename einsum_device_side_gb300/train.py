@@ -203,7 +203,7 @@ class LayerNorm(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
-        need = ctx.needs_input_grad
+        need = (*ctx.needs_input_grad, False, False)  # (weight and bias may not have been given)
         dx, dw, db = layer_norm_backward(dy if dy.stride(-1) == 1 else dy.contiguous(), x, mean, rstd, weight,
                                          want_x=need[0], want_weight=need[1], want_bias=need[2],
                                          weight_dtype=ctx.bias_dtype)

@@ -78,3 +78,10 @@ def test_a_plan_s_tensors_outlive_its_steps_on_another_stream(train, monkeypatch
     assert not train.recorded
     plan.close()
     assert sorted(train.recorded) == sorted((x.data_ptr(), 7) for x in t)
+
+
+@pytest.mark.parametrize("given", [1, 2, 3])
+def test_layer_norm_differentiates_with_any_of_its_arguments(train, given):
+    args = [torch.zeros(3, 8, requires_grad=True), torch.ones(8, requires_grad=True), torch.zeros(8, requires_grad=True)]
+    train.LayerNorm.apply(*args[:given]).sum().backward()
+    assert [a.grad is not None for a in args] == [i < given for i in range(3)]
