@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 
 import torch
+from torch.autograd.function import once_differentiable
 
 import einsum_device_side_gb300 as _pkg
 
@@ -191,7 +192,8 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
 
 
 class LayerNorm(torch.autograd.Function):
-    """Autograd over layer norm: ``LayerNorm.apply(x, weight, bias, eps, out_dtype)``."""
+    """Autograd over layer norm: ``LayerNorm.apply(x, weight, bias, eps, out_dtype)``.  First derivatives only: a second
+    one (``create_graph=True``) raises."""
 
     @staticmethod
     def forward(ctx, x, weight=None, bias=None, eps=1e-5, out_dtype=None):
@@ -201,6 +203,7 @@ class LayerNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         need = (*ctx.needs_input_grad, False, False)  # (weight and bias may not have been given)
@@ -293,7 +296,8 @@ def linear_cross_entropy_backward(dloss: torch.Tensor, x: torch.Tensor, w: torch
 
 
 class LinearCrossEntropy(torch.autograd.Function):
-    """Autograd over the head's loss: ``LinearCrossEntropy.apply(x, w, target, reduction, ignore_index)``."""
+    """Autograd over the head's loss: ``LinearCrossEntropy.apply(x, w, target, reduction, ignore_index)``.  First derivatives
+    only: a second one (``create_graph=True``) raises."""
 
     @staticmethod
     def forward(ctx, x, w, target, reduction="mean", ignore_index=-100):
@@ -303,6 +307,7 @@ class LinearCrossEntropy(torch.autograd.Function):
         return loss
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dloss):
         x, w, target, lse, kept = ctx.saved_tensors
         dx, dw = linear_cross_entropy_backward(dloss, x, w, target, lse, kept if ctx.reduction == "mean" else None,

@@ -40,3 +40,19 @@ def test_rows_that_are_copied_follow_the_stream_given(trop):
     with torch.cuda.stream(side):
         same = [torch.equal(a, b) for a, b in zip((*got, *back), (*want, *grads))]
     assert all(same), same
+
+
+# ------------------------------------------------------------------ autograd
+
+
+def test_a_gradient_penalty_raises(trop):
+    x, w = _normal(1, 5, 32).requires_grad_(), _normal(2, 32).requires_grad_()
+    y = trop.LayerNorm.apply(x, w)
+    dx, = torch.autograd.grad(y.square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        dx.square().sum().backward()
+    h, v = _normal(3, 5, 32).to(B).requires_grad_(), _normal(4, 9, 32).to(B).requires_grad_()
+    loss = trop.LinearCrossEntropy.apply(h, v, torch.arange(5, device="cuda"))
+    dh, = torch.autograd.grad(loss.square(), h, create_graph=True)
+    with pytest.raises(RuntimeError):
+        dh.float().square().sum().backward()

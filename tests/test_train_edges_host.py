@@ -85,3 +85,19 @@ def test_layer_norm_differentiates_with_any_of_its_arguments(train, given):
     args = [torch.zeros(3, 8, requires_grad=True), torch.ones(8, requires_grad=True), torch.zeros(8, requires_grad=True)]
     train.LayerNorm.apply(*args[:given]).sum().backward()
     assert [a.grad is not None for a in args] == [i < given for i in range(3)]
+
+
+def test_second_derivatives_are_refused(train):
+    """What the C calls return has no graph: a second derivative would silently lack these operators' part."""
+    x = torch.zeros(3, 8, requires_grad=True)
+    w = torch.ones(8, requires_grad=True)
+    y = train.LayerNorm.apply(x, w)
+    dx, = torch.autograd.grad((y * y).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="differentiate twice"):
+        dx.sum().backward()
+    h = torch.zeros(3, 8, dtype=torch.bfloat16, requires_grad=True)
+    v = torch.zeros(5, 8, dtype=torch.bfloat16, requires_grad=True)
+    loss = train.LinearCrossEntropy.apply(h, v, torch.zeros(3, dtype=torch.int64))
+    dh, = torch.autograd.grad(loss * loss, h, create_graph=True)
+    with pytest.raises(RuntimeError, match="differentiate twice"):
+        dh.sum().backward()
