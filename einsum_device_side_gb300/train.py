@@ -100,6 +100,19 @@ def _check_vector(t, name: str, like, dtype, n: int):
         _fail(-1, f"{name} must be contiguous")
 
 
+def _result(x, dtype=None):
+    """An uninitialised result of x's shape whose leading axes merge, whatever x's strides are."""
+    return _empty_like(x, dtype=dtype or x.dtype) if x.dim() <= 2 else _empty(x.shape, dtype=dtype or x.dtype, device=x.device)
+
+
+def _result_rows(t, n: int, c: int, name: str):
+    """[..., C] as the matrix that a call writes."""
+    try:
+        return t.view(n, c)
+    except RuntimeError:
+        _fail(-10, f"{name}: the leading axes (shape {tuple(t.shape)}, strides {t.stride()}) must merge into one stride")
+
+
 def _rows(t, name: str):
     """[..., C] as a matrix (a copy only where the leading axes do not merge into one stride)."""
     if t.dim() == 2:
@@ -113,7 +126,8 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.
                eps: float = 1e-5, out_dtype: torch.dtype | None = None, out: torch.Tensor | None = None, stream=None):
     """Layer norm over the last axis: ``(x - mean) * rstd * weight + bias``.
 
-    ``x``: float32, bfloat16 or float16, its last axis contiguous.  ``weight`` and ``bias`` are optional, of one type:
+    ``x``: float32, bfloat16 or float16, its last axis contiguous, its leading axes in any order (where they do not merge
+    into one stride, the rows are copied first; ``out``'s have to merge).  ``weight`` and ``bias`` are optional, of one type:
     x's or float32.  The result has x's type; a float32 ``x`` (a tropical product, say) may give ``out_dtype``
     bfloat16 or float16.  Returns ``(y, mean, rstd)``, the float32 statistics with x's leading shape:
     what ``layer_norm_backward`` reads."""
@@ -127,7 +141,7 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.
         if r < 0:
             _pkg._check(r)
     if out is None:
-        out = _empty_like(x) if out_dtype is None else _empty_like(x, dtype=out_dtype)
+        out = _result(x, out_dtype)
     elif out.shape != x.shape or (out_dtype is not None and out.dtype != out_dtype):
         _fail(-5, f"out is {tuple(out.shape)} {out.dtype}, not {tuple(x.shape)} {out_dtype or x.dtype}")
     mean = _empty(x.shape[:-1], dtype=_f32, device=x.device)
@@ -145,7 +159,7 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.
     _check_vector(weight, "weight", x, wdtype, c)
     _check_vector(bias, "bias", x, wdtype, c)
     _pkg._check(_lib().tropical_layer_norm(_desc(x2), _ptr(weight), _ptr(bias), _CODES.get(wdtype, -1), eps,
-                                        _desc(out.view(n, c)), _ptr(mean), _ptr(rstd), _pkg._stream(stream, x)))
+                                        _desc(_result_rows(out, n, c, "out")), _ptr(mean), _ptr(rstd), _pkg._stream(stream, x)))
     return out, mean, rstd
 
 
@@ -168,7 +182,7 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
         _fail(-5, f"dy has shape {tuple(dy.shape)}, x {tuple(x.shape)}")
     wdtype = weight.dtype if weight is not None else weight_dtype or x.dtype
     c = x.shape[-1]
-    dx = _empty_like(x) if want_x else None
+    dx = _result(x) if want_x else None
     dw = _empty(c, dtype=wdtype, device=x.device) if want_weight else None
     db = None if not want_bias else _empty_like(dw) if want_weight else _empty(c, dtype=wdtype, device=x.device)
     if fc is not None:

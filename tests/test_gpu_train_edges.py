@@ -56,3 +56,30 @@ def test_a_gradient_penalty_raises(trop):
     dh, = torch.autograd.grad(loss.square(), h, create_graph=True)
     with pytest.raises(RuntimeError):
         dh.float().square().sum().backward()
+
+
+# ------------------------------------------------------------------ layouts
+
+
+@pytest.mark.parametrize("dt", [F, B])
+@pytest.mark.parametrize("cols", [64, 33])
+def test_layer_norm_of_leading_axes_in_any_order(trop, dt, cols):
+    """[T, B, C] read as [B, T, C] and the other way, x and dy exchanged separately: bit for bit what contiguous rows give."""
+    w, b = _normal(3, cols).to(dt), _normal(4, cols).to(dt)
+    plain = _normal(1, 7, 5, cols).to(dt), _normal(2, 7, 5, cols).to(dt)
+    want = trop.layer_norm(plain[0], w, b)
+    grads = trop.layer_norm_backward(plain[1], plain[0], *want[1:], w)
+    for swap_x in (False, True):
+        for swap_dy in (False, True):
+            x, dy = (t.transpose(0, 1).contiguous().transpose(0, 1) if s else t for t, s in zip(plain, (swap_x, swap_dy)))
+            got = trop.layer_norm(x, w, b)
+            assert all(torch.equal(p, q) for p, q in zip(got, want))
+            assert all(torch.equal(p, q) for p, q in zip(trop.layer_norm_backward(dy, x, *want[1:], w), grads))
+            leaf = x.detach().requires_grad_()
+            trop.LayerNorm.apply(leaf, w, b).backward(dy)
+            assert torch.equal(leaf.grad, grads[0])
+    with pytest.raises(trop.TropicalError) as e:
+        trop.layer_norm(plain[0], w, b, out=torch.empty(5, 7, cols, device="cuda", dtype=dt).transpose(0, 1))
+    assert e.value.name == "UNSUPPORTED"
+    y16 = trop.layer_norm(plain[0].float().transpose(0, 1), out_dtype=H)[0]
+    assert y16.dtype == H and y16.shape == (5, 7, cols)

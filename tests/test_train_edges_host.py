@@ -101,3 +101,15 @@ def test_second_derivatives_are_refused(train):
     dh, = torch.autograd.grad(loss * loss, h, create_graph=True)
     with pytest.raises(RuntimeError, match="differentiate twice"):
         dh.sum().backward()
+
+
+def test_leading_axes_in_any_order(train):
+    """A dense input with its leading axes exchanged: empty_like would keep the exchanged strides, which make no rows."""
+    x = torch.zeros(5, 4, 8).transpose(0, 1)
+    y, mean, rstd = train.layer_norm(x)
+    assert y.shape == (4, 5, 8) and y.is_contiguous()
+    dx, dw, db = train.layer_norm_backward(x, x, mean, rstd)
+    assert dx.shape == (4, 5, 8) and dx.is_contiguous()
+    with pytest.raises(train._pkg.TropicalError) as e:
+        train.layer_norm(x, out=torch.zeros(5, 4, 8).transpose(0, 1))
+    assert e.value.name == "UNSUPPORTED"
