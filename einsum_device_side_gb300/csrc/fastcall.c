@@ -396,7 +396,7 @@ static int32_t dtype_or(PyObject* obj, int32_t other)
 /* Results allocated here rather than in the Python wrapper, which saves its interpreter several us per
  * call: torch.empty(n, dtype=, device=) and torch.empty_like(t), by the handles set_torch_allocators
  * was given. */
-static PyObject *g_empty, *g_empty_like, *g_f32, *g_empty_kw, *s_device, *s_unbind;
+static PyObject *g_empty, *g_empty_like, *g_f32, *g_empty_kw, *s_device;
 
 static PyObject* fc_set_torch_allocators(PyObject* self, PyObject* const* a, Py_ssize_t nargs)
 {
@@ -419,6 +419,20 @@ static PyObject* new_vector(int64_t n, PyObject* dtype, PyObject* like)
     PyObject* r = NULL;
     if (device) {
         PyObject* args[3] = {size, dtype, device};
+        r = PyObject_Vectorcall(g_empty, args, 1, g_empty_kw);
+    }
+    Py_XDECREF(size);
+    Py_XDECREF(device);
+    return r;
+}
+/* an uninitialised f32 scalar beside `like` */
+static PyObject* new_scalar(PyObject* like)
+{
+    PyObject* size = PyTuple_New(0);
+    PyObject* device = size ? PyObject_GetAttr(like, s_device) : NULL;
+    PyObject* r = NULL;
+    if (device) {
+        PyObject* args[3] = {size, g_f32, device};
         r = PyObject_Vectorcall(g_empty, args, 1, g_empty_kw);
     }
     Py_XDECREF(size);
@@ -596,32 +610,28 @@ static PyObject* fc_linear_ce(PyObject* self, PyObject* const* a, Py_ssize_t nar
     (void)self;
     if (check_nargs(nargs, 6, "linear_ce") < 0) return NULL;
     trop_tensor x, w, t;
-    void *loss = NULL, *lse, *few, *stream;
+    void *loss = NULL, *lse, *total = NULL, *kept, *stream;
     int64_t ignore, reduction;
     long device;
     const int usual = head_operands(a, &x, &w, &t, &device);
     if (usual < 0 || as_i64(a[3], &ignore) < 0 || as_i64(a[4], &reduction) < 0 || obj_stream(a[5], a[0], &stream) < 0) return NULL;
     if (!g_empty || usual > 0 || device < 0) return PyLong_FromLong(PLAIN_PATH);
-    PyObject* of = new_vector(2, g_f32, a[0]);
-    PyObject* ol = of ? new_vector(x.shape[0], g_f32, a[0]) : NULL;
-    PyObject* oe = !ol ? NULL : reduction == 0 ? PyObject_CallOneArg(g_empty_like, ol) : Py_NewRef(Py_None);
-    PyObject* two = oe ? PyObject_CallMethodNoArgs(of, s_unbind) : NULL;
+    /* the loss and the count are tensors of their own: as views of one they could not be changed in place */
+    PyObject* ol = new_vector(x.shape[0], g_f32, a[0]);
+    PyObject* ov = !ol ? NULL : reduction == 0 ? PyObject_CallOneArg(g_empty_like, ol) : new_scalar(a[0]);
+    PyObject* ok = ov ? new_scalar(a[0]) : NULL;
     PyObject* out = NULL;
-    if (two && fresh_ptr(of, &few) == 0 && fresh_ptr(ol, &lse) == 0 && obj_ptr(oe, &loss) == 0) {
+    if (ok && fresh_ptr(ol, &lse) == 0 && fresh_ptr(ov, reduction == 0 ? &loss : &total) == 0 && fresh_ptr(ok, &kept) == 0) {
         int rc;
         Py_BEGIN_ALLOW_THREADS
-        rc = tropical_linear_cross_entropy(&x, &w, &t, ignore, reduction == 1, (float*)loss, (float*)lse,
-                                           reduction == 0 ? NULL : (float*)few, (float*)few + 1, stream);
+        rc = tropical_linear_cross_entropy(&x, &w, &t, ignore, reduction == 1, (float*)loss, (float*)lse, (float*)total,
+                                           (float*)kept, stream);
         Py_END_ALLOW_THREADS
-        if (rc) out = PyLong_FromLong(rc);
-        else if (PyTuple_Check(two) && PyTuple_GET_SIZE(two) == 2)
-            out = PyTuple_Pack(3, reduction == 0 ? oe : PyTuple_GET_ITEM(two, 0), ol, PyTuple_GET_ITEM(two, 1));
-        else PyErr_SetString(PyExc_RuntimeError, "unbind did not give two tensors");
+        out = rc == 0 ? PyTuple_Pack(3, ov, ol, ok) : PyLong_FromLong(rc);
     }
-    Py_XDECREF(of);
     Py_XDECREF(ol);
-    Py_XDECREF(oe);
-    Py_XDECREF(two);
+    Py_XDECREF(ov);
+    Py_XDECREF(ok);
     return out;
 }
 
@@ -733,7 +743,6 @@ PyMODINIT_FUNC PyInit__fastcall(void)
 {
     s_data_ptr = PyUnicode_InternFromString("data_ptr");
     s_device = PyUnicode_InternFromString("device");
-    s_unbind = PyUnicode_InternFromString("unbind");
     s_shape = PyUnicode_InternFromString("shape");
     s_stride = PyUnicode_InternFromString("stride");
     s_dtype = PyUnicode_InternFromString("dtype");

@@ -256,7 +256,8 @@ def linear_cross_entropy(x: torch.Tensor, w: torch.Tensor, target: torch.Tensor,
         if r < 0:
             _pkg._check(r)
     n = x.shape[0] if x.dim() else 0
-    total, kept = _empty(2, dtype=_f32, device=x.device).unbind()
+    # (each a tensor of its own: a view could not be changed in place as an autograd function's result)
+    total, kept = _empty((), dtype=_f32, device=x.device), _empty((), dtype=_f32, device=x.device)
     lse = _empty(n, dtype=_f32, device=x.device)
     loss = _empty_like(lse) if reduction == "none" else None
     each, mean = loss is not None, reduction == "mean"

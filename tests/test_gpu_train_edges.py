@@ -83,3 +83,17 @@ def test_layer_norm_of_leading_axes_in_any_order(trop, dt, cols):
     assert e.value.name == "UNSUPPORTED"
     y16 = trop.layer_norm(plain[0].float().transpose(0, 1), out_dtype=H)[0]
     assert y16.dtype == H and y16.shape == (5, 7, cols)
+
+
+@pytest.mark.parametrize("reduction", ["mean", "sum", "none"])
+def test_the_loss_may_be_changed_in_place(trop, reduction):
+    h, v, t = _normal(3, 50, 32).to(B).requires_grad_(), _normal(4, 90, 32).to(B), torch.arange(50, device="cuda")
+    plain = trop.LinearCrossEntropy.apply(h, v, t, reduction)
+    value = plain.detach().clone()
+    want, = torch.autograd.grad((plain / 4).sum(), h)
+    loss = trop.LinearCrossEntropy.apply(h, v, t, reduction)
+    loss /= 4
+    assert torch.equal(loss.detach(), value / 4)
+    loss.detach().mul_(2)  # what a program that logs the loss may do
+    got, = torch.autograd.grad(loss.sum(), h)
+    assert torch.equal(got, want)

@@ -113,3 +113,16 @@ def test_leading_axes_in_any_order(train):
     with pytest.raises(train._pkg.TropicalError) as e:
         train.layer_norm(x, out=torch.zeros(5, 4, 8).transpose(0, 1))
     assert e.value.name == "UNSUPPORTED"
+
+
+def test_the_loss_is_no_view_and_may_be_changed_in_place(train):
+    h = torch.zeros(3, 8, dtype=torch.bfloat16, requires_grad=True)
+    v = torch.zeros(5, 8, dtype=torch.bfloat16)
+    target = torch.zeros(3, dtype=torch.int64)
+    for reduction in ("mean", "sum", "none"):
+        loss, _, kept = train.linear_cross_entropy(h.detach(), v, target, reduction)
+        assert loss._base is None and kept._base is None and loss.shape == ((3,) if reduction == "none" else ())
+        loss = train.LinearCrossEntropy.apply(h, v, target, reduction)
+        loss /= 4
+        loss.detach().mul_(2)
+        loss.sum().backward()
