@@ -559,8 +559,17 @@ struct Laid {
             p.chunks = (int64_t)h.chunk.size();
             parts.push_back(p);
         }
-        err = cudaMemcpy(memory, image.data(), bytes, cudaMemcpyHostToDevice);
-        return err == cudaSuccess ? (int)TROP_OK : cuda_error(err, "cudaMemcpy (the plan's table)");
+        // The table is in device memory before the plan is handed out: its steps run on any stream, and read it
+        // before they wait for the kernel ahead of them.  (A plain copy from pageable memory may return
+        // while its last part is still on its way, in order with the legacy stream only.)
+        cudaStream_t up = nullptr;
+        err = cudaStreamCreateWithFlags(&up, cudaStreamNonBlocking);
+        if (err != cudaSuccess) return cuda_error(err, "cudaStreamCreateWithFlags (the plan's table)");
+        err = cudaMemcpyAsync(memory, image.data(), bytes, cudaMemcpyHostToDevice, up);
+        const cudaError_t done = cudaStreamSynchronize(up);  // also before `image` goes
+        cudaStreamDestroy(up);
+        if (err == cudaSuccess) err = done;
+        return err == cudaSuccess ? (int)TROP_OK : cuda_error(err, "copy of the plan's table");
     }
 };
 

@@ -42,6 +42,33 @@ def test_rows_that_are_copied_follow_the_stream_given(trop):
     assert all(same), same
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_plan_is_ready_for_any_stream_when_it_is_made(trop, bits):
+    """A plan of many tensors (its table lies in device memory), stepped at once on a stream that waits for nothing."""
+    sizes = [300 + i for i in range(400)]
+    hyper = dict(lr=1e-2, weight_decay=0.0)
+    p, g = [_normal(i, n) for i, n in enumerate(sizes)], [_normal(1000 + i, n) for i, n in enumerate(sizes)]
+    q = [t.clone() for t in p]
+    dtypes = (F, F) if bits == 32 else (torch.int8, torch.uint8)
+    make = lambda: [[torch.zeros(n, dtype=d, device="cuda") for n in sizes] for d in dtypes] + (  # noqa: E731
+        [] if bits == 32 else [[torch.zeros(-(-n // 256), device="cuda") for n in sizes] for _ in range(2)])
+    a, b, values = make(), make(), [[torch.empty(n, device="cuda") for n in sizes] for _ in range(2)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    plan = trop.AdamWPlan(p, g, *a, values=tuple(values) if bits == 8 else None)
+    plan.step(1, stream=side, **hyper)
+    if bits == 8:
+        plan.state_values(stream=side)
+    side.synchronize()
+    trop.adamw_step(q, g, *b, step=1, **hyper)
+    assert all(torch.equal(x, y) for x, y in zip(p, q))
+    assert all(torch.equal(x, y) for s, t in zip(a, b) for x, y in zip(s, t))
+    if bits == 8:
+        want = trop.adamw_state_values(*b)
+        assert all(torch.equal(x, y) for s, t in zip(values, want) for x, y in zip(s, t))
+    plan.close()
+
+
 # ------------------------------------------------------------------ autograd
 
 
