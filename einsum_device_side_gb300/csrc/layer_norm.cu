@@ -1187,6 +1187,10 @@ int norm_rows(const NormJob& j, int nv, dim3 grid, dim3 block, cudaStream_t s)
     return TROP_OK;
 }
 
+// Dynamic shared memory that needs no attribute: a block has 48 KB in all without it, of which static arrays take
+// up to 2 KB (sh[2][32][8]).
+constexpr size_t PLAIN_SMEM = 49152 - 2048;
+
 // Bytes of an SM's rings.
 constexpr size_t RING_BYTES = 196608;
 
@@ -1222,7 +1226,7 @@ int norm_forward(const NormJob& j, int sm, cudaStream_t s)
             const auto kernel = nv == 1   ? k_norm_off<TX, TW, V, 1, 4>
                                 : nv == 2 ? k_norm_off<TX, TW, V, 2, 2>
                                           : k_norm_off<TX, TW, V, 4, sizeof(TX) == 2 ? 1 : 2>;
-            if (smem > 49152) {
+            if (smem > PLAIN_SMEM) {
                 const cudaError_t a = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
                 if (a != cudaSuccess) return cuda_error(a, "cudaFuncSetAttribute(k_norm_off)");
             }
@@ -1341,7 +1345,7 @@ int norm_backward(NormJob j, const NormVec& dw, const NormVec& db, int sm, cudaS
             const size_t smem = off_wide ? off_g * 16 * (8 + sizeof(TW)) : off_block.y > 1 ? off_block.y * (size_t)j.cols * 4 : 0;
             const auto kernel = off_wide ? k_norm_back_off<TX, TW, V, 16 / V, 1, true>
                                          : k_norm_back_off<TX, TW, V, 8 / V, 4, false>;
-            if (smem > 49152) {
+            if (smem > PLAIN_SMEM) {
                 const cudaError_t a = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
                 if (a != cudaSuccess) return cuda_error(a, "cudaFuncSetAttribute(k_norm_back_off)");
             }
@@ -1377,7 +1381,7 @@ int norm_backward(NormJob j, const NormVec& dw, const NormVec& db, int sm, cudaS
                                               : k_norm_back<TX, TY, TW, V, MOST, 1, 512>;
         // warps' sums to add up, or all sums of a wide block: 16 elements a thread, two floats each
         const size_t smem = wide ? (size_t)block.x * 16 * 8 : block.y > 1 ? block.y * (size_t)j.cols * 4 : 0;
-        if (smem > 49152) {
+        if (smem > PLAIN_SMEM) {
             const cudaError_t a = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
             if (a != cudaSuccess) return cuda_error(a, "cudaFuncSetAttribute(k_norm_back)");
         }

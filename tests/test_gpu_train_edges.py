@@ -124,3 +124,22 @@ def test_the_loss_may_be_changed_in_place(trop, reduction):
     loss.detach().mul_(2)  # what a program that logs the loss may do
     got, = torch.autograd.grad(loss.sum(), h)
     assert torch.equal(got, want)
+
+
+# ------------------------------------------------------------------ layer norm: shared memory
+
+
+@pytest.mark.parametrize("rows,cols,dt,wdt", [(700, 6101, F, F), (700, 6111, B, F), (700, 12231, H, H), (4900, 4001, B, F)])
+def test_layer_norm_where_static_and_dynamic_shared_memory_meet_48_kb(trop, rows, cols, dt, wdt):
+    """Widths whose dynamic shared memory is just below 48 KB, with the kernel's static arrays above it."""
+    x, dy, w, b = _normal(1, rows, cols).to(dt), _normal(2, rows, cols).to(dt), _normal(3, cols).to(wdt), _normal(4, cols).to(wdt)
+    y, mean, rstd = trop.layer_norm(x, w, b)
+    dx, dw, db = trop.layer_norm_backward(dy, x, mean, rstd, w)
+    ref = [t.double().requires_grad_() for t in (x, w, b)]
+    torch.nn.functional.layer_norm(ref[0], (cols,), ref[1], ref[2]).backward(dy.double())
+    # f32 sums of up to 12231 terms, and one rounding to the result's type (2^-8, 2^-11) in the 2-norm
+    for got, want in ((dx, ref[0].grad), (dw, ref[1].grad), (db, ref[2].grad)):
+        limit = {F: 0.0, B: 2.0 ** -8, H: 2.0 ** -11}[got.dtype] + 64 * 2.0 ** -24
+        assert float((got.double() - want).norm() / want.norm()) <= limit
+    z = (x.double() - mean.double()[:, None]) * rstd.double()[:, None] * w.double() + b.double()
+    assert float((y.double() - z).norm() / z.norm()) <= {F: 0.0, B: 2.0 ** -8, H: 2.0 ** -11}[dt] + 64 * 2.0 ** -24
