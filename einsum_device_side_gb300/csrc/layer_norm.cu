@@ -36,7 +36,10 @@
 #include <algorithm>
 #include <cstdint>
 #include <initializer_list>
+#include <mutex>
+#include <set>
 #include <type_traits>
+#include <utility>
 
 #define TROP_TU 7  // this file's id in a bounds-violation record
 #include "internal.h"
@@ -1190,6 +1193,34 @@ int norm_rows(const NormJob& j, int nv, dim3 grid, dim3 block, cudaStream_t s)
 // Dynamic shared memory that needs no attribute: a block has 48 KB in all without it, of which static arrays take
 // up to 2 KB (sh[2][32][8]).
 constexpr size_t PLAIN_SMEM = 49152 - 2048;
+// More of it.  The limit is state of the function, which every host thread shares: it is raised once for a kernel and
+// a device, to all that the device has, and never set to one call's need, which another thread's smaller
+// one could take back before the launch.
+int allow_dynamic(const void* kernel)
+{
+    struct Raised {
+        std::mutex mu;
+        std::set<std::pair<int, const void*>> kernels;
+    };
+    static Raised* const raised = new Raised();
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_error(e, "cudaGetDevice");
+    std::lock_guard<std::mutex> lk(raised->mu);
+    if (raised->kernels.count({dev, kernel})) return TROP_OK;
+    int most = 0;
+    cudaFuncAttributes a;
+    e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, kernel);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most - (int)a.sharedSizeBytes);
+    if (e != cudaSuccess) return cuda_error(e, "cudaFuncSetAttribute (layer norm)");
+    try {
+        raised->kernels.insert({dev, kernel});
+    } catch (...) {  // no memory to write it down: asked for again next time
+    }
+    return TROP_OK;
+}
 
 // Bytes of an SM's rings.
 constexpr size_t RING_BYTES = 196608;
@@ -1226,10 +1257,7 @@ int norm_forward(const NormJob& j, int sm, cudaStream_t s)
             const auto kernel = nv == 1   ? k_norm_off<TX, TW, V, 1, 4>
                                 : nv == 2 ? k_norm_off<TX, TW, V, 2, 2>
                                           : k_norm_off<TX, TW, V, 4, sizeof(TX) == 2 ? 1 : 2>;
-            if (smem > PLAIN_SMEM) {
-                const cudaError_t a = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-                if (a != cudaSuccess) return cuda_error(a, "cudaFuncSetAttribute(k_norm_off)");
-            }
+            if (smem > PLAIN_SMEM) TROP_TRY(allow_dynamic((const void*)kernel));
             int per_sm = 0;  // as many blocks as run at once: none waits for a place
             const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, (int)(g * block.y), smem);
             if (e != cudaSuccess) return cuda_error(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor(k_norm_off)");
@@ -1345,10 +1373,7 @@ int norm_backward(NormJob j, const NormVec& dw, const NormVec& db, int sm, cudaS
             const size_t smem = off_wide ? off_g * 16 * (8 + sizeof(TW)) : off_block.y > 1 ? off_block.y * (size_t)j.cols * 4 : 0;
             const auto kernel = off_wide ? k_norm_back_off<TX, TW, V, 16 / V, 1, true>
                                          : k_norm_back_off<TX, TW, V, 8 / V, 4, false>;
-            if (smem > PLAIN_SMEM) {
-                const cudaError_t a = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-                if (a != cudaSuccess) return cuda_error(a, "cudaFuncSetAttribute(k_norm_back_off)");
-            }
+            if (smem > PLAIN_SMEM) TROP_TRY(allow_dynamic((const void*)kernel));
             TROP_LAUNCH(kernel, dim3((unsigned)blocks), off_block, smem, j, period);
         }
     } else if (!fits) {
@@ -1363,8 +1388,7 @@ int norm_backward(NormJob j, const NormVec& dw, const NormVec& db, int sm, cudaS
         const auto kernel = nv == 1   ? k_norm_back_ring<TX, TY, TW, V, 1, 512>
                             : nv == 2 ? k_norm_back_ring<TX, TY, TW, V, 2, 512>
                                       : k_norm_back_ring<TX, TY, TW, V, MOST, 512>;
-        const cudaError_t a = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (a != cudaSuccess) return cuda_error(a, "cudaFuncSetAttribute(k_norm_back_ring)");
+        TROP_TRY(allow_dynamic((const void*)kernel));
         TROP_LAUNCH(kernel, grid, block, smem, j, stages, error);
     } else {
         const dim3 grid((unsigned)blocks);
@@ -1381,10 +1405,7 @@ int norm_backward(NormJob j, const NormVec& dw, const NormVec& db, int sm, cudaS
                                               : k_norm_back<TX, TY, TW, V, MOST, 1, 512>;
         // warps' sums to add up, or all sums of a wide block: 16 elements a thread, two floats each
         const size_t smem = wide ? (size_t)block.x * 16 * 8 : block.y > 1 ? block.y * (size_t)j.cols * 4 : 0;
-        if (smem > PLAIN_SMEM) {
-            const cudaError_t a = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-            if (a != cudaSuccess) return cuda_error(a, "cudaFuncSetAttribute(k_norm_back)");
-        }
+        if (smem > PLAIN_SMEM) TROP_TRY(allow_dynamic((const void*)kernel));
         TROP_LAUNCH(kernel, grid, block, smem, j);
     }
     if (sums) {

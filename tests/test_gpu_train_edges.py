@@ -143,3 +143,34 @@ def test_layer_norm_where_static_and_dynamic_shared_memory_meet_48_kb(trop, rows
         assert float((got.double() - want).norm() / want.norm()) <= limit
     z = (x.double() - mean.double()[:, None]) * rstd.double()[:, None] * w.double() + b.double()
     assert float((y.double() - z).norm() / z.norm()) <= {F: 0.0, B: 2.0 ** -8, H: 2.0 ** -11}[dt] + 64 * 2.0 ** -24
+
+
+def test_layer_norm_from_two_threads_with_other_widths(trop):
+    """Two host threads, each with its stream, on one kernel with different amounts of shared memory: no call may lose its
+    limit to the other's."""
+    import threading
+
+    cases, errors = [], []
+    for seed, (rows, cols) in enumerate(((640, 4096), (2560, 1024))):
+        x, dy, w = _normal(seed, rows, cols), _normal(seed + 2, rows, cols), _normal(seed + 4, cols)
+        _, mean, rstd = trop.layer_norm(x, w)
+        cases.append((dy, x, mean, rstd, w))
+    want = [trop.layer_norm_backward(*c) for c in cases]
+    torch.cuda.synchronize()
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(1500):
+                    got = trop.layer_norm_backward(*cases[i])
+                assert all(torch.equal(a, b) for a, b in zip(got, want[i]))
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
