@@ -83,11 +83,30 @@ enum { ST_ALLOC, ST_HIT, ST_MALLOC, ST_RETIRED, ST_RELEASED, ST_EVWAIT, ST_LEAKE
 int pool_alloc(size_t bytes, cudaStream_t stream, void** out);
 void pool_retire(void* ptr, cudaStream_t stream);
 
-// A block of at most SCRATCH_MOST bytes that stays the stream's (scratch.cpp): false where it is larger
-// or the launches are being captured, and the pool has to serve.  One block per call; it is valid in
-// stream order until the next call on this stream from this host thread.
+// A call's workspace (scratch.cpp): one block of parts, from what the stream keeps where that serves, else from the
+// pool; where the caller captures the call, memory of the captured graph.  It is valid in stream order until the
+// next call on this stream from this host thread.  Every call takes one at most: a second would be the same
+// memory.
 constexpr size_t SCRATCH_MOST = 16u << 20;
-bool stream_scratch(size_t bytes, cudaStream_t s, void** out);
+struct Workspace {
+    cudaStream_t s;
+    size_t bytes = 0;
+    char* base = nullptr;
+    void* own = nullptr;  // to be given back
+    bool captured = false;
+    size_t at_ticket = 0;
+    explicit Workspace(cudaStream_t st) : s(st) {}
+    Workspace(const Workspace&) = delete;
+    ~Workspace();
+    size_t add(size_t n)  // a part's offset
+    {
+        const size_t at = bytes;
+        bytes += (n + 255) / 256 * 256;
+        return at;
+    }
+    int take();
+    int ticket(uint32_t** out);  // after take(): a zeroed arrival counter, which the kernels leave at zero
+};
 void release_scratch();  // the caller has synchronised
 
 // Zeroed per-stream counters for atomic arrival tickets (the kernels reset them to zero).

@@ -1351,19 +1351,14 @@ int norm_backward(NormJob j, const NormVec& dw, const NormVec& db, int sm, cudaS
                                         (int64_t)sm * std::max<int>(1, 512 / (int)(block.x * block.y)));
     else blocks = (int)std::min<int64_t>(j.rows, std::max<int64_t>(1, (int64_t)sm * 8 * 256 / j.cols));
     const size_t bytes = (size_t)blocks * j.cols * 4, spaced = (bytes + 255) / 256 * 256;
-    struct Workspace {
-        void* p = nullptr;
-        cudaStream_t s;
-        ~Workspace() { if (p) pool_retire(p, s); }
-    } ws;
-    ws.s = s;
-    void* part = nullptr;
-    if (sums && !stream_scratch(2 * spaced, s, &part)) {
-        TROP_TRY(pool_alloc(2 * spaced, s, &part));
-        ws.p = part;
+    Workspace ws(s);
+    if (sums) {
+        ws.add(2 * spaced);
+        TROP_TRY(ws.take());
     }
+    char* const part = ws.base;
     void* const pw = dw.p ? part : nullptr;
-    void* const pb = db.p ? (char*)part + spaced : nullptr;
+    void* const pb = db.p ? part + spaced : nullptr;
     j.part_w = (float*)pw;
     j.part_b = (float*)pb;
     j.sp_pw = span_bytes(pw, bytes);

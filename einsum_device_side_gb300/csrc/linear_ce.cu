@@ -855,36 +855,6 @@ struct Matrix16 {
     int64_t rows, cols, ld;
 };
 
-// A call's workspace: one block of parts, from what the stream keeps where that serves, else from the pool and
-// given back in any case.  Every call takes one at most: a second would be the same memory.
-struct Workspace {
-    cudaStream_t s;
-    size_t bytes = 0;
-    char* base = nullptr;
-    void* own = nullptr;
-    explicit Workspace(cudaStream_t st) : s(st) {}
-    ~Workspace()
-    {
-        if (own) pool_retire(own, s);
-    }
-    size_t add(size_t n)  // a part's offset
-    {
-        const size_t at = bytes;
-        bytes += (n + 255) / 256 * 256;
-        return at;
-    }
-    int take()
-    {
-        void* p = nullptr;
-        if (bytes && !stream_scratch(bytes, s, &p)) {
-            TROP_TRY(pool_alloc(bytes, s, &p));
-            own = p;
-        }
-        base = (char*)p;
-        return TROP_OK;
-    }
-};
-
 int grid_for(int64_t n, int sm) { return (int)std::min<int64_t>((n + 255) / 256, (int64_t)sm * 8); }
 
 // The operands as TMA can read them: themselves, or packed copies, both made by one launch.
@@ -1028,11 +998,11 @@ int launch_linear_ce(const LinearCe& q, float* loss, float* lse, float* total, f
     t.sp_lse = span_bytes(t.lse, (size_t)t.rows * 4);
     t.sp_total = span_bytes(t.total, 4);
     t.sp_kept = span_bytes(t.kept, 4);
-    TROP_TRY(stream_tickets(s, 1, &t.ticket));
     const size_t sums = (size_t)std::max(1, cdiv(t.rows, 32)) * sizeof(float2);
     const size_t at_sums = ws.add(sums);
     if (t.rows == 0) {
         TROP_TRY(ws.take());
+        TROP_TRY(ws.ticket(&t.ticket));
         return launch_join(t, (float2*)(ws.base + at_sums), s);
     }
     Operand ox(q.x, ws), ow(q.w, ws);
@@ -1063,6 +1033,7 @@ int launch_linear_ce(const LinearCe& q, float* loss, float* lse, float* total, f
     const size_t pairs = (size_t)t.G * t.stride * sizeof(float2), at = (size_t)(x.rows + 63) / 64 * 64 * 4;
     const size_t at_part = ws.add(pairs), at_logit = ws.add(at);
     TROP_TRY(ws.take());
+    TROP_TRY(ws.ticket(&t.ticket));
     TROP_TRY(pack(ox, ow, ws, sm));
     t.part = j.part = (float2*)(ws.base + at_part);
     t.at = j.at = (float*)(ws.base + at_logit);

@@ -1,4 +1,4 @@
-// scratch.cpp -- small workspace that a stream keeps.
+// scratch.cpp -- the workspace of a call of the training operators.
 //
 // A pool block costs its call an event and a look at every block still retiring (several us of host
 // time when calls follow one another closely).  Calls that need a few MB take them here instead: one
@@ -6,6 +6,9 @@
 // nothing has to be retired.  The thread is part of the key because two threads may enqueue on one
 // stream at once, and their calls' launches then interleave.  A larger request replaces the block;
 // the old one, which earlier launches may still use, is kept until tropical_release_pool.
+//
+// Launches that the caller captures into a graph outlive the call and are replayed in any order with
+// other calls: their workspace is allocated and freed by nodes of that graph, and so is its ticket.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -41,17 +44,10 @@ uint64_t thread_number()
     return mine;
 }
 
-}  // namespace
-
+// A block of at most SCRATCH_MOST bytes that stays the stream's and the thread's; false where the pool has to serve.
 bool stream_scratch(size_t bytes, cudaStream_t s, void** out)
 {
     if (bytes > SCRATCH_MOST || capture_arena()) return false;
-    // a captured launch outlives the call, and is replayed on other streams: its workspace is its own
-    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(s, &cap) != cudaSuccess || cap != cudaStreamCaptureStatusNone) {
-        cudaGetLastError();
-        return false;
-    }
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) {
         cudaGetLastError();
@@ -73,6 +69,48 @@ bool stream_scratch(size_t bytes, cudaStream_t s, void** out)
     }
     *out = k.p;
     return true;
+}
+
+}  // namespace
+
+Workspace::~Workspace()
+{
+    if (!own) return;
+    if (captured) {
+        if (cudaFreeAsync(own, s) != cudaSuccess) cudaGetLastError();  // (the capture has failed: its end says so)
+    } else {
+        pool_retire(own, s);
+    }
+}
+
+int Workspace::take()
+{
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    if (!capture_arena()) {
+        const cudaError_t e = cudaStreamIsCapturing(s, &status);
+        if (e != cudaSuccess) return cuda_error(e, "cudaStreamIsCapturing");
+    }
+    captured = status != cudaStreamCaptureStatusNone;
+    void* p = nullptr;
+    if (captured) {
+        at_ticket = add(sizeof(uint32_t));
+        const cudaError_t e = cudaMallocAsync(&p, bytes, s);
+        if (e != cudaSuccess) return cuda_error(e, "cudaMallocAsync (captured workspace)");
+        own = p;
+    } else if (bytes && !stream_scratch(bytes, s, &p)) {
+        TROP_TRY(pool_alloc(bytes, s, &p));
+        own = p;
+    }
+    base = (char*)p;
+    return TROP_OK;
+}
+
+int Workspace::ticket(uint32_t** out)
+{
+    if (!captured) return stream_tickets(s, 1, out);
+    *out = (uint32_t*)(base + at_ticket);
+    const cudaError_t e = cudaMemsetAsync(*out, 0, sizeof(uint32_t), s);
+    return e == cudaSuccess ? (int)TROP_OK : cuda_error(e, "cudaMemsetAsync (captured ticket)");
 }
 
 void release_scratch()

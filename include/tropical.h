@@ -364,7 +364,9 @@ int tropical_tree_backtrack(int n_inputs, const trop_tensor* inputs, int n_nodes
  * these complete; they have no counterpart on the pages].  Types: f32, bf16,
  * f16 as stated at each; every sum and statistic is held in f32 and every
  * stored value rounded once.  Results repeat bit for bit (no atomics in any
- * sum).  The conventions at the top of this file hold.
+ * sum).  The conventions at the top of this file hold.  The calls may be captured
+ * into a CUDA graph by the caller (after one call on the device outside the
+ * capture); workspace is then allocated and freed by nodes of that graph.
  * ------------------------------------------------------------------------- */
 
 /* Layer norm over the last axis of x [rows, cols]:

@@ -174,3 +174,59 @@ def test_layer_norm_from_two_threads_with_other_widths(trop):
         t.join()
     torch.cuda.synchronize()
     assert not errors, errors
+
+
+# ------------------------------------------------------------------ captured by the caller
+
+
+def _captured(f):
+    """f's results in a graph: (graph, results)."""
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = f()
+    return graph, out
+
+
+def _replayed_beside_eager_calls(f, inputs, others):
+    """A captured f replays with new inputs on another stream, while the stream of the capture and the current one make
+    eager calls of the same sizes."""
+    f()  # the device's first call, outside the capture
+    torch.cuda.synchronize()
+    graph, out = _captured(f)
+    side = torch.cuda.Stream()
+    for k in range(4):
+        values = [t.clone() if k % 2 else u.clone() for t, u in zip(inputs, others)]
+        for t, u in zip(inputs, values):
+            t.copy_(u)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            graph.replay()
+        eager = [f() for _ in range(3)]  # (in the way of the replay's workspace, if it were shared)
+        torch.cuda.synchronize()
+        for e in eager:
+            assert all(torch.equal(a, b) for a, b in zip(out, e))
+
+
+@pytest.mark.parametrize("rows,cols,dt", [(3, 40, F), (2500, 1001, B), (700, 2048, F)])
+def test_layer_norm_captured(trop, rows, cols, dt):
+    x, dy, w = _normal(1, rows, cols).to(dt), _normal(2, rows, cols).to(dt), _normal(3, cols).to(dt)
+
+    def f():
+        y, mean, rstd = trop.layer_norm(x, w)
+        return (y, mean, rstd, *trop.layer_norm_backward(dy, x, mean, rstd, w))
+
+    _replayed_beside_eager_calls(f, (x, dy, w), (2 * x.flip(0), dy.flip(1), w.flip(0)))
+
+
+@pytest.mark.parametrize("n,d,v", [(7, 64, 300), (300, 96, 1000), (1100, 65, 9001)])
+def test_head_captured(trop, n, d, v):
+    x, w = _normal(1, n, d).to(B), (_normal(2, v, d) / 4).to(B)
+    t = torch.randint(0, v, (n,), device="cuda")
+    t[::5] = IGNORE
+    g = torch.rand(n, device="cuda") + 0.5
+
+    def f():
+        loss, lse, kept = trop.linear_cross_entropy(x, w, t)
+        return (loss, lse, kept, *trop.linear_cross_entropy_backward(g, x, w, t, lse))
+
+    _replayed_beside_eager_calls(f, (x, w, t, g), (x.flip(0), w.flip(0), t.flip(0), g.flip(0)))
