@@ -4,8 +4,9 @@
 // time when calls follow one another closely).  Calls that need a few MB take them here instead: one
 // block per (device, stream, host thread), used by one call after the other in stream order, so that
 // nothing has to be retired.  The thread is part of the key because two threads may enqueue on one
-// stream at once, and their calls' launches then interleave.  A larger request replaces the block;
-// the old one, which earlier launches may still use, is kept until tropical_release_pool.
+// stream at once, and their calls' launches then interleave.  A thread that ends leaves its blocks to the
+// next thread on their streams.  A larger request replaces the block; the old one, which earlier
+// launches may still use, is kept until tropical_release_pool.
 //
 // Launches that the caller captures into a graph outlive the call and are replayed in any order with
 // other calls: their workspace is allocated and freed by nodes of that graph, and so is its ticket.
@@ -14,7 +15,7 @@
 #include <atomic>
 #include <map>
 #include <mutex>
-#include <tuple>
+#include <utility>
 #include <vector>
 
 #include "internal.h"
@@ -22,14 +23,18 @@
 namespace trop {
 namespace {
 
+constexpr uint64_t NOBODY = ~0ull;  // a block whose thread has ended
+constexpr size_t MOST_BLOCKS = 64;  // kept in all; calls on further streams and threads use the pool
 struct Kept {
     void* p;
     size_t bytes;
+    uint64_t thread;
 };
-using Key = std::tuple<int, cudaStream_t, uint64_t>;
+using Key = std::pair<int, cudaStream_t>;
 struct Scratch {
     std::mutex mu;
-    std::map<Key, Kept> blocks;
+    std::map<Key, std::vector<Kept>> streams;
+    size_t blocks = 0;
     std::vector<std::pair<int, void*>> replaced;
 };
 Scratch& scratch()
@@ -37,12 +42,22 @@ Scratch& scratch()
     static Scratch* s = new Scratch();
     return *s;
 }
-uint64_t thread_number()
-{
-    static std::atomic<uint64_t> next{0};
-    static thread_local const uint64_t mine = next.fetch_add(1);
-    return mine;
-}
+struct Thread {
+    uint64_t number;
+    Thread()
+    {
+        static std::atomic<uint64_t> next{0};
+        number = next.fetch_add(1);
+    }
+    ~Thread()
+    {
+        Scratch& S = scratch();
+        std::lock_guard<std::mutex> lk(S.mu);
+        for (auto& s : S.streams)
+            for (Kept& k : s.second)
+                if (k.thread == number) k.thread = NOBODY;
+    }
+};
 
 // A block of at most SCRATCH_MOST bytes that stays the stream's and the thread's; false where the pool has to serve.
 bool stream_scratch(size_t bytes, cudaStream_t s, void** out)
@@ -53,22 +68,44 @@ bool stream_scratch(size_t bytes, cudaStream_t s, void** out)
         cudaGetLastError();
         return false;
     }
+    static thread_local const Thread me;
     Scratch& S = scratch();
     std::lock_guard<std::mutex> lk(S.mu);
-    Kept& k = S.blocks[Key(dev, s, thread_number())];
-    if (k.bytes < bytes) {
-        size_t want = 65536;
-        while (want < bytes) want *= 2;
-        void* p = nullptr;
-        if (cudaMalloc(&p, want) != cudaSuccess) {
-            cudaGetLastError();
-            return false;
+    try {
+        std::vector<Kept>& kept = S.streams[Key(dev, s)];
+        Kept* k = nullptr;
+        for (Kept& q : kept)
+            if (q.thread == me.number) k = &q;
+        if (!k)  // (all its launches are ahead of this call's on the stream)
+            for (Kept& q : kept)
+                if (q.thread == NOBODY) k = &q;
+        if (!k || k->bytes < bytes) {
+            if (!k && S.blocks >= MOST_BLOCKS) return false;
+            size_t want = 65536;
+            while (want < bytes) want *= 2;
+            kept.reserve(kept.size() + 1);
+            S.replaced.reserve(S.replaced.size() + 1);
+            void* p = nullptr;
+            if (cudaMalloc(&p, want) != cudaSuccess) {
+                cudaGetLastError();
+                return false;
+            }
+            if (k) {
+                S.replaced.emplace_back(dev, k->p);
+                k->p = p;
+                k->bytes = want;
+            } else {
+                kept.push_back(Kept{p, want, me.number});
+                k = &kept.back();
+                ++S.blocks;
+            }
         }
-        if (k.p) S.replaced.emplace_back(dev, k.p);
-        k = Kept{p, want};
+        k->thread = me.number;
+        *out = k->p;
+        return true;
+    } catch (...) {  // no host memory for the table
+        return false;
     }
-    *out = k.p;
-    return true;
 }
 
 }  // namespace
@@ -117,17 +154,18 @@ void release_scratch()
 {
     Scratch& S = scratch();
     std::lock_guard<std::mutex> lk(S.mu);
-    for (auto& b : S.blocks)
-        if (b.second.p) {
-            cudaSetDevice(std::get<0>(b.first));
-            cudaFree(b.second.p);
+    for (auto& s : S.streams)
+        for (Kept& k : s.second) {
+            cudaSetDevice(s.first.first);
+            cudaFree(k.p);
         }
     for (auto& r : S.replaced) {
         cudaSetDevice(r.first);
         cudaFree(r.second);
     }
-    S.blocks.clear();
+    S.streams.clear();
     S.replaced.clear();
+    S.blocks = 0;
 }
 
 }  // namespace trop

@@ -230,3 +230,32 @@ def test_head_captured(trop, n, d, v):
         return (loss, lse, kept, *trop.linear_cross_entropy_backward(g, x, w, t, lse))
 
     _replayed_beside_eager_calls(f, (x, w, t, g), (x.flip(0), w.flip(0), t.flip(0), g.flip(0)))
+
+
+# ------------------------------------------------------------------ what is kept between calls
+
+
+def test_threads_that_end_leave_their_workspace_to_the_next(trop):
+    import threading
+
+    x, dy, w = _normal(1, 2400, 2048), _normal(2, 2400, 2048), _normal(3, 2048)
+    _, mean, rstd = trop.layer_norm(x, w)
+    want = trop.layer_norm_backward(dy, x, mean, rstd, w)
+    out = []
+
+    def work():
+        out.append(trop.layer_norm_backward(dy, x, mean, rstd, w))
+
+    def run(n):
+        for _ in range(n):
+            t = threading.Thread(target=work)
+            t.start()
+            t.join()
+            got = out.pop()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+        torch.cuda.synchronize()
+
+    run(4)
+    before = torch.cuda.mem_get_info()[0]
+    run(40)  # (a block of this call is some MB)
+    assert before - torch.cuda.mem_get_info()[0] < 8 << 20
