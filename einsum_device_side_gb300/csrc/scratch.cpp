@@ -5,8 +5,9 @@
 // block per (device, stream, host thread), used by one call after the other in stream order, so that
 // nothing has to be retired.  The thread is part of the key because two threads may enqueue on one
 // stream at once, and their calls' launches then interleave.  A thread that ends leaves its blocks to the
-// next thread on their streams.  A larger request replaces the block; the old one, which earlier
-// launches may still use, is kept until tropical_release_pool.
+// next thread on their streams.  Streams are told apart by their id, which, unlike a handle, never comes
+// back after the stream was destroyed with launches still on their way.  A larger request replaces the
+// block; the old one, which earlier launches may still use, is kept until tropical_release_pool.
 //
 // Launches that the caller captures into a graph outlive the call and are replayed in any order with
 // other calls: their workspace is allocated and freed by nodes of that graph, and so is its ticket.
@@ -30,7 +31,7 @@ struct Kept {
     size_t bytes;
     uint64_t thread;
 };
-using Key = std::pair<int, cudaStream_t>;
+using Key = std::pair<int, unsigned long long>;  // device, stream id
 struct Scratch {
     std::mutex mu;
     std::map<Key, std::vector<Kept>> streams;
@@ -64,7 +65,8 @@ bool stream_scratch(size_t bytes, cudaStream_t s, void** out)
 {
     if (bytes > SCRATCH_MOST || capture_arena()) return false;
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) {
+    unsigned long long id = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaStreamGetId(s, &id) != cudaSuccess) {
         cudaGetLastError();
         return false;
     }
@@ -72,7 +74,7 @@ bool stream_scratch(size_t bytes, cudaStream_t s, void** out)
     Scratch& S = scratch();
     std::lock_guard<std::mutex> lk(S.mu);
     try {
-        std::vector<Kept>& kept = S.streams[Key(dev, s)];
+        std::vector<Kept>& kept = S.streams[Key(dev, id)];
         Kept* k = nullptr;
         for (Kept& q : kept)
             if (q.thread == me.number) k = &q;

@@ -259,3 +259,28 @@ def test_threads_that_end_leave_their_workspace_to_the_next(trop):
     before = torch.cuda.mem_get_info()[0]
     run(40)  # (a block of this call is some MB)
     assert before - torch.cuda.mem_get_info()[0] < 8 << 20
+
+
+def test_a_destroyed_stream_s_workspace_is_not_the_next_one_s(trop):
+    """A stream destroyed with its work still on its way: its handle may come back at once for a new stream, whose calls run
+    beside that work."""
+    import ctypes
+
+    runtime = torch.cuda.cudart()
+    x, dy, w = _normal(1, 2400, 1024), _normal(2, 2400, 1024), _normal(3, 1024)
+    _, mean, rstd = trop.layer_norm(x, w)
+    sets = [(dy * k, x, mean, rstd, w) for k in (1.0, 3.0)]
+    want = [trop.layer_norm_backward(*s) for s in sets]
+    torch.cuda.synchronize()
+    results = []
+    for i in range(20):
+        handle = ctypes.c_void_p()
+        assert int(runtime.cudaStreamCreate(ctypes.addressof(handle))) == 0
+        stream = torch.cuda.ExternalStream(handle.value)
+        with torch.cuda.stream(stream):
+            torch.cuda._sleep(200_000)
+            results.append(trop.layer_norm_backward(*sets[i % 2]))
+        assert int(runtime.cudaStreamDestroy(handle.value)) == 0
+    torch.cuda.synchronize()
+    for i, got in enumerate(results):
+        assert all(torch.equal(a, b) for a, b in zip(got, want[i % 2]))
