@@ -85,7 +85,7 @@ bool stream_scratch(size_t bytes, cudaStream_t s, void** out)
             if (!k && S.blocks >= MOST_BLOCKS) return false;
             size_t want = 65536;
             while (want < bytes) want *= 2;
-            kept.reserve(kept.size() + 1);
+            if (!k) kept.reserve(kept.size() + 1);  // (k points into it)
             S.replaced.reserve(S.replaced.size() + 1);
             void* p = nullptr;
             if (cudaMalloc(&p, want) != cudaSuccess) {

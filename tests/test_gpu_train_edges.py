@@ -261,6 +261,26 @@ def test_threads_that_end_leave_their_workspace_to_the_next(trop):
     assert before - torch.cuda.mem_get_info()[0] < 8 << 20
 
 
+def test_kept_workspace_grows_once(trop):
+    """A small call, then larger ones: the block is replaced once for each doubling, and kept from then on."""
+    cases = []
+    for cols in (64, 256, 1024, 4096):
+        x, w = _normal(1, 2400, cols), _normal(3, cols)
+        cases.append((_normal(2, 2400, cols), x, *trop.layer_norm(x, w)[1:], w))
+    with torch.cuda.stream(torch.cuda.Stream()):
+        for c in cases:
+            want = trop.layer_norm_backward(*c)
+        for _ in range(3):  # (the results' own memory)
+            got = trop.layer_norm_backward(*cases[-1])
+        torch.cuda.synchronize()
+        before = torch.cuda.mem_get_info()[0]
+        for _ in range(20):
+            got = trop.layer_norm_backward(*cases[-1])
+        torch.cuda.synchronize()
+        assert before - torch.cuda.mem_get_info()[0] < 8 << 20
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_a_destroyed_stream_s_workspace_is_not_the_next_one_s(trop):
     """A stream destroyed with its work still on its way: its handle may come back at once for a new stream, whose calls run
     beside that work."""
