@@ -95,6 +95,7 @@ struct Workspace {
     void* own = nullptr;  // to be given back
     bool captured = false;
     size_t at_ticket = 0;
+    uint32_t* kept_ticket = nullptr;
     explicit Workspace(cudaStream_t st) : s(st) {}
     Workspace(const Workspace&) = delete;
     ~Workspace();

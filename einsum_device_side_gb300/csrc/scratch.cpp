@@ -8,6 +8,7 @@
 // next thread on their streams.  Streams are told apart by their id, which, unlike a handle, never comes
 // back after the stream was destroyed with launches still on their way.  A larger request replaces the
 // block; the old one, which earlier launches may still use, is kept until tropical_release_pool.
+// Behind each block lies an arrival ticket, zeroed once in stream order.
 //
 // Launches that the caller captures into a graph outlive the call and are replayed in any order with
 // other calls: their workspace is allocated and freed by nodes of that graph, and so is its ticket.
@@ -25,6 +26,7 @@ namespace trop {
 namespace {
 
 constexpr uint64_t NOBODY = ~0ull;  // a block whose thread has ended
+constexpr size_t TICKET = 256;      // bytes behind a block
 constexpr size_t MOST_BLOCKS = 64;  // kept in all; calls on further streams and threads use the pool
 struct Kept {
     void* p;
@@ -60,8 +62,9 @@ struct Thread {
     }
 };
 
-// A block of at most SCRATCH_MOST bytes that stays the stream's and the thread's; false where the pool has to serve.
-bool stream_scratch(size_t bytes, cudaStream_t s, void** out)
+// A block of at most SCRATCH_MOST bytes that stays the stream's and the thread's, and its ticket; false where the pool has
+// to serve.
+bool stream_scratch(size_t bytes, cudaStream_t s, void** out, uint32_t** ticket)
 {
     if (bytes > SCRATCH_MOST || capture_arena()) return false;
     int dev = 0;
@@ -88,8 +91,13 @@ bool stream_scratch(size_t bytes, cudaStream_t s, void** out)
             if (!k) kept.reserve(kept.size() + 1);  // (k points into it)
             S.replaced.reserve(S.replaced.size() + 1);
             void* p = nullptr;
-            if (cudaMalloc(&p, want) != cudaSuccess) {
+            if (cudaMalloc(&p, want + TICKET) != cudaSuccess) {
                 cudaGetLastError();
+                return false;
+            }
+            if (cudaMemsetAsync((char*)p + want, 0, TICKET, s) != cudaSuccess) {
+                cudaGetLastError();
+                cudaFree(p);
                 return false;
             }
             if (k) {
@@ -104,6 +112,7 @@ bool stream_scratch(size_t bytes, cudaStream_t s, void** out)
         }
         k->thread = me.number;
         *out = k->p;
+        *ticket = (uint32_t*)((char*)k->p + k->bytes);
         return true;
     } catch (...) {  // no host memory for the table
         return false;
@@ -136,7 +145,8 @@ int Workspace::take()
         const cudaError_t e = cudaMallocAsync(&p, bytes, s);
         if (e != cudaSuccess) return cuda_error(e, "cudaMallocAsync (captured workspace)");
         own = p;
-    } else if (bytes && !stream_scratch(bytes, s, &p)) {
+    } else if (!stream_scratch(bytes, s, &p, &kept_ticket)) {
+        if (bytes > SCRATCH_MOST) (void)stream_scratch(0, s, &p, &kept_ticket);
         TROP_TRY(pool_alloc(bytes, s, &p));
         own = p;
     }
@@ -146,7 +156,10 @@ int Workspace::take()
 
 int Workspace::ticket(uint32_t** out)
 {
-    if (!captured) return stream_tickets(s, 1, out);
+    if (!captured) {
+        *out = kept_ticket;
+        return kept_ticket ? (int)TROP_OK : stream_tickets(s, 1, out);
+    }
     *out = (uint32_t*)(base + at_ticket);
     const cudaError_t e = cudaMemsetAsync(*out, 0, sizeof(uint32_t), s);
     return e == cudaSuccess ? (int)TROP_OK : cuda_error(e, "cudaMemsetAsync (captured ticket)");

@@ -304,3 +304,26 @@ def test_a_destroyed_stream_s_workspace_is_not_the_next_one_s(trop):
     torch.cuda.synchronize()
     for i, got in enumerate(results):
         assert all(torch.equal(a, b) for a, b in zip(got, want[i % 2]))
+
+
+def test_a_destroyed_stream_s_ticket_is_not_the_next_one_s(trop):
+    """The same for the counter by which the head's last block to finish joins the pairs."""
+    import ctypes
+
+    runtime = torch.cuda.cudart()
+    t = torch.randint(0, 3000, (700,), device="cuda")
+    sets = [((_normal(1, n, 64) * k).to(B), (_normal(2, 3000, 64) / 4).to(B), t[:n]) for n in (20, 700) for k in (1.0, 3.0)]
+    want = [trop.linear_cross_entropy(*s) for s in sets]
+    torch.cuda.synchronize()
+    results = []
+    for i in range(40):
+        handle = ctypes.c_void_p()
+        assert int(runtime.cudaStreamCreate(ctypes.addressof(handle))) == 0
+        stream = torch.cuda.ExternalStream(handle.value)
+        with torch.cuda.stream(stream):
+            torch.cuda._sleep(200_000)
+            results.append(trop.linear_cross_entropy(*sets[i % 4]))
+        assert int(runtime.cudaStreamDestroy(handle.value)) == 0
+    torch.cuda.synchronize()
+    for i, got in enumerate(results):
+        assert all(torch.equal(a, b) for a, b in zip(got, want[i % 4]))
