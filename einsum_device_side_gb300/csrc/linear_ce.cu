@@ -101,10 +101,10 @@ __device__ __forceinline__ int64_t target_of(const Targets& t, int64_t i)
 }
 
 // The tokens' gradients g[i * sg] (over *count, where that is given), and how P is stored for the 16-bit
-// products: times `top` / max |g|, undone in f32 when the products leave.  A target's entry, g (p - 1),
-// is then close to -top when p is small, a value the type holds; g itself would be rounded by the
-// same factor for every token of a batch (0.3 % of all gradients for an unlucky 1 / 7783).  In f16
-// top = 2^14 besides lifts P's entries of g / V into the type's range.
+// products: times `top` / max |g| over the tokens that count, undone in f32 when the products leave.  A
+// target's entry, g (p - 1), is then close to -top when p is small, a value the type holds; g itself would be
+// rounded by the same factor for every token of a batch (0.3 % of all gradients for an unlucky 1 / 7783).  In
+// f16 top = 2^14 besides lifts P's entries of g / V into the type's range.
 struct GradScale {
     const float* g;
     int64_t sg;
@@ -659,13 +659,18 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // ------------------------------------------------------------------ the largest gradient of a batch
-__global__ void __launch_bounds__(1024) k_gscale(const GradScale q, int64_t n, float* scale)
+// Of the tokens that count (an ignored one's P is zero whatever its gradient) and of finite values: one infinite
+// gradient spoils its own token's row, not the others' digits.
+__global__ void __launch_bounds__(1024) k_gscale(const GradScale q, const Targets t, int64_t n, float* scale)
 {
     pdl_wait();
     pdl_signal();
     __shared__ float red[32];
     float m = 0.f;
-    for (int64_t i = threadIdx.x; i < n; i += 1024) m = fmaxf(m, fabsf(grad_of(q, i)));
+    for (int64_t i = threadIdx.x; i < n; i += 1024) {
+        const float v = fabsf(grad_of(q, i));
+        if (target_of(t, i) >= 0 && v < INFINITY) m = fmaxf(m, v);
+    }
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
     __syncthreads();
@@ -1122,7 +1127,7 @@ int launch_linear_ce_backward(const LinearCe& q, const float* g, int64_t sg, con
     const int64_t gsize[1] = {N}, gstride[1] = {sg};
     GradScale grad = {g, sg, kept, nullptr, q.bf16 ? 1.f : 16384.f, span_of(g, 4, 1, gsize, gstride)};
     if (sg != 0) {
-        const cudaError_t e = launch_pdl(k_gscale, dim3(1), dim3(1024), 0, s, grad, N, scale);
+        const cudaError_t e = launch_pdl(k_gscale, dim3(1), dim3(1024), 0, s, grad, targets_of(q), N, scale);
         if (e != cudaSuccess) return cuda_error(e, "k_gscale launch");
         count_launches(1);
         grad.given = scale;

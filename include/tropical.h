@@ -416,8 +416,8 @@ int tropical_linear_cross_entropy(const trop_tensor* x, const trop_tensor* w, co
  *   dx = P w,  dw = P^T x.
  * The logits are formed again, in pieces of the vocabulary; P is rounded to
  * the operands' type for the two products, scaled by 1 / max |g| (in f16 by
- * 2^14 / max |g|, so that small probabilities keep their digits), which is
- * undone in their f32 sums.
+ * 2^14 / max |g|, so that small probabilities keep their digits; the largest
+ * finite one of the tokens that count), which is undone in their f32 sums.
  * dx, dw: nullable, the operands' type and shapes, last axis contiguous.
  * Workspace: P of one piece (at most 512 MiB, or 4096 columns), and the f32
  * sums of dx when its depth is split or comes in several pieces.

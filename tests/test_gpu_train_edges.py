@@ -327,3 +327,28 @@ def test_a_destroyed_stream_s_ticket_is_not_the_next_one_s(trop):
     torch.cuda.synchronize()
     for i, got in enumerate(results):
         assert all(torch.equal(a, b) for a, b in zip(got, want[i % 4]))
+
+
+# ------------------------------------------------------------------ the head's gradients
+
+
+@pytest.mark.parametrize("dt", [B, H])
+@pytest.mark.parametrize("n", [60, 300])
+def test_a_padded_token_s_gradient_counts_nowhere(trop, n, dt):
+    """Whatever it is, the others' gradients stay as they are, bit for bit."""
+    x, w = _normal(1, n, 64).to(dt), (_normal(2, 900, 64) / 4).to(dt)
+    t = torch.randint(0, 900, (n,), device="cuda", generator=torch.Generator("cuda").manual_seed(3))
+    t[5], t[n - 1] = IGNORE, IGNORE
+    _, lse, _ = trop.linear_cross_entropy(x, w, t, "none")
+    g = torch.full((n,), 1 / 8192, device="cuda")
+    dx, dw = trop.linear_cross_entropy_backward(g, x, w, t, lse)
+    for pad in (1e9, float("inf"), float("nan")):
+        g[5], g[n - 1] = pad, -pad
+        px, pw = trop.linear_cross_entropy_backward(g, x, w, t, lse)
+        assert torch.equal(px, dx) and torch.equal(pw, dw)
+    # a kept token's infinite gradient is its own row's
+    g[5] = g[n - 1] = 1 / 8192
+    g[7] = float("inf")
+    px, _ = trop.linear_cross_entropy_backward(g, x, w, t, lse)
+    rest = torch.arange(n, device="cuda") != 7
+    assert torch.equal(px[rest], dx[rest]) and not bool(px[7].isfinite().any())
