@@ -116,6 +116,7 @@ struct GradScale {
 __device__ __forceinline__ float2 scale_of(float m, float top)
 {
     const bool fine = m > 0.f && m < INFINITY;  // nothing kept, all zero, or not finite: P as it is
+    m = fmaxf(m, 7.888609e-31f);  // 2^-100: top / m stays finite; products of smaller gradients round to f16's zero anyway
     return fine ? make_float2(__fdiv_rn(top, m), __fdiv_rn(m, top)) : make_float2(1.f, 1.f);
 }
 __device__ __forceinline__ float grad_of(const GradScale& q, int64_t i)

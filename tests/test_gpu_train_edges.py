@@ -352,3 +352,21 @@ def test_a_padded_token_s_gradient_counts_nowhere(trop, n, dt):
     px, _ = trop.linear_cross_entropy_backward(g, x, w, t, lse)
     rest = torch.arange(n, device="cuda") != 7
     assert torch.equal(px[rest], dx[rest]) and not bool(px[7].isfinite().any())
+
+
+@pytest.mark.parametrize("each", [False, True])
+@pytest.mark.parametrize("n", [60, 300])
+def test_gradients_of_a_subnormal_loss_gradient(trop, n, each):
+    """A gradient of 2^-130: in bf16 the gradients of 1 times 2^-130, to a place of the subnormals; in f16 zero."""
+    for dt in (B, H):
+        x, w = _normal(1, n, 64).to(dt), (_normal(2, 900, 64) / 4).to(dt)
+        t = torch.randint(0, 900, (n,), device="cuda", generator=torch.Generator("cuda").manual_seed(3))
+        _, lse, _ = trop.linear_cross_entropy(x, w, t, "none")
+        one = torch.ones(n if each else (), device="cuda")
+        want = trop.linear_cross_entropy_backward(one, x, w, t, lse)
+        got = trop.linear_cross_entropy_backward(one * 2.0 ** -130, x, w, t, lse)
+        for a, b in zip(got, want):
+            if dt == H:
+                assert not bool(a.any())
+            else:
+                assert float((a.double() - b.double() * 2.0 ** -130).abs().max()) <= 2.0 ** -133
