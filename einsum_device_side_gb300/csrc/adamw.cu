@@ -242,8 +242,8 @@ __global__ void __launch_bounds__(256) k_adamw(const __grid_constant__ TAB tab, 
 
 // A warp per block of 256: lane l has elements 4 l .. and 128 + 4 l .., so that every access of the
 // warp is contiguous.  The largest magnitude is taken over the values' bits, which order like the
-// magnitudes and let a NaN win: a block with a NaN or an infinity has a scale that is not finite,
-// and all of it reads back as NaN.
+// magnitudes and let a NaN win: a block with a NaN or an infinity has a scale of NaN (an infinite one
+// would leave its largest entry infinite and make NaN of the others), so all of it reads back as NaN.
 template <typename TP, typename TG>
 struct Block8 {
     Raw<TP, 4> p[2];
@@ -345,8 +345,8 @@ __device__ __forceinline__ void step_block(const trop_adamw_tensor& t, int64_t b
         const int64_t scales = (t.numel + BLOCK - 1) / BLOCK * 4;
         float* ps = t.exp_avg_scale + base / BLOCK;
         float* qs = t.exp_avg_sq_scale + base / BLOCK;
-        if (TROP_IN(ps, 4, span_bytes_dev(t.exp_avg_scale, scales, rep))) *ps = __fmul_rn(mt, 1.f / 16129.f);
-        if (TROP_IN(qs, 4, span_bytes_dev(t.exp_avg_sq_scale, scales, rep))) *qs = __fmul_rn(rt, 1.f / 65025.f);
+        if (TROP_IN(ps, 4, span_bytes_dev(t.exp_avg_scale, scales, rep))) *ps = mt < INFINITY ? __fmul_rn(mt, 1.f / 16129.f) : NAN;
+        if (TROP_IN(qs, 4, span_bytes_dev(t.exp_avg_sq_scale, scales, rep))) *qs = rt < INFINITY ? __fmul_rn(rt, 1.f / 65025.f) : NAN;
         (void)scales;
     }
 }

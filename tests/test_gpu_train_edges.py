@@ -370,3 +370,20 @@ def test_gradients_of_a_subnormal_loss_gradient(trop, n, each):
                 assert not bool(a.any())
             else:
                 assert float((a.double() - b.double() * 2.0 ** -130).abs().max()) <= 2.0 ** -133
+
+
+# ------------------------------------------------------------------ AdamW
+
+
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), 1e30, float("nan")])
+def test_an_8_bit_block_with_a_state_that_is_not_finite_reads_back_as_nan(trop, bad):
+    """All of the block, the entry itself among it (of 1e30 the square overflows: v, not m)."""
+    p, g = [_normal(1, 600)], [_normal(2, 600)]
+    g[0][300] = bad
+    opt = trop.AdamW(p, g, state_bits=8)
+    opt.step()
+    m, v = trop.adamw_state_values(opt.exp_avg, opt.exp_avg_sq, opt.exp_avg_scale, opt.exp_avg_sq_scale)
+    block = torch.zeros(600, dtype=torch.bool, device="cuda")
+    block[256:512] = True
+    assert torch.equal(v[0].isnan(), block) and bool(v[0][~block].isfinite().all())
+    assert torch.equal(m[0].isnan(), block) if bad != 1e30 else bool(m[0].isfinite().all())
