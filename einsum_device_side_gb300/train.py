@@ -70,6 +70,13 @@ def _stream_object(stream):
     return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream.cuda_stream)
 
 
+def _capturing(stream) -> bool:
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(_stream_object(stream)):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _on_stream(f, stream, *args, **kwargs):
     """``f`` with `stream` current: the copies it makes and the results it allocates then belong to the stream its kernels
     run on, in order with them.  The allocator is told of the tensors that one stream owns and the other uses, so that it
@@ -473,7 +480,8 @@ class AdamWPlan:
 
     def step(self, step: int, lr: float = 1e-3, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
              weight_decay: float = 0.01, grad_scale: float = 1.0, stream=None):
-        """One step; ``step`` counts from 1."""
+        """One step; ``step`` counts from 1.  Captured into a CUDA graph it replays with this step number and these
+        options: of use where the bias corrections are near 1."""
         if self._h is None:
             raise RuntimeError("plan is closed")
         if stream is not None:
@@ -520,7 +528,8 @@ class AdamWPlan:
 class AdamW:
     """AdamW with its states: ``AdamW(params, grads, state_bits=8)``, then ``step()`` whenever the gradients' buffers hold
     new ones.  ``grads`` are the buffers the backward pass writes (``p.grad`` of each parameter by default, which must
-    exist and stay in place).  ``copies`` as in ``adamw_step``."""
+    exist and stay in place).  ``copies`` as in ``adamw_step``.  It counts its steps on the host, so a step cannot be
+    captured into a CUDA graph (``AdamWPlan.step`` can, with the step number given)."""
 
     def __init__(self, params, grads=None, lr: float = 1e-3, beta1: float = 0.9, beta2: float = 0.999,
                  eps: float = 1e-8, weight_decay: float = 0.01, state_bits: int = 32, copies=None):
@@ -548,5 +557,7 @@ class AdamW:
                                self.exp_avg_sq_scale, copies=copies)
 
     def step(self, grad_scale: float = 1.0, stream=None):
+        if _capturing(stream):
+            _fail(-10, "a captured step would repeat its bias corrections at every replay: AdamW counts steps on the host")
         self.steps += 1
         self._plan.step(self.steps, grad_scale=grad_scale, stream=stream, **self.options)

@@ -366,7 +366,9 @@ int tropical_tree_backtrack(int n_inputs, const trop_tensor* inputs, int n_nodes
  * stored value rounded once.  Results repeat bit for bit (no atomics in any
  * sum).  The conventions at the top of this file hold.  The calls may be captured
  * into a CUDA graph by the caller (after one call on the device outside the
- * capture); workspace is then allocated and freed by nodes of that graph.
+ * capture); workspace is then allocated and freed by nodes of that graph.  An
+ * AdamW plan is made outside it, and a captured step replays with the options
+ * (the step number among them) that it was captured with.
  * ------------------------------------------------------------------------- */
 
 /* Layer norm over the last axis of x [rows, cols]:

@@ -387,3 +387,26 @@ def test_an_8_bit_block_with_a_state_that_is_not_finite_reads_back_as_nan(trop, 
     block[256:512] = True
     assert torch.equal(v[0].isnan(), block) and bool(v[0][~block].isfinite().all())
     assert torch.equal(m[0].isnan(), block) if bad != 1e30 else bool(m[0].isfinite().all())
+
+
+def test_a_captured_step_is_refused_where_its_number_would_repeat(trop):
+    """AdamW counts steps on the host; the plan, which is given the number, may be captured."""
+    p, g = [_normal(1, 600)], [_normal(2, 600)]
+    opt = trop.AdamW(p, g)
+    opt.step()
+    m, v = [torch.zeros(600, device="cuda")], [torch.zeros(600, device="cuda")]
+    plan = trop.AdamWPlan(p, g, m, v)
+    q, n, u = [p[0].clone()], [m[0].clone()], [v[0].clone()]
+    graph = torch.cuda.CUDAGraph()
+    refused = None
+    with torch.cuda.graph(graph):
+        try:
+            opt.step()
+        except trop.TropicalError as e:
+            refused = e.name
+        plan.step(1000)
+    assert refused == "UNSUPPORTED" and opt.steps == 1
+    for _ in range(2):
+        graph.replay()
+        trop.adamw_step(q, g, n, u, step=1000)
+    assert torch.equal(p[0], q[0]) and torch.equal(m[0], n[0]) and torch.equal(v[0], u[0])
