@@ -559,5 +559,5 @@ class AdamW:
     def step(self, grad_scale: float = 1.0, stream=None):
         if _capturing(stream):
             _fail(-10, "a captured step would repeat its bias corrections at every replay: AdamW counts steps on the host")
-        self.steps += 1
-        self._plan.step(self.steps, grad_scale=grad_scale, stream=stream, **self.options)
+        self._plan.step(self.steps + 1, grad_scale=grad_scale, stream=stream, **self.options)
+        self.steps += 1  # (a refused step does not count)

@@ -126,3 +126,23 @@ def test_the_loss_is_no_view_and_may_be_changed_in_place(train):
         loss /= 4
         loss.detach().mul_(2)
         loss.sum().backward()
+
+
+def test_a_refused_step_does_not_count(train, monkeypatch):
+    import ctypes
+
+    def create(*args):
+        ctypes.cast(args[-1], ctypes.POINTER(ctypes.c_void_p))[0] = 5
+        return 0
+
+    monkeypatch.setattr(type(train._pkg._lib), "tropical_adamw_plan_create", staticmethod(create), raising=False)
+    monkeypatch.setattr(train, "_capturing", lambda stream: False)
+    monkeypatch.setattr(type(train._pkg._lib), "tropical_last_error", staticmethod(lambda: b"refused"), raising=False)
+    opt = train.AdamW([torch.zeros(4)], [torch.zeros(4)])
+    opt.step()
+    train.answers.append(-1)
+    with pytest.raises(train._pkg.TropicalError):
+        opt.step()
+    after = opt.steps
+    opt._plan._h = None  # (no plan of the library's)
+    assert after == 1
