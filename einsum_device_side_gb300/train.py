@@ -66,6 +66,19 @@ def _tensors(*values):
             yield from _tensors(*v)
 
 
+_OOM = -9
+
+
+def _call(f, *args):
+    """A call of the library.  Its workspace is not torch's: where there is no room for it, torch's allocator gives back
+    what it keeps idle, and the call is made once more."""
+    rc = f(*args)
+    if rc == _OOM and not torch.cuda.is_current_stream_capturing():
+        torch.cuda.empty_cache()
+        rc = f(*args)
+    return rc
+
+
 def _stream_object(stream):
     return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream.cuda_stream)
 
@@ -180,7 +193,7 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
                           want_bias=want_bias, weight_dtype=weight_dtype)
     fc = _fast()
     if want_x and want_weight and want_bias and fc is not None and weight is not None:  # the usual call
-        r = fc.layer_norm_backward(dy, x, mean, rstd, weight, stream)
+        r = _call(fc.layer_norm_backward, dy, x, mean, rstd, weight, stream)
         if r.__class__ is tuple:
             return r
         if r < 0:
@@ -193,7 +206,7 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
     dw = _empty(c, dtype=wdtype, device=x.device) if want_weight else None
     db = None if not want_bias else _empty_like(dw) if want_weight else _empty(c, dtype=wdtype, device=x.device)
     if fc is not None:
-        rc = fc.layer_norm_backward_t(dy, x, mean, rstd, weight, dx, dw, db, stream)
+        rc = _call(fc.layer_norm_backward_t, dy, x, mean, rstd, weight, dx, dw, db, stream)
         if rc == 0:
             return dx, dw, db
         if rc < 0:
@@ -206,7 +219,7 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
     if dy.get_device() != x.get_device():
         _fail(-3, f"dy is on {dy.device}, x on {x.device}")
     mean, rstd = mean.contiguous(), rstd.contiguous()
-    _pkg._check(_lib().tropical_layer_norm_backward(_desc(dy2), _desc(x2), _ptr(mean), _ptr(rstd), _ptr(weight),
+    _pkg._check(_call(_lib().tropical_layer_norm_backward, _desc(dy2), _desc(x2), _ptr(mean), _ptr(rstd), _ptr(weight),
                                                  _CODES.get(wdtype, -1), _desc(None if dx is None else dx.view(n, c)),
                                                  _ptr(dw), _ptr(db), _pkg._stream(stream, x)))
     return dx, dw, db
@@ -257,7 +270,7 @@ def linear_cross_entropy(x: torch.Tensor, w: torch.Tensor, target: torch.Tensor,
     if code is None:
         _fail(-1, f"reduction must be one of {tuple(_REDUCTIONS)}, got {reduction!r}")
     if fc is not None:  # the usual call
-        r = fc.linear_ce(x, w, target, ignore_index, code, stream)
+        r = _call(fc.linear_ce, x, w, target, ignore_index, code, stream)
         if r.__class__ is tuple:
             return r
         if r < 0:
@@ -269,13 +282,13 @@ def linear_cross_entropy(x: torch.Tensor, w: torch.Tensor, target: torch.Tensor,
     loss = _empty_like(lse) if reduction == "none" else None
     each, mean = loss is not None, reduction == "mean"
     if fc is not None:
-        rc = fc.linear_ce_t(x, w, target, ignore_index, mean, loss, lse, None if each else total, kept, stream)
+        rc = _call(fc.linear_ce_t, x, w, target, ignore_index, mean, loss, lse, None if each else total, kept, stream)
         if rc == 0:
             return loss if each else total, lse, kept
         if rc < 0:
             _pkg._check(rc)
     _check_head(x, w, target)
-    _pkg._check(_lib().tropical_linear_cross_entropy(_desc(x), _desc(w), _desc(target), ignore_index, mean, _ptr(loss),
+    _pkg._check(_call(_lib().tropical_linear_cross_entropy, _desc(x), _desc(w), _desc(target), ignore_index, mean, _ptr(loss),
                                                   _ptr(lse), None if each else _ptr(total), _ptr(kept),
                                                   _pkg._stream(stream, x)))
     return loss if each else total, lse, kept
@@ -287,7 +300,8 @@ def linear_cross_entropy_backward(dloss: torch.Tensor, x: torch.Tensor, w: torch
     """Gradient of ``linear_cross_entropy``: ``(dx, dw)`` in the operands' type, an unwanted one None.
 
     ``dloss``: float32, one per token or a scalar for all of them.  With ``kept`` (the mean's gradient) it is divided by
-    that count.  The logits are formed again in pieces of the vocabulary."""
+    that count.  The logits are formed again in pieces of the vocabulary; the workspace (512 MiB for a piece, besides sums
+    and packed copies) stays the library's for the next call, until ``release_pool``."""
     if stream is not None:
         return _on_stream(linear_cross_entropy_backward, stream, dloss, x, w, target, lse, kept, ignore_index, want_x=want_x,
                           want_w=want_w)
@@ -295,7 +309,7 @@ def linear_cross_entropy_backward(dloss: torch.Tensor, x: torch.Tensor, w: torch
     dx = _empty(x.shape, dtype=x.dtype, device=x.device) if want_x else None
     dw = _empty(w.shape, dtype=w.dtype, device=w.device) if want_w else None
     if fc is not None:
-        rc = fc.linear_ce_backward_t(x, w, target, ignore_index, dloss, lse, kept, dx, dw, stream)
+        rc = _call(fc.linear_ce_backward_t, x, w, target, ignore_index, dloss, lse, kept, dx, dw, stream)
         if rc == 0:
             return dx, dw
         if rc < 0:
@@ -311,9 +325,9 @@ def linear_cross_entropy_backward(dloss: torch.Tensor, x: torch.Tensor, w: torch
     for t, name in ((dloss, "dloss"), (kept, "kept")):
         if t is not None and t.get_device() != x.get_device():
             _fail(-3, f"{name} is on {t.device}, x on {x.device}")
-    _pkg._check(_lib().tropical_linear_cross_entropy_backward(
-        _ptr(dloss), dloss.stride(0) if dloss.dim() else 0, _desc(x), _desc(w), _desc(target), ignore_index, _ptr(lse),
-        _ptr(kept), _desc(dx), _desc(dw), _pkg._stream(stream, x)))
+    _pkg._check(_call(
+        _lib().tropical_linear_cross_entropy_backward, _ptr(dloss), dloss.stride(0) if dloss.dim() else 0, _desc(x),
+        _desc(w), _desc(target), ignore_index, _ptr(lse), _ptr(kept), _desc(dx), _desc(dw), _pkg._stream(stream, x)))
     return dx, dw
 
 
@@ -471,7 +485,7 @@ class AdamWPlan:
                 _fail(-1, "values of states that are not in 8 bits")
             states, _ = _state_table(exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, values)
         h = ctypes.c_void_p()
-        _pkg._check(lib.tropical_adamw_plan_create(n, table, p, g, bits, c, states, ctypes.byref(h)))
+        _pkg._check(_call(lib.tropical_adamw_plan_create, n, table, p, g, bits, c, states, ctypes.byref(h)))
         self._h = h.value
         self._keep = [None if t is None else list(t) for t in lists]
         self._streams = {}  # given to step or state_values: they use the tensors

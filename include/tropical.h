@@ -421,8 +421,12 @@ int tropical_linear_cross_entropy(const trop_tensor* x, const trop_tensor* w, co
  * 2^14 / max |g|, so that small probabilities keep their digits; the largest
  * finite one of the tokens that count), which is undone in their f32 sums.
  * dx, dw: nullable, the operands' type and shapes, last axis contiguous.
- * Workspace: P of one piece (at most 512 MiB, or 4096 columns), and the f32
- * sums of dx when its depth is split or comes in several pieces.
+ * Workspace: P of one piece (512 MiB at most up to 65536 tokens; a piece has
+ * 4096 columns at least, so N * 8 KiB above), the f32 sums of dx when its depth
+ * is split or comes in several pieces (the splits' at most 1 GiB, else N * D * 4
+ * bytes), those of a piece of dw when its depth is split (at most 1 GiB), and
+ * the packed copies of x and w where TMA cannot read them.  It stays the
+ * library's for the next call, until tropical_release_pool.
  * Errors: as tropical_linear_cross_entropy. */
 int tropical_linear_cross_entropy_backward(const float* dloss, int64_t dloss_stride, const trop_tensor* x,
                                            const trop_tensor* w, const trop_tensor* target, int64_t ignore_index,

@@ -146,3 +146,35 @@ def test_a_refused_step_does_not_count(train, monkeypatch):
     after = opt.steps
     opt._plan._h = None  # (no plan of the library's)
     assert after == 1
+
+
+@pytest.mark.parametrize("fast", [False, True])
+def test_no_room_for_the_workspace(train, monkeypatch, fast):
+    """The library's workspace is not torch's: before a call gives up, torch's idle memory is given back."""
+    emptied = []
+    monkeypatch.setattr(torch.cuda, "empty_cache", lambda: emptied.append(1))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(type(train._pkg._lib), "tropical_last_error", staticmethod(lambda: b"no room"), raising=False)
+    if fast:
+        class Fast:
+            def __getattr__(self, name):
+                return lambda *args: train.answers.pop(0) if train.answers else 0 if name.endswith("_t") else 1
+        monkeypatch.setattr(train, "_fast", lambda binding=Fast(): binding)
+    h, v = torch.zeros(3, 8, dtype=torch.bfloat16), torch.zeros(5, 8, dtype=torch.bfloat16)
+    t, s, x, w = torch.zeros(3, dtype=torch.int64), torch.zeros(3), torch.zeros(3, 8), torch.zeros(8)
+    calls = (lambda: train.linear_cross_entropy(h, v, t), lambda: train.linear_cross_entropy_backward(s, h, v, t, s),
+             lambda: train.layer_norm_backward(x, x, s, s, w), lambda: train.layer_norm_backward(x, x, s, s))
+    for i, call in enumerate(calls):
+        train.answers[:] = [-9, 0 if not fast or i in (1, 3) else 1]
+        call()
+        assert len(emptied) == i + 1
+    train.answers[:] = [-9, -9]
+    with pytest.raises(train._pkg.TropicalError) as e:
+        calls[1]()
+    assert e.value.name == "OOM"
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    train.answers[:] = [-9]
+    emptied.clear()
+    with pytest.raises(train._pkg.TropicalError):
+        calls[1]()
+    assert not emptied
