@@ -209,6 +209,7 @@ __device__ void ring_failed(uint64_t* full, int stages, int s, uint32_t phase, u
 struct NormJob {
     int64_t rows, cols;
     float inv_cols, eps;
+    float n;  // cols
     const void *x, *dy, *w, *b;
     void *y, *dx;
     int64_t sx, sy, sdy, sdx;
@@ -216,6 +217,16 @@ struct NormJob {
     float *part_w, *part_b;  // [blocks][cols], null: not wanted
     Span sp_x, sp_y, sp_dy, sp_dx, sp_w, sp_b, sp_mean, sp_rstd, sp_pw, sp_pb;
 };
+
+// sum / n: the product with the rounded inverse alone misses a constant row's value by a last place, which the row's
+// small deviation then magnifies.  One residual step makes it the nearest quotient (Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990); a sum that is not finite stays as it is.  (The
+// division itself costs short 16-bit rows 2 of 25 us.)
+__device__ __forceinline__ float over_n(float sum, const NormJob& j)
+{
+    const float q = sum * j.inv_cols, better = __fmaf_rn(__fmaf_rn(-q, j.n, sum), j.inv_cols, q);
+    return better == better ? better : q;
+}
 
 // Threads a block may have: where a thread holds more than 64 bytes of its row, registers allow 256.
 template <typename T, int VEC, int NV>
@@ -233,7 +244,7 @@ __device__ __forceinline__ void norm_row(const NormJob& j, int64_t row, Raw<TX, 
         for (int i = 0; i < pairs<VEC>; ++i) a = p_add(a, pair_of<TX, VEC>(q[k], i));
     float s[1] = {p_sum(a)};
     group_sum_turn<1>(s, sh[0]);
-    const float mean = s[0] * j.inv_cols;
+    const float mean = over_n(s[0], j);
     a = p_of<Pair<VEC>>(0.f);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -335,7 +346,7 @@ __global__ void __launch_bounds__(256, 4) k_norm_short(const NormJob j)
         warp_sum<U>(mean);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            mean[u] *= j.inv_cols;
+            mean[u] = over_n(mean[u], j);
             Pair<VEC> a = p_of<Pair<VEC>>(0.f);
 #pragma unroll
             for (int k = 0; k < NV; ++k)
@@ -488,7 +499,7 @@ __global__ void __launch_bounds__(NV == 4 ? 672 : 256) k_norm_off(const NormJob 
         group_sum_turn<U>(mean, sh[0]);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            mean[u] *= j.inv_cols;
+            mean[u] = over_n(mean[u], j);
             Pair<VEC> a = p_of<Pair<VEC>>(0.f);
             float edge = 0.f;
 #pragma unroll
@@ -559,7 +570,7 @@ __global__ void __launch_bounds__(1024) k_norm_long(const NormJob j)
         s[0] += v[0];
     }
     group_sum<1>(s, sh);
-    const float mean = s[0] * j.inv_cols;
+    const float mean = over_n(s[0], j);
     s[0] = 0.f;
     for (int64_t c = threadIdx.x; c < j.cols; c += 1024) {
         load<TX, 1>(x + c, v, j.sp_x);
@@ -1427,6 +1438,7 @@ NormJob job_of(int64_t rows, int64_t cols, const NormMat& x, const NormVec& w)
     j.rows = rows;
     j.cols = cols;
     j.inv_cols = (float)(1.0 / (double)cols);
+    j.n = (float)cols;
     j.x = x.p;
     j.sx = x.sr;
     j.w = w.p;

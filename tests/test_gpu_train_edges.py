@@ -410,3 +410,27 @@ def test_a_captured_step_is_refused_where_its_number_would_repeat(trop):
         graph.replay()
         trop.adamw_step(q, g, n, u, step=1000)
     assert torch.equal(p[0], q[0]) and torch.equal(m[0], n[0]) and torch.equal(v[0], u[0])
+
+
+# ------------------------------------------------------------------ layer norm: values
+
+
+@pytest.mark.parametrize("rows,cols", [(3, 61), (2500, 61), (2500, 244), (700, 3904), (5, 3904), (2, 31232)])
+def test_constant_rows_give_the_bias(trop, rows, cols):
+    """Whole numbers whose sums are exact in f32: the mean is the row's value, so nothing of it is left."""
+    most = (1 << 24) // cols - 1
+    value = torch.randint(most // 2, most, (rows, 1), device="cuda", generator=torch.Generator("cuda").manual_seed(1)).float()
+    b = _normal(2, cols)
+    y, mean, _ = trop.layer_norm(value.expand(rows, cols).contiguous(), torch.ones(cols, device="cuda"), b)
+    assert torch.equal(mean, value[:, 0]) and torch.equal(y, b.expand(rows, cols))
+
+
+@pytest.mark.parametrize("cols", [1, 3, 7, 41, 61, 244, 1000, 4093, 20011])
+def test_means_are_the_nearest_quotients(trop, cols):
+    """Whole numbers whose sums are exact in f32, over the number of columns: the division's own rounding."""
+    gen = torch.Generator("cuda").manual_seed(cols)
+    most = (1 << 24) // cols
+    x = torch.randint(-most, most + 1, (500, cols), device="cuda", generator=gen).float() * 2.0 ** -20
+    x[0] = 0
+    _, mean, _ = trop.layer_norm(x)
+    assert torch.equal(mean.cpu(), (x.double().sum(1).cpu().float() / torch.tensor(float(cols))))
