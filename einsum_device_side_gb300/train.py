@@ -542,17 +542,19 @@ class AdamWPlan:
 class AdamW:
     """AdamW with its states: ``AdamW(params, grads, state_bits=8)``, then ``step()`` whenever the gradients' buffers hold
     new ones.  ``grads`` are the buffers the backward pass writes (``p.grad`` of each parameter by default, which must
-    exist and stay in place).  ``copies`` as in ``adamw_step``.  It counts its steps on the host, so a step cannot be
-    captured into a CUDA graph (``AdamWPlan.step`` can, with the step number given)."""
+    exist and stay in place, ``zero_grad(set_to_none=False)``: a step finds out if it did not).  ``copies`` as in
+    ``adamw_step``.  It counts its steps on the host, so a step cannot be captured into a CUDA graph (``AdamWPlan.step``
+    can, with the step number given)."""
 
     def __init__(self, params, grads=None, lr: float = 1e-3, beta1: float = 0.9, beta2: float = 0.999,
                  eps: float = 1e-8, weight_decay: float = 0.01, state_bits: int = 32, copies=None):
-        params = [p.detach() for p in params] if grads is not None else list(params)
+        params = list(params)
+        self._owners = params if grads is None else []
         if grads is None:
             grads = [p.grad for p in params]
             if any(g is None for g in grads):
                 _fail(-1, "a parameter has no gradient buffer")
-            params = [p.detach() for p in params]
+        params = [p.detach() for p in params]
         if state_bits not in (8, 32):
             _fail(-1, f"states of {state_bits} bits")
         new = lambda p, dtype, n=None: torch.zeros(p.shape if n is None else n, dtype=dtype, device=p.device)  # noqa: E731
@@ -573,5 +575,8 @@ class AdamW:
     def step(self, grad_scale: float = 1.0, stream=None):
         if _capturing(stream):
             _fail(-10, "a captured step would repeat its bias corrections at every replay: AdamW counts steps on the host")
+        for i, (p, g) in enumerate(zip(self._owners, self.grads)):
+            if p.grad is not g and (p.grad is None or p.grad.data_ptr() != g.data_ptr()):
+                _fail(-1, f"parameter {i} has another gradient buffer than at first: clear gradients in place")
         self._plan.step(self.steps + 1, grad_scale=grad_scale, stream=stream, **self.options)
         self.steps += 1  # (a refused step does not count)

@@ -178,3 +178,32 @@ def test_no_room_for_the_workspace(train, monkeypatch, fast):
     with pytest.raises(train._pkg.TropicalError):
         calls[1]()
     assert not emptied
+
+
+def test_a_parameter_s_new_gradient_buffer_is_noticed(train, monkeypatch):
+    """zero_grad drops the buffers by default and backward makes new ones, which the plan does not know."""
+    import ctypes
+
+    def create(*args):
+        ctypes.cast(args[-1], ctypes.POINTER(ctypes.c_void_p))[0] = 5
+        return 0
+
+    monkeypatch.setattr(type(train._pkg._lib), "tropical_adamw_plan_create", staticmethod(create), raising=False)
+    monkeypatch.setattr(train, "_capturing", lambda stream: False)
+    p = torch.zeros(4, requires_grad=True)
+    p.sum().backward()
+    opt = train.AdamW([p])
+    opt.step()
+    p.grad.zero_()
+    p.sum().backward()
+    opt.step()
+    refused = []
+    for grad in (None, torch.ones(4)):
+        p.grad = grad
+        try:
+            opt.step()
+        except train._pkg.TropicalError as e:
+            refused.append(e.name)
+    steps = opt.steps
+    opt._plan._h = None  # (no plan of the library's)
+    assert refused == ["INVALID_ARG"] * 2 and steps == 2
