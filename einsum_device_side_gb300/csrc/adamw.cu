@@ -10,8 +10,9 @@
 // c in -127 .. 127 that stands for c |c| top / 127^2, top being the block's largest |m|; of v its
 // root r = sqrt(v) is kept, as a code 0 .. 255 that stands for c^2 top / 255^2.  The square law
 // gives small entries a finer step (relative step 2 / c, down to top / 127^2 and top / 255^2) than
-// an even code; r, not v, is what the update divides by, and no r > 0 is coded as 0, so a rounded
-// state can damp an update but never blow it up.  The update itself uses the unrounded new m and v.
+// an even code; r, not v, is what the update divides by, and no r > 0 is coded as 0: a kept r is at
+// most 2.25 times too small (code 1 from 1.5^2 levels down; 1 + 1 / c above), which bounds what rounding
+// adds to a later update.  The update itself uses the unrounded new m and v.
 //
 // The step moves 28 (f32) or 16 (8-bit, f32 parameters) bytes per element and is bound by memory.
 // One launch covers hundreds of tensors: the grid has one block per 4096 elements of any tensor.  A
@@ -19,9 +20,9 @@
 // bisection; that of a plan of many tensors lies in device memory with each block's tensor written
 // down, because a launch with 30 KB of parameters takes the host about 8 us instead of 2.
 //
-// Measured, 2^27 f32 elements in 96 tensors: 32-bit states 532 us, 7.1 TB/s; 8-bit states 632 us with the
-// states' values read back (2^25 elements: the step 119 us, 73 % of the issue slots: the codes' arithmetic, about
-// 85 instructions an element and thread, bounds it before memory does).  Twelve small tensors: 4.7 us, the
+// Measured, 2^27 f32 elements in 96 tensors: 32-bit states 532 us, 7.1 TB/s; 8-bit states 633 us with the
+// states' values read back (the step 435 us, the values 198 us; 2^25 elements: the step 119 us, 73 % of the issue slots:
+// the codes' arithmetic, 98 instructions an element, bounds it before memory does).  Twelve small tensors: 4.7 us, the
 // launch.  4096 elements a block: 16 of each array a thread, all loads on their way before the first is used.
 #include <cuda_runtime.h>
 

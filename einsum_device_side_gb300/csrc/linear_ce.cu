@@ -26,9 +26,9 @@
 // cases are bound by the tensor cores at the clock that the power limit leaves them, small ones by the chain of
 // launches, few tokens by reading the weights (measured, bf16):
 //   8192x2048x65536   forward 1265 us, 1738 TFLOP/s; backward 3960 us, 1666 TFLOP/s of the three products
-//   16x4096x131072    forward 178 us, 6.0 TB/s; backward 570 us
-//   1021x1000x32003   forward 52 us, backward 169 us
-//   16x512x2000       forward 18 us, backward 24 us
+//   16x4096x131072    forward 180 us, 6.0 TB/s; backward 572 us (w read for the logits and again, a gigabyte later, for dx)
+//   1021x1000x32003   forward 53 us, backward 169 us
+//   16x512x2000       forward 13 us, backward 26 us (per call, back to back)
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -930,22 +930,27 @@ int launch_tile(bool bf16, const CUtensorMap& a, const CUtensorMap& b, const CUt
     return bf16 ? launch_tile<MODE, true, S>(a, b, c, j, join, sm, s) : launch_tile<MODE, false, S>(a, b, c, j, join, sm, s);
 }
 
-// Row tiles of a band: as many as keep their operand (a row tile's whole depth) in about 48 MB of
-// the L2, so that the other operand is read from memory once per band.  8192x2048x65536: all 32 row
-// tiles (33 MB) 1269 us, bands of 16 / 12 / 8 / 4 1293 / 1305 / 1330 / 1378 us.
 // Up to this many tokens one row tile of one CTA holds them all, and reading the weights is the work.  Forward
-// against pairs of CTAs and a join of its own: 8 tokens x 4096 x 65536 92 us and 145 us; 64 x 512 x 8000 18 us and
-// 20.5 us; 64 x 2048 x 32000 32.5 us and 34.7 us; at 128 tokens 36.6 us and 34.4 us there, 17.4 us and 20.8 us with 512 x
-// 8000.  Backward, 128x4096x131072: 647 us and 658 us.
+// against pairs of CTAs and a join of its own (back to back): 8 tokens x 4096 x 65536 93 us and 121 us; 64 x 512 x 8000
+// 13.5 us and 16.5 us; 64 x 2048 x 32000 33.6 us and 34.8 us; at 128 tokens 37.7 us and 34.7 us there, 13.6 us and 16.3 us
+// with 512 x 8000, 187 us and 191 us with 4096 x 131072.  Backward, 128x4096x131072: 648 us and 658 us; 128x2048x32000 104 us and
+// 108 us.
 constexpr int64_t FEW_TOKENS = 128;
 // A logit's sum loses up to a last place of its accumulator every 16 products; past this depth two
-// accumulators share it, which leaves no room for a second tile.  Logits of 4096 products: relative error of
-// lse 2.2e-7 (8192x4096x32768 in 1324 us), in one accumulator 4.4e-7 (1284 us).
+// accumulators share it, which halves lse's error and leaves no room for a second tile.  8192 x depth x 32768, lse's
+// relative error and time in one and in two accumulators: 1024 3.1e-7, 342 us and 1.5e-7, 419 us; 2048 6.2e-7, 610 us and
+// 3.0e-7, 690 us; 2304 7.1e-7, 679 us and 3.4e-7, 760 us; 4096 1.3e-6, 1166 us and 6.2e-7, 1236 us.  The rule lets the error of
+// 2048 products stand and pays the second accumulator where it would grow past that.  The backward pass forms
+// its logits in one at every depth: what its probabilities are off by for that (2e-5 relative at 4096) is far
+// below their rounding to 16 bits (2^-9, 2^-12).
 constexpr int64_t DEEP_LOGITS = 2048;
 // Rows of such a tile's box: the tokens' only.  The tile's other rows keep what shared memory holds,
 // and so do the accumulator's, which nobody reads.
 int few_rows(int64_t rows) { return (int)((rows + 7) / 8 * 8); }
 
+// Row tiles of a band: as many as keep their operand (a row tile's whole depth) in about 48 MB of
+// the L2, so that the other operand is read from memory once per band.  8192x2048x65536: all 32 row
+// tiles (33 MB) 1269 us, bands of 16 / 12 / 8 / 4 1293 / 1305 / 1330 / 1378 us.
 int band_of(int mt, int64_t tile_bytes) { return (int)std::min<int64_t>(mt, std::max<int64_t>(8, (48 << 20) / tile_bytes)); }
 int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 

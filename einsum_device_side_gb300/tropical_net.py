@@ -3,8 +3,9 @@
 Next-token prediction on a synthetic chain: token embeddings (float32) go
 through a max-plus layer (``TropicalGemm``: h[i, j] = max_k e[i, k] + A[k, j],
 its gradient routed through the argmax), a layer norm that hands bfloat16 on,
-and a linear head whose cross entropy never forms the logits.  One AdamW plan
-steps all parameters; the head's float32 master weights leave their bfloat16
+and a linear head whose cross entropy never forms the logits.  Two AdamW
+optimisers step the parameters, one for the float32 gradients and one for the
+head's bfloat16 ones; the head's float32 master weights leave their bfloat16
 copy, which the next forward pass reads, in the same pass.
 
     python -m einsum_device_side_gb300.tropical_net
