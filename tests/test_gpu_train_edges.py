@@ -434,3 +434,26 @@ def test_means_are_the_nearest_quotients(trop, cols):
     x[0] = 0
     _, mean, _ = trop.layer_norm(x)
     assert torch.equal(mean.cpu(), (x.double().sum(1).cpu().float() / torch.tensor(float(cols))))
+
+
+def test_a_training_step_captured_through_autograd(trop):
+    """Forward and backward (the latter from autograd's thread) in one graph, replayed on new inputs."""
+    x, w, b = _normal(1, 70, 5, 64), _normal(2, 64).requires_grad_(), _normal(3, 64).requires_grad_()
+    head, t = (_normal(4, 200, 64) / 4).to(B).requires_grad_(), torch.randint(0, 200, (350,), device="cuda")
+    leaves = (w, b, head)
+
+    def step():
+        y = trop.LayerNorm.apply(x, w, b, 1e-5, B)
+        loss = trop.LinearCrossEntropy.apply(y.view(350, 64), head, t)
+        return (loss.detach(), *torch.autograd.grad(loss, leaves))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    graph, out = _captured(step)
+    for k in range(3):
+        x.mul_(-0.5)
+        graph.replay()
+        assert all(torch.equal(a, e) for a, e in zip(out, step()))
