@@ -8,7 +8,8 @@
 // next thread on their streams.  Streams are told apart by their id, which, unlike a handle, never comes
 // back after the stream was destroyed with launches still on their way.  A larger request replaces the
 // block; the old one, which earlier launches may still use, is kept until tropical_release_pool.
-// Behind each block lies an arrival ticket, zeroed once in stream order.
+// Behind each block lies an arrival ticket, zeroed once in stream order; a call without a kept block has its
+// ticket in its workspace, zeroed before its launches.
 //
 // Launches that the caller captures into a graph outlive the call and are replayed in any order with
 // other calls: their workspace is allocated and freed by nodes of that graph, and so is its ticket.
@@ -147,6 +148,7 @@ int Workspace::take()
         own = p;
     } else if (!stream_scratch(bytes, s, &p, &kept_ticket)) {
         if (bytes > SCRATCH_MOST) (void)stream_scratch(0, s, &p, &kept_ticket);
+        at_ticket = add(sizeof(uint32_t));  // (used where no block is kept)
         TROP_TRY(pool_alloc(bytes, s, &p));
         own = p;
     }
@@ -156,13 +158,14 @@ int Workspace::take()
 
 int Workspace::ticket(uint32_t** out)
 {
-    if (!captured) {
+    if (capture_arena()) return stream_tickets(s, 1, out);
+    if (kept_ticket) {
         *out = kept_ticket;
-        return kept_ticket ? (int)TROP_OK : stream_tickets(s, 1, out);
+        return TROP_OK;
     }
     *out = (uint32_t*)(base + at_ticket);
     const cudaError_t e = cudaMemsetAsync(*out, 0, sizeof(uint32_t), s);
-    return e == cudaSuccess ? (int)TROP_OK : cuda_error(e, "cudaMemsetAsync (captured ticket)");
+    return e == cudaSuccess ? (int)TROP_OK : cuda_error(e, "cudaMemsetAsync (ticket)");
 }
 
 void release_scratch()

@@ -329,6 +329,36 @@ def test_a_destroyed_stream_s_ticket_is_not_the_next_one_s(trop):
         assert all(torch.equal(a, b) for a, b in zip(got, want[i % 4]))
 
 
+def test_more_streams_than_blocks_are_kept(trop):
+    """Calls on streams beyond those: workspace from the pool, a ticket of their own."""
+    import ctypes
+
+    runtime = torch.cuda.cudart()
+    trop.release_pool()
+    x, w, t = _normal(1, 300, 64).to(B), (_normal(2, 3000, 64) / 4).to(B), torch.randint(0, 3000, (300,), device="cuda")
+    rows, dy, weight = _normal(3, 400, 256), _normal(4, 400, 256), _normal(5, 256)
+    stats = trop.layer_norm(rows, weight)[1:]
+
+    def f():
+        return (*trop.linear_cross_entropy(x, w, t), *trop.layer_norm_backward(dy, rows, *stats, weight))
+
+    want = f()
+    torch.cuda.synchronize()
+    handles, results = [], []
+    for _ in range(70):
+        handle = ctypes.c_void_p()
+        assert int(runtime.cudaStreamCreate(ctypes.addressof(handle))) == 0
+        handles.append(handle.value)
+        with torch.cuda.stream(torch.cuda.ExternalStream(handle.value)):
+            results += [f(), f()]
+    torch.cuda.synchronize()
+    for got in results:
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    for h in handles:
+        assert int(runtime.cudaStreamDestroy(h)) == 0
+    trop.release_pool()
+
+
 # ------------------------------------------------------------------ the head's gradients
 
 
