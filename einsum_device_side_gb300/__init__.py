@@ -625,7 +625,7 @@ def debug_set_wait_mode(mode: int):
 
 # translation units of the library, by the id the bounds-checked build records with a line
 _BOUNDS_FILES = {1: "unary.cu", 2: "gemm.cu", 3: "gemm64.cu", 4: "gemm_int.cu", 5: "backward.cu", 6: "backtrack.cu",
-                 7: "layer_norm.cu", 8: "adamw.cu", 9: "linear_ce.cu"}
+                 7: "layer_norm.cu", 8: "adamw.cu", 9: "linear_ce.cu", 10: "operands.cu"}
 
 
 def debug_bounds_report(reset: bool = False) -> dict | None:

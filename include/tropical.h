@@ -545,7 +545,7 @@ int tropical_device_wait_timeouts(unsigned int* count, int reset);
  * skipped and counted, and the first one's location and address kept.
  * *line = (file id << 16) | source line, the file ids being 1 unary.cu, 2
  * gemm.cu, 3 gemm64.cu, 4 gemm_int.cu, 5 backward.cu, 6 backtrack.cu, 7
- * layer_norm.cu, 8 adamw.cu, 9 linear_ce.cu.
+ * layer_norm.cu, 8 adamw.cu, 9 linear_ce.cu, 10 operands.cu.
  * Reads the record of the current device without synchronising: call it once
  * the work to inspect has completed.  reset != 0 clears the record.  The
  * normal build returns TROP_ERR_UNSUPPORTED with *count = 0.  It stands in
