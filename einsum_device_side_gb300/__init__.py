@@ -6,8 +6,9 @@ runs in that library's CUDA kernels.  There is no CPU fallback: if the
 library is missing the first call raises.
 
 The training operators that stand around a tropical product and its gradient
-(layer norm, the cross entropy of a linear head, AdamW) are in ``train.py`` and
-reached from here too.
+(layer norm, the cross entropy of a linear head, AdamW) are in ``train.py``, those
+of a residual block around it (its fused norms, activations kept in 8 bits) in
+``block.py``; both are reached from here too.
 
 Semirings: ``"maxplus"`` (max, +), ``"minplus"`` (min, +), ``"maxtimes"``
 (max, *).  Argmax tensors are int32.
@@ -27,6 +28,7 @@ __all__ = [
     "SEMIRINGS",
     "layer_norm", "layer_norm_backward", "LayerNorm", "linear_cross_entropy", "linear_cross_entropy_backward",
     "LinearCrossEntropy", "adamw_step", "adamw_state_values", "AdamWPlan", "AdamW",
+    "activation_pack", "activation_values", "activation_weight_grad", "Linear8", "residual_norm", "residual_norm_backward", "ResidualNorm",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -149,6 +151,11 @@ def load(path: str | None = None):
         "tropical_adamw_plan_step": (I, [P, P, P]),
         "tropical_adamw_plan_values": (I, [P, P]),
         "tropical_adamw_plan_destroy": (I, [P]),
+        "tropical_residual_norm": (I, [P, TP, TP, TP, TP, TP, P, P, P]),
+        "tropical_residual_norm_backward": (I, [P, TP, TP, TP, TP, TP, P, P, I, I, P, P]),
+        "tropical_activation_weight_grad": (I, [TP, TP, TP, TP, P, P]),
+        "tropical_activation_pack": (I, [TP, TP, TP, P]),
+        "tropical_activation_values": (I, [TP, TP, TP, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -159,7 +166,7 @@ def load(path: str | None = None):
     _fc = None if debug else _load_fastcall(path)
     if _fc is not None:
         _fc.set_torch_handles(torch.float32, torch.int32, torch.int64, torch.float64, torch.bfloat16, torch.float16,
-                              _raw_stream or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
+                              torch.int8, torch.uint8, _raw_stream or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
         _fc.set_torch_allocators(torch.empty, torch.empty_like, torch.float32)
     return lib
 
@@ -625,7 +632,7 @@ def debug_set_wait_mode(mode: int):
 
 # translation units of the library, by the id the bounds-checked build records with a line
 _BOUNDS_FILES = {1: "unary.cu", 2: "gemm.cu", 3: "gemm64.cu", 4: "gemm_int.cu", 5: "backward.cu", 6: "backtrack.cu",
-                 7: "layer_norm.cu", 8: "adamw.cu", 9: "linear_ce.cu", 10: "operands.cu"}
+                 7: "layer_norm.cu", 8: "adamw.cu", 9: "linear_ce.cu", 10: "operands.cu", 11: "activation.cu", 12: "residual_norm.cu", 13: "weight_grad.cu"}
 
 
 def debug_bounds_report(reset: bool = False) -> dict | None:
@@ -681,3 +688,5 @@ def plan_describe(spec: str, shape_a, stride_a, shape_b, stride_b) -> str:
 
 from .train import (AdamW, AdamWPlan, LayerNorm, LinearCrossEntropy, adamw_state_values, adamw_step,  # noqa: E402
                     layer_norm, layer_norm_backward, linear_cross_entropy, linear_cross_entropy_backward)
+from .block import (Linear8, ResidualNorm, activation_pack, activation_values,  # noqa: E402
+                    activation_weight_grad, residual_norm, residual_norm_backward)

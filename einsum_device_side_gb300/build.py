@@ -32,7 +32,9 @@ LIB_DEBUG = os.path.join(BUILD_DEBUG, "libtropical_gb300.so")
 VARIANTS = {"release": (BUILD, LIB, []), "debug": (BUILD_DEBUG, LIB_DEBUG, ["-DTROP_DEBUG_BOUNDS=1"])}
 SOURCES = ["runtime.cpp", "api.cpp", "unary.cu", "gemm.cu", "gemm64.cu", "gemm_int.cu", "backtrack.cu", "backward.cu",
            "noalloc.cu"]
-TRAIN = ["train.cpp", "layer_norm.cu", "adamw.cu", "linear_ce.cu", "operands.cu"]  # the training operators
+# the training operators, and those of a residual block
+TRAIN = ["train.cpp", "layer_norm.cu", "adamw.cu", "linear_ce.cu", "operands.cu",
+         "block.cpp", "activation.cu", "residual_norm.cu", "weight_grad.cu"]
 SOURCES += TRAIN + ["scratch.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fno-strict-aliasing",
@@ -53,7 +55,8 @@ def _stale(obj: str, src: str) -> bool:
     deps = [src, os.path.join(CSRC, "internal.h"), os.path.join(CSRC, "bounds.h"),
             os.path.join(ROOT, "include", "tropical.h")]
     if os.path.basename(src) in TRAIN:
-        deps += [os.path.join(CSRC, h) for h in ("train.h", "tcgen05.h", "packed.h", "rows.h", "operands.h", "checks.h")]
+        deps += [os.path.join(CSRC, h) for h in ("train.h", "tcgen05.h", "packed.h", "rows.h", "operands.h", "checks.h",
+                                                  "block.h", "pack8.h")]
     return any(os.path.getmtime(d) > os.path.getmtime(obj) for d in deps)
 
 

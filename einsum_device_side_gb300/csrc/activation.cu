@@ -1,0 +1,283 @@
+// activation.cu -- activations in 8 bits (the format: pack8.h), written and read back.
+//
+// Both directions are bound by memory: a 16-bit element is 2 bytes one way and 1 + 1/32 the other.  A thread has the
+// elements of 16 bytes, 32 / that many neighbouring lanes a group, whose largest magnitude they find by shuffles; U rows'
+// loads are on their way together.  Matrices without gaps are taken as rows of 256 vectors, whatever their width.
+// Rows that do not lie on 16 bytes keep whole vectors all the same: two aligned loads are shifted together (pack), or
+// the vectors are laid where the result's are aligned and the codes shifted (values).
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#define TROP_TU 11  // this file's id in a bounds-violation record
+#include "block.h"
+#include "pack8.h"
+#include "rows.h"
+
+namespace trop {
+namespace {
+
+struct Job8 {
+    int64_t rows, cols, total;  // total: elements of a matrix without gaps taken as rows, else none's end
+    const void* x;              // pack: the elements; values: the result
+    int64_t sx;
+    int8_t* codes;
+    int64_t sc;
+    uint8_t* scales;
+    int64_t ss;
+    int wide_codes;  // rows of codes start on a vector's bytes
+    Span sp_x, sp_c, sp_s;
+};
+
+// VEC elements from any element on, where the aligned 32 bytes around them lie in the matrix; else one by one.  Elements from
+// `left` on are zero.
+template <typename T, int VEC>
+__device__ __forceinline__ void read_any(const T* p, int64_t left, const T* begin, const T* end, Raw<T, VEC>& q, const Span& sp)
+{
+    (void)sp;
+    const uint32_t off = (uint32_t)((uintptr_t)p & 15);
+    const char* const at = reinterpret_cast<const char*>(p) - off;
+    if (at >= reinterpret_cast<const char*>(begin) && at + (off ? 32 : 16) <= reinterpret_cast<const char*>(end)) {
+        uint32_t w[8];
+        const bool in = TROP_IN(at, off ? 32 : 16, sp);
+        const uint4 a = in ? reinterpret_cast<const uint4*>(at)[0] : make_uint4(0, 0, 0, 0);
+        const uint4 b = in && off ? reinterpret_cast<const uint4*>(at)[1] : make_uint4(0, 0, 0, 0);
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+        if (off & 8)
+#pragma unroll
+            for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+        if (off & 4)
+#pragma unroll
+            for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q.w[i] = __funnelshift_r(w[i], w[i + 1], (off & 2) * 8);
+        if (left < VEC)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                constexpr int E = 4 / sizeof(T);
+                if (i * E >= left) q.w[i] = 0;
+                else if (E == 2 && i * E + 1 >= left) q.w[i] &= 0xffffu;
+            }
+    } else {
+        float v[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = i < left && TROP_IN(p + i, sizeof(T), sp) ? to_f32(p[i]) : 0.f;
+        q.set(v);
+    }
+}
+
+template <typename T, bool OFF, int U>
+__global__ void __launch_bounds__(256) k_pack8(const Job8 j)
+{
+    pdl_wait();
+    pdl_signal();
+    constexpr int VEC = 16 / sizeof(T);
+    const int64_t c = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * VEC;
+    const T* const begin = (const T*)j.x;
+    const T* const end = begin + (j.rows - 1) * j.sx + j.cols;
+    const int64_t step = (int64_t)gridDim.y * blockDim.y;
+    for (int64_t row0 = (int64_t)blockIdx.y * blockDim.y; row0 < j.rows; row0 += step * U) {
+        Raw<T, VEC> q[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = row0 + u * step + threadIdx.y;
+            const bool live = row < j.rows && c < j.cols && row * j.cols + c < j.total;
+            const T* p = begin + row * j.sx + c;
+            q[u].zero();
+            if (OFF) {
+                if (live) read_any<T, VEC>(p, j.cols - c, begin, end, q[u], j.sp_x);
+            } else if (live && TROP_IN(p, 16, j.sp_x)) {
+                q[u].read(p);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = row0 + u * step + threadIdx.y;
+            const bool live = row < j.rows && c < j.cols && row * j.cols + c < j.total;
+            const uint32_t e = scale8(group_top8<VEC>(top8<T, VEC>(q[u])));
+            if (!live) continue;
+            Codes<VEC> k;
+            codes8<T, VEC>(q[u], e, k.w);
+            int8_t* to = j.codes + row * j.sc + c;
+            if (!OFF || (j.wide_codes && c + VEC <= j.cols)) {
+                if (TROP_IN(to, VEC, j.sp_c)) k.write(to);
+            } else {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    if (c + i < j.cols && TROP_IN(to + i, 1, j.sp_c)) to[i] = (int8_t)(k.w[i / 4] >> 8 * (i % 4));
+            }
+            uint8_t* s = j.scales + row * j.ss + c / GROUP8;
+            if (c % GROUP8 == 0 && TROP_IN(s, 1, j.sp_s)) *s = (uint8_t)e;
+        }
+    }
+}
+
+// VEC codes from any one on, with the same rule on what lies around them.
+template <int VEC>
+__device__ __forceinline__ void codes_any(const int8_t* p, int64_t left, const int8_t* begin, const int8_t* end, Codes<VEC>& q,
+                                          const Span& sp)
+{
+    (void)sp;
+    constexpr int N = VEC / 4;
+    const uint32_t off = (uint32_t)((uintptr_t)p & 3);
+    const int8_t* const at = p - off;
+    if (left >= VEC && at >= begin && at + VEC + 4 <= end) {
+        uint32_t w[N + 1];
+#pragma unroll
+        for (int i = 0; i <= N; ++i) w[i] = TROP_IN(at + 4 * i, 4, sp) ? reinterpret_cast<const uint32_t*>(at)[i] : 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) q.w[i] = __funnelshift_r(w[i], w[i + 1], off * 8);
+    } else {
+        q.zero();
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            if (i < left && p + i >= begin && TROP_IN(p + i, 1, sp)) q.w[i / 4] |= (uint32_t)(uint8_t)p[i] << 8 * (i % 4);
+    }
+}
+
+template <typename T, bool OFF, int U>
+__global__ void __launch_bounds__(256) k_values8(const Job8 j)
+{
+    pdl_wait();
+    pdl_signal();
+    constexpr int VEC = 16 / sizeof(T);
+    const int64_t vec = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    const int64_t step = (int64_t)gridDim.y * blockDim.y;
+    const int8_t* const end = j.codes + (j.rows - 1) * j.sc + j.cols;
+    for (int64_t row0 = (int64_t)blockIdx.y * blockDim.y; row0 < j.rows; row0 += step * U) {
+        Codes<VEC> q[U];
+        uint32_t s0[U], s1[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = row0 + u * step + threadIdx.y;
+            T* const out = (T*)j.x + row * j.sx;
+            // the first column: where the result's vectors lie on 16 bytes
+            const int64_t c = vec * VEC - (OFF ? (int64_t)((uintptr_t)out & 15) / (int64_t)sizeof(T) : 0);
+            const int8_t* p = j.codes + row * j.sc + c;
+            const uint8_t* s = j.scales + row * j.ss;
+            q[u].zero();
+            s0[u] = s1[u] = LEAST8;
+            if (row >= j.rows || c >= j.cols || row * j.cols + c >= j.total) continue;
+            const int64_t g0 = (c < 0 ? 0 : c) / GROUP8;
+            if (TROP_IN(s + g0, 1, j.sp_s)) s0[u] = s[g0];
+            if (OFF) {
+                const int64_t g1 = (c + VEC > j.cols ? j.cols - 1 : c + VEC - 1) / GROUP8;
+                s1[u] = g1 == g0 ? s0[u] : TROP_IN(s + g1, 1, j.sp_s) ? s[g1] : LEAST8;
+                codes_any<VEC>(p, j.cols - c, c < 0 ? p - c : j.codes, end, q[u], j.sp_c);
+            } else if (TROP_IN(p, VEC, j.sp_c)) {
+                q[u].read(p);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = row0 + u * step + threadIdx.y;
+            T* const out = (T*)j.x + row * j.sx;
+            const int64_t c = vec * VEC - (OFF ? (int64_t)((uintptr_t)out & 15) / (int64_t)sizeof(T) : 0);
+            if (row >= j.rows || c >= j.cols || row * j.cols + c >= j.total) continue;
+            float v[VEC];
+            values8<VEC>(q[u].w, unit8(s0[u]), v);
+            if (OFF && s1[u] != s0[u]) {
+                const float other = unit8(s1[u]);
+                const int64_t edge = (c < 0 ? 0 : c) / GROUP8 * GROUP8 + GROUP8 - c;  // elements of the first group
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    if (i >= edge) v[i] = coded8(q[u].w[i / 4] ^ 0x80808080u, i % 4) * other;
+            }
+            if (!OFF || (c >= 0 && c + VEC <= j.cols)) {
+                store<T, VEC>(out + c, v, j.sp_x);
+            } else {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    if (c + i >= 0 && c + i < j.cols && TROP_IN(out + c + i, sizeof(T), j.sp_x)) out[c + i] = from_f32<T>(v[i]);
+            }
+        }
+    }
+}
+
+// The threads of a row and of several rows in a block of 256, and the grid: as many rows at a time as fill the device
+// with U each.
+struct Shape8 {
+    dim3 grid, block;
+};
+Shape8 shape8(int64_t rows, int64_t vecs, int lanes, int u, int sm)
+{
+    int64_t bx = lanes;
+    while (bx < 256 && bx < vecs) bx *= 2;
+    const int64_t by = 256 / bx, gx = (vecs + bx - 1) / bx;
+    const int64_t most = std::max<int64_t>(1, (int64_t)sm * 16 / gx);
+    int64_t gy = (rows + by - 1) / by;
+    if (gy > most) gy = std::max<int64_t>(most, 1);
+    else if (gy * gx > (int64_t)sm * 8) gy = std::max<int64_t>((gy + u - 1) / u, 1);
+    return {dim3((unsigned)gx, (unsigned)std::min<int64_t>(gy, 65535)), dim3((unsigned)bx, (unsigned)by)};
+}
+
+template <typename T, bool PACK>
+int run8(Job8 j, int sm, cudaStream_t s)
+{
+    constexpr int VEC = 16 / sizeof(T), U = 4;
+    const bool on16 = j.cols % VEC == 0 && aligned(j.x, j.sx, sizeof(T), VEC, j.rows);
+    j.wide_codes = aligned(j.codes, j.sc, 1, VEC, j.rows);
+    const bool off = !on16 || !j.wide_codes;
+    j.total = INT64_MAX;
+    const int64_t groups = (j.cols + GROUP8 - 1) / GROUP8;
+    if (!off && j.cols % GROUP8 == 0 && (j.rows == 1 || (j.sx == j.cols && j.sc == j.cols && j.ss == groups)) &&
+        j.rows < INT64_MAX / j.cols) {  // no gaps: rows of 256 vectors
+        j.total = j.rows * j.cols;
+        j.cols = j.sx = j.sc = std::min<int64_t>(j.total, 256 * VEC);
+        j.ss = j.cols / GROUP8;
+        j.rows = (j.total + j.cols - 1) / j.cols;
+    }
+    const int64_t vecs = (j.cols + VEC - 1) / VEC + (off && !PACK ? 1 : 0);
+    const Shape8 h = shape8(j.rows, vecs, GROUP8 / VEC, U, sm);
+    if constexpr (PACK) {
+        if (off) TROP_LAUNCH((k_pack8<T, true, 2>), h.grid, h.block, 0, j);
+        else TROP_LAUNCH((k_pack8<T, false, U>), h.grid, h.block, 0, j);
+    } else {
+        if (off) TROP_LAUNCH((k_values8<T, true, U>), h.grid, h.block, 0, j);
+        else TROP_LAUNCH((k_values8<T, false, U>), h.grid, h.block, 0, j);
+    }
+    return TROP_OK;
+}
+
+Job8 job8(int64_t rows, int64_t cols, const void* x, int64_t sx, int dtype, const Kept8& k)
+{
+    Job8 j = {};
+    j.rows = rows;
+    j.cols = cols;
+    j.x = x;
+    j.sx = sx;
+    j.codes = k.codes;
+    j.sc = k.sc;
+    j.scales = k.scales;
+    j.ss = k.ss;
+    const int64_t groups = (cols + GROUP8 - 1) / GROUP8;
+    const int64_t size[2] = {rows, cols}, stride[2] = {sx, 1}, cstride[2] = {k.sc, 1}, gsize[2] = {rows, groups}, gstride[2] = {k.ss, 1};
+    j.sp_x = span_of(x, model_bytes(dtype), 2, size, stride);
+    j.sp_c = span_of(k.codes, 1, 2, size, cstride);
+    j.sp_s = span_of(k.scales, 1, 2, gsize, gstride);
+    return j;
+}
+
+}  // namespace
+
+int launch_activation_pack(int64_t rows, int64_t cols, const NormMat& x, const Kept8& k, cudaStream_t s)
+{
+    const DeviceInfo* dev;
+    TROP_TRY(ensure_device(&dev));
+    const Job8 j = job8(rows, cols, x.p, x.sr, x.dtype, k);
+    return x.dtype == TROP_F32    ? run8<float, true>(j, dev->sm_count, s)
+           : x.dtype == TROP_BF16 ? run8<__nv_bfloat16, true>(j, dev->sm_count, s)
+                                  : run8<__half, true>(j, dev->sm_count, s);
+}
+int launch_activation_values(int64_t rows, int64_t cols, const Kept8& k, const NormMat& x, cudaStream_t s)
+{
+    const DeviceInfo* dev;
+    TROP_TRY(ensure_device(&dev));
+    const Job8 j = job8(rows, cols, x.p, x.sr, x.dtype, k);
+    return x.dtype == TROP_F32    ? run8<float, false>(j, dev->sm_count, s)
+           : x.dtype == TROP_BF16 ? run8<__nv_bfloat16, false>(j, dev->sm_count, s)
+                                  : run8<__half, false>(j, dev->sm_count, s);
+}
+
+}  // namespace trop

@@ -34,6 +34,7 @@ int register_gemm64_kernels();
 int register_gemm_int_kernels();
 int register_backtrack_kernels();
 int register_linear_ce_kernels();
+int register_weight_grad_kernels();
 int launch_fill_i32(int32_t* p, int64_t n, int32_t value, cudaStream_t s);
 
 int register_kernels_for_device()
@@ -45,6 +46,7 @@ int register_kernels_for_device()
     TROP_TRY(register_gemm_int_kernels());
     TROP_TRY(register_backtrack_kernels());
     TROP_TRY(register_linear_ce_kernels());
+    TROP_TRY(register_weight_grad_kernels());
     return TROP_OK;
 }
 

@@ -155,7 +155,7 @@ static PyObject* fc_einsum(PyObject* self, PyObject* const* a, Py_ssize_t nargs)
  * attributes), so the Python wrapper does no per-argument work.  set_torch_handles() gives the
  * dtype objects (matched by identity: float32, int32, int64, float64, bfloat16, float16 -> the
  * trop_dtype codes) and the function returning a device's current raw stream. */
-#define N_DTYPES 6       /* f32, i32, i64, f64, bf16, f16: the trop_dtype codes */
+#define N_DTYPES 8       /* f32, i32, i64, f64, bf16, f16, i8, u8: the trop_dtype codes */
 #define N_TROPICAL 4     /* the ones that the tropical operations know */
 static PyObject* g_dtype_obj[N_DTYPES];
 static PyObject* g_raw_stream;
@@ -711,7 +711,7 @@ static PyMethodDef methods[] = {
     {"einsum", (PyCFunction)(void (*)(void))fc_einsum, METH_FASTCALL, "tropical_einsum_pairwise"},
     {"last_error", (PyCFunction)(void (*)(void))fc_last_error, METH_FASTCALL, "tropical_last_error"},
     {"set_torch_handles", (PyCFunction)(void (*)(void))fc_set_torch_handles, METH_FASTCALL,
-     "dtype objects (float32, int32, int64, float64, bfloat16, float16) and the current-raw-stream function"},
+     "dtype objects (float32, int32, int64, float64, bfloat16, float16, int8, uint8) and the current-raw-stream function"},
     {"permute_trace_t", (PyCFunction)(void (*)(void))fc_permute_trace_t, METH_FASTCALL,
      "tropical_permute_trace on tensor objects"},
     {"permute_pair_t", (PyCFunction)(void (*)(void))fc_permute_pair_t, METH_FASTCALL,

@@ -251,49 +251,6 @@ __device__ __forceinline__ void grad_chunk(const RowState& r, float (&v)[32], in
     for (int i = 0; i < 16; ++i) w[i] = r.t == -1 ? 0u : pack2<BF16>(v[2 * i] * r.g, v[2 * i + 1] * r.g);
 }
 
-// `words` 32-bit words of the lane's row into its warp's box from 16-byte piece `piece` on, swizzled as
-// the box's store expects: piece p of row r lies at p ^ (r mod 8), so the lanes' writes spread over all
-// banks.
-template <int WORDS>
-__device__ __forceinline__ void to_box(uint32_t box, int lane, int piece, const uint32_t (&w)[WORDS])
-{
-#pragma unroll
-    for (int i = 0; i < WORDS / 4; ++i)
-        st_shared16(box + lane * 128 + (((piece + i) ^ (lane & 7)) << 4), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-}
-// The warp's box to (x, y), where that lies in the output.
-__device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t box, int lane, int x, int y, int cols, int rows,
-                                          bool add)
-{
-    async_proxy_fence();
-    __syncwarp();
-    if (lane == 0 && x < cols && y < rows) tma_store_2d(map, box, x, y, add);
-}
-// Before the box is written again: the store has read it.
-__device__ __forceinline__ void box_free(int lane)
-{
-    if (lane == 0) tma_store_wait_read();
-    __syncwarp();
-}
-
-// The same for an output whose rows do not start on 16 bytes: the warp writes row after row, its lanes
-// neighbouring elements.
-__device__ __forceinline__ void copy_box(uint32_t box, int lane, int x, int64_t y, const Job& j)
-{
-    __syncwarp();
-    const int rows = (int)min((int64_t)32, j.rows - y);
-    for (int r = 0; r < rows; ++r)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int e = h * 32 + lane;
-            uint16_t v;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(box + r * 128 + (((e >> 3) ^ (r & 7)) << 4) + (e & 7) * 2));
-            uint16_t* dst = (uint16_t*)j.out + (y + r) * j.ldo + x + e;
-            if (x + e < j.cols && TROP_IN(dst, 2, j.sp_out)) *dst = v;
-        }
-    __syncwarp();
-}
-
 // ------------------------------------------------------------------ joining the units' pairs
 // lse and loss of `rows` tokens from their units' (reference, sum) pairs; the losses' sum.
 struct JoinJob {
@@ -611,7 +568,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     to_box<16>(box, lane, (c % 2) * 4, w);
                     if (c % 2 == 0) continue;
                     if (MODE == GRAD || j.vec) store_box(&map_c, box, lane, col - 32, row0, j.cols, j.rows, false);
-                    else copy_box(box, lane, col - 32, row0, j);
+                    else copy_box<uint16_t>(box, lane, col - 32, row0, j.rows, j.cols, j.out, j.ldo, j.sp_out);
                 }
             }
             if (MODE == LSE && ok) {
@@ -786,7 +743,6 @@ int few_rows(int64_t rows) { return (int)((rows + 7) / 8 * 8); }
 // the L2, so that the other operand is read from memory once per band.  8192x2048x65536: all 32 row
 // tiles (33 MB) 1269 us, bands of 16 / 12 / 8 / 4 1293 / 1305 / 1330 / 1378 us.
 int band_of(int mt, int64_t tile_bytes) { return (int)std::min<int64_t>(mt, std::max<int64_t>(8, (48 << 20) / tile_bytes)); }
-int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 Targets targets_of(const LinearCe& q)
 {
@@ -895,22 +851,6 @@ int launch_linear_ce(const LinearCe& q, float* loss, float* lse, float* total, f
     return launch_join(t, (float2*)(ws.base + at_sums), s);
 }
 
-// Splits of a product's depth of kt stages: the fewest rounds of stages, each split costing about the time of
-// 8 stages more for its partial sums of `bytes` (1 GiB of them at most).  dw of 8192x128x256, one tile of 128
-// stages, takes 64 splits: the whole backward pass 30 us, without splits 55 us.
-int splits(int tiles, int kt, int teams, int64_t bytes)
-{
-    int ks = 1;
-    int64_t best = INT64_MAX;
-    for (int c = 1; c <= std::min(kt, 64); ++c) {
-        const int per = cdiv(kt, c);
-        if (cdiv(kt, per) != c) continue;
-        if (c > 1 && c * bytes > (int64_t)1 << 30) break;
-        const int64_t cost = (int64_t)cdiv((int64_t)tiles * c, teams) * (per + (c > 1 ? 8 : 0));
-        if (cost < best) best = cost, ks = c;
-    }
-    return ks;
-}
 // The splits' f32 sums [ks][slab rows][lda], added in order, into rows of 16-bit elements.
 int launch_split_join(bool bf16, const float* acc, int ks, int64_t slab, int64_t lda, int64_t rows, int64_t D, uint16_t* out,
                       int64_t ldo, const GradScale& grad, int sm, cudaStream_t s)

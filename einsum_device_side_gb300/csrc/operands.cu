@@ -101,23 +101,9 @@ EncodeTiledFn encode_tiled()
     return fn;
 }
 
-}  // namespace
-
-int make_map(CUtensorMap* map, int type, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows)
+template <typename F>
+int encode_checked(F encode)
 {
-    const bool wide = type == TROP_F32;
-    const EncodeTiledFn enc = encode_tiled();
-    if (!enc) return set_error(TROP_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
-    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * (wide ? 4 : 2)};
-    const cuuint32_t box[2] = {wide ? 32u : 64u, (cuuint32_t)box_rows}, one[2] = {1, 1};
-    auto encode = [&] {
-        return enc(map,
-                   wide                ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                   : type == TROP_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                   2, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    };
     CUresult r = encode();
     if (r == CUDA_ERROR_INVALID_CONTEXT) {  // a host thread (autograd's, say) that has not touched the device yet
         int dev = 0;
@@ -127,6 +113,37 @@ int make_map(CUtensorMap* map, int type, const void* base, int64_t cols, int64_t
     }
     if (r != CUDA_SUCCESS) return set_error(TROP_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
     return TROP_OK;
+}
+
+}  // namespace
+
+int make_map(CUtensorMap* map, int type, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows)
+{
+    const bool wide = type == TROP_F32;
+    const EncodeTiledFn enc = encode_tiled();
+    if (!enc) return set_error(TROP_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * (wide ? 4 : 2)};
+    const cuuint32_t box[2] = {wide ? 32u : 64u, (cuuint32_t)box_rows}, one[2] = {1, 1};
+    return encode_checked([&] {
+        return enc(map,
+                   wide                ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                   : type == TROP_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                   2, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    });
+}
+int make_map8(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows)
+{
+    const EncodeTiledFn enc = encode_tiled();
+    if (!enc) return set_error(TROP_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld};
+    const cuuint32_t box[2] = {128u, (cuuint32_t)box_rows}, one[2] = {1, 1};
+    return encode_checked([&] {
+        return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, one,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    });
 }
 
 int pack(Operand& x, Operand& w, const Workspace& ws, int sm)
@@ -143,6 +160,31 @@ int pack(Operand& x, Operand& w, const Workspace& ws, int sm)
     if (e != cudaSuccess) return cuda_error(e, "k_pack launch");
     count_launches(1);
     return TROP_OK;
+}
+
+int pack(Operand& x, const Workspace& ws, int sm)
+{
+    if (!x.packed) return TROP_OK;
+    x.m.p = (const uint16_t*)(ws.base + x.at);
+    const dim3 grid((unsigned)std::min<int64_t>((x.a.rows + 7) / 8, (int64_t)sm * 8));
+    const cudaError_t e = launch_pdl(k_pack, grid, dim3(32, 8), 0, ws.s, x.job(), x.job());
+    if (e != cudaSuccess) return cuda_error(e, "k_pack launch");
+    count_launches(1);
+    return TROP_OK;
+}
+
+int splits(int tiles, int kt, int teams, int64_t bytes)
+{
+    int ks = 1;
+    int64_t best = INT64_MAX;
+    for (int c = 1; c <= std::min(kt, 64); ++c) {
+        const int per = cdiv(kt, c);
+        if (cdiv(kt, per) != c) continue;
+        if (c > 1 && c * bytes > (int64_t)1 << 30) break;
+        const int64_t cost = (int64_t)cdiv((int64_t)tiles * c, teams) * (per + (c > 1 ? 8 : 0));
+        if (cost < best) best = cost, ks = c;
+    }
+    return ks;
 }
 
 }  // namespace trop

@@ -14,6 +14,9 @@ namespace trop {
 // a row-major matrix of bf16, f16 or f32, its rows 16-byte aligned, in boxes of `box_rows` x 128 bytes
 int make_map(CUtensorMap* map, int type, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows);
 
+// rows of bytes, on 16 bytes, in boxes of `box_rows` x 128 that lie in shared memory as they are
+int make_map8(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows);
+
 struct Matrix16 {
     const uint16_t* p;
     int64_t rows, cols, ld;
@@ -51,5 +54,12 @@ struct Operand {
     }
 };
 int pack(Operand& x, Operand& w, const Workspace& ws, int sm);  // the copies of those that need one
+int pack(Operand& x, const Workspace& ws, int sm);
+
+inline int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+// Splits of a product's depth of kt stages: the fewest rounds of stages, each split costing about the time of
+// 8 stages more for its partial sums of `bytes` (1 GiB of them at most).  dw of 8192x128x256, one tile of 128
+// stages, takes 64 splits: the whole backward pass 30 us, without splits 55 us.
+int splits(int tiles, int kt, int teams, int64_t bytes);
 
 }  // namespace trop

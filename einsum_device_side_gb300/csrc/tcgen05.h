@@ -205,6 +205,60 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar)
             : "memory");
 }
 
+// ---------------------------------------------------------------- results through shared memory
+// `words` 32-bit words of the lane's row into its warp's box from 16-byte piece `piece` on, swizzled as
+// the box's store expects: piece p of row r lies at p ^ (r mod 8), so the lanes' writes spread over all
+// banks.
+template <int WORDS>
+__device__ __forceinline__ void to_box(uint32_t box, int lane, int piece, const uint32_t (&w)[WORDS])
+{
+#pragma unroll
+    for (int i = 0; i < WORDS / 4; ++i)
+        st_shared16(box + lane * 128 + (((piece + i) ^ (lane & 7)) << 4), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+}
+// The warp's box to (x, y), where that lies in the output.
+__device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t box, int lane, int x, int y, int cols, int rows,
+                                          bool add)
+{
+    async_proxy_fence();
+    __syncwarp();
+    if (lane == 0 && x < cols && y < rows) tma_store_2d(map, box, x, y, add);
+}
+// Before the box is written again: the store has read it.
+__device__ __forceinline__ void box_free(int lane)
+{
+    if (lane == 0) tma_store_wait_read();
+    __syncwarp();
+}
+// The same for an output whose rows do not start on 16 bytes: the warp writes row after row, its lanes
+// neighbouring elements.
+template <typename T>
+__device__ __forceinline__ void copy_box(uint32_t box, int lane, int x, int64_t y, int64_t rows, int64_t cols, void* out, int64_t ldo,
+                                         const Span& sp)
+{
+    (void)sp;
+    __syncwarp();
+    constexpr int PER = 128 / sizeof(T), PIECE = 16 / sizeof(T);
+    const int n = (int)min((int64_t)32, rows - y);
+    for (int r = 0; r < n; ++r)
+#pragma unroll
+        for (int h = 0; h < PER / 32; ++h) {
+            const int e = h * 32 + lane;
+            const uint32_t at = box + r * 128 + (((e / PIECE) ^ (r & 7)) << 4) + (e % PIECE) * sizeof(T);
+            T* dst = (T*)out + (y + r) * ldo + x + e;
+            if (sizeof(T) == 2) {
+                uint16_t v;
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
+                if (x + e < cols && TROP_IN(dst, 2, sp)) *(uint16_t*)dst = v;
+            } else {
+                uint32_t v;
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
+                if (x + e < cols && TROP_IN(dst, 4, sp)) *(uint32_t*)dst = v;
+            }
+        }
+    __syncwarp();
+}
+
 __device__ __forceinline__ float ex2(float x)
 {
     float y;

@@ -18,7 +18,8 @@ from torch.autograd.function import once_differentiable
 
 import einsum_device_side_gb300 as _pkg
 
-_CODES = {torch.float32: 0, torch.int32: 1, torch.int64: 2, torch.float64: 3, torch.bfloat16: 4, torch.float16: 5}
+_CODES = {torch.float32: 0, torch.int32: 1, torch.int64: 2, torch.float64: 3, torch.bfloat16: 4, torch.float16: 5,
+          torch.int8: 6, torch.uint8: 7}
 BLOCK = 256  # elements that share one scale of an 8-bit AdamW state
 
 

@@ -86,9 +86,18 @@ extern "C" {
 #define TROP_MAX_RANK 32
 
 typedef enum { TROP_MAXPLUS = 0, TROP_MINPLUS = 1, TROP_MAXTIMES = 2 } trop_semiring;
-/* TROP_BF16 and TROP_F16 are types of the training operators only; the tropical operations refuse
- * them with TROP_ERR_DTYPE. */
-typedef enum { TROP_F32 = 0, TROP_I32 = 1, TROP_I64 = 2, TROP_F64 = 3, TROP_BF16 = 4, TROP_F16 = 5 } trop_dtype;
+/* TROP_BF16, TROP_F16, TROP_I8 and TROP_U8 are types of the training operators only; the tropical
+ * operations refuse them with TROP_ERR_DTYPE. */
+typedef enum {
+    TROP_F32 = 0,
+    TROP_I32 = 1,
+    TROP_I64 = 2,
+    TROP_F64 = 3,
+    TROP_BF16 = 4,
+    TROP_F16 = 5,
+    TROP_I8 = 6,
+    TROP_U8 = 7
+} trop_dtype;
 
 enum {
     TROP_OK = 0,
@@ -508,6 +517,93 @@ typedef struct trop_adamw_state_s {
 } trop_adamw_state;
 int tropical_adamw_state_values(int64_t n, const trop_adamw_state* states, void* stream);
 
+/* Activations in 8 bits, kept for the backward pass.  32 consecutive elements of a
+ * row of x [rows, cols] (f32, bf16 or f16) are a group; a row's last one may be
+ * part-filled.  For a group whose largest magnitude has the f32 exponent byte b,
+ *   scale = max(6, b),  unit = 2^(scale - 133),
+ *   code = x / unit rounded to nearest even, at most 127 in magnitude,
+ * every step exact but the one rounding; the value that a code stands for is
+ * code unit.  It is off by at most half a unit, 1 / 128 of the group's largest
+ * magnitude, and by less than a unit above 127.5 units.  A group that holds an
+ * infinity or a NaN has scale 255 and codes 0, and reads back as NaN.
+ * codes: i8 [rows, cols]; scales: u8 [rows, ceil(cols / 32)].  All three have
+ * contiguous columns and any row stride (rows of codes that start on 8 bytes,
+ * or 4 for f32, are written in whole vectors).  tropical_activation_values
+ * writes the values to x, rounded to its type.
+ * Errors: INVALID_ARG, SHAPE, DTYPE, UNSUPPORTED (last axis strided, an extent
+ * of 2^31 - 1024 or more), HOST_POINTER, DEVICE_MISMATCH, CUDA. */
+int tropical_activation_pack(const trop_tensor* x, const trop_tensor* codes, const trop_tensor* scales, void* stream);
+int tropical_activation_values(const trop_tensor* codes, const trop_tensor* scales, const trop_tensor* x, void* stream);
+
+/* The weight gradient of a linear layer whose input was kept in 8 bits:
+ *   dw[o, c] = sum over the tokens of dy[t, o] x[t, c],  db[o] = sum of dy[t, o]
+ * with x the values that codes and scales [T, C] stand for, in dy's type (exact
+ * for bf16; in f16, values outside its range become infinities), products
+ * exact, sums in f32.  dy: [T, O], bf16 or f16, any strides.  dw: [O, C], of
+ * dy's type or f32, contiguous columns.  db: nullable, [O] of dw's type.  No
+ * token: zeros.  Long sums that few tiles have are split and joined in a fixed
+ * order: results repeat bit for bit.  Rows of dy or of codes that TMA cannot
+ * read (not on 16 bytes) are laid out in workspace first.
+ * Errors: INVALID_ARG, SHAPE, DTYPE, UNSUPPORTED (columns of codes, scales or dw
+ * strided, extents of 2^31 - 1024 or more, too many tiles), HOST_POINTER,
+ * DEVICE_MISMATCH, OOM, CUDA. */
+int tropical_activation_weight_grad(const trop_tensor* dy, const trop_tensor* codes, const trop_tensor* scales,
+                                    const trop_tensor* dw, void* db, void* stream);
+
+/* An 8-bit copy: codes and scales as tropical_activation_pack writes them. */
+typedef struct {
+    const trop_tensor* codes;
+    const trop_tensor* scales;
+} trop_kept;
+
+/* The norms after and before a block, fused with its gate, its residual scale
+ * and the addition to the residual stream.  Per row, with a the gate's function:
+ *   v = N(u) post_weight + post_bias  (post_norm; else u),
+ *   r = alpha x + scale a(gate) v,    y = N(r) weight + bias,
+ *   N(t) = (t - mean) / sqrt(mean of (t - mean)^2 + eps);  rms norm: mean = 0.
+ * norm: 0 layer, 1 rms.  gate_act: 0 the gate itself, 1 its sigmoid, 2 gate
+ * sigmoid(gate).  The vectors [cols] are of wdtype (y's type or f32) and each
+ * nullable (ones, zeros, no vector); scale_vector takes the place of scale. */
+typedef struct {
+    int norm, post_norm, gate_act, wdtype;
+    double alpha, scale, eps;
+    const void *weight, *bias, *post_weight, *post_bias, *scale_vector;
+} trop_residual_options;
+
+/* x, u, y, r: [rows, cols], contiguous columns, any row stride.  r has x's type;
+ * u and gate have it too, or 16 bits beside an f32 x; y has u's type, or 16 bits
+ * beside an f32 u.  gate: nullable, [rows, cols] or [rows, 1].  Sums and the
+ * stream inside a row are f32, each stored value is rounded once.  stats:
+ * nullable f32 [4][rows], mean and rstd of u's norm (0 and 1 without one) and of
+ * r's: what the backward call reads.  kept: nullable, three 8-bit copies that
+ * the call leaves of u, gate and the stored r (all three; gate's members are NULL
+ * where it is absent or one a row).
+ * Errors: INVALID_ARG, SHAPE (cols == 0 or shapes differ), DTYPE, UNSUPPORTED
+ * (last axis strided, an extent of 2^31 - 1024 or more), HOST_POINTER,
+ * DEVICE_MISMATCH, CUDA. */
+int tropical_residual_norm(const trop_residual_options* options, const trop_tensor* x, const trop_tensor* u,
+                           const trop_tensor* gate, const trop_tensor* y, const trop_tensor* r, float* stats,
+                           const trop_kept* kept, void* stream);
+
+/* Gradients wanted; each nullable.  The tensors have the types and shapes of x,
+ * u and gate, the vectors are [cols] of wdtype; dscale is scale_vector's. */
+typedef struct {
+    const trop_tensor *dx, *du, *dgate;
+    void *dscale, *dweight, *dbias, *dpost_weight, *dpost_bias;
+} trop_residual_grads;
+
+/* Backward of tropical_residual_norm.  dy: y's gradient; dr: nullable, what
+ * reaches r from elsewhere (x's type).  r, u and gate as the forward call had
+ * them, or with `kept` their 8-bit copies (r and u NULL, gate only if it is one a
+ * row), then with x_dtype and u_dtype the types of the gradients; without `kept`
+ * the two are not read.  The column sums are added in a fixed order: results
+ * repeat bit for bit.  No row: zeros in the vectors' gradients.
+ * Errors: as tropical_residual_norm, plus OOM. */
+int tropical_residual_norm_backward(const trop_residual_options* options, const trop_tensor* dy, const trop_tensor* dr,
+                                    const trop_tensor* r, const trop_tensor* u, const trop_tensor* gate,
+                                    const float* stats, const trop_kept* kept, int x_dtype, int u_dtype,
+                                    const trop_residual_grads* grads, void* stream);
+
 /* Drain the workspace retirement queue: wait for every pending event and
  * return the blocks to the pool [WR "Open decisions" 1: explicit
  * synchronize() is a drain point].  The only call that may block the host. */
@@ -545,7 +641,8 @@ int tropical_device_wait_timeouts(unsigned int* count, int reset);
  * skipped and counted, and the first one's location and address kept.
  * *line = (file id << 16) | source line, the file ids being 1 unary.cu, 2
  * gemm.cu, 3 gemm64.cu, 4 gemm_int.cu, 5 backward.cu, 6 backtrack.cu, 7
- * layer_norm.cu, 8 adamw.cu, 9 linear_ce.cu, 10 operands.cu.
+ * layer_norm.cu, 8 adamw.cu, 9 linear_ce.cu, 10 operands.cu,
+ * 11 activation.cu, 12 residual_norm.cu, 13 weight_grad.cu.
  * Reads the record of the current device without synchronising: call it once
  * the work to inspect has completed.  reset != 0 clears the record.  The
  * normal build returns TROP_ERR_UNSUPPORTED with *count = 0.  It stands in
