@@ -2,7 +2,7 @@
 //
 // Both directions are bound by memory: a 16-bit element is 2 bytes one way and 1 + 1/32 the other.  A thread has the
 // elements of 16 bytes, 32 / that many neighbouring lanes a group, whose largest magnitude they find by shuffles; U rows'
-// loads are on their way together.  Matrices without gaps are taken as rows of 256 vectors, whatever their width.
+// loads are on their way together.  Matrices without gaps are taken as one row.
 // Rows that do not lie on 16 bytes keep whole vectors all the same: two aligned loads are shifted together (pack), or
 // the vectors are laid where the result's are aligned and the codes shifted (values).
 #include <cuda_runtime.h>
@@ -19,8 +19,8 @@ namespace trop {
 namespace {
 
 struct Job8 {
-    int64_t rows, cols, total;  // total: elements of a matrix without gaps taken as rows, else none's end
-    const void* x;              // pack: the elements; values: the result
+    int64_t rows, cols;
+    const void* x;  // pack: the elements; values: the result
     int64_t sx;
     int8_t* codes;
     int64_t sc;
@@ -33,7 +33,7 @@ struct Job8 {
 // VEC elements from any element on, where the aligned 32 bytes around them lie in the matrix; else one by one.  Elements from
 // `left` on are zero.
 template <typename T, int VEC>
-__device__ __forceinline__ void read_any(const T* p, int64_t left, const T* begin, const T* end, Raw<T, VEC>& q, const Span& sp)
+__device__ __forceinline__ void read_any(const T* p, int left, const T* begin, const T* end, Raw<T, VEC>& q, const Span& sp)
 {
     (void)sp;
     const uint32_t off = (uint32_t)((uintptr_t)p & 15);
@@ -68,12 +68,12 @@ __device__ __forceinline__ void read_any(const T* p, int64_t left, const T* begi
 }
 
 template <typename T, bool OFF, int U>
-__global__ void __launch_bounds__(256) k_pack8(const Job8 j)
+__global__ void __launch_bounds__(256, 4) k_pack8(const Job8 j)
 {
     pdl_wait();
     pdl_signal();
     constexpr int VEC = 16 / sizeof(T);
-    const int64_t c = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * VEC;
+    const int c = (int)(blockIdx.x * blockDim.x + threadIdx.x) * VEC, cols = (int)j.cols;
     const T* const begin = (const T*)j.x;
     const T* const end = begin + (j.rows - 1) * j.sx + j.cols;
     const int64_t step = (int64_t)gridDim.y * blockDim.y;
@@ -82,11 +82,11 @@ __global__ void __launch_bounds__(256) k_pack8(const Job8 j)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t row = row0 + u * step + threadIdx.y;
-            const bool live = row < j.rows && c < j.cols && row * j.cols + c < j.total;
+            const bool live = row < j.rows && c < cols;
             const T* p = begin + row * j.sx + c;
             q[u].zero();
             if (OFF) {
-                if (live) read_any<T, VEC>(p, j.cols - c, begin, end, q[u], j.sp_x);
+                if (live) read_any<T, VEC>(p, cols - c, begin, end, q[u], j.sp_x);
             } else if (live && TROP_IN(p, 16, j.sp_x)) {
                 q[u].read(p);
             }
@@ -94,18 +94,18 @@ __global__ void __launch_bounds__(256) k_pack8(const Job8 j)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t row = row0 + u * step + threadIdx.y;
-            const bool live = row < j.rows && c < j.cols && row * j.cols + c < j.total;
+            const bool live = row < j.rows && c < cols;
             const uint32_t e = scale8(group_top8<VEC>(top8<T, VEC>(q[u])));
             if (!live) continue;
             Codes<VEC> k;
             codes8<T, VEC>(q[u], e, k.w);
             int8_t* to = j.codes + row * j.sc + c;
-            if (!OFF || (j.wide_codes && c + VEC <= j.cols)) {
+            if (!OFF || (j.wide_codes && c + VEC <= cols)) {
                 if (TROP_IN(to, VEC, j.sp_c)) k.write(to);
             } else {
 #pragma unroll
                 for (int i = 0; i < VEC; ++i)
-                    if (c + i < j.cols && TROP_IN(to + i, 1, j.sp_c)) to[i] = (int8_t)(k.w[i / 4] >> 8 * (i % 4));
+                    if (c + i < cols && TROP_IN(to + i, 1, j.sp_c)) to[i] = (int8_t)(k.w[i / 4] >> 8 * (i % 4));
             }
             uint8_t* s = j.scales + row * j.ss + c / GROUP8;
             if (c % GROUP8 == 0 && TROP_IN(s, 1, j.sp_s)) *s = (uint8_t)e;
@@ -113,16 +113,17 @@ __global__ void __launch_bounds__(256) k_pack8(const Job8 j)
     }
 }
 
-// VEC codes from any one on, with the same rule on what lies around them.
+// VEC codes from any byte on: the aligned words around them, where those lie in the matrix (whatever row of it), shifted
+// together; at the matrix's own ends one by one.  Bytes outside the row are whatever they are: nobody stores them.
 template <int VEC>
-__device__ __forceinline__ void codes_any(const int8_t* p, int64_t left, const int8_t* begin, const int8_t* end, Codes<VEC>& q,
+__device__ __forceinline__ void codes_any(const int8_t* p, int skip, int left, const int8_t* begin, const int8_t* end, Codes<VEC>& q,
                                           const Span& sp)
 {
     (void)sp;
     constexpr int N = VEC / 4;
     const uint32_t off = (uint32_t)((uintptr_t)p & 3);
     const int8_t* const at = p - off;
-    if (left >= VEC && at >= begin && at + VEC + 4 <= end) {
+    if (at >= begin && at + VEC + 4 <= end) {
         uint32_t w[N + 1];
 #pragma unroll
         for (int i = 0; i <= N; ++i) w[i] = TROP_IN(at + 4 * i, 4, sp) ? reinterpret_cast<const uint32_t*>(at)[i] : 0;
@@ -132,66 +133,120 @@ __device__ __forceinline__ void codes_any(const int8_t* p, int64_t left, const i
         q.zero();
 #pragma unroll
         for (int i = 0; i < VEC; ++i)
-            if (i < left && p + i >= begin && TROP_IN(p + i, 1, sp)) q.w[i / 4] |= (uint32_t)(uint8_t)p[i] << 8 * (i % 4);
+            if (i >= skip && i < left && TROP_IN(p + i, 1, sp)) q.w[i / 4] |= (uint32_t)(uint8_t)p[i] << 8 * (i % 4);
     }
 }
 
+// (Registers are held down to where the loads of several rows from many warps are on their way: ragged rows at 193 registers
+// a thread and with both edges of every row one by one took 232 us for 40950x1001 f16.)
 template <typename T, bool OFF, int U>
-__global__ void __launch_bounds__(256) k_values8(const Job8 j)
+__global__ void __launch_bounds__(256, 4) k_values8(const Job8 j)
 {
     pdl_wait();
     pdl_signal();
     constexpr int VEC = 16 / sizeof(T);
-    const int64_t vec = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    const int vec = blockIdx.x * blockDim.x + threadIdx.x, cols = (int)j.cols;
     const int64_t step = (int64_t)gridDim.y * blockDim.y;
     const int8_t* const end = j.codes + (j.rows - 1) * j.sc + j.cols;
-    for (int64_t row0 = (int64_t)blockIdx.y * blockDim.y; row0 < j.rows; row0 += step * U) {
+    // the first column of the thread's vector of a row: where the result's vectors lie on 16 bytes
+    auto column = [&](const T* out) { return vec * VEC - (OFF ? (int)((uint32_t)(uintptr_t)out & 15) / (int)sizeof(T) : 0); };
+    for (int64_t row0 = (int64_t)blockIdx.y * blockDim.y + threadIdx.y; row0 < j.rows; row0 += step * U) {
         Codes<VEC> q[U];
         uint32_t s0[U], s1[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t row = row0 + u * step + threadIdx.y;
-            T* const out = (T*)j.x + row * j.sx;
-            // the first column: where the result's vectors lie on 16 bytes
-            const int64_t c = vec * VEC - (OFF ? (int64_t)((uintptr_t)out & 15) / (int64_t)sizeof(T) : 0);
+            const int64_t row = row0 + u * step;
+            const int c = column((const T*)j.x + row * j.sx);
             const int8_t* p = j.codes + row * j.sc + c;
             const uint8_t* s = j.scales + row * j.ss;
-            q[u].zero();
             s0[u] = s1[u] = LEAST8;
-            if (row >= j.rows || c >= j.cols || row * j.cols + c >= j.total) continue;
-            const int64_t g0 = (c < 0 ? 0 : c) / GROUP8;
-            if (TROP_IN(s + g0, 1, j.sp_s)) s0[u] = s[g0];
-            if (OFF) {
-                const int64_t g1 = (c + VEC > j.cols ? j.cols - 1 : c + VEC - 1) / GROUP8;
-                s1[u] = g1 == g0 ? s0[u] : TROP_IN(s + g1, 1, j.sp_s) ? s[g1] : LEAST8;
-                codes_any<VEC>(p, j.cols - c, c < 0 ? p - c : j.codes, end, q[u], j.sp_c);
-            } else if (TROP_IN(p, VEC, j.sp_c)) {
-                q[u].read(p);
+            if (row < j.rows && c < cols) {
+                const int g0 = max(c, 0) / GROUP8, g1 = min(c + VEC - 1, cols - 1) / GROUP8;
+                if (TROP_IN(s + g0, 1, j.sp_s)) s0[u] = s[g0];
+                if (OFF && TROP_IN(s + g1, 1, j.sp_s)) s1[u] = s[g1];
+                if (OFF) codes_any<VEC>(p, -c, cols - c, j.codes, end, q[u], j.sp_c);
+                else if (TROP_IN(p, VEC, j.sp_c)) q[u].read(p);
             }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t row = row0 + u * step + threadIdx.y;
+            const int64_t row = row0 + u * step;
             T* const out = (T*)j.x + row * j.sx;
-            const int64_t c = vec * VEC - (OFF ? (int64_t)((uintptr_t)out & 15) / (int64_t)sizeof(T) : 0);
-            if (row >= j.rows || c >= j.cols || row * j.cols + c >= j.total) continue;
+            const int c = column(out);
+            if (row >= j.rows || c >= cols) continue;
             float v[VEC];
-            values8<VEC>(q[u].w, unit8(s0[u]), v);
-            if (OFF && s1[u] != s0[u]) {
+            const float unit = unit8(s0[u]);
+            if (OFF) {
                 const float other = unit8(s1[u]);
-                const int64_t edge = (c < 0 ? 0 : c) / GROUP8 * GROUP8 + GROUP8 - c;  // elements of the first group
+                const int edge = max(c, 0) / GROUP8 * GROUP8 + GROUP8 - c;  // elements up to the first group's end
 #pragma unroll
-                for (int i = 0; i < VEC; ++i)
-                    if (i >= edge) v[i] = coded8(q[u].w[i / 4] ^ 0x80808080u, i % 4) * other;
+                for (int i = 0; i < VEC; ++i) v[i] = coded8(q[u].w[i / 4] ^ 0x80808080u, i % 4) * (i < edge ? unit : other);
+            } else {
+                values8<VEC>(q[u].w, unit, v);
             }
-            if (!OFF || (c >= 0 && c + VEC <= j.cols)) {
+            if (!OFF || (c >= 0 && c + VEC <= cols)) {
                 store<T, VEC>(out + c, v, j.sp_x);
             } else {
 #pragma unroll
                 for (int i = 0; i < VEC; ++i)
-                    if (c + i >= 0 && c + i < j.cols && TROP_IN(out + c + i, sizeof(T), j.sp_x)) out[c + i] = from_f32<T>(v[i]);
+                    if (c + i >= 0 && c + i < cols && TROP_IN(out + c + i, sizeof(T), j.sp_x)) out[c + i] = from_f32<T>(v[i]);
             }
         }
+    }
+}
+
+// Matrices without gaps, in whole groups: U vectors of a thread, a block's width apart.
+template <typename T, int U>
+__global__ void __launch_bounds__(256) k_pack8_flat(const T* x, int8_t* codes, uint8_t* scales, int64_t vecs, Span sp_x, Span sp_c,
+                                                    Span sp_s)
+{
+    pdl_wait();
+    pdl_signal();
+    constexpr int VEC = 16 / sizeof(T);
+    const int64_t first = (int64_t)blockIdx.x * (256 * U) + threadIdx.x;
+    Raw<T, VEC> q[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t i = first + u * 256;
+        q[u].zero();
+        if (i < vecs && TROP_IN(x + i * VEC, 16, sp_x)) q[u].read(x + i * VEC);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t i = first + u * 256;
+        const uint32_t e = scale8(group_top8<VEC>(top8<T, VEC>(q[u])));
+        Codes<VEC> k;
+        codes8<T, VEC>(q[u], e, k.w);
+        if (i >= vecs) break;
+        if (TROP_IN(codes + i * VEC, VEC, sp_c)) k.write(codes + i * VEC);
+        if (i % (GROUP8 / VEC) == 0 && TROP_IN(scales + i / (GROUP8 / VEC), 1, sp_s)) scales[i / (GROUP8 / VEC)] = (uint8_t)e;
+    }
+}
+template <typename T, int U>
+__global__ void __launch_bounds__(256) k_values8_flat(const int8_t* codes, const uint8_t* scales, T* x, int64_t vecs, Span sp_c, Span sp_s,
+                                                      Span sp_x)
+{
+    pdl_wait();
+    pdl_signal();
+    constexpr int VEC = 16 / sizeof(T);
+    const int64_t first = (int64_t)blockIdx.x * (256 * U) + threadIdx.x;
+    Codes<VEC> q[U];
+    uint32_t e[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t i = first + u * 256;
+        q[u].zero();
+        e[u] = LEAST8;
+        if (i < vecs && TROP_IN(codes + i * VEC, VEC, sp_c)) q[u].read(codes + i * VEC);
+        if (i < vecs && TROP_IN(scales + i / (GROUP8 / VEC), 1, sp_s)) e[u] = scales[i / (GROUP8 / VEC)];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t i = first + u * 256;
+        if (i >= vecs) break;
+        float v[VEC];
+        values8<VEC>(q[u].w, unit8(e[u]), v);
+        store<T, VEC>(x + i * VEC, v, sp_x);
     }
 }
 
@@ -215,18 +270,22 @@ Shape8 shape8(int64_t rows, int64_t vecs, int lanes, int u, int sm)
 template <typename T, bool PACK>
 int run8(Job8 j, int sm, cudaStream_t s)
 {
-    constexpr int VEC = 16 / sizeof(T), U = 4;
+    constexpr int VEC = 16 / sizeof(T), U = 4;  // (rows off 16 bytes: 2)
     const bool on16 = j.cols % VEC == 0 && aligned(j.x, j.sx, sizeof(T), VEC, j.rows);
     j.wide_codes = aligned(j.codes, j.sc, 1, VEC, j.rows);
     const bool off = !on16 || !j.wide_codes;
-    j.total = INT64_MAX;
     const int64_t groups = (j.cols + GROUP8 - 1) / GROUP8;
-    if (!off && j.cols % GROUP8 == 0 && (j.rows == 1 || (j.sx == j.cols && j.sc == j.cols && j.ss == groups)) &&
-        j.rows < INT64_MAX / j.cols) {  // no gaps: rows of 256 vectors
-        j.total = j.rows * j.cols;
-        j.cols = j.sx = j.sc = std::min<int64_t>(j.total, 256 * VEC);
-        j.ss = j.cols / GROUP8;
-        j.rows = (j.total + j.cols - 1) / j.cols;
+    if (!off && j.cols % GROUP8 == 0 && (j.rows == 1 || (j.sx == j.cols && j.sc == j.cols && j.ss == groups))) {
+        const int64_t vecs = j.rows * groups * (GROUP8 / VEC), blocks = (vecs + 256 * U - 1) / (256 * U);
+        if (blocks <= INT32_MAX) {
+            const dim3 grid((unsigned)blocks), block(256);
+            if constexpr (PACK)
+                TROP_LAUNCH((k_pack8_flat<T, U>), grid, block, 0, (const T*)j.x, j.codes, j.scales, vecs, j.sp_x, j.sp_c, j.sp_s);
+            else
+                TROP_LAUNCH((k_values8_flat<T, U>), grid, block, 0, (const int8_t*)j.codes, (const uint8_t*)j.scales, (T*)j.x, vecs, j.sp_c,
+                            j.sp_s, j.sp_x);
+            return TROP_OK;
+        }
     }
     const int64_t vecs = (j.cols + VEC - 1) / VEC + (off && !PACK ? 1 : 0);
     const Shape8 h = shape8(j.rows, vecs, GROUP8 / VEC, U, sm);
@@ -234,7 +293,7 @@ int run8(Job8 j, int sm, cudaStream_t s)
         if (off) TROP_LAUNCH((k_pack8<T, true, 2>), h.grid, h.block, 0, j);
         else TROP_LAUNCH((k_pack8<T, false, U>), h.grid, h.block, 0, j);
     } else {
-        if (off) TROP_LAUNCH((k_values8<T, true, U>), h.grid, h.block, 0, j);
+        if (off) TROP_LAUNCH((k_values8<T, true, 2>), h.grid, h.block, 0, j);
         else TROP_LAUNCH((k_values8<T, false, U>), h.grid, h.block, 0, j);
     }
     return TROP_OK;
