@@ -133,19 +133,6 @@ int make_map(CUtensorMap* map, int type, const void* base, int64_t cols, int64_t
                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     });
 }
-int make_map8(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows, int box_cols)
-{
-    const EncodeTiledFn enc = encode_tiled();
-    if (!enc) return set_error(TROP_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
-    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld};
-    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows}, one[2] = {1, 1};
-    return encode_checked([&] {
-        return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, one,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    });
-}
-
 int pack(Operand& x, Operand& w, const Workspace& ws, int sm)
 {
     int64_t blocks = 0;

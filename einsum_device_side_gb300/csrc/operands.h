@@ -14,9 +14,6 @@ namespace trop {
 // a row-major matrix of bf16, f16 or f32, its rows 16-byte aligned, in boxes of `box_rows` x 128 bytes
 int make_map(CUtensorMap* map, int type, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows);
 
-// rows of bytes, on 16 bytes, in boxes of `box_rows` x `box_cols` that lie in shared memory as they are
-int make_map8(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows, int box_cols);
-
 struct Matrix16 {
     const uint16_t* p;
     int64_t rows, cols, ld;

@@ -5,14 +5,15 @@
 // dy bf16 or f16, sums in f32, results in dy's type or f32, rounded once.  A code has seven bits and its scale is a power
 // of two, so bf16 operands hold the values exactly (f16 where they lie in its range).
 //
-// Tiles of 256 x 256 of dw by pairs of CTAs, as the products of linear_ce.cu, with one step more: what TMA brings of x is
-// codes, and warps of their own turn a stage's codes into the 16-bit operand tile.  A stage is 64 tokens; a CTA's part
-// is 128 columns of dy (16 KB), 128 columns of codes (8 KB) and the operand made of those (16 KB).
-//   warp 0       loads: dy's boxes onto the pair's first CTA's barrier, the codes' onto the CTA's own
-//   warp 1       products (first CTA), one thread
+// The codes become operands in workspace, a piece of x's columns at a time (64 MiB: it is still in the L2 when the products
+// read it), by the kernel of activation.cu; the products are tiles of 256 x 256 of dw by pairs of CTAs, both operands
+// token-major as they lie:
+//   warp 0       loads: boxes of 64 tokens x 64 columns of dy and of x, by TMA into a ring of six stages
+//   warp 1       products, one thread of the pair's first CTA
 //   warps 4-11   results: tensor memory to dw, or to the f32 sums of a split of the tokens
-//   warps 12-19  codes to operands: 2.5 instructions an element (bytes to f32 by permutation, two at a time by packed
-//                operations), under half of the issue slots that the products of a stage leave
+// (Codes that came by TMA and were made operands inside this kernel, by warps of their own: 8192^3 bf16 2034 us, in
+// pieces 640 us.  The tensor cores' own reads take three quarters of the shared memory's rate, so that those warps' loads
+// and stores waited 1200 cycles each; 64x16384x4096 to f32 55 us and 54 us.)
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -32,17 +33,11 @@ namespace trop {
 namespace {
 
 constexpr int TK = 64, TM = 256, TN = 256;
-constexpr int A_BYTES = 128 * TK * 2, B_BYTES = 128 * TK * 2, C_BYTES = 128 * TK;
-constexpr int S_BYTES = TK * 16;  // 16 groups' scales of every token: TMA's least, and four of them the CTA's
-constexpr int STAGES = 4, CODES = 6;     // of dy and of the operand made of codes; of codes
-constexpr int LEAD = 2;
-constexpr int EPI_WARPS = 8, CONV_WARPS = 8, THREADS = 128 + 32 * (EPI_WARPS + CONV_WARPS);
-// The warps that convert take the stages in turn, in groups: a warp's waits, fences and the latency of its loads are the stage's
-// cost beside the instructions, and are paid once for more rows.  (A ring's slots are a multiple of the groups: each
-// then belongs to one of them, which waits for every one of its phases.)
-constexpr int GROUPS = 2, GROUP_WARPS = CONV_WARPS / GROUPS, GROUP_ROWS = TK / 4 / GROUP_WARPS;
+constexpr int HALF_BYTES = 128 * TK * 2;  // a CTA's part of either operand in a stage
+constexpr int STAGE_BYTES = 2 * HALF_BYTES, STAGES = 6;
+constexpr int EPI_WARPS = 8, THREADS = 128 + 32 * EPI_WARPS;
 constexpr int BOX_BYTES = 4096;
-constexpr int SMEM = STAGES * (A_BYTES + B_BYTES) + CODES * (C_BYTES + S_BYTES) + EPI_WARPS * BOX_BYTES + 1024;
+constexpr int SMEM = STAGES * STAGE_BYTES + EPI_WARPS * BOX_BYTES + 1024;
 
 struct Job {
     int mt, nt, kt, kper, units;
@@ -70,59 +65,26 @@ __device__ __forceinline__ Unit unit_of(const Job& j, int u)
     return r;
 }
 
-// The stages of a pair of CTAs, one after the other.
-struct Stage {
-    const Job& j;
-    int u, step, k;
-    uint32_t n = 0;
-    Unit t;
-    __device__ __forceinline__ Stage(const Job& j_, int first, int step_) : j(j_), u(first), step(step_), k(0)
-    {
-        if (more()) t = unit_of(j, u), k = t.k0;
-    }
-    __device__ __forceinline__ bool more() const { return u < j.units; }
-    __device__ __forceinline__ void next()
-    {
-        ++n;
-        if (++k < t.k1) return;
-        u += step;
-        if (more()) t = unit_of(j, u), k = t.k0;
-    }
-};
-
-// 16 codes of one scale as two 16-byte pieces of 16-bit elements
-template <bool BF16>
-__device__ __forceinline__ void to_operand(const uint4& q, float unit, uint32_t (&w)[8])
-{
-    const uint32_t in[4] = {q.x, q.y, q.z, q.w};
-    float v[16];
-    values8<16>(in, unit, v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = pack2<BF16>(v[2 * i], v[2 * i + 1]);
-}
-
 template <bool BF16>
 __global__ void __launch_bounds__(THREADS, 1)
-    k_weight_grad(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_k,
-                  const __grid_constant__ CUtensorMap map_s, const __grid_constant__ CUtensorMap map_c, const __grid_constant__ Job j)
+    k_weight_grad(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                  const __grid_constant__ CUtensorMap map_c, const __grid_constant__ Job j)
 {
     extern __shared__ uint8_t dyn[];
-    __shared__ __align__(8) uint64_t full[STAGES], ready[STAGES], empty[STAGES], codes[CODES], kempty[CODES], tfull[2], tempty[2], drain;
+    __shared__ __align__(8) uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], drain;
     __shared__ uint32_t tmem_slot;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
-    const uint32_t ring_a = (smem_u32(dyn) + 1023u) & ~1023u, ring_b = ring_a + STAGES * A_BYTES;
-    const uint32_t boxes = ring_b + STAGES * B_BYTES, ring_k = boxes + EPI_WARPS * BOX_BYTES, ring_s = ring_k + CODES * C_BYTES;
+    const uint32_t ring = (smem_u32(dyn) + 1023u) & ~1023u, boxes = ring + STAGES * STAGE_BYTES;
     const int first = blockIdx.x / 2, step = gridDim.x / 2;
 
     if (warp == 1 && lane == 0) {
-        for (int s = 0; s < STAGES; ++s) mbar_init(&full[s], 1), mbar_init(&ready[s], GROUP_WARPS * 2), mbar_init(&empty[s], 1);
-        for (int s = 0; s < CODES; ++s) mbar_init(&codes[s], 1), mbar_init(&kempty[s], GROUP_WARPS);
+        for (int s = 0; s < STAGES; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
         for (int b = 0; b < 2; ++b) mbar_init(&tfull[b], 1), mbar_init(&tempty[b], EPI_WARPS * 2);
         mbar_init(&drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 0 && lane == 0) tma_prefetch_map(&map_a), tma_prefetch_map(&map_k), tma_prefetch_map(&map_s);
+    if (warp == 0 && lane == 0) tma_prefetch_map(&map_a), tma_prefetch_map(&map_b);
     if (warp == 2) tmem_alloc_all<2>(&tmem_slot);
     tc_fence_before();
     __syncthreads();
@@ -133,33 +95,30 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     bool ok = true;
     if (warp == 0) {
-        if (lane == 0) {  // loads: codes LEAD stages ahead of dy, which is not wanted before they are operands
-            Stage at_a(j, first, step), at_c(j, first, step);
-            while (at_a.more() && ok) {
-                while (at_c.more() && at_c.n <= at_a.n + LEAD) {
-                    const uint32_t s = at_c.n % CODES;
-                    if (!(ok = mbar_wait(&kempty[s], (at_c.n / CODES & 1) ^ 1))) break;
-                    const int cn = at_c.t.n * TN + rank * 128;
-                    mbar_expect_tx(&codes[s], C_BYTES + S_BYTES);
-                    tma_load_2d<1>(ring_k + s * C_BYTES, &map_k, cn, at_c.k * TK, smem_u32(&codes[s]));
-                    tma_load_2d<1>(ring_s + s * S_BYTES, &map_s, cn / GROUP8 / 16 * 16, at_c.k * TK, smem_u32(&codes[s]));
-                    at_c.next();
-                }
-                if (!ok) break;
-                const uint32_t s = at_a.n % STAGES;
-                if (!(ok = mbar_wait(&empty[s], (at_a.n / STAGES & 1) ^ 1))) break;
-                const int am = at_a.t.m * TM + rank * 128;
-                if (rank == 0) mbar_expect_tx(&full[s], 2 * A_BYTES);
-                const uint32_t bar = mapa(smem_u32(&full[s]), 0);
+        if (lane == 0) {  // loads
+            int s = 0;
+            uint32_t phase = 0, issued = 0;
+            for (int u = first; u < j.units && ok; u += step) {
+                const Unit t = unit_of(j, u);
+                const int am = t.m * TM + rank * 128, bn = t.n * TN + rank * 128;
+                for (int k = t.k0; k < t.k1; ++k) {
+                    if (!(ok = mbar_wait(&empty[s], phase ^ 1))) break;
+                    if (rank == 0) mbar_expect_tx(&full[s], 2 * STAGE_BYTES);
+                    const uint32_t bar = mapa(smem_u32(&full[s]), 0), to = ring + s * STAGE_BYTES;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) tma_load_2d<2>(ring_a + s * A_BYTES + c * 8192, &map_a, am + 64 * c, at_a.k * TK, bar);
-                at_a.next();
+                    for (int c = 0; c < 2; ++c) {
+                        tma_load_2d<2>(to + c * 8192, &map_a, am + 64 * c, k * TK, bar);
+                        tma_load_2d<2>(to + HALF_BYTES + c * 8192, &map_b, bn + 64 * c, k * TK, bar);
+                    }
+                    ++issued;
+                    if (++s == STAGES) s = 0, phase ^= 1;
+                }
             }
-            if (!ok) {  // no copy may land after the CTA has left
-                for (uint32_t i = at_c.n - min(at_c.n, (uint32_t)CODES); i < at_c.n; ++i) (void)mbar_wait(&codes[i % CODES], i / CODES & 1);
-                if (rank == 0)
-                    for (uint32_t i = at_a.n - min(at_a.n, (uint32_t)STAGES); i < at_a.n; ++i) (void)mbar_wait(&full[i % STAGES], i / STAGES & 1);
-            }
+            if (!ok && rank == 0)  // no copy may land after the CTA has left
+                for (uint32_t i = 0; i < min(issued, (uint32_t)STAGES); ++i) {
+                    if (--s < 0) s = STAGES - 1, phase ^= 1;
+                    (void)mbar_wait(&full[s], phase);
+                }
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {  // products
@@ -172,9 +131,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!(ok = mbar_wait_cluster(&tempty[buf], ((tile >> 1) & 1) ^ 1))) break;
                 tc_fence_after();
                 for (int k = t.k0; k < t.k1; ++k) {
-                    if (!(ok = mbar_wait_cluster(&full[s], phase) && mbar_wait_cluster(&ready[s], phase))) break;
+                    if (!(ok = mbar_wait_cluster(&full[s], phase))) break;
                     tc_fence_after();
-                    const uint64_t da = smem_desc(ring_a + s * A_BYTES, 8192), db = smem_desc(ring_b + s * B_BYTES, 8192);
+                    const uint32_t at = ring + s * STAGE_BYTES;
+                    const uint64_t da = smem_desc(at, 8192), db = smem_desc(at + HALF_BYTES, 8192);
 #pragma unroll
                     for (int i = 0; i < TK / 16; ++i) tc_mma<2>(acc, da + i * 128, db + i * 128, idesc, k > t.k0 || i > 0);
                     tc_commit<2>(&empty[s]);
@@ -185,52 +145,6 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (!ok) {  // no product may run after the CTA has left
                 tc_commit<2>(&drain);
                 (void)mbar_wait(&drain, 0);
-            }
-        }
-    } else if (warp >= 4 + EPI_WARPS) {  // codes to operands
-        const int w = (warp - 4 - EPI_WARPS) % GROUP_WARPS, group = (warp - 4 - EPI_WARPS) / GROUP_WARPS;
-        const int piece = lane & 7;   // 16 columns each
-        const int swap = piece >> 2;  // (the two halves' stores then meet no bank twice)
-        uint32_t n = 0;               // stages so far
-        for (int u = first; u < j.units && ok; u += step) {
-            const Unit t = unit_of(j, u);
-            const uint32_t at_scale = ((t.n * TN + rank * 128) / GROUP8) % 16 + (piece >> 1);
-            for (int k = t.k0; k < t.k1; ++k, ++n) {
-                if (n % GROUPS != group) continue;
-                const uint32_t s = n % CODES, b = n % STAGES;
-                ok = mbar_wait(&codes[s], n / CODES & 1) && mbar_wait(&empty[b], (n / STAGES & 1) ^ 1);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                const uint32_t from = ring_k + s * C_BYTES, scales = ring_s + s * S_BYTES + at_scale;
-                uint4 q[GROUP_ROWS];
-                uint32_t e[GROUP_ROWS];
-#pragma unroll
-                for (int i = 0; i < GROUP_ROWS; ++i) {
-                    const int row = w * (4 * GROUP_ROWS) + i * 4 + (lane >> 3);
-                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(q[i].x), "=r"(q[i].y), "=r"(q[i].z), "=r"(q[i].w)
-                                 : "r"(from + row * 128 + piece * 16));
-                    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(e[i]) : "r"(scales + row * 16));
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&kempty[s]), rank));
-#pragma unroll
-                for (int i = 0; i < GROUP_ROWS; ++i) {
-                    const int row = w * (4 * GROUP_ROWS) + i * 4 + (lane >> 3);
-                    uint32_t v[8];
-                    to_operand<BF16>(q[i], unit8(e[i]), v);
-                    const uint32_t to = ring_b + b * B_BYTES + (piece >> 2) * 8192 + row * 128;
-                    const int at = (piece & 3) * 2;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const bool up = h != swap;
-                        st_shared16(to + (((at + up) ^ (row & 7)) << 4), up ? v[4] : v[0], up ? v[5] : v[1], up ? v[6] : v[2],
-                                    up ? v[7] : v[3]);
-                    }
-                }
-                async_proxy_fence();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&ready[b]), 0));
             }
         }
     } else if (warp >= 4) {  // results
@@ -363,49 +277,12 @@ __global__ void __launch_bounds__(256) k_column_sums(const T* dy, int64_t sr, in
     }
 }
 
-// Rows of codes or scales onto 16 bytes, for TMA.
-__global__ void __launch_bounds__(256) k_lay_bytes(const uint8_t* in, int64_t sr, int64_t rows, int64_t cols, uint8_t* out, int64_t ld,
-                                                   Span sp)
-{
-    pdl_wait();
-    pdl_signal();
-    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y)
-        for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < cols; c += (int64_t)gridDim.x * 256)
-            out[r * ld + c] = TROP_IN(in + r * sr + c, 1, sp) ? in[r * sr + c] : (uint8_t)0;
-}
-
 #define GRAD_LAUNCH(kernel, grid, block, ...)                                      \
     do {                                                                           \
         const cudaError_t e_ = launch_pdl(kernel, grid, block, 0, s, __VA_ARGS__); \
         if (e_ != cudaSuccess) return cuda_error(e_, #kernel " launch");           \
         count_launches(1);                                                         \
     } while (0)
-
-struct Laid {
-    const uint8_t* p;
-    int64_t cols, sr, rows, ld;
-    size_t at = 0;
-    bool copied = false;
-    Laid(const void* p_, int64_t cols_, int64_t sr_, int64_t rows_, Workspace& ws) : p((const uint8_t*)p_), cols(cols_), sr(sr_), rows(rows_), ld(sr_)
-    {
-        if (rows == 1) ld = (cols + 15) / 16 * 16;  // no second row: any pitch
-        copied = cols > 0 && (ld % 16 || ((uintptr_t)p & 15) || ld < cols || ld >= (int64_t)1 << 39);
-        if (!copied) return;
-        ld = (cols + 15) / 16 * 16;
-        at = ws.add((size_t)rows * ld);
-    }
-    int copy(const Workspace& ws, int sm)
-    {
-        if (!copied) return TROP_OK;
-        const cudaStream_t s = ws.s;
-        uint8_t* to = (uint8_t*)(ws.base + at);
-        const int64_t size[2] = {rows, cols}, stride[2] = {sr, 1};
-        GRAD_LAUNCH(k_lay_bytes, dim3((unsigned)std::min<int64_t>((cols + 255) / 256, 64), (unsigned)std::min<int64_t>(rows, sm * 8)), dim3(256), p,
-                    sr, rows, cols, to, ld, span_of(p, 1, 2, size, stride));
-        p = to;
-        return TROP_OK;
-    }
-};
 
 template <typename T, typename TO>
 int bias_sums(const Operand& o, TO* out, float* part, int parts, cudaStream_t s)
@@ -430,20 +307,21 @@ int bias_parts(const Mat16& dy, int sm)
     return (int)std::max<int64_t>(1, std::min<int64_t>(dy.rows / 64, 2 * sm / across));
 }
 
+// Splits' sums into columns c0 .. c0 + cols of dw.
 template <typename TO>
-int join(const float* acc, int ks, int64_t slab, int64_t lda, const WeightGrad& q, int sm, cudaStream_t s)
+int join(const float* acc, int ks, int64_t slab, int64_t lda, const WeightGrad& q, int64_t c0, int64_t cols, int sm, cudaStream_t s)
 {
-    const int64_t rows = q.dy.cols, cols = q.cols;
-    const int64_t size[2] = {rows, cols}, stride[2] = {q.ldw, 1};
-    const Span sp_out = span_of(q.dw, sizeof(TO), 2, size, stride), sp_acc = span_bytes(acc, (size_t)ks * slab * lda * 4);
-    const bool vec = cols % 4 == 0 && q.ldw % 4 == 0 && (uintptr_t)q.dw % (4 * sizeof(TO)) == 0;
+    const int64_t rows = q.dy.cols, size[2] = {rows, cols}, stride[2] = {q.ldw, 1};
+    TO* const out = (TO*)q.dw + c0;
+    const Span sp_out = span_of(out, sizeof(TO), 2, size, stride), sp_acc = span_bytes(acc, (size_t)ks * slab * lda * 4);
+    const bool vec = cols % 4 == 0 && q.ldw % 4 == 0 && (uintptr_t)out % (4 * sizeof(TO)) == 0;
     const int grid = (int)std::min<int64_t>((rows * cols / (vec ? 4 : 1) + 255) / 256, (int64_t)sm * 8);
     const auto kernel = vec ? k_grad_join<TO, true> : k_grad_join<TO, false>;
-    GRAD_LAUNCH(kernel, dim3(grid), dim3(256), acc, ks, slab * lda, lda, rows, cols, (TO*)q.dw, q.ldw, sp_acc, sp_out);
+    GRAD_LAUNCH(kernel, dim3(grid), dim3(256), acc, ks, slab * lda, lda, rows, cols, out, q.ldw, sp_acc, sp_out);
     return TROP_OK;
 }
 
-int launch(bool bf16, const CUtensorMap& a, const CUtensorMap& k, const CUtensorMap& ks8, const CUtensorMap& c, const Job& j, int sm, cudaStream_t s)
+int launch(bool bf16, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const Job& j, int sm, cudaStream_t s)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)std::min(j.units, sm / 2) * 2);
@@ -458,8 +336,8 @@ int launch(bool bf16, const CUtensorMap& a, const CUtensorMap& k, const CUtensor
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    const cudaError_t e = bf16 ? cudaLaunchKernelEx(&cfg, k_weight_grad<true>, a, k, ks8, c, j)
-                               : cudaLaunchKernelEx(&cfg, k_weight_grad<false>, a, k, ks8, c, j);
+    const cudaError_t e = bf16 ? cudaLaunchKernelEx(&cfg, k_weight_grad<true>, a, b, c, j)
+                               : cudaLaunchKernelEx(&cfg, k_weight_grad<false>, a, b, c, j);
     if (e != cudaSuccess) return cuda_error(e, "k_weight_grad launch");
     count_launches(1);
     return TROP_OK;
@@ -484,25 +362,19 @@ int launch_weight_grad(const WeightGrad& q, cudaStream_t s)
     const int type = q.bf16 ? TROP_BF16 : TROP_F16;
     Workspace ws(s);
     Operand dy(q.dy, ws);
-    // codes and scales as TMA reads them: rows on 16 bytes, else copies
-    Laid codes(q.x.codes, C, q.x.sc, T, ws), scales(q.x.scales, cdiv(C, GROUP8), q.x.ss, T, ws);
-    Job j = {};
-    j.rows = (int)O;
-    j.cols = (int)C;
-    j.mt = cdiv(O, TM);
-    j.nt = cdiv(C, TN);
-    j.kt = cdiv(T, TK);
-    const int ks = C == 0 ? 1 : splits(j.mt * j.nt, j.kt, sm / 2, O * C * 4);
-    j.kper = cdiv(j.kt, ks);
-    j.units = j.mt * j.nt * ks;
-    const int64_t lda = (C + 3) / 4 * 4, pad_rows = (O + 31) / 32 * 32;
+    // a piece of x's columns: whole tiles, 64 MiB of values (at least 1024 columns)
+    const int64_t whole = (C + TN - 1) / TN * TN;
+    const int64_t piece = std::min(whole, std::max<int64_t>((32 << 20) / T / TN * TN, 1024));
+    const int64_t ldx = (std::min(piece, C) + 7) / 8 * 8;
+    const size_t at_x = ws.add((size_t)T * ldx * 2);
+    const int mt = cdiv(O, TM), kt = cdiv(T, TK);
+    const int ks = C == 0 ? 1 : splits(mt * cdiv(std::min(piece, C), TN), kt, sm / 2, O * std::min(piece, C) * 4);
+    const int64_t lda = (std::min(piece, C) + 3) / 4 * 4, pad_rows = (O + 31) / 32 * 32;
     const size_t at_acc = ks > 1 ? ws.add((size_t)ks * pad_rows * lda * 4) : 0;
     const int parts = q.db ? bias_parts(q.dy, sm) : 1;
     const size_t at_part = parts > 1 ? ws.add((size_t)parts * O * 4) : 0;
     if (ws.bytes) TROP_TRY(ws.take());
     TROP_TRY(pack(dy, ws, sm));
-    TROP_TRY(codes.copy(ws, sm));
-    TROP_TRY(scales.copy(ws, sm));
     if (q.db) {
         float* part = parts > 1 ? (float*)(ws.base + at_part) : nullptr;
         if (q.bf16)
@@ -512,32 +384,44 @@ int launch_weight_grad(const WeightGrad& q, cudaStream_t s)
             TROP_TRY(q.wide ? (bias_sums<__half, float>(dy, (float*)q.db, part, parts, s))
                             : (bias_sums<__half, __half>(dy, (__half*)q.db, part, parts, s)));
     }
-    if (C == 0) return TROP_OK;
-    TROP_TRY(device_error_word(&j.error));
-    j.wide = q.wide;
-    CUtensorMap a, k, ks8, c;
-    TROP_TRY(make_map(&a, type, dy.m.p, O, T, dy.m.ld, TK));
-    TROP_TRY(make_map8(&k, codes.p, C, T, codes.ld, TK, 128));
-    TROP_TRY(make_map8(&ks8, scales.p, scales.cols, T, scales.ld, TK, 16));
+    void* const x = ws.base + at_x;
     float* const acc = (float*)(ws.base + at_acc);
-    c = a;
-    if (ks > 1) {
-        j.pad_rows = (int)pad_rows;
-        TROP_TRY(make_map(&c, TROP_F32, acc, C, ks * pad_rows, lda, 32));
-    } else {
-        const int64_t size[2] = {O, C}, stride[2] = {q.ldw, 1};
-        const int64_t on16 = q.wide ? 4 : 8;
-        j.out = q.dw;
-        j.ldo = q.ldw;
-        j.vec = (uintptr_t)q.dw % 16 == 0 && (q.ldw % on16 == 0 && q.ldw >= C && q.ldw < (int64_t)1 << 37);
-        j.sp_out = span_of(q.dw, q.wide ? 4 : 2, 2, size, stride);
-        if (j.vec) TROP_TRY(make_map(&c, q.wide ? (int)TROP_F32 : type, q.dw, C, O, q.ldw, 32));
+    const size_t elem = q.wide ? 4 : 2;
+    for (int64_t c0 = 0; c0 < C; c0 += piece) {
+        const int64_t cols = std::min(piece, C - c0);
+        TROP_TRY(launch_activation_values(T, cols, {q.x.codes + c0, q.x.sc, q.x.scales + c0 / GROUP8, q.x.ss}, {x, ldx, type}, s));
+        Job j = {};
+        TROP_TRY(device_error_word(&j.error));
+        j.rows = (int)O;
+        j.cols = (int)cols;
+        j.mt = mt;
+        j.nt = cdiv(cols, TN);
+        j.kt = kt;
+        j.kper = cdiv(kt, ks);
+        j.units = j.mt * j.nt * ks;
+        j.wide = q.wide;
+        CUtensorMap a, b, c;
+        TROP_TRY(make_map(&a, type, dy.m.p, O, T, dy.m.ld, TK));
+        TROP_TRY(make_map(&b, type, x, cols, T, ldx, TK));
+        c = a;
+        if (ks > 1) {
+            j.pad_rows = (int)pad_rows;
+            TROP_TRY(make_map(&c, TROP_F32, acc, cols, ks * pad_rows, lda, 32));
+        } else {
+            const int64_t size[2] = {O, cols}, stride[2] = {q.ldw, 1};
+            j.out = (char*)q.dw + c0 * elem;
+            j.ldo = q.ldw;
+            j.vec = (uintptr_t)j.out % 16 == 0 && q.ldw * elem % 16 == 0 && q.ldw >= cols && q.ldw < (int64_t)1 << 37;
+            j.sp_out = span_of(j.out, elem, 2, size, stride);
+            if (j.vec) TROP_TRY(make_map(&c, q.wide ? (int)TROP_F32 : type, j.out, cols, O, q.ldw, 32));
+        }
+        TROP_TRY(launch(q.bf16, a, b, c, j, sm, s));
+        if (ks > 1)
+            TROP_TRY(q.wide   ? join<float>(acc, ks, pad_rows, lda, q, c0, cols, sm, s)
+                     : q.bf16 ? join<__nv_bfloat16>(acc, ks, pad_rows, lda, q, c0, cols, sm, s)
+                              : join<__half>(acc, ks, pad_rows, lda, q, c0, cols, sm, s));
     }
-    TROP_TRY(launch(q.bf16, a, k, ks8, c, j, sm, s));
-    if (ks == 1) return TROP_OK;
-    return q.wide   ? join<float>(acc, ks, pad_rows, lda, q, sm, s)
-           : q.bf16 ? join<__nv_bfloat16>(acc, ks, pad_rows, lda, q, sm, s)
-                    : join<__half>(acc, ks, pad_rows, lda, q, sm, s);
+    return TROP_OK;
 }
 
 }  // namespace trop
