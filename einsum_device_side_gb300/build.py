@@ -34,7 +34,8 @@ SOURCES = ["runtime.cpp", "api.cpp", "unary.cu", "gemm.cu", "gemm64.cu", "gemm_i
            "noalloc.cu"]
 # the training operators, and those of a residual block
 TRAIN = ["train.cpp", "layer_norm.cu", "adamw.cu", "linear_ce.cu", "operands.cu",
-         "block.cpp", "activation.cu", "residual_norm.cu", "weight_grad.cu"]
+         "block.cpp", "activation.cu", "residual_norm.cu", "weight_grad.cu",
+         *(f"residual_types_{t}.cu" for t in ("f32", "f32_bf16", "f32_f16", "f32_f32_bf16", "f32_f32_f16", "bf16", "f16"))]
 SOURCES += TRAIN + ["scratch.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fno-strict-aliasing",
@@ -56,7 +57,7 @@ def _stale(obj: str, src: str) -> bool:
             os.path.join(ROOT, "include", "tropical.h")]
     if os.path.basename(src) in TRAIN:
         deps += [os.path.join(CSRC, h) for h in ("train.h", "tcgen05.h", "packed.h", "rows.h", "operands.h", "checks.h",
-                                                  "block.h", "pack8.h")]
+                                                  "block.h", "pack8.h", "residual_job.h", "residual_norm.cuh")]
     return any(os.path.getmtime(d) > os.path.getmtime(obj) for d in deps)
 
 

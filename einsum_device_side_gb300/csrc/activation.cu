@@ -113,30 +113,6 @@ __global__ void __launch_bounds__(256, 4) k_pack8(const Job8 j)
     }
 }
 
-// VEC codes from any byte on: the aligned words around them, where those lie in the matrix (whatever row of it), shifted
-// together; at the matrix's own ends one by one.  Bytes outside the row are whatever they are: nobody stores them.
-template <int VEC>
-__device__ __forceinline__ void codes_any(const int8_t* p, int skip, int left, const int8_t* begin, const int8_t* end, Codes<VEC>& q,
-                                          const Span& sp)
-{
-    (void)sp;
-    constexpr int N = VEC / 4;
-    const uint32_t off = (uint32_t)((uintptr_t)p & 3);
-    const int8_t* const at = p - off;
-    if (at >= begin && at + VEC + 4 <= end) {
-        uint32_t w[N + 1];
-#pragma unroll
-        for (int i = 0; i <= N; ++i) w[i] = TROP_IN(at + 4 * i, 4, sp) ? reinterpret_cast<const uint32_t*>(at)[i] : 0;
-#pragma unroll
-        for (int i = 0; i < N; ++i) q.w[i] = __funnelshift_r(w[i], w[i + 1], off * 8);
-    } else {
-        q.zero();
-#pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            if (i >= skip && i < left && TROP_IN(p + i, 1, sp)) q.w[i / 4] |= (uint32_t)(uint8_t)p[i] << 8 * (i % 4);
-    }
-}
-
 // (Registers are held down to where the loads of several rows from many warps are on their way: ragged rows at 193 registers
 // a thread and with both edges of every row one by one took 232 us for 40950x1001 f16.)
 template <typename T, bool OFF, int U>

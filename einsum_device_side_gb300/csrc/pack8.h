@@ -135,6 +135,29 @@ struct Codes {
         }
     }
 };
+// VEC codes from any byte on: the aligned words around them, where those lie in the matrix (whatever row of it), shifted
+// together; at the matrix's own ends one by one.  Bytes outside the row are whatever they are: nobody stores them.
+template <int VEC>
+__device__ __forceinline__ void codes_any(const int8_t* p, int skip, int left, const int8_t* begin, const int8_t* end, Codes<VEC>& q,
+                                          const Span& sp)
+{
+    (void)sp;
+    constexpr int N = VEC / 4;
+    const uint32_t off = (uint32_t)((uintptr_t)p & 3);
+    const int8_t* const at = p - off;
+    if (at >= begin && at + VEC + 4 <= end) {
+        uint32_t w[N + 1];
+#pragma unroll
+        for (int i = 0; i <= N; ++i) w[i] = TROP_IN(at + 4 * i, 4, sp) ? reinterpret_cast<const uint32_t*>(at)[i] : 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) q.w[i] = __funnelshift_r(w[i], w[i + 1], off * 8);
+    } else {
+        q.zero();
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            if (i >= skip && i < left && TROP_IN(p + i, 1, sp)) q.w[i / 4] |= (uint32_t)(uint8_t)p[i] << 8 * (i % 4);
+    }
+}
 #endif
 
 }  // namespace trop

@@ -1,0 +1,1174 @@
+// residual_norm.cuh -- the norms after and before a block, fused with its gate, its residual scale and the addition to the
+// residual stream; forward and backward.
+//
+//   v = N(u) pw + pb  (or u),   r = alpha x + s a(g) v,   y = N(r) w + b              (per row)
+//   N(t) = (t - mean) rstd  with  rstd = 1 / sqrt(mean_c (t - mean)^2 + eps);  of the rms norm mean = 0.
+// With h = N(r), e = dy w, uh = N(u) (or u), d the whole gradient of r and J the norm's transposed Jacobian,
+//   J(e, h, rstd) = rstd (e - mean_c e - h mean_c(e h))   (no middle term of the rms norm):
+//   d = dr + J(e, h, rstd),  dx = alpha d,  dg = d s v a'(g),  du = J(d s a pw, uh, rstd_u)  (or d s a),
+//   dw = sum_r dy h,  db = sum_r dy,  and with A1 = sum_r d a uh, A2 = sum_r d a:
+//   dpw = s A1,  dpb = s A2,  ds = pw A1 + pb A2  (A1 without a norm of u).
+//
+// x, r and their gradients have one type (S), u, gate and theirs another (U), y and dy a third (Y): f32, bf16 or f16;
+// sums, statistics and the stream inside a row are f32, and each stored value is rounded once.  y is the norm of the
+// unrounded r.  The backward pass reads r, u and gate as they are or as 8-bit copies (pack8.h), which forward leaves in
+// the same pass: of the stored, rounded r, so that they are what a separate call would make of it.
+// Included by one file for each set of types (residual_types_*.cu), which are compiled side by side; residual_norm.cu lays
+// out the jobs and chooses among them.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "residual_job.h"
+#include "pack8.h"
+#include "rows.h"
+#include "tcgen05.h"
+
+namespace trop {
+namespace {
+
+// A row's statistics from two passes over registers: a first mean, then the sums of the deviations from it and of their
+// squares, which correct each other (Chan, Golub and LeVeque, "Algorithms for computing the sample variance", 1983): the
+// first mean's error, some last places, is what the deviations' mean says, so that a constant row's mean is its value and
+// its norm zero, whatever the deviation is divided by.
+__device__ __forceinline__ void finish_stats(float sum, float squares, const ResJob& j, float& mean, float& rstd)
+{
+    const float off = sum * j.inv_cols, var = fmaxf(__fmaf_rn(-off, sum, squares), 0.f) + (squares - squares);  // (NaN stays)
+    mean += off;
+    rstd = __fdiv_rn(1.f, __fsqrt_rn(__fmaf_rn(var, j.inv_cols, j.eps)));
+}
+
+// The gate's value and slope.  The exponential's and the reciprocal's hardware approximations are good to 2^-22, and the
+// values are rounded with the products that follow.
+__device__ __forceinline__ float sigmoid(float g)
+{
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(g * -1.4426950408889634f)));
+    return r;
+}
+__device__ __forceinline__ float gate_value(float g, int act)
+{
+    if (act == 0) return g;
+    const float s = sigmoid(g);
+    return act == 1 ? s : g * s;
+}
+__device__ __forceinline__ void gate_both(float g, int act, float& value, float& slope)
+{
+    value = g, slope = 1.f;
+    if (act == 0) return;
+    const float s = sigmoid(g), t = s * (1.f - s);
+    value = act == 1 ? s : g * s;
+    slope = act == 1 ? t : __fmaf_rn(g, t, s);
+}
+
+// ------------------------------------------------------------------ vectors of a row
+// A thread's vector k of a row.  OFF: rows that do not start on 16 bytes.  A block then takes rows of one offset only
+// (which repeats every `period` rows, and is the same for every tensor), so that its threads' vectors, the 16-byte granules of
+// its rows, hold the same columns in all of them: column c = vector * VEC - off, and a row's first and last vector may lie
+// partly outside it.
+template <int VEC>
+__device__ __forceinline__ int column(int k, int off) { return (int)(k * blockDim.x + threadIdx.x) * VEC - off; }
+// (of the CTAs that share a row, each has a part of its vectors: `off` is then less by the parts before)
+template <int VEC>
+__device__ __forceinline__ bool whole(int c, int cols) { return c >= 0 && c + VEC <= cols; }
+
+struct Walk {  // the rows of a block's group: cls + period * (first + i * step)
+    int off, cls, period;
+    int64_t first, step;
+    __device__ __forceinline__ int64_t row(int64_t n) const { return cls + period * n; }
+};
+template <typename T, int VEC, bool OFF>
+__device__ __forceinline__ Walk walk_of(const void* base, int64_t stride, int period, int block, int blocks)
+{
+    Walk w = {0, 0, 1, 0, 0};
+    if (OFF) {
+        w.period = period;
+        w.cls = block % period;
+        w.off = (int)(((uintptr_t)((const T*)base + w.cls * stride) / sizeof(T)) % VEC);
+    }
+    w.first = (int64_t)(block / w.period) * blockDim.y + threadIdx.y;
+    w.step = (int64_t)(blocks / w.period) * blockDim.y;
+    return w;
+}
+
+// A vector of a row; outside the row zero.
+template <typename T, int VEC, bool OFF>
+__device__ __forceinline__ void fetch(Raw<T, VEC>& q, const RowsAt& a, int64_t row, int c, const ResJob& j)
+{
+    const int cols = (int)j.cols;
+    const T* p = (const T*)a.p + row * a.s + c;
+    q.zero();
+    if (c >= cols) return;
+    if constexpr (!OFF) {
+        if (TROP_IN(p, VEC * sizeof(T), a.sp)) q.read(p);
+    } else {
+        const T *const begin = (const T*)a.p, *const end = begin + (j.rows - 1) * a.s + cols;
+        if (p >= begin && p + VEC <= end) {
+            if (TROP_IN(p, VEC * sizeof(T), a.sp)) q.read(p);
+            if (!whole<VEC>(c, cols)) {
+                constexpr int E = 4 / sizeof(T);  // elements of a word
+#pragma unroll
+                for (int i = 0; i < Raw<T, VEC>::N; ++i) {
+                    uint32_t mask = 0;
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        if (c + i * E + e >= 0 && c + i * E + e < cols) mask |= (E == 1 ? 0xffffffffu : 0xffffu) << 16 * e;
+                    q.w[i] &= mask;
+                }
+            }
+        } else {  // at the matrix's own ends
+            float v[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[i] = c + i >= 0 && c + i < cols && TROP_IN(p + i, sizeof(T), a.sp) ? to_f32(p[i]) : 0.f;
+            q.set(v);
+        }
+    }
+}
+template <typename T, int VEC, bool OFF>
+__device__ __forceinline__ void put(const RowsAt& a, int64_t row, int c, const Raw<T, VEC>& q, int cols)
+{
+    T* p = (T*)a.p + row * a.s + c;
+    if (!OFF || whole<VEC>(c, cols)) {
+        if (c < cols && TROP_IN(p, VEC * sizeof(T), a.sp)) q.write(p);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            if (c + i >= 0 && c + i < cols && TROP_IN(p + i, sizeof(T), a.sp)) p[i] = from_f32<T>(q.get(i));
+    }
+}
+template <typename T, int VEC, bool OFF>
+__device__ __forceinline__ void put(const RowsAt& a, int64_t row, int c, const Pair<VEC> (&o)[pairs<VEC>], int cols)
+{
+    float v[VEC];
+    apart<VEC>(o, v);
+    Raw<T, VEC> q;
+    q.set(v);
+    put<T, VEC, OFF>(a, row, c, q, cols);
+}
+
+// VEC elements of a vector over the columns: f32, or of type T; `none` where it is absent, zero outside the row.  OFF: from
+// the block's shared copy, moved by the offset.
+template <typename T, int VEC, bool OFF>
+struct Vectors {
+    const uint8_t* shared;
+    int span;  // bytes of one
+    __device__ __forceinline__ void get(int which, const VecAt& a, int k, int c, const ResJob& j, float none, Pair<VEC> (&o)[pairs<VEC>]) const
+    {
+        float v[VEC];
+        if (OFF) {
+            const int at = (k * blockDim.x + threadIdx.x) * VEC;
+            if (j.wide_w) {
+                Raw<float, VEC> q;
+                q.read((const float*)(shared + which * span) + at);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) v[i] = q.get(i);
+            } else {
+                Raw<T, VEC> q;
+                q.read((const T*)(shared + which * span) + at);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) v[i] = q.get(i);
+            }
+        } else if (!a.p || c >= (int)j.cols) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[i] = c < (int)j.cols ? none : 0.f;
+        } else if (j.wide_w) {
+            load<float, VEC>((const float*)a.p + c, v, a.sp);
+        } else {
+            load<T, VEC>((const T*)a.p + c, v, a.sp);
+        }
+#pragma unroll
+        for (int i = 0; i < pairs<VEC>; ++i) o[i] = pair_at<VEC>(v, i);
+    }
+    // all of the block; five of NV * blockDim.x vectors each
+    template <int NV>
+    __device__ __forceinline__ void init(uint8_t* dyn, int off, const ResJob& j, const VecAt (&all)[5], const float (&none)[5])
+    {
+        shared = dyn;
+        span = NV * blockDim.x * VEC * (j.wide_w ? 4 : (int)sizeof(T));
+        if (!OFF) return;
+        for (int which = 0; which < 5; ++which)
+            for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < NV * VEC * (int)blockDim.x; i += blockDim.x * blockDim.y) {
+                const int c = i - off;
+                const bool in = c >= 0 && c < (int)j.cols;
+                const VecAt& a = all[which];
+                if (j.wide_w)
+                    ((float*)(dyn + which * span))[i] =
+                        !in ? 0.f : !a.p ? none[which] : TROP_IN((const float*)a.p + c, 4, a.sp) ? ((const float*)a.p)[c] : 0.f;
+                else
+                    ((T*)(dyn + which * span))[i] = !in || (a.p && !TROP_IN((const T*)a.p + c, sizeof(T), a.sp)) ? from_f32<T>(0.f)
+                                                    : a.p                                                     ? ((const T*)a.p)[c]
+                                                                                                              : from_f32<T>(none[which]);
+            }
+        __syncthreads();
+    }
+};
+// (a number's scale may need more digits than T has: it is a factor of its own where there is no vector of it)
+
+// A vector of a row, or of its 8-bit copy, whose rows start where they like: the aligned words around it shifted together, and
+// two groups' units where it lies in two.
+template <typename T, int VEC, bool CODED, bool OFF>
+struct Held {
+    Raw<T, VEC> q;
+    __device__ __forceinline__ void read(const RowsAt& a, const Rows8&, int64_t row, int c, const ResJob& j) { fetch<T, VEC, OFF>(q, a, row, c, j); }
+    __device__ __forceinline__ void again() { q.again(); }
+    __device__ __forceinline__ void get(Pair<VEC> (&o)[pairs<VEC>], int, int) const
+    {
+#pragma unroll
+        for (int i = 0; i < pairs<VEC>; ++i) o[i] = pair_of<T, VEC>(q, i);
+    }
+};
+template <typename T, int VEC, bool OFF>
+struct Held<T, VEC, true, OFF> {
+    Codes<VEC> k;
+    uint32_t e, e2;
+    __device__ __forceinline__ void read(const RowsAt&, const Rows8& a, int64_t row, int c, const ResJob& j)
+    {
+        const int cols = (int)j.cols;
+        const int8_t* p = a.codes + row * a.sc + c;
+        const uint8_t* s = a.scales + row * a.ss;
+        k.zero();
+        e = e2 = LEAST8;
+        if (c >= cols) return;
+        const int g = max(c, 0) / GROUP8;
+        if (TROP_IN(s + g, 1, a.sp_s)) e = s[g];
+        if constexpr (OFF) {
+            const int g2 = min(c + VEC - 1, cols - 1) / GROUP8;
+            if (TROP_IN(s + g2, 1, a.sp_s)) e2 = s[g2];
+            codes_any<VEC>(p, -c, cols - c, a.codes, a.codes + (j.rows - 1) * a.sc + cols, k, a.sp_c);
+            if (!whole<VEC>(c, cols)) {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    if (c + i < 0 || c + i >= cols) k.w[i / 4] &= ~(0xffu << 8 * (i % 4));
+            }
+        } else if (TROP_IN(p, VEC, a.sp_c)) {
+            k.read(p);
+        }
+    }
+    __device__ __forceinline__ void again() {}
+    __device__ __forceinline__ void get(Pair<VEC> (&o)[pairs<VEC>], int c, int) const
+    {
+        float v[VEC];
+        const float unit = unit8(e);
+        if (OFF) {
+            const float other = unit8(e2);
+            const int edge = max(c, 0) / GROUP8 * GROUP8 + GROUP8 - c;  // elements up to the first group's end
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[i] = coded8(k.w[i / 4] ^ 0x80808080u, i % 4) * (i < edge ? unit : other);
+        } else {
+            values8<VEC>(k.w, unit, v);
+        }
+#pragma unroll
+        for (int i = 0; i < pairs<VEC>; ++i) o[i] = pair_at<VEC>(v, i);
+    }
+};
+
+__device__ __forceinline__ float row_gate(const ResJob& j, int64_t row, bool is_f32, bool is_bf16)
+{
+    if (is_f32) {
+        const float* p = (const float*)j.g.p + row * j.g.s;
+        return TROP_IN(p, 4, j.g.sp) ? *p : 0.f;
+    }
+    const uint16_t* p = (const uint16_t*)j.g.p + row * j.g.s;
+    const uint16_t h = TROP_IN(p, 2, j.g.sp) ? *p : (uint16_t)0;
+    return is_bf16 ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
+}
+template <typename U>
+__device__ __forceinline__ float row_gate(const ResJob& j, int64_t row)
+{
+    return row_gate(j, row, sizeof(U) == 4, std::is_same<U, bf16>::value);
+}
+template <typename U>
+__device__ __forceinline__ void put_row_gate(const ResJob& j, int64_t row, float v)
+{
+    U* p = (U*)j.dg.p + row * j.dg.s;
+    if (TROP_IN(p, sizeof(U), j.dg.sp)) *p = from_f32<U>(v);
+}
+__device__ __forceinline__ float stat(const ResJob& j, int which, int64_t row)
+{
+    const float* p = j.stats + which * j.rows + row;
+    return TROP_IN(p, 4, j.sp_stats) ? *p : 0.f;
+}
+__device__ __forceinline__ void put_stat(const ResJob& j, int which, int64_t row, float v)
+{
+    float* p = j.stats + which * j.rows + row;
+    if (j.stats && TROP_IN(p, 4, j.sp_stats)) *p = v;
+}
+
+// The codes of a group's lanes (all of the warp take part; `live`: this one's vector is in the row).
+template <typename T, int VEC>
+__device__ __forceinline__ void keep(const Rows8& a, int64_t row, int64_t c, bool live, const Raw<T, VEC>& q)
+{
+    const uint32_t e = scale8(group_top8<VEC>(live ? top8<T, VEC>(q) : 0u));
+    if (!live) return;
+    Codes<VEC> k;
+    codes8<T, VEC>(q, e, k.w);
+    int8_t* p = a.codes + row * a.sc + c;
+    uint8_t* s = a.scales + row * a.ss + c / GROUP8;
+    if (TROP_IN(p, VEC, a.sp_c)) k.write(p);
+    if (c % GROUP8 == 0 && TROP_IN(s, 1, a.sp_s)) *s = (uint8_t)e;
+}
+
+// Two sums over a row's group (a warp, or the whole block): each half of a warp takes one of them, so that five shuffles
+// serve both; the warps' sums are read four at a time.  Callers alternate between two of `sh`, [2][32] floats that
+// start as zeros, which leaves one barrier a call.
+__device__ __forceinline__ void row_sums(float& a, float& b, float (*sh)[32])
+{
+    const bool up = threadIdx.x & 16;
+    float v = (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (blockDim.x == 32) {
+        const float w = __shfl_xor_sync(0xffffffffu, v, 16);
+        a = up ? w : v;
+        b = up ? v : w;
+        return;
+    }
+    if ((threadIdx.x & 15) == 0) sh[up][threadIdx.x >> 5] = v;
+    __syncthreads();
+    a = b = 0.f;
+    for (int w = 0; w < (int)(blockDim.x >> 5); w += 4) {
+        const float4 p = *reinterpret_cast<const float4*>(&sh[0][w]), q = *reinterpret_cast<const float4*>(&sh[1][w]);
+        a += (p.x + p.y) + (p.z + p.w);
+        b += (q.x + q.y) + (q.z + q.w);
+    }
+}
+// The same where `ctas` CTAs of a cluster share the row, up to eight of 16 warps: every warp hands its sums to all of them, and the
+// one barrier is the cluster's.
+__device__ __forceinline__ void row_sums_wide(float& a, float& b, float (*sh)[128], uint32_t rank, uint32_t ctas)
+{
+    const bool up = threadIdx.x & 16;
+    float v = (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    const uint32_t to = threadIdx.x & 15;  // lanes of either half: a CTA each
+    if (to < ctas)
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa(smem_u32(&sh[up][rank * 16 + (threadIdx.x >> 5)]), to)), "f"(v) : "memory");
+    cluster_sync_all();
+    a = b = 0.f;
+    for (uint32_t w = 0; w < ctas * 16; w += 4) {
+        const float4 p = *reinterpret_cast<const float4*>(&sh[0][w]), q = *reinterpret_cast<const float4*>(&sh[1][w]);
+        a += (p.x + p.y) + (p.z + p.w);
+        b += (q.x + q.y) + (q.z + q.w);
+    }
+}
+__device__ __forceinline__ void zero_sums(float* sh, int n)
+{
+    for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < n; i += blockDim.x * blockDim.y) sh[i] = 0.f;
+    if (blockDim.x > 32) __syncthreads();
+}
+
+// ------------------------------------------------------------------ forward
+// Elements are worked on in packed pairs: with one at a time the instructions (81 an element), not memory, bound
+// 16384x4096 bf16 at 206 us.
+template <int VEC, int NV>
+using Pairs = Pair<VEC>[NV][pairs<VEC>];
+
+// Mean and rstd of a row in a group's registers (zeros outside it).
+template <int VEC, int NV, bool OFF>
+__device__ __forceinline__ void row_stats(const ResJob& j, const Pairs<VEC, NV>& t, int off, float (*sh)[2][32], int& turn, float& mean,
+                                          float& rstd)
+{
+    const int cols = (int)j.cols;
+    float s0 = 0.f, s1 = 0.f;
+    mean = 0.f;
+    if (!j.rms) {
+        Pair<VEC> a = p_of<Pair<VEC>>(0.f);
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int i = 0; i < pairs<VEC>; ++i) a = p_add(a, t[k][i]);
+        s0 = p_sum(a);
+        row_sums(s0, s1, sh[turn]);
+        turn ^= 1;
+        mean = s0 * j.inv_cols;
+    }
+    Pair<VEC> a = p_of<Pair<VEC>>(0.f), b = a;
+    float edge_a = 0.f, edge_b = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int c = column<VEC>(k, off);
+        if (OFF ? whole<VEC>(c, cols) : c < cols) {
+#pragma unroll
+            for (int i = 0; i < pairs<VEC>; ++i) {
+                const Pair<VEC> d = p_add(t[k][i], p_of<Pair<VEC>>(-mean));
+                a = p_add(a, d);
+                b = p_fma(d, d, b);
+            }
+        } else if (OFF && c < cols) {
+            float v[VEC];
+            apart<VEC>(t[k], v);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const float d = c + i >= 0 && c + i < cols ? v[i] - mean : 0.f;
+                edge_a += d;
+                edge_b = __fmaf_rn(d, d, edge_b);
+            }
+        }
+    }
+    s0 = j.rms ? 0.f : p_sum(a) + edge_a;
+    s1 = p_sum(b) + edge_b;
+    row_sums(s0, s1, sh[turn]);
+    turn ^= 1;
+    finish_stats(s0, s1, j, mean, rstd);
+}
+
+// t times the gate of a vector
+template <int VEC>
+__device__ __forceinline__ void gated(Pair<VEC> (&t)[pairs<VEC>], const Pair<VEC> (&g)[pairs<VEC>], int act)
+{
+    if (act == 0) {
+#pragma unroll
+        for (int i = 0; i < pairs<VEC>; ++i) t[i] = p_mul(t[i], g[i]);
+    } else {
+        float v[VEC];
+        apart<VEC>(g, v);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = gate_value(v[i], act);
+#pragma unroll
+        for (int i = 0; i < pairs<VEC>; ++i) t[i] = p_mul(t[i], pair_at<VEC>(v, i));
+    }
+}
+
+template <typename S, typename U, typename Y, int VEC, int NV, int MAXT, bool OFF>
+__global__ void __launch_bounds__(MAXT) k_residual(const ResJob j, int period)
+{
+    pdl_wait();
+    pdl_signal();
+    extern __shared__ __align__(16) uint8_t dyn[];
+    __shared__ __align__(16) float sh[2][2][32];
+    zero_sums(&sh[0][0][0], 128);
+    const int cols = (int)j.cols;
+    const Walk walk = walk_of<U, VEC, OFF>(j.u.p, j.u.s, period, blockIdx.x, gridDim.x);
+    Vectors<Y, VEC, OFF> vec;
+    vec.template init<NV>(dyn, walk.off, j, {j.w, j.b, j.pw, j.pb, j.s}, {1.f, 0.f, 1.f, 0.f, 1.f});
+    const float scale = j.s.p ? 1.f : j.scale;
+    int turn = 0;
+    for (int64_t n = walk.first; walk.row(n) < j.rows; n += walk.step) {
+        const int64_t row = walk.row(n);
+        Raw<U, VEC> qu[NV], qg[NV];
+        Raw<S, VEC> qx[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = column<VEC>(k, walk.off);
+            fetch<U, VEC, OFF>(qu[k], j.u, row, c, j);
+            fetch<S, VEC, OFF>(qx[k], j.x, row, c, j);
+            if (j.gate == GATE_FULL) fetch<U, VEC, OFF>(qg[k], j.g, row, c, j);
+        }
+        const float ga = scale * (j.gate == GATE_ROW ? gate_value(row_gate<U>(j, row), j.act) : 1.f);
+        if (!OFF && j.ku.codes) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int c = column<VEC>(k, 0);
+                keep<U, VEC>(j.ku, row, c, c < cols, qu[k]);
+                if (j.gate == GATE_FULL) keep<U, VEC>(j.kg, row, c, c < cols, qg[k]);
+            }
+        }
+        Pairs<VEC, NV> t;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int i = 0; i < pairs<VEC>; ++i) t[k][i] = pair_of<U, VEC>(qu[k], i);
+        float um = 0.f, ur = 1.f, mean, rstd;
+        if (j.post) row_stats<VEC, NV, OFF>(j, t, walk.off, sh, turn, um, ur);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = column<VEC>(k, walk.off);
+            Pair<VEC> f[pairs<VEC>], o[pairs<VEC>];
+            if (j.post) {
+                vec.get(2, j.pw, k, c, j, 1.f, f);
+                vec.get(3, j.pb, k, c, j, 0.f, o);
+#pragma unroll
+                for (int i = 0; i < pairs<VEC>; ++i)
+                    t[k][i] = p_fma(p_mul(p_add(t[k][i], p_of<Pair<VEC>>(-um)), p_of<Pair<VEC>>(ur)), f[i], o[i]);
+            }
+            if (j.s.p) {
+                vec.get(4, j.s, k, c, j, 1.f, f);
+#pragma unroll
+                for (int i = 0; i < pairs<VEC>; ++i) t[k][i] = p_mul(t[k][i], f[i]);
+            }
+            if (j.gate == GATE_FULL) {
+#pragma unroll
+                for (int i = 0; i < pairs<VEC>; ++i) o[i] = pair_of<U, VEC>(qg[k], i);
+                gated<VEC>(t[k], o, j.act);
+            }
+#pragma unroll
+            for (int i = 0; i < pairs<VEC>; ++i)
+                t[k][i] = p_fma(p_of<Pair<VEC>>(j.alpha), pair_of<S, VEC>(qx[k], i), p_mul(t[k][i], p_of<Pair<VEC>>(ga)));
+            float v[VEC];
+            apart<VEC>(t[k], v);
+            Raw<S, VEC> q;
+            q.set(v);
+            put<S, VEC, OFF>(j.r, row, c, q, cols);
+            if (!OFF && j.kr.codes) keep<S, VEC>(j.kr, row, c, c < cols, q);
+        }
+        row_stats<VEC, NV, OFF>(j, t, walk.off, sh, turn, mean, rstd);
+        if (threadIdx.x == 0) put_stat(j, 0, row, um), put_stat(j, 1, row, ur), put_stat(j, 2, row, mean), put_stat(j, 3, row, rstd);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = column<VEC>(k, walk.off);
+            if (c >= cols) continue;
+            Pair<VEC> f[pairs<VEC>], o[pairs<VEC>];
+            vec.get(0, j.w, k, c, j, 1.f, f);
+            vec.get(1, j.b, k, c, j, 0.f, o);
+#pragma unroll
+            for (int i = 0; i < pairs<VEC>; ++i)
+                f[i] = p_fma(p_mul(p_add(t[k][i], p_of<Pair<VEC>>(-mean)), p_of<Pair<VEC>>(rstd)), f[i], o[i]);
+            put<Y, VEC, OFF>(j.y, row, c, f, cols);
+        }
+    }
+}
+
+// The scalar forms that the long rows' kernels use.
+template <typename T>
+__device__ __forceinline__ float one_of(const VecAt& a, int64_t c, const ResJob& j, float none)
+{
+    if (!a.p) return none;
+    if (j.wide_w) return TROP_IN((const float*)a.p + c, 4, a.sp) ? ((const float*)a.p)[c] : 0.f;
+    return TROP_IN((const T*)a.p + c, sizeof(T), a.sp) ? to_f32(((const T*)a.p)[c]) : 0.f;
+}
+template <typename T>
+__device__ __forceinline__ void put_one(const RowsAt& a, int64_t row, int64_t c, float v)
+{
+    T* p = (T*)a.p + row * a.s + c;
+    if (TROP_IN(p, sizeof(T), a.sp)) *p = from_f32<T>(v);
+}
+
+// Rows longer than a block's registers, or whose tensors do not lie alike: a block per row walks over it once for every sum; r
+// is formed again each time.
+template <typename S, typename U, typename Y>
+__global__ void __launch_bounds__(1024) k_residual_long(const ResJob j)
+{
+    pdl_wait();
+    pdl_signal();
+    __shared__ float sh[2][32][1];
+    const int64_t row = blockIdx.x;
+    const float ga = j.gate == GATE_ROW ? gate_value(row_gate<U>(j, row), j.act) : 1.f;
+    int turn = 0;
+    auto of = [&](const RowsAt& a, int64_t c, auto type) {
+        using T = decltype(type);
+        const T* p = (const T*)a.p + row * a.s + c;
+        return c < j.cols && TROP_IN(p, sizeof(T), a.sp) ? to_f32(*p) : 0.f;
+    };
+    // sum over the row of f(column)
+    auto sum = [&](auto f) {
+        float s[1] = {0.f};
+        for (int64_t c = threadIdx.x; c < j.cols; c += blockDim.x) s[0] += f(c);
+        group_sum_turn<1>(s, sh[turn]);
+        turn ^= 1;
+        return s[0];
+    };
+    auto stats = [&](auto f, float& mean, float& rstd) {
+        mean = j.rms ? 0.f : sum(f) * j.inv_cols;
+        const float m = mean, off = j.rms ? 0.f : sum([&](int64_t c) { return f(c) - m; });
+        finish_stats(off, sum([&](int64_t c) { return (f(c) - m) * (f(c) - m); }), j, mean, rstd);
+    };
+    float um = 0.f, ur = 1.f, mean, rstd;
+    auto u_at = [&](int64_t c) { return of(j.u, c, U()); };
+    if (j.post) stats(u_at, um, ur);
+    auto r_at = [&](int64_t c) {
+        float t = u_at(c);
+        if (j.post) t = __fmaf_rn((t - um) * ur, one_of<Y>(j.pw, c, j, 1.f), one_of<Y>(j.pb, c, j, 0.f));
+        return __fmaf_rn(j.alpha, of(j.x, c, S()), t * one_of<Y>(j.s, c, j, j.scale) * (j.gate == GATE_FULL ? gate_value(of(j.g, c, U()), j.act) : ga));
+    };
+    stats(r_at, mean, rstd);
+    if (threadIdx.x == 0) put_stat(j, 0, row, um), put_stat(j, 1, row, ur), put_stat(j, 2, row, mean), put_stat(j, 3, row, rstd);
+    for (int64_t c0 = 0; c0 < j.cols; c0 += blockDim.x) {
+        const int64_t c = c0 + threadIdx.x;
+        const bool live = c < j.cols;
+        const float t = live ? r_at(c) : 0.f;
+        const float one[1] = {t};
+        Raw<S, 1> q;
+        q.set(one);
+        if (live) {
+            S* r = (S*)j.r.p + row * j.r.s + c;
+            if (TROP_IN(r, sizeof(S), j.r.sp)) q.write(r);
+            put_one<Y>(j.y, row, c, __fmaf_rn((t - mean) * rstd, one_of<Y>(j.w, c, j, 1.f), one_of<Y>(j.b, c, j, 0.f)));
+        }
+        if (j.kr.codes) keep<S, 1>(j.kr, row, c, live, q);
+        if (j.ku.codes) {
+            Raw<U, 1> v;
+            const float uv[1] = {live ? u_at(c) : 0.f};
+            v.set(uv);
+            keep<U, 1>(j.ku, row, c, live, v);
+            if (j.gate == GATE_FULL) {
+                const float gv[1] = {live ? of(j.g, c, U()) : 0.f};
+                v.set(gv);
+                keep<U, 1>(j.kg, row, c, live, v);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ backward
+// d, the whole gradient of r, from dr, e = dy w and h.
+__device__ __forceinline__ float grad_r(float dr, float e, float h, float rstd, float flat, float along)
+{
+    return __fmaf_rn(rstd, e - flat - h * along, dr);
+}
+
+// A block's column sums into its rows of the partial sums; blocks of several warps that each took rows of their own add
+// theirs in warp order, through `across` [warps][cols].
+template <int VEC, int NV>
+__device__ __forceinline__ void put_partials(const ResJob& j, const Pair<VEC> (&acc)[4][NV][pairs<VEC>], float* across, int off, int block)
+{
+    const int cols = (int)j.cols;
+#pragma unroll
+    for (int which = 0; which < 4; ++which) {
+        if (!(j.want >> which & 1)) continue;
+        float* part = j.part + ((int64_t)block * 4 + which) * cols;
+        if (blockDim.y > 1) __syncthreads();
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = column<VEC>(k, off);
+            float v[VEC];
+            apart<VEC>(acc[which][k], v);
+            if (blockDim.y == 1 && VEC % 4 == 0 && cols % VEC == 0 && off % VEC == 0) {
+                if (c < cols) store<float, VEC>(part + c, v, j.sp_part);
+                continue;
+            }
+            float* to = blockDim.y > 1 ? across + threadIdx.y * cols : part;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                if (c + i >= 0 && c + i < cols && (blockDim.y > 1 || TROP_IN(part + c + i, 4, j.sp_part))) to[c + i] = v[i];
+        }
+        if (blockDim.y > 1) {
+            __syncthreads();
+            for (int c = threadIdx.y * 32 + threadIdx.x; c < cols; c += 32 * blockDim.y) {
+                float a = 0.f;
+                for (int r = 0; r < (int)blockDim.y; ++r) a += across[r * cols + c];
+                if (TROP_IN(part + c, 4, j.sp_part)) part[c] = a;
+            }
+        }
+    }
+}
+
+// Rows of more than 4096 columns are shared by the CTAs of a cluster (WIDE): a thread that had more of a row than eight
+// elements would have no room for its columns' four sums.
+template <typename S, typename U, typename Y, int VEC, int NV, bool CODED, bool OFF, bool WIDE>
+__global__ void __launch_bounds__(512) k_residual_back(const ResJob j, int period)
+{
+    pdl_wait();
+    pdl_signal();
+    extern __shared__ __align__(16) uint8_t dyn[];
+    constexpr int SUMS = WIDE ? 128 : 32;
+    __shared__ __align__(16) float sh[3][2][SUMS];
+    zero_sums(&sh[0][0][0], 6 * SUMS);
+    const int cols = (int)j.cols;
+    const uint32_t rank = WIDE ? cluster_ctarank() : 0, ctas = WIDE ? cluster_ctas() : 1;
+    const int block = blockIdx.x / ctas;
+    Walk walk = walk_of<Y, VEC, OFF>(j.dy.p, j.dy.s, period, block, gridDim.x / ctas);
+    if (WIDE) {
+        walk.off -= rank * NV * blockDim.x * VEC;
+        cluster_sync_all();  // the others' sums are zeros
+    }
+    auto sums = [&](float& a, float& b, int which) {
+        if constexpr (WIDE) row_sums_wide(a, b, sh[which], rank, ctas);
+        else row_sums(a, b, sh[which]);
+    };
+    Vectors<Y, VEC, OFF> vec;
+    vec.template init<NV>(dyn, walk.off, j, {j.w, j.b, j.pw, j.pb, j.s}, {1.f, 0.f, 1.f, 0.f, 1.f});
+    const float scale = j.s.p ? 1.f : j.scale;
+    Pair<VEC> acc[4][NV][pairs<VEC>];
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int i = 0; i < pairs<VEC>; ++i) acc[a][k][i] = p_of<Pair<VEC>>(0.f);
+    using P = Pair<VEC>;
+    int turn = 0;
+    for (int64_t n = walk.first; walk.row(n) < j.rows; n += walk.step) {
+        const int64_t row = walk.row(n);
+        Held<Y, VEC, false, OFF> qy[NV];
+        Held<S, VEC, false, OFF> qd[NV];
+        Held<S, VEC, CODED, OFF> qr[NV];
+        Held<U, VEC, CODED, OFF> qu[NV], qg[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = column<VEC>(k, walk.off);
+            qy[k].read(j.dy, j.kr, row, c, j);
+            qr[k].read(j.r, j.kr, row, c, j);
+            if (j.dr.p) qd[k].read(j.dr, j.kr, row, c, j);
+            else qd[k].q.zero();
+            qu[k].read(j.u, j.ku, row, c, j);
+            if (j.gate == GATE_FULL) qg[k].read(j.g, j.kg, row, c, j);
+        }
+        const float um = stat(j, 0, row), ur = stat(j, 1, row), mean = stat(j, 2, row), rstd = stat(j, 3, row);
+        float ga = 1.f, gs = 1.f;
+        if (j.gate == GATE_ROW) gate_both(row_gate<U>(j, row), j.act, ga, gs);
+        P h[NV][pairs<VEC>], e[NV][pairs<VEC>];
+        P sum0 = p_of<P>(0.f), sum1 = sum0;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = column<VEC>(k, walk.off);
+            P w[pairs<VEC>];
+            vec.get(0, j.w, k, c, j, 1.f, w);
+            qy[k].get(e[k], c, cols);
+            qr[k].get(h[k], c, cols);
+#pragma unroll
+            for (int i = 0; i < pairs<VEC>; ++i) {
+                h[k][i] = p_mul(p_add(h[k][i], p_of<P>(-mean)), p_of<P>(rstd));
+                acc[0][k][i] = p_fma(e[k][i], h[k][i], acc[0][k][i]);
+                acc[1][k][i] = p_add(acc[1][k][i], e[k][i]);
+                e[k][i] = p_mul(e[k][i], w[i]);
+                sum0 = p_add(sum0, e[k][i]);
+                sum1 = p_fma(e[k][i], h[k][i], sum1);
+            }
+        }
+        float s0 = p_sum(sum0), s1 = p_sum(sum1);
+        sums(s0, s1, turn);
+        const P flat = p_of<P>(j.rms ? 0.f : -s0 * j.inv_cols), along = p_of<P>(-s1 * j.inv_cols);
+        P sum2 = sum0 = sum1 = p_of<P>(0.f);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = column<VEC>(k, walk.off);
+            P o[pairs<VEC>], d[pairs<VEC>], f[pairs<VEC>], a[pairs<VEC>];
+            qd[k].get(d, c, cols);
+#pragma unroll
+            for (int i = 0; i < pairs<VEC>; ++i) {
+                d[i] = p_fma(p_of<P>(rstd), p_fma(h[k][i], along, p_add(e[k][i], flat)), d[i]);
+                o[i] = p_mul(p_of<P>(j.alpha), d[i]);
+            }
+            if (j.dx.p && c < cols) put<S, VEC, OFF>(j.dx, row, c, o, cols);
+            qu[k].get(h[k], c, cols);  // from here on h is u's
+            if (j.post)
+#pragma unroll
+                for (int i = 0; i < pairs<VEC>; ++i) h[k][i] = p_mul(p_add(h[k][i], p_of<P>(-um)), p_of<P>(ur));
+            // o: d times the scale and, once v and the gate's slope are in, the gate's gradient; a: the gate
+            vec.get(4, j.s, k, c, j, 1.f, f);
+#pragma unroll
+            for (int i = 0; i < pairs<VEC>; ++i) o[i] = p_mul(p_mul(d[i], f[i]), p_of<P>(scale));
+            if (j.gate == GATE_FULL) {
+                qg[k].get(a, c, cols);
+                if (j.act != 0) {
+                    float g[VEC], slope[VEC];
+                    apart<VEC>(a, g);
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) gate_both(g[i], j.act, g[i], slope[i]);
+#pragma unroll
+                    for (int i = 0; i < pairs<VEC>; ++i) a[i] = pair_at<VEC>(g, i), f[i] = pair_at<VEC>(slope, i);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < pairs<VEC>; ++i) a[i] = p_of<P>(ga);
+            }
+            P slope[pairs<VEC>];
+#pragma unroll
+            for (int i = 0; i < pairs<VEC>; ++i) {
+                slope[i] = f[i];
+                const P da = p_mul(d[i], a[i]);
+                acc[2][k][i] = p_fma(da, h[k][i], acc[2][k][i]);
+                acc[3][k][i] = p_add(acc[3][k][i], da);
+                e[k][i] = p_mul(o[i], a[i]);
+                d[i] = h[k][i];  // v
+            }
+            if (j.post) {
+                P pb[pairs<VEC>];
+                vec.get(2, j.pw, k, c, j, 1.f, f);
+                vec.get(3, j.pb, k, c, j, 0.f, pb);
+#pragma unroll
+                for (int i = 0; i < pairs<VEC>; ++i) {
+                    d[i] = p_fma(h[k][i], f[i], pb[i]);
+                    e[k][i] = p_mul(e[k][i], f[i]);
+                    sum0 = p_add(sum0, e[k][i]);
+                    sum1 = p_fma(e[k][i], h[k][i], sum1);
+                }
+            }
+            if (j.gate == GATE_FULL && j.dg.p) {
+#pragma unroll
+                for (int i = 0; i < pairs<VEC>; ++i) {
+                    o[i] = p_mul(o[i], d[i]);
+                    if (j.act != 0) o[i] = p_mul(o[i], slope[i]);
+                }
+                if (c < cols) put<U, VEC, OFF>(j.dg, row, c, o, cols);
+            } else if (j.gate == GATE_ROW) {
+#pragma unroll
+                for (int i = 0; i < pairs<VEC>; ++i) sum2 = p_fma(o[i], d[i], sum2);
+            }
+        }
+        s0 = p_sum(sum0), s1 = p_sum(sum1);
+        if (j.post) sums(s0, s1, turn ^ 1);
+        else turn ^= 1;  // (the next row's first sums take the other of the two)
+        if (j.gate == GATE_ROW) {
+            float s2 = p_sum(sum2), none = 0.f;
+            sums(s2, none, 2);
+            if (j.dg.p && threadIdx.x == 0 && rank == 0) put_row_gate<U>(j, row, s2 * gs);
+        }
+        if (j.du.p) {
+            const P flat2 = p_of<P>(j.rms ? 0.f : -s0 * j.inv_cols), along2 = p_of<P>(-s1 * j.inv_cols);
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int c = column<VEC>(k, walk.off);
+                if (j.post)
+#pragma unroll
+                    for (int i = 0; i < pairs<VEC>; ++i)
+                        e[k][i] = p_mul(p_of<P>(ur), p_fma(h[k][i], along2, p_add(e[k][i], flat2)));
+                if (c < cols) put<U, VEC, OFF>(j.du, row, c, e[k], cols);
+            }
+        }
+    }
+    if (j.want) put_partials<VEC, NV>(j, acc, reinterpret_cast<float*>(dyn), walk.off, block);
+    if (WIDE) cluster_sync_all();  // no CTA leaves before the others have written its sums
+}
+
+// Rows longer than that: a block per row, three walks; the row's two sums of the norm of r are left for the columns.
+template <typename S, typename U, typename Y, bool CODED>
+struct LongRow {
+    const ResJob& j;
+    int64_t row;
+    float um, ur, mean, rstd, ga, gs;
+    __device__ LongRow(const ResJob& j_, int64_t row_) : j(j_), row(row_), ga(1.f), gs(1.f)
+    {
+        um = stat(j, 0, row), ur = stat(j, 1, row), mean = stat(j, 2, row), rstd = stat(j, 3, row);
+        if (j.gate == GATE_ROW) gate_both(row_gate<U>(j, row), j.act, ga, gs);
+    }
+    template <typename T, bool C>
+    __device__ float of(const RowsAt& a, const Rows8& k, int64_t c) const
+    {
+        Held<T, 1, C, false> q;
+        float v[1];
+        q.read(a, k, row, (int)c, j);
+        q.get(v, (int)c, (int)j.cols);
+        return v[0];
+    }
+    __device__ float vec(const VecAt& a, int64_t c, float none) const { return one_of<Y>(a, c, j, none); }
+    __device__ void first(int64_t c, float& dy, float& h) const
+    {
+        dy = of<Y, false>(j.dy, j.kr, c);
+        h = (of<S, CODED>(j.r, j.kr, c) - mean) * rstd;
+    }
+    // d; and da, uh and what the gate's gradient is (dg), dv pw
+    __device__ float second(int64_t c, float flat, float along, float& da, float& uh, float& dg, float& q) const
+    {
+        float dy, h, a = ga, slope = 1.f;
+        first(c, dy, h);
+        const float dr = j.dr.p ? of<S, false>(j.dr, j.kr, c) : 0.f;
+        const float d = grad_r(dr, dy * vec(j.w, c, 1.f), h, rstd, flat, along);
+        const float u = of<U, CODED>(j.u, j.ku, c), pw = vec(j.pw, c, 1.f);
+        uh = j.post ? (u - um) * ur : u;
+        if (j.gate == GATE_FULL) gate_both(of<U, CODED>(j.g, j.kg, c), j.act, a, slope);
+        const float ds = d * vec(j.s, c, j.scale);
+        da = d * a;
+        dg = ds * (j.post ? __fmaf_rn(uh, pw, vec(j.pb, c, 0.f)) : u) * slope;
+        q = j.post ? ds * a * pw : ds * a;
+        return d;
+    }
+};
+template <typename S, typename U, typename Y, bool CODED>
+__global__ void __launch_bounds__(1024) k_residual_back_long(const ResJob j)
+{
+    pdl_wait();
+    pdl_signal();
+    __shared__ float sh[2][32][3];
+    const LongRow<S, U, Y, CODED> at(j, blockIdx.x);
+    float s[3] = {0.f, 0.f, 0.f}, dy, h, da, uh, dg, q;
+    for (int64_t c = threadIdx.x; c < j.cols; c += blockDim.x) {
+        at.first(c, dy, h);
+        const float e = dy * at.vec(j.w, c, 1.f);
+        s[0] += e;
+        s[1] = __fmaf_rn(e, h, s[1]);
+    }
+    group_sum_turn<3>(s, sh[0]);
+    const float flat = j.rms ? 0.f : s[0] * j.inv_cols, along = s[1] * j.inv_cols;
+    if (j.sums && threadIdx.x == 0 && TROP_IN(j.sums + 2 * at.row, 8, j.sp_sums)) j.sums[2 * at.row] = flat, j.sums[2 * at.row + 1] = along;
+    s[0] = s[1] = s[2] = 0.f;
+    for (int64_t c = threadIdx.x; c < j.cols; c += blockDim.x) {
+        at.second(c, flat, along, da, uh, dg, q);
+        s[0] += q;
+        s[1] = __fmaf_rn(q, uh, s[1]);
+        s[2] += dg;
+    }
+    group_sum_turn<3>(s, sh[1]);
+    const float flat2 = j.rms ? 0.f : s[0] * j.inv_cols, along2 = s[1] * j.inv_cols;
+    for (int64_t c = threadIdx.x; c < j.cols; c += blockDim.x) {
+        const float d = at.second(c, flat, along, da, uh, dg, q);
+        if (j.dx.p) put_one<S>(j.dx, at.row, c, j.alpha * d);
+        if (j.dg.p && j.gate == GATE_FULL) put_one<U>(j.dg, at.row, c, dg);
+        if (j.du.p) put_one<U>(j.du, at.row, c, j.post ? at.ur * (q - flat2 - uh * along2) : q);
+    }
+    if (j.dg.p && j.gate == GATE_ROW && threadIdx.x == 0) put_row_gate<U>(j, at.row, s[2] * at.gs);
+}
+// The columns' sums over rows blockIdx.y, + gridDim.y, ...: a thread per column.
+template <typename S, typename U, typename Y, bool CODED>
+__global__ void __launch_bounds__(256) k_residual_columns(const ResJob j)
+{
+    pdl_wait();
+    pdl_signal();
+    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (c >= j.cols) return;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f}, dy, h, da, uh, dg, q;
+    for (int64_t row = blockIdx.y; row < j.rows; row += gridDim.y) {
+        const LongRow<S, U, Y, CODED> at(j, row);
+        at.first(c, dy, h);
+        acc[0] = __fmaf_rn(dy, h, acc[0]);
+        acc[1] += dy;
+        if (!(j.want & (SUM_1 | SUM_2))) continue;
+        const bool in = TROP_IN(j.sums + 2 * row, 8, j.sp_sums);
+        at.second(c, in ? j.sums[2 * row] : 0.f, in ? j.sums[2 * row + 1] : 0.f, da, uh, dg, q);
+        acc[2] = __fmaf_rn(da, uh, acc[2]);
+        acc[3] += da;
+    }
+#pragma unroll
+    for (int which = 0; which < 4; ++which) {
+        float* part = j.part + ((int64_t)blockIdx.y * 4 + which) * j.cols + c;
+        if ((j.want >> which & 1) && TROP_IN(part, 4, j.sp_part)) *part = acc[which];
+    }
+}
+
+// The blocks' column sums, in block order: 32 columns per block of threads, 32 warps taking every 32nd block's sums.
+// blockIdx.y: dw, db, or what comes of A1 and A2.
+__device__ __forceinline__ float column_sum(const JoinJob& j, int which, float (*sh)[33])
+{
+    const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
+    float a = 0.f;
+    if (c < j.cols) {
+        float v[4];
+        int b = threadIdx.y;
+        for (; b + 96 < j.blocks; b += 128) {  // four loads on their way
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float* p = j.part + ((int64_t)(b + 32 * k) * 4 + which) * j.cols + c;
+                v[k] = TROP_IN(p, 4, j.sp_part) ? *p : 0.f;
+            }
+            a += (v[0] + v[1]) + (v[2] + v[3]);
+        }
+        for (; b < j.blocks; b += 32) {
+            const float* p = j.part + ((int64_t)b * 4 + which) * j.cols + c;
+            if (TROP_IN(p, 4, j.sp_part)) a += *p;
+        }
+    }
+    __syncthreads();
+    sh[threadIdx.y][threadIdx.x] = a;
+    __syncthreads();
+    a = sh[threadIdx.x][threadIdx.y];  // warp y sums column y's 32 values
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    return a;
+}
+template <typename Y>
+__global__ void __launch_bounds__(1024) k_residual_join(const JoinJob j)
+{
+    pdl_wait();
+    pdl_signal();
+    __shared__ float sh[32][33];
+    const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.y;
+    const bool mine = threadIdx.x == 0 && c < j.cols;
+    auto at = [&](const VecAt& a, float none) {
+        if (!a.p) return none;
+        if (j.wide_w) return TROP_IN((const float*)a.p + c, 4, a.sp) ? ((const float*)a.p)[c] : 0.f;
+        return TROP_IN((const Y*)a.p + c, sizeof(Y), a.sp) ? to_f32(((const Y*)a.p)[c]) : 0.f;
+    };
+    auto put = [&](void* to, float v, const Span& sp) {
+        (void)sp;
+        if (!to) return;
+        if (j.wide_w) {
+            if (TROP_IN((float*)to + c, 4, sp)) ((float*)to)[c] = v;
+        } else if (TROP_IN((Y*)to + c, sizeof(Y), sp)) {
+            ((Y*)to)[c] = from_f32<Y>(v);
+        }
+    };
+    if (blockIdx.y < 2) {
+        void* to = blockIdx.y ? j.db : j.dw;
+        if (!to) return;
+        const float a = column_sum(j, blockIdx.y, sh);
+        if (mine) put(to, a, blockIdx.y ? j.sp_db : j.sp_dw);
+        return;
+    }
+    const bool first = j.dpw || j.ds, second = j.dpb || (j.ds && j.post && j.pb.p);
+    const float a1 = first ? column_sum(j, 2, sh) : 0.f, a2 = second ? column_sum(j, 3, sh) : 0.f;
+    if (!mine) return;
+    const float s = at(j.s, j.scale);
+    put(j.dpw, s * a1, j.sp_dpw);
+    put(j.dpb, s * a2, j.sp_dpb);
+    if (j.ds) put(j.ds, j.post ? __fmaf_rn(at(j.pw, 1.f), a1, second ? at(j.pb, 0.f) * a2 : 0.f) : a1, j.sp_ds);
+}
+
+// ------------------------------------------------------------------ host
+// A row's group: threads and vectors per thread.  Many rows: as many elements per thread as there may be, down to a warp a
+// row; few rows: spread over more threads.
+bool shape_of(int64_t units, int vec, int most_elems, int most_threads, int64_t rows, int sm, int warps, int* nv, dim3* block)
+{
+    *nv = 0;
+    for (int n = std::max(1, most_elems / vec); n >= 1; n /= 2) {
+        const int64_t g = ((units + n - 1) / n + 31) / 32 * 32;
+        if (g > most_threads) break;
+        *nv = n;
+        *block = g == 32 ? dim3(32, (unsigned)warps) : dim3((unsigned)g, 1);
+        if (rows * (g / 32) >= (int64_t)sm * 8) return true;
+    }
+    return *nv > 0;
+}
+
+template <typename S, typename U, typename Y>
+struct Types {
+    static constexpr int VEC = sizeof(U) == 2 ? 8 : 4;  // elements of the narrower rows' 16 bytes
+};
+// The rows' places in granules of VEC elements: after how many rows they repeat, the same for all the matrices (1: every row
+// starts on one); 0 where they differ, or too many rows share none.
+struct Places {
+    int vec;
+    int64_t rows;
+    int64_t base = -1, stride = 0;
+    bool same = true;
+    void add(const RowsAt& a, size_t elem)
+    {
+        if (!a.p) return;
+        const int64_t b = (uintptr_t)a.p / elem % vec, s = rows > 1 ? a.s % vec : 0;
+        if (base < 0) base = b, stride = s;
+        else if (b != base || s != stride) same = false;
+    }
+    int period() const
+    {
+        if (!same) return 0;
+        int p = 1;
+        while (p * stride % vec) p *= 2;
+        return p;
+    }
+    bool on() const { return same && base <= 0 && stride == 0; }
+};
+bool on8(const Rows8& k, int vec, int64_t rows) { return aligned(k.codes, k.sc, 1, vec, rows); }
+
+int launch_pack(const RowsAt& a, int dtype, const Rows8& k, int64_t rows, int64_t cols, cudaStream_t s)
+{
+    return launch_activation_pack(rows, cols, {a.p, a.s, dtype}, {k.codes, k.sc, k.scales, k.ss}, s);
+}
+template <typename T>
+constexpr int dtype_of() { return sizeof(T) == 4 ? (int)TROP_F32 : std::is_same<T, bf16>::value ? (int)TROP_BF16 : (int)TROP_F16; }
+
+dim3 long_block(int64_t cols) { return dim3((unsigned)std::min<int64_t>(1024, (cols + 31) / 32 * 32)); }
+
+}  // namespace
+
+template <typename S, typename U, typename Y>
+int residual_forward(const ResJob& j, int sm, cudaStream_t s)
+{
+    constexpr int V = Types<S, U, Y>::VEC;
+    const size_t we = j.wide_w ? 4 : sizeof(Y);
+    Places at = {V, j.rows};
+    at.add(j.x, sizeof(S)), at.add(j.r, sizeof(S)), at.add(j.u, sizeof(U)), at.add(j.y, sizeof(Y));
+    if (j.gate == GATE_FULL) at.add(j.g, sizeof(U));
+    bool vec = j.cols % V == 0 && at.on() && on8(j.ku, V, j.rows) && on8(j.kg, V, j.rows) && on8(j.kr, V, j.rows);
+    for (const VecAt* a : {&j.w, &j.b, &j.pw, &j.pb, &j.s}) vec = vec && aligned(a->p, 0, we, V, 1);
+    const int period = at.period();
+    int nv = 0;
+    dim3 block;
+    if (!vec && period > 0 && j.cols >= 2 * V &&
+        shape_of((j.cols + V - 1) / V + 1, V, 16, 1024, j.rows, sm, 8, &nv, &block) && (size_t)5 * nv * block.x * V * we <= 196608) {
+        // off the granules: whole vectors all the same; the copies, whose groups lie across these, by a pass of their own
+        ResJob k = j;
+        k.ku.codes = k.kg.codes = k.kr.codes = nullptr;
+        const size_t smem = (size_t)5 * nv * block.x * V * we;
+        const auto kernel = nv == 1          ? k_residual<S, U, Y, V, 1, 1024, true>
+                            : nv * V < 16    ? k_residual<S, U, Y, V, 2, 1024, true>
+                            : block.x <= 512 ? k_residual<S, U, Y, V, 16 / V, 512, true>
+                                             : k_residual<S, U, Y, V, 16 / V, 1024, true>;
+        TROP_TRY(allow_dynamic((const void*)kernel));
+        int per_sm = 0;  // as many blocks as run at once: none waits for a place
+        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, (int)(block.x * block.y), smem);
+        if (e != cudaSuccess) return cuda_error(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor(k_residual)");
+        int64_t blocks = std::min<int64_t>((j.rows + block.y - 1) / block.y, (int64_t)sm * std::max(1, per_sm));
+        blocks = std::max<int64_t>(1, blocks / period) * period;
+        TROP_LAUNCH(kernel, dim3((unsigned)blocks), block, smem, k, period);
+        if (j.ku.codes) TROP_TRY(launch_pack(j.u, dtype_of<U>(), j.ku, j.rows, j.cols, s));
+        if (j.kg.codes) TROP_TRY(launch_pack(j.g, dtype_of<U>(), j.kg, j.rows, j.cols, s));
+        if (j.kr.codes) TROP_TRY(launch_pack(j.r, dtype_of<S>(), j.kr, j.rows, j.cols, s));
+        return TROP_OK;
+    }
+    if (!vec || !shape_of(j.cols / V, V, 16, 1024, j.rows, sm, 8, &nv, &block)) {
+        TROP_LAUNCH((k_residual_long<S, U, Y>), dim3((unsigned)j.rows), long_block(j.cols), 0, j);
+        return TROP_OK;
+    }
+    const dim3 grid((unsigned)((j.rows + block.y - 1) / block.y));
+    const auto kernel = nv == 1          ? k_residual<S, U, Y, V, 1, 1024, false>
+                        : nv * V < 16    ? k_residual<S, U, Y, V, 2, 1024, false>
+                        : block.x <= 512 ? k_residual<S, U, Y, V, 16 / V, 512, false>
+                                         : k_residual<S, U, Y, V, 16 / V, 1024, false>;
+    TROP_LAUNCH(kernel, grid, block, 0, j, 1);
+    return TROP_OK;
+}
+
+template <typename S, typename U, typename Y, bool CODED>
+int residual_backward(ResJob j, JoinJob t, int sm, cudaStream_t s)
+{
+    constexpr int V = Types<S, U, Y>::VEC;
+    const size_t we = j.wide_w ? 4 : sizeof(Y);
+    Places at = {V, j.rows};
+    at.add(j.dy, sizeof(Y)), at.add(j.dr, sizeof(S)), at.add(j.dx, sizeof(S)), at.add(j.du, sizeof(U));
+    if (j.gate == GATE_FULL) at.add(j.dg, sizeof(U));
+    if (!CODED) {
+        at.add(j.r, sizeof(S)), at.add(j.u, sizeof(U));
+        if (j.gate == GATE_FULL) at.add(j.g, sizeof(U));
+    }
+    bool vec = j.cols % V == 0 && at.on() && (!CODED || (on8(j.ku, V, j.rows) && on8(j.kg, V, j.rows) && on8(j.kr, V, j.rows)));
+    for (const VecAt* a : {&j.w, &j.pw, &j.pb, &j.s}) vec = vec && aligned(a->p, 0, we, V, 1);
+    const int period = at.period();
+    // eight elements a thread, up to 512 threads; more columns: up to eight CTAs of them
+    const bool off = !vec && period > 0 && j.cols >= 2 * V;
+    const int64_t units = off ? (j.cols + V - 1) / V + 1 : j.cols / V;
+    const int64_t ctas = (units * V + 4095) / 4096;
+    int nv = 0;
+    dim3 block;
+    bool fits = (vec || off) && ctas <= 8;
+    if (fits && ctas == 1) shape_of(units, V, 8, 512, j.rows, sm, 4, &nv, &block);
+    else if (fits) nv = 8 / V, block = dim3((unsigned)(((units + ctas * nv - 1) / (ctas * nv) + 31) / 32 * 32), 1);
+    const size_t vectors = off ? (size_t)5 * nv * block.x * V * we : 0, across = block.y > 1 && j.want ? block.y * (size_t)j.cols * 4 : 0;
+    const size_t smem = std::max(vectors, across);  // (5 x 4096 f32 at most)
+    int64_t blocks = fits ? std::min<int64_t>((j.rows + block.y - 1) / block.y,
+                                              std::max<int64_t>(1, (int64_t)sm / ctas) * std::max<int>(1, 512 / (int)(block.x * block.y)))
+                          : std::min<int64_t>(j.rows, std::max<int64_t>(1, (int64_t)sm * 8 * 256 / j.cols));
+    if (fits && off) blocks = std::max<int64_t>(1, blocks / period) * period;
+    if (j.rows == 0) blocks = 0;  // sums over no rows
+    const size_t part = j.want && j.rows ? (size_t)blocks * 4 * j.cols * 4 : 0, sums = !fits && (j.want & (SUM_1 | SUM_2)) ? (size_t)j.rows * 8 : 0;
+    Workspace ws(s);
+    const size_t at_part = ws.add(part), at_sums = ws.add(sums);
+    if (ws.bytes) {
+        TROP_TRY(ws.take());
+        j.part = part ? (float*)(ws.base + at_part) : nullptr;
+        j.sums = sums ? (float*)(ws.base + at_sums) : nullptr;
+        j.sp_part = span_bytes(j.part, part);
+        j.sp_sums = span_bytes(j.sums, sums);
+    }
+    if (j.rows == 0) {
+    } else if (!fits) {
+        if (j.dx.p || j.du.p || j.dg.p || j.sums)
+            TROP_LAUNCH((k_residual_back_long<S, U, Y, CODED>), dim3((unsigned)j.rows), long_block(j.cols), 0, j);
+        if (j.want)
+            TROP_LAUNCH((k_residual_columns<S, U, Y, CODED>), dim3((unsigned)((j.cols + 255) / 256), (unsigned)blocks), dim3(256), 0, j);
+    } else if (ctas == 1) {
+        const auto kernel = off ? (nv == 1 ? k_residual_back<S, U, Y, V, 1, CODED, true, false> : k_residual_back<S, U, Y, V, 8 / V, CODED, true, false>)
+                                : (nv == 1 ? k_residual_back<S, U, Y, V, 1, CODED, false, false> : k_residual_back<S, U, Y, V, 8 / V, CODED, false, false>);
+        if (smem > PLAIN_SMEM) TROP_TRY(allow_dynamic((const void*)kernel));
+        TROP_LAUNCH(kernel, dim3((unsigned)blocks), block, smem, j, period);
+    } else {
+        const auto kernel = off ? k_residual_back<S, U, Y, V, 8 / V, CODED, true, true> : k_residual_back<S, U, Y, V, 8 / V, CODED, false, true>;
+        if (smem > PLAIN_SMEM) TROP_TRY(allow_dynamic((const void*)kernel));
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(blocks * ctas));
+        cfg.blockDim = block;
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = (unsigned)ctas;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, j, period);
+        if (e != cudaSuccess) return cuda_error(e, "k_residual_back launch");
+        count_launches(1);
+    }
+    if (j.want) {
+        t.part = j.part;
+        t.blocks = (int)blocks;
+        t.sp_part = j.sp_part;
+        TROP_LAUNCH((k_residual_join<Y>), dim3((unsigned)((j.cols + 31) / 32), 3), dim3(32, 32), 0, t);
+    }
+    return TROP_OK;
+}
+
+}  // namespace trop
