@@ -19,11 +19,13 @@ struct Rows8 {  // 8-bit copies, null: absent
     uint8_t* scales;
     int64_t ss;
     Span sp_c, sp_s;
+    uint32_t sb = 0, ssb = 0;  // the strides, where 32 bits hold them
 };
 struct RowsAt {
     void* p;
     int64_t s;
     Span sp;
+    uint32_t sb = 0;  // the stride in bytes, where 32 bits hold it
 };
 struct VecAt {
     const void* p;
@@ -55,7 +57,7 @@ struct JoinJob {
 
 // by the types of x and r, of u and gate, of y
 template <typename S, typename U, typename Y>
-int residual_forward(const ResJob& j, int sm, cudaStream_t s);
+int residual_forward(ResJob j, int sm, cudaStream_t s);
 template <typename S, typename U, typename Y, bool CODED>
 int residual_backward(ResJob j, JoinJob t, int sm, cudaStream_t s);
 

@@ -75,62 +75,39 @@ __device__ __forceinline__ int column(int k, int off) { return (int)(k * blockDi
 template <int VEC>
 __device__ __forceinline__ bool whole(int c, int cols) { return c >= 0 && c + VEC <= cols; }
 
-struct Walk {  // the rows of a block's group: cls + period * (first + i * step)
-    int off, cls, period;
-    int64_t first, step;
-    __device__ __forceinline__ int64_t row(int64_t n) const { return cls + period * n; }
+struct Walk {  // a group's rows: first, + step, ...  (rows are below 2^31, and no step passes 2^31)
+    int off;
+    uint32_t first, step;
 };
 template <typename T, int VEC, bool OFF>
 __device__ __forceinline__ Walk walk_of(const void* base, int64_t stride, int period, int block, int blocks)
 {
-    Walk w = {0, 0, 1, 0, 0};
+    Walk w = {0, 0, 0};
+    int cls = 0;
     if (OFF) {
-        w.period = period;
-        w.cls = block % period;
-        w.off = (int)(((uintptr_t)((const T*)base + w.cls * stride) / sizeof(T)) % VEC);
+        cls = block % period;
+        w.off = (int)(((uintptr_t)((const T*)base + cls * stride) / sizeof(T)) % VEC);
+    } else {
+        period = 1;
     }
-    w.first = (int64_t)(block / w.period) * blockDim.y + threadIdx.y;
-    w.step = (int64_t)(blocks / w.period) * blockDim.y;
+    w.first = cls + period * ((uint32_t)(block / period) * blockDim.y + threadIdx.y);
+    w.step = period * ((uint32_t)(blocks / period) * blockDim.y);
     return w;
 }
-
-// A vector of a row; outside the row zero.
-template <typename T, int VEC, bool OFF>
-__device__ __forceinline__ void fetch(Raw<T, VEC>& q, const RowsAt& a, int64_t row, int c, const ResJob& j)
+// A row's element c.  Rows lie less than 2^32 bytes apart here, which makes their address one wide multiplication: with
+// 64-bit strides the addresses were a third of the backward pass's instructions.
+template <typename T>
+__device__ __forceinline__ T* elem(const RowsAt& a, uint32_t row, int c)
 {
-    const int cols = (int)j.cols;
-    const T* p = (const T*)a.p + row * a.s + c;
-    q.zero();
-    if (c >= cols) return;
-    if constexpr (!OFF) {
-        if (TROP_IN(p, VEC * sizeof(T), a.sp)) q.read(p);
-    } else {
-        const T *const begin = (const T*)a.p, *const end = begin + (j.rows - 1) * a.s + cols;
-        if (p >= begin && p + VEC <= end) {
-            if (TROP_IN(p, VEC * sizeof(T), a.sp)) q.read(p);
-            if (!whole<VEC>(c, cols)) {
-                constexpr int E = 4 / sizeof(T);  // elements of a word
-#pragma unroll
-                for (int i = 0; i < Raw<T, VEC>::N; ++i) {
-                    uint32_t mask = 0;
-#pragma unroll
-                    for (int e = 0; e < E; ++e)
-                        if (c + i * E + e >= 0 && c + i * E + e < cols) mask |= (E == 1 ? 0xffffffffu : 0xffffu) << 16 * e;
-                    q.w[i] &= mask;
-                }
-            }
-        } else {  // at the matrix's own ends
-            float v[VEC];
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) v[i] = c + i >= 0 && c + i < cols && TROP_IN(p + i, sizeof(T), a.sp) ? to_f32(p[i]) : 0.f;
-            q.set(v);
-        }
-    }
+    return reinterpret_cast<T*>((char*)a.p + (uint64_t)row * a.sb) + c;
 }
+__device__ __forceinline__ int8_t* codes_at(const Rows8& a, uint32_t row, int c) { return a.codes + (uint64_t)row * a.sb + c; }
+__device__ __forceinline__ uint8_t* scales_at(const Rows8& a, uint32_t row, int group) { return a.scales + (uint64_t)row * a.ssb + group; }
+
 template <typename T, int VEC, bool OFF>
-__device__ __forceinline__ void put(const RowsAt& a, int64_t row, int c, const Raw<T, VEC>& q, int cols)
+__device__ __forceinline__ void put(const RowsAt& a, uint32_t row, int c, const Raw<T, VEC>& q, int cols)
 {
-    T* p = (T*)a.p + row * a.s + c;
+    T* p = elem<T>(a, row, c);
     if (!OFF || whole<VEC>(c, cols)) {
         if (c < cols && TROP_IN(p, VEC * sizeof(T), a.sp)) q.write(p);
     } else {
@@ -140,7 +117,7 @@ __device__ __forceinline__ void put(const RowsAt& a, int64_t row, int c, const R
     }
 }
 template <typename T, int VEC, bool OFF>
-__device__ __forceinline__ void put(const RowsAt& a, int64_t row, int c, const Pair<VEC> (&o)[pairs<VEC>], int cols)
+__device__ __forceinline__ void put(const RowsAt& a, uint32_t row, int c, const Pair<VEC> (&o)[pairs<VEC>], int cols)
 {
     float v[VEC];
     apart<VEC>(o, v);
@@ -188,84 +165,259 @@ struct Vectors {
     {
         shared = dyn;
         span = NV * blockDim.x * VEC * (j.wide_w ? 4 : (int)sizeof(T));
-        if (!OFF) return;
-        for (int which = 0; which < 5; ++which)
-            for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < NV * VEC * (int)blockDim.x; i += blockDim.x * blockDim.y) {
-                const int c = i - off;
-                const bool in = c >= 0 && c < (int)j.cols;
-                const VecAt& a = all[which];
-                if (j.wide_w)
-                    ((float*)(dyn + which * span))[i] =
-                        !in ? 0.f : !a.p ? none[which] : TROP_IN((const float*)a.p + c, 4, a.sp) ? ((const float*)a.p)[c] : 0.f;
-                else
-                    ((T*)(dyn + which * span))[i] = !in || (a.p && !TROP_IN((const T*)a.p + c, sizeof(T), a.sp)) ? from_f32<T>(0.f)
-                                                    : a.p                                                     ? ((const T*)a.p)[c]
-                                                                                                              : from_f32<T>(none[which]);
-            }
-        __syncthreads();
+        if constexpr (OFF) {
+            for (int which = 0; which < 5; ++which)
+                for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < NV * VEC * (int)blockDim.x; i += blockDim.x * blockDim.y) {
+                    const int c = i - off;
+                    const bool in = c >= 0 && c < (int)j.cols;
+                    const VecAt& a = all[which];
+                    if (j.wide_w)
+                        ((float*)(dyn + which * span))[i] =
+                            !in ? 0.f : !a.p ? none[which] : TROP_IN((const float*)a.p + c, 4, a.sp) ? ((const float*)a.p)[c] : 0.f;
+                    else
+                        ((T*)(dyn + which * span))[i] = !in || (a.p && !TROP_IN((const T*)a.p + c, sizeof(T), a.sp)) ? from_f32<T>(0.f)
+                                                        : a.p                                                     ? ((const T*)a.p)[c]
+                                                                                                                  : from_f32<T>(none[which]);
+                }
+            __syncthreads();
+        }
     }
 };
 // (a number's scale may need more digits than T has: it is a factor of its own where there is no vector of it)
 
-// A vector of a row, or of its 8-bit copy, whose rows start where they like: the aligned words around it shifted together, and
-// two groups' units where it lies in two.
+// ------------------------------------------------------------------ rows on their way
+// A group's rows come through shared memory ahead of their turn: a stage of the ring holds a row of every tensor, and the
+// barrier of a later sum says that it has been read.  Rows on 16 bytes come by one bulk copy a tensor, which an mbarrier counts.
+// Of the others (OFF) every thread copies its own vectors and waits for those alone.
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from, int bytes, bool in)
+{
+    const int n = in ? bytes : 0;  // (what is not there arrives as zeros)
+    if (bytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(n) : "memory");
+    else if (bytes == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(from), "r"(n) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_wait(int stages)  // the oldest of `stages` groups
+{
+    if (stages >= 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
+    else if (stages == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (stages == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// One tensor's part of a stage: BYTES for each vector of each thread.  OFF: a piece of every thread's beside the others'.  `to`:
+// the part's shared address; `t` of `threads`.
 template <typename T, int VEC, bool CODED, bool OFF>
-struct Held {
-    Raw<T, VEC> q;
-    __device__ __forceinline__ void read(const RowsAt& a, const Rows8&, int64_t row, int c, const ResJob& j) { fetch<T, VEC, OFF>(q, a, row, c, j); }
-    __device__ __forceinline__ void again() { q.again(); }
-    __device__ __forceinline__ void get(Pair<VEC> (&o)[pairs<VEC>], int, int) const
+struct In {
+    static constexpr int BYTES = VEC * sizeof(T), PIECE = BYTES < 16 ? BYTES : 16;
+    static __device__ __forceinline__ bool inside(const T* p, const RowsAt& a, const ResJob& j)
     {
+        if (!OFF) return true;
+        const T* const begin = (const T*)a.p;
+        return p >= begin && p + VEC <= begin + (j.rows - 1) * a.s + j.cols;
+    }
+    static __device__ __forceinline__ void issue(uint32_t to, int t, int threads, const RowsAt& a, const Rows8&, uint32_t row, int c, const ResJob& j)
+    {
+        if (c >= (int)j.cols) return;
+        const T* p = elem<T>(a, row, c);
+        const bool in = inside(p, a, j) && TROP_IN(p, BYTES, a.sp);
+#pragma unroll
+        for (int i = 0; i < BYTES / PIECE; ++i)
+            copy_async(to + (i * threads + t) * PIECE, in ? reinterpret_cast<const char*>(p) + i * PIECE : (const char*)a.p, PIECE, in);
+    }
+    static __device__ __forceinline__ void take(Raw<T, VEC>& q, uint32_t to, int t, int threads, const RowsAt& a, uint32_t row, int c, const ResJob& j)
+    {
+        const int cols = (int)j.cols;
+        q.zero();
+        if (c >= cols) return;
+#pragma unroll
+        for (int i = 0; i < BYTES / PIECE; ++i) {
+            const uint32_t from = OFF ? to + (i * threads + t) * PIECE : to + t * BYTES + i * PIECE;
+            if constexpr (PIECE == 16)
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(q.w[4 * i]), "=r"(q.w[4 * i + 1]), "=r"(q.w[4 * i + 2]), "=r"(q.w[4 * i + 3])
+                             : "r"(from)
+                             : "memory");
+            else
+                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(q.w[0]), "=r"(q.w[1]) : "r"(from) : "memory");
+        }
+        if (OFF && !whole<VEC>(c, cols)) {
+            const T* p = elem<T>(a, row, c);
+            if (inside(p, a, j)) {
+                constexpr int E = 4 / sizeof(T);  // elements of a word
+#pragma unroll
+                for (int i = 0; i < Raw<T, VEC>::N; ++i) {
+                    uint32_t mask = 0;
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        if (c + i * E + e >= 0 && c + i * E + e < cols) mask |= (E == 1 ? 0xffffffffu : 0xffffu) << 16 * e;
+                    q.w[i] &= mask;
+                }
+            } else {  // at the matrix's own ends: one by one
+                float v[VEC];
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) v[i] = c + i >= 0 && c + i < cols && TROP_IN(p + i, sizeof(T), a.sp) ? to_f32(p[i]) : 0.f;
+                q.set(v);
+            }
+        }
+    }
+    static __device__ __forceinline__ void take(Pair<VEC> (&o)[pairs<VEC>], uint32_t to, int t, int threads, const RowsAt& a, const Rows8&, uint32_t row,
+                                                int c, uint32_t, const ResJob& j)
+    {
+        Raw<T, VEC> q;
+        take(q, to, t, threads, a, row, c, j);
 #pragma unroll
         for (int i = 0; i < pairs<VEC>; ++i) o[i] = pair_of<T, VEC>(q, i);
     }
 };
-template <typename T, int VEC, bool OFF>
-struct Held<T, VEC, true, OFF> {
-    Codes<VEC> k;
-    uint32_t e, e2;
-    __device__ __forceinline__ void read(const RowsAt&, const Rows8& a, int64_t row, int c, const ResJob& j)
+// 8-bit copies.  Of rows on 16 bytes the codes alone come this way (`e`: the scale, fetched a row ahead).  Of the others the
+// aligned words around the codes, shifted together afterwards, and the words of the two groups that they may lie in.  Words that reach outside the matrix are not
+// copied; their bytes are read when they are wanted.
+template <typename T, int VEC>
+struct In<T, VEC, true, false> {
+    static constexpr int BYTES = VEC;
+    static __device__ __forceinline__ void take(Pair<VEC> (&o)[pairs<VEC>], uint32_t to, int t, int, const RowsAt&, const Rows8&, uint32_t,
+                                                int c, uint32_t e, const ResJob& j)
+    {
+        Codes<VEC> k;
+        k.zero();
+        if (c < (int)j.cols) {
+            if constexpr (VEC == 8)
+                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(k.w[0]), "=r"(k.w[1]) : "r"(to + t * 8) : "memory");
+            else
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(k.w[0]) : "r"(to + t * 4) : "memory");
+        }
+        float v[VEC];
+        values8<VEC>(k.w, unit8(e), v);
+#pragma unroll
+        for (int i = 0; i < pairs<VEC>; ++i) o[i] = pair_at<VEC>(v, i);
+    }
+};
+template <typename T, int VEC>
+struct In<T, VEC, true, true> {
+    static constexpr int WORDS = VEC / 4 + 1, SCALES = 2, BYTES = 4 * (WORDS + SCALES);
+    static __device__ __forceinline__ const uint8_t* scale_at(const Rows8& a, uint32_t row, int c, int which, const ResJob& j)
+    {
+        return scales_at(a, row, (which ? min(c + VEC - 1, (int)j.cols - 1) : max(c, 0)) / GROUP8);
+    }
+    static __device__ __forceinline__ bool scale_inside(const uint8_t* s, const Rows8& a, const ResJob& j)
+    {
+        const uint8_t* const w = s - ((uintptr_t)s & 3);
+        return w >= a.scales && w + 4 <= a.scales + (j.rows - 1) * a.ss + ((int)j.cols + GROUP8 - 1) / GROUP8;
+    }
+    static __device__ __forceinline__ bool inside(const int8_t* p, const Rows8& a, const ResJob& j)
+    {
+        const int8_t* const w = p - ((uintptr_t)p & 3);
+        return w >= a.codes && w + 4 * WORDS <= a.codes + (j.rows - 1) * a.sc + j.cols;
+    }
+    static __device__ __forceinline__ void issue(uint32_t to, int t, int threads, const RowsAt&, const Rows8& a, uint32_t row, int c, const ResJob& j)
+    {
+        if (c >= (int)j.cols) return;
+        const int8_t* p = codes_at(a, row, c);
+        const int8_t* w = p - ((uintptr_t)p & 3);
+        const bool in = inside(p, a, j) && TROP_IN(w, 4 * WORDS, a.sp_c);
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) copy_async(to + (i * threads + t) * 4, w + 4 * i, 4, in);
+#pragma unroll
+        for (int i = 0; i < SCALES; ++i) {
+            const uint8_t* q = scale_at(a, row, c, i, j);
+            const bool there = scale_inside(q, a, j);
+            const uint8_t* word = q - ((uintptr_t)q & 3);
+            const bool ok = there && TROP_IN(word, 4, a.sp_s);
+            copy_async(to + ((WORDS + i) * threads + t) * 4, (const void*)((uintptr_t)word), 4, ok);
+        }
+    }
+    static __device__ __forceinline__ void take(Pair<VEC> (&o)[pairs<VEC>], uint32_t to, int t, int threads, const RowsAt&, const Rows8& a, uint32_t row,
+                                                int c, uint32_t, const ResJob& j)
     {
         const int cols = (int)j.cols;
-        const int8_t* p = a.codes + row * a.sc + c;
-        const uint8_t* s = a.scales + row * a.ss;
+        Codes<VEC> k;
         k.zero();
-        e = e2 = LEAST8;
-        if (c >= cols) return;
-        const int g = max(c, 0) / GROUP8;
-        if (TROP_IN(s + g, 1, a.sp_s)) e = s[g];
-        if constexpr (OFF) {
-            const int g2 = min(c + VEC - 1, cols - 1) / GROUP8;
-            if (TROP_IN(s + g2, 1, a.sp_s)) e2 = s[g2];
-            codes_any<VEC>(p, -c, cols - c, a.codes, a.codes + (j.rows - 1) * a.sc + cols, k, a.sp_c);
+        uint32_t e[SCALES];
+#pragma unroll
+        for (int i = 0; i < SCALES; ++i) e[i] = LEAST8;
+        if (c < cols) {
+            const int8_t* p = codes_at(a, row, c);
+            if (inside(p, a, j)) {
+                uint32_t w[WORDS];
+#pragma unroll
+                for (int i = 0; i < WORDS; ++i)
+                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[i]) : "r"(to + (i * threads + t) * 4) : "memory");
+#pragma unroll
+                for (int i = 0; i + 1 < WORDS; ++i) k.w[i] = __funnelshift_r(w[i], w[i + 1], ((uint32_t)(uintptr_t)p & 3) * 8);
+            } else {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    if (c + i >= 0 && c + i < cols && TROP_IN(p + i, 1, a.sp_c)) k.w[i / 4] |= (uint32_t)(uint8_t)p[i] << 8 * (i % 4);
+            }
             if (!whole<VEC>(c, cols)) {
 #pragma unroll
                 for (int i = 0; i < VEC; ++i)
                     if (c + i < 0 || c + i >= cols) k.w[i / 4] &= ~(0xffu << 8 * (i % 4));
             }
-        } else if (TROP_IN(p, VEC, a.sp_c)) {
-            k.read(p);
-        }
-    }
-    __device__ __forceinline__ void again() {}
-    __device__ __forceinline__ void get(Pair<VEC> (&o)[pairs<VEC>], int c, int) const
-    {
-        float v[VEC];
-        const float unit = unit8(e);
-        if (OFF) {
-            const float other = unit8(e2);
-            const int edge = max(c, 0) / GROUP8 * GROUP8 + GROUP8 - c;  // elements up to the first group's end
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) v[i] = coded8(k.w[i / 4] ^ 0x80808080u, i % 4) * (i < edge ? unit : other);
-        } else {
-            values8<VEC>(k.w, unit, v);
+            for (int i = 0; i < SCALES; ++i) {
+                const uint8_t* q = scale_at(a, row, c, i, j);
+                uint32_t w;
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(to + ((WORDS + i) * threads + t) * 4) : "memory");
+                e[i] = w >> ((uint32_t)(uintptr_t)q & 3) * 8 & 0xffu;
+                if (!scale_inside(q, a, j)) e[i] = TROP_IN(q, 1, a.sp_s) ? *q : LEAST8;
+            }
         }
+        float v[VEC];
+        const float unit = unit8(e[0]);
+        const float other = unit8(e[SCALES - 1]);
+        const int edge = max(c, 0) / GROUP8 * GROUP8 + GROUP8 - c;  // elements up to the first group's end
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = coded8(k.w[i / 4] ^ 0x80808080u, i % 4) * (i < edge ? unit : other);
 #pragma unroll
         for (int i = 0; i < pairs<VEC>; ++i) o[i] = pair_at<VEC>(v, i);
     }
 };
 
-__device__ __forceinline__ float row_gate(const ResJob& j, int64_t row, bool is_f32, bool is_bf16)
+// A group's ring of bulk copies: part `i` of a stage begins at `at[i]`.  A copy that did not land in its bounded wait is
+// reported, after which nothing more is fetched or waited for.
+struct Ring {
+    uint64_t* full;  // [4], the group's
+    bool ok;
+    __device__ __forceinline__ void init(uint64_t (*all)[4], int stages)
+    {
+        full = all[threadIdx.y];
+        ok = true;
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < stages; ++i) mbar_init(full + i, 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+        __syncthreads();
+    }
+    __device__ __forceinline__ void wait(int slot, uint32_t phase, uint32_t* error)
+    {
+        if (ok && !mbar_wait(full + slot, phase)) {
+            ok = false;
+            *(volatile uint32_t*)error = 1;
+            __threadfence_system();
+        }
+    }
+    // after a failure: the copies still on their way get one more wait each before the block leaves
+    __device__ __forceinline__ void leave(int stages)
+    {
+        if (ok || threadIdx.x != 0) return;
+        for (int i = 0; i < 2 * stages; ++i) (void)mbar_wait(full + i % stages, i / stages);
+    }
+};
+template <typename T>
+__device__ __forceinline__ bool row_in(const RowsAt& a, uint32_t row, int c, int n)
+{
+    return TROP_IN(elem<T>(a, row, c), n * sizeof(T), a.sp);
+}
+__device__ __forceinline__ void bulk_to(uint32_t to, const void* from, uint32_t bytes, uint64_t* bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to), "l"(from), "r"(bytes),
+                 "r"(smem_u32(bar))
+                 : "memory");
+}
+
+__device__ __forceinline__ float row_gate(const ResJob& j, uint32_t row, bool is_f32, bool is_bf16)
 {
     if (is_f32) {
         const float* p = (const float*)j.g.p + row * j.g.s;
@@ -276,22 +428,22 @@ __device__ __forceinline__ float row_gate(const ResJob& j, int64_t row, bool is_
     return is_bf16 ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
 }
 template <typename U>
-__device__ __forceinline__ float row_gate(const ResJob& j, int64_t row)
+__device__ __forceinline__ float row_gate(const ResJob& j, uint32_t row)
 {
     return row_gate(j, row, sizeof(U) == 4, std::is_same<U, bf16>::value);
 }
 template <typename U>
-__device__ __forceinline__ void put_row_gate(const ResJob& j, int64_t row, float v)
+__device__ __forceinline__ void put_row_gate(const ResJob& j, uint32_t row, float v)
 {
     U* p = (U*)j.dg.p + row * j.dg.s;
     if (TROP_IN(p, sizeof(U), j.dg.sp)) *p = from_f32<U>(v);
 }
-__device__ __forceinline__ float stat(const ResJob& j, int which, int64_t row)
+__device__ __forceinline__ float stat(const ResJob& j, int which, uint32_t row)
 {
     const float* p = j.stats + which * j.rows + row;
     return TROP_IN(p, 4, j.sp_stats) ? *p : 0.f;
 }
-__device__ __forceinline__ void put_stat(const ResJob& j, int which, int64_t row, float v)
+__device__ __forceinline__ void put_stat(const ResJob& j, int which, uint32_t row, float v)
 {
     float* p = j.stats + which * j.rows + row;
     if (j.stats && TROP_IN(p, 4, j.sp_stats)) *p = v;
@@ -299,7 +451,7 @@ __device__ __forceinline__ void put_stat(const ResJob& j, int which, int64_t row
 
 // The codes of a group's lanes (all of the warp take part; `live`: this one's vector is in the row).
 template <typename T, int VEC>
-__device__ __forceinline__ void keep(const Rows8& a, int64_t row, int64_t c, bool live, const Raw<T, VEC>& q)
+__device__ __forceinline__ void keep(const Rows8& a, uint32_t row, int64_t c, bool live, const Raw<T, VEC>& q)
 {
     const uint32_t e = scale8(group_top8<VEC>(live ? top8<T, VEC>(q) : 0u));
     if (!live) return;
@@ -311,8 +463,18 @@ __device__ __forceinline__ void keep(const Rows8& a, int64_t row, int64_t c, boo
     if (c % GROUP8 == 0 && TROP_IN(s, 1, a.sp_s)) *s = (uint8_t)e;
 }
 
+// The sums over either half of a warp, for all of it.
+__device__ __forceinline__ void halves(float v, float& a, float& b)
+{
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    const float w = __shfl_xor_sync(0xffffffffu, v, 16);
+    const bool up = threadIdx.x & 16;
+    a = up ? w : v;
+    b = up ? v : w;
+}
 // Two sums over a row's group (a warp, or the whole block): each half of a warp takes one of them, so that five shuffles
-// serve both; the warps' sums are read four at a time.  Callers alternate between two of `sh`, [2][32] floats that
+// serve both, of the warps' sums too.  Callers alternate between two of `sh`, [2][32] floats that
 // start as zeros, which leaves one barrier a call.
 __device__ __forceinline__ void row_sums(float& a, float& b, float (*sh)[32])
 {
@@ -328,12 +490,10 @@ __device__ __forceinline__ void row_sums(float& a, float& b, float (*sh)[32])
     }
     if ((threadIdx.x & 15) == 0) sh[up][threadIdx.x >> 5] = v;
     __syncthreads();
-    a = b = 0.f;
-    for (int w = 0; w < (int)(blockDim.x >> 5); w += 4) {
-        const float4 p = *reinterpret_cast<const float4*>(&sh[0][w]), q = *reinterpret_cast<const float4*>(&sh[1][w]);
-        a += (p.x + p.y) + (p.z + p.w);
-        b += (q.x + q.y) + (q.z + q.w);
-    }
+    const int l = threadIdx.x & 15;
+    v = sh[up][l];
+    if (blockDim.x > 512) v += sh[up][l + 16];
+    halves(v, a, b);
 }
 // The same where `ctas` CTAs of a cluster share the row, up to eight of 16 warps: every warp hands its sums to all of them, and the
 // one barrier is the cluster's.
@@ -347,12 +507,9 @@ __device__ __forceinline__ void row_sums_wide(float& a, float& b, float (*sh)[12
     if (to < ctas)
         asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa(smem_u32(&sh[up][rank * 16 + (threadIdx.x >> 5)]), to)), "f"(v) : "memory");
     cluster_sync_all();
-    a = b = 0.f;
-    for (uint32_t w = 0; w < ctas * 16; w += 4) {
-        const float4 p = *reinterpret_cast<const float4*>(&sh[0][w]), q = *reinterpret_cast<const float4*>(&sh[1][w]);
-        a += (p.x + p.y) + (p.z + p.w);
-        b += (q.x + q.y) + (q.z + q.w);
-    }
+    const float4 p = *reinterpret_cast<const float4*>(&sh[up][8 * to]), q = *reinterpret_cast<const float4*>(&sh[up][8 * to + 4]);
+    v = ((p.x + p.y) + (p.z + p.w)) + ((q.x + q.y) + (q.z + q.w));
+    halves(v, a, b);
 }
 __device__ __forceinline__ void zero_sums(float* sh, int n)
 {
@@ -433,44 +590,76 @@ __device__ __forceinline__ void gated(Pair<VEC> (&t)[pairs<VEC>], const Pair<VEC
 }
 
 template <typename S, typename U, typename Y, int VEC, int NV, int MAXT, bool OFF>
-__global__ void __launch_bounds__(MAXT) k_residual(const ResJob j, int period)
+__global__ void __launch_bounds__(MAXT) k_residual(const ResJob j, int period, int stages, uint32_t* error)
 {
     pdl_wait();
     pdl_signal();
     extern __shared__ __align__(16) uint8_t dyn[];
     __shared__ __align__(16) float sh[2][2][32];
+    __shared__ __align__(8) uint64_t full[8][4];
     zero_sums(&sh[0][0][0], 128);
     const int cols = (int)j.cols;
     const Walk walk = walk_of<U, VEC, OFF>(j.u.p, j.u.s, period, blockIdx.x, gridDim.x);
     Vectors<Y, VEC, OFF> vec;
     vec.template init<NV>(dyn, walk.off, j, {j.w, j.b, j.pw, j.pb, j.s}, {1.f, 0.f, 1.f, 0.f, 1.f});
     const float scale = j.s.p ? 1.f : j.scale;
-    int turn = 0;
-    for (int64_t n = walk.first; walk.row(n) < j.rows; n += walk.step) {
-        const int64_t row = walk.row(n);
-        Raw<U, VEC> qu[NV], qg[NV];
-        Raw<S, VEC> qx[NV];
+    using InU = In<U, VEC, false, OFF>;
+    using InS = In<S, VEC, false, OFF>;
+    const int wide = OFF ? blockDim.x * blockDim.y : blockDim.x;  // threads whose vectors lie together
+    const int t0 = OFF ? threadIdx.y * blockDim.x + threadIdx.x : threadIdx.x;
+    const int at_x = NV * InU::BYTES * wide, at_g = at_x + NV * InS::BYTES * wide;
+    const int size = at_g + (j.gate == GATE_FULL ? NV * InU::BYTES * wide : 0), stage = OFF ? size : size * blockDim.y;
+    const uint32_t base = smem_u32(dyn) + (OFF ? 5 * vec.span : threadIdx.y * size);
+    Ring ring;
+    if (!OFF) ring.init(full, stages);
+    auto issue = [&](uint32_t row, int slot) {
+        const uint32_t to = base + slot * stage;
+        if constexpr (OFF) {
+            if (row < (uint32_t)j.rows) {
+#pragma unroll
+                for (int k = 0; k < NV; ++k) {
+                    const int c = column<VEC>(k, walk.off);
+                    InU::issue(to + k * InU::BYTES * wide, t0, wide, j.u, j.ku, row, c, j);
+                    InS::issue(to + at_x + k * InS::BYTES * wide, t0, wide, j.x, j.kr, row, c, j);
+                    if (j.gate == GATE_FULL) InU::issue(to + at_g + k * InU::BYTES * wide, t0, wide, j.g, j.kg, row, c, j);
+                }
+            }
+            copies_commit();
+        } else if (threadIdx.x == 0 && row < (uint32_t)j.rows && ring.ok) {
+            const bool g = j.gate == GATE_FULL;
+            if (row_in<U>(j.u, row, 0, cols) && row_in<S>(j.x, row, 0, cols) && (!g || row_in<U>(j.g, row, 0, cols))) {
+                const uint32_t bu = cols * sizeof(U), bx = cols * sizeof(S);
+                uint64_t* const bar = ring.full + slot;
+                mbar_expect_tx(bar, bx + (g ? 2 : 1) * bu);
+                bulk_to(to, elem<U>(j.u, row, 0), bu, bar);
+                bulk_to(to + at_x, elem<S>(j.x, row, 0), bx, bar);
+                if (g) bulk_to(to + at_g, elem<U>(j.g, row, 0), bu, bar);
+            } else {
+                mbar_expect_tx(ring.full + slot, 0);
+            }
+        }
+    };
+    for (int i = 0; i < stages; ++i) issue(walk.first + i * walk.step, i);
+    int turn = 0, slot = 0;
+    uint32_t phase = 0;
+    float gate = 0.f;
+    if (j.gate == GATE_ROW && walk.first < (uint32_t)j.rows) gate = row_gate<U>(j, walk.first);
+    for (uint32_t row = walk.first; row < (uint32_t)j.rows; row += walk.step) {
+        const float ga = scale * (j.gate == GATE_ROW ? gate_value(gate, j.act) : 1.f);
+        if (j.gate == GATE_ROW && row + walk.step < (uint32_t)j.rows) gate = row_gate<U>(j, row + walk.step);
+        if (OFF) copies_wait(stages);
+        else ring.wait(slot, phase, error);
+        const uint32_t from = base + slot * stage;
+        Pairs<VEC, NV> t;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int c = column<VEC>(k, walk.off);
-            fetch<U, VEC, OFF>(qu[k], j.u, row, c, j);
-            fetch<S, VEC, OFF>(qx[k], j.x, row, c, j);
-            if (j.gate == GATE_FULL) fetch<U, VEC, OFF>(qg[k], j.g, row, c, j);
+            Raw<U, VEC> q;
+            InU::take(q, from + k * InU::BYTES * wide, t0, wide, j.u, row, c, j);
+            if (!OFF && j.ku.codes) keep<U, VEC>(j.ku, row, c, c < cols, q);
+#pragma unroll
+            for (int i = 0; i < pairs<VEC>; ++i) t[k][i] = pair_of<U, VEC>(q, i);
         }
-        const float ga = scale * (j.gate == GATE_ROW ? gate_value(row_gate<U>(j, row), j.act) : 1.f);
-        if (!OFF && j.ku.codes) {
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int c = column<VEC>(k, 0);
-                keep<U, VEC>(j.ku, row, c, c < cols, qu[k]);
-                if (j.gate == GATE_FULL) keep<U, VEC>(j.kg, row, c, c < cols, qg[k]);
-            }
-        }
-        Pairs<VEC, NV> t;
-#pragma unroll
-        for (int k = 0; k < NV; ++k)
-#pragma unroll
-            for (int i = 0; i < pairs<VEC>; ++i) t[k][i] = pair_of<U, VEC>(qu[k], i);
         float um = 0.f, ur = 1.f, mean, rstd;
         if (j.post) row_stats<VEC, NV, OFF>(j, t, walk.off, sh, turn, um, ur);
 #pragma unroll
@@ -490,21 +679,28 @@ __global__ void __launch_bounds__(MAXT) k_residual(const ResJob j, int period)
                 for (int i = 0; i < pairs<VEC>; ++i) t[k][i] = p_mul(t[k][i], f[i]);
             }
             if (j.gate == GATE_FULL) {
+                Raw<U, VEC> g;
+                InU::take(g, from + at_g + k * InU::BYTES * wide, t0, wide, j.g, row, c, j);
+                if (!OFF && j.kg.codes) keep<U, VEC>(j.kg, row, c, c < cols, g);
 #pragma unroll
-                for (int i = 0; i < pairs<VEC>; ++i) o[i] = pair_of<U, VEC>(qg[k], i);
+                for (int i = 0; i < pairs<VEC>; ++i) o[i] = pair_of<U, VEC>(g, i);
                 gated<VEC>(t[k], o, j.act);
             }
+            Raw<S, VEC> q;
+            InS::take(q, from + at_x + k * InS::BYTES * wide, t0, wide, j.x, row, c, j);
 #pragma unroll
             for (int i = 0; i < pairs<VEC>; ++i)
-                t[k][i] = p_fma(p_of<Pair<VEC>>(j.alpha), pair_of<S, VEC>(qx[k], i), p_mul(t[k][i], p_of<Pair<VEC>>(ga)));
+                t[k][i] = p_fma(p_of<Pair<VEC>>(j.alpha), pair_of<S, VEC>(q, i), p_mul(t[k][i], p_of<Pair<VEC>>(ga)));
             float v[VEC];
             apart<VEC>(t[k], v);
-            Raw<S, VEC> q;
             q.set(v);
             put<S, VEC, OFF>(j.r, row, c, q, cols);
             if (!OFF && j.kr.codes) keep<S, VEC>(j.kr, row, c, c < cols, q);
         }
         row_stats<VEC, NV, OFF>(j, t, walk.off, sh, turn, mean, rstd);
+        if (!OFF && blockDim.x == 32) __syncwarp();
+        issue(row + stages * walk.step, slot);  // (all of the group have passed a sum since they read the stage)
+        if (++slot == stages) slot = 0, phase ^= 1;
         if (threadIdx.x == 0) put_stat(j, 0, row, um), put_stat(j, 1, row, ur), put_stat(j, 2, row, mean), put_stat(j, 3, row, rstd);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -519,6 +715,7 @@ __global__ void __launch_bounds__(MAXT) k_residual(const ResJob j, int period)
             put<Y, VEC, OFF>(j.y, row, c, f, cols);
         }
     }
+    if (!OFF) ring.leave(stages);
 }
 
 // The scalar forms that the long rows' kernels use.
@@ -648,13 +845,14 @@ __device__ __forceinline__ void put_partials(const ResJob& j, const Pair<VEC> (&
 // Rows of more than 4096 columns are shared by the CTAs of a cluster (WIDE): a thread that had more of a row than eight
 // elements would have no room for its columns' four sums.
 template <typename S, typename U, typename Y, int VEC, int NV, bool CODED, bool OFF, bool WIDE>
-__global__ void __launch_bounds__(512) k_residual_back(const ResJob j, int period)
+__global__ void __launch_bounds__(512) k_residual_back(const ResJob j, int period, int stages, uint32_t* error)
 {
     pdl_wait();
     pdl_signal();
     extern __shared__ __align__(16) uint8_t dyn[];
     constexpr int SUMS = WIDE ? 128 : 32;
     __shared__ __align__(16) float sh[3][2][SUMS];
+    __shared__ __align__(8) uint64_t full[8][4];
     zero_sums(&sh[0][0][0], 6 * SUMS);
     const int cols = (int)j.cols;
     const uint32_t rank = WIDE ? cluster_ctarank() : 0, ctas = WIDE ? cluster_ctas() : 1;
@@ -679,26 +877,97 @@ __global__ void __launch_bounds__(512) k_residual_back(const ResJob j, int perio
 #pragma unroll
             for (int i = 0; i < pairs<VEC>; ++i) acc[a][k][i] = p_of<Pair<VEC>>(0.f);
     using P = Pair<VEC>;
-    int turn = 0;
-    for (int64_t n = walk.first; walk.row(n) < j.rows; n += walk.step) {
-        const int64_t row = walk.row(n);
-        Held<Y, VEC, false, OFF> qy[NV];
-        Held<S, VEC, false, OFF> qd[NV];
-        Held<S, VEC, CODED, OFF> qr[NV];
-        Held<U, VEC, CODED, OFF> qu[NV], qg[NV];
+    using InY = In<Y, VEC, false, OFF>;
+    using InD = In<S, VEC, false, OFF>;
+    using InR = In<S, VEC, CODED, OFF>;
+    using InU = In<U, VEC, CODED, OFF>;
+    const int wide = OFF ? blockDim.x * blockDim.y : blockDim.x;  // threads whose vectors lie together
+    const int t0 = OFF ? threadIdx.y * blockDim.x + threadIdx.x : threadIdx.x;
+    const int at_r = NV * InY::BYTES * wide, at_u = at_r + NV * InR::BYTES * wide, at_d = at_u + NV * InU::BYTES * wide;
+    const int at_g = at_d + (j.dr.p ? NV * InD::BYTES * wide : 0);
+    const int size = at_g + (j.gate == GATE_FULL ? NV * InU::BYTES * wide : 0), stage = OFF ? size : size * blockDim.y;
+    const uint32_t base = smem_u32(dyn) + (OFF ? 5 * vec.span : threadIdx.y * size);
+    Ring ring;
+    if (!OFF) ring.init(full, stages);
+    auto issue = [&](uint32_t row, int slot) {
+        const uint32_t to = base + slot * stage;
+        if constexpr (OFF) {
+            if (row < (uint32_t)j.rows) {
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int c = column<VEC>(k, walk.off);
-            qy[k].read(j.dy, j.kr, row, c, j);
-            qr[k].read(j.r, j.kr, row, c, j);
-            if (j.dr.p) qd[k].read(j.dr, j.kr, row, c, j);
-            else qd[k].q.zero();
-            qu[k].read(j.u, j.ku, row, c, j);
-            if (j.gate == GATE_FULL) qg[k].read(j.g, j.kg, row, c, j);
+                for (int k = 0; k < NV; ++k) {
+                    const int c = column<VEC>(k, walk.off);
+                    InY::issue(to + k * InY::BYTES * wide, t0, wide, j.dy, j.kr, row, c, j);
+                    InR::issue(to + at_r + k * InR::BYTES * wide, t0, wide, j.r, j.kr, row, c, j);
+                    InU::issue(to + at_u + k * InU::BYTES * wide, t0, wide, j.u, j.ku, row, c, j);
+                    if (j.dr.p) InD::issue(to + at_d + k * InD::BYTES * wide, t0, wide, j.dr, j.kr, row, c, j);
+                    if (j.gate == GATE_FULL) InU::issue(to + at_g + k * InU::BYTES * wide, t0, wide, j.g, j.kg, row, c, j);
+                }
+            }
+            copies_commit();
+        } else if (threadIdx.x == 0 && row < (uint32_t)j.rows && ring.ok) {
+            const int c = -walk.off, n = max(0, min(cols - c, (int)(NV * blockDim.x) * VEC));
+            const bool g = j.gate == GATE_FULL, d = j.dr.p;
+            bool in = row_in<Y>(j.dy, row, c, n) && (!d || row_in<S>(j.dr, row, c, n));
+            if constexpr (CODED) {
+                in = in && TROP_IN(codes_at(j.kr, row, c), n, j.kr.sp_c) && TROP_IN(codes_at(j.ku, row, c), n, j.ku.sp_c) &&
+                     (!g || TROP_IN(codes_at(j.kg, row, c), n, j.kg.sp_c));
+            } else {
+                in = in && row_in<S>(j.r, row, c, n) && row_in<U>(j.u, row, c, n) && (!g || row_in<U>(j.g, row, c, n));
+            }
+            uint64_t* const bar = ring.full + slot;
+            if (in && n > 0) {
+                const uint32_t br = n * (CODED ? 1 : sizeof(S)), bu = n * (CODED ? 1 : sizeof(U)), by = n * sizeof(Y), bd = n * sizeof(S);
+                mbar_expect_tx(bar, by + br + (g ? 2 : 1) * bu + (d ? bd : 0));
+                bulk_to(to, elem<Y>(j.dy, row, c), by, bar);
+                bulk_to(to + at_r, CODED ? (void*)codes_at(j.kr, row, c) : (void*)elem<S>(j.r, row, c), br, bar);
+                if (d) bulk_to(to + at_d, elem<S>(j.dr, row, c), bd, bar);
+                bulk_to(to + at_u, CODED ? (void*)codes_at(j.ku, row, c) : (void*)elem<U>(j.u, row, c), bu, bar);
+                if (g) bulk_to(to + at_g, CODED ? (void*)codes_at(j.kg, row, c) : (void*)elem<U>(j.g, row, c), bu, bar);
+            } else {
+                mbar_expect_tx(bar, 0);
+            }
         }
-        const float um = stat(j, 0, row), ur = stat(j, 1, row), mean = stat(j, 2, row), rstd = stat(j, 3, row);
+    };
+    // a row's statistics, gate and scales, fetched a row ahead
+    constexpr bool SCALED = CODED && !OFF;
+    float um, ur, mean, rstd, gate;
+    uint32_t sr[NV], su[NV], sg[NV];
+    auto scale_of = [&](const Rows8& a, uint32_t row, int c) -> uint32_t {
+        const uint8_t* p = scales_at(a, row, c / GROUP8);
+        return c < cols && TROP_IN(p, 1, a.sp_s) ? *p : LEAST8;
+    };
+    auto ahead = [&](uint32_t row) {
+        um = ur = mean = rstd = gate = 0.f;
+        if (row >= (uint32_t)j.rows) return;
+        um = stat(j, 0, row), ur = stat(j, 1, row), mean = stat(j, 2, row), rstd = stat(j, 3, row);
+        if (j.gate == GATE_ROW) gate = row_gate<U>(j, row);
+        if constexpr (SCALED) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int c = column<VEC>(k, walk.off);
+                sr[k] = scale_of(j.kr, row, c);
+                su[k] = scale_of(j.ku, row, c);
+                if (j.gate == GATE_FULL) sg[k] = scale_of(j.kg, row, c);
+            }
+        }
+    };
+#pragma unroll
+    for (int k = 0; k < NV; ++k) sr[k] = su[k] = sg[k] = LEAST8;
+    for (int i = 0; i < stages; ++i) issue(walk.first + i * walk.step, i);
+    int turn = 0, slot = 0;
+    uint32_t phase = 0;
+    ahead(walk.first);
+    for (uint32_t row = walk.first; row < (uint32_t)j.rows; row += walk.step) {
+        const uint32_t from = base + slot * stage;
+        const float um0 = um, ur0 = ur, mean0 = mean, rstd0 = rstd;
+        uint32_t er[NV], eu[NV], eg[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) er[k] = sr[k], eu[k] = su[k], eg[k] = sg[k];
         float ga = 1.f, gs = 1.f;
-        if (j.gate == GATE_ROW) gate_both(row_gate<U>(j, row), j.act, ga, gs);
+        if (j.gate == GATE_ROW) gate_both(gate, j.act, ga, gs);
+        ahead(row + walk.step);
+        if (OFF) copies_wait(stages);
+        else ring.wait(slot, phase, error);
         P h[NV][pairs<VEC>], e[NV][pairs<VEC>];
         P sum0 = p_of<P>(0.f), sum1 = sum0;
 #pragma unroll
@@ -706,11 +975,11 @@ __global__ void __launch_bounds__(512) k_residual_back(const ResJob j, int perio
             const int c = column<VEC>(k, walk.off);
             P w[pairs<VEC>];
             vec.get(0, j.w, k, c, j, 1.f, w);
-            qy[k].get(e[k], c, cols);
-            qr[k].get(h[k], c, cols);
+            InY::take(e[k], from + k * InY::BYTES * wide, t0, wide, j.dy, j.kr, row, c, 0, j);
+            InR::take(h[k], from + at_r + k * InR::BYTES * wide, t0, wide, j.r, j.kr, row, c, er[k], j);
 #pragma unroll
             for (int i = 0; i < pairs<VEC>; ++i) {
-                h[k][i] = p_mul(p_add(h[k][i], p_of<P>(-mean)), p_of<P>(rstd));
+                h[k][i] = p_mul(p_add(h[k][i], p_of<P>(-mean0)), p_of<P>(rstd0));
                 acc[0][k][i] = p_fma(e[k][i], h[k][i], acc[0][k][i]);
                 acc[1][k][i] = p_add(acc[1][k][i], e[k][i]);
                 e[k][i] = p_mul(e[k][i], w[i]);
@@ -720,29 +989,39 @@ __global__ void __launch_bounds__(512) k_residual_back(const ResJob j, int perio
         }
         float s0 = p_sum(sum0), s1 = p_sum(sum1);
         sums(s0, s1, turn);
+        // (bulk copies: all of the group have read the stage before this one)
+        if (!OFF && row != walk.first) {
+            if (blockDim.x == 32) __syncwarp();
+            issue(row + (stages - 1) * walk.step, slot == 0 ? stages - 1 : slot - 1);
+        }
         const P flat = p_of<P>(j.rms ? 0.f : -s0 * j.inv_cols), along = p_of<P>(-s1 * j.inv_cols);
         P sum2 = sum0 = sum1 = p_of<P>(0.f);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int c = column<VEC>(k, walk.off);
             P o[pairs<VEC>], d[pairs<VEC>], f[pairs<VEC>], a[pairs<VEC>];
-            qd[k].get(d, c, cols);
+            if (j.dr.p) {
+                InD::take(d, from + at_d + k * InD::BYTES * wide, t0, wide, j.dr, j.kr, row, c, 0, j);
+            } else {
+#pragma unroll
+                for (int i = 0; i < pairs<VEC>; ++i) d[i] = p_of<P>(0.f);
+            }
 #pragma unroll
             for (int i = 0; i < pairs<VEC>; ++i) {
-                d[i] = p_fma(p_of<P>(rstd), p_fma(h[k][i], along, p_add(e[k][i], flat)), d[i]);
+                d[i] = p_fma(p_of<P>(rstd0), p_fma(h[k][i], along, p_add(e[k][i], flat)), d[i]);
                 o[i] = p_mul(p_of<P>(j.alpha), d[i]);
             }
             if (j.dx.p && c < cols) put<S, VEC, OFF>(j.dx, row, c, o, cols);
-            qu[k].get(h[k], c, cols);  // from here on h is u's
+            InU::take(h[k], from + at_u + k * InU::BYTES * wide, t0, wide, j.u, j.ku, row, c, eu[k], j);  // from here on h is u's
             if (j.post)
 #pragma unroll
-                for (int i = 0; i < pairs<VEC>; ++i) h[k][i] = p_mul(p_add(h[k][i], p_of<P>(-um)), p_of<P>(ur));
+                for (int i = 0; i < pairs<VEC>; ++i) h[k][i] = p_mul(p_add(h[k][i], p_of<P>(-um0)), p_of<P>(ur0));
             // o: d times the scale and, once v and the gate's slope are in, the gate's gradient; a: the gate
             vec.get(4, j.s, k, c, j, 1.f, f);
 #pragma unroll
             for (int i = 0; i < pairs<VEC>; ++i) o[i] = p_mul(p_mul(d[i], f[i]), p_of<P>(scale));
             if (j.gate == GATE_FULL) {
-                qg[k].get(a, c, cols);
+                InU::take(a, from + at_g + k * InU::BYTES * wide, t0, wide, j.g, j.kg, row, c, eg[k], j);
                 if (j.act != 0) {
                     float g[VEC], slope[VEC];
                     apart<VEC>(a, g);
@@ -789,6 +1068,7 @@ __global__ void __launch_bounds__(512) k_residual_back(const ResJob j, int perio
                 for (int i = 0; i < pairs<VEC>; ++i) sum2 = p_fma(o[i], d[i], sum2);
             }
         }
+        if (OFF) issue(row + stages * walk.step, slot);
         s0 = p_sum(sum0), s1 = p_sum(sum1);
         if (j.post) sums(s0, s1, turn ^ 1);
         else turn ^= 1;  // (the next row's first sums take the other of the two)
@@ -805,11 +1085,14 @@ __global__ void __launch_bounds__(512) k_residual_back(const ResJob j, int perio
                 if (j.post)
 #pragma unroll
                     for (int i = 0; i < pairs<VEC>; ++i)
-                        e[k][i] = p_mul(p_of<P>(ur), p_fma(h[k][i], along2, p_add(e[k][i], flat2)));
+                        e[k][i] = p_mul(p_of<P>(ur0), p_fma(h[k][i], along2, p_add(e[k][i], flat2)));
                 if (c < cols) put<U, VEC, OFF>(j.du, row, c, e[k], cols);
             }
         }
+        if (++slot == stages) slot = 0, phase ^= 1;
     }
+    if (!OFF) ring.leave(stages);
+    if (j.want && blockDim.y > 1) __syncthreads();  // (the warps' sums go where the ring was)
     if (j.want) put_partials<VEC, NV>(j, acc, reinterpret_cast<float*>(dyn), walk.off, block);
     if (WIDE) cluster_sync_all();  // no CTA leaves before the others have written its sums
 }
@@ -828,11 +1111,13 @@ struct LongRow {
     template <typename T, bool C>
     __device__ float of(const RowsAt& a, const Rows8& k, int64_t c) const
     {
-        Held<T, 1, C, false> q;
-        float v[1];
-        q.read(a, k, row, (int)c, j);
-        q.get(v, (int)c, (int)j.cols);
-        return v[0];
+        if (C) {
+            const int8_t* p = k.codes + row * k.sc + c;
+            const uint8_t* s = k.scales + row * k.ss + c / GROUP8;
+            return TROP_IN(p, 1, k.sp_c) && TROP_IN(s, 1, k.sp_s) ? (float)*p * unit8(*s) : 0.f;
+        }
+        const T* p = (const T*)a.p + row * a.s + c;
+        return TROP_IN(p, sizeof(T), a.sp) ? to_f32(*p) : 0.f;
     }
     __device__ float vec(const VecAt& a, int64_t c, float none) const { return one_of<Y>(a, c, j, none); }
     __device__ void first(int64_t c, float& dy, float& h) const
@@ -1010,15 +1295,26 @@ struct Types {
 // starts on one); 0 where they differ, or too many rows share none.
 struct Places {
     int vec;
-    int64_t rows;
+    int64_t rows, cols;
     int64_t base = -1, stride = 0;
-    bool same = true;
-    void add(const RowsAt& a, size_t elem)
+    bool same = true, bulk = true;  // bulk: whole rows in units of 16 bytes
+    void add(RowsAt& a, size_t elem)
     {
         if (!a.p) return;
-        const int64_t b = (uintptr_t)a.p / elem % vec, s = rows > 1 ? a.s % vec : 0;
+        const int64_t step = rows > 1 ? a.s : 0, b = (uintptr_t)a.p / elem % vec, s = step % vec;
         if (base < 0) base = b, stride = s;
         else if (b != base || s != stride) same = false;
+        if (step < 0 || step * elem >> 32) same = false;
+        a.sb = (uint32_t)(step * elem);
+        if ((uintptr_t)a.p % 16 || step * elem % 16 || cols * elem % 16) bulk = false;
+    }
+    void add(Rows8& k)
+    {
+        if (!k.codes) return;
+        const int64_t step = rows > 1 ? k.sc : 0, ss = rows > 1 ? k.ss : 0;
+        if (step < 0 || step >> 32 || ss < 0 || ss >> 32) same = false;
+        k.sb = (uint32_t)step, k.ssb = (uint32_t)ss;
+        if ((uintptr_t)k.codes % 16 || step % 16 || cols % 16) bulk = false;
     }
     int period() const
     {
@@ -1027,9 +1323,8 @@ struct Places {
         while (p * stride % vec) p *= 2;
         return p;
     }
-    bool on() const { return same && base <= 0 && stride == 0; }
+    bool on() const { return same && base <= 0 && stride == 0 && bulk; }
 };
-bool on8(const Rows8& k, int vec, int64_t rows) { return aligned(k.codes, k.sc, 1, vec, rows); }
 
 int launch_pack(const RowsAt& a, int dtype, const Rows8& k, int64_t rows, int64_t cols, cudaStream_t s)
 {
@@ -1038,55 +1333,77 @@ int launch_pack(const RowsAt& a, int dtype, const Rows8& k, int64_t rows, int64_
 template <typename T>
 constexpr int dtype_of() { return sizeof(T) == 4 ? (int)TROP_F32 : std::is_same<T, bf16>::value ? (int)TROP_BF16 : (int)TROP_F16; }
 
+// Stages of a ring: up to four rows, in what a block's share of the SM's shared memory leaves.
+constexpr size_t SM_SMEM = 227 * 1024;
+int stages_of(size_t stage, size_t beside, int per_sm)
+{
+    const size_t share = SM_SMEM / per_sm - 1024 - 4096;  // (a block's own kilobyte, and the static arrays)
+    const size_t n = share > beside ? (share - beside) / stage : 0;
+    return (int)std::min<size_t>(4, n);
+}
+
 dim3 long_block(int64_t cols) { return dim3((unsigned)std::min<int64_t>(1024, (cols + 31) / 32 * 32)); }
 
 }  // namespace
 
 template <typename S, typename U, typename Y>
-int residual_forward(const ResJob& j, int sm, cudaStream_t s)
+int residual_forward(ResJob j, int sm, cudaStream_t s)
 {
     constexpr int V = Types<S, U, Y>::VEC;
     const size_t we = j.wide_w ? 4 : sizeof(Y);
-    Places at = {V, j.rows};
+    Places at = {V, j.rows, j.cols};
     at.add(j.x, sizeof(S)), at.add(j.r, sizeof(S)), at.add(j.u, sizeof(U)), at.add(j.y, sizeof(Y));
     if (j.gate == GATE_FULL) at.add(j.g, sizeof(U));
-    bool vec = j.cols % V == 0 && at.on() && on8(j.ku, V, j.rows) && on8(j.kg, V, j.rows) && on8(j.kr, V, j.rows);
+    at.add(j.ku), at.add(j.kg), at.add(j.kr);
+    bool vec = j.cols % V == 0 && at.on();
     for (const VecAt* a : {&j.w, &j.b, &j.pw, &j.pb, &j.s}) vec = vec && aligned(a->p, 0, we, V, 1);
     const int period = at.period();
-    int nv = 0;
+    const bool off = !vec && period > 0 && j.cols >= 2 * V;
+    const int64_t units = off ? (j.cols + V - 1) / V + 1 : j.cols / V;
+    int nv = 0, stages = 0;
     dim3 block;
-    if (!vec && period > 0 && j.cols >= 2 * V &&
-        shape_of((j.cols + V - 1) / V + 1, V, 16, 1024, j.rows, sm, 8, &nv, &block) && (size_t)5 * nv * block.x * V * we <= 196608) {
-        // off the granules: whole vectors all the same; the copies, whose groups lie across these, by a pass of their own
-        ResJob k = j;
-        k.ku.codes = k.kg.codes = k.kr.codes = nullptr;
-        const size_t smem = (size_t)5 * nv * block.x * V * we;
-        const auto kernel = nv == 1          ? k_residual<S, U, Y, V, 1, 1024, true>
-                            : nv * V < 16    ? k_residual<S, U, Y, V, 2, 1024, true>
-                            : block.x <= 512 ? k_residual<S, U, Y, V, 16 / V, 512, true>
-                                             : k_residual<S, U, Y, V, 16 / V, 1024, true>;
-        TROP_TRY(allow_dynamic((const void*)kernel));
-        int per_sm = 0;  // as many blocks as run at once: none waits for a place
-        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, (int)(block.x * block.y), smem);
-        if (e != cudaSuccess) return cuda_error(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor(k_residual)");
-        int64_t blocks = std::min<int64_t>((j.rows + block.y - 1) / block.y, (int64_t)sm * std::max(1, per_sm));
-        blocks = std::max<int64_t>(1, blocks / period) * period;
-        TROP_LAUNCH(kernel, dim3((unsigned)blocks), block, smem, k, period);
-        if (j.ku.codes) TROP_TRY(launch_pack(j.u, dtype_of<U>(), j.ku, j.rows, j.cols, s));
-        if (j.kg.codes) TROP_TRY(launch_pack(j.g, dtype_of<U>(), j.kg, j.rows, j.cols, s));
-        if (j.kr.codes) TROP_TRY(launch_pack(j.r, dtype_of<S>(), j.kr, j.rows, j.cols, s));
-        return TROP_OK;
+    size_t smem = 0;
+    if ((vec || off) && shape_of(units, V, 16, 1024, j.rows, sm, 8, &nv, &block)) {
+        const int threads = block.x * block.y;
+        const size_t beside = off ? (size_t)5 * nv * block.x * V * we : 0;
+        const size_t stage = (size_t)nv * threads * V * (sizeof(S) + sizeof(U) * (j.gate == GATE_FULL ? 2 : 1));
+        // Of bulk copies one stage a block, more blocks: with two the ring takes the L1 cache that keeps the vectors
+        // (16384x4096, f32 stream beside bf16: 158 us against 186; all f32: 230 against 285).
+        stages = std::min(off ? 2 : 1, stages_of(stage, beside, std::max(1, (off ? 768 : 1024) / threads)));
+        if (stages == 0) stages = std::min(1, stages_of(stage, beside, 1));
+        smem = beside + stages * stage;
     }
-    if (!vec || !shape_of(j.cols / V, V, 16, 1024, j.rows, sm, 8, &nv, &block)) {
+    if (stages == 0) {
         TROP_LAUNCH((k_residual_long<S, U, Y>), dim3((unsigned)j.rows), long_block(j.cols), 0, j);
         return TROP_OK;
     }
-    const dim3 grid((unsigned)((j.rows + block.y - 1) / block.y));
-    const auto kernel = nv == 1          ? k_residual<S, U, Y, V, 1, 1024, false>
-                        : nv * V < 16    ? k_residual<S, U, Y, V, 2, 1024, false>
-                        : block.x <= 512 ? k_residual<S, U, Y, V, 16 / V, 512, false>
-                                         : k_residual<S, U, Y, V, 16 / V, 1024, false>;
-    TROP_LAUNCH(kernel, grid, block, 0, j, 1);
+    ResJob k = j;
+    if (off) k.ku.codes = k.kg.codes = k.kr.codes = nullptr;  // (whose groups lie across these vectors: a pass of their own)
+    const auto kernel = off ? (nv == 1          ? k_residual<S, U, Y, V, 1, 1024, true>
+                               : nv * V < 16    ? k_residual<S, U, Y, V, 2, 1024, true>
+                               : block.x <= 512 ? k_residual<S, U, Y, V, 16 / V, 512, true>
+                                                : k_residual<S, U, Y, V, 16 / V, 1024, true>)
+                            : (nv == 1          ? k_residual<S, U, Y, V, 1, 1024, false>
+                               : nv * V < 16    ? k_residual<S, U, Y, V, 2, 1024, false>
+                               : block.x <= 512 ? k_residual<S, U, Y, V, 16 / V, 512, false>
+                                                : k_residual<S, U, Y, V, 16 / V, 1024, false>);
+    if (smem > PLAIN_SMEM) TROP_TRY(allow_dynamic((const void*)kernel));
+    int64_t blocks = (j.rows + block.y - 1) / block.y;
+    if (blocks > sm) {  // as many as run at once
+        int per_sm = 0;
+        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, (int)(block.x * block.y), smem);
+        if (e != cudaSuccess) return cuda_error(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor(k_residual)");
+        blocks = std::min<int64_t>(blocks, (int64_t)sm * std::max(1, per_sm));
+    }
+    if (off) blocks = std::max<int64_t>(1, blocks / period) * period;
+    uint32_t* error;
+    TROP_TRY(device_error_word(&error));
+    TROP_LAUNCH(kernel, dim3((unsigned)blocks), block, smem, k, period, stages, error);
+    if (off) {
+        if (j.ku.codes) TROP_TRY(launch_pack(j.u, dtype_of<U>(), j.ku, j.rows, j.cols, s));
+        if (j.kg.codes) TROP_TRY(launch_pack(j.g, dtype_of<U>(), j.kg, j.rows, j.cols, s));
+        if (j.kr.codes) TROP_TRY(launch_pack(j.r, dtype_of<S>(), j.kr, j.rows, j.cols, s));
+    }
     return TROP_OK;
 }
 
@@ -1095,14 +1412,16 @@ int residual_backward(ResJob j, JoinJob t, int sm, cudaStream_t s)
 {
     constexpr int V = Types<S, U, Y>::VEC;
     const size_t we = j.wide_w ? 4 : sizeof(Y);
-    Places at = {V, j.rows};
+    Places at = {V, j.rows, j.cols};
     at.add(j.dy, sizeof(Y)), at.add(j.dr, sizeof(S)), at.add(j.dx, sizeof(S)), at.add(j.du, sizeof(U));
     if (j.gate == GATE_FULL) at.add(j.dg, sizeof(U));
     if (!CODED) {
         at.add(j.r, sizeof(S)), at.add(j.u, sizeof(U));
         if (j.gate == GATE_FULL) at.add(j.g, sizeof(U));
+    } else {
+        at.add(j.ku), at.add(j.kg), at.add(j.kr);
     }
-    bool vec = j.cols % V == 0 && at.on() && (!CODED || (on8(j.ku, V, j.rows) && on8(j.kg, V, j.rows) && on8(j.kr, V, j.rows)));
+    bool vec = j.cols % V == 0 && at.on();
     for (const VecAt* a : {&j.w, &j.pw, &j.pb, &j.s}) vec = vec && aligned(a->p, 0, we, V, 1);
     const int period = at.period();
     // eight elements a thread, up to 512 threads; more columns: up to eight CTAs of them
@@ -1115,9 +1434,18 @@ int residual_backward(ResJob j, JoinJob t, int sm, cudaStream_t s)
     if (fits && ctas == 1) shape_of(units, V, 8, 512, j.rows, sm, 4, &nv, &block);
     else if (fits) nv = 8 / V, block = dim3((unsigned)(((units + ctas * nv - 1) / (ctas * nv) + 31) / 32 * 32), 1);
     const size_t vectors = off ? (size_t)5 * nv * block.x * V * we : 0, across = block.y > 1 && j.want ? block.y * (size_t)j.cols * 4 : 0;
-    const size_t smem = std::max(vectors, across);  // (5 x 4096 f32 at most)
-    int64_t blocks = fits ? std::min<int64_t>((j.rows + block.y - 1) / block.y,
-                                              std::max<int64_t>(1, (int64_t)sm / ctas) * std::max<int>(1, 512 / (int)(block.x * block.y)))
+    int stages = 0;
+    size_t smem = 0;
+    const int threads = block.x * block.y, per_sm = fits ? std::max(1, 512 / threads) : 1;
+    if (fits) {
+        const size_t copy = CODED ? (off ? V + 12 : V) : 0, pr = CODED ? copy : V * sizeof(S), pu = CODED ? copy : V * sizeof(U);
+        const size_t stage = (size_t)nv * threads * (V * sizeof(Y) + pr + pu * (j.gate == GATE_FULL ? 2 : 1) + (j.dr.p ? V * sizeof(S) : 0));
+        // (bulk copies: two, for the vectors' sake as above; 16384x4096 f32 337 us against 433 of three)
+        stages = std::min(off ? 4 : 2, stages_of(stage, vectors, per_sm));
+        smem = std::max(vectors + stages * stage, across);
+        fits = stages > (off ? 0 : 1);  // (a bulk ring is filled a row late)
+    }
+    int64_t blocks = fits ? std::min<int64_t>((j.rows + block.y - 1) / block.y, std::max<int64_t>(1, (int64_t)sm / ctas) * per_sm)
                           : std::min<int64_t>(j.rows, std::max<int64_t>(1, (int64_t)sm * 8 * 256 / j.cols));
     if (fits && off) blocks = std::max<int64_t>(1, blocks / period) * period;
     if (j.rows == 0) blocks = 0;  // sums over no rows
@@ -1131,6 +1459,8 @@ int residual_backward(ResJob j, JoinJob t, int sm, cudaStream_t s)
         j.sp_part = span_bytes(j.part, part);
         j.sp_sums = span_bytes(j.sums, sums);
     }
+    uint32_t* error = nullptr;
+    if (fits) TROP_TRY(device_error_word(&error));
     if (j.rows == 0) {
     } else if (!fits) {
         if (j.dx.p || j.du.p || j.dg.p || j.sums)
@@ -1141,7 +1471,7 @@ int residual_backward(ResJob j, JoinJob t, int sm, cudaStream_t s)
         const auto kernel = off ? (nv == 1 ? k_residual_back<S, U, Y, V, 1, CODED, true, false> : k_residual_back<S, U, Y, V, 8 / V, CODED, true, false>)
                                 : (nv == 1 ? k_residual_back<S, U, Y, V, 1, CODED, false, false> : k_residual_back<S, U, Y, V, 8 / V, CODED, false, false>);
         if (smem > PLAIN_SMEM) TROP_TRY(allow_dynamic((const void*)kernel));
-        TROP_LAUNCH(kernel, dim3((unsigned)blocks), block, smem, j, period);
+        TROP_LAUNCH(kernel, dim3((unsigned)blocks), block, smem, j, period, stages, error);
     } else {
         const auto kernel = off ? k_residual_back<S, U, Y, V, 8 / V, CODED, true, true> : k_residual_back<S, U, Y, V, 8 / V, CODED, false, true>;
         if (smem > PLAIN_SMEM) TROP_TRY(allow_dynamic((const void*)kernel));
@@ -1158,7 +1488,7 @@ int residual_backward(ResJob j, JoinJob t, int sm, cudaStream_t s)
         attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 2;
-        const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, j, period);
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, j, period, stages, error);
         if (e != cudaSuccess) return cuda_error(e, "k_residual_back launch");
         count_launches(1);
     }

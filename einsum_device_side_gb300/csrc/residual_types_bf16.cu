@@ -3,7 +3,7 @@
 #include "residual_norm.cuh"
 
 namespace trop {
-template int residual_forward<bf16, bf16, bf16>(const ResJob&, int, cudaStream_t);
+template int residual_forward<bf16, bf16, bf16>(ResJob, int, cudaStream_t);
 template int residual_backward<bf16, bf16, bf16, false>(ResJob, JoinJob, int, cudaStream_t);
 template int residual_backward<bf16, bf16, bf16, true>(ResJob, JoinJob, int, cudaStream_t);
 }  // namespace trop

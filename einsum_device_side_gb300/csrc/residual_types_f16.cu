@@ -3,7 +3,7 @@
 #include "residual_norm.cuh"
 
 namespace trop {
-template int residual_forward<__half, __half, __half>(const ResJob&, int, cudaStream_t);
+template int residual_forward<__half, __half, __half>(ResJob, int, cudaStream_t);
 template int residual_backward<__half, __half, __half, false>(ResJob, JoinJob, int, cudaStream_t);
 template int residual_backward<__half, __half, __half, true>(ResJob, JoinJob, int, cudaStream_t);
 }  // namespace trop

@@ -3,7 +3,7 @@
 #include "residual_norm.cuh"
 
 namespace trop {
-template int residual_forward<float, float, float>(const ResJob&, int, cudaStream_t);
+template int residual_forward<float, float, float>(ResJob, int, cudaStream_t);
 template int residual_backward<float, float, float, false>(ResJob, JoinJob, int, cudaStream_t);
 template int residual_backward<float, float, float, true>(ResJob, JoinJob, int, cudaStream_t);
 }  // namespace trop

@@ -3,7 +3,7 @@
 #include "residual_norm.cuh"
 
 namespace trop {
-template int residual_forward<float, float, bf16>(const ResJob&, int, cudaStream_t);
+template int residual_forward<float, float, bf16>(ResJob, int, cudaStream_t);
 template int residual_backward<float, float, bf16, false>(ResJob, JoinJob, int, cudaStream_t);
 template int residual_backward<float, float, bf16, true>(ResJob, JoinJob, int, cudaStream_t);
 }  // namespace trop

@@ -3,7 +3,7 @@
 #include "residual_norm.cuh"
 
 namespace trop {
-template int residual_forward<float, float, __half>(const ResJob&, int, cudaStream_t);
+template int residual_forward<float, float, __half>(ResJob, int, cudaStream_t);
 template int residual_backward<float, float, __half, false>(ResJob, JoinJob, int, cudaStream_t);
 template int residual_backward<float, float, __half, true>(ResJob, JoinJob, int, cudaStream_t);
 }  // namespace trop
