@@ -15,7 +15,7 @@ from torch.autograd.function import once_differentiable
 
 import einsum_device_side_gb300 as _pkg
 
-from .train import _CODES, _call, _check_vector, _desc, _fail, _lib, _on_stream, _ptr, _result, _result_rows, _rows
+from .train import _CODES, _call, _check_vector, _desc, _fail, _fast, _lib, _on_stream, _ptr, _result, _result_rows, _rows
 
 GROUP = 32  # elements of a row that share one scale of an 8-bit copy
 
@@ -25,7 +25,9 @@ def _new_codes(shape, device):
     kernel that reads them, whatever C is."""
     groups = -(-shape[-1] // GROUP)
     codes = torch.empty((*shape[:-1], groups * GROUP), dtype=torch.int8, device=device)
-    return codes[..., :shape[-1]], torch.empty((*shape[:-1], groups), dtype=torch.uint8, device=device)
+    if codes.shape[-1] != shape[-1]:
+        codes = codes[..., :shape[-1]]
+    return codes, torch.empty((*shape[:-1], groups), dtype=torch.uint8, device=device)
 
 
 def _kept_rows(codes, scales, name: str):
@@ -49,9 +51,15 @@ def activation_pack(x: torch.Tensor, stream=None):
     A group with an infinity or a NaN reads back as NaN."""
     if stream is not None:
         return _on_stream(activation_pack, stream, x)
+    fc, codes = _fast(), None
+    if fc is not None and x.dim() > 1:
+        codes, scales = _new_codes(x.shape, x.device)
+        if fc.activation_pack_t(x, codes, scales) == 0:  # the usual call
+            return codes, scales
     lib = _lib()
     x2 = _rows(x, "x")
-    codes, scales = _new_codes(x.shape, x.device)
+    if codes is None:
+        codes, scales = _new_codes(x.shape, x.device)
     n, c = x2.shape
     _pkg._check(lib.tropical_activation_pack(_desc(x2), _desc(_result_rows(codes, n, c, "codes")),
                                              _desc(scales.view(n, -(-c // GROUP))), _pkg._stream(None, x)))
@@ -63,9 +71,12 @@ def activation_values(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dt
     where they lie in its range)."""
     if stream is not None:
         return _on_stream(activation_values, stream, codes, scales, dtype)
+    fc = _fast()
+    out = torch.empty(codes.shape, dtype=dtype, device=codes.device)
+    if fc is not None and codes.shape[:-1] == scales.shape[:-1] and fc.activation_values_t(codes, scales, out) == 0:  # the usual call
+        return out
     lib = _lib()
     k2, s2 = _kept_rows(codes, scales, "codes")
-    out = torch.empty(codes.shape, dtype=dtype, device=codes.device)
     _pkg._check(lib.tropical_activation_values(_desc(k2), _desc(s2), _desc(out.view(k2.shape)), _pkg._stream(None, codes)))
     return out
 
@@ -80,6 +91,12 @@ def activation_weight_grad(dy: torch.Tensor, codes: torch.Tensor, scales: torch.
     float32; results have dy's type or float32 (``out_dtype``)."""
     if stream is not None:
         return _on_stream(activation_weight_grad, stream, dy, codes, scales, out_dtype, want_bias)
+    fc = _fast()
+    if fc is not None and dy.dim() == 2 and codes.dim() == 2 and dy.shape[0] == codes.shape[0] == scales.shape[0]:  # the usual call
+        dw = torch.empty((dy.shape[1], codes.shape[1]), dtype=out_dtype or dy.dtype, device=dy.device)
+        db = torch.empty(dy.shape[1], dtype=dw.dtype, device=dy.device) if want_bias else None
+        if fc.activation_weight_grad_t(dy, codes, scales, dw, db) == 0:
+            return dw, db
     lib = _lib()
     k2, s2 = _kept_rows(codes, scales, "codes")
     if codes.shape[:-1] != dy.shape[:-1]:
@@ -149,18 +166,24 @@ def _pointer(t):
     return None if d is None else ctypes.pointer(d._obj)
 
 
-def _options(like, c, weight, bias, post_weight, post_bias, scale, post_norm, norm, gate_act, alpha, eps, wdtype):
-    """The C options, and the vectors' type."""
+def _options(weight, bias, post_weight, post_bias, scale, post_norm, norm, gate_act, alpha, eps):
+    """The options' values in the order that the bindings take them; the vectors as they were given."""
     if norm not in _NORMS or gate_act not in _ACTS:
         _fail(-1, f"norm must be one of {tuple(_NORMS)}, gate_act one of {tuple(_ACTS)}, got {norm!r} and {gate_act!r}")
     vector = scale if isinstance(scale, torch.Tensor) else None
-    given = [v for v in (weight, bias, post_weight, post_bias, vector) if v is not None]
-    wdtype = given[0].dtype if given else wdtype
-    for v, name in ((weight, "weight"), (bias, "bias"), (post_weight, "post_weight"), (post_bias, "post_bias"), (vector, "scale")):
+    return (_NORMS[norm], 1 if post_norm else 0, _ACTS[gate_act], alpha, 1.0 if scale is None or vector is not None else scale, eps,
+            weight, bias, post_weight, post_bias, vector)
+
+
+def _options_struct(values, like, c, wdtype):
+    """The C options, their vectors checked."""
+    for v, name in zip(values[6:], ("weight", "bias", "post_weight", "post_bias", "scale")):
         _check_vector(v, name, like, wdtype, c)
-    return _Options(_NORMS[norm], bool(post_norm), _ACTS[gate_act], _CODES.get(wdtype, -1), alpha,
-                    1.0 if scale is None or vector is not None else scale, eps, _ptr(weight), _ptr(bias), _ptr(post_weight),
-                    _ptr(post_bias), _ptr(vector)), wdtype
+    return _Options(*values[:3], _CODES.get(wdtype, -1), *values[3:6], *map(_ptr, values[6:]))
+
+
+def _vector_type(values, otherwise):
+    return next((v.dtype for v in values[6:] if v is not None), otherwise)
 
 
 def _beside(t, name: str, like, shape):
@@ -206,20 +229,28 @@ def residual_norm(x: torch.Tensor, u: torch.Tensor, weight: torch.Tensor | None 
         return _on_stream(residual_norm, stream, x, u, weight, bias, gate=gate, gate_act=gate_act, scale=scale,
                           post_weight=post_weight, post_bias=post_bias, post_norm=post_norm, norm=norm, alpha=alpha, eps=eps,
                           out_dtype=out_dtype, keep=keep)
-    lib = _lib()
-    x2, u2 = _rows(x, "x"), _rows(u, "u")
-    n, c = x2.shape
-    _beside(u, "u", x, x.shape)
-    g2 = _gate_rows(gate, x, x.shape)
-    o, _ = _options(x, c, weight, bias, post_weight, post_bias, scale, post_norm, norm, gate_act, alpha, eps, x.dtype)
+    values = _options(weight, bias, post_weight, post_bias, scale, post_norm, norm, gate_act, alpha, eps)
+    if x.dim() == 0:
+        _fail(-1, "x has no axis")
+    c = x.shape[-1]
+    full = gate is not None and gate.dim() > 0 and gate.shape[-1] == c
     y, r = _result(u, out_dtype), _result(x)
     stats = torch.empty((4, *x.shape[:-1]), dtype=torch.float32, device=x.device)
-    kept = table = None
+    kept, copies = None, (None,) * 6
     if keep:
-        full = gate is not None and gate.shape[-1] == c
         ku, kr = _new_codes(x.shape, x.device), _new_codes(x.shape, x.device)
         kg = _new_codes(x.shape, x.device) if full else gate
-        kept, (table, _) = (ku, kg, kr), _kept_table(ku, kg if full else None, kr)
+        kept, copies = (ku, kg, kr), (*ku, *(kg if full else (None, None)), *kr)
+    fc = _fast()
+    if fc is not None and fc.residual_norm_t(*values, x, u, gate, y, r, stats, *copies) == 0:  # the usual call
+        return y, r, stats, kept
+    lib = _lib()
+    x2, u2 = _rows(x, "x"), _rows(u, "u")
+    n = x2.shape[0]
+    _beside(u, "u", x, x.shape)
+    g2 = _gate_rows(gate, x, x.shape)
+    o = _options_struct(values, x, c, _vector_type(values, x.dtype))
+    table, _held = _kept_table(ku, kg if full else None, kr) if keep else (None, None)
     _pkg._check(lib.tropical_residual_norm(ctypes.byref(o), _desc(x2), _desc(u2), _desc(g2), _desc(_result_rows(y, n, c, "y")),
                                            _desc(_result_rows(r, n, c, "r")), _ptr(stats), table, _pkg._stream(None, x)))
     return y, r, stats, kept
@@ -255,46 +286,59 @@ def residual_norm_backward(dy: torch.Tensor, dr: torch.Tensor | None, r, u, stat
         return _on_stream(residual_norm_backward, stream, dy, dr, r, u, stats, weight, bias, gate=gate, gate_act=gate_act,
                           scale=scale, post_weight=post_weight, post_bias=post_bias, post_norm=post_norm, norm=norm,
                           alpha=alpha, want=want, x_dtype=x_dtype, u_dtype=u_dtype)
-    lib = _lib()
+    values = _options(weight, bias, post_weight, post_bias, scale, post_norm, norm, gate_act, alpha, 0.0)
     want = _GRADS if want is None else want
-    dy2 = _rows(dy, "dy")
-    n, c = dy2.shape
-    shape, lead = dy.shape, dy.shape[:-1]
-    copies = isinstance(r, tuple)
+    shape = dy.shape
+    if not shape:
+        _fail(-1, "dy has no axis")
+    c = shape[-1]
+    copies, coded = isinstance(r, tuple), isinstance(gate, tuple)
     if copies != isinstance(u, tuple):
         _fail(-1, "r and u are both 8-bit copies, or neither is")
-    g2 = table = r2 = u2 = None
+    if coded and not copies:
+        _fail(-1, "the gate's 8-bit copy without r's and u's")
     if copies:
-        coded = isinstance(gate, tuple)
-        for pair, name in ((r, "r"), (u, "u"), (gate if coded else r, "gate")):
-            _beside(pair[0], name, dy, shape)
-        table, held = _kept_table(u, gate if coded else None, r)
-        if not coded:
-            g2 = _gate_rows(gate, dy, shape)
         x_dtype = x_dtype or (dr.dtype if dr is not None else dy.dtype)
         u_dtype = u_dtype or dy.dtype
     else:
-        if isinstance(gate, tuple):
-            _fail(-1, "the gate's 8-bit copy without r's and u's")
+        x_dtype, u_dtype = r.dtype, u.dtype
+    wdtype = _vector_type(values, dy.dtype)
+    new = lambda name, dtype, cols=c: torch.empty((*shape[:-1], cols), dtype=dtype, device=dy.device) if name in want else None  # noqa: E731
+    vec = lambda name, v: torch.empty(c, dtype=wdtype, device=dy.device) if v is not None and name in want else None  # noqa: E731
+    dx, du = new("x", x_dtype), new("u", u_dtype)
+    dgate = None if gate is None else new("gate", u_dtype, (gate[0] if coded else gate).shape[-1])
+    vectors = [vec("scale", values[10]), vec("weight", weight), vec("bias", bias), vec("post_weight", post_weight),
+               vec("post_bias", post_bias)]
+    plain = None if coded else gate
+    types = _CODES.get(x_dtype, -1), _CODES.get(u_dtype, -1)
+    fc = _fast()
+    if fc is not None:
+        given = (None, None, plain) if copies else (r, u, plain)
+        kept = (*u, *(gate if coded else (None, None)), *r) if copies else (None,) * 6
+        if fc.residual_norm_backward_t(*values, dy, dr, *given, stats, *kept, dx, du, dgate, *vectors, *types) == 0:  # the usual call
+            return dx, du, dgate, *vectors
+    lib = _lib()
+    dy2 = _rows(dy, "dy")
+    n = dy2.shape[0]
+    r2 = u2 = table = None
+    if copies:
+        for pair, name in ((r, "r"), (u, "u"), (gate if coded else r, "gate")):
+            _beside(pair[0], name, dy, shape)
+        table, _held = _kept_table(u, gate if coded else None, r)
+    else:
         _beside(r, "r", dy, shape)
         _beside(u, "u", dy, shape)
-        r2, u2, g2 = _rows(r, "r"), _rows(u, "u"), _gate_rows(gate, dy, shape)
-        x_dtype, u_dtype = r.dtype, u.dtype
+        r2, u2 = _rows(r, "r"), _rows(u, "u")
+    g2 = _gate_rows(plain, dy, shape)
     if dr is not None:
         _beside(dr, "dr", dy, shape)
     _check_vector(stats.reshape(-1), "stats", dy, torch.float32, 4 * n)
-    o, wdtype = _options(dy, c, weight, bias, post_weight, post_bias, scale, post_norm, norm, gate_act, alpha, 0.0, dy.dtype)
-    new = lambda name, dtype, cols=c: torch.empty((*lead, cols), dtype=dtype, device=dy.device) if name in want else None  # noqa: E731
-    vec = lambda name, v: torch.empty(c, dtype=wdtype, device=dy.device) if v is not None and name in want else None  # noqa: E731
-    dx, du = new("x", x_dtype), new("u", u_dtype)
-    dgate = None if gate is None else new("gate", u_dtype, gate[0].shape[-1] if copies and coded else gate.shape[-1])
-    vectors = [vec("scale", scale if isinstance(scale, torch.Tensor) else None), vec("weight", weight), vec("bias", bias),
-               vec("post_weight", post_weight), vec("post_bias", post_bias)]
+    o = _options_struct(values, dy, c, wdtype)
     dr2, stats = None if dr is None else _rows(dr, "dr"), stats.contiguous()
     flat = lambda t: None if t is None else _pointer(t.view(n, t.shape[-1]))  # noqa: E731
     grads = _Grads(flat(dx), flat(du), flat(dgate), *[_ptr(v) for v in vectors])
-    _pkg._check(_call(lib.tropical_residual_norm_backward, ctypes.byref(o), _desc(dy2),
-                      _desc(dr2), _desc(r2), _desc(u2), _desc(g2), _ptr(stats), table, _CODES.get(x_dtype, -1), _CODES.get(u_dtype, -1), ctypes.byref(grads), _pkg._stream(None, dy)))
+    _pkg._check(_call(lib.tropical_residual_norm_backward, ctypes.byref(o), _desc(dy2), _desc(dr2), _desc(r2), _desc(u2),
+                      _desc(g2), _ptr(stats), table, *types, ctypes.byref(grads), _pkg._stream(None, dy)))
     return dx, du, dgate, *vectors
 
 

@@ -696,6 +696,215 @@ static PyObject* fc_adamw_plan_values(PyObject* self, PyObject* const* a, Py_ssi
     return PyLong_FromLong(rc);
 }
 
+/* ---- operators of a residual block.  Their results are allocated by the Python wrapper, which goes through its own
+ * checks and the plain path wherever one of these returns anything but 0. */
+
+/* a matrix on `device` (rows merged): 0, PLAIN_PATH, or -1 */
+static int obj_rows(PyObject* obj, long device, trop_tensor* t)
+{
+    if (obj_tensor_of(t, obj, N_DTYPES) < 0) return -1;
+    const long d = obj_device(obj);
+    return d == -2 ? -1 : d != device || d < 0 || as_rows(t) ? PLAIN_PATH : 0;
+}
+#define ROWS(obj, t)                                          \
+    do {                                                      \
+        const int v_ = obj_rows((obj), device, (t));          \
+        if (v_ < 0) return NULL;                              \
+        if (v_ > 0) return PyLong_FromLong(PLAIN_PATH);       \
+    } while (0)
+
+/* activation_pack_t(x, codes, scales), activation_values_t(codes, scales, x) */
+static PyObject* activation_t(PyObject* const* a, Py_ssize_t nargs, int pack)
+{
+    if (check_nargs(nargs, 3, pack ? "activation_pack_t" : "activation_values_t") < 0) return NULL;
+    trop_tensor x, codes, scales;
+    void* stream;
+    PyObject *ox = a[pack ? 0 : 2], *oc = a[pack ? 1 : 0], *os = a[pack ? 2 : 1];
+    const long device = obj_device(ox);
+    if (device == -2 || obj_stream(Py_None, ox, &stream) < 0) return NULL;
+    ROWS(ox, &x);
+    ROWS(oc, &codes);
+    ROWS(os, &scales);
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = pack ? tropical_activation_pack(&x, &codes, &scales, stream) : tropical_activation_values(&codes, &scales, &x, stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+static PyObject* fc_activation_pack_t(PyObject* self, PyObject* const* a, Py_ssize_t nargs)
+{
+    (void)self;
+    return activation_t(a, nargs, 1);
+}
+static PyObject* fc_activation_values_t(PyObject* self, PyObject* const* a, Py_ssize_t nargs)
+{
+    (void)self;
+    return activation_t(a, nargs, 0);
+}
+
+/* activation_weight_grad_t(dy, codes, scales, dw, db or None) */
+static PyObject* fc_activation_weight_grad_t(PyObject* self, PyObject* const* a, Py_ssize_t nargs)
+{
+    (void)self;
+    if (check_nargs(nargs, 5, "activation_weight_grad_t") < 0) return NULL;
+    trop_tensor dy, codes, scales, dw;
+    void *db, *stream;
+    const long device = obj_device(a[0]);
+    if (device == -2 || obj_stream(Py_None, a[0], &stream) < 0 || obj_ptr(a[4], &db) < 0) return NULL;
+    ROWS(a[0], &dy);
+    ROWS(a[1], &codes);
+    ROWS(a[2], &scales);
+    ROWS(a[3], &dw);
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = tropical_activation_weight_grad(&dy, &codes, &scales, &dw, db, stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
+/* The options (norm, post_norm, gate_act, alpha, scale, eps, weight, bias, post_weight, post_bias, scale vector) at a[0..10], the
+ * vectors each a tensor or None and of one type (y's where there is none): 0, PLAIN_PATH, or -1 */
+static int residual_options(PyObject* const* a, int64_t n, int32_t dtype, long device, trop_residual_options* o)
+{
+    int64_t v[3];
+    for (int i = 0; i < 3; ++i)
+        if (as_i64(a[i], &v[i]) < 0) return -1;
+    if (as_double(a[3], &o->alpha) < 0 || as_double(a[4], &o->scale) < 0 || as_double(a[5], &o->eps) < 0) return -1;
+    int32_t wdtype = dtype;
+    for (int i = 10; i >= 6; --i) wdtype = dtype_or(a[i], wdtype);
+    if (wdtype == -2) return -1;
+    void* p[5];
+    for (int i = 0; i < 5; ++i) {
+        const int rc = obj_vector(a[6 + i], n, wdtype, device, &p[i]);
+        if (rc != 0) return rc;
+    }
+    o->norm = (int)v[0], o->post_norm = (int)v[1], o->gate_act = (int)v[2], o->wdtype = wdtype;
+    o->weight = p[0], o->bias = p[1], o->post_weight = p[2], o->post_bias = p[3], o->scale_vector = p[4];
+    return 0;
+}
+#define OPTIONS(a, n, dtype, o)                                             \
+    do {                                                                    \
+        const int v_ = residual_options((a), (n), (dtype), device, (o));    \
+        if (v_ < 0) return NULL;                                            \
+        if (v_ > 0) return PyLong_FromLong(PLAIN_PATH);                     \
+    } while (0)
+
+/* u's, the gate's and r's 8-bit copies at a[0..5] (codes, scales; None: not kept) */
+static int residual_kept(PyObject* const* a, long device, trop_tensor* t, trop_kept* kept)
+{
+    for (int i = 0; i < 3; ++i) {
+        kept[i].codes = kept[i].scales = NULL;
+        if (a[2 * i] == Py_None) continue;
+        int rc = obj_rows(a[2 * i], device, &t[2 * i]);
+        if (rc == 0) rc = obj_rows(a[2 * i + 1], device, &t[2 * i + 1]);
+        if (rc != 0) return rc;
+        kept[i].codes = &t[2 * i];
+        kept[i].scales = &t[2 * i + 1];
+    }
+    return 0;
+}
+#define KEPT(a, t, kept)                                      \
+    do {                                                      \
+        const int v_ = residual_kept((a), device, (t), (kept)); \
+        if (v_ < 0) return NULL;                              \
+        if (v_ > 0) return PyLong_FromLong(PLAIN_PATH);       \
+    } while (0)
+
+/* two tensor objects of one shape, or (but > 0) of one but for `but` in the last place: 0, PLAIN_PATH, or -1 */
+static int same_shape(PyObject* p, PyObject* q, int64_t but)
+{
+    PyObject* s = PyObject_GetAttr(p, s_shape);
+    PyObject* t = s ? PyObject_GetAttr(q, s_shape) : NULL;
+    int rc = t ? 0 : -1;
+    if (rc == 0) {
+        const Py_ssize_t n = PyTuple_Check(s) && PyTuple_Check(t) ? PyTuple_GET_SIZE(s) : -1;
+        if (n < 1 || PyTuple_GET_SIZE(t) != n) rc = PLAIN_PATH;
+        for (Py_ssize_t i = 0; i < n && rc == 0; ++i) {
+            int64_t x, y;
+            if (as_i64(PyTuple_GET_ITEM(s, i), &x) < 0 || as_i64(PyTuple_GET_ITEM(t, i), &y) < 0) rc = -1;
+            else if (x != y && !(i == n - 1 && but > 0 && y == but)) rc = PLAIN_PATH;
+        }
+    }
+    Py_XDECREF(s);
+    Py_XDECREF(t);
+    return rc;
+}
+#define SAME(p, q, but)                                       \
+    do {                                                      \
+        const int v_ = same_shape((p), (q), (but));           \
+        if (v_ < 0) return NULL;                              \
+        if (v_ > 0) return PyLong_FromLong(PLAIN_PATH);       \
+    } while (0)
+
+/* residual_norm_t(options x11, x, u, gate or None, y, r, stats, copies x6) */
+static PyObject* fc_residual_norm_t(PyObject* self, PyObject* const* a, Py_ssize_t nargs)
+{
+    (void)self;
+    if (check_nargs(nargs, 23, "residual_norm_t") < 0) return NULL;
+    trop_tensor x, u, g, y, r, t[6];
+    trop_residual_options o;
+    trop_kept kept[3];
+    void *stats, *stream;
+    const long device = obj_device(a[11]);
+    if (device == -2 || obj_stream(Py_None, a[11], &stream) < 0 || obj_ptr(a[16], &stats) < 0) return NULL;
+    SAME(a[11], a[12], 0);
+    if (a[13] != Py_None) SAME(a[11], a[13], 1);
+    ROWS(a[11], &x);
+    ROWS(a[12], &u);
+    if (a[13] != Py_None) ROWS(a[13], &g);
+    ROWS(a[14], &y);
+    ROWS(a[15], &r);
+    OPTIONS(a, x.shape[1], x.dtype, &o);
+    KEPT(a + 17, t, kept);
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = tropical_residual_norm(&o, &x, &u, a[13] == Py_None ? NULL : &g, &y, &r, (float*)stats, a[17] == Py_None ? NULL : kept, stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
+/* residual_norm_backward_t(options x11, dy, dr, r, u, gate, stats, copies x6, dx, du, dgate, dscale, dweight, dbias, dpost_weight,
+ * dpost_bias, x's dtype, u's dtype): None where a tensor is not given or not wanted */
+static PyObject* fc_residual_norm_backward_t(PyObject* self, PyObject* const* a, Py_ssize_t nargs)
+{
+    (void)self;
+    if (check_nargs(nargs, 33, "residual_norm_backward_t") < 0) return NULL;
+    trop_tensor in[5], t[6], out[3];
+    trop_residual_options o;
+    trop_residual_grads grads;
+    trop_kept kept[3];
+    void *stats, *stream, *v[5];
+    const long device = obj_device(a[11]);
+    if (device == -2 || obj_stream(Py_None, a[11], &stream) < 0) return NULL;
+    for (int i = 0; i < 5; ++i) {
+        if (a[11 + i] == Py_None) continue;
+        SAME(a[11], a[11 + i], i == 4 ? 1 : 0);
+        ROWS(a[11 + i], &in[i]);
+    }
+    for (int i = 0; i < 3; ++i) {
+        if (a[17 + 2 * i] != Py_None) SAME(a[11], a[17 + 2 * i], 0);
+        if (a[23 + i] != Py_None) ROWS(a[23 + i], &out[i]);
+    }
+    VECTOR(a[16], 4 * in[0].shape[0], TROP_F32, &stats);
+    OPTIONS(a, in[0].shape[1], in[0].dtype, &o);
+    KEPT(a + 17, t, kept);
+    for (int i = 0; i < 5; ++i)
+        if (obj_ptr(a[26 + i], &v[i]) < 0) return NULL;
+    grads.dx = a[23] == Py_None ? NULL : &out[0];
+    grads.du = a[24] == Py_None ? NULL : &out[1];
+    grads.dgate = a[25] == Py_None ? NULL : &out[2];
+    grads.dscale = v[0], grads.dweight = v[1], grads.dbias = v[2], grads.dpost_weight = v[3], grads.dpost_bias = v[4];
+    int64_t xt, ut;
+    if (as_i64(a[31], &xt) < 0 || as_i64(a[32], &ut) < 0) return NULL;
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = tropical_residual_norm_backward(&o, &in[0], a[12] == Py_None ? NULL : &in[1], a[13] == Py_None ? NULL : &in[2],
+                                         a[14] == Py_None ? NULL : &in[3], a[15] == Py_None ? NULL : &in[4], (const float*)stats,
+                                         a[17] == Py_None ? NULL : kept, (int)xt, (int)ut, &grads, stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
 static PyObject* fc_last_error(PyObject* self, PyObject* const* a, Py_ssize_t nargs)
 {
     (void)self;
@@ -733,6 +942,11 @@ static PyMethodDef methods[] = {
      "tropical_linear_cross_entropy_backward on tensor objects"},
     {"adamw_plan_step", (PyCFunction)(void (*)(void))fc_adamw_plan_step, METH_FASTCALL, "tropical_adamw_plan_step"},
     {"adamw_plan_values", (PyCFunction)(void (*)(void))fc_adamw_plan_values, METH_FASTCALL, "tropical_adamw_plan_values"},
+    {"activation_pack_t", (PyCFunction)(void (*)(void))fc_activation_pack_t, METH_FASTCALL, "tropical_activation_pack on tensor objects"},
+    {"activation_values_t", (PyCFunction)(void (*)(void))fc_activation_values_t, METH_FASTCALL, "tropical_activation_values on tensor objects"},
+    {"activation_weight_grad_t", (PyCFunction)(void (*)(void))fc_activation_weight_grad_t, METH_FASTCALL, "tropical_activation_weight_grad on tensor objects"},
+    {"residual_norm_t", (PyCFunction)(void (*)(void))fc_residual_norm_t, METH_FASTCALL, "tropical_residual_norm on tensor objects"},
+    {"residual_norm_backward_t", (PyCFunction)(void (*)(void))fc_residual_norm_backward_t, METH_FASTCALL, "tropical_residual_norm_backward on tensor objects"},
     {NULL, NULL, 0, NULL},
 };
 
