@@ -87,16 +87,23 @@ __device__ __forceinline__ void codes8(const Raw<T, VEC>& q, uint32_t e, uint32_
 }
 
 // Code i of a word as an f32: its byte, with the sign bit turned, under 2^23 is 2^23 + 128 + code.
-__device__ __forceinline__ float coded8(uint32_t turned, int i)
-{
-    return __uint_as_float(__byte_perm(turned, 0x4b000000u, 0x7540 + i)) - 8388736.f;
-}
+__device__ __forceinline__ float raised8(uint32_t turned, int i) { return __uint_as_float(__byte_perm(turned, 0x4b000000u, 0x7540 + i)); }
+__device__ __forceinline__ float coded8(uint32_t turned, int i) { return raised8(turned, i) - 8388736.f; }
 // VEC codes' values
 template <int VEC>
 __device__ __forceinline__ void values8(const uint32_t (&w)[(VEC + 3) / 4], float unit, float (&v)[VEC])
 {
+    if constexpr (VEC == 1) {
+        v[0] = coded8(w[0] ^ 0x80808080u, 0) * unit;
+    } else {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = coded8(w[i / 4] ^ 0x80808080u, i % 4) * unit;
+        for (int i = 0; i < VEC; i += 2) {  // in packed pairs
+            const uint32_t t = w[i / 4] ^ 0x80808080u;
+            const float2 p = __fmul2_rn(__fadd2_rn(make_float2(raised8(t, i % 4), raised8(t, i % 4 + 1)), make_float2(-8388736.f, -8388736.f)),
+                                        make_float2(unit, unit));
+            v[i] = p.x, v[i + 1] = p.y;
+        }
+    }
 }
 
 // VEC codes in one access

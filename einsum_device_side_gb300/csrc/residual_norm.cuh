@@ -126,29 +126,24 @@ __device__ __forceinline__ void put(const RowsAt& a, uint32_t row, int c, const 
     put<T, VEC, OFF>(a, row, c, q, cols);
 }
 
-// VEC elements of a vector over the columns: f32, or of type T; `none` where it is absent, zero outside the row.  OFF: from
-// the block's shared copy, moved by the offset.
-template <typename T, int VEC, bool OFF>
+// VEC elements of a vector over the columns: f32, or of type T; `none` where it is absent, zero outside the row.  SHARED: from
+// the block's shared copies (five, in the order of the job's), moved by the row's offset.  They spare the address and the checks of
+// every row's five loads; 32-bit vectors of on-grid rows stay in L1, which has the room that the copies would take.
+template <typename T, int VEC, bool OFF, bool SHARED>
 struct Vectors {
     const uint8_t* shared;
     int span;  // bytes of one
-    __device__ __forceinline__ void get(int which, const VecAt& a, int k, int c, const ResJob& j, float none, Pair<VEC> (&o)[pairs<VEC>]) const
+    template <typename V>
+    __device__ __forceinline__ void read(const V* p, float (&v)[VEC]) const
     {
-        float v[VEC];
-        if (OFF) {
-            const int at = (k * blockDim.x + threadIdx.x) * VEC;
-            if (j.wide_w) {
-                Raw<float, VEC> q;
-                q.read((const float*)(shared + which * span) + at);
+        Raw<V, VEC> q;
+        q.read(p);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) v[i] = q.get(i);
-            } else {
-                Raw<T, VEC> q;
-                q.read((const T*)(shared + which * span) + at);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) v[i] = q.get(i);
-            }
-        } else if (!a.p || c >= (int)j.cols) {
+        for (int i = 0; i < VEC; ++i) v[i] = q.get(i);
+    }
+    __device__ __forceinline__ void fetch(const VecAt& a, int c, const ResJob& j, float none, float (&v)[VEC]) const
+    {
+        if (!a.p || c >= (int)j.cols) {
 #pragma unroll
             for (int i = 0; i < VEC; ++i) v[i] = c < (int)j.cols ? none : 0.f;
         } else if (j.wide_w) {
@@ -156,31 +151,67 @@ struct Vectors {
         } else {
             load<T, VEC>((const T*)a.p + c, v, a.sp);
         }
+    }
+    __device__ __forceinline__ void get(int which, const VecAt& a, int k, int c, const ResJob& j, float none, Pair<VEC> (&o)[pairs<VEC>]) const
+    {
+        float v[VEC];
+        if (SHARED) {
+            const int at = (k * blockDim.x + threadIdx.x) * VEC;
+            if (j.wide_w) read((const float*)(shared + which * span) + at, v);
+            else read((const T*)(shared + which * span) + at, v);
+        } else {
+            fetch(a, c, j, none, v);
+        }
 #pragma unroll
         for (int i = 0; i < pairs<VEC>; ++i) o[i] = pair_at<VEC>(v, i);
     }
     // all of the block; five of NV * blockDim.x vectors each
     template <int NV>
-    __device__ __forceinline__ void init(uint8_t* dyn, int off, const ResJob& j, const VecAt (&all)[5], const float (&none)[5])
+    __device__ __forceinline__ void init(uint8_t* dyn, int off, const ResJob& j)
     {
         shared = dyn;
         span = NV * blockDim.x * VEC * (j.wide_w ? 4 : (int)sizeof(T));
-        if constexpr (OFF) {
-            for (int which = 0; which < 5; ++which)
-                for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < NV * VEC * (int)blockDim.x; i += blockDim.x * blockDim.y) {
-                    const int c = i - off;
-                    const bool in = c >= 0 && c < (int)j.cols;
+        if constexpr (!SHARED) return;
+        const VecAt all[5] = {j.w, j.b, j.pw, j.pb, j.s};
+        const float none[5] = {1.f, 0.f, 1.f, 0.f, 1.f};
+        if constexpr (!OFF) {
+            if (threadIdx.y == 0)
+#pragma unroll
+                for (int which = 0; which < 5; ++which)
+#pragma unroll
+                    for (int k = 0; k < NV; ++k) {
+                        float v[VEC];
+                        fetch(all[which], column<VEC>(k, off), j, none[which], v);
+                        const int at = (k * blockDim.x + threadIdx.x) * VEC;
+                        if (j.wide_w) {
+                            Raw<float, VEC> q;
+                            q.set(v);
+                            q.write((float*)(dyn + which * span) + at);
+                        } else {
+                            Raw<T, VEC> q;
+                            q.set(v);
+                            q.write((T*)(dyn + which * span) + at);
+                        }
+                    }
+        } else {
+            for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < NV * VEC * (int)blockDim.x; i += blockDim.x * blockDim.y) {
+                const int c = i - off;
+                const bool in = c >= 0 && c < (int)j.cols;
+                float v[5];
+#pragma unroll
+                for (int which = 0; which < 5; ++which) {
                     const VecAt& a = all[which];
-                    if (j.wide_w)
-                        ((float*)(dyn + which * span))[i] =
-                            !in ? 0.f : !a.p ? none[which] : TROP_IN((const float*)a.p + c, 4, a.sp) ? ((const float*)a.p)[c] : 0.f;
-                    else
-                        ((T*)(dyn + which * span))[i] = !in || (a.p && !TROP_IN((const T*)a.p + c, sizeof(T), a.sp)) ? from_f32<T>(0.f)
-                                                        : a.p                                                     ? ((const T*)a.p)[c]
-                                                                                                                  : from_f32<T>(none[which]);
+                    v[which] = !in ? 0.f : !a.p ? none[which] : j.wide_w ? (TROP_IN((const float*)a.p + c, 4, a.sp) ? ((const float*)a.p)[c] : 0.f)
+                               : TROP_IN((const T*)a.p + c, sizeof(T), a.sp) ? to_f32(((const T*)a.p)[c]) : 0.f;
                 }
-            __syncthreads();
+#pragma unroll
+                for (int which = 0; which < 5; ++which) {
+                    if (j.wide_w) ((float*)(dyn + which * span))[i] = v[which];
+                    else ((T*)(dyn + which * span))[i] = from_f32<T>(v[which]);
+                }
+            }
         }
+        __syncthreads();
     }
 };
 // (a number's scale may need more digits than T has: it is a factor of its own where there is no vector of it)
@@ -495,22 +526,46 @@ __device__ __forceinline__ void row_sums(float& a, float& b, float (*sh)[32])
     if (blockDim.x > 512) v += sh[up][l + 16];
     halves(v, a, b);
 }
-// The same where `ctas` CTAs of a cluster share the row, up to eight of 16 warps: every warp hands its sums to all of them, and the
-// one barrier is the cluster's.
-__device__ __forceinline__ void row_sums_wide(float& a, float& b, float (*sh)[128], uint32_t rank, uint32_t ctas)
-{
-    const bool up = threadIdx.x & 16;
-    float v = (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, 16);
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    const uint32_t to = threadIdx.x & 15;  // lanes of either half: a CTA each
-    if (to < ctas)
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa(smem_u32(&sh[up][rank * 16 + (threadIdx.x >> 5)]), to)), "f"(v) : "memory");
-    cluster_sync_all();
-    const float4 p = *reinterpret_cast<const float4*>(&sh[up][8 * to]), q = *reinterpret_cast<const float4*>(&sh[up][8 * to + 4]);
-    v = ((p.x + p.y) + (p.z + p.w)) + ((q.x + q.y) + (q.z + q.w));
-    halves(v, a, b);
-}
+// The same where `ctas` CTAs of a cluster share the row, up to eight of 16 warps: every warp hands its two sums to all of them by
+// asynchronous stores, which each CTA's mbarrier counts.  (A barrier of the cluster's also waits for the row's stores to
+// memory: 4096x8192 f16 from copies, 253 us.)  Callers alternate as above: whoever has a turn's sums knows that all warps have read
+// those of the turn before.  A wait that runs out is reported.
+struct WideSums {
+    float2 (*sh)[128];
+    uint64_t* bar;
+    uint32_t rank, ctas, phases;
+    __device__ __forceinline__ void init()
+    {
+        phases = 0;
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < 3; ++i) mbar_init(bar + i, 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+    }
+    __device__ __forceinline__ void operator()(float& a, float& b, int which, uint32_t* error)
+    {
+        const bool up = threadIdx.x & 16;
+        float v = (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, 16);
+        halves(v, a, b);
+        const uint32_t warps = blockDim.x >> 5, to = threadIdx.x & 31;
+        if (threadIdx.x == 0) mbar_expect_tx(bar + which, ctas * warps * 8);
+        if (to < ctas)
+            asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
+                             mapa(smem_u32(&sh[which][rank * 16 + (threadIdx.x >> 5)]), to)),
+                         "f"(a), "f"(b), "r"(mapa(smem_u32(bar + which), to))
+                         : "memory");
+        if (!mbar_wait_cluster(bar + which, phases >> which & 1)) {
+            *(volatile uint32_t*)error = 1;
+            __threadfence_system();
+        }
+        phases ^= 1u << which;
+        const float4 p = *reinterpret_cast<const float4*>(&sh[which][4 * to]), q = *reinterpret_cast<const float4*>(&sh[which][4 * to + 2]);
+        a = (p.x + p.z) + (q.x + q.z);
+        b = (p.y + p.w) + (q.y + q.w);
+        v = (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, 16);
+        halves(v, a, b);
+    }
+};
 __device__ __forceinline__ void zero_sums(float* sh, int n)
 {
     for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < n; i += blockDim.x * blockDim.y) sh[i] = 0.f;
@@ -594,14 +649,15 @@ __global__ void __launch_bounds__(MAXT) k_residual(const ResJob j, int period, i
 {
     pdl_wait();
     pdl_signal();
+    constexpr bool SHARED = OFF;
     extern __shared__ __align__(16) uint8_t dyn[];
     __shared__ __align__(16) float sh[2][2][32];
     __shared__ __align__(8) uint64_t full[8][4];
     zero_sums(&sh[0][0][0], 128);
     const int cols = (int)j.cols;
     const Walk walk = walk_of<U, VEC, OFF>(j.u.p, j.u.s, period, blockIdx.x, gridDim.x);
-    Vectors<Y, VEC, OFF> vec;
-    vec.template init<NV>(dyn, walk.off, j, {j.w, j.b, j.pw, j.pb, j.s}, {1.f, 0.f, 1.f, 0.f, 1.f});
+    Vectors<Y, VEC, OFF, SHARED> vec;
+    vec.template init<NV>(dyn, walk.off, j);
     const float scale = j.s.p ? 1.f : j.scale;
     using InU = In<U, VEC, false, OFF>;
     using InS = In<S, VEC, false, OFF>;
@@ -609,7 +665,7 @@ __global__ void __launch_bounds__(MAXT) k_residual(const ResJob j, int period, i
     const int t0 = OFF ? threadIdx.y * blockDim.x + threadIdx.x : threadIdx.x;
     const int at_x = NV * InU::BYTES * wide, at_g = at_x + NV * InS::BYTES * wide;
     const int size = at_g + (j.gate == GATE_FULL ? NV * InU::BYTES * wide : 0), stage = OFF ? size : size * blockDim.y;
-    const uint32_t base = smem_u32(dyn) + (OFF ? 5 * vec.span : threadIdx.y * size);
+    const uint32_t base = smem_u32(dyn) + (SHARED ? 5 * vec.span : 0) + (OFF ? 0 : threadIdx.y * size);
     Ring ring;
     if (!OFF) ring.init(full, stages);
     auto issue = [&](uint32_t row, int slot) {
@@ -842,6 +898,9 @@ __device__ __forceinline__ void put_partials(const ResJob& j, const Pair<VEC> (&
     }
 }
 
+template <typename Y, bool OFF>
+constexpr bool shared_vectors = OFF || sizeof(Y) == 2;
+
 // Rows of more than 4096 columns are shared by the CTAs of a cluster (WIDE): a thread that had more of a row than eight
 // elements would have no room for its columns' four sums.
 template <typename S, typename U, typename Y, int VEC, int NV, bool CODED, bool OFF, bool WIDE>
@@ -849,25 +908,30 @@ __global__ void __launch_bounds__(512) k_residual_back(const ResJob j, int perio
 {
     pdl_wait();
     pdl_signal();
+    constexpr bool SHARED = shared_vectors<Y, OFF>;
     extern __shared__ __align__(16) uint8_t dyn[];
     constexpr int SUMS = WIDE ? 128 : 32;
     __shared__ __align__(16) float sh[3][2][SUMS];
+    __shared__ __align__(8) uint64_t arrived[3];
     __shared__ __align__(8) uint64_t full[8][4];
     zero_sums(&sh[0][0][0], 6 * SUMS);
     const int cols = (int)j.cols;
     const uint32_t rank = WIDE ? cluster_ctarank() : 0, ctas = WIDE ? cluster_ctas() : 1;
     const int block = blockIdx.x / ctas;
     Walk walk = walk_of<Y, VEC, OFF>(j.dy.p, j.dy.s, period, block, gridDim.x / ctas);
+    WideSums others = {reinterpret_cast<float2(*)[128]>(&sh[0][0][0]), arrived, rank, ctas, 0};
     if (WIDE) {
         walk.off -= rank * NV * blockDim.x * VEC;
-        cluster_sync_all();  // the others' sums are zeros
+        others.init();
+        __syncthreads();
+        cluster_sync_all();  // the others' sums are zeros, and their mbarriers ready
     }
     auto sums = [&](float& a, float& b, int which) {
-        if constexpr (WIDE) row_sums_wide(a, b, sh[which], rank, ctas);
+        if constexpr (WIDE) others(a, b, which, error);
         else row_sums(a, b, sh[which]);
     };
-    Vectors<Y, VEC, OFF> vec;
-    vec.template init<NV>(dyn, walk.off, j, {j.w, j.b, j.pw, j.pb, j.s}, {1.f, 0.f, 1.f, 0.f, 1.f});
+    Vectors<Y, VEC, OFF, SHARED> vec;
+    vec.template init<NV>(dyn, walk.off, j);
     const float scale = j.s.p ? 1.f : j.scale;
     Pair<VEC> acc[4][NV][pairs<VEC>];
 #pragma unroll
@@ -886,7 +950,7 @@ __global__ void __launch_bounds__(512) k_residual_back(const ResJob j, int perio
     const int at_r = NV * InY::BYTES * wide, at_u = at_r + NV * InR::BYTES * wide, at_d = at_u + NV * InU::BYTES * wide;
     const int at_g = at_d + (j.dr.p ? NV * InD::BYTES * wide : 0);
     const int size = at_g + (j.gate == GATE_FULL ? NV * InU::BYTES * wide : 0), stage = OFF ? size : size * blockDim.y;
-    const uint32_t base = smem_u32(dyn) + (OFF ? 5 * vec.span : threadIdx.y * size);
+    const uint32_t base = smem_u32(dyn) + (SHARED ? 5 * vec.span : 0) + (OFF ? 0 : threadIdx.y * size);
     Ring ring;
     if (!OFF) ring.init(full, stages);
     auto issue = [&](uint32_t row, int slot) {
@@ -1433,7 +1497,7 @@ int residual_backward(ResJob j, JoinJob t, int sm, cudaStream_t s)
     bool fits = (vec || off) && ctas <= 8;
     if (fits && ctas == 1) shape_of(units, V, 8, 512, j.rows, sm, 4, &nv, &block);
     else if (fits) nv = 8 / V, block = dim3((unsigned)(((units + ctas * nv - 1) / (ctas * nv) + 31) / 32 * 32), 1);
-    const size_t vectors = off ? (size_t)5 * nv * block.x * V * we : 0, across = block.y > 1 && j.want ? block.y * (size_t)j.cols * 4 : 0;
+    const size_t vectors = off || shared_vectors<Y, false> ? (size_t)5 * nv * block.x * V * we : 0, across = block.y > 1 && j.want ? block.y * (size_t)j.cols * 4 : 0;
     int stages = 0;
     size_t smem = 0;
     const int threads = block.x * block.y, per_sm = fits ? std::max(1, 512 / threads) : 1;
