@@ -20,14 +20,16 @@ from .train import _CODES, _call, _check_vector, _desc, _fail, _fast, _lib, _on_
 GROUP = 32  # elements of a row that share one scale of an 8-bit copy
 
 
+_empty, _f32, _i8, _u8 = torch.empty, torch.float32, torch.int8, torch.uint8
+
+
 def _new_codes(shape, device):
     """Uninitialised codes and scales of a [..., C] activation.  Rows of codes start on 32 bytes: whole vectors for every
     kernel that reads them, whatever C is."""
-    groups = -(-shape[-1] // GROUP)
-    codes = torch.empty((*shape[:-1], groups * GROUP), dtype=torch.int8, device=device)
-    if codes.shape[-1] != shape[-1]:
-        codes = codes[..., :shape[-1]]
-    return codes, torch.empty((*shape[:-1], groups), dtype=torch.uint8, device=device)
+    *lead, c = shape
+    groups = -(-c // GROUP)
+    codes = _empty((*lead, groups * GROUP), dtype=_i8, device=device)
+    return codes if c == groups * GROUP else codes[..., :c], _empty((*lead, groups), dtype=_u8, device=device)
 
 
 def _kept_rows(codes, scales, name: str):
@@ -51,9 +53,9 @@ def activation_pack(x: torch.Tensor, stream=None):
     A group with an infinity or a NaN reads back as NaN."""
     if stream is not None:
         return _on_stream(activation_pack, stream, x)
-    fc, codes = _fast(), None
-    if fc is not None and x.dim() > 1:
-        codes, scales = _new_codes(x.shape, x.device)
+    fc, codes, shape = _fast(), None, x.shape
+    if fc is not None and len(shape) > 1:
+        codes, scales = _new_codes(shape, x.device)
         if fc.activation_pack_t(x, codes, scales) == 0:  # the usual call
             return codes, scales
     lib = _lib()
@@ -139,6 +141,7 @@ class Linear8(torch.autograd.Function):
         return (dx, dw if need[1] else None, db)[:len(ctx.needs_input_grad)]
 
 
+_NONE_KEPT = (None,) * 6
 _NORMS = {"layer": 0, "rms": 1}
 _ACTS = {"none": 0, "sigmoid": 1, "silu": 2}
 
@@ -230,16 +233,17 @@ def residual_norm(x: torch.Tensor, u: torch.Tensor, weight: torch.Tensor | None 
                           post_weight=post_weight, post_bias=post_bias, post_norm=post_norm, norm=norm, alpha=alpha, eps=eps,
                           out_dtype=out_dtype, keep=keep)
     values = _options(weight, bias, post_weight, post_bias, scale, post_norm, norm, gate_act, alpha, eps)
-    if x.dim() == 0:
+    shape, device = x.shape, x.device
+    if not shape:
         _fail(-1, "x has no axis")
-    c = x.shape[-1]
-    full = gate is not None and gate.dim() > 0 and gate.shape[-1] == c
+    *lead, c = shape
     y, r = _result(u, out_dtype), _result(x)
-    stats = torch.empty((4, *x.shape[:-1]), dtype=torch.float32, device=x.device)
-    kept, copies = None, (None,) * 6
+    stats = _empty((4, *lead), dtype=_f32, device=device)
+    kept, copies, full = None, _NONE_KEPT, False
     if keep:
-        ku, kr = _new_codes(x.shape, x.device), _new_codes(x.shape, x.device)
-        kg = _new_codes(x.shape, x.device) if full else gate
+        full = gate is not None and gate.dim() > 0 and gate.shape[-1] == c
+        ku, kr = _new_codes(shape, device), _new_codes(shape, device)
+        kg = _new_codes(shape, device) if full else gate
         kept, copies = (ku, kg, kr), (*ku, *(kg if full else (None, None)), *kr)
     fc = _fast()
     if fc is not None and fc.residual_norm_t(*values, x, u, gate, y, r, stats, *copies) == 0:  # the usual call
@@ -247,8 +251,8 @@ def residual_norm(x: torch.Tensor, u: torch.Tensor, weight: torch.Tensor | None 
     lib = _lib()
     x2, u2 = _rows(x, "x"), _rows(u, "u")
     n = x2.shape[0]
-    _beside(u, "u", x, x.shape)
-    g2 = _gate_rows(gate, x, x.shape)
+    _beside(u, "u", x, shape)
+    g2 = _gate_rows(gate, x, shape)
     o = _options_struct(values, x, c, _vector_type(values, x.dtype))
     table, _held = _kept_table(ku, kg if full else None, kr) if keep else (None, None)
     _pkg._check(lib.tropical_residual_norm(ctypes.byref(o), _desc(x2), _desc(u2), _desc(g2), _desc(_result_rows(y, n, c, "y")),
@@ -288,10 +292,10 @@ def residual_norm_backward(dy: torch.Tensor, dr: torch.Tensor | None, r, u, stat
                           alpha=alpha, want=want, x_dtype=x_dtype, u_dtype=u_dtype)
     values = _options(weight, bias, post_weight, post_bias, scale, post_norm, norm, gate_act, alpha, 0.0)
     want = _GRADS if want is None else want
-    shape = dy.shape
+    shape, device = dy.shape, dy.device
     if not shape:
         _fail(-1, "dy has no axis")
-    c = shape[-1]
+    *lead, c = shape
     copies, coded = isinstance(r, tuple), isinstance(gate, tuple)
     if copies != isinstance(u, tuple):
         _fail(-1, "r and u are both 8-bit copies, or neither is")
@@ -303,8 +307,8 @@ def residual_norm_backward(dy: torch.Tensor, dr: torch.Tensor | None, r, u, stat
     else:
         x_dtype, u_dtype = r.dtype, u.dtype
     wdtype = _vector_type(values, dy.dtype)
-    new = lambda name, dtype, cols=c: torch.empty((*shape[:-1], cols), dtype=dtype, device=dy.device) if name in want else None  # noqa: E731
-    vec = lambda name, v: torch.empty(c, dtype=wdtype, device=dy.device) if v is not None and name in want else None  # noqa: E731
+    new = lambda name, dtype, cols=c: _empty((*lead, cols), dtype=dtype, device=device) if name in want else None  # noqa: E731
+    vec = lambda name, v: _empty(c, dtype=wdtype, device=device) if v is not None and name in want else None  # noqa: E731
     dx, du = new("x", x_dtype), new("u", u_dtype)
     dgate = None if gate is None else new("gate", u_dtype, (gate[0] if coded else gate).shape[-1])
     vectors = [vec("scale", values[10]), vec("weight", weight), vec("bias", bias), vec("post_weight", post_weight),
@@ -314,7 +318,7 @@ def residual_norm_backward(dy: torch.Tensor, dr: torch.Tensor | None, r, u, stat
     fc = _fast()
     if fc is not None:
         given = (None, None, plain) if copies else (r, u, plain)
-        kept = (*u, *(gate if coded else (None, None)), *r) if copies else (None,) * 6
+        kept = (*u, *(gate if coded else (None, None)), *r) if copies else _NONE_KEPT
         if fc.residual_norm_backward_t(*values, dy, dr, *given, stats, *kept, dx, du, dgate, *vectors, *types) == 0:  # the usual call
             return dx, du, dgate, *vectors
     lib = _lib()

@@ -1268,41 +1268,42 @@ __global__ void __launch_bounds__(256) k_residual_columns(const ResJob j)
 }
 
 // The blocks' column sums, in block order: 32 columns per block of threads, 32 warps taking every 32nd block's sums.
-// blockIdx.y: dw, db, or what comes of A1 and A2.
-__device__ __forceinline__ float column_sum(const JoinJob& j, int which, float (*sh)[33])
+// blockIdx.y: dw, db, or what comes of A1 and A2, whose loads are on their way together.
+template <int N>
+__device__ __forceinline__ void column_sums(const JoinJob& j, int which, const bool (&wanted)[N], float (*sh)[32][33], float (&a)[N])
 {
     const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
-    float a = 0.f;
-    if (c < j.cols) {
-        float v[4];
-        int b = threadIdx.y;
-        for (; b + 96 < j.blocks; b += 128) {  // four loads on their way
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float* p = j.part + ((int64_t)(b + 32 * k) * 4 + which) * j.cols + c;
-                v[k] = TROP_IN(p, 4, j.sp_part) ? *p : 0.f;
-            }
-            a += (v[0] + v[1]) + (v[2] + v[3]);
+    for (int n = 0; n < N; ++n) a[n] = 0.f;
+    if (c < j.cols)
+        for (int b = threadIdx.y; b < j.blocks; b += 128) {  // four blocks' loads on their way
+            float v[N][4];
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float* p = j.part + ((int64_t)(b + 32 * k) * 4 + which + n) * j.cols + c;
+                    v[n][k] = wanted[n] && b + 32 * k < j.blocks && TROP_IN(p, 4, j.sp_part) ? *p : 0.f;
+                }
+#pragma unroll
+            for (int n = 0; n < N; ++n) a[n] += (v[n][0] + v[n][1]) + (v[n][2] + v[n][3]);
         }
-        for (; b < j.blocks; b += 32) {
-            const float* p = j.part + ((int64_t)b * 4 + which) * j.cols + c;
-            if (TROP_IN(p, 4, j.sp_part)) a += *p;
-        }
+#pragma unroll
+    for (int n = 0; n < N; ++n) sh[n][threadIdx.y][threadIdx.x] = a[n];
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        a[n] = sh[n][threadIdx.x][threadIdx.y];  // warp y sums column y's 32 values
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) a[n] += __shfl_xor_sync(0xffffffffu, a[n], o);
     }
-    __syncthreads();
-    sh[threadIdx.y][threadIdx.x] = a;
-    __syncthreads();
-    a = sh[threadIdx.x][threadIdx.y];  // warp y sums column y's 32 values
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-    return a;
 }
 template <typename Y>
 __global__ void __launch_bounds__(1024) k_residual_join(const JoinJob j)
 {
     pdl_wait();
     pdl_signal();
-    __shared__ float sh[32][33];
+    __shared__ float sh[2][32][33];
     const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.y;
     const bool mine = threadIdx.x == 0 && c < j.cols;
     auto at = [&](const VecAt& a, float none) {
@@ -1322,17 +1323,20 @@ __global__ void __launch_bounds__(1024) k_residual_join(const JoinJob j)
     if (blockIdx.y < 2) {
         void* to = blockIdx.y ? j.db : j.dw;
         if (!to) return;
-        const float a = column_sum(j, blockIdx.y, sh);
-        if (mine) put(to, a, blockIdx.y ? j.sp_db : j.sp_dw);
+        float a[1];
+        column_sums<1>(j, blockIdx.y, {true}, sh, a);
+        if (mine) put(to, a[0], blockIdx.y ? j.sp_db : j.sp_dw);
         return;
     }
     const bool first = j.dpw || j.ds, second = j.dpb || (j.ds && j.post && j.pb.p);
-    const float a1 = first ? column_sum(j, 2, sh) : 0.f, a2 = second ? column_sum(j, 3, sh) : 0.f;
+    if (!first && !second) return;
+    const float s = mine ? at(j.s, j.scale) : 0.f, pw = mine ? at(j.pw, 1.f) : 0.f, pb = mine ? at(j.pb, 0.f) : 0.f;
+    float a[2];
+    column_sums<2>(j, 2, {first, second}, sh, a);
     if (!mine) return;
-    const float s = at(j.s, j.scale);
-    put(j.dpw, s * a1, j.sp_dpw);
-    put(j.dpb, s * a2, j.sp_dpb);
-    if (j.ds) put(j.ds, j.post ? __fmaf_rn(at(j.pw, 1.f), a1, second ? at(j.pb, 0.f) * a2 : 0.f) : a1, j.sp_ds);
+    put(j.dpw, s * a[0], j.sp_dpw);
+    put(j.dpb, s * a[1], j.sp_dpb);
+    if (j.ds) put(j.ds, j.post ? __fmaf_rn(pw, a[0], second ? pb * a[1] : 0.f) : a[0], j.sp_ds);
 }
 
 // ------------------------------------------------------------------ host
