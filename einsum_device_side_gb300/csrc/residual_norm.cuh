@@ -1513,7 +1513,33 @@ int residual_backward(ResJob j, JoinJob t, int sm, cudaStream_t s)
         smem = std::max(vectors + stages * stage, across);
         fits = stages > (off ? 0 : 1);  // (a bulk ring is filled a row late)
     }
-    int64_t blocks = fits ? std::min<int64_t>((j.rows + block.y - 1) / block.y, std::max<int64_t>(1, (int64_t)sm / ctas) * per_sm)
+    int64_t most = std::max<int64_t>(1, (int64_t)sm * per_sm / ctas);
+    const auto wide = off ? k_residual_back<S, U, Y, V, 8 / V, CODED, true, true> : k_residual_back<S, U, Y, V, 8 / V, CODED, false, true>;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    if (fits && ctas > 1) {
+        if (smem > PLAIN_SMEM) TROP_TRY(allow_dynamic((const void*)wide));
+        cfg.gridDim = dim3((unsigned)(most * ctas));
+        cfg.blockDim = block;
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = (unsigned)ctas;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        // As many as run at once: a cluster's CTAs lie in one part of the chip, where some SMs may be left over.  (4096x16384 bf16,
+        // 36 clusters of four instead of 38: 341 us against 611, of which the last two clusters ran alone for half.)
+        if (j.rows > 1) {
+            int clusters = 0;
+            const cudaError_t e = cudaOccupancyMaxActiveClusters(&clusters, wide, &cfg);
+            if (e != cudaSuccess) return cuda_error(e, "cudaOccupancyMaxActiveClusters(k_residual_back)");
+            most = std::min<int64_t>(most, std::max(1, clusters));
+        }
+    }
+    int64_t blocks = fits ? std::min<int64_t>((j.rows + block.y - 1) / block.y, most)
                           : std::min<int64_t>(j.rows, std::max<int64_t>(1, (int64_t)sm * 8 * 256 / j.cols));
     if (fits && off) blocks = std::max<int64_t>(1, blocks / period) * period;
     if (j.rows == 0) blocks = 0;  // sums over no rows
@@ -1541,22 +1567,8 @@ int residual_backward(ResJob j, JoinJob t, int sm, cudaStream_t s)
         if (smem > PLAIN_SMEM) TROP_TRY(allow_dynamic((const void*)kernel));
         TROP_LAUNCH(kernel, dim3((unsigned)blocks), block, smem, j, period, stages, error);
     } else {
-        const auto kernel = off ? k_residual_back<S, U, Y, V, 8 / V, CODED, true, true> : k_residual_back<S, U, Y, V, 8 / V, CODED, false, true>;
-        if (smem > PLAIN_SMEM) TROP_TRY(allow_dynamic((const void*)kernel));
-        cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(blocks * ctas));
-        cfg.blockDim = block;
-        cfg.dynamicSmemBytes = smem;
-        cfg.stream = s;
-        cudaLaunchAttribute attr[2];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        attr[1].id = cudaLaunchAttributeClusterDimension;
-        attr[1].val.clusterDim.x = (unsigned)ctas;
-        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 2;
-        const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, j, period, stages, error);
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, wide, j, period, stages, error);
         if (e != cudaSuccess) return cuda_error(e, "k_residual_back launch");
         count_launches(1);
     }
