@@ -898,8 +898,9 @@ __device__ __forceinline__ void put_partials(const ResJob& j, const Pair<VEC> (&
     }
 }
 
-template <typename Y, bool OFF>
-constexpr bool shared_vectors = OFF || sizeof(Y) == 2;
+// (f32 vectors beside f32 rows would leave no room for two stages)
+template <typename U, typename Y, bool OFF>
+constexpr bool shared_vectors = OFF || (sizeof(U) == 2 && sizeof(Y) == 2);
 
 // Rows of more than 4096 columns are shared by the CTAs of a cluster (WIDE): a thread that had more of a row than eight
 // elements would have no room for its columns' four sums.
@@ -908,7 +909,7 @@ __global__ void __launch_bounds__(512) k_residual_back(const ResJob j, int perio
 {
     pdl_wait();
     pdl_signal();
-    constexpr bool SHARED = shared_vectors<Y, OFF>;
+    constexpr bool SHARED = shared_vectors<U, Y, OFF>;
     extern __shared__ __align__(16) uint8_t dyn[];
     constexpr int SUMS = WIDE ? 128 : 32;
     __shared__ __align__(16) float sh[3][2][SUMS];
@@ -1501,7 +1502,7 @@ int residual_backward(ResJob j, JoinJob t, int sm, cudaStream_t s)
     bool fits = (vec || off) && ctas <= 8;
     if (fits && ctas == 1) shape_of(units, V, 8, 512, j.rows, sm, 4, &nv, &block);
     else if (fits) nv = 8 / V, block = dim3((unsigned)(((units + ctas * nv - 1) / (ctas * nv) + 31) / 32 * 32), 1);
-    const size_t vectors = off || shared_vectors<Y, false> ? (size_t)5 * nv * block.x * V * we : 0, across = block.y > 1 && j.want ? block.y * (size_t)j.cols * 4 : 0;
+    const size_t vectors = off || shared_vectors<U, Y, false> ? (size_t)5 * nv * block.x * V * we : 0, across = block.y > 1 && j.want ? block.y * (size_t)j.cols * 4 : 0;
     int stages = 0;
     size_t smem = 0;
     const int threads = block.x * block.y, per_sm = fits ? std::max(1, 512 / threads) : 1;
