@@ -94,7 +94,7 @@ def activation_weight_grad(dy: torch.Tensor, codes: torch.Tensor, scales: torch.
     if stream is not None:
         return _on_stream(activation_weight_grad, stream, dy, codes, scales, out_dtype, want_bias)
     fc = _fast()
-    if fc is not None and dy.dim() == 2 and codes.dim() == 2 and dy.shape[0] == codes.shape[0] == scales.shape[0]:  # the usual call
+    if fc is not None and dy.dim() == codes.dim() == scales.dim() == 2 and dy.shape[0] == codes.shape[0] == scales.shape[0]:  # the usual call
         dw = torch.empty((dy.shape[1], codes.shape[1]), dtype=out_dtype or dy.dtype, device=dy.device)
         db = torch.empty(dy.shape[1], dtype=dw.dtype, device=dy.device) if want_bias else None
         if fc.activation_weight_grad_t(dy, codes, scales, dw, db) == 0:
@@ -310,7 +310,7 @@ def residual_norm_backward(dy: torch.Tensor, dr: torch.Tensor | None, r, u, stat
     new = lambda name, dtype, cols=c: _empty((*lead, cols), dtype=dtype, device=device) if name in want else None  # noqa: E731
     vec = lambda name, v: _empty(c, dtype=wdtype, device=device) if v is not None and name in want else None  # noqa: E731
     dx, du = new("x", x_dtype), new("u", u_dtype)
-    dgate = None if gate is None else new("gate", u_dtype, (gate[0] if coded else gate).shape[-1])
+    dgate = None if gate is None else new("gate", u_dtype, ((gate[0] if coded else gate).shape or (1,))[-1])
     vectors = [vec("scale", values[10]), vec("weight", weight), vec("bias", bias), vec("post_weight", post_weight),
                vec("post_bias", post_bias)]
     plain = None if coded else gate

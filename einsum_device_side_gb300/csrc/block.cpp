@@ -318,8 +318,8 @@ extern "C" int tropical_residual_norm_backward(const trop_residual_options* opti
         if (grads->dx) TROP_TRY(check(g.dx.p, "dx"));
         if (grads->du) TROP_TRY(check(g.du.p, "du"));
         if (grads->dgate) TROP_TRY(check(g.dgate.p, "dgate"));
-        TROP_TRY(residual_vectors(check, q));
     }
+    TROP_TRY(residual_vectors(check, q));  // (sums over no rows read them too)
     const struct {
         void* p;
         const char* name;

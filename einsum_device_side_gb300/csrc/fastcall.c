@@ -713,6 +713,12 @@ static int obj_rows(PyObject* obj, long device, trop_tensor* t)
         if (v_ > 0) return PyLong_FromLong(PLAIN_PATH);       \
     } while (0)
 
+#define DEVICE_OR_PLAIN                                       \
+    do {                                                      \
+        if (device == -2) return NULL;                        \
+        if (device < 0) return PyLong_FromLong(PLAIN_PATH);   \
+    } while (0)
+
 /* activation_pack_t(x, codes, scales), activation_values_t(codes, scales, x) */
 static PyObject* activation_t(PyObject* const* a, Py_ssize_t nargs, int pack)
 {
@@ -721,7 +727,8 @@ static PyObject* activation_t(PyObject* const* a, Py_ssize_t nargs, int pack)
     void* stream;
     PyObject *ox = a[pack ? 0 : 2], *oc = a[pack ? 1 : 0], *os = a[pack ? 2 : 1];
     const long device = obj_device(ox);
-    if (device == -2 || obj_stream(Py_None, ox, &stream) < 0) return NULL;
+    DEVICE_OR_PLAIN;
+    if (obj_stream(Py_None, ox, &stream) < 0) return NULL;
     ROWS(ox, &x);
     ROWS(oc, &codes);
     ROWS(os, &scales);
@@ -750,7 +757,8 @@ static PyObject* fc_activation_weight_grad_t(PyObject* self, PyObject* const* a,
     trop_tensor dy, codes, scales, dw;
     void *db, *stream;
     const long device = obj_device(a[0]);
-    if (device == -2 || obj_stream(Py_None, a[0], &stream) < 0 || obj_ptr(a[4], &db) < 0) return NULL;
+    DEVICE_OR_PLAIN;
+    if (obj_stream(Py_None, a[0], &stream) < 0 || obj_ptr(a[4], &db) < 0) return NULL;
     ROWS(a[0], &dy);
     ROWS(a[1], &codes);
     ROWS(a[2], &scales);
@@ -846,7 +854,8 @@ static PyObject* fc_residual_norm_t(PyObject* self, PyObject* const* a, Py_ssize
     trop_kept kept[3];
     void *stats, *stream;
     const long device = obj_device(a[11]);
-    if (device == -2 || obj_stream(Py_None, a[11], &stream) < 0 || obj_ptr(a[16], &stats) < 0) return NULL;
+    DEVICE_OR_PLAIN;
+    if (obj_stream(Py_None, a[11], &stream) < 0 || obj_ptr(a[16], &stats) < 0) return NULL;
     SAME(a[11], a[12], 0);
     if (a[13] != Py_None) SAME(a[11], a[13], 1);
     ROWS(a[11], &x);
@@ -875,7 +884,8 @@ static PyObject* fc_residual_norm_backward_t(PyObject* self, PyObject* const* a,
     trop_kept kept[3];
     void *stats, *stream, *v[5];
     const long device = obj_device(a[11]);
-    if (device == -2 || obj_stream(Py_None, a[11], &stream) < 0) return NULL;
+    DEVICE_OR_PLAIN;
+    if (obj_stream(Py_None, a[11], &stream) < 0) return NULL;
     for (int i = 0; i < 5; ++i) {
         if (a[11 + i] == Py_None) continue;
         SAME(a[11], a[11 + i], i == 4 ? 1 : 0);

@@ -205,3 +205,24 @@ def test_a_deep_network(trop, capture):
     for k in want:
         err, size = float((got[k].double() - want[k]).norm()), float(want[k].norm())
         assert err <= 0.1 * size, (k, err / size)
+
+
+@pytest.mark.parametrize("S, U, Y, keep", [(F, F, B, False), (F, F, H, True), (F, B, B, False), (F, B, B, True), (B, B, B, False), (H, H, H, True)])
+@pytest.mark.parametrize("rows, cols", [(20, 1000), (300, 4096), (160, 8192), (40, 9001)])
+def test_32_bit_vectors_beside_16_bit_results(trop, rows, cols, S, U, Y, keep):
+    t, o = make(rows, cols, S, U, Y, W=F, gate_act="silu", seed=cols)
+    check(trop, t, o, S, U, Y, keep)
+
+
+def test_vectors_of_a_call_over_no_rows(trop):
+    """They are read for the sums' products: on the host they are refused there too."""
+    import ctypes
+
+    from einsum_device_side_gb300 import block, train
+    x = torch.empty(0, 8, device="cuda")
+    host, grad = torch.ones(8), torch.empty(8, device="cuda")
+    o = block._Options(0, 1, 0, 0, 1.0, 1.0, 0.0, None, None, host.data_ptr(), None, None)
+    g = block._Grads(None, None, None, None, None, None, grad.data_ptr(), None)
+    rc = trop._lib.tropical_residual_norm_backward(ctypes.byref(o), train._desc(x), None, train._desc(x), train._desc(x), None, None, None, 0,
+                                                   0, ctypes.byref(g), None)
+    assert trop.ERRORS.get(rc) == "HOST_POINTER"
