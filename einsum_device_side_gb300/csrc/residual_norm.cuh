@@ -128,7 +128,9 @@ __device__ __forceinline__ void put(const RowsAt& a, uint32_t row, int c, const 
 
 // VEC elements of a vector over the columns: f32, or of type T; `none` where it is absent, zero outside the row.  SHARED: from
 // the block's shared copies (five, in the order of the job's), moved by the row's offset.  They spare the address and the checks of
-// every row's five loads; 32-bit vectors of on-grid rows stay in L1, which has the room that the copies would take.
+// every row's five loads; 32-bit vectors of on-grid rows stay in L1, which has the room that the copies would take.  Forward, where
+// an SM has four blocks, each with copies of its own, that holds for all but blocks of several rows (65536x512 bf16 67 us
+// against 79; 4096x8192 f16 with copies 146 us against 108).
 template <typename T, int VEC, bool OFF, bool SHARED>
 struct Vectors {
     const uint8_t* shared;
@@ -573,8 +575,10 @@ __device__ __forceinline__ void zero_sums(float* sh, int n)
 }
 
 // ------------------------------------------------------------------ forward
-// Elements are worked on in packed pairs: with one at a time the instructions (81 an element), not memory, bound
-// 16384x4096 bf16 at 206 us.
+// A group of threads, a warp or a block, has a row, which stays in registers between the norms: 16 elements a thread where
+// there are many rows.  16384x4096 with a gate: f32 stream beside bf16 157 us, 6.0 TB/s, memory's rate; all bf16 162 us, 4.1 TB/s,
+// and with 8-bit copies 233 us, both bound by instructions (72 % of the issue slots: unpacking, three passes over the
+// row, codes).  Elements are worked on in packed pairs: one at a time, 81 instructions an element, it was 206 us.
 template <int VEC, int NV>
 using Pairs = Pair<VEC>[NV][pairs<VEC>];
 
@@ -644,12 +648,15 @@ __device__ __forceinline__ void gated(Pair<VEC> (&t)[pairs<VEC>], const Pair<VEC
     }
 }
 
-template <typename S, typename U, typename Y, int VEC, int NV, int MAXT, bool OFF>
+// (f32 vectors beside f32 rows would leave no room for two stages)
+template <typename U, typename Y, bool OFF>
+constexpr bool shared_vectors = OFF || (sizeof(U) == 2 && sizeof(Y) == 2);
+
+template <typename S, typename U, typename Y, int VEC, int NV, int MAXT, bool OFF, bool SHARED = OFF>
 __global__ void __launch_bounds__(MAXT) k_residual(const ResJob j, int period, int stages, uint32_t* error)
 {
     pdl_wait();
     pdl_signal();
-    constexpr bool SHARED = OFF;
     extern __shared__ __align__(16) uint8_t dyn[];
     __shared__ __align__(16) float sh[2][2][32];
     __shared__ __align__(8) uint64_t full[8][4];
@@ -898,12 +905,11 @@ __device__ __forceinline__ void put_partials(const ResJob& j, const Pair<VEC> (&
     }
 }
 
-// (f32 vectors beside f32 rows would leave no room for two stages)
-template <typename U, typename Y, bool OFF>
-constexpr bool shared_vectors = OFF || (sizeof(U) == 2 && sizeof(Y) == 2);
-
-// Rows of more than 4096 columns are shared by the CTAs of a cluster (WIDE): a thread that had more of a row than eight
-// elements would have no room for its columns' four sums.
+// A thread has eight columns at most, whose four sums it keeps in registers over all of its block's rows: 128 registers, so that
+// an SM has one block of 512 threads (4096 columns).  Longer rows are shared by the CTAs of a cluster (WIDE).  What bounds it is a
+// row's two rounds of sums, which nothing else on the SM covers, and instructions (90 an element, half of the issue slots):
+// 16384x4096 bf16 248 us, 4.3 TB/s, from copies 272 us; 4096x8192 f16 from copies 180 us; f32 335 us, 4.8 TB/s.  (Two blocks of
+// 256 threads an SM, as clusters of twice as many: 16384x4096 bf16 292 us, 4096x8192 294 us.)
 template <typename S, typename U, typename Y, int VEC, int NV, bool CODED, bool OFF, bool WIDE>
 __global__ void __launch_bounds__(512) k_residual_back(const ResJob j, int period, int stages, uint32_t* error)
 {
@@ -1434,7 +1440,8 @@ int residual_forward(ResJob j, int sm, cudaStream_t s)
     size_t smem = 0;
     if ((vec || off) && shape_of(units, V, 16, 1024, j.rows, sm, 8, &nv, &block)) {
         const int threads = block.x * block.y;
-        const size_t beside = off ? (size_t)5 * nv * block.x * V * we : 0;
+        const bool shared = shared_vectors<U, Y, false> && block.y > 1;
+        const size_t beside = off || shared ? (size_t)5 * nv * block.x * V * we : 0;
         const size_t stage = (size_t)nv * threads * V * (sizeof(S) + sizeof(U) * (j.gate == GATE_FULL ? 2 : 1));
         // Of bulk copies one stage a block, more blocks: with two the ring takes the L1 cache that keeps the vectors
         // (16384x4096, f32 stream beside bf16: 158 us against 186; all f32: 230 against 285).
@@ -1448,14 +1455,16 @@ int residual_forward(ResJob j, int sm, cudaStream_t s)
     }
     ResJob k = j;
     if (off) k.ku.codes = k.kg.codes = k.kr.codes = nullptr;  // (whose groups lie across these vectors: a pass of their own)
-    const auto kernel = off ? (nv == 1          ? k_residual<S, U, Y, V, 1, 1024, true>
-                               : nv * V < 16    ? k_residual<S, U, Y, V, 2, 1024, true>
-                               : block.x <= 512 ? k_residual<S, U, Y, V, 16 / V, 512, true>
-                                                : k_residual<S, U, Y, V, 16 / V, 1024, true>)
-                            : (nv == 1          ? k_residual<S, U, Y, V, 1, 1024, false>
-                               : nv * V < 16    ? k_residual<S, U, Y, V, 2, 1024, false>
-                               : block.x <= 512 ? k_residual<S, U, Y, V, 16 / V, 512, false>
-                                                : k_residual<S, U, Y, V, 16 / V, 1024, false>);
+    auto kernel = off ? (nv == 1          ? k_residual<S, U, Y, V, 1, 1024, true>
+                         : nv * V < 16    ? k_residual<S, U, Y, V, 2, 1024, true>
+                         : block.x <= 512 ? k_residual<S, U, Y, V, 16 / V, 512, true>
+                                          : k_residual<S, U, Y, V, 16 / V, 1024, true>)
+                      : (nv == 1          ? k_residual<S, U, Y, V, 1, 1024, false>
+                         : nv * V < 16    ? k_residual<S, U, Y, V, 2, 1024, false>
+                         : block.x <= 512 ? k_residual<S, U, Y, V, 16 / V, 512, false>
+                                          : k_residual<S, U, Y, V, 16 / V, 1024, false>);
+    if constexpr (shared_vectors<U, Y, false>)
+        if (!off && block.y > 1) kernel = nv == 1 ? k_residual<S, U, Y, V, 1, 512, false, true> : k_residual<S, U, Y, V, 16 / V, 512, false, true>;
     if (smem > PLAIN_SMEM) TROP_TRY(allow_dynamic((const void*)kernel));
     int64_t blocks = (j.rows + block.y - 1) / block.y;
     if (blocks > sm) {  // as many as run at once
