@@ -201,3 +201,26 @@ def test_refusals(trop):
     assert name(trop.activation_values, codes, scales.to(torch.int8), B) == "DTYPE"
     assert name(trop.activation_values, codes, scales, torch.float64) == "DTYPE"
     assert name(trop.activation_values, codes, scales.cpu(), B) == "DEVICE_MISMATCH"
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("cols", [16, 17, 31, 33, 100, 1001, 4097])
+def test_values_of_ragged_rows_anywhere_in_memory(trop, cols, dt):
+    """Results that start on any element, without gaps between their rows; nothing beside them is written."""
+    from einsum_device_side_gb300 import train
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    for rows, shift in ((2, 0), (3, 1), (257, 3), (64, 6), (1000, 7)):
+        x = torch.randn(rows, cols, generator=g, device="cuda") * torch.rand(rows, 1, generator=g, device="cuda") * 50
+        codes, scales = trop.activation_pack(x)
+        if shift == 3:  # copies without gaps
+            codes = codes.contiguous()
+        scales[0, 0] = 255  # a group that is not finite
+        units = torch.exp2(scales.double() - 133).repeat_interleave(32, 1)[:, :cols]
+        units[0, :32] = float("nan")
+        want = (codes.double() * units).to(dt)
+        buf = torch.full((rows * cols + 24,), -3.0, dtype=dt, device="cuda")
+        out = buf[8 + shift:8 + shift + rows * cols].view(rows, cols)
+        assert trop._lib.tropical_activation_values(train._desc(codes), train._desc(scales), train._desc(out), None) == 0
+        torch.cuda.synchronize()
+        assert torch.equal(out.nan_to_num(nan=1e4), want.nan_to_num(nan=1e4))
+        assert bool((buf[:8 + shift] == -3).all()) and bool((buf[8 + shift + rows * cols:] == -3).all())
