@@ -1274,45 +1274,51 @@ __global__ void __launch_bounds__(256) k_residual_columns(const ResJob j)
     }
 }
 
-// The blocks' column sums, in block order: 32 columns per block of threads, 32 warps taking every 32nd block's sums.
-// blockIdx.y: dw, db, or what comes of A1 and A2, whose loads are on their way together.
-template <int N>
-__device__ __forceinline__ void column_sums(const JoinJob& j, int which, const bool (&wanted)[N], float (*sh)[32][33], float (&a)[N])
+// The blocks' column sums, in block order: 32 columns per block of threads, whose warps take every WARPS'th block's
+// sums.  blockIdx.y: dw, db, or what comes of A1 and A2, whose loads are on their way together.  It is bound by the latency of those
+// loads: 32 warps where every SM has one block of them at most (608 blocks' sums of 1001 columns 9 us, with 16 warps 15), else 16,
+// of which an SM takes three (76 blocks' sums of 8192 columns 7 us, with 32 warps 13).
+template <int N, int WARPS>
+__device__ __forceinline__ void column_sums(const JoinJob& j, int which, const bool (&wanted)[N], float (*sh)[WARPS][32], float (&a)[N])
 {
+    constexpr int AHEAD = 8 / N;  // blocks whose loads are on their way
     const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
 #pragma unroll
     for (int n = 0; n < N; ++n) a[n] = 0.f;
     if (c < j.cols)
-        for (int b = threadIdx.y; b < j.blocks; b += 128) {  // four blocks' loads on their way
-            float v[N][4];
+        for (int b = threadIdx.y; b < j.blocks; b += WARPS * AHEAD) {
+            float v[N][AHEAD];
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k)
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    const float* p = j.part + ((int64_t)(b + WARPS * k) * 4 + which + n) * j.cols + c;
+                    v[n][k] = wanted[n] && b + WARPS * k < j.blocks && TROP_IN(p, 4, j.sp_part) ? *p : 0.f;
+                }
 #pragma unroll
             for (int n = 0; n < N; ++n)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float* p = j.part + ((int64_t)(b + 32 * k) * 4 + which + n) * j.cols + c;
-                    v[n][k] = wanted[n] && b + 32 * k < j.blocks && TROP_IN(p, 4, j.sp_part) ? *p : 0.f;
-                }
-#pragma unroll
-            for (int n = 0; n < N; ++n) a[n] += (v[n][0] + v[n][1]) + (v[n][2] + v[n][3]);
+                for (int k = 0; k < AHEAD; k += 2) a[n] += v[n][k] + v[n][k + 1];
         }
 #pragma unroll
     for (int n = 0; n < N; ++n) sh[n][threadIdx.y][threadIdx.x] = a[n];
     __syncthreads();
+    if (threadIdx.y != 0) return;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-        a[n] = sh[n][threadIdx.x][threadIdx.y];  // warp y sums column y's 32 values
+        a[n] = 0.f;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) a[n] += __shfl_xor_sync(0xffffffffu, a[n], o);
+        for (int w = 0; w < WARPS; w += 2) a[n] += sh[n][w][threadIdx.x] + sh[n][w + 1][threadIdx.x];
     }
 }
-template <typename Y>
-__global__ void __launch_bounds__(1024) k_residual_join(const JoinJob j)
+template <typename Y, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, WARPS == 16 ? 3 : 1) k_residual_join(const JoinJob j)
 {
     pdl_wait();
     pdl_signal();
-    __shared__ float sh[2][32][33];
-    const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.y;
-    const bool mine = threadIdx.x == 0 && c < j.cols;
+    __shared__ float sh[2][WARPS][32];
+    const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
+    const bool mine = threadIdx.y == 0 && c < j.cols;
     auto at = [&](const VecAt& a, float none) {
         if (!a.p) return none;
         if (j.wide_w) return TROP_IN((const float*)a.p + c, 4, a.sp) ? ((const float*)a.p)[c] : 0.f;
@@ -1331,7 +1337,7 @@ __global__ void __launch_bounds__(1024) k_residual_join(const JoinJob j)
         void* to = blockIdx.y ? j.db : j.dw;
         if (!to) return;
         float a[1];
-        column_sums<1>(j, blockIdx.y, {true}, sh, a);
+        column_sums<1, WARPS>(j, blockIdx.y, {true}, sh, a);
         if (mine) put(to, a[0], blockIdx.y ? j.sp_db : j.sp_dw);
         return;
     }
@@ -1339,7 +1345,7 @@ __global__ void __launch_bounds__(1024) k_residual_join(const JoinJob j)
     if (!first && !second) return;
     const float s = mine ? at(j.s, j.scale) : 0.f, pw = mine ? at(j.pw, 1.f) : 0.f, pb = mine ? at(j.pb, 0.f) : 0.f;
     float a[2];
-    column_sums<2>(j, 2, {first, second}, sh, a);
+    column_sums<2, WARPS>(j, 2, {first, second}, sh, a);
     if (!mine) return;
     put(j.dpw, s * a[0], j.sp_dpw);
     put(j.dpb, s * a[1], j.sp_dpb);
@@ -1586,7 +1592,9 @@ int residual_backward(ResJob j, JoinJob t, int sm, cudaStream_t s)
         t.part = j.part;
         t.blocks = (int)blocks;
         t.sp_part = j.sp_part;
-        TROP_LAUNCH((k_residual_join<Y>), dim3((unsigned)((j.cols + 31) / 32), 3), dim3(32, 32), 0, t);
+        const dim3 grid((unsigned)((j.cols + 31) / 32), 3);
+        if ((int64_t)grid.x * 3 <= sm) TROP_LAUNCH((k_residual_join<Y, 32>), grid, dim3(32, 32), 0, t);
+        else TROP_LAUNCH((k_residual_join<Y, 16>), grid, dim3(32, 16), 0, t);
     }
     return TROP_OK;
 }
