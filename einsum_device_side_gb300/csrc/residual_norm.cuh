@@ -907,8 +907,8 @@ __device__ __forceinline__ void put_partials(const ResJob& j, const Pair<VEC> (&
 
 // A thread has eight columns at most, whose four sums it keeps in registers over all of its block's rows: 128 registers, so that
 // an SM has one block of 512 threads (4096 columns).  Longer rows are shared by the CTAs of a cluster (WIDE).  What bounds it is a
-// row's two rounds of sums, which nothing else on the SM covers, and instructions (90 an element, half of the issue slots):
-// 16384x4096 bf16 248 us, 4.3 TB/s, from copies 272 us; 4096x8192 f16 from copies 180 us; f32 335 us, 4.8 TB/s.  (Two blocks of
+// row's two rounds of sums, which nothing else on the SM covers, and instructions (83 an element, half of the issue slots):
+// 16384x4096 bf16 246 us, 4.4 TB/s, from copies 270 us; 4096x8192 f16 from copies 176 us; f32 335 us, 4.8 TB/s.  (Two blocks of
 // 256 threads an SM, as clusters of twice as many: 16384x4096 bf16 292 us, 4096x8192 294 us.)
 template <typename S, typename U, typename Y, int VEC, int NV, bool CODED, bool OFF, bool WIDE>
 __global__ void __launch_bounds__(512) k_residual_back(const ResJob j, int period, int stages, uint32_t* error)
