@@ -20,7 +20,7 @@ from .train import _CODES, _call, _check_vector, _desc, _fail, _fast, _lib, _on_
 GROUP = 32  # elements of a row that share one scale of an 8-bit copy
 
 
-_empty, _f32, _i8, _u8 = torch.empty, torch.float32, torch.int8, torch.uint8
+_empty, _empty_like, _f32, _i8, _u8 = torch.empty, torch.empty_like, torch.float32, torch.int8, torch.uint8
 
 
 def _new_codes(shape, device):
@@ -271,6 +271,7 @@ def _kept_table(*pairs):
 
 
 _GRADS = ("x", "u", "gate", "scale", "weight", "bias", "post_weight", "post_bias")
+_ALL_GRADS = frozenset(_GRADS)
 
 
 def residual_norm_backward(dy: torch.Tensor, dr: torch.Tensor | None, r, u, stats: torch.Tensor,
@@ -291,7 +292,7 @@ def residual_norm_backward(dy: torch.Tensor, dr: torch.Tensor | None, r, u, stat
                           scale=scale, post_weight=post_weight, post_bias=post_bias, post_norm=post_norm, norm=norm,
                           alpha=alpha, want=want, x_dtype=x_dtype, u_dtype=u_dtype)
     values = _options(weight, bias, post_weight, post_bias, scale, post_norm, norm, gate_act, alpha, 0.0)
-    want = _GRADS if want is None else want
+    want = _ALL_GRADS if want is None else want
     shape, device = dy.shape, dy.device
     if not shape:
         _fail(-1, "dy has no axis")
@@ -308,7 +309,7 @@ def residual_norm_backward(dy: torch.Tensor, dr: torch.Tensor | None, r, u, stat
         x_dtype, u_dtype = r.dtype, u.dtype
     wdtype = _vector_type(values, dy.dtype)
     new = lambda name, dtype, cols=c: _empty((*lead, cols), dtype=dtype, device=device) if name in want else None  # noqa: E731
-    vec = lambda name, v: _empty(c, dtype=wdtype, device=device) if v is not None and name in want else None  # noqa: E731
+    vec = lambda name, v: _empty_like(v) if v is not None and name in want else None  # noqa: E731
     dx, du = new("x", x_dtype), new("u", u_dtype)
     dgate = None if gate is None else new("gate", u_dtype, ((gate[0] if coded else gate).shape or (1,))[-1])
     vectors = [vec("scale", values[10]), vec("weight", weight), vec("bias", bias), vec("post_weight", post_weight),
