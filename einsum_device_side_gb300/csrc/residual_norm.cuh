@@ -238,22 +238,26 @@ __device__ __forceinline__ void copies_wait(int stages)  // the oldest of `stage
     else asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
+// a row with `n` others before it and after it
+__device__ __forceinline__ bool amid(uint32_t row, uint32_t n, const ResJob& j) { return row >= n && row + n < (uint32_t)j.rows; }
+
 // One tensor's part of a stage: BYTES for each vector of each thread.  OFF: a piece of every thread's beside the others'.  `to`:
 // the part's shared address; `t` of `threads`.
 template <typename T, int VEC, bool CODED, bool OFF>
 struct In {
     static constexpr int BYTES = VEC * sizeof(T), PIECE = BYTES < 16 ? BYTES : 16;
-    static __device__ __forceinline__ bool inside(const T* p, const RowsAt& a, const ResJob& j)
+    // Whether the vector lies in the matrix, whatever row of it: all in its row, or over the edge of a row with others on both sides
+    // that lie far enough off.  (By 32-bit comparisons that the tensors
+    // share: 65536x1001 bf16 backward 370 us; by those of their 64-bit addresses 425 us.)
+    static __device__ __forceinline__ bool inside(uint32_t row, int c, const RowsAt& a, const ResJob& j)
     {
-        if (!OFF) return true;
-        const T* const begin = (const T*)a.p;
-        return p >= begin && p + VEC <= begin + (j.rows - 1) * a.s + j.cols;
+        return !OFF || whole<VEC>(c, (int)j.cols) || (amid(row, 1, j) && a.sb >= VEC * sizeof(T));
     }
     static __device__ __forceinline__ void issue(uint32_t to, int t, int threads, const RowsAt& a, const Rows8&, uint32_t row, int c, const ResJob& j)
     {
         if (c >= (int)j.cols) return;
         const T* p = elem<T>(a, row, c);
-        const bool in = inside(p, a, j) && TROP_IN(p, BYTES, a.sp);
+        const bool in = inside(row, c, a, j) && TROP_IN(p, BYTES, a.sp);
 #pragma unroll
         for (int i = 0; i < BYTES / PIECE; ++i)
             copy_async(to + (i * threads + t) * PIECE, in ? reinterpret_cast<const char*>(p) + i * PIECE : (const char*)a.p, PIECE, in);
@@ -276,7 +280,7 @@ struct In {
         }
         if (OFF && !whole<VEC>(c, cols)) {
             const T* p = elem<T>(a, row, c);
-            if (inside(p, a, j)) {
+            if (inside(row, c, a, j)) {
                 constexpr int E = 4 / sizeof(T);  // elements of a word
 #pragma unroll
                 for (int i = 0; i < Raw<T, VEC>::N; ++i) {
@@ -333,28 +337,28 @@ struct In<T, VEC, true, true> {
     {
         return scales_at(a, row, (which ? min(c + VEC - 1, (int)j.cols - 1) : max(c, 0)) / GROUP8);
     }
-    static __device__ __forceinline__ bool scale_inside(const uint8_t* s, const Rows8& a, const ResJob& j)
+    // the words around a scale, up to three bytes to either side; and around the codes
+    static __device__ __forceinline__ bool scale_inside(uint32_t row, int c, int which, const Rows8& a, const ResJob& j)
     {
-        const uint8_t* const w = s - ((uintptr_t)s & 3);
-        return w >= a.scales && w + 4 <= a.scales + (j.rows - 1) * a.ss + ((int)j.cols + GROUP8 - 1) / GROUP8;
+        const int g = (which ? min(c + VEC - 1, (int)j.cols - 1) : max(c, 0)) / GROUP8;
+        return (g >= 3 && (g + 3) * GROUP8 < (int)j.cols) || (amid(row, 3, j) && a.ssb >= 1);
     }
-    static __device__ __forceinline__ bool inside(const int8_t* p, const Rows8& a, const ResJob& j)
+    static __device__ __forceinline__ bool inside(uint32_t row, int c, const Rows8& a, const ResJob& j)
     {
-        const int8_t* const w = p - ((uintptr_t)p & 3);
-        return w >= a.codes && w + 4 * WORDS <= a.codes + (j.rows - 1) * a.sc + j.cols;
+        return (c >= 3 && c + 4 * WORDS <= (int)j.cols) || (amid(row, 1, j) && a.sb >= 16);
     }
     static __device__ __forceinline__ void issue(uint32_t to, int t, int threads, const RowsAt&, const Rows8& a, uint32_t row, int c, const ResJob& j)
     {
         if (c >= (int)j.cols) return;
         const int8_t* p = codes_at(a, row, c);
         const int8_t* w = p - ((uintptr_t)p & 3);
-        const bool in = inside(p, a, j) && TROP_IN(w, 4 * WORDS, a.sp_c);
+        const bool in = inside(row, c, a, j) && TROP_IN(w, 4 * WORDS, a.sp_c);
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) copy_async(to + (i * threads + t) * 4, w + 4 * i, 4, in);
 #pragma unroll
         for (int i = 0; i < SCALES; ++i) {
             const uint8_t* q = scale_at(a, row, c, i, j);
-            const bool there = scale_inside(q, a, j);
+            const bool there = scale_inside(row, c, i, a, j);
             const uint8_t* word = q - ((uintptr_t)q & 3);
             const bool ok = there && TROP_IN(word, 4, a.sp_s);
             copy_async(to + ((WORDS + i) * threads + t) * 4, (const void*)((uintptr_t)word), 4, ok);
@@ -371,7 +375,7 @@ struct In<T, VEC, true, true> {
         for (int i = 0; i < SCALES; ++i) e[i] = LEAST8;
         if (c < cols) {
             const int8_t* p = codes_at(a, row, c);
-            if (inside(p, a, j)) {
+            if (inside(row, c, a, j)) {
                 uint32_t w[WORDS];
 #pragma unroll
                 for (int i = 0; i < WORDS; ++i)
@@ -394,7 +398,7 @@ struct In<T, VEC, true, true> {
                 uint32_t w;
                 asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(to + ((WORDS + i) * threads + t) * 4) : "memory");
                 e[i] = w >> ((uint32_t)(uintptr_t)q & 3) * 8 & 0xffu;
-                if (!scale_inside(q, a, j)) e[i] = TROP_IN(q, 1, a.sp_s) ? *q : LEAST8;
+                if (!scale_inside(row, c, i, a, j)) e[i] = TROP_IN(q, 1, a.sp_s) ? *q : LEAST8;
             }
         }
         float v[VEC];
