@@ -292,7 +292,10 @@ def residual_norm_backward(dy: torch.Tensor, dr: torch.Tensor | None, r, u, stat
                           scale=scale, post_weight=post_weight, post_bias=post_bias, post_norm=post_norm, norm=norm,
                           alpha=alpha, want=want, x_dtype=x_dtype, u_dtype=u_dtype)
     values = _options(weight, bias, post_weight, post_bias, scale, post_norm, norm, gate_act, alpha, 0.0)
-    want = _ALL_GRADS if want is None else want
+    if want is None:
+        want = _ALL_GRADS
+    elif not _ALL_GRADS.issuperset(want := {want} if isinstance(want, str) else set(want)):
+        _fail(-1, f"want must name some of {_GRADS}, got {sorted(map(str, want - _ALL_GRADS))}")
     shape, device = dy.shape, dy.device
     if not shape:
         _fail(-1, "dy has no axis")

@@ -193,3 +193,12 @@ def test_wrappers_refuse_host_tensors_and_wrong_words(trop):
     for f, a in ((trop.residual_norm, (x, x)), (trop.activation_pack, (x,)), (trop.residual_norm_backward, (x, None, x, x, st)),
                  (trop.activation_values, (torch.zeros(3, 8, dtype=torch.int8), torch.zeros(3, 1, dtype=torch.uint8)))):
         assert refused(f, *a) in ("HOST_POINTER", "CUDA", "DEVICE_MISMATCH")
+
+
+@pytest.mark.parametrize("want", [("x", "weigth"), "post weight", ["dx"]])
+def test_unknown_names_of_gradients_are_refused(trop, want):
+    """A misspelt name would leave a gradient out in silence."""
+    x = torch.zeros(3, 8)
+    with pytest.raises(trop.TropicalError) as e:
+        trop.residual_norm_backward(x, None, x, x, torch.zeros(4, 3), want=want)
+    assert e.value.name == "INVALID_ARG" and "want" in str(e.value)
