@@ -224,7 +224,7 @@ struct Vectors {
 // Of the others (OFF) every thread copies its own vectors and waits for those alone.
 __device__ __forceinline__ void copy_async(uint32_t to, const void* from, int bytes, bool in)
 {
-    const int n = in ? bytes : 0;  // (what is not there arrives as zeros)
+    const int n = in ? bytes : 0;  // (what is not there arrives as zeros; its address has to be aligned all the same)
     if (bytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(n) : "memory");
     else if (bytes == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(from), "r"(n) : "memory");
     else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(n) : "memory");
@@ -260,7 +260,7 @@ struct In {
         const bool in = inside(row, c, a, j) && TROP_IN(p, BYTES, a.sp);
 #pragma unroll
         for (int i = 0; i < BYTES / PIECE; ++i)
-            copy_async(to + (i * threads + t) * PIECE, in ? reinterpret_cast<const char*>(p) + i * PIECE : (const char*)a.p, PIECE, in);
+            copy_async(to + (i * threads + t) * PIECE, reinterpret_cast<const char*>(p) + i * PIECE, PIECE, in);
     }
     static __device__ __forceinline__ void take(Raw<T, VEC>& q, uint32_t to, int t, int threads, const RowsAt& a, uint32_t row, int c, const ResJob& j)
     {
