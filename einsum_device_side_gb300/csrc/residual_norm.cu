@@ -92,6 +92,9 @@ int launch_residual_norm_backward(const Residual& q, const NormMat& dy, const No
     const DeviceInfo* dev;
     TROP_TRY(ensure_device(&dev));
     ResJob j = job_of(q);
+    // No gradient depends on y's bias, so that its address is not among those that the route asks after: it is left out, or the
+    // blocks' copies of the vectors would read it in whole vectors wherever it starts.
+    j.b = {};
     j.dy = rows_at(dy, q.rows, q.cols);
     j.dr = rows_at(dr, q.rows, q.cols);
     j.dx = rows_at(g.dx, q.rows, q.cols);

@@ -1,4 +1,4 @@
-"""The residual block's operators at the borders of what they accept.
+"""The residual block's operators at the borders of what they accept: matrices and vectors that start anywhere in a buffer.
 
 Limits as in test_gpu_residual_norm.py: a stored value is off by at most eps / 2 of its type relative to itself, sums in
 32 bits lose less than 1e-5 of the terms that a result is the sum of."""
@@ -30,5 +30,24 @@ def test_few_rows_from_any_element_on(trop, S, U, Y, shift):
         for k in ("x", "u", "gate", "dy", "dr"):
             flat = torch.empty(shift + rows * (cols + gap), dtype=t[k].dtype, device="cuda")
             t[k] = flat.as_strided((rows, cols), (cols + gap, 1), shift).copy_(t[k])
+        for keep in (False, True):
+            check(trop, t, o, S, U, Y, keep)
+
+
+def off16(v):
+    """The same vector one element behind the start of a buffer."""
+    to = torch.empty(v.numel() + 1, dtype=v.dtype, device=v.device)[1:]
+    return to.copy_(v)
+
+
+@pytest.mark.parametrize("name", ["weight", "bias", "post_weight", "post_bias", "scale"])
+@pytest.mark.parametrize("S, U, Y, W", [(B, B, B, B), (H, H, H, H), (F, B, B, B), (F, B, B, F), (F, F, F, F), (F, F, B, B)])
+def test_one_vector_off_16_bytes(trop, S, U, Y, W, name):
+    """As a view of a flat buffer of parameters has it, the other vectors on 16 bytes: short rows, rows of one block and of a
+    cluster, plain and from copies."""
+    for rows, cols in ((90, 64), (40, 1024), (6, 4096), (3, 8192)):
+        t, o = make(rows, cols, S, U, Y, W, gate_act="silu")
+        t[name] = off16(t[name])
+        assert t[name].data_ptr() % 16
         for keep in (False, True):
             check(trop, t, o, S, U, Y, keep)
