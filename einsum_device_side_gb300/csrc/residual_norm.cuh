@@ -1560,7 +1560,7 @@ int residual_backward(ResJob j, JoinJob t, int sm, cudaStream_t s)
         }
     }
     int64_t blocks = fits ? std::min<int64_t>((j.rows + block.y - 1) / block.y, most)
-                          : std::min<int64_t>(j.rows, std::max<int64_t>(1, (int64_t)sm * 8 * 256 / j.cols));
+                          : std::min({j.rows, (int64_t)65535, std::max<int64_t>(1, (int64_t)sm * 8 * 256 / j.cols)});  // (a grid's y)
     if (fits && off) blocks = std::max<int64_t>(1, blocks / period) * period;
     if (j.rows == 0) blocks = 0;  // sums over no rows
     const size_t part = j.want && j.rows ? (size_t)blocks * 4 * j.cols * 4 : 0, sums = !fits && (j.want & (SUM_1 | SUM_2)) ? (size_t)j.rows * 8 : 0;

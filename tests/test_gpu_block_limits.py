@@ -1,4 +1,5 @@
-"""The residual block's operators at the borders of what they accept: matrices and vectors that start anywhere in a buffer.
+"""The residual block's operators at the borders of what they accept: matrices and vectors that start anywhere in a buffer,
+few columns in many rows.
 
 Limits as in test_gpu_residual_norm.py: a stored value is off by at most eps / 2 of its type relative to itself, sums in
 32 bits lose less than 1e-5 of the terms that a result is the sum of."""
@@ -51,3 +52,13 @@ def test_one_vector_off_16_bytes(trop, S, U, Y, W, name):
         assert t[name].data_ptr() % 16
         for keep in (False, True):
             check(trop, t, o, S, U, Y, keep)
+
+
+@pytest.mark.parametrize("keep", [False, True])
+@pytest.mark.parametrize("dt", [F, B, H])
+@pytest.mark.parametrize("cols", [1, 2, 3, 4, 5])
+def test_few_columns_in_many_rows(trop, cols, dt, keep):
+    """More rows than a grid's second dimension counts.  The column sums of up to 65535 blocks are joined by 32 warps, each a chain of
+    1024 additions over sums of two (and one of 32): up to 1060 2^-24 = 6.3e-5 of the terms."""
+    t, o = make(70001, cols, dt, dt, dt, norm="rms", gate_act="sigmoid")
+    check(trop, t, o, dt, dt, dt, keep, lost=7e-5)
