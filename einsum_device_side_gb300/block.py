@@ -9,6 +9,7 @@ stream or the one given (``stream``; copies and results too).
 from __future__ import annotations
 
 import ctypes
+import math
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -284,8 +285,8 @@ def residual_norm_backward(dy: torch.Tensor, dr: torch.Tensor | None, r, u, stat
     tensor given (``bias`` is not read but for that) and None for the others; ``want``: the names of those to compute, of
     "x", "u", "gate", "scale", "weight", "bias", "post_weight", "post_bias".
 
-    ``dy``: y's gradient; ``dr``: what reaches r from elsewhere, or None.  ``r``, ``u`` and ``gate``: as the forward call had
-    them, or their 8-bit copies (pairs; a gate of one value a row stays as it is).  From copies the gradients' types are
+    ``dy``: y's gradient; ``dr``: what reaches r from elsewhere, or None; ``stats``: the forward call's, [4, ...leading].  ``r``,
+    ``u`` and ``gate``: as the forward call had them, or their 8-bit copies (pairs; a gate of one value a row stays as it is).  From copies the gradients' types are
     ``x_dtype`` (by default dr's, else dy's) and ``u_dtype`` (dy's)."""
     if stream is not None:
         return _on_stream(residual_norm_backward, stream, dy, dr, r, u, stats, weight, bias, gate=gate, gate_act=gate_act,
@@ -300,6 +301,8 @@ def residual_norm_backward(dy: torch.Tensor, dr: torch.Tensor | None, r, u, stat
     if not shape:
         _fail(-1, "dy has no axis")
     *lead, c = shape
+    if stats.shape != (4, *lead) and stats.shape != (4, math.prod(lead)):  # (as a matrix of the rows: the same in memory)
+        _fail(-5, f"stats has shape {tuple(stats.shape)}, not {(4, *lead)}")
     copies, coded = isinstance(r, tuple), isinstance(gate, tuple)
     if copies != isinstance(u, tuple):
         _fail(-1, "r and u are both 8-bit copies, or neither is")

@@ -202,3 +202,12 @@ def test_unknown_names_of_gradients_are_refused(trop, want):
     with pytest.raises(trop.TropicalError) as e:
         trop.residual_norm_backward(x, None, x, x, torch.zeros(4, 3), want=want)
     assert e.value.name == "INVALID_ARG" and "want" in str(e.value)
+
+
+@pytest.mark.parametrize("lead, wrong", [((3,), (3, 4)), ((4,), (16,)), ((2, 6), (12, 4)), ((2, 6), (4, 6, 2)), ((3,), (4, 3, 1)), ((), (1, 4))])
+def test_statistics_of_another_shape_are_refused(trop, lead, wrong):
+    """As many elements in another order would be read as other rows' statistics."""
+    x = torch.zeros(*lead, 8)
+    with pytest.raises(trop.TropicalError) as e:
+        trop.residual_norm_backward(x, None, x, x, torch.zeros(wrong))
+    assert e.value.name == "SHAPE" and "stats" in str(e.value)
