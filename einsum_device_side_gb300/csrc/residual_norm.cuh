@@ -33,10 +33,12 @@ namespace {
 // A row's statistics from two passes over registers: a first mean, then the sums of the deviations from it and of their
 // squares, which correct each other (Chan, Golub and LeVeque, "Algorithms for computing the sample variance", 1983): the
 // first mean's error, some last places, is what the deviations' mean says, so that a constant row's mean is its value and
-// its norm zero, whatever the deviation is divided by.
+// its norm zero, whatever the deviation is divided by.  Squares that pass f32's range make the deviation infinite and the norm zero, as
+// layer_norm's do; a NaN stays.
 __device__ __forceinline__ void finish_stats(float sum, float squares, const ResJob& j, float& mean, float& rstd)
 {
-    const float off = sum * j.inv_cols, var = fmaxf(__fmaf_rn(-off, sum, squares), 0.f) + (squares - squares);  // (NaN stays)
+    const bool finite = squares < __uint_as_float(0x7f800000u);
+    const float off = finite ? sum * j.inv_cols : 0.f, var = finite ? fmaxf(__fmaf_rn(-off, sum, squares), 0.f) : squares;
     mean += off;
     rstd = __fdiv_rn(1.f, __fsqrt_rn(__fmaf_rn(var, j.inv_cols, j.eps)));
 }

@@ -1,5 +1,5 @@
 """The residual block's operators at the borders of what they accept: matrices and vectors that start anywhere in a buffer,
-few columns in many rows.
+few columns in many rows, values near the ends of their types.
 
 Limits as in test_gpu_residual_norm.py: a stored value is off by at most eps / 2 of its type relative to itself, sums in
 32 bits lose less than 1e-5 of the terms that a result is the sum of."""
@@ -62,3 +62,35 @@ def test_few_columns_in_many_rows(trop, cols, dt, keep):
     1024 additions over sums of two (and one of 32): up to 1060 2^-24 = 6.3e-5 of the terms."""
     t, o = make(70001, cols, dt, dt, dt, norm="rms", gate_act="sigmoid")
     check(trop, t, o, dt, dt, dt, keep, lost=7e-5)
+
+
+@pytest.mark.parametrize("norm", ["layer", "rms"])
+@pytest.mark.parametrize("S, U, Y", [(F, F, F), (B, B, B), (F, B, B)])
+@pytest.mark.parametrize("cols", [64, 1001, 4096, 8192, 20001])
+def test_squares_past_the_range_of_f32(trop, cols, S, U, Y, norm):
+    """A finite row whose squares pass f32's range has an infinite deviation: its norm is zero, as layer_norm's is, what comes back
+    through it too, and the rows beside it are what they are without it."""
+    t, o = make(9, cols, S, U, Y, norm=norm, gate="row")
+    tensors = {k: t[k] for k in ("gate", "scale", "post_weight", "post_bias")}
+
+    def call():
+        y, r, stats, _ = trop.residual_norm(t["x"], t["u"], t["weight"], t["bias"], **tensors, **o)
+        return y, r, stats, trop.residual_norm_backward(t["dy"], t["dr"], r, t["u"], stats, t["weight"], t["bias"], **tensors, **o)
+
+    y0, r0, stats0, g0 = call()
+    t["x"][2] *= 1e25
+    t["u"][5] *= 1e25
+    y, r, stats, g = call()
+    assert torch.equal(y[2], t["bias"].to(Y)) and float(stats[3, 2]) == 0 and float(stats[1, 5]) == 0
+    assert all(bool(v.isfinite().all()) for v in (y, r, stats, *g))
+    assert not bool(g[1][5].any())
+    # with a norm of zero all of d comes from dr: alpha dr, one rounding in f32 and one to the type
+    want = 0.7 * t["dr"][2].double()
+    assert bool(((g[0][2].double() - want).abs() <= (torch.finfo(S).eps / 2 + 2 ** -23) * want.abs()).all())
+    others = [0, 1, 3, 4, 6, 7, 8]
+    for a, b in zip((y, r, *g[:3]), (y0, r0, *g0[:3])):
+        assert torch.equal(a[others], b[others])
+    if Y == F and norm == "layer":
+        x = t["x"]
+        mine = trop.residual_norm(x, torch.zeros_like(x), None, t["bias"], post_norm=False)[0]
+        assert torch.equal(mine[2], trop.layer_norm(x, torch.ones_like(t["bias"]), t["bias"])[0][2])
