@@ -1526,14 +1526,19 @@ int residual_backward(ResJob j, JoinJob t, int sm, cudaStream_t s)
     const size_t vectors = off || shared_vectors<U, Y, false> ? (size_t)5 * nv * block.x * V * we : 0, across = block.y > 1 && j.want ? block.y * (size_t)j.cols * 4 : 0;
     int stages = 0;
     size_t smem = 0;
-    const int threads = block.x * block.y, per_sm = fits ? std::max(1, 512 / threads) : 1;
+    const int threads = block.x * block.y;
+    int per_sm = fits ? std::max(1, 512 / threads) : 1;
     if (fits) {
         const size_t copy = CODED ? (off ? V + 12 : V) : 0, pr = CODED ? copy : V * sizeof(S), pu = CODED ? copy : V * sizeof(U);
         const size_t stage = (size_t)nv * threads * (V * sizeof(Y) + pr + pu * (j.gate == GATE_FULL ? 2 : 1) + (j.dr.p ? V * sizeof(S) : 0));
         // (bulk copies: two, for the vectors' sake as above; 16384x4096 f32 337 us against 433 of three)
+        // Where eight blocks of 64 threads leave no room for two beside 32-bit vectors, a gate and dr, seven do (65536x512, f32 stream
+        // beside bf16: 152 us, 1590 us by the long rows' kernels).
+        const int least = off ? 1 : 2;  // (a bulk ring is filled a row late)
         stages = std::min(off ? 4 : 2, stages_of(stage, vectors, per_sm));
+        while (stages < least && per_sm > 1) stages = std::min(off ? 4 : 2, stages_of(stage, vectors, --per_sm));
         smem = std::max(vectors + stages * stage, across);
-        fits = stages > (off ? 0 : 1);  // (a bulk ring is filled a row late)
+        fits = stages >= least;
     }
     int64_t most = std::max<int64_t>(1, (int64_t)sm * per_sm / ctas);
     const auto wide = off ? k_residual_back<S, U, Y, V, 8 / V, CODED, true, true> : k_residual_back<S, U, Y, V, 8 / V, CODED, false, true>;

@@ -1,5 +1,5 @@
 """The residual block's operators at the borders of what they accept: matrices and vectors that start anywhere in a buffer,
-few columns in many rows, values near the ends of their types.
+few columns in many rows, values near the ends of their types, the routes that calls take.
 
 Limits as in test_gpu_residual_norm.py: a stored value is off by at most eps / 2 of its type relative to itself, sums in
 32 bits lose less than 1e-5 of the terms that a result is the sum of."""
@@ -94,3 +94,32 @@ def test_squares_past_the_range_of_f32(trop, cols, S, U, Y, norm):
         x = t["x"]
         mine = trop.residual_norm(x, torch.zeros_like(x), None, t["bias"], post_norm=False)[0]
         assert torch.equal(mine[2], trop.layer_norm(x, torch.ones_like(t["bias"]), t["bias"])[0][2])
+
+
+@pytest.mark.parametrize("S, U, Y, W", [(F, F, F, F), (B, B, B, B), (B, B, B, F), (F, B, B, B), (F, B, B, F), (F, F, B, B), (F, F, B, F)])
+def test_rows_on_16_bytes_take_no_long_rows_kernels(trop, S, U, Y, W):
+    """Backward, whatever is given beside the rows: one kernel over the rows and one that joins the column sums, where the long rows'
+    take a third for the sums.  Few rows and as many as fill the device, up to the widest that a cluster shares."""
+    for rows, widths in ((1300, (16, 32, 64, 128, 256, 272, 320, 400, 512, 528, 1024)), (2, (48, 528, 2048, 4096, 4112, 8192, 12288, 20000, 32768))):
+        for cols in widths:
+            t, o = make(rows, cols, S, U, Y, W)
+            for keep in (False, True):
+                y, r, stats, kept = trop.residual_norm(t["x"], t["u"], t["weight"], t["bias"], scale=t["scale"], gate=t["gate"], post_weight=t["post_weight"],
+                                                       post_bias=t["post_bias"], out_dtype=Y if Y != U else None, keep=keep, **o)
+                u, g, r = kept if keep else (t["u"], t["gate"], r)
+                for gate in (g, None):
+                    for dr in (t["dr"], None):
+                        before = trop.stats()["kernel_launches"]
+                        trop.residual_norm_backward(t["dy"], dr, r, u, stats, t["weight"], t["bias"], scale=t["scale"], gate=gate, x_dtype=S, u_dtype=U,
+                                                    post_weight=t["post_weight"], post_bias=t["post_bias"], **o)
+                        assert trop.stats()["kernel_launches"] - before == 2, (rows, cols, keep, gate is None, dr is None)
+
+
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("S, U", [(F, B), (F, H)])
+@pytest.mark.parametrize("rows, cols", [(7, 272), (1300, 264), (1300, 512), (9000, 400)])
+def test_32_bit_vectors_where_blocks_are_small(trop, rows, cols, S, U, act):
+    """Blocks of 64 threads whose two stages, beside 32-bit vectors, an eighth of the shared memory does not hold."""
+    t, o = make(rows, cols, S, U, U, F, gate_act=act, seed=rows)
+    # column sums of 9000 rows: 152 x 7 blocks' at a time, chains of fewer additions than test_few_columns_in_many_rows
+    check(trop, t, o, S, U, U)
