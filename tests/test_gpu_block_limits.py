@@ -123,3 +123,26 @@ def test_32_bit_vectors_where_blocks_are_small(trop, rows, cols, S, U, act):
     t, o = make(rows, cols, S, U, U, F, gate_act=act, seed=rows)
     # column sums of 9000 rows: 152 x 7 blocks' at a time, chains of fewer additions than test_few_columns_in_many_rows
     check(trop, t, o, S, U, U)
+
+
+@pytest.mark.parametrize("kind", ["full", "row"])
+@pytest.mark.parametrize("act", ["sigmoid", "silu"])
+@pytest.mark.parametrize("cols", [5, 100, 1024, 20001])
+def test_32_bit_gates_far_from_zero(trop, cols, act, kind):
+    """Element by element, relative to each: the stream's value is the gate's, whose gradient is its slope.  The exponential is good to 2
+    units in the last place (2^-22), the reciprocal to one (2^-23), the denominator and the product with the gate round by 2^-24 each, as
+    do the three products with ones: the sigmoid is off by 4.2e-7, the value by less than 2^-20.  The slopes are s (1 - s), and s + g s
+    (1 - s), whose terms cancel to no less than a quarter of them up to g = -2: below five times the sigmoid's and some
+    roundings, 2^-18."""
+    rows = 65
+    g = torch.linspace(-87, -2, rows * (cols if kind == "full" else 1), device="cuda").view(rows, -1)
+    one = torch.ones(rows, cols, device="cuda")
+    y, r, stats, _ = trop.residual_norm(torch.zeros_like(one), one, gate=g, gate_act=act, post_norm=False)
+    wide = g.double().requires_grad_()
+    want = (torch.sigmoid if act == "sigmoid" else torch.nn.functional.silu)(wide)
+    assert bool(((r.double() - want) / want).abs().max() <= 2 ** -20)
+    slope, = torch.autograd.grad(want.sum(), wide)
+    # dy zero and dr one: all that reaches the gate is its slope; of a gate of a row, summed over equal elements
+    dg = trop.residual_norm_backward(torch.zeros_like(one), one, r, one, stats, gate=g, gate_act=act, post_norm=False, want="gate")[2]
+    want = slope if kind == "full" else slope * cols
+    assert bool(((dg.double() - want) / want).abs().max() <= 2 ** -18)
