@@ -40,6 +40,13 @@ int kept8(const trop_tensor* codes, const trop_tensor* scales, const char* name,
     return TROP_OK;
 }
 
+// a vector of elements of that many bytes, or none
+int element_start(const void* p, const char* name, size_t bytes)
+{
+    if ((uintptr_t)p % bytes) return set_error(TROP_ERR_INVALID_ARG, "%s does not start on an element of its type", name);
+    return TROP_OK;
+}
+
 int extents(int64_t rows, int64_t cols)
 {
     if (rows > MOST || cols > MOST) return set_error(TROP_ERR_UNSUPPORTED, "extents above %lld", (long long)MOST);
@@ -129,8 +136,7 @@ int residual_vectors(PointerCheck& check, const Residual& q)
     } all[] = {{q.weight, "weight"}, {q.bias, "bias"}, {q.post_weight, "post_weight"}, {q.post_bias, "post_bias"}, {q.scale_vector, "scale"}};
     for (const auto& a : all) {
         if (!a.p) continue;
-        if ((uintptr_t)a.p % model_bytes(q.wdtype))
-            return set_error(TROP_ERR_INVALID_ARG, "%s does not start on an element of its type", a.name);
+        TROP_TRY(element_start(a.p, a.name, model_bytes(q.wdtype)));
         TROP_TRY(check(a.p, a.name));
     }
     return TROP_OK;
@@ -179,6 +185,7 @@ extern "C" int tropical_residual_norm(const trop_residual_options* options, cons
     TROP_TRY(float_rows(u, "u", false));
     TROP_TRY(float_rows(y, "y", true));
     TROP_TRY(float_rows(r, "r", true));
+    TROP_TRY(element_start(stats, "stats", 4));
     q.has_gate = gate != nullptr;
     q.gate_cols = 1;
     if (gate) TROP_TRY(residual_gate(gate, "gate", q.rows, q.cols, u->dtype, false, &q.gate_cols));
@@ -235,6 +242,7 @@ extern "C" int tropical_residual_norm_backward(const trop_residual_options* opti
     if (q.cols == 0) return set_error(TROP_ERR_SHAPE, "a norm over no elements");
     TROP_TRY(extents(q.rows, q.cols));
     TROP_TRY(float_rows(dy, "dy", false));
+    TROP_TRY(element_start(stats, "stats", 4));
     if (dr) {
         TROP_TRY(same_shape(dr, "dr", q.rows, q.cols));
         if (dr->dtype != x_dtype) return set_error(TROP_ERR_DTYPE, "dr has dtype %d, x %d", dr->dtype, x_dtype);
@@ -297,6 +305,12 @@ extern "C" int tropical_residual_norm_backward(const trop_residual_options* opti
     const bool vectors = g.dscale || g.dweight || g.dbias || g.dpost_weight || g.dpost_bias;
     if (vectors && options->wdtype != dy->dtype && options->wdtype != TROP_F32)
         return set_error(TROP_ERR_DTYPE, "the vectors' gradients have dtype %d: dy's (%d) or f32 is wanted", options->wdtype, dy->dtype);
+    const struct {
+        void* p;
+        const char* name;
+    } vecs[] = {{g.dscale, "dscale"}, {g.dweight, "dweight"}, {g.dbias, "dbias"}, {g.dpost_weight, "dpost_weight"}, {g.dpost_bias, "dpost_bias"}};
+    for (const auto& v : vecs)
+        if (v.p) TROP_TRY(element_start(v.p, v.name, model_bytes(q.wdtype)));
     TROP_TRY(ensure_device(nullptr));
     if (!vectors && (q.rows == 0 || (!g.dx.p && !g.du.p && !g.dgate.p))) return TROP_OK;
     PointerCheck check;
@@ -320,10 +334,6 @@ extern "C" int tropical_residual_norm_backward(const trop_residual_options* opti
         if (grads->dgate) TROP_TRY(check(g.dgate.p, "dgate"));
     }
     TROP_TRY(residual_vectors(check, q));  // (sums over no rows read them too)
-    const struct {
-        void* p;
-        const char* name;
-    } vecs[] = {{g.dscale, "dscale"}, {g.dweight, "dweight"}, {g.dbias, "dbias"}, {g.dpost_weight, "dpost_weight"}, {g.dpost_bias, "dpost_bias"}};
     for (const auto& v : vecs)
         if (v.p) TROP_TRY(check(v.p, v.name));
     q.stats = const_cast<float*>(stats);

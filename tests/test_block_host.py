@@ -211,3 +211,25 @@ def test_statistics_of_another_shape_are_refused(trop, lead, wrong):
     with pytest.raises(trop.TropicalError) as e:
         trop.residual_norm_backward(x, None, x, x, torch.zeros(wrong))
     assert e.value.name == "SHAPE" and "stats" in str(e.value)
+
+
+def test_statistics_and_gradients_start_on_an_element(trop, block):
+    """As the vectors do: an address inside an element would be a misaligned access."""
+    at = lambda *d: ctypes.byref(_tensor(trop, *d))  # noqa: E731
+    like = (BF16, (4, 40))
+
+    def forward(stats):
+        o = block._Options(norm=0, post_norm=1, gate_act=0, wdtype=BF16, alpha=1.0, scale=1.0, eps=1e-5)
+        return trop.ERRORS.get(trop._lib.tropical_residual_norm(ctypes.byref(o), at(*like), at(*like), None, at(*like), at(*like), stats, None, None))
+
+    def backward(stats, wdtype, **grads):
+        o = block._Options(norm=0, post_norm=1, gate_act=0, wdtype=wdtype, alpha=1.0, scale=1.0, eps=0.0, scale_vector=4096)
+        g = block._Grads(**grads)
+        return trop.ERRORS.get(trop._lib.tropical_residual_norm_backward(ctypes.byref(o), at(*like), None, at(*like), at(*like), None, stats, None,
+                                                                         BF16, BF16, ctypes.byref(g), None))
+
+    assert forward(4098) == "INVALID_ARG"
+    assert backward(4098, BF16, dweight=4096) == "INVALID_ARG"
+    for name in ("dscale", "dweight", "dbias", "dpost_weight", "dpost_bias"):
+        assert backward(4096, BF16, **{name: 4097}) == "INVALID_ARG"
+        assert backward(4096, F32, **{name: 4098}) == "INVALID_ARG"
