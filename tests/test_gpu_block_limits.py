@@ -146,3 +146,35 @@ def test_32_bit_gates_far_from_zero(trop, cols, act, kind):
     dg = trop.residual_norm_backward(torch.zeros_like(one), one, r, one, stats, gate=g, gate_act=act, post_norm=False, want="gate")[2]
     want = slope if kind == "full" else slope * cols
     assert bool(((dg.double() - want) / want).abs().max() <= 2 ** -18)
+
+
+@pytest.mark.parametrize("kind", ["full", "row"])
+@pytest.mark.parametrize("keep", [False, True])
+@pytest.mark.parametrize("S, U, Y", [(F, F, F), (B, B, B), (F, B, B)])
+@pytest.mark.parametrize("rows, cols", [(2500, 33), (1300, 512), (700, 1001), (90, 4097), (330, 8192), (9, 20001)])
+def test_rows_beside_others_that_hold_anything(trop, rows, cols, S, U, Y, keep, kind):
+    """A row's results are the same bits whatever the rows beside it hold, forward and backward: other values, infinities, NaN."""
+    t, o = make(rows, cols, S, U, Y, gate_act="silu", gate=kind)
+
+    def call():
+        tensors = {k: t[k] for k in ("gate", "scale", "post_weight", "post_bias")}
+        y, r, stats, kept = trop.residual_norm(t["x"], t["u"], t["weight"], t["bias"], **tensors, **o, keep=keep)
+        ku, kg, kr = kept if keep else (t["u"], t["gate"], r)
+        tensors["gate"] = kg
+        g = trop.residual_norm_backward(t["dy"], t["dr"], kr, ku, stats, t["weight"], t["bias"], **tensors, **o, x_dtype=S, u_dtype=U)
+        copies = [v for pair in (kept or ()) if isinstance(pair, tuple) for v in pair]
+        return [y, r, stats.t(), *g[:3], *copies]
+
+    before = call()
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    others = torch.rand(rows, generator=gen, device="cuda") < 0.5
+    others[1::4] = False  # (some of each)
+    others[0] = True
+    for k in ("x", "u", "gate", "dy", "dr"):
+        new = torch.randn(t[k].shape, generator=gen, device="cuda") * 100
+        at = torch.rand(t[k].shape, generator=gen, device="cuda")
+        new[at < 0.02] = float("inf")
+        new[at > 0.98] = float("nan")
+        t[k] = torch.where(others[:, None], new.to(t[k].dtype), t[k])
+    for a, b in zip(call(), before):
+        assert torch.equal(a[~others], b[~others])
