@@ -892,7 +892,10 @@ static PyObject* fc_residual_norm_backward_t(PyObject* self, PyObject* const* a,
         ROWS(a[11 + i], &in[i]);
     }
     for (int i = 0; i < 3; ++i) {
-        if (a[17 + 2 * i] != Py_None) SAME(a[11], a[17 + 2 * i], 0);
+        if (a[17 + 2 * i] != Py_None) {  /* codes, and a scale for each 32 of a row's */
+            SAME(a[11], a[17 + 2 * i], 0);
+            SAME(a[11], a[18 + 2 * i], (in[0].shape[1] + 31) / 32);
+        }
         if (a[23 + i] != Py_None) ROWS(a[23 + i], &out[i]);
     }
     VECTOR(a[16], 4 * in[0].shape[0], TROP_F32, &stats);

@@ -178,3 +178,23 @@ def test_rows_beside_others_that_hold_anything(trop, rows, cols, S, U, Y, keep, 
         t[k] = torch.where(others[:, None], new.to(t[k].dtype), t[k])
     for a, b in zip(call(), before):
         assert torch.equal(a[~others], b[~others])
+
+
+def test_scales_of_other_leading_axes_are_refused(trop):
+    """As many rows in another order would be read as other rows' scales, of each of the three copies."""
+    t, o = make(6, 64, B, B, B)
+    v = lambda a: a.view(2, 3, -1)  # noqa: E731
+    y, r, stats, kept = trop.residual_norm(v(t["x"]), v(t["u"]), gate=v(t["gate"]), **o, keep=True)
+    args = lambda k: (v(t["dy"]), v(t["dr"]), k[2], k[0], stats)  # noqa: E731
+    want = trop.residual_norm_backward(*args(kept), gate=kept[1], **o)
+    for i in range(3):
+        for wrong in (kept[i][1].view(3, 2, -1), kept[i][1].view(6, -1), kept[i][1].view(2, 6, -1)):
+            bad = [*kept]
+            bad[i] = (kept[i][0], wrong)
+            with pytest.raises(trop.TropicalError) as e:
+                trop.residual_norm_backward(*args(bad), gate=bad[1], **o)
+            assert e.value.name == "SHAPE"
+    # and by the matrices of the same rows
+    flat = [tuple(c.reshape(6, -1) for c in k) for k in kept]
+    got = trop.residual_norm_backward(t["dy"], t["dr"], flat[2], flat[0], stats.view(4, 6), gate=flat[1], **o)
+    assert all(torch.equal(a.reshape(6, -1), b) for a, b in zip(want[:3], got[:3]))
