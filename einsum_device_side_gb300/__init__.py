@@ -8,7 +8,8 @@ library is missing the first call raises.
 The training operators that stand around a tropical product and its gradient
 (layer norm, the cross entropy of a linear head, AdamW) are in ``train.py``, those
 of a residual block around it (its fused norms, activations kept in 8 bits) in
-``block.py``; both are reached from here too.
+``block.py``; both are reached from here too.  (``Linear8``'s forward product and its
+input's gradient are torch's.)
 
 Semirings: ``"maxplus"`` (max, +), ``"minplus"`` (min, +), ``"maxtimes"``
 (max, *).  Argmax tensors are int32.

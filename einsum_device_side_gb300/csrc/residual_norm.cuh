@@ -587,7 +587,7 @@ __device__ __forceinline__ void zero_sums(float* sh, int n)
 
 // ------------------------------------------------------------------ forward
 // A group of threads, a warp or a block, has a row, which stays in registers between the norms: 16 elements a thread where
-// there are many rows.  16384x4096 with a gate: f32 stream beside bf16 157 us, 6.0 TB/s, memory's rate; all bf16 162 us, 4.1 TB/s,
+// there are many rows.  16384x4096 with a gate: f32 stream beside bf16 158 to 166 us, 5.7 to 6.0 TB/s, memory's rate; all bf16 162 us, 4.1 TB/s,
 // and with 8-bit copies 233 us, both bound by instructions (72 % of the issue slots: unpacking, three passes over the
 // row, codes).  Elements are worked on in packed pairs: one at a time, 81 instructions an element, it was 206 us.
 template <int VEC, int NV>

@@ -539,7 +539,8 @@ int tropical_activation_values(const trop_tensor* codes, const trop_tensor* scal
  *   dw[o, c] = sum over the tokens of dy[t, o] x[t, c],  db[o] = sum of dy[t, o]
  * with x the values that codes and scales [T, C] stand for, in dy's type (exact
  * for bf16; in f16, values outside its range become infinities), products
- * exact, sums in f32.  dy: [T, O], bf16 or f16, any strides.  dw: [O, C], of
+ * exact, sums in f32, one chain over the tokens (of 16384, an f32 result is off
+ * by 1e-6 of its norm).  dy: [T, O], bf16 or f16, any strides.  dw: [O, C], of
  * dy's type or f32, contiguous columns.  db: nullable, [O] of dw's type.  No
  * token: zeros.  Long sums that few tiles have are split and joined in a fixed
  * order: results repeat bit for bit.  Rows of dy or of codes that TMA cannot
@@ -573,7 +574,8 @@ typedef struct {
 /* x, u, y, r: [rows, cols], contiguous columns, any row stride.  r has x's type;
  * u and gate have it too, or 16 bits beside an f32 x; y has u's type, or 16 bits
  * beside an f32 u.  gate: nullable, [rows, cols] or [rows, 1].  Sums and the
- * stream inside a row are f32, each stored value is rounded once.  stats:
+ * stream inside a row are f32, each stored value is rounded once; a finite row
+ * whose squares pass f32's range has rstd 0 and gives its bias.  stats:
  * nullable f32 [4][rows], mean and rstd of u's norm (0 and 1 without one) and of
  * r's: what the backward call reads.  kept: nullable, three 8-bit copies that
  * the call leaves of u, gate and the stored r (all three; gate's members are NULL
