@@ -92,8 +92,7 @@ def activation_weight_grad(dy: torch.Tensor, codes: torch.Tensor, scales: torch.
 
     ``dy`` [..., O]: bfloat16 or float16, any strides; ``codes``, ``scales``: ``activation_pack`` of x [..., C], whose
     values enter in dy's type (bfloat16 holds them exactly; float16 makes infinities of those outside its range).  Sums are
-    float32, one chain over the tokens (a float32 result over 16384 of them is off by 1e-6 of its norm); results have dy's type or
-    float32 (``out_dtype``)."""
+    float32; results have dy's type or float32 (``out_dtype``)."""
     if stream is not None:
         return _on_stream(activation_weight_grad, stream, dy, codes, scales, out_dtype, want_bias)
     fc = _fast()

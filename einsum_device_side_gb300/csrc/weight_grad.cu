@@ -11,8 +11,7 @@
 //   warp 0       loads: boxes of 64 tokens x 64 columns of dy and of x, by TMA into a ring of six stages
 //   warp 1       products, one thread of the pair's first CTA
 //   warps 4-11   results: tensor memory to dw, or to the f32 sums of a split of the tokens
-// 8192^3 bf16: 640 us in short runs (1718 TFLOP/s), 714 to 754 under the power limit.  A sum is one chain of accumulations, which loses
-// up to a last place every 16 tokens: f32 results of 16384x4096x4096 are off by 1.1e-6 of the norm, the plain f32 product by 5.1e-7.
+// 8192^3 bf16: 640 us in short runs (1718 TFLOP/s), 714 to 754 under the power limit.
 // (Codes that came by TMA and were made operands inside this kernel, by warps of their own: 8192^3 bf16 2034 us, in
 // pieces 640 us.  The tensor cores' own reads take three quarters of the shared memory's rate, so that those warps' loads
 // and stores waited 1200 cycles each; 64x16384x4096 to f32 55 us and 54 us.)
@@ -35,6 +34,10 @@ namespace trop {
 namespace {
 
 constexpr int TK = 64, TM = 256, TN = 256;
+// Stages of one chain of accumulations of an f32 result.  A chain loses up to a last place every 16 tokens, 2.2e-10 to 4.3e-10 of its norm
+// a token: 2.8e-6 over 8192, 7.0e-6 over 16384, where the plain f32 product is off by 3.1e-7 and 5.1e-7.  Chains of 2048 tokens that the
+// copies to memory add up in f32 are off by 4.5e-7 over any number of tokens (8192^3 bf16 to f32 721 to 725 us, one chain 654).
+constexpr int CHAIN = 2048 / TK;
 constexpr int HALF_BYTES = 128 * TK * 2;  // a CTA's part of either operand in a stage
 constexpr int STAGE_BYTES = 2 * HALF_BYTES, STAGES = 6;
 constexpr int EPI_WARPS = 8, THREADS = 128 + 32 * EPI_WARPS;
@@ -43,8 +46,9 @@ constexpr int SMEM = STAGES * STAGE_BYTES + EPI_WARPS * BOX_BYTES + 1024;
 
 struct Job {
     int mt, nt, kt, kper, units;
+    int chain;       // stages of one accumulation: a unit's chains are added up in memory
     int rows, cols;  // of dw
-    void* out;       // null: f32 sums of splits, through map_c
+    void* out;       // null: f32 sums, through map_c
     int64_t ldo;
     int wide, vec;   // out is f32; its rows lie on 16 bytes: through map_c
     int pad_rows;    // rows of one split's sums
@@ -127,22 +131,25 @@ __global__ void __launch_bounds__(THREADS, 1)
             constexpr uint32_t idesc = mma_desc(BF16, true, true, TM, TN);
             int s = 0;
             uint32_t phase = 0, tile = 0;
-            for (int u = first; u < j.units && ok; u += step, ++tile) {
+            for (int u = first; u < j.units && ok; u += step) {
                 const Unit t = unit_of(j, u);
-                const uint32_t buf = tile & 1, acc = tmem + buf * TN;
-                if (!(ok = mbar_wait_cluster(&tempty[buf], ((tile >> 1) & 1) ^ 1))) break;
-                tc_fence_after();
-                for (int k = t.k0; k < t.k1; ++k) {
-                    if (!(ok = mbar_wait_cluster(&full[s], phase))) break;
+                for (int k0 = t.k0; k0 < t.k1 && ok; k0 += j.chain, ++tile) {
+                    const uint32_t buf = tile & 1, acc = tmem + buf * TN;
+                    if (!(ok = mbar_wait_cluster(&tempty[buf], ((tile >> 1) & 1) ^ 1))) break;
                     tc_fence_after();
-                    const uint32_t at = ring + s * STAGE_BYTES;
-                    const uint64_t da = smem_desc(at, 8192), db = smem_desc(at + HALF_BYTES, 8192);
+                    const int k1 = min(t.k1, k0 + j.chain);
+                    for (int k = k0; k < k1; ++k) {
+                        if (!(ok = mbar_wait_cluster(&full[s], phase))) break;
+                        tc_fence_after();
+                        const uint32_t at = ring + s * STAGE_BYTES;
+                        const uint64_t da = smem_desc(at, 8192), db = smem_desc(at + HALF_BYTES, 8192);
 #pragma unroll
-                    for (int i = 0; i < TK / 16; ++i) tc_mma<2>(acc, da + i * 128, db + i * 128, idesc, k > t.k0 || i > 0);
-                    tc_commit<2>(&empty[s]);
-                    if (++s == STAGES) s = 0, phase ^= 1;
+                        for (int i = 0; i < TK / 16; ++i) tc_mma<2>(acc, da + i * 128, db + i * 128, idesc, k > k0 || i > 0);
+                        tc_commit<2>(&empty[s]);
+                        if (++s == STAGES) s = 0, phase ^= 1;
+                    }
+                    if (ok) tc_commit<2>(&tfull[buf]);
                 }
-                if (ok) tc_commit<2>(&tfull[buf]);
             }
             if (!ok) {  // no product may run after the CTA has left
                 tc_commit<2>(&drain);
@@ -153,44 +160,49 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int quad = warp & 3, half = (warp - 4) >> 2;
         const uint32_t box = boxes + (warp - 4) * BOX_BYTES;
         uint32_t tile = 0;
-        for (int u = first; u < j.units && ok; u += step, ++tile) {
+        for (int u = first; u < j.units && ok; u += step) {
             const Unit t = unit_of(j, u);
-            const uint32_t buf = tile & 1;
-            ok = mbar_wait(&tfull[buf], (tile >> 1) & 1);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t src = tmem + buf * TN + half * 128 + ((uint32_t)(quad * 32) << 16);
-            const int row0 = t.m * TM + rank * 128 + quad * 32;
-            uint32_t v[2][32];
-            tmem_ld32(src, v[0]);
+            for (int k0 = t.k0; k0 < t.k1; k0 += j.chain, ++tile) {
+                const uint32_t buf = tile & 1;
+                ok = mbar_wait(&tfull[buf], (tile >> 1) & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const bool add = k0 > t.k0;  // to the chains before, which are in memory by then: in their order
+                if (add && lane == 0) tma_store_wait();
+                __syncwarp();
+                const uint32_t src = tmem + buf * TN + half * 128 + ((uint32_t)(quad * 32) << 16);
+                const int row0 = t.m * TM + rank * 128 + quad * 32;
+                uint32_t v[2][32];
+                tmem_ld32(src, v[0]);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                tmem_wait_ld(v[c & 1]);
-                if (c < 3) tmem_ld32(src + (c + 1) * 32, v[(c + 1) & 1]);
-                else {  // the accumulator is in registers: the next tile may fill it
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&tempty[buf]), 0));
-                }
-                const int col = t.n * TN + half * 128 + c * 32;
-                if (!j.out || j.wide) {  // f32: a box of 32 columns
-                    box_free(lane);
-                    to_box<32>(box, lane, 0, v[c & 1]);
-                    if (!j.out)
-                        store_box(&map_c, box, lane, col, t.split * j.pad_rows + row0, j.cols, t.split * j.pad_rows + j.rows, false);
-                    else if (j.vec) store_box(&map_c, box, lane, col, row0, j.cols, j.rows, false);
-                    else copy_box<float>(box, lane, col, row0, j.rows, j.cols, j.out, j.ldo, j.sp_out);
-                    continue;
-                }
-                uint32_t w[16];
+                for (int c = 0; c < 4; ++c) {
+                    tmem_wait_ld(v[c & 1]);
+                    if (c < 3) tmem_ld32(src + (c + 1) * 32, v[(c + 1) & 1]);
+                    else {  // the accumulator is in registers: the next tile may fill it
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&tempty[buf]), 0));
+                    }
+                    const int col = t.n * TN + half * 128 + c * 32;
+                    if (!j.out || j.wide) {  // f32: a box of 32 columns
+                        box_free(lane);
+                        to_box<32>(box, lane, 0, v[c & 1]);
+                        if (!j.out)
+                            store_box(&map_c, box, lane, col, t.split * j.pad_rows + row0, j.cols, t.split * j.pad_rows + j.rows, add);
+                        else if (j.vec) store_box(&map_c, box, lane, col, row0, j.cols, j.rows, add);
+                        else copy_box<float>(box, lane, col, row0, j.rows, j.cols, j.out, j.ldo, j.sp_out);  // (one chain)
+                        continue;
+                    }
+                    uint32_t w[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) w[i] = pack2<BF16>(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1]));
-                if (c % 2 == 0) box_free(lane);  // a box of 64 columns, in two halves
-                to_box<16>(box, lane, (c % 2) * 4, w);
-                if (c % 2 == 0) continue;
-                if (j.vec) store_box(&map_c, box, lane, col - 32, row0, j.cols, j.rows, false);
-                else copy_box<uint16_t>(box, lane, col - 32, row0, j.rows, j.cols, j.out, j.ldo, j.sp_out);
+                    for (int i = 0; i < 16; ++i) w[i] = pack2<BF16>(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1]));
+                    if (c % 2 == 0) box_free(lane);  // a box of 64 columns, in two halves
+                    to_box<16>(box, lane, (c % 2) * 4, w);
+                    if (c % 2 == 0) continue;
+                    if (j.vec) store_box(&map_c, box, lane, col - 32, row0, j.cols, j.rows, false);
+                    else copy_box<uint16_t>(box, lane, col - 32, row0, j.rows, j.cols, j.out, j.ldo, j.sp_out);
+                }
             }
         }
         if (lane == 0) tma_store_wait();
@@ -207,7 +219,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp == 2) tmem_free_all<2>(tmem);
 }
 
-// The splits' sums [ks][slab][lda], added in order, four columns of a row per thread where rows allow 16-byte loads.
+// The sums [ks][slab][lda], added in order, four columns of a row per thread where rows allow 16-byte loads.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) k_grad_join(const float* acc, int ks, int64_t slice, int64_t lda, int64_t rows, int64_t cols,
                                                    T* out, int64_t ldo, Span sp_acc, Span sp_out)
@@ -372,7 +384,13 @@ int launch_weight_grad(const WeightGrad& q, cudaStream_t s)
     const int mt = cdiv(O, TM), kt = cdiv(T, TK);
     const int ks = C == 0 ? 1 : splits(mt * cdiv(std::min(piece, C), TN), kt, sm / 2, O * std::min(piece, C) * 4);
     const int64_t lda = (std::min(piece, C) + 3) / 4 * 4, pad_rows = (O + 31) / 32 * 32;
-    const size_t at_acc = ks > 1 ? ws.add((size_t)ks * pad_rows * lda * 4) : 0;
+    const size_t elem = q.wide ? 4 : 2;
+    // (pieces start on whole tiles)
+    const bool vec = (uintptr_t)q.dw % 16 == 0 && q.ldw * elem % 16 == 0 && q.ldw >= C && q.ldw < (int64_t)1 << 37;
+    // sums in workspace: of splits, and of chains where the result's rows take no copies (8192x4864x2047 bf16 to f32 160 us; added by
+    // loads and stores there 308)
+    const bool sums = ks > 1 || (q.wide && !vec && kt > CHAIN);
+    const size_t at_acc = sums ? ws.add((size_t)ks * pad_rows * lda * 4) : 0;
     const int parts = q.db ? bias_parts(q.dy, sm) : 1;
     const size_t at_part = parts > 1 ? ws.add((size_t)parts * O * 4) : 0;
     if (ws.bytes) TROP_TRY(ws.take());
@@ -388,7 +406,6 @@ int launch_weight_grad(const WeightGrad& q, cudaStream_t s)
     }
     void* const x = ws.base + at_x;
     float* const acc = (float*)(ws.base + at_acc);
-    const size_t elem = q.wide ? 4 : 2;
     for (int64_t c0 = 0; c0 < C; c0 += piece) {
         const int64_t cols = std::min(piece, C - c0);
         TROP_TRY(launch_activation_values(T, cols, {q.x.codes + c0, q.x.sc, q.x.scales + c0 / GROUP8, q.x.ss}, {x, ldx, type}, s));
@@ -401,24 +418,25 @@ int launch_weight_grad(const WeightGrad& q, cudaStream_t s)
         j.kt = kt;
         j.kper = cdiv(kt, ks);
         j.units = j.mt * j.nt * ks;
+        j.chain = q.wide ? CHAIN : kt;
         j.wide = q.wide;
         CUtensorMap a, b, c;
         TROP_TRY(make_map(&a, type, dy.m.p, O, T, dy.m.ld, TK));
         TROP_TRY(make_map(&b, type, x, cols, T, ldx, TK));
         c = a;
-        if (ks > 1) {
+        if (sums) {
             j.pad_rows = (int)pad_rows;
             TROP_TRY(make_map(&c, TROP_F32, acc, cols, ks * pad_rows, lda, 32));
         } else {
             const int64_t size[2] = {O, cols}, stride[2] = {q.ldw, 1};
             j.out = (char*)q.dw + c0 * elem;
             j.ldo = q.ldw;
-            j.vec = (uintptr_t)j.out % 16 == 0 && q.ldw * elem % 16 == 0 && q.ldw >= cols && q.ldw < (int64_t)1 << 37;
+            j.vec = vec;
             j.sp_out = span_of(j.out, elem, 2, size, stride);
             if (j.vec) TROP_TRY(make_map(&c, q.wide ? (int)TROP_F32 : type, j.out, cols, O, q.ldw, 32));
         }
         TROP_TRY(launch(q.bf16, a, b, c, j, sm, s));
-        if (ks > 1)
+        if (sums)
             TROP_TRY(q.wide   ? join<float>(acc, ks, pad_rows, lda, q, c0, cols, sm, s)
                      : q.bf16 ? join<__nv_bfloat16>(acc, ks, pad_rows, lda, q, c0, cols, sm, s)
                               : join<__half>(acc, ks, pad_rows, lda, q, c0, cols, sm, s));

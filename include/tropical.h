@@ -539,8 +539,7 @@ int tropical_activation_values(const trop_tensor* codes, const trop_tensor* scal
  *   dw[o, c] = sum over the tokens of dy[t, o] x[t, c],  db[o] = sum of dy[t, o]
  * with x the values that codes and scales [T, C] stand for, in dy's type (exact
  * for bf16; in f16, values outside its range become infinities), products
- * exact, sums in f32, one chain over the tokens (of 16384, an f32 result is off
- * by 1e-6 of its norm).  dy: [T, O], bf16 or f16, any strides.  dw: [O, C], of
+ * exact, sums in f32.  dy: [T, O], bf16 or f16, any strides.  dw: [O, C], of
  * dy's type or f32, contiguous columns.  db: nullable, [O] of dw's type.  No
  * token: zeros.  Long sums that few tiles have are split and joined in a fixed
  * order: results repeat bit for bit.  Rows of dy or of codes that TMA cannot

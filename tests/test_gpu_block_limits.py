@@ -198,3 +198,28 @@ def test_scales_of_other_leading_axes_are_refused(trop):
     flat = [tuple(c.reshape(6, -1) for c in k) for k in kept]
     got = trop.residual_norm_backward(t["dy"], t["dr"], flat[2], flat[0], stats.view(4, 6), gate=flat[1], **o)
     assert all(torch.equal(a.reshape(6, -1), b) for a, b in zip(want[:3], got[:3]))
+
+
+@pytest.mark.parametrize("dt", [B, H])
+@pytest.mark.parametrize("tokens, out, cols", [(4096, 4864, 2048), (7000, 4864, 2047), (2049, 130, 70), (16500, 64, 96), (40000, 300, 1000), (65536, 2050, 258)])
+def test_long_sums_of_32_bit_weight_gradients(trop, tokens, out, cols, dt):
+    """No chain of accumulations of a 32-bit result is longer than 2048 tokens: one over 8192 is off by six times what the plain 32-bit
+    product is.  Products are exact, and a chain is taken to lose up to a last place every 16 of them; the chains' sums and the
+    splits' are joined by as many roundings."""
+    g = torch.Generator(device="cuda").manual_seed(tokens)
+    dy, x = torch.randn(tokens, out, generator=g, device="cuda").to(dt), torch.randn(tokens, cols, generator=g, device="cuda").to(dt)
+    codes, scales = trop.activation_pack(x)
+    dw, _ = trop.activation_weight_grad(dy, codes, scales, out_dtype=F)
+    want, size = torch.zeros(out, cols, dtype=torch.float64, device="cuda"), torch.zeros(out, cols, dtype=torch.float64, device="cuda")
+    for i in range(0, tokens, 4096):
+        d, v = dy[i:i + 4096].double(), trop.activation_values(codes[i:i + 4096], scales[i:i + 4096], F).double()
+        want += d.T @ v
+        size += d.abs().T @ v.abs()
+    assert bool(((dw.double() - want).abs() <= (2048 / 16 + tokens / 2048 + 64) * 2.0 ** -24 * size).all())
+    assert torch.equal(dw, trop.activation_weight_grad(dy, codes, scales, out_dtype=F)[0])
+    if out == 4864:  # of 152 tiles, no split: the chains one after another
+        parts = [trop.activation_weight_grad(dy[i:i + 2048], codes[i:i + 2048], scales[i:i + 2048], out_dtype=F)[0] for i in range(0, tokens, 2048)]
+        total = parts[0]
+        for p in parts[1:]:
+            total = total + p
+        assert torch.equal(dw, total)
