@@ -223,3 +223,41 @@ def test_long_sums_of_32_bit_weight_gradients(trop, tokens, out, cols, dt):
         for p in parts[1:]:
             total = total + p
         assert torch.equal(dw, total)
+
+
+def test_threads_at_once(trop):
+    """Host threads, each on a stream of its own and with other sizes, as bit for bit what one thread gives."""
+    import threading
+
+    sizes = [(300, 1001), (700, 2048), (90, 8192), (64, 64)]
+    jobs = []
+    for rows, cols in sizes:
+        t, o = make(rows, cols, B, B, B, gate_act="silu")
+        tensors = {k: t[k] for k in ("gate", "scale", "post_weight", "post_bias")}
+
+        def step(t=t, o=o, tensors=tensors):
+            y, r, stats, kept = trop.residual_norm(t["x"], t["u"], t["weight"], t["bias"], **tensors, **o, keep=True)
+            g = trop.residual_norm_backward(t["dy"], t["dr"], kept[2], kept[0], stats, t["weight"], t["bias"], **{**tensors, "gate": kept[1]}, **o)
+            return (y, r, stats, *g, trop.activation_values(*kept[2], B), *trop.activation_weight_grad(t["dy"], *kept[0], out_dtype=F, want_bias=True))
+
+        jobs.append((step, step()))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(step, want):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(25):
+                    got = step()
+                    torch.cuda.current_stream().synchronize()
+                    if not all(torch.equal(a, b) for a, b in zip(got, want)):
+                        wrong.append("differs")
+        except Exception as e:
+            wrong.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs + jobs]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not wrong, wrong[:3]
